@@ -357,7 +357,7 @@ def _logp_own(s):
 def _logp_train_own(s):
     ms = _ms()
     r = ms.token_logprobs_fwd(s["logits"], s["targets"], scale=s["scale"])
-    d = ms.token_logprobs_bwd(s["logits"], s["targets"], r["lse"], r["entropy"], s["dlogprob"],
+    d = ms.token_logprobs_bwd(s["logits"], s["targets"], r["stats"], r["entropy"], s["dlogprob"],
                               s["dentropy"], scale=s["scale"])
     return {"logprob": r["logprob"], "entropy": r["entropy"], "dlogits": d}
 
