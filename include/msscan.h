@@ -341,6 +341,137 @@ ms_status ms_conv1d_silu(const void* x, const float* weight, const float* bias,
                          int32_t batch, int64_t seqlen, int32_t d_inner, int32_t io,
                          void* stream);
 
+/*
+ * Gated linear recurrence: the scan of a layer whose state is one value a
+ * channel and whose decay is a gate of the input.  With elementwise gates
+ * from their pre-activations r and i, and a rate lam per channel,
+ *
+ *   a[b,t,d] = exp(-sharpness * softplus(lam[d]) * sigmoid(r[b,t,d]))
+ *   h        = A * h + sqrt(1 - a^2) * sigmoid(i[b,t,d]) * x[b,t,d]
+ *              A = a, or 0 where reset[b,t] != 0       (h starts at h0, else 0)
+ *   y[b,t,d] = h                           (z == NULL)
+ *            = h * z * sigmoid(z)          (z given)
+ *
+ *   x, r, i, z, y : [batch][seqlen][d_inner] io dtype (z optional)
+ *   lam           : [d_inner] fp32
+ *   sharpness     : > 0 and finite (MS_ERR_SHAPE otherwise)
+ *   reset         : [batch][seqlen] bytes, optional.  A nonzero byte starts a
+ *                   new sequence there: nothing of the state before it comes
+ *                   through, NaN and infinities included (nor does anything
+ *                   through a step whose decay is exactly 0).
+ *   h0, h_last    : [batch][d_inner] fp32, optional.  h_last may equal h0.
+ *   states        : optional; receives the state before steps 0, 32, 64, ...
+ *                   ([batch][ceil(seqlen / 32)][d_inner] fp32, that is
+ *                   ms_gated_scan_states_bytes), for ms_gated_scan_bwd.
+ *   workspace     : ms_gated_scan_workspace_bytes bytes (may be 0), 16-byte
+ *                   aligned, no initialisation needed.
+ * batch, seqlen, d_inner and io as in ms_dims (MS_ERR_UNSUPPORTED when
+ * batch * ceil(d_inner / 32) exceeds 2^31 - 1).  The state, the decay and the
+ * gates are fp32; y is rounded once.  Deterministic.
+ *
+ * ms_gated_scan_bwd: gradients for dy and, optionally, dh_last ([batch]
+ *   [d_inner] fp32), from the same inputs and the states the forward saved
+ *   (h0 is in them).  dx, dr, di, dz in the io dtype (dz required with z),
+ *   dlam [d_inner] fp32 (sum over batch and time), dh0 [batch][d_inner] fp32
+ *   (optional).  No gradient crosses a reset.  The derivative of
+ *   sqrt(1 - a^2) is taken together with that of a, and stays finite where a
+ *   tends to 1.  Outputs must not overlap inputs.
+ * ms_gated_step: one timestep; h [batch][d_inner] fp32 is updated in place;
+ *   x_t, r_t, i_t, z_t, y_t [batch][d_inner].
+ */
+size_t ms_gated_scan_workspace_bytes(int32_t batch, int64_t seqlen, int32_t d_inner, int32_t io);
+size_t ms_gated_scan_states_bytes(int32_t batch, int64_t seqlen, int32_t d_inner);
+ms_status ms_gated_scan_fwd(const void* x, const void* r, const void* i, const float* lam,
+                            float sharpness, const void* z, const uint8_t* reset, void* y,
+                            const float* h0, float* h_last, float* states, int32_t batch,
+                            int64_t seqlen, int32_t d_inner, int32_t io, void* workspace,
+                            size_t workspace_bytes, void* stream);
+size_t ms_gated_scan_bwd_workspace_bytes(int32_t batch, int64_t seqlen, int32_t d_inner,
+                                         int32_t io);
+ms_status ms_gated_scan_bwd(const void* x, const void* r, const void* i, const float* lam,
+                            float sharpness, const void* z, const uint8_t* reset,
+                            const float* states, const void* dy, const float* dh_last, void* dx,
+                            void* dr, void* di, void* dz, float* dlam, float* dh0, int32_t batch,
+                            int64_t seqlen, int32_t d_inner, int32_t io, void* workspace,
+                            size_t workspace_bytes, void* stream);
+ms_status ms_gated_step(float* h, const void* x_t, const void* r_t, const void* i_t,
+                        const float* lam, float sharpness, const void* z_t, void* y_t,
+                        int32_t batch, int32_t d_inner, int32_t io, void* stream);
+
+/*
+ * Embedding lookup with scaling, and the gradient of its table:
+ *
+ *   out[k][:]     = scale * weight[ids[k]][:]                  (rounded once)
+ *   dweight[v][:] = scale * sum over k with ids[k] == v of dy[k][:]
+ *
+ *   ids      : [n] int32 or int64 (id_bits 32 or 64; MS_ERR_DTYPE otherwise).
+ *              An id outside [0, rows) yields a row of zeros and has no
+ *              gradient; nothing is read for it.
+ *   weight   : [rows][dim] io dtype        out, dy : [n][dim] io dtype
+ *   dweight  : [rows][dim] grad_dtype (MS_F32 or MS_BF16); every row is
+ *              written, zero where no id names it.
+ *   padding  : an id whose row gets no gradient, or -1.
+ *   n in 0 .. 2^31-1 (0: the lookup does nothing, the gradient is all zero);
+ *   rows in 1 .. 2^31-1; dim in 1 .. 2^24; scale finite.
+ *   workspace: ms_embed_bwd_workspace_bytes, 16-byte aligned, no
+ *              initialisation needed.
+ * The gradient sorts the ids, stably, and sums in fp32 in an order that
+ * depends on the ids alone: deterministic.  MS_ERR_UNSUPPORTED when a launch
+ * would need more than 2^31 - 1 workgroups.
+ */
+ms_status ms_embed_fwd(const void* ids, int32_t id_bits, const void* weight, float scale,
+                       void* out, int64_t n, int64_t rows, int32_t dim, int32_t io, void* stream);
+size_t ms_embed_bwd_workspace_bytes(int64_t n, int64_t rows, int32_t dim, int32_t io);
+ms_status ms_embed_bwd(const void* ids, int32_t id_bits, const void* dy, float scale,
+                       int64_t padding, void* dweight, int32_t grad_dtype, int64_t n,
+                       int64_t rows, int32_t dim, int32_t io, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Log probabilities of given tokens, with each row's entropy and its most
+ * likely tokens.  Per row of logits, with x = scale * logit (scale = one over
+ * the temperature):
+ *
+ *   lse = log sum_v exp(x_v)          logprob = x_target - lse
+ *   entropy = lse - sum_v p_v x_v     p_v = exp(x_v - lse)
+ *   top_id, top_logprob: the `top` largest logits, largest first, equal ones
+ *   by the lower token, and their x - lse
+ *
+ *   logits  : [rows] rows of vocab io values, ld >= vocab apart
+ *   targets : [rows] int32 or int64 (id_bits), optional.  A target outside
+ *             [0, vocab) is no target: its logprob is 0, without gradient.
+ *   logprob (needs targets), entropy, lse : [rows] fp32, each optional
+ *   stats   : [rows][2] fp32, optional: the row's largest logit and
+ *             lse - scale * that logit, for the gradient (lse alone would lose
+ *             the sum beside a large maximum)
+ *   top     : 0 .. 64 and <= vocab; top_logprob [rows][top] fp32 and top_id
+ *             [rows][top] int32 are required when it is not 0
+ *   rows in 0 .. 2^31-1 (0: nothing is done), vocab in 1 .. 2^31-1, scale > 0
+ *   and finite.
+ * Masked logits of -inf have probability 0 and add nothing to the entropy.  A
+ * row that is all -inf has lse -inf, logprob -inf, entropy 0 and alternatives
+ * of log probability -inf.  A NaN or +inf makes the row's results NaN; a NaN
+ * is never an alternative (where too few are left, top_id is -1).
+ * Sums are fp32, in an order that depends on the shape alone: deterministic.
+ *
+ * ms_token_logprobs_bwd: dlogits [rows] rows, ldd >= vocab apart, io dtype,
+ *   for dlogprob and dentropy ([rows] fp32, each optional), from the same
+ *   logits, targets, scale and the stats (and entropy, with dentropy) that the
+ *   forward wrote.  The alternatives carry no gradient.  A row that is all
+ *   -inf gets zeros.  dlogits may be logits itself (with ldd == ld).
+ */
+size_t ms_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int32_t top, int32_t io);
+ms_status ms_token_logprobs_fwd(const void* logits, int64_t ld, const void* targets,
+                                int32_t id_bits, float scale, float* logprob, float* entropy,
+                                float* lse, float* stats, int32_t top, float* top_logprob,
+                                int32_t* top_id, int64_t rows, int64_t vocab, int32_t io, void* workspace,
+                                size_t workspace_bytes, void* stream);
+ms_status ms_token_logprobs_bwd(const void* logits, int64_t ld, const void* targets,
+                                int32_t id_bits, float scale, const float* stats,
+                                const float* entropy, const float* dlogprob,
+                                const float* dentropy, void* dlogits, int64_t ldd, int64_t rows,
+                                int64_t vocab, int32_t io, void* stream);
+
 /* Static text for a status code. */
 const char* ms_status_string(ms_status s);
 

@@ -12,6 +12,12 @@ import ctypes
 import os
 from typing import Optional
 
+from . import lm
+from .lm import (embed, embed_bwd, embed_bwd_workspace_bytes, embed_fwd, gated_scan,  # noqa: F401
+                 gated_scan_bwd, gated_scan_bwd_workspace_bytes, gated_scan_fwd,
+                 gated_scan_states, gated_scan_workspace_bytes, gated_step, token_logprobs,
+                 token_logprobs_bwd, token_logprobs_fwd, token_logprobs_workspace_bytes)
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmsscan.so")
 
@@ -31,7 +37,7 @@ EXPORTS = ("ms_scan_workspace_bytes", "ms_scan_fwd", "ms_state_update", "ms_stat
            "ms_conv1d_silu", "ms_scan_bwd_workspace_bytes", "ms_scan_bwd",
            "ms_scan_fwd_dtproj", "ms_scan_dtproj_workspace_bytes", "ms_scan_fwd_noalloc",
            "ms_scan_checkpoint_bytes", "ms_scan_fwd_checkpoint",
-           "ms_scan_bwd_checkpoint_workspace_bytes", "ms_scan_bwd_checkpoint")
+           "ms_scan_bwd_checkpoint_workspace_bytes", "ms_scan_bwd_checkpoint") + lm.EXPORTS
 
 PHASES = ("prep", "summary", "carry", "main", "step", "conv", "reduce")  # ms_phase order
 
@@ -119,6 +125,7 @@ def load(path: Optional[str] = None):
     lib.ms_profile_begin.argtypes = [i32]
     lib.ms_profile_end.restype = ctypes.c_int
     lib.ms_profile_end.argtypes = [ctypes.POINTER(MsProfile)]
+    lm.declare(lib)
     if path is None:
         _lib = lib
     return lib

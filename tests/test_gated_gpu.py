@@ -1,0 +1,280 @@
+"""The gated linear recurrence (ms_gated_scan_fwd / _bwd, ms_gated_step)
+against its fp64 definition.
+
+Bounds: the library's own (helpers.bound: fp32 1e-4 (1 + |ref|), bf16 2 ulp +
+1e-3) for y and the state.  A decay of up to 0.999 remembers about 1000 steps,
+and each step's decay carries at most one rounding of exp2 (2^-23): 1.2e-4 of
+the state's size in the worst case, a few 1e-6 as they fall.  Gradients:
+lm_reference.grad_bound."""
+import numpy as np
+import pytest
+import torch
+
+import lm_reference as ref
+from helpers import assert_within
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+IO = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def inputs(b, L, d, io, gate, start, reset, seed=0):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    n = lambda *s: torch.randn(s, generator=g, device=DEV)  # noqa: E731
+    keep = 0.9 + 0.099 * torch.rand(d, generator=g, device=DEV)
+    s = {k: n(b, L, d).to(IO[io]) for k in ("x", "r", "i", "dy")}
+    s["lam"] = torch.log(torch.expm1(-torch.log(keep) / 8.0))
+    s["z"] = n(b, L, d).to(IO[io]) if gate else None
+    s["h0"] = n(b, d) if start else None
+    s["dh_last"] = n(b, d) if start else None
+    s["reset"] = (torch.rand(b, L, generator=g, device=DEV) < 0.02).to(torch.uint8) \
+        if reset else None
+    return s
+
+
+# b, L, d: one step, block edges of 32 / 128 / 256, several blocks; channel
+# counts of whole vectors, of none (below four), and with a tail
+SHAPES = [(1, 1, 1), (3, 1, 64), (2, 31, 3), (1, 32, 32), (2, 33, 33), (1, 127, 5), (2, 129, 100),
+          (1, 255, 64), (3, 256, 7), (1, 257, 36), (2, 1000, 66), (1, 2500, 2), (70, 5, 40)]
+KINDS = [(False, False, False), (True, True, False), (True, False, True), (False, True, True)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_forward_and_backward(gpu, shape, io):
+    b, L, d = shape
+    for k, (gate, start, reset) in enumerate(KINDS):
+        s = inputs(b, L, d, io, gate, start, reset, seed=100 + k)
+        hl = torch.full((b, d), float("nan"), device=DEV)
+        states = gpu.gated_scan_states(s["x"])
+        y = gpu.gated_scan_fwd(s["x"], s["r"], s["i"], s["lam"], s["z"], reset=s["reset"],
+                               h0=s["h0"], h_last=hl, states=states)
+        yr, hs, hr = ref.gated_forward(s["x"], s["r"], s["i"], s["lam"], s["z"], s["h0"],
+                                       s["reset"])
+        assert_within(y, yr.numpy(), io, f"y {gate, start, reset}")
+        assert_within(hl, hr.numpy(), "f32", f"h_last {gate, start, reset}")
+        first = torch.zeros(b, 1, d, dtype=torch.float64) if s["h0"] is None else \
+            s["h0"].cpu().double().unsqueeze(1)
+        before = torch.cat([first, hs[:, :-1]], 1)[:, ::32]
+        assert_within(states, before.numpy(), "f32", "states")
+        got = gpu.gated_scan_bwd(s["x"], s["r"], s["i"], s["lam"], s["dy"], states, s["z"],
+                                 reset=s["reset"], dh_last=s["dh_last"])
+        want = ref.gated_backward(s["x"], s["r"], s["i"], s["lam"], s["dy"], s["z"], s["h0"],
+                                  s["dh_last"], s["reset"])
+        assert (got["dz"] is None) == (s["z"] is None)
+        for name, w in want.items():
+            o = io if name in ("dx", "dr", "di", "dz") else "f32"
+            ref.assert_close(got[name], w.numpy(), ref.grad_bound(w.numpy(), o),
+                             f"{name} {gate, start, reset}")
+
+
+def test_gradient_against_differences(gpu):
+    """Central differences of the fp64 forward along a random direction of
+    every input.  Step 1e-6: truncation about 1e-12, rounding about 1e-9 of a
+    loss of order 10; the GPU's fp32 gradient adds 1e-6 of the sum of
+    |gradient| |direction|."""
+    s = inputs(2, 150, 12, "f32", True, True, True, seed=7)
+    names = ("x", "r", "i", "lam", "z", "h0")
+    states = gpu.gated_scan_states(s["x"])
+    gpu.gated_scan_fwd(s["x"], s["r"], s["i"], s["lam"], s["z"], reset=s["reset"], h0=s["h0"],
+                       states=states)
+    got = gpu.gated_scan_bwd(s["x"], s["r"], s["i"], s["lam"], s["dy"], states, s["z"],
+                             reset=s["reset"], dh_last=s["dh_last"])
+    v64 = {k: s[k].cpu().double() for k in names}
+
+    def loss(v):
+        y, _, hl = ref.gated_forward(v["x"], v["r"], v["i"], v["lam"], v["z"], v["h0"], s["reset"])
+        return float((y * s["dy"].cpu().double()).sum() + (hl * s["dh_last"].cpu().double()).sum())
+
+    rng = torch.Generator().manual_seed(3)
+    for k in names:
+        v = torch.randn(v64[k].shape, generator=rng, dtype=torch.float64)
+        e = 1e-6
+        diff = (loss({**v64, k: v64[k] + e * v}) - loss({**v64, k: v64[k] - e * v})) / (2 * e)
+        g = got["d" + k].cpu().double()
+        lim = 1e-5 * float((g.abs() * v.abs()).sum()) + 1e-6
+        assert abs(float((g * v).sum()) - diff) <= lim, (k, float((g * v).sum()), diff)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_steps_equal_the_scan(gpu, io):
+    s = inputs(3, 70, 50, io, True, True, False, seed=11)
+    hl = s["h0"].clone()
+    y = gpu.gated_scan_fwd(s["x"], s["r"], s["i"], s["lam"], s["z"], h0=hl, h_last=hl)  # aliased
+    yr, _, hr = ref.gated_forward(s["x"], s["r"], s["i"], s["lam"], s["z"], s["h0"])
+    h = s["h0"].clone()
+    for t in range(70):
+        yt = gpu.gated_step(h, *(s[k][:, t].contiguous() for k in ("x", "r", "i")), s["lam"],
+                            s["z"][:, t].contiguous())
+        assert_within(yt, yr[:, t].numpy(), io, f"y_t {t}")
+    assert_within(h, hr.numpy(), "f32", "h")
+    assert_within(hl, hr.numpy(), "f32", "h_last over h0")
+    assert_within(y, yr.numpy(), io, "y")
+
+
+def test_pieces_equal_the_whole(gpu):
+    s = inputs(2, 600, 70, "f32", False, True, True, seed=12)
+    yr, _, hr = ref.gated_forward(s["x"], s["r"], s["i"], s["lam"], None, s["h0"], s["reset"])
+    h, parts = s["h0"].clone(), []
+    for t0, t1 in ((0, 1), (1, 300), (300, 600)):
+        p = {k: s[k][:, t0:t1].contiguous() for k in ("x", "r", "i", "reset")}
+        hn = torch.empty_like(h)
+        parts.append(gpu.gated_scan_fwd(p["x"], p["r"], p["i"], s["lam"], reset=p["reset"], h0=h,
+                                        h_last=hn))
+        h = hn
+    assert_within(torch.cat(parts, 1), yr.numpy(), "f32", "y")
+    assert_within(h, hr.numpy(), "f32", "h_last")
+
+
+@pytest.mark.parametrize("d", [40, 37])
+def test_extreme_gates(gpu, d):
+    """Gates far out (decay exactly 0 and 1), rates far out, zero inputs:
+    results stay those of the definition, and gradients finite."""
+    s = inputs(2, 90, d, "f32", True, True, False, seed=13)
+    s["r"][:, 5] = 200.0
+    s["r"][:, 9] = -200.0
+    s["r"][0, 20:30] = -90.0
+    s["i"][:, 7] = -150.0
+    s["i"][:, 8] = 150.0
+    s["lam"][0], s["lam"][1], s["lam"][2], s["lam"][3] = -80.0, -30.0, 60.0, -120.0
+    s["x"][1] = 0.0
+    hl, states = torch.empty(2, d, device=DEV), gpu.gated_scan_states(s["x"])
+    y = gpu.gated_scan_fwd(s["x"], s["r"], s["i"], s["lam"], s["z"], h0=s["h0"], h_last=hl,
+                           states=states)
+    yr, _, hr = ref.gated_forward(s["x"], s["r"], s["i"], s["lam"], s["z"], s["h0"])
+    assert_within(y, yr.numpy(), "f32")
+    assert_within(hl, hr.numpy(), "f32")
+    got = gpu.gated_scan_bwd(s["x"], s["r"], s["i"], s["lam"], s["dy"], states, s["z"],
+                             dh_last=s["dh_last"])
+    want = ref.gated_backward(s["x"], s["r"], s["i"], s["lam"], s["dy"], s["z"], s["h0"],
+                              s["dh_last"])
+    for name, w in want.items():
+        assert torch.isfinite(got[name]).all(), name
+        ref.assert_close(got[name], w.numpy(), ref.grad_bound(w.numpy(), "f32"), name)
+
+
+def test_nan_and_infinity_stay_where_they_belong(gpu):
+    """A NaN reaches its own channel from its step on, and not past a reset."""
+    s = inputs(2, 400, 44, "f32", False, True, False, seed=14)
+    s["reset"] = torch.zeros(2, 400, dtype=torch.uint8, device=DEV)
+    s["reset"][:, 300] = 1
+    s["reset"][1, 50] = 1
+    s["x"][0, 100, 3] = float("nan")
+    s["x"][0, 130, 9] = float("inf")
+    s["h0"][1, 5] = float("nan")
+    hl, states = torch.empty(2, 44, device=DEV), gpu.gated_scan_states(s["x"])
+    y = gpu.gated_scan_fwd(s["x"], s["r"], s["i"], s["lam"], reset=s["reset"], h0=s["h0"],
+                           h_last=hl, states=states)
+    yr, _, hr = ref.gated_forward(s["x"], s["r"], s["i"], s["lam"], None, s["h0"], s["reset"])
+    assert torch.isnan(y[0, 100:300, 3]).all() and torch.isfinite(y[0, 300:, 3]).all()
+    assert torch.isinf(y[0, 130:300, 9]).all() and torch.isfinite(y[0, 300:, 9]).all()
+    assert torch.isnan(y[1, :50, 5]).all() and torch.isfinite(y[1, 50:, 5]).all()
+    rest = torch.isfinite(yr)
+    assert (torch.isfinite(y).cpu() == rest).all()
+    assert_within(torch.where(rest.to(DEV), y, torch.zeros_like(y)),
+                  torch.where(rest, yr, torch.zeros_like(yr)).numpy(), "f32")
+    assert_within(hl, hr.numpy(), "f32")
+    # backward: no gradient crosses the reset either
+    s["dy"][0, 350, 7] = float("nan")
+    g = gpu.gated_scan_bwd(s["x"], s["r"], s["i"], s["lam"], s["dy"], states, reset=s["reset"])
+    assert torch.isnan(g["dx"][0, 300:351, 7]).all()
+    assert torch.isfinite(g["dx"][0, :300, 7]).all() and torch.isfinite(g["dx"][0, 351:, 7]).all()
+    assert torch.isfinite(g["dr"][0, 300:, 3]).all() and torch.isfinite(g["dx"][0, :, 3]).all()
+
+
+def test_repeats_bit_for_bit_also_on_another_stream(gpu):
+    s = inputs(2, 3000, 72, "bf16", True, True, True, seed=15)
+
+    def call(stream=None):
+        hl, st = torch.empty(2, 72, device=DEV), gpu.gated_scan_states(s["x"])
+        y = gpu.gated_scan_fwd(s["x"], s["r"], s["i"], s["lam"], s["z"], reset=s["reset"],
+                               h0=s["h0"], h_last=hl, states=st, stream=stream)
+        g = gpu.gated_scan_bwd(s["x"], s["r"], s["i"], s["lam"], s["dy"], st, s["z"],
+                               reset=s["reset"], dh_last=s["dh_last"], stream=stream)
+        return [y, hl] + [g[k] for k in sorted(g)]
+
+    first = call()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream):
+        again = call(stream)
+        torch.cuda.synchronize()
+        for p, q in zip(first, again):
+            assert torch.equal(p, q)
+
+
+def test_in_a_graph(gpu):
+    s = inputs(1, 5000, 40, "bf16", True, True, True, seed=16)
+    io = gpu.MS_BF16
+    y, hl, st = torch.empty_like(s["x"]), torch.empty(1, 40, device=DEV), \
+        gpu.gated_scan_states(s["x"])
+    wf = torch.empty(max(1, gpu.gated_scan_workspace_bytes(1, 5000, 40, io)), dtype=torch.uint8,
+                     device=DEV)
+    wb = torch.empty(gpu.gated_scan_bwd_workspace_bytes(1, 5000, 40, io), dtype=torch.uint8,
+                     device=DEV)
+
+    def call():
+        gpu.gated_scan_fwd(s["x"], s["r"], s["i"], s["lam"], s["z"], reset=s["reset"], h0=s["h0"],
+                           y=y, h_last=hl, states=st, workspace=wf)
+        return gpu.gated_scan_bwd(s["x"], s["r"], s["i"], s["lam"], s["dy"], st, s["z"],
+                                  reset=s["reset"], dh_last=s["dh_last"], workspace=wb)
+
+    want = {k: v.clone() for k, v in call().items()}
+    yw, hw = y.clone(), hl.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = call()
+    for rep in range(3):
+        for t in (y, hl, st, *out.values()):
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, yw) and torch.equal(hl, hw), rep
+        for k in want:
+            assert torch.equal(out[k], want[k]), (rep, k)
+        call()
+        torch.cuda.synchronize()
+
+
+def test_autograd(gpu):
+    s = inputs(2, 80, 24, "f32", True, True, False, seed=17)
+    t = {k: s[k].clone().requires_grad_() for k in ("x", "r", "i", "lam", "z", "h0")}
+    y, hl = gpu.gated_scan(t["x"], t["r"], t["i"], t["lam"], t["z"], t["h0"], return_last=True)
+    ((y * s["dy"]).sum() + (hl * s["dh_last"]).sum()).backward()
+    want = ref.gated_backward(s["x"], s["r"], s["i"], s["lam"], s["dy"], s["z"], s["h0"],
+                              s["dh_last"])
+    for k in t:
+        w = want["d" + k].numpy()
+        ref.assert_close(t[k].grad, w, ref.grad_bound(w, "f32"), k)
+
+
+def test_refusals(gpu):
+    s = inputs(2, 10, 8, "f32", False, False, False)
+    x, r, i, lam = s["x"], s["r"], s["i"], s["lam"]
+    with pytest.raises(TypeError):
+        gpu.gated_scan_fwd(x.half(), r, i, lam)
+    with pytest.raises(TypeError):
+        gpu.gated_scan_fwd(x, r.bfloat16(), i, lam)
+    with pytest.raises(ValueError, match="shape"):
+        gpu.gated_scan_fwd(x, r[:, :9].contiguous(), i, lam)
+    with pytest.raises(ValueError, match="contiguous"):
+        gpu.gated_scan_fwd(x.transpose(0, 1).contiguous().transpose(0, 1), r, i, lam)
+    with pytest.raises(ValueError, match="device"):
+        gpu.gated_scan_fwd(x.cpu(), r, i, lam)
+    with pytest.raises(ValueError, match="states"):
+        gpu.gated_scan_bwd(x, r, i, lam, s["dy"], None)
+    for c in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(gpu.MsError, match="sharpness"):
+            gpu.gated_scan_fwd(x, r, i, lam, c=c)
+    with pytest.raises(gpu.MsError, match="seqlen"):
+        gpu.gated_scan_fwd(x[:, :0], r[:, :0], i[:, :0], lam)
+    with pytest.raises(gpu.MsError, match="16-byte"):
+        flat = torch.zeros(2 * 10 * 8 + 1, device=DEV)[1:].view(2, 10, 8)
+        gpu.gated_scan_fwd(flat, r, i, lam)
+    with pytest.raises(gpu.MsError, match="workspace"):
+        gpu.gated_scan_bwd(x, r, i, lam, s["dy"], gpu.gated_scan_states(x),
+                           workspace=torch.empty(1, dtype=torch.uint8, device=DEV))
+    np.testing.assert_equal(gpu.gated_scan_states(x).shape, (2, 1, 8))

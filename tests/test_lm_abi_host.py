@@ -1,0 +1,115 @@
+"""Host-only checks of the language-model operators' C ABI: sizes, and every
+refusal that needs no GPU (nothing is launched on any of these calls)."""
+import ctypes
+
+import pytest
+import torch
+
+import selective_state_space_81_amd as ms
+
+NONE = ctypes.c_size_t(-1).value
+P = 16  # an aligned address that is never read
+
+
+def test_sizes():
+    lib = ms.load()
+    assert lib.ms_gated_scan_states_bytes(2, 33, 5) == 2 * 2 * 5 * 4
+    assert lib.ms_gated_scan_states_bytes(1, 32, 8) == 8 * 4
+    for bad in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (-1, 5, 5), (1, 1 << 31, 1)):
+        assert lib.ms_gated_scan_states_bytes(*bad) == NONE
+        assert lib.ms_gated_scan_workspace_bytes(*bad, 1) == NONE
+        assert lib.ms_gated_scan_bwd_workspace_bytes(*bad, 1) == NONE
+    assert lib.ms_gated_scan_workspace_bytes(1, 1, 1, 7) == NONE
+    assert lib.ms_gated_scan_bwd_workspace_bytes(8, 2048, 1536, 1) % 256 == 0
+    assert lib.ms_embed_bwd_workspace_bytes(0, 10, 8, 0) != NONE
+    for bad in ((-1, 10, 8, 0), (1 << 31, 10, 8, 0), (5, 0, 8, 0), (5, 10, 0, 0), (5, 10, 8, 3)):
+        assert lib.ms_embed_bwd_workspace_bytes(*bad) == NONE
+    assert lib.ms_token_logprobs_workspace_bytes(0, 100, 5, 0) != NONE
+    for bad in ((-1, 9, 0, 0), (1, 0, 0, 0), (1, 9, 10, 0), (1, 900, 65, 0), (1, 9, -1, 0),
+                (1, 9, 0, 2)):
+        assert lib.ms_token_logprobs_workspace_bytes(*bad) == NONE
+
+
+def test_gated_refusals():
+    lib = ms.load()
+
+    def fwd(x=P, y=P, lam=P, c=8.0, h0=None, b=1, L=40, d=8, io=1):
+        return lib.ms_gated_scan_fwd(x, P, P, lam, c, None, None, y, h0, None, None, b, L, d, io,
+                                     P, 1 << 40, None)
+
+    assert fwd(x=None) == 1 and fwd(y=None) == 1 and fwd(lam=None) == 1
+    assert fwd(b=0) == 2 and fwd(L=0) == 2 and fwd(d=0) == 2 and fwd(L=1 << 31) == 2
+    assert fwd(io=2) == 3
+    assert fwd(x=24) == 5 and fwd(h0=8) == 5
+    for c in (0.0, -2.0, float("inf"), float("nan")):
+        assert fwd(c=c) == 2
+    assert b"sharpness" in lib.ms_last_error()
+
+    def bwd(z=None, dz=None, states=P, ws=P, n=1 << 40):
+        return lib.ms_gated_scan_bwd(P, P, P, P, 8.0, z, None, states, P, None, P, P, P, dz, P,
+                                     None, 1, 40, 8, 1, ws, n, None)
+
+    assert bwd(states=None) == 1 and bwd(z=P) == 1
+    assert bwd(ws=None) == 6 and bwd(n=8) == 6
+    assert lib.ms_gated_step(None, P, P, P, P, 8.0, None, P, 1, 8, 1, None) == 1
+    assert lib.ms_gated_step(P, P, P, P, P, 8.0, None, P, 0, 8, 1, None) == 2
+    assert lib.ms_gated_step(P, P, 20, P, P, 8.0, None, P, 1, 8, 1, None) == 5
+
+
+def test_embed_refusals():
+    lib = ms.load()
+
+    def fwd(ids=P, bits=64, w=P, scale=1.0, n=5, rows=10, dim=8, io=0):
+        return lib.ms_embed_fwd(ids, bits, w, scale, P, n, rows, dim, io, None)
+
+    assert fwd(ids=None) == 1 and fwd(w=None) == 1
+    assert fwd(bits=16) == 3 and fwd(io=4) == 3
+    assert fwd(n=-1) == 2 and fwd(rows=0) == 2 and fwd(dim=0) == 2 and fwd(dim=1 << 25) == 2
+    assert fwd(scale=float("nan")) == 2
+    assert fwd(w=8) == 5
+    assert fwd(ids=None, n=0) == 0  # nothing to do, nothing launched
+
+    def bwd(ids=P, dw=P, gd=0, ws=P, n=1 << 40):
+        return lib.ms_embed_bwd(ids, 64, P, 1.0, -1, dw, gd, 5, 10, 8, 0, ws, n, None)
+
+    assert bwd(ids=None) == 1 and bwd(dw=None) == 1 and bwd(gd=5) == 3
+    assert bwd(ws=None) == 6 and bwd(n=1) == 6 and bwd(ws=8) == 5
+
+
+def test_logprob_refusals():
+    lib = ms.load()
+
+    def fwd(x=P, ld=40, t=P, bits=64, scale=1.0, lp=P, top=0, tl=None, ti=None, rows=3, V=40,
+            io=0, ws=P):
+        return lib.ms_token_logprobs_fwd(x, ld, t, bits, scale, lp, P, P, P, top, tl, ti, rows, V, io,
+                                         ws, 1 << 40, None)
+
+    assert fwd(x=None) == 1 and fwd(t=None) == 1 and fwd(top=2) == 1 and fwd(top=2, tl=P) == 1
+    assert fwd(ld=39) == 2 and fwd(V=0) == 2 and fwd(rows=-1) == 2 and fwd(top=65) == 2
+    assert fwd(bits=8) == 3 and fwd(io=9) == 3
+    assert fwd(scale=0.0) == 2 and fwd(scale=float("inf")) == 2
+    assert fwd(x=4) == 5
+    assert fwd(rows=0, x=None) == 0
+    assert fwd(rows=1, V=50000, ld=50000, ws=None) == 6
+
+    def bwd(x=P, t=P, stats=P, ent=P, gl=P, gh=P, d=P, ld=40, ldd=40):
+        return lib.ms_token_logprobs_bwd(x, ld, t, 64, 1.0, stats, ent, gl, gh, d, ldd, 3, 40, 0,
+                                         None)
+
+    assert bwd(x=None) == 1 and bwd(stats=None) == 1 and bwd(d=None) == 1
+    assert bwd(t=None) == 1 and bwd(ent=None) == 1
+    assert bwd(ldd=39) == 2 and bwd(ldd=48) == 2  # over the logits with another stride
+
+
+def test_binding_refuses_host_tensors():
+    x = torch.zeros(2, 4, 8)
+    with pytest.raises(ValueError, match="device"):
+        ms.gated_scan_fwd(x, x, x, torch.zeros(8))
+    with pytest.raises(ValueError, match="device"):
+        ms.gated_step(x[:, 0], x[:, 0], x[:, 0], x[:, 0], torch.zeros(8))
+    with pytest.raises(ValueError, match="device"):
+        ms.embed_fwd(torch.zeros(3, dtype=torch.int64), torch.zeros(5, 8))
+    with pytest.raises(ValueError, match="device"):
+        ms.embed_bwd(torch.zeros(3, dtype=torch.int64), torch.zeros(3, 8), 5)
+    with pytest.raises(ValueError, match="device"):
+        ms.token_logprobs_fwd(torch.zeros(3, 8))
