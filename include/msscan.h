@@ -360,13 +360,13 @@ ms_status ms_conv1d_silu(const void* x, const float* weight, const float* bias,
  *                   through, NaN and infinities included (nor does anything
  *                   through a step whose decay is exactly 0).
  *   h0, h_last    : [batch][d_inner] fp32, optional.  h_last may equal h0.
- *   states        : optional; receives the state before steps 0, 32, 64, ...
- *                   ([batch][ceil(seqlen / 32)][d_inner] fp32, that is
+ *   states        : optional; receives the state before steps 0, 16, 32, ...
+ *                   ([batch][ceil(seqlen / 16)][d_inner] fp32, that is
  *                   ms_gated_scan_states_bytes), for ms_gated_scan_bwd.
  *   workspace     : ms_gated_scan_workspace_bytes bytes (may be 0), 16-byte
  *                   aligned, no initialisation needed.
- * batch, seqlen, d_inner and io as in ms_dims (MS_ERR_UNSUPPORTED when
- * batch * ceil(d_inner / 32) exceeds 2^31 - 1).  The state, the decay and the
+ * batch, seqlen, d_inner and io as in ms_dims (MS_ERR_UNSUPPORTED where a
+ * launch would need more than 2^31 - 1 workgroups).  The state, the decay and the
  * gates are fp32; y is rounded once.  Deterministic.
  *
  * ms_gated_scan_bwd: gradients for dy and, optionally, dh_last ([batch]

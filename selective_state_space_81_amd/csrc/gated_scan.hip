@@ -14,13 +14,13 @@
 // q keeps la / n together: as la -> 0 the ratio goes to 0 like sqrt(-la/2),
 // so the gradient stays finite where d n / d la alone does not.
 //
-// Layout.  A workgroup owns CH = VEC * LC neighbouring channels and kWaves
-// consecutive pieces of time; lane (rg, lc) of a wave holds VEC channels at
-// TAU consecutive steps, RG = 64 / LC such groups side by side in time.  Each
-// lane composes its own steps into one affine map (P, H), the groups of a
-// wave are joined by a shuffle scan, the waves through LDS, and the workgroup
-// walks its channels along the sequence with the state in registers, so every
-// input is read once and every output written once.
+// Layout.  A workgroup owns CH = VEC * LC neighbouring channels and one block
+// of time, a wave a piece of it; lane (rg, lc) holds VEC channels at TAU
+// consecutive steps, RG = 64 / LC such groups side by side in time.  Each lane
+// composes its own steps into one affine map (P, H), the groups of a wave are
+// joined by a shuffle scan, the waves through LDS and the blocks by look-back
+// (Chain below), so every input is read once and every output written once
+// whatever the number of channels.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -88,12 +88,12 @@ struct RowIo<1, false> {
 };
 
 template <class R>
-__device__ __forceinline__ typename R::T ld_row(const typename R::E* p) {
-    return *reinterpret_cast<const typename R::M*>(p);
+__device__ __forceinline__ typename R::T ld_row(const char* row, uint32_t off) {
+    return *reinterpret_cast<const typename R::M*>(row + off);
 }
 template <class R>
-__device__ __forceinline__ void st_row(typename R::E* p, typename R::T v) {
-    *reinterpret_cast<typename R::M*>(p) = v;
+__device__ __forceinline__ void st_row(char* row, uint32_t off, typename R::T v) {
+    *reinterpret_cast<typename R::M*>(row + off) = v;
 }
 
 // ---- the gates of one element ------------------------------------------------------
@@ -134,370 +134,532 @@ __device__ __forceinline__ float apply(float P, float h, float H) {
     return v;
 }
 
-// ---- forward ------------------------------------------------------------------------
-template <int VEC_, bool BF16_>
-struct Shape {
-    static constexpr int VEC = VEC_;
+// ---- geometry -----------------------------------------------------------------------
+// VEC channels and TAU steps a lane, LC lanes across channels, W waves along
+// time.  BLOCKS: a workgroup takes one block of TB steps and gets the state
+// before it from the workgroups of earlier blocks (see Chain); otherwise it
+// walks its channels' whole sequence.
+template <int VEC_, int LC_, int TAU_, int W_, bool BF16_>
+struct Geo {
+    static constexpr int VEC = VEC_, LC = LC_, TAU = TAU_, W = W_;
     static constexpr bool BF16 = BF16_;
-    static constexpr int LC = VEC == 4 ? 8 : 32;  // lanes across channels
-    static constexpr int RG = 64 / LC;            // time groups in a wave
-    static constexpr int CH = VEC * LC;           // channels of a workgroup
+    static constexpr int RG = 64 / LC;         // time groups in a wave
+    static constexpr int CH = VEC * LC;        // channels of a workgroup
+    static constexpr int TW = TAU * RG;        // steps of a wave
+    static constexpr int TB = TW * W;          // steps of a workgroup
+    static_assert(TW % kGatedBlock == 0, "a wave starts at a saved state");
 };
-constexpr int kWaves = 4;
 
-// Lane geometry shared by the passes.
-template <class S>
+// Channel tiles of a batch row; a chain is one tile of one batch row.
+template <class G>
+__device__ __forceinline__ uint32_t tiles_of(const GatedArgs& a) {
+    return ((uint32_t)a.Dn + G::CH - 1) / G::CH;
+}
+
+// Lane geometry of chain `chain`.
+template <class G>
 struct Lane {
     int lane, wave, rg, lc, b, ch;
-    bool live;     // the lane's channels exist
-    int64_t base;  // element offset of (b, 0, ch)
-    __device__ __forceinline__ Lane(const GatedArgs& a) {
+    bool live;    // the lane's channels exist
+    uint32_t chb, rowb;  // byte offset of the lane's channels, bytes of a row
+    __device__ __forceinline__ Lane(const GatedArgs& a, uint32_t chain) {
         lane = threadIdx.x & 63;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        rg = lane / S::LC;
-        lc = lane % S::LC;
-        const uint32_t tiles = ((uint32_t)a.Dn + S::CH - 1) / S::CH;
-        const uint32_t l = xcd_logical(blockIdx.x, gridDim.x);
-        b = (int)(l / tiles);
-        ch = (int)(l % tiles) * S::CH + lc * S::VEC;
+        rg = lane / G::LC;
+        lc = lane % G::LC;
+        const uint32_t tiles = tiles_of<G>(a);
+        b = (int)(chain / tiles);
+        ch = (int)(chain % tiles) * G::CH + lc * G::VEC;
         live = ch < a.Dn;
         // The last lane of a channel count that VEC does not divide takes the
         // last VEC channels; some are its neighbour's too, and both store the
         // same values.  Lanes past it read them and store nothing.
-        ch = min(ch, a.Dn - S::VEC);
-        base = (int64_t)b * a.L * a.Dn + ch;
+        ch = min(ch, a.Dn - G::VEC);
+        constexpr int E = G::BF16 ? 2 : 4;
+        chb = (uint32_t)ch * E;
+        rowb = (uint32_t)a.Dn * E;  // below 2^24 (the entry points check d_inner)
+    }
+    // Byte offset of the lane's step j within its wave's TW steps, of which
+    // `left` exist (reads past them repeat the last one).
+    __device__ __forceinline__ uint32_t at(int j, int left) const {
+        return __umul24((uint32_t)min(rg * G::TAU + j, left - 1), rowb) + chb;
+    }
+    // Address of step t of the wave's batch row (wave-uniform).
+    __device__ __forceinline__ const char* row(const GatedArgs& a, const void* p, int64_t t) const {
+        return static_cast<const char*>(p) + ((int64_t)b * a.L + t) * rowb;
+    }
+    __device__ __forceinline__ char* row(const GatedArgs& a, void* p, int64_t t) const {
+        return static_cast<char*>(p) + ((int64_t)b * a.L + t) * rowb;
     }
 };
 
-template <int VEC, bool BF16, bool GATE, bool RESET>
-__global__ void __launch_bounds__(64 * kWaves) gated_fwd(GatedArgs a) {
-    using S = Shape<VEC, BF16>;
-    using R = RowIo<VEC, BF16>;
-    using T = typename R::T;
-    constexpr int TAU = VEC == 4 ? 8 : 16;
-    constexpr int LC = S::LC, RG = S::RG, TW = TAU * RG, TB = TW * kWaves;
-    static_assert(TW % kGatedBlock == 0, "a wave starts at a saved state");
-    __shared__ float2 s_sum[2][kWaves][S::CH];
-    const Lane<S> g(a);
-    using E = typename R::E;
-    const E* px = static_cast<const E*>(a.x) + g.base;
-    const E* pr = static_cast<const E*>(a.r) + g.base;
-    const E* pi = static_cast<const E*>(a.i) + g.base;
-    const E* pz = static_cast<const E*>(a.z) + g.base;
-    E* py = static_cast<E*>(a.y) + g.base;
-    const int64_t rs = a.Dn;
+// The channel of slot threadIdx.x (lane lc's channel c is slot lc * VEC + c).
+template <class G>
+__device__ __forceinline__ int slot_channel(const GatedArgs& a, uint32_t chain) {
+    const int ch = (int)(chain % tiles_of<G>(a)) * G::CH + (int)threadIdx.x / G::VEC * G::VEC;
+    return min(ch, a.Dn - G::VEC) + (int)threadIdx.x % G::VEC;
+}
 
-    float k[VEC], carry[VEC];
-#pragma unroll
-    for (int c = 0; c < VEC; ++c) {
-        k[c] = -a.sharp * kLog2e * softplus_rel(a.lam[g.ch + c]);
-        carry[c] = a.h0 ? a.h0[(int64_t)g.b * a.Dn + g.ch + c] : 0.f;
+// ---- the state between blocks -----------------------------------------------------------
+// Blocks of one chain run on different workgroups.  Each publishes what it
+// does to a state, (P, H), as soon as it has read its inputs, and the state
+// after it once it knows the one before; a block looks back over up to
+// kWindow others for the nearest published state and applies the (P, H)
+// between in order, so the result is that of a serial chain whatever the
+// timing.  Work is handed out by a counter, earlier blocks first: a block
+// that is waited for has been started, and waits for earlier ones only, so
+// every wait ends.  A word of all ones is not yet published (the preparing
+// kernel writes it; published NaNs have another pattern).  The words are
+// single relaxed atomics at device scope: each carries its whole message, so
+// no fence orders anything else.
+constexpr uint32_t kNotYet = 0xffffffffu;
+constexpr int kWindow = 8;
+
+__device__ __forceinline__ float plain_nan(float v) { return v == v ? v : __builtin_nanf(""); }
+
+__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint32_t peek(const uint32_t* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// State words of one chain: [block][CH], in the order blocks are taken.
+struct Chain {
+    uint64_t* map;    // (P, H) of a block
+    uint32_t* state;  // the state after a block
+    int ch, stride;   // this lane's channel, channels of a block
+
+    __device__ __forceinline__ void publish_map(int64_t blk, float P, float H) const {
+        const uint64_t w = ((uint64_t)__float_as_uint(plain_nan(H)) << 32) |
+                           __float_as_uint(plain_nan(P));
+        __hip_atomic_store(map + blk * stride + ch, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
+    __device__ __forceinline__ void publish_state(int64_t blk, float h) const {
+        __hip_atomic_store(state + blk * stride + ch, __float_as_uint(plain_nan(h)),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    // The state before block blk >= 1.
+    template <bool RESET>
+    __device__ __forceinline__ float before(int64_t blk) const {
+        for (;;) {
+            uint32_t st[kWindow];
+            uint64_t mp[kWindow];
+#pragma unroll
+            for (int k = 0; k < kWindow; ++k) {
+                const int64_t j = max(blk - 1 - k, (int64_t)0) * stride + ch;
+                st[k] = peek(state + j);
+                mp[k] = peek(map + j);
+            }
+            // nearest state; every map nearer than it has to be there
+            int at = -1;
+            bool whole = true;
+#pragma unroll
+            for (int k = 0; k < kWindow; ++k) {
+                if (at < 0 && whole && st[k] != kNotYet) at = k;
+                whole = whole && (uint32_t)mp[k] != kNotYet;
+            }
+            if (at >= 0) {
+                float h = 0.f;
+#pragma unroll
+                for (int k = kWindow - 1; k >= 0; --k) {
+                    if (k == at) h = __uint_as_float(st[k]);
+                    if (k < at)
+                        h = apply<RESET>(__uint_as_float((uint32_t)mp[k]), h,
+                                         __uint_as_float((uint32_t)(mp[k] >> 32)));
+                }
+                return h;
+            }
+            __builtin_amdgcn_s_sleep(1);
+        }
+    }
+};
+
+__device__ __forceinline__ Chain chain_of(const GatedArgs& a, uint32_t chain, int ch, int CH) {
+    return Chain{a.map + (int64_t)chain * a.blocks * CH, a.state + (int64_t)chain * a.blocks * CH,
+                 ch, CH};
+}
+
+// Nothing published, no work handed out.
+__global__ void __launch_bounds__(256) gated_prepare(GatedArgs a, int64_t words) {
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x, n = (int64_t)gridDim.x * 256;
+    for (int64_t k = t; k < words; k += n) {
+        a.state[k] = kNotYet;
+        a.map[k] = ~(uint64_t)0;
+    }
+    if (t == 0) *a.ticket = 0;
+}
+
+__global__ void __launch_bounds__(256) gated_copy(const float* from, float* to, int64_t n) {
+    for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += (int64_t)gridDim.x * 256)
+        to[k] = from[k];
+}
+
+// This workgroup's chain and its turn in it: earlier turns of all chains first.
+__device__ __forceinline__ void take_work(const GatedArgs& a, uint32_t& chain, int64_t& turn) {
+    if (a.blocks == 1) {
+        chain = blockIdx.x;
+        turn = 0;
+        return;
+    }
+    __shared__ uint32_t s_ticket;
+    if (threadIdx.x == 0) s_ticket = atomicAdd(a.ticket, 1u);
+    __syncthreads();
+    const uint32_t t = __builtin_amdgcn_readfirstlane(s_ticket);
+    const uint32_t chains = gridDim.x / (uint32_t)a.blocks;
+    chain = t % chains;
+    turn = t / chains;
+}
+
+// ---- forward ------------------------------------------------------------------------
+template <class G, bool GATE, bool RESET>
+__global__ void __launch_bounds__(64 * G::W) gated_fwd(GatedArgs a) {
+    constexpr int VEC = G::VEC, LC = G::LC, RG = G::RG, TAU = G::TAU, TW = G::TW, TB = G::TB,
+                  W = G::W;
+    using R = RowIo<VEC, G::BF16>;
+    using T = typename R::T;
+    __shared__ float2 s_sum[W][G::CH];
+    __shared__ float s_h[G::CH];
+    uint32_t chain;
+    int64_t blk;
+    take_work(a, chain, blk);
+    const Lane<G> g(a, chain);
+    const int64_t tw = blk * TB + g.wave * TW;  // the wave's first step
+    const int64_t tr = min(tw, a.L - 1);  // a wave past the end reads the last step
+    const int left = (int)min(a.L - tr, (int64_t)TW);
+    const int mine = (int)min(a.L - tw, (int64_t)TW) - g.rg * TAU;  // the lane's steps
 
     T rx[TAU], rr[TAU], ri[TAU], rz[TAU];
-    auto load = [&](int64_t t0, const E* p, T(&w)[TAU]) {
+    auto load = [&](const void* p, T(&w)[TAU]) {
+        const char* q = g.row(a, p, tr);
 #pragma unroll
-        for (int j = 0; j < TAU; ++j) w[j] = ld_row<R>(p + min(t0 + j, a.L - 1) * rs);
+        for (int j = 0; j < TAU; ++j) w[j] = ld_row<R>(q, g.at(j, left));
     };
-    int64_t t0 = (int64_t)g.wave * TW + g.rg * TAU;  // the lane's first step
-    load(t0, px, rx);
-    load(t0, pr, rr);
-    load(t0, pi, ri);
-    if constexpr (GATE) load(t0, pz, rz);
+    load(a.r, rr);
+    load(a.i, ri);
+    load(a.x, rx);
+    if constexpr (GATE) load(a.z, rz);
+    float k[VEC];
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) k[c] = -a.sharp * kLog2e * softplus_rel(a.lam[g.ch + c]);
 
-    int par = 0;
-    for (int64_t tb = 0; tb < a.L; tb += TB, t0 += TB, par ^= 1) {
-        // the lane's steps as A[j], B[j] and composed as (P, H)
-        float A[TAU][VEC], B[TAU][VEC], P[VEC], H[VEC];
+    // the lane's steps as A[j], B[j] and composed as (P, H)
+    float A[TAU][VEC], B[TAU][VEC], P[VEC], H[VEC];
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) P[c] = 1.f, H[c] = 0.f;
+    for (int c = 0; c < VEC; ++c) P[c] = 1.f, H[c] = 0.f;
 #pragma unroll
-        for (int j = 0; j < TAU; ++j) {
-            const bool in = t0 + j < a.L;
-            bool cut = false;
-            if constexpr (RESET) cut = in && a.reset[(int64_t)g.b * a.L + t0 + j] != 0;
-            float x[VEC], r[VEC], i[VEC];
-            R::unpack(rx[j], x);
-            R::unpack(rr[j], r);
-            R::unpack(ri[j], i);
+    for (int j = 0; j < TAU; ++j) {
+        const bool in = j < mine;
+        bool cut = false;
+        if constexpr (RESET) cut = in && a.reset[(int64_t)g.b * a.L + tw + g.rg * TAU + j] != 0;
+        float x[VEC], r[VEC], i[VEC];
+        R::unpack(rx[j], x);
+        R::unpack(rr[j], r);
+        R::unpack(ri[j], i);
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                const float la2 = k[c] * sigmoid_f(r[c]);
-                const float e = hw_exp2(la2);
-                const float n = sqrt_f(one_minus_square(la2, e));
-                A[j][c] = in ? (cut ? 0.f : e) : 1.f;
-                B[j][c] = in ? n * sigmoid_f(i[c]) * x[c] : 0.f;
-                H[c] = apply<RESET>(A[j][c], H[c], B[j][c]);
-                P[c] *= A[j][c];
-            }
-        }
-        if (tb + TB < a.L) {  // the next block's inputs travel during the exchange below
-            load(t0 + TB, px, rx);
-            load(t0 + TB, pr, rr);
-            load(t0 + TB, pi, ri);
-        }
-        // inclusive scan over the wave's time groups, then the wave's total to LDS
-#pragma unroll
-        for (int off = LC; off < 64; off <<= 1) {
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                const float Pu = __shfl_up(P[c], off), Hu = __shfl_up(H[c], off);
-                if (g.lane >= off) {
-                    H[c] = apply<RESET>(P[c], Hu, H[c]);
-                    P[c] *= Pu;
-                }
-            }
-        }
-        if (g.rg == RG - 1) {
-#pragma unroll
-            for (int c = 0; c < VEC; ++c)
-                s_sum[par][g.wave][g.lc * VEC + c] = make_float2(P[c], H[c]);
-        }
-        float h[VEC];
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {  // exclusive
-            P[c] = __shfl_up(P[c], LC);
-            H[c] = __shfl_up(H[c], LC);
-            if (g.rg == 0) P[c] = 1.f, H[c] = 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            if (w == g.wave) {
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) h[c] = apply<RESET>(P[c], carry[c], H[c]);
-            }
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                const float2 q = s_sum[par][w][g.lc * VEC + c];
-                carry[c] = apply<RESET>(q.x, carry[c], q.y);
-            }
-        }
-        if (a.states && g.live && t0 % kGatedBlock == 0 && t0 < a.L) {
-            float* st = a.states + ((int64_t)g.b * a.nstates + t0 / kGatedBlock) * a.Dn + g.ch;
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) st[c] = h[c];
-        }
-#pragma unroll
-        for (int j = 0; j < TAU; ++j) {
-            float o[VEC];
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                h[c] = apply<RESET>(A[j][c], h[c], B[j][c]);
-                o[c] = h[c];
-            }
-            if constexpr (GATE) {
-                float z[VEC];
-                R::unpack(rz[j], z);
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) o[c] *= silu_f(z[c]);
-            }
-            if (g.live && t0 + j < a.L) st_row<R>(py + (t0 + j) * rs, R::pack(o));
-        }
-        if constexpr (GATE) {
-            if (tb + TB < a.L) load(t0 + TB, pz, rz);
+        for (int c = 0; c < VEC; ++c) {
+            const float la2 = k[c] * sigmoid_f(r[c]);
+            const float e = hw_exp2(la2);
+            const float n = sqrt_f(one_minus_square(la2, e));
+            A[j][c] = in ? (cut ? 0.f : e) : 1.f;
+            B[j][c] = in ? n * sigmoid_f(i[c]) * x[c] : 0.f;
+            H[c] = apply<RESET>(A[j][c], H[c], B[j][c]);
+            P[c] *= A[j][c];
         }
     }
-    if (a.h_last && g.live && g.wave == 0 && g.rg == 0) {
+    // inclusive scan over the wave's time groups, then the wave's total to LDS
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) a.h_last[(int64_t)g.b * a.Dn + g.ch + c] = carry[c];
+    for (int off = LC; off < 64; off <<= 1) {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            const float Pu = __shfl_up(P[c], off), Hu = __shfl_up(H[c], off);
+            if (g.lane >= off) {
+                H[c] = apply<RESET>(P[c], Hu, H[c]);
+                P[c] *= Pu;
+            }
+        }
+    }
+    if (g.rg == RG - 1) {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) s_sum[g.wave][g.lc * VEC + c] = make_float2(P[c], H[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {  // exclusive
+        P[c] = __shfl_up(P[c], LC);
+        H[c] = __shfl_up(H[c], LC);
+        if (g.rg == 0) P[c] = 1.f, H[c] = 0.f;
+    }
+    __syncthreads();
+    if (threadIdx.x < G::CH) {  // one lane a channel: publish, look back, publish
+        const Chain cn = chain_of(a, chain, threadIdx.x, G::CH);
+        const bool last = blk == a.blocks - 1;
+        float bp = 1.f, bh = 0.f, hb;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float2 q = s_sum[w][threadIdx.x];
+            bh = apply<RESET>(q.x, bh, q.y);
+            bp *= q.x;
+        }
+        if (blk > 0) {
+            if (!last) cn.publish_map(blk, bp, bh);
+            hb = cn.before<RESET>(blk);
+        } else {
+            hb = a.h0 ? a.h0[(int64_t)g.b * a.Dn + slot_channel<G>(a, chain)] : 0.f;
+        }
+        const float after = apply<RESET>(bp, hb, bh);
+        if (!last) cn.publish_state(blk, after);
+        else if (a.h_last) a.h_last[(int64_t)g.b * a.Dn + slot_channel<G>(a, chain)] = after;
+        s_h[threadIdx.x] = hb;
+    }
+    __syncthreads();
+    float h[VEC];
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) h[c] = s_h[g.lc * VEC + c];
+    for (int w = 0; w < g.wave; ++w) {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            const float2 q = s_sum[w][g.lc * VEC + c];
+            h[c] = apply<RESET>(q.x, h[c], q.y);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) h[c] = apply<RESET>(P[c], h[c], H[c]);
+    if (!g.live || mine <= 0) return;
+    if (a.states && g.rg * TAU % kGatedBlock == 0) {
+        float* st = a.states +
+                    ((int64_t)g.b * a.nstates + (tw + g.rg * TAU) / kGatedBlock) * a.Dn + g.ch;
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) st[c] = h[c];
+    }
+    char* py = g.row(a, a.y, tw);
+#pragma unroll
+    for (int j = 0; j < TAU; ++j) {
+        float o[VEC];
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            h[c] = apply<RESET>(A[j][c], h[c], B[j][c]);
+            o[c] = h[c];
+        }
+        if constexpr (GATE) {
+            float z[VEC];
+            R::unpack(rz[j], z);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) o[c] *= silu_f(z[c]);
+        }
+        if (j < mine) st_row<R>(py, g.at(j, left), R::pack(o));
     }
 }
 
 // ---- backward -----------------------------------------------------------------------
-// The same walk from the end of the sequence.  Each wave starts its forward
+// The same blocks from the end of the sequence.  Each wave starts its forward
 // recurrence from the state saved before its first step, so only the message
-// A_t g_t travels between waves (through LDS) and blocks (in registers).
-template <int VEC, bool BF16, bool GATE, bool RESET>
-__global__ void __launch_bounds__(64 * kWaves) gated_bwd(GatedArgs a) {
-    using S = Shape<VEC, BF16>;
-    using R = RowIo<VEC, BF16>;
+// A_t g_t travels between waves (through LDS) and blocks.
+template <class G, bool GATE, bool RESET>
+__global__ void __launch_bounds__(64 * G::W) gated_bwd(GatedArgs a) {
+    constexpr int VEC = G::VEC, LC = G::LC, RG = G::RG, TAU = G::TAU, TW = G::TW, TB = G::TB,
+                  W = G::W;
+    using R = RowIo<VEC, G::BF16>;
     using T = typename R::T;
-    using E = typename R::E;
-    constexpr int TAU = VEC == 4 ? 4 : 16;
-    constexpr int LC = S::LC, RG = S::RG, TW = TAU * RG, TB = TW * kWaves;
     static_assert(TW == kGatedBlock, "a wave starts at a saved state");
-    __shared__ float2 s_sum[2][kWaves][S::CH];
-    __shared__ float s_lam[kWaves][S::CH];
-    const Lane<S> g(a);
-    auto in_ptr = [&](const void* p) { return static_cast<const E*>(p) + g.base; };
-    auto out_ptr = [&](void* p) { return static_cast<E*>(p) + g.base; };
-    const E *px = in_ptr(a.x), *pr = in_ptr(a.r), *pi = in_ptr(a.i), *pz = in_ptr(a.z),
-            *pg = in_ptr(a.dy);
-    E *ox = out_ptr(a.dx), *orr = out_ptr(a.dr), *oi = out_ptr(a.di), *oz = out_ptr(a.dz);
-    const int64_t rs = a.Dn;
+    __shared__ float2 s_sum[W][G::CH];
+    __shared__ float s_h[G::CH];
+    __shared__ float s_lam[W][G::CH];
+    uint32_t chain;
+    int64_t turn;  // this block's place from the end
+    take_work(a, chain, turn);
+    const int64_t blk = a.blocks - 1 - turn;
+    const Lane<G> g(a, chain);
+    const int64_t tw = blk * TB + g.wave * TW;
+    const int64_t tr = min(tw, a.L - 1);
+    const int left = (int)min(a.L - tr, (int64_t)TW);
+    const int mine = (int)min(a.L - tw, (int64_t)TW) - g.rg * TAU;
 
-    float k[VEC], carry[VEC], dlam[VEC];
+    T rx[TAU], rr[TAU], ri[TAU], rz[TAU], ry[TAU];
+    auto load = [&](const void* p, T(&w)[TAU]) {
+        const char* q = g.row(a, p, tr);
+#pragma unroll
+        for (int j = 0; j < TAU; ++j) w[j] = ld_row<R>(q, g.at(j, left));
+    };
+    load(a.r, rr);
+    load(a.i, ri);
+    load(a.x, rx);
+    float h[VEC];
+    const float* st = a.states + ((int64_t)g.b * a.nstates + tr / kGatedBlock) * a.Dn + g.ch;
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) h[c] = st[c];
+    load(a.dy, ry);
+    if constexpr (GATE) load(a.z, rz);
+    float k[VEC], dlam[VEC];
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
         k[c] = -a.sharp * kLog2e * softplus_rel(a.lam[g.ch + c]);
-        carry[c] = a.dh_last ? a.dh_last[(int64_t)g.b * a.Dn + g.ch + c] : 0.f;
         dlam[c] = 0.f;
     }
-    int par = 0;
-    const int64_t nb = (a.L + TB - 1) / TB;
-    for (int64_t blk = nb - 1; blk >= 0; --blk, par ^= 1) {
-        const int64_t tw = blk * TB + g.wave * TW;  // the wave's first step
-        const int64_t t0 = tw + g.rg * TAU;
-        T rx[TAU], rr[TAU], ri[TAU], rz[TAU], rg_[TAU];
+    // forward: A, h_{t-1}
+    float sr[TAU][VEC], e[TAU][VEC], A[TAU][VEC], hp[TAU][VEC], n[TAU][VEC], si[TAU][VEC];
+    float P[VEC], H[VEC];
 #pragma unroll
-        for (int j = 0; j < TAU; ++j) {
-            const int64_t o = min(t0 + j, a.L - 1) * rs;
-            rx[j] = ld_row<R>(px + o);
-            rr[j] = ld_row<R>(pr + o);
-            ri[j] = ld_row<R>(pi + o);
-            rg_[j] = ld_row<R>(pg + o);
-            if constexpr (GATE) rz[j] = ld_row<R>(pz + o);
-        }
-        // forward: A, h_{t-1}
-        float sr[TAU][VEC], e[TAU][VEC], A[TAU][VEC], hp[TAU][VEC], n[TAU][VEC], si[TAU][VEC];
-        float P[VEC], H[VEC], h[VEC];
+    for (int c = 0; c < VEC; ++c) P[c] = 1.f, H[c] = 0.f;
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) P[c] = 1.f, H[c] = 0.f;
-        bool in[TAU];
-#pragma unroll
-        for (int j = 0; j < TAU; ++j) {
-            in[j] = t0 + j < a.L;
-            bool cut = false;
-            if constexpr (RESET) cut = in[j] && a.reset[(int64_t)g.b * a.L + t0 + j] != 0;
-            float x[VEC], r[VEC], i[VEC];
-            R::unpack(rx[j], x);
-            R::unpack(rr[j], r);
-            R::unpack(ri[j], i);
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                sr[j][c] = sigmoid_f(r[c]);
-                si[j][c] = sigmoid_f(i[c]);
-                const float la2 = k[c] * sr[j][c];
-                e[j][c] = hw_exp2(la2);
-                n[j][c] = sqrt_f(one_minus_square(la2, e[j][c]));
-                A[j][c] = in[j] ? (cut ? 0.f : e[j][c]) : 1.f;
-                H[c] = apply<RESET>(A[j][c], H[c], in[j] ? n[j][c] * si[j][c] * x[c] : 0.f);
-                P[c] *= A[j][c];
-            }
-        }
-#pragma unroll
-        for (int off = LC; off < 64; off <<= 1) {
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                const float Pu = __shfl_up(P[c], off), Hu = __shfl_up(H[c], off);
-                if (g.lane >= off) {
-                    H[c] = apply<RESET>(P[c], Hu, H[c]);
-                    P[c] *= Pu;
-                }
-            }
-        }
-        {
-            const int64_t sb = min(tw / kGatedBlock, a.nstates - 1);  // past the end: unused
-            const float* st = a.states + ((int64_t)g.b * a.nstates + sb) * a.Dn + g.ch;
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                float Pe = __shfl_up(P[c], LC), He = __shfl_up(H[c], LC);
-                if (g.rg == 0) Pe = 1.f, He = 0.f;
-                h[c] = apply<RESET>(Pe, st[c], He);
-            }
-        }
-        // h_{t-1} of every step, dz, and the gradient arriving at h_t from y_t
-        float gh[TAU][VEC];
-#pragma unroll
-        for (int j = 0; j < TAU; ++j) {
-            float x[VEC], dy[VEC];
-            R::unpack(rx[j], x);
-            R::unpack(rg_[j], dy);
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                hp[j][c] = h[c];
-                h[c] = apply<RESET>(A[j][c], h[c], in[j] ? n[j][c] * si[j][c] * x[c] : 0.f);
-                gh[j][c] = in[j] ? dy[c] : 0.f;
-            }
-            if constexpr (GATE) {
-                float z[VEC], dz[VEC];
-                R::unpack(rz[j], z);
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) {
-                    const float sz = sigmoid_f(z[c]);
-                    dz[c] = dy[c] * h[c] * sz * fmaf(z[c], 1.f - sz, 1.f);
-                    gh[j][c] *= z[c] * sz;
-                    if (!in[j]) gh[j][c] = 0.f;
-                }
-                if (g.live && in[j]) st_row<R>(oz + (t0 + j) * rs, R::pack(dz));
-            }
-        }
-        // the message to the step before the lane: c_out = P c_in + C
-        float C[VEC];
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) P[c] = 1.f, C[c] = 0.f;
-#pragma unroll
-        for (int j = TAU - 1; j >= 0; --j) {
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                C[c] = apply<RESET>(A[j][c], gh[j][c] + C[c], 0.f);
-                P[c] *= A[j][c];
-            }
-        }
-#pragma unroll
-        for (int off = LC; off < 64; off <<= 1) {
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                const float Pd = __shfl_down(P[c], off), Cd = __shfl_down(C[c], off);
-                if (g.lane + off < 64) {
-                    C[c] = apply<RESET>(P[c], Cd, C[c]);
-                    P[c] *= Pd;
-                }
-            }
-        }
-        if (g.rg == 0) {
-#pragma unroll
-            for (int c = 0; c < VEC; ++c)
-                s_sum[par][g.wave][g.lc * VEC + c] = make_float2(P[c], C[c]);
-        }
+    for (int j = 0; j < TAU; ++j) {
+        const bool in = j < mine;
+        bool cut = false;
+        if constexpr (RESET) cut = in && a.reset[(int64_t)g.b * a.L + tw + g.rg * TAU + j] != 0;
+        float x[VEC], r[VEC], i[VEC];
+        R::unpack(rx[j], x);
+        R::unpack(rr[j], r);
+        R::unpack(ri[j], i);
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
-            P[c] = __shfl_down(P[c], LC);
-            C[c] = __shfl_down(C[c], LC);
-            if (g.rg == RG - 1) P[c] = 1.f, C[c] = 0.f;
+            sr[j][c] = sigmoid_f(r[c]);
+            si[j][c] = sigmoid_f(i[c]);
+            const float la2 = k[c] * sr[j][c];
+            e[j][c] = hw_exp2(la2);
+            n[j][c] = sqrt_f(one_minus_square(la2, e[j][c]));
+            A[j][c] = in ? (cut ? 0.f : e[j][c]) : 1.f;
+            H[c] = apply<RESET>(A[j][c], H[c], in ? n[j][c] * si[j][c] * x[c] : 0.f);
+            P[c] *= A[j][c];
         }
-        __syncthreads();
-        float m[VEC];  // the message arriving from the step after the lane's last
+    }
 #pragma unroll
-        for (int w = kWaves - 1; w >= 0; --w) {
-            if (w == g.wave) {
+    for (int off = LC; off < 64; off <<= 1) {
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) m[c] = apply<RESET>(P[c], carry[c], C[c]);
-            }
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                const float2 q = s_sum[par][w][g.lc * VEC + c];
-                carry[c] = apply<RESET>(q.x, carry[c], q.y);
-            }
-        }
-#pragma unroll
-        for (int j = TAU - 1; j >= 0; --j) {
-            float x[VEC], dx[VEC], dr[VEC], di[VEC];
-            R::unpack(rx[j], x);
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                const float gt = gh[j][c] + m[c];  // dL/dh_t
-                m[c] = apply<RESET>(A[j][c], gt, 0.f);
-                const float s = si[j][c], la = k[c] * kLn2 * sr[j][c];
-                const float ratio = n[j][c] > 0.f ? la * hw_rcp(n[j][c]) : 0.f;
-                const float keep = apply<RESET>(A[j][c], hp[j][c], 0.f) * la;
-                const float q = gt * fmaf(-s * x[c] * e[j][c], e[j][c] * ratio, keep);
-                dx[c] = gt * n[j][c] * s;
-                di[c] = dx[c] * x[c] * (1.f - s);
-                dr[c] = q * (1.f - sr[j][c]);
-                dlam[c] += in[j] ? q : 0.f;
-            }
-            if (g.live && in[j]) {
-                st_row<R>(ox + (t0 + j) * rs, R::pack(dx));
-                st_row<R>(orr + (t0 + j) * rs, R::pack(dr));
-                st_row<R>(oi + (t0 + j) * rs, R::pack(di));
+        for (int c = 0; c < VEC; ++c) {
+            const float Pu = __shfl_up(P[c], off), Hu = __shfl_up(H[c], off);
+            if (g.lane >= off) {
+                H[c] = apply<RESET>(P[c], Hu, H[c]);
+                P[c] *= Pu;
             }
         }
     }
-    if (a.dh0 && g.live && g.wave == 0 && g.rg == 0) {
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) a.dh0[(int64_t)g.b * a.Dn + g.ch + c] = carry[c];
+    for (int c = 0; c < VEC; ++c) {
+        float Pe = __shfl_up(P[c], LC), He = __shfl_up(H[c], LC);
+        if (g.rg == 0) Pe = 1.f, He = 0.f;
+        h[c] = apply<RESET>(Pe, h[c], He);
+    }
+    // h_{t-1} of every step, dz, and the gradient arriving at h_t from y_t
+    float gh[TAU][VEC];
+    char* oz = g.row(a, a.dz, tw);
+#pragma unroll
+    for (int j = 0; j < TAU; ++j) {
+        const bool in = j < mine;
+        float x[VEC], dy[VEC];
+        R::unpack(rx[j], x);
+        R::unpack(ry[j], dy);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            hp[j][c] = h[c];
+            h[c] = apply<RESET>(A[j][c], h[c], in ? n[j][c] * si[j][c] * x[c] : 0.f);
+            gh[j][c] = dy[c];
+        }
+        if constexpr (GATE) {
+            float z[VEC], dz[VEC];
+            R::unpack(rz[j], z);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                const float sz = sigmoid_f(z[c]);
+                dz[c] = dy[c] * h[c] * sz * fmaf(z[c], 1.f - sz, 1.f);
+                gh[j][c] *= z[c] * sz;
+            }
+            if (g.live && in) st_row<R>(oz, g.at(j, left), R::pack(dz));
+        }
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) gh[j][c] = in ? gh[j][c] : 0.f;
+    }
+    // the message to the step before the lane: c_out = P c_in + C
+    float C[VEC];
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) P[c] = 1.f, C[c] = 0.f;
+#pragma unroll
+    for (int j = TAU - 1; j >= 0; --j) {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            C[c] = apply<RESET>(A[j][c], gh[j][c] + C[c], 0.f);
+            P[c] *= A[j][c];
+        }
+    }
+#pragma unroll
+    for (int off = LC; off < 64; off <<= 1) {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            const float Pd = __shfl_down(P[c], off), Cd = __shfl_down(C[c], off);
+            if (g.lane + off < 64) {
+                C[c] = apply<RESET>(P[c], Cd, C[c]);
+                P[c] *= Pd;
+            }
+        }
+    }
+    if (g.rg == 0) {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) s_sum[g.wave][g.lc * VEC + c] = make_float2(P[c], C[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+        P[c] = __shfl_down(P[c], LC);
+        C[c] = __shfl_down(C[c], LC);
+        if (g.rg == RG - 1) P[c] = 1.f, C[c] = 0.f;
+    }
+    __syncthreads();
+    if (threadIdx.x < G::CH) {  // one lane a channel: publish, look back, publish
+        const Chain cn = chain_of(a, chain, threadIdx.x, G::CH);
+        const bool last = blk == 0;
+        float bp = 1.f, bc = 0.f, cb;
+#pragma unroll
+        for (int w = W - 1; w >= 0; --w) {
+            const float2 q = s_sum[w][threadIdx.x];
+            bc = apply<RESET>(q.x, bc, q.y);
+            bp *= q.x;
+        }
+        if (turn > 0) {
+            if (!last) cn.publish_map(turn, bp, bc);
+            cb = cn.before<RESET>(turn);
+        } else {
+            cb = a.dh_last ? a.dh_last[(int64_t)g.b * a.Dn + slot_channel<G>(a, chain)] : 0.f;
+        }
+        const float out = apply<RESET>(bp, cb, bc);
+        if (!last) cn.publish_state(turn, out);
+        else if (a.dh0) a.dh0[(int64_t)g.b * a.Dn + slot_channel<G>(a, chain)] = out;
+        s_h[threadIdx.x] = cb;
+    }
+    __syncthreads();
+    float m[VEC];  // the message arriving from the step after the lane's last
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) m[c] = s_h[g.lc * VEC + c];
+    for (int w = W - 1; w > g.wave; --w) {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            const float2 q = s_sum[w][g.lc * VEC + c];
+            m[c] = apply<RESET>(q.x, m[c], q.y);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) m[c] = apply<RESET>(P[c], m[c], C[c]);
+    char *ox = g.row(a, a.dx, tw), *orr = g.row(a, a.dr, tw), *oi = g.row(a, a.di, tw);
+#pragma unroll
+    for (int j = TAU - 1; j >= 0; --j) {
+        const bool in = j < mine;
+        float x[VEC], dx[VEC], dr[VEC], di[VEC];
+        R::unpack(rx[j], x);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            const float gt = gh[j][c] + m[c];  // dL/dh_t
+            m[c] = apply<RESET>(A[j][c], gt, 0.f);
+            const float s = si[j][c], la = k[c] * kLn2 * sr[j][c];
+            const float ratio = n[j][c] > 0.f ? la * hw_rcp(n[j][c]) : 0.f;
+            const float keep = apply<RESET>(A[j][c], hp[j][c], 0.f) * la;
+            const float q = gt * fmaf(-s * x[c] * e[j][c], e[j][c] * ratio, keep);
+            dx[c] = gt * n[j][c] * s;
+            di[c] = dx[c] * x[c] * (1.f - s);
+            dr[c] = q * (1.f - sr[j][c]);
+            dlam[c] += in ? q : 0.f;
+        }
+        if (g.live && in) {
+            const uint32_t o = g.at(j, left);
+            st_row<R>(ox, o, R::pack(dx));
+            st_row<R>(orr, o, R::pack(dr));
+            st_row<R>(oi, o, R::pack(di));
+        }
     }
     // sum of q over the lane groups (shuffles) and the waves (LDS)
 #pragma unroll
@@ -509,23 +671,41 @@ __global__ void __launch_bounds__(64 * kWaves) gated_bwd(GatedArgs a) {
         for (int c = 0; c < VEC; ++c) s_lam[g.wave][g.lc * VEC + c] = dlam[c];
     }
     __syncthreads();
-    if (g.live && g.wave == 0 && g.rg == 0) {
+    if (threadIdx.x < G::CH && (int)(chain % tiles_of<G>(a)) * G::CH +
+                                       (int)threadIdx.x / VEC * VEC < a.Dn) {
+        float v = 0.f;
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) v += s_lam[w][g.lc * VEC + c];
-            a.part[(int64_t)g.b * a.Dn + g.ch + c] = v;
-        }
+        for (int w = 0; w < W; ++w) v += s_lam[w][threadIdx.x];
+        a.part[((int64_t)g.b * a.blocks + blk) * a.Dn + slot_channel<G>(a, chain)] = v;
     }
 }
 
-// dlam[d] = sigmoid/softplus(lam) * sum of the partials, in order
-__global__ void __launch_bounds__(256) gated_dlam(GatedArgs a, int64_t rows) {
-    const int d = blockIdx.x * 256 + threadIdx.x;
-    if (d >= a.Dn) return;
+// dlam[d] = sigmoid/softplus(lam) * sum of the partials over `rows`: 16 waves
+// take equal ranges of rows for 64 channels, joined in order.
+constexpr int kLamWaves = 16;
+__global__ void __launch_bounds__(64 * kLamWaves) gated_dlam(GatedArgs a, int64_t rows) {
+    __shared__ float s_v[kLamWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int d = blockIdx.x * 64 + lane;
+    const int64_t r0 = rows * wave / kLamWaves, r1 = rows * (wave + 1) / kLamWaves;
     float v = 0.f;
-    for (int64_t i = 0; i < rows; ++i) v += a.part[i * a.Dn + d];
+    if (d < a.Dn) {
+        int64_t i = r0;
+        for (; i + 8 <= r1; i += 8) {
+            float w[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) w[u] = a.part[(i + u) * a.Dn + d];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v += w[u];
+        }
+        for (; i < r1; ++i) v += a.part[i * a.Dn + d];
+    }
+    s_v[wave][lane] = v;
+    __syncthreads();
+    if (wave != 0 || d >= a.Dn) return;
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kLamWaves; ++w) v += s_v[w][lane];
     a.dlam[d] = v * sigmoid_over_softplus(a.lam[d]);
 }
 
@@ -562,58 +742,142 @@ __global__ void __launch_bounds__(256) gated_step(GatedArgs a, int64_t nvec) {
     static_cast<T*>(a.y)[v] = R::pack(o);
 }
 
-template <int VEC, bool BF16>
-unsigned gated_grid(const GatedArgs& a) {
-    constexpr int CH = Shape<VEC, BF16>::CH;
-    return (unsigned)((a.Dn + CH - 1) / CH) * (unsigned)a.batch;
+// ---- variants -------------------------------------------------------------------------
+template <bool BF16>
+using Fwd = Geo<4, 16, 8, 4, BF16>;
+template <bool BF16>
+using Bwd = Geo<4, 16, 4, 4, BF16>;
+// fewer than four channels
+template <bool BF16>
+using FwdOne = Geo<1, 4, 2, 8, BF16>;
+template <bool BF16>
+using BwdOne = Geo<1, 4, 1, 8, BF16>;
+
+// The sizes that a launch and its workspace go by.
+struct Cut {
+    int ch, tb, w;
+    int64_t chains, blocks;
+};
+template <class G>
+Cut cut_of(int batch, int64_t L, int Dn) {
+    return Cut{G::CH, G::TB, G::W, (int64_t)((Dn + G::CH - 1) / G::CH) * batch,
+               (L + G::TB - 1) / G::TB};
+}
+Cut fwd_cut(int batch, int64_t L, int Dn) {  // the same for both io types
+    return Dn < 4 ? cut_of<FwdOne<true>>(batch, L, Dn) : cut_of<Fwd<true>>(batch, L, Dn);
+}
+Cut bwd_cut(int batch, int64_t L, int Dn) {
+    return Dn < 4 ? cut_of<BwdOne<true>>(batch, L, Dn) : cut_of<Bwd<true>>(batch, L, Dn);
 }
 
-template <int VEC, bool BF16>
-void fwd_variant(const GatedArgs& a, hipStream_t s) {
-    const dim3 grid(gated_grid<VEC, BF16>(a)), blk(64 * kWaves);
-    if (a.z && a.reset) hipLaunchKernelGGL((gated_fwd<VEC, BF16, true, true>), grid, blk, 0, s, a);
-    else if (a.z) hipLaunchKernelGGL((gated_fwd<VEC, BF16, true, false>), grid, blk, 0, s, a);
-    else if (a.reset) hipLaunchKernelGGL((gated_fwd<VEC, BF16, false, true>), grid, blk, 0, s, a);
-    else hipLaunchKernelGGL((gated_fwd<VEC, BF16, false, false>), grid, blk, 0, s, a);
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+// Words between blocks: [ticket][state][map]; nothing for one block.
+struct Ws {
+    size_t state, map, words, total;
+};
+Ws ws_of(const Cut& c) {
+    Ws w{};
+    if (c.blocks < 2) return w;
+    w.words = (size_t)c.chains * (size_t)c.blocks * c.ch;
+    w.state = 256;
+    w.map = w.state + up256(w.words * 4);
+    w.total = w.map + up256(w.words * 8);
+    return w;
 }
 
-template <int VEC, bool BF16>
-void bwd_variant(const GatedArgs& a, hipStream_t s) {
-    const dim3 grid(gated_grid<VEC, BF16>(a)), blk(64 * kWaves);
-    if (a.z && a.reset) hipLaunchKernelGGL((gated_bwd<VEC, BF16, true, true>), grid, blk, 0, s, a);
-    else if (a.z) hipLaunchKernelGGL((gated_bwd<VEC, BF16, true, false>), grid, blk, 0, s, a);
-    else if (a.reset) hipLaunchKernelGGL((gated_bwd<VEC, BF16, false, true>), grid, blk, 0, s, a);
-    else hipLaunchKernelGGL((gated_bwd<VEC, BF16, false, false>), grid, blk, 0, s, a);
-}
-
-}  // namespace
-
-// Four channels a lane wherever there are four.  (h_last over h0 with a
-// channel count that four does not divide: a workgroup may store a shared
-// channel's h_last before its neighbour has read the h0 there.)
-static bool four_channels(const GatedArgs& a) {
-    return a.Dn % 4 == 0 || (a.Dn >= 4 && (!a.h0 || a.h0 != a.h_last));
-}
-
-size_t gated_bwd_part_floats(int batch, int64_t, int Dn) { return (size_t)batch * (size_t)Dn; }
-
-hipError_t launch_gated_fwd(const GatedArgs& a, bool bf16, hipStream_t s) {
-    ProfScope ps(s, kPhaseMain);
-    if (four_channels(a)) bf16 ? fwd_variant<4, true>(a, s) : fwd_variant<4, false>(a, s);
-    else bf16 ? fwd_variant<1, true>(a, s) : fwd_variant<1, false>(a, s);
+hipError_t prepare(GatedArgs& a, const Cut& c, void* workspace, hipStream_t s) {
+    a.blocks = c.blocks;
+    if (c.blocks < 2) return hipSuccess;
+    const Ws w = ws_of(c);
+    char* ws = static_cast<char*>(workspace);
+    a.ticket = reinterpret_cast<uint32_t*>(ws);
+    a.state = reinterpret_cast<uint32_t*>(ws + w.state);
+    a.map = reinterpret_cast<uint64_t*>(ws + w.map);
+    ProfScope ps(s, kPhasePrep);
+    const size_t n = (w.words + 255) / 256;
+    hipLaunchKernelGGL(gated_prepare, dim3((unsigned)(n < 2048 ? n : 2048)), dim3(256), 0, s, a,
+                       (int64_t)w.words);
     return hipGetLastError();
 }
 
-hipError_t launch_gated_bwd(const GatedArgs& a, bool bf16, hipStream_t s) {
+#define MS_GATED_VARIANT_(kernel, ...)                                                           \
+    do {                                                                                         \
+        if (a.z && a.reset) hipLaunchKernelGGL((kernel<__VA_ARGS__, true, true>), grid, blk, 0, s, a); \
+        else if (a.z) hipLaunchKernelGGL((kernel<__VA_ARGS__, true, false>), grid, blk, 0, s, a);      \
+        else if (a.reset) hipLaunchKernelGGL((kernel<__VA_ARGS__, false, true>), grid, blk, 0, s, a);  \
+        else hipLaunchKernelGGL((kernel<__VA_ARGS__, false, false>), grid, blk, 0, s, a);              \
+    } while (0)
+
+}  // namespace
+
+int64_t gated_workgroups(int batch, int64_t L, int Dn) {
+    const Cut f = fwd_cut(batch, L, Dn), b = bwd_cut(batch, L, Dn);
+    const double n = (double)f.chains * (double)f.blocks, m = (double)b.chains * (double)b.blocks;
+    return (int64_t)(n > m ? n : m);
+}
+
+// A channel count that four does not divide: some channels belong to two
+// lanes, maybe of two workgroups, and where h_last lies over h0 one may store
+// it before the other has read it.  Then h0 is copied first.
+static size_t start_bytes(int batch, int Dn) {
+    return Dn > 4 && Dn % 4 ? up256((size_t)batch * (size_t)Dn * 4) : 0;
+}
+
+size_t gated_fwd_ws(int batch, int64_t L, int Dn) {
+    return ws_of(fwd_cut(batch, L, Dn)).total + start_bytes(batch, Dn);
+}
+
+// The backward's partial sums of dlam follow its words.
+size_t gated_bwd_ws(int batch, int64_t L, int Dn) {
+    const Cut c = bwd_cut(batch, L, Dn);
+    return ws_of(c).total + up256((size_t)batch * (size_t)c.blocks * (size_t)Dn * 4);
+}
+
+hipError_t launch_gated_fwd(GatedArgs a, bool bf16, void* workspace, hipStream_t s) {
+    const Cut c = fwd_cut(a.batch, a.L, a.Dn);
+    const hipError_t e = prepare(a, c, workspace, s);
+    if (e != hipSuccess) return e;
+    if (a.h0 && a.h0 == a.h_last && start_bytes(a.batch, a.Dn)) {
+        float* start = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws_of(c).total);
+        const int64_t n = (int64_t)a.batch * a.Dn, g = (n + 255) / 256;
+        ProfScope ps(s, kPhasePrep);
+        hipLaunchKernelGGL(gated_copy, dim3((unsigned)(g < 2048 ? g : 2048)), dim3(256), 0, s,
+                           a.h0, start, n);
+        a.h0 = start;
+    }
+    ProfScope ps(s, kPhaseMain);
+    const dim3 grid((unsigned)(c.chains * c.blocks)), blk(64 * c.w);
+    if (a.Dn >= 4) {
+        if (bf16) MS_GATED_VARIANT_(gated_fwd, Fwd<true>);
+        else MS_GATED_VARIANT_(gated_fwd, Fwd<false>);
+    } else {
+        if (bf16) MS_GATED_VARIANT_(gated_fwd, FwdOne<true>);
+        else MS_GATED_VARIANT_(gated_fwd, FwdOne<false>);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_gated_bwd(GatedArgs a, bool bf16, void* workspace, hipStream_t s) {
+    const Cut c = bwd_cut(a.batch, a.L, a.Dn);
+    hipError_t e = prepare(a, c, workspace, s);
+    if (e != hipSuccess) return e;
+    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws_of(c).total);
     {
         ProfScope ps(s, kPhaseMain);
-        if (four_channels(a)) bf16 ? bwd_variant<4, true>(a, s) : bwd_variant<4, false>(a, s);
-        else bf16 ? bwd_variant<1, true>(a, s) : bwd_variant<1, false>(a, s);
+        const dim3 grid((unsigned)(c.chains * c.blocks)), blk(64 * c.w);
+        if (a.Dn >= 4) {
+            if (bf16) MS_GATED_VARIANT_(gated_bwd, Bwd<true>);
+            else MS_GATED_VARIANT_(gated_bwd, Bwd<false>);
+        } else {
+            if (bf16) MS_GATED_VARIANT_(gated_bwd, BwdOne<true>);
+            else MS_GATED_VARIANT_(gated_bwd, BwdOne<false>);
+        }
     }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     ProfScope ps(s, kPhaseReduce);
-    hipLaunchKernelGGL(gated_dlam, dim3((a.Dn + 255) / 256), dim3(256), 0, s, a, (int64_t)a.batch);
+    hipLaunchKernelGGL(gated_dlam, dim3((a.Dn + 63) / 64), dim3(64 * kLamWaves), 0, s, a,
+                       (int64_t)a.batch * a.blocks);
     return hipGetLastError();
 }
 

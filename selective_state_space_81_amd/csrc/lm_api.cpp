@@ -65,8 +65,10 @@ ms_status check_gated(int32_t batch, int64_t seqlen, int32_t d_inner, int32_t io
     if (d_inner < 1) return fail(MS_ERR_SHAPE, "d_inner=%d must be >= 1", d_inner);
     if ((double)batch * (double)seqlen * (double)d_inner > 0x1p56)
         return fail(MS_ERR_SHAPE, "batch x seqlen x d_inner exceeds 2^56");
-    if ((int64_t)batch * ((d_inner + 31LL) / 32) > kMax31)
-        return fail(MS_ERR_UNSUPPORTED, "batch x d_inner / 32 must be <= 2^31-1");
+    if ((d_inner + 63) / 64 > 65535 || batch > 65535)
+        return fail(MS_ERR_UNSUPPORTED, "d_inner/64 and batch must be <= 65535");
+    if (gated_workgroups(batch, seqlen, d_inner) > kMax31)
+        return fail(MS_ERR_UNSUPPORTED, "batch x seqlen x d_inner needs more than 2^31-1 workgroups");
     return check_io(io);
 }
 
@@ -75,8 +77,6 @@ ms_status check_sharpness(float c) {
         return fail(MS_ERR_SHAPE, "sharpness=%g must be > 0 and finite", (double)c);
     return MS_OK;
 }
-
-size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 int64_t state_rows(int64_t seqlen) { return (seqlen + kGatedBlock - 1) / kGatedBlock; }
 
@@ -116,7 +116,7 @@ extern "C" {
 
 size_t ms_gated_scan_workspace_bytes(int32_t batch, int64_t seqlen, int32_t d_inner, int32_t io) {
     if (check_gated(batch, seqlen, d_inner, io) != MS_OK) return (size_t)-1;
-    return 0;
+    return gated_fwd_ws(batch, seqlen, d_inner);
 }
 
 size_t ms_gated_scan_states_bytes(int32_t batch, int64_t seqlen, int32_t d_inner) {
@@ -144,13 +144,13 @@ ms_status ms_gated_scan_fwd(const void* x, const void* r, const void* i, const f
     a.h_last = h_last; a.states = states; a.sharp = sharpness; a.L = seqlen;
     a.nstates = state_rows(seqlen); a.batch = batch; a.Dn = d_inner;
     prof_call();
-    return launched(launch_gated_fwd(a, io == MS_BF16, static_cast<hipStream_t>(stream)));
+    return launched(launch_gated_fwd(a, io == MS_BF16, workspace, static_cast<hipStream_t>(stream)));
 }
 
 size_t ms_gated_scan_bwd_workspace_bytes(int32_t batch, int64_t seqlen, int32_t d_inner,
                                          int32_t io) {
     if (check_gated(batch, seqlen, d_inner, io) != MS_OK) return (size_t)-1;
-    return round256(gated_bwd_part_floats(batch, seqlen, d_inner) * sizeof(float));
+    return gated_bwd_ws(batch, seqlen, d_inner);
 }
 
 ms_status ms_gated_scan_bwd(const void* x, const void* r, const void* i, const float* lam,
@@ -176,10 +176,10 @@ ms_status ms_gated_scan_bwd(const void* x, const void* r, const void* i, const f
     a.x = x; a.r = r; a.i = i; a.z = z; a.lam = lam; a.reset = reset; a.dy = dy;
     a.states = const_cast<float*>(states);  // only read
     a.dh_last = dh_last; a.dx = dx; a.dr = dr; a.di = di; a.dz = dz; a.dlam = dlam; a.dh0 = dh0;
-    a.part = static_cast<float*>(workspace); a.sharp = sharpness; a.L = seqlen;
+    a.sharp = sharpness; a.L = seqlen;
     a.nstates = state_rows(seqlen); a.batch = batch; a.Dn = d_inner;
     prof_call();
-    return launched(launch_gated_bwd(a, io == MS_BF16, static_cast<hipStream_t>(stream)));
+    return launched(launch_gated_bwd(a, io == MS_BF16, workspace, static_cast<hipStream_t>(stream)));
 }
 
 ms_status ms_gated_step(float* h, const void* x_t, const void* r_t, const void* i_t,

@@ -11,7 +11,7 @@ namespace msscan {
 
 // ---- gated linear recurrence (gated_scan.hip) --------------------------------
 // Saved states: h before every kGatedBlock-th step, [batch][ceil(L/kGatedBlock)][Dn].
-constexpr int kGatedBlock = 32;
+constexpr int kGatedBlock = 16;
 
 struct GatedArgs {
     const void* x;
@@ -33,7 +33,12 @@ struct GatedArgs {
     void* dz;
     float* dlam;
     float* dh0;   // or null
-    float* part;  // workspace: partial sums of dlam, [batch][Dn]
+    float* part;  // workspace: partial sums of dlam, [batch][blocks][Dn]
+    // workspace of blocks on workgroups of their own
+    uint32_t* ticket;  // work handed out
+    uint32_t* state;   // [chains][blocks][channels of a chain]: state after a block
+    uint64_t* map;     // the same: what a block does to a state
+    int64_t blocks;    // blocks of a chain
     float sharp;
     int64_t L;
     int64_t nstates;  // ceil(L / kGatedBlock)
@@ -41,9 +46,11 @@ struct GatedArgs {
     int Dn;
 };
 
-size_t gated_bwd_part_floats(int batch, int64_t L, int Dn);
-hipError_t launch_gated_fwd(const GatedArgs& a, bool bf16, hipStream_t s);
-hipError_t launch_gated_bwd(const GatedArgs& a, bool bf16, hipStream_t s);
+int64_t gated_workgroups(int batch, int64_t L, int Dn);  // of the larger of both passes
+size_t gated_fwd_ws(int batch, int64_t L, int Dn);  // bytes
+size_t gated_bwd_ws(int batch, int64_t L, int Dn);
+hipError_t launch_gated_fwd(GatedArgs a, bool bf16, void* workspace, hipStream_t s);
+hipError_t launch_gated_bwd(GatedArgs a, bool bf16, void* workspace, hipStream_t s);
 // One step: a.h_last is the state [batch][Dn], updated in place; L is 1.
 hipError_t launch_gated_step(const GatedArgs& a, bool bf16, hipStream_t s);
 

@@ -21,7 +21,7 @@ EXPORTS = ("ms_gated_scan_workspace_bytes", "ms_gated_scan_states_bytes", "ms_ga
            "ms_embed_fwd", "ms_embed_bwd_workspace_bytes", "ms_embed_bwd",
            "ms_token_logprobs_workspace_bytes", "ms_token_logprobs_fwd", "ms_token_logprobs_bwd")
 
-GATED_BLOCK = 32  # steps between the saved states of the gated scan
+GATED_BLOCK = 16  # steps between the saved states of the gated scan
 MAX_TOP = 64      # most alternatives of token_logprobs
 
 
@@ -142,7 +142,7 @@ def gated_scan_bwd_workspace_bytes(batch: int, seqlen: int, d_inner: int, io: in
 
 def gated_scan_states(x, stream=None):
     """An empty buffer for the states that gated_scan_fwd saves for
-    gated_scan_bwd: [batch, ceil(L / 32), d_inner] fp32."""
+    gated_scan_bwd: [batch, ceil(L / 16), d_inner] fp32."""
     import torch
     b, L, d = x.shape
     return _Call(x, stream).empty((b, -(-L // GATED_BLOCK), d), torch.float32)

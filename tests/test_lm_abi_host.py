@@ -13,8 +13,8 @@ P = 16  # an aligned address that is never read
 
 def test_sizes():
     lib = ms.load()
-    assert lib.ms_gated_scan_states_bytes(2, 33, 5) == 2 * 2 * 5 * 4
-    assert lib.ms_gated_scan_states_bytes(1, 32, 8) == 8 * 4
+    assert lib.ms_gated_scan_states_bytes(2, 33, 5) == 2 * 3 * 5 * 4
+    assert lib.ms_gated_scan_states_bytes(1, 16, 8) == 8 * 4
     for bad in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (-1, 5, 5), (1, 1 << 31, 1)):
         assert lib.ms_gated_scan_states_bytes(*bad) == NONE
         assert lib.ms_gated_scan_workspace_bytes(*bad, 1) == NONE
