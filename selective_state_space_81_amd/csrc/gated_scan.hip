@@ -39,12 +39,13 @@ using namespace dev;
 // Rows of an odd channel count are aligned to their element only, so the
 // vector accesses assume no more (gfx950 serves them unaligned).
 template <int VEC, bool BF16>
-struct RowIo;
+struct RowIo;  // out(): every value -infinity
 template <>
 struct RowIo<4, true> {
     typedef uint16_t E;
     typedef uint32_t T __attribute__((ext_vector_type(2)));
     typedef T M __attribute__((aligned(2)));
+    static __device__ __forceinline__ T out() { return T{0xff80ff80u, 0xff80ff80u}; }
     static __device__ __forceinline__ void unpack(T w, float (&v)[4]) {
         v[0] = __uint_as_float(w[0] << 16);
         v[1] = __uint_as_float(w[0] & 0xffff0000u);
@@ -61,6 +62,7 @@ struct RowIo<1, true> {
     typedef uint16_t E;
     typedef uint16_t T;
     typedef T M;
+    static __device__ __forceinline__ T out() { return 0xff80; }
     static __device__ __forceinline__ void unpack(T w, float (&v)[1]) {
         v[0] = __uint_as_float((uint32_t)w << 16);
     }
@@ -71,6 +73,10 @@ struct RowIo<4, false> {
     typedef float E;
     typedef float T __attribute__((ext_vector_type(4)));
     typedef T M __attribute__((aligned(4)));
+    static __device__ __forceinline__ T out() {
+        const float f = -__builtin_inff();
+        return T{f, f, f, f};
+    }
     static __device__ __forceinline__ void unpack(T w, float (&v)[4]) {
         v[0] = w[0], v[1] = w[1], v[2] = w[2], v[3] = w[3];
     }
@@ -83,6 +89,7 @@ struct RowIo<1, false> {
     typedef float E;
     typedef float T;
     typedef T M;
+    static __device__ __forceinline__ T out() { return -__builtin_inff(); }
     static __device__ __forceinline__ void unpack(T w, float (&v)[1]) { v[0] = w; }
     static __device__ __forceinline__ T pack(const float (&v)[1]) { return v[0]; }
 };
@@ -110,17 +117,16 @@ __device__ __forceinline__ float sigmoid_over_softplus(float v) {
     return 1.f / ((1.f + expf(-v)) * softplus_rel(v));
 }
 
-// 1 - a^2 for a = 2^la2.  With x = ln(a^2) in (-1/8, 0] the series of
-// -expm1(x) to x^5 (the next term is below 3e-8 relative); further out
+// 1 - a^2 for a = 2^t.  For ln(a^2) in (-1/8, 0] -t times a cubic in t fitted
+// to (1 - 4^t) / -t there (Chebyshev nodes, 1.6e-08 relative); further out
 // 1 - a^2 itself, whose cancellation costs at most 8 rounding errors of a^2
 // (5e-7 relative, halved by the root).
-__device__ __forceinline__ float one_minus_square(float la2, float a) {
-    const float x = la2 * (2.f * kLn2);
-    float p = fmaf(x, 1.f / 120.f, 1.f / 24.f);
-    p = fmaf(x, p, 1.f / 6.f);
-    p = fmaf(x, p, 0.5f);
-    p = fmaf(x, p, 1.f);
-    return x > -0.125f ? -x * p : fmaf(-a, a, 1.f);
+constexpr float kSquareNear = 0.0901684401f;
+__device__ __forceinline__ float one_minus_square(float t, float a) {
+    float p = fmaf(t, 0.146416157f, 0.443615764f);
+    p = fmaf(t, p, 0.960898519f);
+    p = fmaf(t, p, 1.38629436f);
+    return t > -kSquareNear ? -t * p : fmaf(-a, a, 1.f);
 }
 
 __device__ __forceinline__ float sqrt_f(float v) { return __builtin_amdgcn_sqrtf(v); }
@@ -134,6 +140,15 @@ __device__ __forceinline__ float apply(float P, float h, float H) {
     return v;
 }
 
+#ifndef GS_BT
+#define GS_BT 4
+#endif
+#ifndef GS_BW
+#define GS_BW 4
+#endif
+#ifndef GS_BO
+#define GS_BO 3
+#endif
 // ---- geometry -----------------------------------------------------------------------
 // VEC channels and TAU steps a lane, LC lanes across channels, W waves along
 // time.  BLOCKS: a workgroup takes one block of TB steps and gets the state
@@ -193,11 +208,28 @@ struct Lane {
     }
 };
 
-// The channel of slot threadIdx.x (lane lc's channel c is slot lc * VEC + c).
+// Where a wave's steps are in block blk (the same for every chain).
 template <class G>
-__device__ __forceinline__ int slot_channel(const GatedArgs& a, uint32_t chain) {
-    const int ch = (int)(chain % tiles_of<G>(a)) * G::CH + (int)threadIdx.x / G::VEC * G::VEC;
-    return min(ch, a.Dn - G::VEC) + (int)threadIdx.x % G::VEC;
+struct Place {
+    int64_t tw, tr;  // its first step; that step, or the last of all where it is past the end
+    int left;        // steps from tr on that exist, TW at most
+    bool ragged;     // not all of the wave's steps exist
+    int own;         // how many do (<= 0: none)
+    __device__ __forceinline__ Place(const GatedArgs& a, int64_t blk) {
+        tw = blk * G::TB + (int64_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * G::TW;
+        tr = min(tw, a.L - 1);
+        left = (int)min(a.L - tr, (int64_t)G::TW);
+        own = (int)min(a.L - tw, (int64_t)G::TW);
+        ragged = own < G::TW;
+    }
+    __device__ __forceinline__ int mine(const Lane<G>& g) const { return own - g.rg * G::TAU; }
+};
+
+// The channel of a chain's slot (lane lc's channel c is slot lc * VEC + c).
+template <class G>
+__device__ __forceinline__ int slot_channel(const GatedArgs& a, uint32_t chain, int slot) {
+    const int ch = (int)(chain % tiles_of<G>(a)) * G::CH + slot / G::VEC * G::VEC;
+    return min(ch, a.Dn - G::VEC) + slot % G::VEC;
 }
 
 // ---- the state between blocks -----------------------------------------------------------
@@ -213,22 +245,21 @@ __device__ __forceinline__ int slot_channel(const GatedArgs& a, uint32_t chain) 
 // single relaxed atomics at device scope: each carries its whole message, so
 // no fence orders anything else.
 constexpr uint32_t kNotYet = 0xffffffffu;
-constexpr int kWindow = 8;
+constexpr int kWindow = 4;
 
 __device__ __forceinline__ float plain_nan(float v) { return v == v ? v : __builtin_nanf(""); }
 
-__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ uint32_t peek(const uint32_t* p) {
+template <class T>
+__device__ __forceinline__ T peek(const T* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // State words of one chain: [block][CH], in the order blocks are taken.
+template <int stride>
 struct Chain {
     uint64_t* map;    // (P, H) of a block
     uint32_t* state;  // the state after a block
-    int ch, stride;   // this lane's channel, channels of a block
+    int ch;           // this lane's channel
 
     __device__ __forceinline__ void publish_map(int64_t blk, float P, float H) const {
         const uint64_t w = ((uint64_t)__float_as_uint(plain_nan(H)) << 32) |
@@ -239,17 +270,20 @@ struct Chain {
         __hip_atomic_store(state + blk * stride + ch, __float_as_uint(plain_nan(h)),
                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    // The state before block blk >= 1.
+    // The state before block blk >= 1.  The first block publishes a state and
+    // never a map, so what the window holds before it (another chain's words,
+    // or the room left in front of the first) is never taken.
     template <bool RESET>
     __device__ __forceinline__ float before(int64_t blk) const {
+        const uint32_t* ps = state + (blk - 1) * stride + ch;
+        const uint64_t* pm = map + (blk - 1) * stride + ch;
         for (;;) {
             uint32_t st[kWindow];
             uint64_t mp[kWindow];
 #pragma unroll
             for (int k = 0; k < kWindow; ++k) {
-                const int64_t j = max(blk - 1 - k, (int64_t)0) * stride + ch;
-                st[k] = peek(state + j);
-                mp[k] = peek(map + j);
+                st[k] = peek(ps - k * stride);
+                mp[k] = peek(pm - k * stride);
             }
             // nearest state; every map nearer than it has to be there
             int at = -1;
@@ -275,9 +309,10 @@ struct Chain {
     }
 };
 
-__device__ __forceinline__ Chain chain_of(const GatedArgs& a, uint32_t chain, int ch, int CH) {
-    return Chain{a.map + (int64_t)chain * a.blocks * CH, a.state + (int64_t)chain * a.blocks * CH,
-                 ch, CH};
+template <class G>
+__device__ __forceinline__ Chain<G::CH> chain_of(const GatedArgs& a, uint32_t chain) {
+    const int64_t at = (int64_t)chain * a.blocks * G::CH;
+    return Chain<G::CH>{a.map + at, a.state + at, (int)threadIdx.x};
 }
 
 // Nothing published, no work handed out.
@@ -296,52 +331,71 @@ __global__ void __launch_bounds__(256) gated_copy(const float* from, float* to, 
 }
 
 // This workgroup's chain and its turn in it: earlier turns of all chains first.
-__device__ __forceinline__ void take_work(const GatedArgs& a, uint32_t& chain, int64_t& turn) {
-    if (a.blocks == 1) {
-        chain = blockIdx.x;
-        turn = 0;
-        return;
-    }
+struct Work {
+    uint32_t chain;
+    int64_t turn;
+};
+__device__ __forceinline__ Work take_work(const GatedArgs& a) {
+    if (a.blocks == 1) return Work{blockIdx.x, 0};
     __shared__ uint32_t s_ticket;
     if (threadIdx.x == 0) s_ticket = atomicAdd(a.ticket, 1u);
     __syncthreads();
-    const uint32_t t = __builtin_amdgcn_readfirstlane(s_ticket);
-    const uint32_t chains = gridDim.x / (uint32_t)a.blocks;
-    chain = t % chains;
-    turn = t / chains;
+    const uint32_t t = __builtin_amdgcn_readfirstlane(s_ticket), turn = t / a.chains;
+    return Work{t - turn * a.chains, turn};
+}
+
+// -c log2 e softplus(lam) of the workgroup's channels, one a thread, for all
+// lanes through LDS (the logarithm would cost each lane VEC times over).
+template <class G>
+__device__ __forceinline__ void share_rates(const GatedArgs& a, uint32_t chain,
+                                            float (&s_k)[G::CH]) {
+    if (threadIdx.x < G::CH)
+        s_k[threadIdx.x] = -a.sharp * kLog2e *
+                           softplus_rel(a.lam[slot_channel<G>(a, chain, (int)threadIdx.x)]);
+}
+
+// Steps past the end of the sequence are given gates and inputs that make
+// them the identity: r = -infinity is a decay of exactly 1, and x = 0.
+template <class R, int TAU>
+__device__ __forceinline__ void pad_steps(int mine, typename R::T (&r)[TAU],
+                                          typename R::T (&x)[TAU]) {
+#pragma unroll
+    for (int j = 0; j < TAU; ++j)
+        if (j >= mine) r[j] = R::out(), x[j] = typename R::T{};
 }
 
 // ---- forward ------------------------------------------------------------------------
 template <class G, bool GATE, bool RESET>
-__global__ void __launch_bounds__(64 * G::W) gated_fwd(GatedArgs a) {
+__global__ void __launch_bounds__(64 * G::W, G::BF16 ? 3 : 2) gated_fwd(GatedArgs a) {
     constexpr int VEC = G::VEC, LC = G::LC, RG = G::RG, TAU = G::TAU, TW = G::TW, TB = G::TB,
                   W = G::W;
     using R = RowIo<VEC, G::BF16>;
     using T = typename R::T;
     __shared__ float2 s_sum[W][G::CH];
-    __shared__ float s_h[G::CH];
-    uint32_t chain;
-    int64_t blk;
-    take_work(a, chain, blk);
+    __shared__ float s_h[G::CH], s_k[G::CH];
+    const Work wk = take_work(a);
+    const uint32_t chain = wk.chain;
+    const int64_t blk = wk.turn;
+    const bool last = blk == a.blocks - 1;
     const Lane<G> g(a, chain);
-    const int64_t tw = blk * TB + g.wave * TW;  // the wave's first step
-    const int64_t tr = min(tw, a.L - 1);  // a wave past the end reads the last step
-    const int left = (int)min(a.L - tr, (int64_t)TW);
-    const int mine = (int)min(a.L - tw, (int64_t)TW) - g.rg * TAU;  // the lane's steps
+    const Place<G> pl(a, blk);
+    const int mine = pl.mine(g);
 
     T rx[TAU], rr[TAU], ri[TAU], rz[TAU];
     auto load = [&](const void* p, T(&w)[TAU]) {
-        const char* q = g.row(a, p, tr);
+        const char* q = g.row(a, p, pl.tr);
 #pragma unroll
-        for (int j = 0; j < TAU; ++j) w[j] = ld_row<R>(q, g.at(j, left));
+        for (int j = 0; j < TAU; ++j) w[j] = ld_row<R>(q, g.at(j, pl.left));
     };
     load(a.r, rr);
     load(a.i, ri);
     load(a.x, rx);
-    if constexpr (GATE) load(a.z, rz);
+    share_rates<G>(a, chain, s_k);
+    __syncthreads();
     float k[VEC];
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) k[c] = -a.sharp * kLog2e * softplus_rel(a.lam[g.ch + c]);
+    for (int c = 0; c < VEC; ++c) k[c] = s_k[g.lc * VEC + c];
+    if (pl.ragged) pad_steps<R, TAU>(mine, rr, rx);
 
     // the lane's steps as A[j], B[j] and composed as (P, H)
     float A[TAU][VEC], B[TAU][VEC], P[VEC], H[VEC];
@@ -349,9 +403,9 @@ __global__ void __launch_bounds__(64 * G::W) gated_fwd(GatedArgs a) {
     for (int c = 0; c < VEC; ++c) P[c] = 1.f, H[c] = 0.f;
 #pragma unroll
     for (int j = 0; j < TAU; ++j) {
-        const bool in = j < mine;
         bool cut = false;
-        if constexpr (RESET) cut = in && a.reset[(int64_t)g.b * a.L + tw + g.rg * TAU + j] != 0;
+        if constexpr (RESET)
+            cut = j < mine && a.reset[(int64_t)g.b * a.L + pl.tw + g.rg * TAU + j] != 0;
         float x[VEC], r[VEC], i[VEC];
         R::unpack(rx[j], x);
         R::unpack(rr[j], r);
@@ -361,12 +415,14 @@ __global__ void __launch_bounds__(64 * G::W) gated_fwd(GatedArgs a) {
             const float la2 = k[c] * sigmoid_f(r[c]);
             const float e = hw_exp2(la2);
             const float n = sqrt_f(one_minus_square(la2, e));
-            A[j][c] = in ? (cut ? 0.f : e) : 1.f;
-            B[j][c] = in ? n * sigmoid_f(i[c]) * x[c] : 0.f;
+            A[j][c] = cut ? 0.f : e;
+            B[j][c] = n * sigmoid_f(i[c]) * x[c];
             H[c] = apply<RESET>(A[j][c], H[c], B[j][c]);
             P[c] *= A[j][c];
         }
+        __builtin_amdgcn_sched_barrier(0);  // one step's temporaries at a time
     }
+    if constexpr (GATE) load(a.z, rz);  // needed last: travels during the exchange
     // inclusive scan over the wave's time groups, then the wave's total to LDS
 #pragma unroll
     for (int off = LC; off < 64; off <<= 1) {
@@ -381,7 +437,8 @@ __global__ void __launch_bounds__(64 * G::W) gated_fwd(GatedArgs a) {
     }
     if (g.rg == RG - 1) {
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) s_sum[g.wave][g.lc * VEC + c] = make_float2(P[c], H[c]);
+        for (int c = 0; c < VEC; ++c)
+            s_sum[g.wave][g.lc * VEC + c] = make_float2(P[c], H[c]);
     }
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {  // exclusive
@@ -391,24 +448,24 @@ __global__ void __launch_bounds__(64 * G::W) gated_fwd(GatedArgs a) {
     }
     __syncthreads();
     if (threadIdx.x < G::CH) {  // one lane a channel: publish, look back, publish
-        const Chain cn = chain_of(a, chain, threadIdx.x, G::CH);
-        const bool last = blk == a.blocks - 1;
+        const Chain<G::CH> cn = chain_of<G>(a, chain);
         float bp = 1.f, bh = 0.f, hb;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const float2 q = s_sum[w][threadIdx.x];
-            bh = apply<RESET>(q.x, bh, q.y);
-            bp *= q.x;
+            const float2 v = s_sum[w][threadIdx.x];
+            bh = apply<RESET>(v.x, bh, v.y);
+            bp *= v.x;
         }
+        const int64_t at = (int64_t)g.b * a.Dn + slot_channel<G>(a, chain, (int)threadIdx.x);
         if (blk > 0) {
             if (!last) cn.publish_map(blk, bp, bh);
-            hb = cn.before<RESET>(blk);
+            hb = cn.template before<RESET>(blk);
         } else {
-            hb = a.h0 ? a.h0[(int64_t)g.b * a.Dn + slot_channel<G>(a, chain)] : 0.f;
+            hb = a.h0 ? a.h0[at] : 0.f;
         }
         const float after = apply<RESET>(bp, hb, bh);
         if (!last) cn.publish_state(blk, after);
-        else if (a.h_last) a.h_last[(int64_t)g.b * a.Dn + slot_channel<G>(a, chain)] = after;
+        else if (a.h_last) a.h_last[at] = after;
         s_h[threadIdx.x] = hb;
     }
     __syncthreads();
@@ -418,35 +475,36 @@ __global__ void __launch_bounds__(64 * G::W) gated_fwd(GatedArgs a) {
     for (int w = 0; w < g.wave; ++w) {
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
-            const float2 q = s_sum[w][g.lc * VEC + c];
-            h[c] = apply<RESET>(q.x, h[c], q.y);
+            const float2 v = s_sum[w][g.lc * VEC + c];
+            h[c] = apply<RESET>(v.x, h[c], v.y);
         }
     }
 #pragma unroll
     for (int c = 0; c < VEC; ++c) h[c] = apply<RESET>(P[c], h[c], H[c]);
-    if (!g.live || mine <= 0) return;
-    if (a.states && g.rg * TAU % kGatedBlock == 0) {
-        float* st = a.states +
-                    ((int64_t)g.b * a.nstates + (tw + g.rg * TAU) / kGatedBlock) * a.Dn + g.ch;
+    if (g.live && mine > 0) {
+        if (a.states && g.rg * TAU % kGatedBlock == 0) {
+            const int64_t row = (int64_t)g.b * a.nstates + (pl.tw + g.rg * TAU) / kGatedBlock;
+            float* st = a.states + row * a.Dn + g.ch;
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) st[c] = h[c];
-    }
-    char* py = g.row(a, a.y, tw);
-#pragma unroll
-    for (int j = 0; j < TAU; ++j) {
-        float o[VEC];
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-            h[c] = apply<RESET>(A[j][c], h[c], B[j][c]);
-            o[c] = h[c];
+            for (int c = 0; c < VEC; ++c) st[c] = h[c];
         }
-        if constexpr (GATE) {
-            float z[VEC];
-            R::unpack(rz[j], z);
+        char* py = g.row(a, a.y, pl.tw);
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) o[c] *= silu_f(z[c]);
+        for (int j = 0; j < TAU; ++j) {
+            float o[VEC];
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                h[c] = apply<RESET>(A[j][c], h[c], B[j][c]);
+                o[c] = h[c];
+            }
+            if constexpr (GATE) {
+                float z[VEC];
+                R::unpack(rz[j], z);
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) o[c] *= silu_f(z[c]);
+            }
+            if (j < mine) st_row<R>(py, g.at(j, pl.left), R::pack(o));
         }
-        if (j < mine) st_row<R>(py, g.at(j, left), R::pack(o));
     }
 }
 
@@ -455,24 +513,22 @@ __global__ void __launch_bounds__(64 * G::W) gated_fwd(GatedArgs a) {
 // recurrence from the state saved before its first step, so only the message
 // A_t g_t travels between waves (through LDS) and blocks.
 template <class G, bool GATE, bool RESET>
-__global__ void __launch_bounds__(64 * G::W) gated_bwd(GatedArgs a) {
+__global__ void __launch_bounds__(64 * G::W, GS_BO) gated_bwd(GatedArgs a) {
     constexpr int VEC = G::VEC, LC = G::LC, RG = G::RG, TAU = G::TAU, TW = G::TW, TB = G::TB,
                   W = G::W;
     using R = RowIo<VEC, G::BF16>;
     using T = typename R::T;
-    static_assert(TW == kGatedBlock, "a wave starts at a saved state");
+    static_assert(TW % kGatedBlock == 0, "a wave starts at a saved state");
     __shared__ float2 s_sum[W][G::CH];
-    __shared__ float s_h[G::CH];
+    __shared__ float s_h[G::CH], s_k[G::CH];
     __shared__ float s_lam[W][G::CH];
-    uint32_t chain;
-    int64_t turn;  // this block's place from the end
-    take_work(a, chain, turn);
-    const int64_t blk = a.blocks - 1 - turn;
+    const Work wk = take_work(a);
+    const int64_t turn = wk.turn, blk = a.blocks - 1 - turn;  // turn 0 is the last block
+    const uint32_t chain = wk.chain;
+    const Place<G> pl(a, blk);
     const Lane<G> g(a, chain);
-    const int64_t tw = blk * TB + g.wave * TW;
-    const int64_t tr = min(tw, a.L - 1);
-    const int left = (int)min(a.L - tr, (int64_t)TW);
-    const int mine = (int)min(a.L - tw, (int64_t)TW) - g.rg * TAU;
+    const int64_t tw = pl.tw, tr = pl.tr;
+    const int left = pl.left, mine = pl.mine(g);
 
     T rx[TAU], rr[TAU], ri[TAU], rz[TAU], ry[TAU];
     auto load = [&](const void* p, T(&w)[TAU]) {
@@ -489,10 +545,16 @@ __global__ void __launch_bounds__(64 * G::W) gated_bwd(GatedArgs a) {
     for (int c = 0; c < VEC; ++c) h[c] = st[c];
     load(a.dy, ry);
     if constexpr (GATE) load(a.z, rz);
+    share_rates<G>(a, chain, s_k);
+    if (pl.ragged) {  // no gradient arrives at steps past the end either
+        pad_steps<R, TAU>(mine, rr, rx);
+        pad_steps<R, TAU>(mine, ry, ry);
+    }
+    __syncthreads();
     float k[VEC], dlam[VEC];
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
-        k[c] = -a.sharp * kLog2e * softplus_rel(a.lam[g.ch + c]);
+        k[c] = s_k[g.lc * VEC + c];
         dlam[c] = 0.f;
     }
     // forward: A, h_{t-1}
@@ -502,9 +564,9 @@ __global__ void __launch_bounds__(64 * G::W) gated_bwd(GatedArgs a) {
     for (int c = 0; c < VEC; ++c) P[c] = 1.f, H[c] = 0.f;
 #pragma unroll
     for (int j = 0; j < TAU; ++j) {
-        const bool in = j < mine;
         bool cut = false;
-        if constexpr (RESET) cut = in && a.reset[(int64_t)g.b * a.L + tw + g.rg * TAU + j] != 0;
+        if constexpr (RESET)
+            cut = j < mine && a.reset[(int64_t)g.b * a.L + tw + g.rg * TAU + j] != 0;
         float x[VEC], r[VEC], i[VEC];
         R::unpack(rx[j], x);
         R::unpack(rr[j], r);
@@ -516,10 +578,11 @@ __global__ void __launch_bounds__(64 * G::W) gated_bwd(GatedArgs a) {
             const float la2 = k[c] * sr[j][c];
             e[j][c] = hw_exp2(la2);
             n[j][c] = sqrt_f(one_minus_square(la2, e[j][c]));
-            A[j][c] = in ? (cut ? 0.f : e[j][c]) : 1.f;
-            H[c] = apply<RESET>(A[j][c], H[c], in ? n[j][c] * si[j][c] * x[c] : 0.f);
+            A[j][c] = cut ? 0.f : e[j][c];
+            H[c] = apply<RESET>(A[j][c], H[c], n[j][c] * si[j][c] * x[c]);
             P[c] *= A[j][c];
         }
+        __builtin_amdgcn_sched_barrier(0);  // one step's temporaries at a time
     }
 #pragma unroll
     for (int off = LC; off < 64; off <<= 1) {
@@ -550,7 +613,7 @@ __global__ void __launch_bounds__(64 * G::W) gated_bwd(GatedArgs a) {
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
             hp[j][c] = h[c];
-            h[c] = apply<RESET>(A[j][c], h[c], in ? n[j][c] * si[j][c] * x[c] : 0.f);
+            h[c] = apply<RESET>(A[j][c], h[c], n[j][c] * si[j][c] * x[c]);
             gh[j][c] = dy[c];
         }
         if constexpr (GATE) {
@@ -564,8 +627,14 @@ __global__ void __launch_bounds__(64 * G::W) gated_bwd(GatedArgs a) {
             }
             if (g.live && in) st_row<R>(oz, g.at(j, left), R::pack(dz));
         }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    if (pl.ragged) {  // a padded step's own q is 0 whatever its state holds
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) gh[j][c] = in ? gh[j][c] : 0.f;
+        for (int j = 0; j < TAU; ++j)
+#pragma unroll
+            for (int c = 0; c < VEC; ++c)
+                if (j >= mine) gh[j][c] = 0.f, hp[j][c] = 0.f;
     }
     // the message to the step before the lane: c_out = P c_in + C
     float C[VEC];
@@ -602,7 +671,7 @@ __global__ void __launch_bounds__(64 * G::W) gated_bwd(GatedArgs a) {
     }
     __syncthreads();
     if (threadIdx.x < G::CH) {  // one lane a channel: publish, look back, publish
-        const Chain cn = chain_of(a, chain, threadIdx.x, G::CH);
+        const Chain<G::CH> cn = chain_of<G>(a, chain);
         const bool last = blk == 0;
         float bp = 1.f, bc = 0.f, cb;
 #pragma unroll
@@ -613,13 +682,13 @@ __global__ void __launch_bounds__(64 * G::W) gated_bwd(GatedArgs a) {
         }
         if (turn > 0) {
             if (!last) cn.publish_map(turn, bp, bc);
-            cb = cn.before<RESET>(turn);
+            cb = cn.template before<RESET>(turn);
         } else {
-            cb = a.dh_last ? a.dh_last[(int64_t)g.b * a.Dn + slot_channel<G>(a, chain)] : 0.f;
+            cb = a.dh_last ? a.dh_last[(int64_t)g.b * a.Dn + slot_channel<G>(a, chain, (int)threadIdx.x)] : 0.f;
         }
         const float out = apply<RESET>(bp, cb, bc);
         if (!last) cn.publish_state(turn, out);
-        else if (a.dh0) a.dh0[(int64_t)g.b * a.Dn + slot_channel<G>(a, chain)] = out;
+        else if (a.dh0) a.dh0[(int64_t)g.b * a.Dn + slot_channel<G>(a, chain, (int)threadIdx.x)] = out;
         s_h[threadIdx.x] = cb;
     }
     __syncthreads();
@@ -652,7 +721,7 @@ __global__ void __launch_bounds__(64 * G::W) gated_bwd(GatedArgs a) {
             dx[c] = gt * n[j][c] * s;
             di[c] = dx[c] * x[c] * (1.f - s);
             dr[c] = q * (1.f - sr[j][c]);
-            dlam[c] += in ? q : 0.f;
+            dlam[c] += q;
         }
         if (g.live && in) {
             const uint32_t o = g.at(j, left);
@@ -660,6 +729,7 @@ __global__ void __launch_bounds__(64 * G::W) gated_bwd(GatedArgs a) {
             st_row<R>(orr, o, R::pack(dr));
             st_row<R>(oi, o, R::pack(di));
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
     // sum of q over the lane groups (shuffles) and the waves (LDS)
 #pragma unroll
@@ -676,7 +746,7 @@ __global__ void __launch_bounds__(64 * G::W) gated_bwd(GatedArgs a) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < W; ++w) v += s_lam[w][threadIdx.x];
-        a.part[((int64_t)g.b * a.blocks + blk) * a.Dn + slot_channel<G>(a, chain)] = v;
+        a.part[((int64_t)g.b * a.blocks + blk) * a.Dn + slot_channel<G>(a, chain, (int)threadIdx.x)] = v;
     }
 }
 
@@ -746,12 +816,12 @@ __global__ void __launch_bounds__(256) gated_step(GatedArgs a, int64_t nvec) {
 template <bool BF16>
 using Fwd = Geo<4, 16, 8, 4, BF16>;
 template <bool BF16>
-using Bwd = Geo<4, 16, 4, 4, BF16>;
+using Bwd = Geo<4, 16, GS_BT, GS_BW, BF16>;
 // fewer than four channels
 template <bool BF16>
-using FwdOne = Geo<1, 4, 2, 8, BF16>;
+using FwdOne = Geo<1, 4, 2, 4, BF16>;
 template <bool BF16>
-using BwdOne = Geo<1, 4, 1, 8, BF16>;
+using BwdOne = Geo<1, 4, 1, GS_BW, BF16>;
 
 // The sizes that a launch and its workspace go by.
 struct Cut {
@@ -763,11 +833,13 @@ Cut cut_of(int batch, int64_t L, int Dn) {
     return Cut{G::CH, G::TB, G::W, (int64_t)((Dn + G::CH - 1) / G::CH) * batch,
                (L + G::TB - 1) / G::TB};
 }
-Cut fwd_cut(int batch, int64_t L, int Dn) {  // the same for both io types
-    return Dn < 4 ? cut_of<FwdOne<true>>(batch, L, Dn) : cut_of<Fwd<true>>(batch, L, Dn);
+Cut fwd_cut(int batch, int64_t L, int Dn, bool bf16) {
+    if (Dn < 4) return cut_of<FwdOne<true>>(batch, L, Dn);
+    return bf16 ? cut_of<Fwd<true>>(batch, L, Dn) : cut_of<Fwd<false>>(batch, L, Dn);
 }
-Cut bwd_cut(int batch, int64_t L, int Dn) {
-    return Dn < 4 ? cut_of<BwdOne<true>>(batch, L, Dn) : cut_of<Bwd<true>>(batch, L, Dn);
+Cut bwd_cut(int batch, int64_t L, int Dn, bool bf16) {
+    if (Dn < 4) return cut_of<BwdOne<true>>(batch, L, Dn);
+    return bf16 ? cut_of<Bwd<true>>(batch, L, Dn) : cut_of<Bwd<false>>(batch, L, Dn);
 }
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
@@ -780,14 +852,16 @@ Ws ws_of(const Cut& c) {
     Ws w{};
     if (c.blocks < 2) return w;
     w.words = (size_t)c.chains * (size_t)c.blocks * c.ch;
-    w.state = 256;
-    w.map = w.state + up256(w.words * 4);
+    const size_t front = (size_t)kWindow * c.ch;  // read, never taken (Chain::before)
+    w.state = 256 + up256(front * 4);
+    w.map = w.state + up256(w.words * 4) + up256(front * 8);
     w.total = w.map + up256(w.words * 8);
     return w;
 }
 
 hipError_t prepare(GatedArgs& a, const Cut& c, void* workspace, hipStream_t s) {
     a.blocks = c.blocks;
+    a.chains = (uint32_t)c.chains;
     if (c.blocks < 2) return hipSuccess;
     const Ws w = ws_of(c);
     char* ws = static_cast<char*>(workspace);
@@ -811,8 +885,8 @@ hipError_t prepare(GatedArgs& a, const Cut& c, void* workspace, hipStream_t s) {
 
 }  // namespace
 
-int64_t gated_workgroups(int batch, int64_t L, int Dn) {
-    const Cut f = fwd_cut(batch, L, Dn), b = bwd_cut(batch, L, Dn);
+int64_t gated_workgroups(int batch, int64_t L, int Dn, bool bf16) {
+    const Cut f = fwd_cut(batch, L, Dn, bf16), b = bwd_cut(batch, L, Dn, bf16);
     const double n = (double)f.chains * (double)f.blocks, m = (double)b.chains * (double)b.blocks;
     return (int64_t)(n > m ? n : m);
 }
@@ -824,18 +898,18 @@ static size_t start_bytes(int batch, int Dn) {
     return Dn > 4 && Dn % 4 ? up256((size_t)batch * (size_t)Dn * 4) : 0;
 }
 
-size_t gated_fwd_ws(int batch, int64_t L, int Dn) {
-    return ws_of(fwd_cut(batch, L, Dn)).total + start_bytes(batch, Dn);
+size_t gated_fwd_ws(int batch, int64_t L, int Dn, bool bf16) {
+    return ws_of(fwd_cut(batch, L, Dn, bf16)).total + start_bytes(batch, Dn);
 }
 
 // The backward's partial sums of dlam follow its words.
-size_t gated_bwd_ws(int batch, int64_t L, int Dn) {
-    const Cut c = bwd_cut(batch, L, Dn);
+size_t gated_bwd_ws(int batch, int64_t L, int Dn, bool bf16) {
+    const Cut c = bwd_cut(batch, L, Dn, bf16);
     return ws_of(c).total + up256((size_t)batch * (size_t)c.blocks * (size_t)Dn * 4);
 }
 
 hipError_t launch_gated_fwd(GatedArgs a, bool bf16, void* workspace, hipStream_t s) {
-    const Cut c = fwd_cut(a.batch, a.L, a.Dn);
+    const Cut c = fwd_cut(a.batch, a.L, a.Dn, bf16);
     const hipError_t e = prepare(a, c, workspace, s);
     if (e != hipSuccess) return e;
     if (a.h0 && a.h0 == a.h_last && start_bytes(a.batch, a.Dn)) {
@@ -859,7 +933,7 @@ hipError_t launch_gated_fwd(GatedArgs a, bool bf16, void* workspace, hipStream_t
 }
 
 hipError_t launch_gated_bwd(GatedArgs a, bool bf16, void* workspace, hipStream_t s) {
-    const Cut c = bwd_cut(a.batch, a.L, a.Dn);
+    const Cut c = bwd_cut(a.batch, a.L, a.Dn, bf16);
     hipError_t e = prepare(a, c, workspace, s);
     if (e != hipSuccess) return e;
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws_of(c).total);

@@ -67,9 +67,10 @@ ms_status check_gated(int32_t batch, int64_t seqlen, int32_t d_inner, int32_t io
         return fail(MS_ERR_SHAPE, "batch x seqlen x d_inner exceeds 2^56");
     if ((d_inner + 63) / 64 > 65535 || batch > 65535)
         return fail(MS_ERR_UNSUPPORTED, "d_inner/64 and batch must be <= 65535");
-    if (gated_workgroups(batch, seqlen, d_inner) > kMax31)
+    ms_status st = check_io(io);
+    if (st == MS_OK && gated_workgroups(batch, seqlen, d_inner, io == MS_BF16) > kMax31)
         return fail(MS_ERR_UNSUPPORTED, "batch x seqlen x d_inner needs more than 2^31-1 workgroups");
-    return check_io(io);
+    return st;
 }
 
 ms_status check_sharpness(float c) {
@@ -116,7 +117,7 @@ extern "C" {
 
 size_t ms_gated_scan_workspace_bytes(int32_t batch, int64_t seqlen, int32_t d_inner, int32_t io) {
     if (check_gated(batch, seqlen, d_inner, io) != MS_OK) return (size_t)-1;
-    return gated_fwd_ws(batch, seqlen, d_inner);
+    return gated_fwd_ws(batch, seqlen, d_inner, io == MS_BF16);
 }
 
 size_t ms_gated_scan_states_bytes(int32_t batch, int64_t seqlen, int32_t d_inner) {
@@ -150,7 +151,7 @@ ms_status ms_gated_scan_fwd(const void* x, const void* r, const void* i, const f
 size_t ms_gated_scan_bwd_workspace_bytes(int32_t batch, int64_t seqlen, int32_t d_inner,
                                          int32_t io) {
     if (check_gated(batch, seqlen, d_inner, io) != MS_OK) return (size_t)-1;
-    return gated_bwd_ws(batch, seqlen, d_inner);
+    return gated_bwd_ws(batch, seqlen, d_inner, io == MS_BF16);
 }
 
 ms_status ms_gated_scan_bwd(const void* x, const void* r, const void* i, const float* lam,

@@ -39,6 +39,7 @@ struct GatedArgs {
     uint32_t* state;   // [chains][blocks][channels of a chain]: state after a block
     uint64_t* map;     // the same: what a block does to a state
     int64_t blocks;    // blocks of a chain
+    uint32_t chains;   // channel tiles of all batch rows
     float sharp;
     int64_t L;
     int64_t nstates;  // ceil(L / kGatedBlock)
@@ -46,9 +47,9 @@ struct GatedArgs {
     int Dn;
 };
 
-int64_t gated_workgroups(int batch, int64_t L, int Dn);  // of the larger of both passes
-size_t gated_fwd_ws(int batch, int64_t L, int Dn);  // bytes
-size_t gated_bwd_ws(int batch, int64_t L, int Dn);
+int64_t gated_workgroups(int batch, int64_t L, int Dn, bool bf16);  // of the larger of both passes
+size_t gated_fwd_ws(int batch, int64_t L, int Dn, bool bf16);  // bytes
+size_t gated_bwd_ws(int batch, int64_t L, int Dn, bool bf16);
 hipError_t launch_gated_fwd(GatedArgs a, bool bf16, void* workspace, hipStream_t s);
 hipError_t launch_gated_bwd(GatedArgs a, bool bf16, void* workspace, hipStream_t s);
 // One step: a.h_last is the state [batch][Dn], updated in place; L is 1.
