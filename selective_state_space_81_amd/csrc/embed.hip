@@ -154,11 +154,10 @@ __global__ void __launch_bounds__(256) embed_fwd(EmbedArgs a) {
 }
 
 // ---- sort -----------------------------------------------------------------------------
-// Least significant digit first, kDigitBits at most a pass.  A workgroup
-// takes a.tile consecutive entries, each of its waves a quarter of them in
-// order; entries of one digit keep their order because a wave ranks 64 of
-// them at a time by lane (ballots), adds what it has placed before, and starts
-// after the waves and workgroups before it.
+// Least significant digit first, a.bits (kDigitBits at most) a pass: count the
+// digits of each tile, then place every entry.  Entries of one digit keep their
+// order: a wave ranks 64 of them at a time by lane (ballots), adds what it has
+// ranked before, and starts after the waves and tiles before it.
 constexpr int kDigits = 1 << kDigitBits;
 
 // The sort key of entry i: its token, or `rows` (sorted last, and ignored)
@@ -172,55 +171,110 @@ __device__ __forceinline__ uint32_t pass_key(const EmbedArgs& a, const SortPass&
     return p.first ? key_of(a, i) : p.key_in[i];
 }
 
-// lanes of the wave holding the same digit (of those in `in`)
-__device__ __forceinline__ uint64_t same_digit(uint32_t d, uint64_t in) {
-    uint64_t m = in;
+// lanes of the wave holding the same digit of `bits` bits (of those in `in`)
+__device__ __forceinline__ uint64_t same_digit(uint32_t d, uint64_t in, int bits) {
+    uint32_t lo = (uint32_t)in, hi = (uint32_t)(in >> 32);
 #pragma unroll
     for (int b = 0; b < kDigitBits; ++b) {
-        const uint64_t v = __ballot((d >> b) & 1);
-        m &= ((d >> b) & 1) ? v : ~v;
+        if (b >= bits) break;
+        const uint32_t other = ((d >> b) & 1) - 1;  // all ones where the bit is 0
+        const uint64_t v = __ballot(other == 0);
+        lo &= (uint32_t)v ^ other;
+        hi &= (uint32_t)(v >> 32) ^ other;
     }
-    return m;
+    return ((uint64_t)hi << 32) | lo;
 }
+
+// Entries a thread holds: with 8 a workgroup's chain of rounds is longer (53
+// against 46 us for the gradient of 16384 tokens), with 2 the tiles are more
+// than what reads their counts likes (648 against 636 us for 131072).
+constexpr int kSortRounds = 4;
+constexpr int kSubtile = 256 * kSortRounds;  // entries a workgroup places at a time
 
 // hist[tile][digit]
 __global__ void __launch_bounds__(256) sort_count(EmbedArgs a, SortPass p) {
     __shared__ uint32_t s_n[kDigits];
+    const int64_t i0 = (int64_t)blockIdx.x * a.tile, i1 = min(a.n, i0 + a.tile);
     for (int d = threadIdx.x; d < kDigits; d += 256) s_n[d] = 0;
     __syncthreads();
-    const int64_t i0 = (int64_t)blockIdx.x * a.tile, i1 = min(a.n, i0 + a.tile);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += 256)
-        atomicAdd(&s_n[(pass_key(a, p, i) >> p.shift) & (kDigits - 1)], 1u);  // whole numbers
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kSubtile) {
+        uint32_t key[kSortRounds];
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r) key[r] = pass_key(a, p, min(i + 256 * r, i1 - 1));
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r)
+            if (i + 256 * r < i1) atomicAdd(&s_n[(key[r] >> p.shift) & p.mask], 1u);  // whole numbers
+    }
     __syncthreads();
     for (int d = threadIdx.x; d < kDigits; d += 256)
         p.hist[(int64_t)blockIdx.x * kDigits + d] = s_n[d];
 }
 
-__global__ void __launch_bounds__(256) sort_place(EmbedArgs a, SortPass p) {
-    __shared__ uint32_t s_n[4][kDigits];  // per wave: counts, then the next place of each digit
-    __shared__ uint32_t s_wave[4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int d = threadIdx.x; d < 4 * kDigits; d += 256) (&s_n[0][0])[d] = 0;
-    __syncthreads();
-    const int64_t part = a.tile / 4;
-    const int64_t i0 = min(a.n, (int64_t)blockIdx.x * a.tile + wave * part);
-    const int64_t i1 = min(a.n, i0 + part);
-    for (int64_t i = i0 + lane; i < i1; i += 64)
-        atomicAdd(&s_n[wave][(pass_key(a, p, i) >> p.shift) & (kDigits - 1)], 1u);
-    // entries of smaller digits everywhere, and of this digit in earlier tiles
-    constexpr int PER = kDigits / 256;
-    uint32_t before[PER], total[PER], sum = 0;
+// Among the wave's entries of each round: how many of the digit come before,
+// and (bit r of the result) whether this is the last of them; then the same
+// over the wave's rounds, with the counts of digits so far in s_n.
+template <int ROUNDS, class N>
+__device__ __forceinline__ void rank_rounds(const uint32_t (&digit)[ROUNDS], uint32_t in, int rounds,
+                                            int bits, int lane, N* s_n, uint32_t (&rank)[ROUNDS]) {
+    uint32_t last = 0;
 #pragma unroll
-    for (int q = 0; q < PER; ++q) {
-        before[q] = total[q] = 0;
-        const uint32_t* h = p.hist + threadIdx.x * PER + q;
-        for (int t = 0; t < a.tiles; ++t) {
-            const uint32_t v = h[(int64_t)t * kDigits];
-            total[q] += v;
-            if (t < (int)blockIdx.x) before[q] += v;
-        }
-        sum += total[q];
+    for (int r = 0; r < ROUNDS; ++r) {
+        if (r >= rounds) break;
+        const bool here = (in >> r) & 1;
+        const uint64_t m = same_digit(digit[r], __ballot(here), bits);
+        rank[r] = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
+                                            __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+        last |= (here && (m >> lane) == 1 ? 1u : 0u) << r;
     }
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        if (r >= rounds) break;
+        N* q = s_n + digit[r];
+        rank[r] += *q;
+        __builtin_amdgcn_wave_barrier();  // read before the digit's last lane counts the round
+        if ((last >> r) & 1) *q = (N)(rank[r] + 1);
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+__global__ void __launch_bounds__(256) sort_place(EmbedArgs a, SortPass p) {
+    __shared__ uint32_t s_n[4][kDigits];  // per wave: counts, then the first place of each digit
+    __shared__ uint32_t s_wave[4];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t0 = (int64_t)blockIdx.x * a.tile, t1 = min(a.n, t0 + a.tile);
+    // a wave takes 64 * kSortRounds neighbouring entries of a subtile
+    uint32_t key[kSortRounds], pos[kSortRounds];
+    auto load = [&](int64_t sub) {
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r) {
+            const int64_t i = min(sub + wave * (64 * kSortRounds) + 64 * r + lane, t1 - 1);
+            key[r] = pass_key(a, p, i);
+            pos[r] = p.first ? (uint32_t)i : p.pos_in[i];
+        }
+    };
+    load(t0);
+    // entries of smaller digits everywhere, and of this digit in earlier tiles;
+    // a thread takes two neighbouring digits
+    static_assert(kDigits == 2 * 256, "two digits a thread");
+    uint32_t before[2] = {0, 0}, total[2] = {0, 0};
+    {
+        const uint2* h = reinterpret_cast<const uint2*>(p.hist) + threadIdx.x;
+        constexpr int U = 16;  // tiles whose counts travel together
+        for (int k = 0; k < a.tiles; k += U) {
+            uint2 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                v[u] = k + u < a.tiles ? h[(int64_t)(k + u) * (kDigits / 2)] : make_uint2(0, 0);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                total[0] += v[u].x;
+                total[1] += v[u].y;
+                if (k + u < (int)blockIdx.x) before[0] += v[u].x, before[1] += v[u].y;
+            }
+        }
+    }
+    const uint32_t sum = total[0] + total[1];
     uint32_t inc = sum;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -229,42 +283,133 @@ __global__ void __launch_bounds__(256) sort_place(EmbedArgs a, SortPass p) {
     }
     if (lane == 63) s_wave[wave] = inc;
     __syncthreads();
-    uint32_t at = inc - sum;
-    for (int w = 0; w < wave; ++w) at += s_wave[w];
+    uint32_t start[2];  // next place of the thread's digits
+    start[0] = inc - sum;
+    for (int w = 0; w < wave; ++w) start[0] += s_wave[w];
+    start[1] = start[0] + total[0] + before[1];
+    start[0] += before[0];
+
+    for (int64_t sub = t0; sub < t1; sub += kSubtile) {
+        if (sub > t0) load(sub);
+        for (int d = threadIdx.x; d < 4 * kDigits; d += 256) (&s_n[0][0])[d] = 0;
+        __syncthreads();
+        uint32_t digit[kSortRounds], rank[kSortRounds], in = 0;
 #pragma unroll
-    for (int q = 0; q < PER; ++q) {
-        const int d = threadIdx.x * PER + q;
-        uint32_t place = at + before[q];
-        for (int w = 0; w < 4; ++w) {
-            const uint32_t v = s_n[w][d];
-            s_n[w][d] = place;
-            place += v;
+        for (int r = 0; r < kSortRounds; ++r) {
+            digit[r] = (key[r] >> p.shift) & p.mask;
+            in |= (sub + wave * (64 * kSortRounds) + 64 * r + lane < t1 ? 1u : 0u) << r;
         }
-        at += total[q];
+        rank_rounds<kSortRounds>(digit, in, kSortRounds, a.bits, lane, s_n[wave], rank);
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t v = s_n[w][2 * threadIdx.x + q];
+                s_n[w][2 * threadIdx.x + q] = start[q];
+                start[q] += v;
+            }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r) {
+            if ((in >> r) & 1) {
+                const uint32_t at = s_n[wave][digit[r]] + rank[r];
+                p.key_out[at] = key[r];
+                p.pos_out[at] = pos[r];
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    for (int64_t i = i0; i < i1; i += 64) {
-        const bool in = i + lane < i1;
-        const uint32_t key = in ? pass_key(a, p, i + lane) : 0;
-        const uint32_t d = (key >> p.shift) & (kDigits - 1);
-        const uint64_t m = same_digit(d, __ballot(in));
-        uint32_t place = 0;
-        if (in) place = s_n[wave][d] + __popcll(m & ((1ull << lane) - 1));
-        // all lanes have read the place before its last holder moves it on
-        __builtin_amdgcn_wave_barrier();
-        if (in && (m >> lane) == 1) s_n[wave][d] = place + 1;
-        __builtin_amdgcn_wave_barrier();
-        if (in) {
-            p.key_out[place] = key;
-            p.pos_out[place] = p.first ? (uint32_t)(i + lane) : p.pos_in[i + lane];
+}
+
+// Up to kSmall entries: one workgroup sorts them whole, in LDS, all passes in
+// one launch, in the same manner.
+constexpr int kSmallWaves = 16, kSmallRounds = kSmall / (64 * kSmallWaves);
+
+__global__ void __launch_bounds__(64 * kSmallWaves) sort_small(EmbedArgs a, SortPass p) {
+    __shared__ uint32_t s_key[kSmall];
+    __shared__ uint16_t s_pos[kSmall];
+    __shared__ uint16_t s_n[kSmallWaves][kDigits];  // places stay below kSmall
+    __shared__ uint32_t s_wave[kSmallWaves];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = (int)a.n;
+    const int rounds = (n + 64 * kSmallWaves - 1) / (64 * kSmallWaves);
+    const int i0 = wave * rounds * 64 + lane;  // entry of round r: i0 + 64 r
+    uint32_t key[kSmallRounds], digit[kSmallRounds], rank[kSmallRounds], in = 0;
+    uint16_t pos[kSmallRounds];
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r) {
+        const int i = i0 + 64 * r;
+        const bool here = r < rounds && i < n;
+        in |= (here ? 1u : 0u) << r;
+        key[r] = here ? key_of(a, i) : 0;
+        pos[r] = (uint16_t)i;
+    }
+    for (int pass = 0; pass < a.passes; ++pass) {
+        for (int d = tid; d < kSmallWaves * kDigits / 2; d += 64 * kSmallWaves)
+            reinterpret_cast<uint32_t*>(&s_n[0][0])[d] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSmallRounds; ++r)
+            digit[r] = (key[r] >> (pass * a.bits)) & ((1u << a.bits) - 1);
+        rank_rounds<kSmallRounds>(digit, in, rounds, a.bits, lane, s_n[wave], rank);
+        __syncthreads();
+        // first place of each digit, and of each wave within it
+        uint32_t total = 0;
+        if (tid < kDigits) {
+#pragma unroll
+            for (int w = 0; w < kSmallWaves; ++w) total += s_n[w][tid];
         }
+        uint32_t inc = total;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const uint32_t v = __shfl_up(inc, off);
+            if (lane >= off) inc += v;
+        }
+        if (lane == 63) s_wave[wave] = inc;
+        __syncthreads();
+        if (tid < kDigits) {
+            uint32_t at = inc - total;
+            for (int w = 0; w < wave; ++w) at += s_wave[w];
+#pragma unroll
+            for (int w = 0; w < kSmallWaves; ++w) {
+                const uint32_t v = s_n[w][tid];
+                s_n[w][tid] = (uint16_t)at;
+                at += v;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSmallRounds; ++r) {
+            if ((in >> r) & 1) {
+                const uint32_t at = s_n[wave][digit[r]] + rank[r];
+                s_key[at] = key[r];
+                s_pos[at] = pos[r];
+            }
+        }
+        __syncthreads();
+        if (pass + 1 < a.passes) {
+#pragma unroll
+            for (int r = 0; r < kSmallRounds; ++r)
+                if ((in >> r) & 1) key[r] = s_key[i0 + 64 * r], pos[r] = s_pos[i0 + 64 * r];
+        }
+    }
+    for (int i = tid; i < n; i += 64 * kSmallWaves) {
+        p.key_out[i] = s_key[i];
+        p.pos_out[i] = s_pos[i];
     }
 }
 
 // ---- sums -----------------------------------------------------------------------------
-// Workgroups first cover the sorted entries, a.chunk of them by 256 * VEC
-// columns each; the rest write the zero rows of tokens that do not occur,
-// kZeroRows rows by 256 * VEC columns each.
+// A group of a.lanes threads (64, 128 or 256: what the columns of one pass
+// need) takes a.chunk sorted entries, or kZeroRows rows of the table, by
+// a.lanes * VEC columns.  Groups first cover the sorted entries; the rest
+// write the zero rows of tokens that do not occur.  (Clearing the gradient in
+// the sort's launches, which leave the chip empty, measured 46 against 43 us
+// for 16384 rows of 768 bf16: it slows the sort.)  A group for every run of one token instead, with no
+// walk over runs, measured twice the time (1350 against 645 us for 131072
+// rows of 2048 fp32): its three dependent loads then bring one row.
 constexpr int kZeroRows = 16;
 
 // First sorted entry whose key is not below v.
@@ -278,47 +423,56 @@ __device__ __forceinline__ int64_t lower_bound(const uint32_t* key, int64_t n, u
     return lo;
 }
 
+// This thread's piece of work (the same for a wave) and its first column;
+// false where the table has no such column.
+template <int VEC>
+__device__ __forceinline__ bool place(const EmbedArgs& a, int64_t& work, int& col) {
+    const int per = 256 / a.lanes;  // groups in a workgroup
+    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / a.lanes);
+    const int64_t l = (int64_t)blockIdx.x * per + group;
+    const int32_t cgroups = (a.D + a.lanes * VEC - 1) / (a.lanes * VEC);
+    work = l / cgroups;
+    col = ((int)(l - work * cgroups) * a.lanes + (int)(threadIdx.x % a.lanes)) * VEC;
+    const bool ok = col < a.D;
+    col = min(col, a.D - VEC);
+    return ok;
+}
+
 template <bool BF16, int VEC, bool GBF16>
 __global__ void __launch_bounds__(256) embed_sum(EmbedArgs a, const uint32_t* key,
                                                  const uint32_t* pos) {
     using V = Vec<BF16, VEC>;
     using E = typename V::E;
-    const int32_t cgroups = (a.D + 256 * VEC - 1) / (256 * VEC);
-    const int64_t l = blockIdx.x;
-    const int64_t work = l / cgroups;
-    const int cg = (int)(l - work * cgroups);
-    int col = (cg * 256 + (int)threadIdx.x) * VEC;
-    const bool live = col < a.D;
-    col = min(col, a.D - VEC);
+    int64_t work;
+    int col;
+    const bool live = place<VEC>(a, work, col);
+    if (work >= a.chunks + a.zeros) return;
     if (work >= a.chunks) {
-        __shared__ int s_has[kZeroRows];
         const int64_t v0 = (work - a.chunks) * kZeroRows;
-        if (threadIdx.x < kZeroRows) {
-            const int64_t v = v0 + threadIdx.x;
-            int has = 1;  // nothing to write past the table
-            if (v < a.rows) {
-                const int64_t at = lower_bound(key, a.n, (uint32_t)v);
-                has = at < a.n && key[at] == (uint32_t)v;
-            }
-            s_has[threadIdx.x] = has;
+        // lane k of the wave finds out whether token v0 + k occurs
+        const int64_t v = v0 + (threadIdx.x & (kZeroRows - 1));
+        bool has = true;  // nothing to write past the table
+        if (v < a.rows) {
+            const int64_t at = lower_bound(key, a.n, (uint32_t)v);
+            has = at < a.n && key[at] == (uint32_t)v;
         }
-        __syncthreads();
+        const uint64_t m = __ballot(has);
         if (!live) return;
         const float zero[VEC] = {};
         for (int k = 0; k < kZeroRows; ++k)
-            if (!s_has[k]) store_grad<VEC, GBF16>(a.dweight, (v0 + k) * a.D + col, zero);
+            if (!((m >> k) & 1)) store_grad<VEC, GBF16>(a.dweight, (v0 + k) * a.D + col, zero);
         return;
     }
-    if (!live) return;
     const int64_t e0 = work * a.chunk, e1 = min(a.n, e0 + a.chunk);
     // a run that starts before the chunk, or goes on after it, leaves a part
     const uint32_t prev = e0 > 0 ? key[e0 - 1] : 0xffffffffu;
     const uint32_t next = e1 < a.n ? key[e1] : 0xffffffffu;
+    const int lane = threadIdx.x & 63;
     float acc[VEC] = {};
     uint32_t cur = key[e0];
     bool head = cur == prev;  // the current run began in an earlier chunk
     auto flush = [&](bool goes_on) {
-        if (cur >= (uint32_t)a.rows) return;  // ignored entries
+        if (cur >= (uint32_t)a.rows || !live) return;  // ignored entries, columns past the row
         if (head || goes_on) {
             float* q = a.part + (2 * work + (head ? 0 : 1)) * (int64_t)a.D + col;
 #pragma unroll
@@ -331,73 +485,100 @@ __global__ void __launch_bounds__(256) embed_sum(EmbedArgs a, const uint32_t* ke
         }
     };
     const E* dy = static_cast<const E*>(a.dy) + col;
-    constexpr int U = 8;
-    for (int64_t e = e0; e < e1; e += U) {
-        typename V::T w[U];
-        uint32_t kk[U];
+    constexpr int U = 8;  // rows on the way at a time
+    for (int64_t b = e0; b < e1; b += 64) {
+        // a lane an entry, so that all positions arrive together; then one
+        // entry after another, the same for the whole wave
+        const int64_t at = min(b + lane, e1 - 1);
+        const uint32_t kl = key[at], pl = pos[at];
+        const int m = (int)min(e1 - b, (int64_t)64);
+        for (int e = 0; e < m; e += U) {
+            typename V::T w[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t at = min(e + u, e1 - 1);
-            kk[u] = key[at];
-            w[u] = ldv<V>(dy + (int64_t)pos[at] * a.D);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (e + u >= e1) break;
-            if (kk[u] != cur) {
-                flush(false);
-                cur = kk[u];
-                head = false;
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) acc[c] = 0.f;
+            for (int u = 0; u < U; ++u) {
+                const uint32_t row = __builtin_amdgcn_readlane(pl, min(e + u, 63));
+                w[u] = ldv<V>(dy + (int64_t)row * a.D);
             }
-            float v[VEC];
-            V::unpack(w[u], v);
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) acc[c] += v[c];
+            for (int u = 0; u < U; ++u) {
+                if (e + u >= m) break;
+                const uint32_t k = __builtin_amdgcn_readlane(kl, e + u);
+                if (k != cur) {
+                    flush(false);
+                    cur = k;
+                    head = false;
+#pragma unroll
+                    for (int c = 0; c < VEC; ++c) acc[c] = 0.f;
+                }
+                float v[VEC];
+                V::unpack(w[u], v);
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) acc[c] += v[c];
+            }
         }
     }
     flush(cur == next);
 }
 
-// Joins the pieces of runs that cross chunks: the workgroup of the chunk where
-// a run starts adds its tail part and the head parts of the chunks after it,
-// in order.
+// Joins the pieces of runs that cross chunks: the group of the chunk where a
+// run starts adds its tail part and the head parts of the chunks after it, in
+// order, with kJoin of them on the way at a time.
+constexpr int kJoin = 16;
+
 template <int VEC, bool GBF16>
 __global__ void __launch_bounds__(256) embed_join(EmbedArgs a, const uint32_t* key) {
-    const int32_t cgroups = (a.D + 256 * VEC - 1) / (256 * VEC);
-    const int64_t work = blockIdx.x / cgroups;
-    const int cg = (int)(blockIdx.x - work * cgroups);
-    int col = (cg * 256 + (int)threadIdx.x) * VEC;
-    if (col >= a.D) return;
-    col = min(col, a.D - VEC);
+    int64_t work;
+    int col;
+    const bool live = place<VEC>(a, work, col);
+    if (work >= a.chunks - 1) return;  // the last chunk starts nothing that goes on
     const int64_t e0 = work * a.chunk, e1 = e0 + a.chunk;
-    if (e1 >= a.n) return;  // the last chunk starts nothing that goes on
     const uint32_t run = key[e1 - 1];
     if (run >= (uint32_t)a.rows || key[e1] != run) return;  // nothing goes on
     if (e0 > 0 && key[e0 - 1] == run) return;               // it started before this chunk
-    const int64_t end = lower_bound(key, a.n, run + 1);     // one past the run
-    const int64_t last = (end - 1) / a.chunk;               // the chunk of its last entry
+    // the chunk of its last entry: the chunks after this one that begin with it
+    int64_t last = work;
+    for (;;) {
+        const int64_t k = last + 1 + (threadIdx.x & 63);
+        const uint64_t other = ~__ballot(k < a.chunks && key[k * a.chunk] == run);
+        if (other) {
+            last += __ffsll((unsigned long long)other) - 1;
+            break;
+        }
+        last += 64;
+    }
+    if (!live) return;
+    const int64_t D = a.D;
     float acc[VEC];
-    const float* q = a.part + (2 * work + 1) * (int64_t)a.D + col;
+    const float* q = a.part + (2 * work + 1) * D + col;
 #pragma unroll
     for (int c = 0; c < VEC; ++c) acc[c] = q[c];
-    for (int64_t k = work + 1; k <= last; ++k) {
-        q = a.part + 2 * k * (int64_t)a.D + col;
+    int64_t k = work + 1;
+    for (; k + kJoin <= last + 1; k += kJoin) {
+        float v[kJoin][VEC];
+#pragma unroll
+        for (int u = 0; u < kJoin; ++u)
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) v[u][c] = a.part[2 * (k + u) * D + col + c];
+#pragma unroll
+        for (int u = 0; u < kJoin; ++u)
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) acc[c] += v[u][c];
+    }
+    for (; k <= last; ++k) {
+        q = a.part + 2 * k * D + col;
 #pragma unroll
         for (int c = 0; c < VEC; ++c) acc[c] += q[c];
     }
 #pragma unroll
     for (int c = 0; c < VEC; ++c) acc[c] *= a.scale;
-    store_grad<VEC, GBF16>(a.dweight, (int64_t)run * a.D + col, acc);
+    store_grad<VEC, GBF16>(a.dweight, (int64_t)run * D + col, acc);
 }
 
 template <bool BF16, int VEC>
 hipError_t sum_variant(const EmbedArgs& a, bool gbf16, const uint32_t* key, const uint32_t* pos,
                        hipStream_t s) {
-    const int64_t cgroups = (a.D + 256 * VEC - 1) / (256 * VEC);
-    const int64_t zero = (a.rows + kZeroRows - 1) / kZeroRows;
-    const dim3 grid((unsigned)((a.chunks + zero) * cgroups)), blk(256);
+    const int64_t cgroups = (a.D + a.lanes * VEC - 1) / (a.lanes * VEC), per = 256 / a.lanes;
+    const dim3 grid((unsigned)(((a.chunks + a.zeros) * cgroups + per - 1) / per)), blk(256);
     {
         ProfScope ps(s, kPhaseMain);
         if (gbf16) hipLaunchKernelGGL((embed_sum<BF16, VEC, true>), grid, blk, 0, s, a, key, pos);
@@ -406,7 +587,7 @@ hipError_t sum_variant(const EmbedArgs& a, bool gbf16, const uint32_t* key, cons
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.chunks < 2) return e;
     ProfScope ps(s, kPhaseReduce);
-    const dim3 jgrid((unsigned)((a.chunks - 1) * cgroups));
+    const dim3 jgrid((unsigned)(((a.chunks - 1) * cgroups + per - 1) / per));
     if (gbf16) hipLaunchKernelGGL((embed_join<VEC, true>), jgrid, blk, 0, s, a, key);
     else hipLaunchKernelGGL((embed_join<VEC, false>), jgrid, blk, 0, s, a, key);
     return hipGetLastError();
@@ -420,8 +601,8 @@ int embed_vec(int D, bool bf16) {
 }
 
 int64_t embed_sum_workgroups(const EmbedArgs& a, bool bf16) {
-    const int64_t per = 256 * (int64_t)embed_vec(a.D, bf16);
-    return (a.chunks + (a.rows + kZeroRows - 1) / kZeroRows) * ((a.D + per - 1) / per);
+    const int64_t per = (int64_t)a.lanes * embed_vec(a.D, bf16);
+    return (a.chunks + a.zeros) * ((a.D + per - 1) / per);
 }
 
 int64_t embed_fwd_workgroups(const EmbedArgs& a, bool bf16) {
@@ -443,10 +624,10 @@ hipError_t launch_embed_fwd(const EmbedArgs& a, bool bf16, hipStream_t s) {
     return hipGetLastError();
 }
 
-void embed_plan(EmbedArgs& a) {
+void embed_plan(EmbedArgs& a, bool bf16) {
     // at most kMaxTiles tiles, so that a workgroup of sort_place reads the
     // whole count matrix from L2 in little time
-    const int64_t quantum = 2048;
+    const int64_t quantum = kSubtile;
     int64_t tile = (a.n + kMaxTiles - 1) / kMaxTiles;
     tile = (tile + quantum - 1) / quantum * quantum;
     a.tile = tile < quantum ? quantum : tile;
@@ -454,8 +635,18 @@ void embed_plan(EmbedArgs& a) {
     int bits = 1;  // keys run from 0 to rows
     while (bits < 32 && ((uint64_t)a.rows >> bits) != 0) ++bits;
     a.passes = (bits + kDigitBits - 1) / kDigitBits;
-    a.chunk = 32;
+    a.bits = (bits + a.passes - 1) / a.passes;
+    const int vec = embed_vec(a.D, bf16);
+    const int64_t vecs = (a.D + vec - 1) / vec;
+    a.lanes = vecs <= 64 ? 64 : vecs <= 128 ? 128 : 256;
+    // chunks: enough groups to fill the chip, long enough that a frequent
+    // token's run has few pieces to join
+    const int64_t cgroups = (vecs + a.lanes - 1) / a.lanes;
+    const int64_t chunk = a.n * cgroups * a.lanes / (2048 * 256);
+    a.chunk = chunk < 32 ? 32 : chunk > 256 ? 256 : chunk;
     a.chunks = (a.n + a.chunk - 1) / a.chunk;
+    a.small = a.n > 0 && a.n <= kSmall;
+    a.zeros = (a.rows + kZeroRows - 1) / kZeroRows;
 }
 
 // [hist][key x2][pos x2][parts], 256-byte aligned regions
@@ -481,23 +672,26 @@ hipError_t launch_embed_bwd(EmbedArgs a, bool bf16, bool gbf16, void* workspace,
     const EmbedWs w = embed_ws(a);
     a.part = reinterpret_cast<float*>(ws + w.part);
     int out = 0;
-    if (a.n > 0) {
-        for (int k = 0; k < a.passes; ++k) {
-            SortPass p{};
-            p.first = k == 0;
-            p.shift = k * kDigitBits;
-            p.hist = reinterpret_cast<uint32_t*>(ws + w.hist);
-            out = k & 1;
-            p.key_in = reinterpret_cast<uint32_t*>(ws + w.key[out ^ 1]);
-            p.pos_in = reinterpret_cast<uint32_t*>(ws + w.pos[out ^ 1]);
-            p.key_out = reinterpret_cast<uint32_t*>(ws + w.key[out]);
-            p.pos_out = reinterpret_cast<uint32_t*>(ws + w.pos[out]);
-            ProfScope ps(s, kPhasePrep);
+    SortPass p{};
+    p.hist = reinterpret_cast<uint32_t*>(ws + w.hist);
+    for (int k = 0; a.n > 0 && k < (a.small ? 1 : a.passes); ++k) {
+        p.first = k == 0;
+        p.shift = k * a.bits;
+        p.mask = (1u << a.bits) - 1;
+        out = k & 1;
+        p.key_in = reinterpret_cast<uint32_t*>(ws + w.key[out ^ 1]);
+        p.pos_in = reinterpret_cast<uint32_t*>(ws + w.pos[out ^ 1]);
+        p.key_out = reinterpret_cast<uint32_t*>(ws + w.key[out]);
+        p.pos_out = reinterpret_cast<uint32_t*>(ws + w.pos[out]);
+        ProfScope ps(s, kPhasePrep);
+        if (a.small) {
+            hipLaunchKernelGGL(sort_small, dim3(1), dim3(64 * kSmallWaves), 0, s, a, p);
+        } else {
             hipLaunchKernelGGL(sort_count, dim3(a.tiles), dim3(256), 0, s, a, p);
             hipLaunchKernelGGL(sort_place, dim3(a.tiles), dim3(256), 0, s, a, p);
-            const hipError_t e = hipGetLastError();
-            if (e != hipSuccess) return e;
         }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
     const uint32_t* key = reinterpret_cast<uint32_t*>(ws + w.key[out]);
     const uint32_t* pos = reinterpret_cast<uint32_t*>(ws + w.pos[out]);

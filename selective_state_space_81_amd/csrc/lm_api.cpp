@@ -226,7 +226,7 @@ size_t ms_embed_bwd_workspace_bytes(int64_t n, int64_t rows, int32_t dim, int32_
     if (check_embed(n, rows, dim, io) != MS_OK) return (size_t)-1;
     EmbedArgs a{};
     a.n = n; a.rows = rows; a.D = dim;
-    embed_plan(a);
+    embed_plan(a, io == MS_BF16);
     return embed_ws(a).total;
 }
 
@@ -246,7 +246,7 @@ ms_status ms_embed_bwd(const void* ids, int32_t id_bits, const void* dy, float s
     EmbedArgs a{};
     a.ids = ids; a.wide = id_bits == 64; a.dy = dy; a.scale = scale; a.padding = padding;
     a.dweight = dweight; a.n = n; a.rows = rows; a.D = dim;
-    embed_plan(a);
+    embed_plan(a, io == MS_BF16);
     if ((st = check_workspace(embed_ws(a).total, workspace, workspace_bytes)) != MS_OK) return st;
     if (embed_sum_workgroups(a, io == MS_BF16) > kMax31)
         return fail(MS_ERR_UNSUPPORTED, "n, rows and dim need more than 2^31-1 workgroups");

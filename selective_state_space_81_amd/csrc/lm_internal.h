@@ -58,6 +58,7 @@ hipError_t launch_gated_step(const GatedArgs& a, bool bf16, hipStream_t s);
 // ---- embedding (embed.hip) ----------------------------------------------------
 constexpr int kDigitBits = 9;   // sort digit: two passes up to 2^18 tokens
 constexpr int kMaxTiles = 256;  // sort workgroups
+constexpr int kSmall = 4096;    // entries one workgroup sorts
 
 struct EmbedArgs {
     const void* ids;     // [n], int32 or int64
@@ -76,8 +77,12 @@ struct EmbedArgs {
     int64_t tile;  // entries a sort workgroup takes
     int tiles;
     int passes;
-    int64_t chunk;  // sorted entries a workgroup sums
+    int bits;       // of a pass's digit
+    int small;      // one workgroup sorts
+    int lanes;      // threads that share a piece of the sums
+    int64_t chunk;  // sorted entries in a piece
     int64_t chunks;
+    int64_t zeros;  // pieces that write rows of tokens that do not occur
 };
 struct SortPass {
     const uint32_t* key_in;
@@ -86,13 +91,14 @@ struct SortPass {
     uint32_t* pos_out;
     uint32_t* hist;  // [tiles][1 << kDigitBits]
     int shift;
+    uint32_t mask;
     int first;  // keys come from the ids, positions are the entries' own
 };
 struct EmbedWs {
     size_t hist, key[2], pos[2], part, total;
 };
 int embed_vec(int D, bool bf16);
-void embed_plan(EmbedArgs& a);  // from n, rows, D
+void embed_plan(EmbedArgs& a, bool bf16);  // from n, rows, D
 EmbedWs embed_ws(const EmbedArgs& a);
 int64_t embed_fwd_workgroups(const EmbedArgs& a, bool bf16);
 int64_t embed_sum_workgroups(const EmbedArgs& a, bool bf16);

@@ -66,7 +66,8 @@ def check_grad(gpu, ids, dy, rows, scale=1.0, padding=-1, grad_dtype=None):
 @pytest.mark.parametrize("n,rows,dim", [(1, 1, 1), (5, 3, 2), (31, 40, 8), (32, 7, 33), (33, 1, 64),
                                         (1000, 17, 100), (2048, 2000, 24), (2049, 9, 16),
                                         (9000, 600, 40), (70000, 300, 12), (600, 300000, 9),
-                                        (64, 5, 2500)])
+                                        (64, 5, 2500), (16384, 5000, 8), (16385, 5000, 8),
+                                        (20000, 300000, 3), (17000, 1, 100)])
 def test_gradient(gpu, n, rows, dim, io):
     g = gen(n + rows)
     dy = torch.randn(n, dim, generator=g, device=DEV).to(IO[io])
@@ -77,7 +78,7 @@ def test_gradient(gpu, n, rows, dim, io):
     check_grad(gpu, ids, dy, rows, grad_dtype=torch.bfloat16)
 
 
-@pytest.mark.parametrize("n", [32, 33, 64, 100, 5000])
+@pytest.mark.parametrize("n", [32, 33, 64, 100, 5000, 30000])
 def test_runs_across_workgroups(gpu, n):
     g = gen(n)
     dy = torch.randn(n, 20, generator=g, device=DEV)
