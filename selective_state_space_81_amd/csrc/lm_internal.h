@@ -123,7 +123,7 @@ struct LogprobArgs {
     void* dlogits;          // [rows][ldd]
     // workspace: per (row, split) partial sums and sorted keys
     float* part;     // [rows][splits][4]
-    uint64_t* list;  // [rows][splits][kMaxTop]
+    uint64_t* list;  // [rows][splits][top]
     float scale;
     int wide;
     int64_t rows;
@@ -131,7 +131,8 @@ struct LogprobArgs {
     int64_t ld;
     int64_t ldd;
     int top;
-    int splits;
+    int splits;    // workgroups of a row
+    uint32_t per;  // vectors each of them takes
 };
 struct LogprobWs {
     size_t part, list, total;

@@ -12,6 +12,7 @@ until that stream has passed them.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import selective_state_space_81_amd as ms
@@ -56,17 +57,18 @@ class _Call:
     its stream when that is not the current one (their memory could otherwise
     be handed out again while the call still uses it)."""
 
+    __slots__ = ("torch", "device", "stream", "other")
+
     def __init__(self, like, stream):
         import torch
-        self.torch, self.device = torch, like.device
-        current = torch.cuda.current_stream(like.device)
-        if stream is None:
-            self.stream, self.other = current.cuda_stream, None
-        else:
-            self.stream = stream if isinstance(stream, int) else stream.cuda_stream
-            self.other = None
-            if self.stream != current.cuda_stream:
-                self.other = torch.cuda.ExternalStream(self.stream, device=like.device) \
+        self.torch, self.device, self.other = torch, like.device, None
+        # the current stream's handle, without building a Stream around it
+        self.stream = torch._C._cuda_getCurrentRawStream(self.device.index)
+        if stream is not None:
+            given = stream if isinstance(stream, int) else stream.cuda_stream
+            if given != self.stream:
+                self.stream = given
+                self.other = torch.cuda.ExternalStream(given, device=self.device) \
                     if isinstance(stream, int) else stream
 
     def empty(self, shape, dtype):
@@ -81,22 +83,28 @@ class _Call:
             given = self.empty(need, self.torch.uint8)
         if given is None:
             return None, 0, None
+        if given.device != self.device or not given.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
         return given.data_ptr(), given.numel() * given.element_size(), given
 
-    def run(self, name, *args):
-        fn = getattr(ms.load(), name)
-        if self.torch.cuda.current_device() != self.device.index:
+    def run(self, fn, *args):
+        if self.torch._C._cuda_getDevice() != self.device.index:
             with self.torch.cuda.device(self.device):
                 rc = fn(*args, self.stream)
         else:
             rc = fn(*args, self.stream)
-        ms._check(rc)
+        if rc:
+            ms._check(rc)
 
 
-def _same_device(first, *others) -> None:
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
+def _chk(t, name, dtype, shape, device) -> None:
+    """The package's check of a tensor argument, and its device.  Written to
+    cost little when all is well: a step of a few microseconds makes a dozen."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and
+                     t.is_contiguous()):
+        return
+    ms._chk(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _size(n: int, what: str) -> int:
@@ -107,33 +115,32 @@ def _size(n: int, what: str) -> int:
 
 # ---- gated linear recurrence -------------------------------------------------------------
 
-def _chk_gated(x, r, i, lam, z, reset, h0, h_last):
+def _chk_gated(x, r, i, lam, z, reset):
+    """Checks of the arguments both passes share; (shape, device, io, reset)."""
     import torch
     if not getattr(x, "is_cuda", False) or x.dim() != 3:
         raise ValueError("x must be a [batch, L, d_inner] device tensor")
-    io = ms._io(x)
-    shape, f32 = tuple(x.shape), torch.float32
-    ms._chk(r, "r", x.dtype, shape)
-    ms._chk(i, "i", x.dtype, shape)
-    ms._chk(x, "x", x.dtype, shape)
-    ms._chk(lam, "lam", f32, shape[2:])
-    ms._chk(z, "z", x.dtype, shape)
+    io, shape, dev, dt = ms._io(x), x.shape, x.device, x.dtype
+    _chk(x, "x", dt, shape, dev)
+    _chk(r, "r", dt, shape, dev)
+    _chk(i, "i", dt, shape, dev)
+    _chk(lam, "lam", torch.float32, shape[2:], dev)
+    _chk(z, "z", dt, shape, dev)
     if reset is not None:
         if reset.dtype == torch.bool:
             reset = reset.view(torch.uint8)
-        ms._chk(reset, "reset", torch.uint8, shape[:2])
-    ms._chk(h0, "h0", f32, (shape[0], shape[2]))
-    ms._chk(h_last, "h_last", f32, (shape[0], shape[2]))
-    _same_device(x, r, i, lam, z, reset, h0, h_last)
-    return shape, io, reset
+        _chk(reset, "reset", torch.uint8, shape[:2], dev)
+    return shape, dev, io, reset
 
 
+@functools.lru_cache(maxsize=1024)
 def gated_scan_workspace_bytes(batch: int, seqlen: int, d_inner: int, io: int) -> int:
     """ms_gated_scan_workspace_bytes: workspace of gated_scan_fwd."""
     return _size(ms.load().ms_gated_scan_workspace_bytes(batch, seqlen, d_inner, io),
                  "the gated scan")
 
 
+@functools.lru_cache(maxsize=1024)
 def gated_scan_bwd_workspace_bytes(batch: int, seqlen: int, d_inner: int, io: int) -> int:
     """ms_gated_scan_bwd_workspace_bytes: workspace of gated_scan_bwd."""
     return _size(ms.load().ms_gated_scan_bwd_workspace_bytes(batch, seqlen, d_inner, io),
@@ -157,16 +164,19 @@ def gated_scan_fwd(x, r, i, lam, z=None, *, c=8.0, reset=None, y=None, h0=None, 
     what the backward needs.  Allocates y (and the workspace) when not given.
     Returns y."""
     import torch
-    (b, L, d), io, reset = _chk_gated(x, r, i, lam, z, reset, h0, h_last)
-    ms._chk(y, "y", x.dtype, (b, L, d))
-    ms._chk(states, "states", torch.float32, (b, -(-L // GATED_BLOCK), d))
-    _same_device(x, y, states)
+    shape, dev, io, reset = _chk_gated(x, r, i, lam, z, reset)
+    b, L, d = shape
+    f32 = torch.float32
+    _chk(h0, "h0", f32, (b, d), dev)
+    _chk(h_last, "h_last", f32, (b, d), dev)
+    _chk(y, "y", x.dtype, shape, dev)
+    _chk(states, "states", f32, (b, -(-L // GATED_BLOCK), d), dev)
     call = _Call(x, stream)
     if y is None:
-        y = call.empty((b, L, d), x.dtype)
+        y = call.empty(shape, x.dtype)
     wp, wn, keep = call.workspace(workspace, gated_scan_workspace_bytes(b, L, d, io))
     p = ms._ptr
-    call.run("ms_gated_scan_fwd", p(x), p(r), p(i), p(lam), c, p(z), p(reset), p(y), p(h0),
+    call.run(ms.load().ms_gated_scan_fwd, p(x), p(r), p(i), p(lam), c, p(z), p(reset), p(y), p(h0),
              p(h_last), p(states), b, L, d, io, wp, wn)
     return y
 
@@ -177,22 +187,24 @@ def gated_scan_bwd(x, r, i, lam, dy, states, z=None, *, c=8.0, reset=None, dh_la
     for dy (and optionally dh_last), with the states it saved.  Returns a dict:
     dx, dr, di, dz (io dtype; dz None without z), dlam and dh0 (fp32)."""
     import torch
-    (b, L, d), io, reset = _chk_gated(x, r, i, lam, z, reset, None, None)
+    shape, dev, io, reset = _chk_gated(x, r, i, lam, z, reset)
+    b, L, d = shape
     f32 = torch.float32
     if states is None:
         raise ValueError("states is required (gated_scan_fwd fills it)")
-    ms._chk(states, "states", f32, (b, -(-L // GATED_BLOCK), d))
-    ms._chk(dy, "dy", x.dtype, (b, L, d))
-    ms._chk(dh_last, "dh_last", f32, (b, d))
-    _same_device(x, states, dy, dh_last)
+    if dy is None:
+        raise ValueError("dy is required")
+    _chk(states, "states", f32, (b, -(-L // GATED_BLOCK), d), dev)
+    _chk(dy, "dy", x.dtype, shape, dev)
+    _chk(dh_last, "dh_last", f32, (b, d), dev)
     call = _Call(x, stream)
-    out = {k: call.empty((b, L, d), x.dtype) for k in ("dx", "dr", "di")}
-    out["dz"] = call.empty((b, L, d), x.dtype) if z is not None else None
+    out = {k: call.empty(shape, x.dtype) for k in ("dx", "dr", "di")}
+    out["dz"] = call.empty(shape, x.dtype) if z is not None else None
     out["dlam"] = call.empty((d,), f32)
     out["dh0"] = call.empty((b, d), f32) if want_dh0 else None
     wp, wn, keep = call.workspace(workspace, gated_scan_bwd_workspace_bytes(b, L, d, io))
     p = ms._ptr
-    call.run("ms_gated_scan_bwd", p(x), p(r), p(i), p(lam), c, p(z), p(reset), p(states), p(dy),
+    call.run(ms.load().ms_gated_scan_bwd, p(x), p(r), p(i), p(lam), c, p(z), p(reset), p(states), p(dy),
              p(dh_last), p(out["dx"]), p(out["dr"]), p(out["di"]), p(out["dz"]), p(out["dlam"]),
              p(out["dh0"]), b, L, d, io, wp, wn)
     return out
@@ -204,21 +216,22 @@ def gated_step(h, x_t, r_t, i_t, lam, z_t=None, *, c=8.0, y_t=None, stream=None)
     import torch
     if not getattr(x_t, "is_cuda", False) or x_t.dim() != 2:
         raise ValueError("x_t must be a [batch, d_inner] device tensor")
-    io = ms._io(x_t)
-    shape = tuple(x_t.shape)
-    ms._chk(h, "h", torch.float32, shape)
-    ms._chk(x_t, "x_t", x_t.dtype, shape)
-    ms._chk(r_t, "r_t", x_t.dtype, shape)
-    ms._chk(i_t, "i_t", x_t.dtype, shape)
-    ms._chk(lam, "lam", torch.float32, shape[1:])
-    ms._chk(z_t, "z_t", x_t.dtype, shape)
-    ms._chk(y_t, "y_t", x_t.dtype, shape)
-    _same_device(x_t, h, r_t, i_t, lam, z_t, y_t)
+    io, shape, dev, dt = ms._io(x_t), x_t.shape, x_t.device, x_t.dtype
+    f32 = torch.float32
+    if h is None:
+        raise ValueError("h is required")
+    _chk(h, "h", f32, shape, dev)
+    _chk(x_t, "x_t", dt, shape, dev)
+    _chk(r_t, "r_t", dt, shape, dev)
+    _chk(i_t, "i_t", dt, shape, dev)
+    _chk(lam, "lam", f32, shape[1:], dev)
+    _chk(z_t, "z_t", dt, shape, dev)
+    _chk(y_t, "y_t", dt, shape, dev)
     call = _Call(x_t, stream)
     if y_t is None:
-        y_t = call.empty(shape, x_t.dtype)
+        y_t = call.empty(shape, dt)
     p = ms._ptr
-    call.run("ms_gated_step", p(h), p(x_t), p(r_t), p(i_t), p(lam), c, p(z_t), p(y_t),
+    call.run(ms.load().ms_gated_step, p(h), p(x_t), p(r_t), p(i_t), p(lam), c, p(z_t), p(y_t),
              shape[0], shape[1], io)
     return y_t
 
@@ -242,20 +255,20 @@ def embed_fwd(ids, weight, *, scale=1.0, out=None, stream=None):
         raise ValueError("weight must be a [rows, dim] device tensor")
     io = ms._io(weight)
     rows, dim = weight.shape
-    bits = _id_bits(ids, "ids")
-    ms._chk(ids, "ids", ids.dtype, ids.shape)
-    ms._chk(weight, "weight", weight.dtype, (rows, dim))
+    bits, dev = _id_bits(ids, "ids"), weight.device
+    _chk(ids, "ids", ids.dtype, ids.shape, dev)
+    _chk(weight, "weight", weight.dtype, weight.shape, dev)
     shape = (*ids.shape, dim)
-    ms._chk(out, "out", weight.dtype, shape)
-    _same_device(weight, ids, out)
+    _chk(out, "out", weight.dtype, shape, dev)
     call = _Call(weight, stream)
     if out is None:
         out = call.empty(shape, weight.dtype)
-    call.run("ms_embed_fwd", ms._ptr(ids), bits, ms._ptr(weight), scale, ms._ptr(out),
+    call.run(ms.load().ms_embed_fwd, ms._ptr(ids), bits, ms._ptr(weight), scale, ms._ptr(out),
              ids.numel(), rows, dim, io)
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def embed_bwd_workspace_bytes(n: int, rows: int, dim: int, io: int) -> int:
     """ms_embed_bwd_workspace_bytes: workspace of embed_bwd."""
     return _size(ms.load().ms_embed_bwd_workspace_bytes(n, rows, dim, io),
@@ -272,22 +285,21 @@ def embed_bwd(ids, dy, rows, *, scale=1.0, padding=-1, grad_dtype=None, dweight=
         raise ValueError("dy must be a [*ids.shape, dim] device tensor")
     io = ms._io(dy)
     bits = _id_bits(ids, "ids")
-    dim = dy.shape[-1]
-    ms._chk(ids, "ids", ids.dtype, ids.shape)
-    ms._chk(dy, "dy", dy.dtype, (*ids.shape, dim))
+    dim, dev = dy.shape[-1], dy.device
+    _chk(ids, "ids", ids.dtype, ids.shape, dev)
+    _chk(dy, "dy", dy.dtype, (*ids.shape, dim), dev)
     if grad_dtype is None:
         grad_dtype = dy.dtype if dweight is None else dweight.dtype
     if grad_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"grad_dtype must be float32 or bfloat16, got {grad_dtype}")
-    ms._chk(dweight, "dweight", grad_dtype, (rows, dim))
-    _same_device(dy, ids, dweight)
+    _chk(dweight, "dweight", grad_dtype, (rows, dim), dev)
     n = ids.numel()
     need = embed_bwd_workspace_bytes(n, rows, dim, io)
     call = _Call(dy, stream)
     if dweight is None:
         dweight = call.empty((rows, dim), grad_dtype)
     wp, wn, keep = call.workspace(workspace, need)
-    call.run("ms_embed_bwd", ms._ptr(ids), bits, ms._ptr(dy), scale, padding, ms._ptr(dweight),
+    call.run(ms.load().ms_embed_bwd, ms._ptr(ids), bits, ms._ptr(dy), scale, padding, ms._ptr(dweight),
              ms.MS_BF16 if grad_dtype == torch.bfloat16 else ms.MS_F32, n, rows, dim, io, wp, wn)
     return dweight
 
@@ -307,14 +319,14 @@ def _chk_logits(logits, name="logits"):
     return rows, vocab, ld
 
 
-def _chk_targets(targets, rows):
+def _chk_targets(targets, rows, device):
     if targets is None:
         return 64
-    bits = _id_bits(targets, "targets")
-    ms._chk(targets, "targets", targets.dtype, (rows,))
-    return bits
+    _chk(targets, "targets", targets.dtype, (rows,), device)
+    return _id_bits(targets, "targets")
 
 
+@functools.lru_cache(maxsize=1024)
 def token_logprobs_workspace_bytes(rows: int, vocab: int, top: int, io: int) -> int:
     """ms_token_logprobs_workspace_bytes: workspace of token_logprobs_fwd."""
     return _size(ms.load().ms_token_logprobs_workspace_bytes(rows, vocab, top, io),
@@ -330,8 +342,7 @@ def token_logprobs_fwd(logits, targets=None, *, top=0, scale=1.0, workspace=None
     import torch
     rows, vocab, ld = _chk_logits(logits)
     io = ms._io(logits)
-    bits = _chk_targets(targets, rows)
-    _same_device(logits, targets)
+    bits = _chk_targets(targets, rows, logits.device)
     f32 = torch.float32
     need = token_logprobs_workspace_bytes(rows, vocab, top, io)
     call = _Call(logits, stream)
@@ -342,7 +353,7 @@ def token_logprobs_fwd(logits, targets=None, *, top=0, scale=1.0, workspace=None
            "top_id": call.empty((rows, top), torch.int32)}
     wp, wn, keep = call.workspace(workspace, need)
     p = ms._ptr
-    call.run("ms_token_logprobs_fwd", p(logits), ld, p(targets), bits, scale, p(out["logprob"]),
+    call.run(ms.load().ms_token_logprobs_fwd, p(logits), ld, p(targets), bits, scale, p(out["logprob"]),
              p(out["entropy"]), p(out["lse"]), p(out["stats"]), top, p(out["top_logprob"]),
              p(out["top_id"]), rows, vocab, io, wp, wn)
     return out
@@ -357,11 +368,12 @@ def token_logprobs_bwd(logits, targets, stats, entropy=None, dlogprob=None, dent
     import torch
     rows, vocab, ld = _chk_logits(logits)
     io = ms._io(logits)
-    bits = _chk_targets(targets, rows)
+    dev = logits.device
+    bits = _chk_targets(targets, rows, dev)
     f32 = torch.float32
-    ms._chk(stats, "stats", f32, (rows, 2))
+    _chk(stats, "stats", f32, (rows, 2), dev)
     for t, name in ((entropy, "entropy"), (dlogprob, "dlogprob"), (dentropy, "dentropy")):
-        ms._chk(t, name, f32, (rows,))
+        _chk(t, name, f32, (rows,), dev)
     call = _Call(logits, stream)
     if dlogits is None:
         dlogits = call.empty((rows, vocab), logits.dtype)
@@ -370,9 +382,10 @@ def token_logprobs_bwd(logits, targets, stats, entropy=None, dlogprob=None, dent
         raise TypeError(f"dlogits must be {logits.dtype}, got {dlogits.dtype}")
     if (r2, v2) != (rows, vocab):
         raise ValueError(f"dlogits must have shape {(rows, vocab)}, got {(r2, v2)}")
-    _same_device(logits, targets, stats, entropy, dlogprob, dentropy, dlogits)
+    if dlogits.device != dev:
+        raise ValueError(f"dlogits is on {dlogits.device}, not on {dev}")
     p = ms._ptr
-    call.run("ms_token_logprobs_bwd", p(logits), ld, p(targets), bits, scale, p(stats), p(entropy),
+    call.run(ms.load().ms_token_logprobs_bwd, p(logits), ld, p(targets), bits, scale, p(stats), p(entropy),
              p(dlogprob), p(dentropy), p(dlogits), ldd, rows, vocab, io)
     return dlogits
 
