@@ -6,20 +6,21 @@
 //   dlogit_v = scale * (g_lp ([v = t] - p_v) - g_H p_v (log p_v + H))
 //
 // Both are bound by memory: the forward reads every logit once, the gradient
-// reads and writes each once.  The forward keeps, per lane, the running
-// maximum m, s = sum 2^d and T = sum d 2^d with d = (logit - m) c and
-// c = scale log2 e, moved to a new maximum by (s, T) -> 2^delta (s, T + delta s).
-// Sums of d, not of x, so that the entropy ln s - ln2 T / s has no
-// cancellation against a large maximum.
+// reads and writes each once.  The forward keeps, per lane, a reference r near
+// the running maximum, s = sum 2^d and T = sum d 2^d with d = c logit - r (one
+// fused operation) and c = scale log2 e, moved to a new reference by
+// (s, T) -> 2^delta (s, T + delta s).  Sums of d, not of x, so that the entropy
+// ln2 (log2 s - T / s) has no cancellation against a large maximum.
 //
 // Alternatives come from the same pass.  A wave holds a threshold that at least
-// `top` of its logits reach, first from the maxima of its lanes' first block
-// (the top-th largest of 64), and notes the tokens that reach it; blocks whose
-// maximum, known from the softmax, stays below cost one comparison.  Few tokens
-// are noted (some ten of 10000 at top 5), so at the end each finds its rank by
-// counting the larger ones of its workgroup, in LDS.  Should more than 64 come
-// together before that (rows that rise), the wave sorts them, keeps the best
-// and raises its threshold.
+// `top` logits of the row reach, first from the maxima of its lanes' first
+// block (the top-th largest of them), and the best of what the workgroup's
+// other waves have found.  A lane whose block of 32 (16 in fp32) logits reaches
+// it, known from the maximum that the softmax needs anyway, notes the block:
+// one comparison a block, and some four notes in 2000 logits at top 5.  At the
+// end few of the noted blocks reach the last threshold; those are read again
+// (they are in cache), and each logit that reaches it finds its rank by
+// counting the larger ones of the workgroup, in LDS.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -34,6 +35,9 @@ namespace {
 
 using namespace dev;
 
+#ifndef LP_U
+#define LP_U 4
+#endif
 #ifndef LP_OCC
 #define LP_OCC 4
 #endif
@@ -44,8 +48,10 @@ using namespace dev;
 #define LP_MIN 4096
 #endif
 constexpr int kLpWaves = 4;
-constexpr int kMaxJoin = 1024;  // keys of a row's splits together
-constexpr float kLowest = -3.402823466e38f;
+constexpr int kMaxKeys = 1024;  // keys that a workgroup ranks
+// References stay within +-kFar; a row whose largest logit is past it (all of
+// them the type's lowest value, say) has its sums taken again by far_row.
+constexpr float kFar = 1e38f;
 // Exponents below this give 2^d = 0 in fp32; d is held here in the products
 // d 2^d, where -inf times 0 would be NaN.
 constexpr float kDead = -200.f;
@@ -123,15 +129,15 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // ---- softmax statistics ---------------------------------------------------------------
 struct Stat {
-    float m, s, T;
-    __device__ __forceinline__ void move(float mn, float c) {
-        const float dl = fmaxf((m - mn) * c, kDead), f = hw_exp2(dl);
+    float r, s, T;
+    __device__ __forceinline__ void move(float to) {
+        const float dl = fmaxf(r - to, kDead), f = hw_exp2(dl);
         T = f * fmaf(dl, s, T);
         s *= f;
-        m = mn;
+        r = to;
     }
-    __device__ __forceinline__ void join_wave(float c) {
-        move(wave_max(m), c);
+    __device__ __forceinline__ void join_wave() {
+        move(wave_max(r));
         s = wave_sum(s);
         T = wave_sum(T);
     }
@@ -188,77 +194,113 @@ __device__ __forceinline__ uint64_t merge_in(uint64_t list, uint64_t v, int lane
     return v;
 }
 
-// What a wave has noted: up to 127 tokens in LDS (its own part), and, once
-// more than 64 have come together, the best of those before them as a list.
-template <class L>
-struct Noted {
-    const typename L::E* x;  // the row
-    uint32_t* tok;           // [128]
-    uint64_t list;           // lane l: the (l+1)-th best so far, or 0
-    float thr;               // what a logit has to reach to be noted
-    int top, count, lane;
-    bool listed;
+// Blocks that a wave has noted, in LDS: the first token and the largest logit
+// of each.  kNoteRoom: what is kept of a flush (below) is at most what came
+// together since the one before (kNoteFlush and a block of 64 lanes) and fewer
+// than `top` (64) more, and another block may follow.
+constexpr int kNoteFlush = 128, kNoteRoom = kNoteFlush + 64 + 64 + 64;
+struct Notes {
+    uint32_t first[kNoteRoom];
+    float high[kNoteRoom];
+};
 
-    __device__ __forceinline__ void init(const typename L::E* row, uint32_t* t, int top_,
-                                         int lane_) {
-        x = row;
-        tok = t;
-        list = 0;
-        thr = -__builtin_inff();
+struct Noted {
+    Notes* q;
+    float thr;    // what a block's largest logit has to reach to be noted
+    float bound;  // what at least `top` logits of the wave reach
+    int top, count, lane;
+
+    __device__ __forceinline__ void init(Notes* notes, int top_, int lane_) {
+        q = notes;
+        thr = bound = -__builtin_inff();
         top = top_;
         count = 0;
         lane = lane_;
-        listed = false;
     }
-    // First threshold: the top-th largest lane maximum, as the least of those
-    // with fewer than `top` above them.
-    __device__ __forceinline__ void seed(float lane_max) {
-        const float v = lane_max == lane_max ? lane_max : -__builtin_inff();
+    // A value that at least `top` of the wave's logits reach: the top-th largest
+    // of its 64 lanes' maxima, or, for few alternatives, of the maxima of 16
+    // quads of lanes (a threshold almost as high for a quarter of the work), as
+    // the least of those with fewer than `top` above them.
+    __device__ __forceinline__ float reached(float lane_max) const {
+        float v = lane_max == lane_max ? lane_max : -__builtin_inff();
         int above = 0;
+        auto count_above = [&](auto step) {
 #pragma unroll 16
-        for (int l = 0; l < 64; ++l)
-            above += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l)) > v;
-        thr = -wave_max(above < top ? -v : -__builtin_inff());
-    }
-    __device__ __forceinline__ uint64_t key_at(int k) const {
-        const uint32_t t = tok[k];
-        return top_key(L::one(x + t), t);
-    }
-    // Logits of later blocks have higher tokens than those of the list, so a
-    // tie with the top-th does not enter.
-    __device__ __forceinline__ void flush() {
-        wave_sync();
-        const uint64_t v = lane < count ? key_at(lane) : 0;
-        const uint32_t rest = lane + 64 < count ? tok[lane + 64] : 0;
-        wave_sync();
-        tok[lane] = rest;
-        count = count > 64 ? count - 64 : 0;
-        list = merge_in(list, v, lane);
-        listed = true;
-        const uint64_t k = shfl64(list, top - 1);
-        if (k) thr = next_above(key_value(k));
-    }
-    // Notes the lane's tokens first + (bit / N) * 64 N + bit % N, one for each
-    // bit of `bits`.
-    template <int N>
-    __device__ __forceinline__ void note(uint32_t bits, uint32_t first) {
-        for (;;) {
-            const uint64_t m = __ballot(bits != 0);
-            if (!m) return;
-            if (bits) {
-                const int b = __builtin_ctz(bits);
-                bits &= bits - 1;
-                tok[count + __popcll(m & ((1ull << lane) - 1))] = first + b / N * (64 * N) + b % N;
-            }
-            count += __popcll(m);
-            if (count >= 64) flush();
+            for (int l = 0; l < 64; l += decltype(step)::value)
+                above += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l)) > v;
+        };
+        if (top <= 8) {
+            auto dpp = [&](auto ctrl) {
+                v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(
+                                 __float_as_int(v), decltype(ctrl)::value, 0xf, 0xf, true)));
+            };
+            dpp(std::integral_constant<int, 0xB1>{});  // quad_perm 1,0,3,2
+            dpp(std::integral_constant<int, 0x4E>{});  // quad_perm 2,3,0,1
+            count_above(std::integral_constant<int, 4>{});
+        } else {
+            count_above(std::integral_constant<int, 1>{});
         }
+        return -wave_max(above < top ? -v : -__builtin_inff());
+    }
+    __device__ __forceinline__ void note(bool in, uint32_t first, float high) {
+        const uint64_t m = __ballot(in);
+        if (in) {
+            const int k = count + __popcll(m & ((1ull << lane) - 1));
+            q->first[k] = first;
+            q->high[k] = high;
+        }
+        count += __popcll(m);
+        if (count >= kNoteFlush) flush();
+    }
+    // Many notes (rows that rise): the top-th largest of their maxima is reached
+    // by `top` logits, so notes below it go.  Blocks to come have higher tokens
+    // and have to exceed it.
+    __device__ __forceinline__ void flush() {
+        constexpr int K = kNoteRoom / 64;
+        wave_sync();
+        uint32_t first[K], o[K];
+        float high[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const bool in = k * 64 + lane < count;
+            first[k] = in ? q->first[k * 64 + lane] : 0;
+            high[k] = in ? q->high[k * 64 + lane] : 0.f;
+            const uint32_t b = __float_as_uint(high[k] + 0.f);
+            o[k] = in ? b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u) : 0;  // ordered; 0 is below all
+        }
+        uint32_t x = 0;  // the largest number that `top` of them reach, bit by bit
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t y = x | (1u << bit);
+            int n = 0;
+#pragma unroll
+            for (int k = 0; k < K; ++k) n += __popcll(__ballot(o[k] >= y));
+            if (n >= top) x = y;
+        }
+        wave_sync();
+        int kept = 0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const bool in = o[k] != 0 && o[k] >= x;
+            const uint64_t m = __ballot(in);
+            if (in) {
+                const int at = kept + __popcll(m & ((1ull << lane) - 1));
+                q->first[at] = first[k];
+                q->high[at] = high[k];
+            }
+            kept += __popcll(m);
+        }
+        count = kept;
+        if (x) {
+            bound = __uint_as_float(x ^ ((x >> 31) ? 0x80000000u : 0xffffffffu));
+            thr = fmaxf(thr, next_above(bound));
+        }
+        wave_sync();
     }
 };
 
 // The `top` best of n keys in LDS, sorted, to out[0 .. top) (0 where there are
 // not so many): each key's rank is the number of larger ones.  A key that is
-// not there is 0; others differ.
+// not there is 0; others differ.  By the whole workgroup.
 __device__ __forceinline__ void rank_keys(const uint64_t* key, int n, int top, uint64_t* out) {
     for (int k = threadIdx.x; k < top; k += blockDim.x) out[k] = 0;
     __syncthreads();
@@ -272,42 +314,81 @@ __device__ __forceinline__ void rank_keys(const uint64_t* key, int n, int top, u
     __syncthreads();
 }
 
-// What the rows' results are once the statistics and the sorted keys are known.
+// What the rows' results are once the statistics and the sorted keys are
+// known; high: the row's largest logit.
 __device__ __forceinline__ void finish_row(const LogprobArgs& a, int64_t row, const Stat& st,
-                                           float target_logit, bool has_target,
+                                           float high, float target_logit, bool has_target,
                                            const uint64_t* best) {
-    const bool empty = st.s == 0.f;  // every logit is -inf
-    const float lns = empty ? 0.f : logf(st.s);
+    const float c = a.scale * kLog2e;
+    const bool empty = high == -__builtin_inff() && st.s == 0.f;  // every logit is -inf
+    const bool far = !(fabsf(high * c) < kFar);    // then r stands for high itself: see far_row
+    const float l2 = empty ? 0.f : log2f(st.s);
+    // Neither lse - scale * high nor the entropy is below 0; the rounding of r
+    // can leave them there by 2^-24 of it (a NaN stays).
+    auto at_least_0 = [](float v) { return v < 0.f ? 0.f : v; };
+    const float rest = empty ? -__builtin_inff()
+                             : at_least_0((l2 + (far ? 0.f : fmaf(-high, c, st.r))) * kLn2);
+    // x - lse of a logit
+    auto logp = [&](float v) {
+        return empty ? -__builtin_inff() : fmaf(v - high, a.scale, -rest);
+    };
     if (threadIdx.x == 0) {
-        if (a.lse) a.lse[row] = empty ? -__builtin_inff() : fmaf(st.m, a.scale, lns);
+        if (a.lse) a.lse[row] = empty ? rest : fmaf(high, a.scale, rest);
         if (a.stats) {
-            a.stats[2 * row] = st.m;
-            a.stats[2 * row + 1] = empty ? -__builtin_inff() : lns;
+            a.stats[2 * row] = high;
+            a.stats[2 * row + 1] = rest;
         }
-        if (a.entropy) a.entropy[row] = empty ? 0.f : lns - kLn2 * (st.T / st.s);
-        if (a.logprob) {
-            float lp = 0.f;
-            if (has_target)
-                lp = empty ? -__builtin_inff() : (target_logit - st.m) * a.scale - lns;
-            a.logprob[row] = lp;
-        }
+        if (a.entropy) a.entropy[row] = empty ? 0.f : at_least_0(kLn2 * (l2 - st.T / st.s));
+        if (a.logprob) a.logprob[row] = has_target ? logp(target_logit) : 0.f;
     }
     if ((int)threadIdx.x < a.top) {
         const uint64_t k = best[threadIdx.x];
-        float lp = -__builtin_inff();
-        if (k && !empty) lp = (key_value(k) - st.m) * a.scale - lns;
         a.top_id[row * a.top + threadIdx.x] = k ? (int32_t)~(uint32_t)k : -1;
-        a.top_logprob[row * a.top + threadIdx.x] = lp;
+        a.top_logprob[row * a.top + threadIdx.x] = k ? logp(key_value(k)) : -__builtin_inff();
     }
 }
 
-// Joins the statistics of a few waves or splits, one a lane, in every lane.
-__device__ __forceinline__ Stat join_lanes(const float* part, int n, int stride, float c) {
+// Joins the statistics of a few waves or splits, one a lane, in every lane
+// ({r, s, T, largest logit} each, `stride` apart).
+__device__ __forceinline__ Stat join_lanes(const float* part, int n, int stride, float& high) {
     const int lane = threadIdx.x & 63;
-    Stat st{kLowest, 0.f, 0.f};
-    if (lane < n) st = Stat{part[lane * stride], part[lane * stride + 1], part[lane * stride + 2]};
-    st.join_wave(c);
+    Stat st{-kFar, 0.f, 0.f};
+    float h = -__builtin_inff();
+    if (lane < n) {
+        const float* q = part + lane * stride;
+        st = Stat{q[0], q[1], q[2]};
+        h = q[3];
+    }
+    st.join_wave();
+    high = wave_max(h);
     return st;
+}
+
+// s and T of a row whose largest logit is so far out that c * logit does not
+// fit, with d = (logit - high) c, by one wave; r is left 0.
+template <class L>
+__device__ __forceinline__ Stat far_row(const typename L::E* x, int64_t V, float high, float c) {
+    Stat st{0.f, 0.f, 0.f};
+    for (int64_t i = threadIdx.x & 63; i < V; i += 64) {
+        const float d = (L::one(x + i) - high) * c, w = hw_exp2(d);
+        st.s += w;
+        st.T = fmaf(w, fmaxf(d, kDead), st.T);
+    }
+    st.s = wave_sum(st.s);
+    st.T = wave_sum(st.T);
+    return st;
+}
+
+// The end of a row, by the workgroup's first wave, from parts as join_lanes reads them.
+template <class L>
+__device__ __forceinline__ void end_row(const LogprobArgs& a, int64_t row, const float* part, int n,
+                                        const typename L::E* x, float target_logit,
+                                        bool has_target, const uint64_t* best) {
+    float high;
+    Stat st = join_lanes(part, n, 4, high);
+    const float c = a.scale * kLog2e;
+    if (high != -__builtin_inff() && !(fabsf(high * c) < kFar)) st = far_row<L>(x, a.V, high, c);
+    finish_row(a, row, st, high, target_logit, has_target, best);
 }
 
 // ---- forward ------------------------------------------------------------------------------
@@ -315,11 +396,11 @@ template <bool BF16, bool TOP>
 __global__ void __launch_bounds__(64 * kLpWaves, LP_OCC) logprob_fwd(LogprobArgs a) {
     using L = Lg<BF16>;
     using E = typename L::E;
-    constexpr int N = L::N, U = 4;  // vectors a lane takes of a block
-    __shared__ uint64_t s_key[TOP ? kLpWaves * 128 : 1], s_best[TOP ? kMaxTop : 1];
-    __shared__ uint32_t s_tok[TOP ? kLpWaves : 1][TOP ? 128 : 1];
-    __shared__ float s_stat[kLpWaves][3];
-    __shared__ int s_count[kLpWaves];
+    constexpr int N = L::N, U = LP_U;  // vectors a lane takes of a block
+    __shared__ uint64_t s_key[TOP ? kMaxKeys : 1], s_best[TOP ? kMaxTop : 1];
+    __shared__ Notes s_notes[TOP ? kLpWaves : 1];
+    __shared__ float s_stat[kLpWaves][4], s_thr[kLpWaves];
+    __shared__ int s_count;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const float c = a.scale * kLog2e;
@@ -337,138 +418,221 @@ __global__ void __launch_bounds__(64 * kLpWaves, LP_OCC) logprob_fwd(LogprobArgs
     }
     const E* x = static_cast<const E*>(a.logits) + row * a.ld;
 
-    Stat st{kLowest, 0.f, 0.f};
-    Noted<L> noted;
-    if constexpr (TOP) noted.init(x, s_tok[wave], a.top, lane);
+    Stat st{-kFar, 0.f, 0.f};
+    float high = -__builtin_inff();  // the lane's largest logit
+    Noted noted;
+    if constexpr (TOP) {
+        noted.init(&s_notes[wave], a.top, lane);
+        if (threadIdx.x < kLpWaves) s_thr[threadIdx.x] = -__builtin_inff();
+        if (threadIdx.x == 0) s_count = 0;
+        __syncthreads();
+    }
+    auto shared_threshold = [&]() {
+        float t = -__builtin_inff();
+#pragma unroll
+        for (int k = 0; k < kLpWaves; ++k)
+            t = fmaxf(t, __hip_atomic_load(&s_thr[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
+        return t;
+    };
     bool first = true;
 
-    // the lane's K logits (-inf where there is none: `have` of them are)
-    auto take = [&](auto& v, auto K, uint32_t have, uint32_t token) {
+    // the lane's K logits (-inf where there is none; any: one is), from `token`
+    auto take = [&](auto& v, auto K, bool any, uint32_t token) {
         constexpr int kN = decltype(K)::value;
         float mb = v[0];
 #pragma unroll
         for (int e = 1; e < kN; ++e) mb = fmaxf(mb, v[e]);
         if constexpr (TOP) {
             if (first) {
-                noted.seed(mb);
                 first = false;
+                noted.bound = noted.reached(mb);
+                if (lane == 0)
+                    __hip_atomic_store(&s_thr[wave], noted.bound, __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_WORKGROUP);
+                noted.thr = noted.bound;
             }
-            if (__any(mb >= noted.thr)) {
-                uint32_t bits = 0;
-#pragma unroll
-                for (int e = kN - 1; e >= 0; --e) bits = 2 * bits + (v[e] >= noted.thr ? 1u : 0u);
-                noted.template note<N>(bits & have, token);
-            }
+            // (How much of the other waves' thresholds is here by now changes
+            // what is noted, not what comes out.)
+            noted.thr = fmaxf(noted.thr, shared_threshold());
+            const bool in = any && mb >= noted.thr;
+            if (__any(in)) noted.note(in, token, mb);
         }
-        st.move(fmaxf(st.m, mb), c);
+        high = fmaxf(high, mb);
+        st.move(fminf(fmaxf(st.r, mb * c), kFar));
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
-            const float d = (v[e] - st.m) * c, w = hw_exp2(d);
+            const float d = fmaf(v[e], c, -st.r), w = hw_exp2(d);
             st.s += w;
             st.T = fmaf(w, fmaxf(d, kDead), st.T);
         }
     };
 
-    typename L::T w[U], nx[U];
+    typename L::T w0[U], w1[U];
     auto load = [&](uint32_t b, typename L::T(&r)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u) r[u] = L::load(x + (int64_t)min(b + u * 64 + lane, v1 - 1) * N);
     };
-    uint32_t b = v0 + wave * (64 * U);
-    if (b < v1) load(b, w);
-    // the target's logit travels beside the row
-    const int64_t target = target_of(a, row);
-    float tl = 0.f;
-    if (wave == 0 && target >= 0) tl = L::one(x + target);
-    for (; b < v1; b += 64 * U * kLpWaves) {
-        const uint32_t bn = b + 64 * U * kLpWaves;
-        if (bn < v1) load(bn, nx);
+    auto block = [&](uint32_t b, const typename L::T(&r)[U]) {
         float v[U * N];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float t[N];
-            L::unpack(w[u], t);
+            L::unpack(r[u], t);
 #pragma unroll
             for (int e = 0; e < N; ++e) v[u * N + e] = t[e];
         }
-        uint32_t have = U * N == 32 ? 0xffffffffu : (1u << (U * N)) - 1;
+        bool any = true;
         if (b + 64 * U > v1) {  // the end of the vectors
-            have = 0;
+            any = b + lane < v1;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const bool in = b + u * 64 + lane < v1;
-                if (in) have |= ((1u << N) - 1) << (u * N);
 #pragma unroll
                 for (int e = 0; e < N; ++e) v[u * N + e] = in ? v[u * N + e] : -__builtin_inff();
             }
         }
-        take(v, std::integral_constant<int, U * N>{}, have, (b + lane) * N);
-#pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = nx[u];
+        take(v, std::integral_constant<int, U * N>{}, any, (b + lane) * N);
+    };
+    constexpr uint32_t kStep = 64 * U * kLpWaves;
+    uint32_t b = v0 + wave * (64 * U);
+    if (b < v1) load(b, w0);
+    // the target's logit travels beside the row
+    const int64_t target = target_of(a, row);
+    float tl = 0.f;
+    if (wave == 0 && target >= 0) tl = L::one(x + target);
+    while (b < v1) {  // two blocks a turn, one under way while the other is taken
+        if (b + kStep < v1) load(b + kStep, w1);
+        block(b, w0);
+        b += kStep;
+        if (b >= v1) break;
+        if (b + kStep < v1) load(b + kStep, w0);
+        block(b, w1);
+        b += kStep;
     }
     if (wave == 0 && last && (int64_t)nvec * N < a.V) {  // the row's last V % N logits
         const int64_t i = (int64_t)nvec * N + lane;
         const bool in = i < a.V;
         float v[1] = {in ? L::one(x + i) : -__builtin_inff()};
-        take(v, std::integral_constant<int, 1>{}, in ? 1u : 0u, (uint32_t)i);
+        take(v, std::integral_constant<int, 1>{}, in, (uint32_t)i);
     }
-    st.join_wave(c);
-    if (lane == 0) s_stat[wave][0] = st.m, s_stat[wave][1] = st.s, s_stat[wave][2] = st.T;
+    if constexpr (TOP) {
+        const float t = fmaxf(noted.reached(high), noted.bound);
+        if (lane == 0)
+            __hip_atomic_store(&s_thr[wave], t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    }
+    st.join_wave();
+    high = wave_max(high);
+    if (lane == 0) {
+        s_stat[wave][0] = st.r;
+        s_stat[wave][1] = st.s;
+        s_stat[wave][2] = st.T;
+        s_stat[wave][3] = high;
+    }
+    __syncthreads();
     const int64_t at = row * a.splits + (a.splits > 1 ? blockIdx.x % (uint32_t)a.splits : 0);
     if constexpr (TOP) {
-        wave_sync();
-        if (lane == 0) s_count[wave] = noted.count + (noted.listed ? a.top : 0);
-        __syncthreads();
-        int k0 = 0, n = 0;
+        // Noted blocks that reach the row's last threshold, G logits each, read
+        // again 64 / G blocks at a time; f gets every logit that reaches it.
+        const float t = shared_threshold();
+        constexpr int G = U * N;
+        auto read_again = [&](auto f) {
+            const Notes& q = s_notes[wave];
+            for (int k0 = 0; k0 < noted.count; k0 += 64) {
+                const bool in = k0 + lane < noted.count && q.high[k0 + lane] >= t;
+                uint64_t m = __ballot(in);
+                const uint32_t mine = in ? q.first[k0 + lane] : 0;
+                while (m) {
+                    uint32_t from = 0xffffffffu;
 #pragma unroll
-        for (int k = 0; k < kLpWaves; ++k) {
-            if (k == wave) k0 = n;
-            n += s_count[k];
+                    for (int g = 0; g < 64 / G; ++g) {
+                        if (!m) break;
+                        const int l = __ffsll((unsigned long long)m) - 1;
+                        m &= m - 1;
+                        const uint32_t v = __builtin_amdgcn_readlane(mine, l);
+                        if (lane / G == g) from = v;
+                    }
+                    const int e = lane % G;
+                    const uint32_t tok = from + e / N * (64 * N) + e % N;
+                    // a block ends with the vectors; the logits after them are alone
+                    const bool have = from != 0xffffffffu && (from < v1 * N ? tok < v1 * N : e == 0);
+                    float v = -__builtin_inff();
+                    if (have) v = L::one(x + tok);
+                    f(have && v >= t, v, tok);
+                }
+            }
+        };
+        read_again([&](bool in, float v, uint32_t tok) {
+            if (!in) return;
+            const int at = atomicAdd(&s_count, 1);  // any order: ranks do not depend on it
+            if (at < kMaxKeys) s_key[at] = top_key(v, tok);
+        });
+        __syncthreads();
+        int n = s_count;
+        if (n > kMaxKeys) {  // many equal logits: each wave's 64 best by merging
+            uint64_t list = 0;
+            read_again([&](bool in, float v, uint32_t tok) {
+                list = merge_in(list, in ? top_key(v, tok) : 0, lane);
+            });
+            __syncthreads();
+            s_key[wave * 64 + lane] = list;
+            n = 64 * kLpWaves;
+            __syncthreads();
         }
-        if (lane < noted.count) s_key[k0 + lane] = noted.key_at(lane);
-        if (noted.listed && lane < a.top) s_key[k0 + noted.count + lane] = noted.list;
-        __syncthreads();
         rank_keys(s_key, n, a.top, s_best);
-    } else {
-        __syncthreads();
     }
     if (a.splits > 1) {
         if constexpr (TOP) {
             if ((int)threadIdx.x < a.top) a.list[at * a.top + threadIdx.x] = s_best[threadIdx.x];
         }
         if (wave != 0) return;
-        st = join_lanes(&s_stat[0][0], kLpWaves, 3, c);
+        st = join_lanes(&s_stat[0][0], kLpWaves, 4, high);
         if (lane == 0) {
-            a.part[at * 4] = st.m;
+            a.part[at * 4] = st.r;
             a.part[at * 4 + 1] = st.s;
             a.part[at * 4 + 2] = st.T;
+            a.part[at * 4 + 3] = high;
         }
         return;
     }
     if (wave != 0) return;
-    st = join_lanes(&s_stat[0][0], kLpWaves, 3, c);
-    finish_row(a, row, st, tl, target >= 0, s_best);
+    end_row<L>(a, row, &s_stat[0][0], kLpWaves, x, tl, target >= 0, s_best);
 }
 
-// Joins the splits of a row (64 at most, and kMaxJoin keys).
+// Joins the splits of a row (64 at most, and kMaxKeys keys).
 template <bool BF16, bool TOP>
 __global__ void __launch_bounds__(64 * kLpWaves) logprob_join(LogprobArgs a) {
     using L = Lg<BF16>;
-    __shared__ uint64_t s_key[TOP ? kMaxJoin : 1], s_best[TOP ? kMaxTop : 1];
+    __shared__ uint64_t s_key[TOP ? kMaxKeys : 1], s_best[TOP ? kMaxTop : 1];
     const int64_t row = blockIdx.x;
+    const typename L::E* x = static_cast<const typename L::E*>(a.logits) + row * a.ld;
     const int64_t target = target_of(a, row);
     float tl = 0.f;
-    if (threadIdx.x == 0 && target >= 0)
-        tl = L::one(static_cast<const typename L::E*>(a.logits) + row * a.ld + target);
+    if (threadIdx.x == 0 && target >= 0) tl = L::one(x + target);
     if constexpr (TOP) {
-        const int n = a.splits * a.top;
-        for (int k = threadIdx.x; k < n; k += 64 * kLpWaves) s_key[k] = a.list[row * n + k];
+        // every split has `top` keys not below its last: the best such last
+        // bounds the row's, and few keys reach it
+        __shared__ uint64_t s_bound;
+        __shared__ int s_count;
+        const uint64_t* list = a.list + row * a.splits * a.top;
+        if (threadIdx.x < 64) {
+            uint64_t b = (int)threadIdx.x < a.splits ? list[threadIdx.x * a.top + a.top - 1] : 0;
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1) {
+                const uint64_t o = shfl64(b, threadIdx.x ^ off);
+                b = b > o ? b : o;
+            }
+            if (threadIdx.x == 0) s_bound = b, s_count = 0;
+        }
         __syncthreads();
-        rank_keys(s_key, n, a.top, s_best);
+        for (int k = threadIdx.x; k < a.splits * a.top; k += 64 * kLpWaves) {
+            const uint64_t v = list[k];
+            if (v && v >= s_bound) s_key[atomicAdd(&s_count, 1)] = v;
+        }
+        __syncthreads();
+        rank_keys(s_key, s_count, a.top, s_best);
     }
     if (threadIdx.x >= 64) return;
-    finish_row(a, row, join_lanes(a.part + row * a.splits * 4, a.splits, 4, a.scale * kLog2e), tl,
-               target >= 0, s_best);
+    end_row<L>(a, row, a.part + row * a.splits * 4, a.splits, x, tl, target >= 0, s_best);
 }
 
 // ---- gradient -------------------------------------------------------------------------------
@@ -540,7 +704,7 @@ void logprob_plan(LogprobArgs& a, bool bf16) {
     // about 1024 workgroups, of LP_MIN logits at least
     const int64_t vec = bf16 ? 8 : 4, nvec = a.V / vec;
     int64_t n = a.rows > 0 ? (LP_WG + a.rows - 1) / a.rows : 1;
-    const int64_t most = (a.V + LP_MIN - 1) / LP_MIN, keys = a.top ? kMaxJoin / a.top : 64;
+    const int64_t most = (a.V + LP_MIN - 1) / LP_MIN, keys = a.top ? kMaxKeys / a.top : 64;
     if (n > most) n = most;
     if (n > keys) n = keys;
     if (n > 64) n = 64;
