@@ -35,18 +35,6 @@ namespace {
 
 using namespace dev;
 
-#ifndef LP_U
-#define LP_U 4
-#endif
-#ifndef LP_OCC
-#define LP_OCC 4
-#endif
-#ifndef LP_WG
-#define LP_WG 1024
-#endif
-#ifndef LP_MIN
-#define LP_MIN 4096
-#endif
 constexpr int kLpWaves = 4;
 constexpr int kMaxKeys = 1024;  // keys that a workgroup ranks
 // References stay within +-kFar; a row whose largest logit is past it (all of
@@ -393,10 +381,11 @@ __device__ __forceinline__ void end_row(const LogprobArgs& a, int64_t row, const
 
 // ---- forward ------------------------------------------------------------------------------
 template <bool BF16, bool TOP>
-__global__ void __launch_bounds__(64 * kLpWaves, LP_OCC) logprob_fwd(LogprobArgs a) {
+__global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(LogprobArgs a) {
     using L = Lg<BF16>;
     using E = typename L::E;
-    constexpr int N = L::N, U = LP_U;  // vectors a lane takes of a block
+    constexpr int N = L::N, U = TOP ? 2 : 4;  // vectors a lane takes of a block
+    constexpr int D = 3;                            // blocks in hand or under way
     __shared__ uint64_t s_key[TOP ? kMaxKeys : 1], s_best[TOP ? kMaxTop : 1];
     __shared__ Notes s_notes[TOP ? kLpWaves : 1];
     __shared__ float s_stat[kLpWaves][4], s_thr[kLpWaves];
@@ -467,7 +456,7 @@ __global__ void __launch_bounds__(64 * kLpWaves, LP_OCC) logprob_fwd(LogprobArgs
         }
     };
 
-    typename L::T w0[U], w1[U];
+    typename L::T w[D][U];
     auto load = [&](uint32_t b, typename L::T(&r)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u) r[u] = L::load(x + (int64_t)min(b + u * 64 + lane, v1 - 1) * N);
@@ -495,19 +484,22 @@ __global__ void __launch_bounds__(64 * kLpWaves, LP_OCC) logprob_fwd(LogprobArgs
     };
     constexpr uint32_t kStep = 64 * U * kLpWaves;
     uint32_t b = v0 + wave * (64 * U);
-    if (b < v1) load(b, w0);
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d)
+        if (b + d * kStep < v1) load(b + d * kStep, w[d]);
     // the target's logit travels beside the row
     const int64_t target = target_of(a, row);
     float tl = 0.f;
     if (wave == 0 && target >= 0) tl = L::one(x + target);
-    while (b < v1) {  // two blocks a turn, one under way while the other is taken
-        if (b + kStep < v1) load(b + kStep, w1);
-        block(b, w0);
-        b += kStep;
-        if (b >= v1) break;
-        if (b + kStep < v1) load(b + kStep, w0);
-        block(b, w1);
-        b += kStep;
+    while (b < v1) {  // D blocks a turn, D - 1 under way while one is taken
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const uint32_t ahead = b + (D - 1) * kStep;
+            if (ahead < v1) load(ahead, w[(d + D - 1) % D]);
+            block(b, w[d]);
+            b += kStep;
+            if (b >= v1) break;
+        }
     }
     if (wave == 0 && last && (int64_t)nvec * N < a.V) {  // the row's last V % N logits
         const int64_t i = (int64_t)nvec * N + lane;
@@ -701,10 +693,11 @@ uint32_t grad_chunks(const LogprobArgs& a, bool bf16) {
 }  // namespace
 
 void logprob_plan(LogprobArgs& a, bool bf16) {
-    // about 1024 workgroups, of LP_MIN logits at least
+    // Few rows are split over about 512 workgroups, of 4096 logits at least (64
+    // rows of 131072 at top 20: 20 us, with 1024 27, with 256 21).
     const int64_t vec = bf16 ? 8 : 4, nvec = a.V / vec;
-    int64_t n = a.rows > 0 ? (LP_WG + a.rows - 1) / a.rows : 1;
-    const int64_t most = (a.V + LP_MIN - 1) / LP_MIN, keys = a.top ? kMaxKeys / a.top : 64;
+    int64_t n = a.rows > 0 ? (512 + a.rows - 1) / a.rows : 1;
+    const int64_t most = (a.V + 4095) / 4096, keys = a.top ? kMaxKeys / a.top : 64;
     if (n > most) n = most;
     if (n > keys) n = keys;
     if (n > 64) n = 64;
