@@ -366,7 +366,7 @@ ms_status ms_conv1d_silu(const void* x, const float* weight, const float* bias,
  *   workspace     : ms_gated_scan_workspace_bytes bytes (may be 0), 16-byte
  *                   aligned, no initialisation needed.
  * batch, seqlen, d_inner and io as in ms_dims (MS_ERR_UNSUPPORTED where a
- * launch would need more than 2^31 - 1 workgroups).  The state, the decay and the
+ * launch would need more than 2^24 - 1 workgroups).  The state, the decay and the
  * gates are fp32; y is rounded once.  Deterministic.
  *
  * ms_gated_scan_bwd: gradients for dy and, optionally, dh_last ([batch]
@@ -417,7 +417,7 @@ ms_status ms_gated_step(float* h, const void* x_t, const void* r_t, const void* 
  *              initialisation needed.
  * The gradient sorts the ids, stably, and sums in fp32 in an order that
  * depends on the ids alone: deterministic.  MS_ERR_UNSUPPORTED when a launch
- * would need more than 2^31 - 1 workgroups.
+ * would need more than 2^24 - 1 workgroups.
  */
 ms_status ms_embed_fwd(const void* ids, int32_t id_bits, const void* weight, float scale,
                        void* out, int64_t n, int64_t rows, int32_t dim, int32_t io, void* stream);
@@ -446,8 +446,8 @@ ms_status ms_embed_bwd(const void* ids, int32_t id_bits, const void* dy, float s
  *             the sum beside a large maximum)
  *   top     : 0 .. 64 and <= vocab; top_logprob [rows][top] fp32 and top_id
  *             [rows][top] int32 are required when it is not 0
- *   rows in 0 .. 2^31-1 (0: nothing is done), vocab in 1 .. 2^31-1, scale > 0
- *   and finite.
+ *   rows in 0 .. 2^24-1 (0: nothing is done; MS_ERR_UNSUPPORTED past it), vocab
+ *   in 1 .. 2^31-1, scale > 0 and finite.
  * Masked logits of -inf have probability 0 and add nothing to the entropy.  A
  * row that is all -inf has lse -inf, logprob -inf, entropy 0 and alternatives
  * of log probability -inf.  A NaN or +inf makes the row's results NaN; a NaN

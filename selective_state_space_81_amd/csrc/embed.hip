@@ -578,7 +578,7 @@ template <bool BF16, int VEC>
 hipError_t sum_variant(const EmbedArgs& a, bool gbf16, const uint32_t* key, const uint32_t* pos,
                        hipStream_t s) {
     const int64_t cgroups = (a.D + a.lanes * VEC - 1) / (a.lanes * VEC), per = 256 / a.lanes;
-    const dim3 grid((unsigned)(((a.chunks + a.zeros) * cgroups + per - 1) / per)), blk(256);
+    const dim3 grid((unsigned)embed_sum_workgroups(a, BF16)), blk(256);
     {
         ProfScope ps(s, kPhaseMain);
         if (gbf16) hipLaunchKernelGGL((embed_sum<BF16, VEC, true>), grid, blk, 0, s, a, key, pos);
@@ -601,8 +601,8 @@ int embed_vec(int D, bool bf16) {
 }
 
 int64_t embed_sum_workgroups(const EmbedArgs& a, bool bf16) {
-    const int64_t per = (int64_t)a.lanes * embed_vec(a.D, bf16);
-    return (a.chunks + a.zeros) * ((a.D + per - 1) / per);
+    const int64_t cols = (int64_t)a.lanes * embed_vec(a.D, bf16), per = 256 / a.lanes;
+    return ((a.chunks + a.zeros) * ((a.D + cols - 1) / cols) + per - 1) / per;
 }
 
 int64_t embed_fwd_workgroups(const EmbedArgs& a, bool bf16) {

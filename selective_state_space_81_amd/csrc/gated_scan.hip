@@ -973,21 +973,30 @@ hipError_t launch_gated_bwd(GatedArgs a, bool bf16, void* workspace, hipStream_t
     return hipGetLastError();
 }
 
-template <int VEC, int BR>
-static void step_variant(const GatedArgs& a, bool bf16, hipStream_t s) {
-    const int64_t n = (int64_t)((a.batch + BR - 1) / BR) * (a.Dn / VEC);
-    const dim3 grid((unsigned)((n + 255) / 256)), blk(256);
-    if (bf16) hipLaunchKernelGGL((gated_step<VEC, BR, true>), grid, blk, 0, s, a);
-    else hipLaunchKernelGGL((gated_step<VEC, BR, false>), grid, blk, 0, s, a);
+// Two batch rows a thread where that leaves the chip half full of threads or
+// more (512 x 2560 bf16: 8.3 us, one row 9.1, four 8.6, eight 9.0).
+static int step_rows(const GatedArgs& a) {
+    return a.Dn % 4 == 0 && (int64_t)a.batch * (a.Dn / 4) >= 256 * 1024 ? 2 : 1;
+}
+
+int64_t gated_step_workgroups(const GatedArgs& a) {
+    const int br = step_rows(a), vecs = a.Dn % 4 ? a.Dn : a.Dn / 4;
+    return ((int64_t)((a.batch + br - 1) / br) * vecs + 255) / 256;
 }
 
 hipError_t launch_gated_step(const GatedArgs& a, bool bf16, hipStream_t s) {
     ProfScope ps(s, kPhaseStep);
-    // Two batch rows a thread where that leaves the chip half full of threads
-    // or more (512 x 2560 bf16: 8.3 us, one row 9.1, four 8.6, eight 9.0).
-    if (a.Dn % 4) step_variant<1, 1>(a, bf16, s);
-    else if ((int64_t)a.batch * (a.Dn / 4) >= 256 * 1024) step_variant<4, 2>(a, bf16, s);
-    else step_variant<4, 1>(a, bf16, s);
+    const dim3 grid((unsigned)gated_step_workgroups(a)), blk(256);
+    if (a.Dn % 4) {
+        if (bf16) hipLaunchKernelGGL((gated_step<1, 1, true>), grid, blk, 0, s, a);
+        else hipLaunchKernelGGL((gated_step<1, 1, false>), grid, blk, 0, s, a);
+    } else if (step_rows(a) == 2) {
+        if (bf16) hipLaunchKernelGGL((gated_step<4, 2, true>), grid, blk, 0, s, a);
+        else hipLaunchKernelGGL((gated_step<4, 2, false>), grid, blk, 0, s, a);
+    } else {
+        if (bf16) hipLaunchKernelGGL((gated_step<4, 1, true>), grid, blk, 0, s, a);
+        else hipLaunchKernelGGL((gated_step<4, 1, false>), grid, blk, 0, s, a);
+    }
     return hipGetLastError();
 }
 

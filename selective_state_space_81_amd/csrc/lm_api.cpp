@@ -58,19 +58,24 @@ ms_status launched(hipError_t e) {
 
 // ---- gated linear recurrence ---------------------------------------------------
 
-ms_status check_gated(int32_t batch, int64_t seqlen, int32_t d_inner, int32_t io) {
+ms_status check_gated_sizes(int32_t batch, int64_t seqlen, int32_t d_inner, int32_t io) {
     if (batch < 1) return fail(MS_ERR_SHAPE, "batch=%d must be >= 1", batch);
     if (seqlen < 1 || seqlen > kMax31)
         return fail(MS_ERR_SHAPE, "seqlen=%lld must be in [1, 2^31-1]", (long long)seqlen);
     if (d_inner < 1) return fail(MS_ERR_SHAPE, "d_inner=%d must be >= 1", d_inner);
     if ((double)batch * (double)seqlen * (double)d_inner > 0x1p56)
         return fail(MS_ERR_SHAPE, "batch x seqlen x d_inner exceeds 2^56");
+    return check_io(io);
+}
+
+ms_status check_gated(int32_t batch, int64_t seqlen, int32_t d_inner, int32_t io) {
+    ms_status st = check_gated_sizes(batch, seqlen, d_inner, io);
+    if (st != MS_OK) return st;
     if ((d_inner + 63) / 64 > 65535 || batch > 65535)
         return fail(MS_ERR_UNSUPPORTED, "d_inner/64 and batch must be <= 65535");
-    ms_status st = check_io(io);
-    if (st == MS_OK && gated_workgroups(batch, seqlen, d_inner, io == MS_BF16) > kMax31)
-        return fail(MS_ERR_UNSUPPORTED, "batch x seqlen x d_inner needs more than 2^31-1 workgroups");
-    return st;
+    if (gated_workgroups(batch, seqlen, d_inner, io == MS_BF16) > kMaxGroups)
+        return fail(MS_ERR_UNSUPPORTED, "batch x seqlen x d_inner needs more than 2^24-1 workgroups");
+    return MS_OK;
 }
 
 ms_status check_sharpness(float c) {
@@ -99,6 +104,8 @@ ms_status check_logprobs(int64_t rows, int64_t vocab, int32_t top, int32_t io) {
         return fail(MS_ERR_SHAPE, "rows=%lld must be in [0, 2^31-1]", (long long)rows);
     if (vocab < 1 || vocab > kMax31)
         return fail(MS_ERR_SHAPE, "vocab=%lld must be in [1, 2^31-1]", (long long)vocab);
+    if (rows > kMaxGroups)
+        return fail(MS_ERR_UNSUPPORTED, "rows=%lld must be below 2^24", (long long)rows);
     if (top < 0 || top > kMaxTop || top > vocab)
         return fail(MS_ERR_SHAPE, "top=%d must be in [0, %d] and at most vocab", top, kMaxTop);
     return check_io(io);
@@ -187,17 +194,17 @@ ms_status ms_gated_step(float* h, const void* x_t, const void* r_t, const void* 
                         const float* lam, float sharpness, const void* z_t, void* y_t,
                         int32_t batch, int32_t d_inner, int32_t io, void* stream) {
     clear_error();
-    ms_status st = check_gated(batch, 1, d_inner, io);
+    ms_status st = check_gated_sizes(batch, 1, d_inner, io);
     if (st != MS_OK) return st;
     if ((st = check_sharpness(sharpness)) != MS_OK) return st;
     if (!h || !x_t || !r_t || !i_t || !lam || !y_t)
         return fail(MS_ERR_NULL, "h, x_t, r_t, i_t, lam and y_t are required");
     if ((st = check_aligned({h, x_t, r_t, i_t, lam, z_t, y_t})) != MS_OK) return st;
-    if ((int64_t)batch * d_inner > kMax31 * 256)
-        return fail(MS_ERR_UNSUPPORTED, "batch x d_inner must be < 2^39");
     GatedArgs a{};
     a.x = x_t; a.r = r_t; a.i = i_t; a.z = z_t; a.lam = lam; a.h_last = h; a.y = y_t;
     a.sharp = sharpness; a.L = 1; a.batch = batch; a.Dn = d_inner;
+    if (gated_step_workgroups(a) > kMaxGroups)
+        return fail(MS_ERR_UNSUPPORTED, "batch x d_inner needs more than 2^24-1 workgroups");
     prof_call();
     return launched(launch_gated_step(a, io == MS_BF16, static_cast<hipStream_t>(stream)));
 }
@@ -216,8 +223,8 @@ ms_status ms_embed_fwd(const void* ids, int32_t id_bits, const void* weight, flo
     EmbedArgs a{};
     a.ids = ids; a.wide = id_bits == 64; a.weight = weight; a.scale = scale; a.out = out; a.n = n;
     a.rows = rows; a.D = dim;
-    if (embed_fwd_workgroups(a, io == MS_BF16) > kMax31)
-        return fail(MS_ERR_UNSUPPORTED, "n x dim needs more than 2^31-1 workgroups");
+    if (embed_fwd_workgroups(a, io == MS_BF16) > kMaxGroups)
+        return fail(MS_ERR_UNSUPPORTED, "n x dim needs more than 2^24-1 workgroups");
     prof_call();
     return launched(launch_embed_fwd(a, io == MS_BF16, static_cast<hipStream_t>(stream)));
 }
@@ -248,8 +255,8 @@ ms_status ms_embed_bwd(const void* ids, int32_t id_bits, const void* dy, float s
     a.dweight = dweight; a.n = n; a.rows = rows; a.D = dim;
     embed_plan(a, io == MS_BF16);
     if ((st = check_workspace(embed_ws(a).total, workspace, workspace_bytes)) != MS_OK) return st;
-    if (embed_sum_workgroups(a, io == MS_BF16) > kMax31)
-        return fail(MS_ERR_UNSUPPORTED, "n, rows and dim need more than 2^31-1 workgroups");
+    if (embed_sum_workgroups(a, io == MS_BF16) > kMaxGroups)
+        return fail(MS_ERR_UNSUPPORTED, "n, rows and dim need more than 2^24-1 workgroups");
     prof_call();
     return launched(launch_embed_bwd(a, io == MS_BF16, grad_dtype == MS_BF16, workspace,
                                      static_cast<hipStream_t>(stream)));
@@ -319,8 +326,8 @@ ms_status ms_token_logprobs_bwd(const void* logits, int64_t ld, const void* targ
     a.entropy = const_cast<float*>(entropy);  // only read
     a.dlogprob = dlogprob; a.dentropy = dentropy; a.dlogits = dlogits; a.scale = scale;
     a.rows = rows; a.V = vocab; a.ld = ld; a.ldd = ldd;
-    if (logprob_bwd_workgroups(a, io == MS_BF16) > kMax31)
-        return fail(MS_ERR_UNSUPPORTED, "rows x vocab needs more than 2^31-1 workgroups");
+    if (logprob_bwd_workgroups(a, io == MS_BF16) > kMaxGroups)
+        return fail(MS_ERR_UNSUPPORTED, "rows x vocab needs more than 2^24-1 workgroups");
     prof_call();
     return launched(launch_logprob_bwd(a, io == MS_BF16, static_cast<hipStream_t>(stream)));
 }

@@ -9,6 +9,10 @@
 
 namespace msscan {
 
+// Workgroups of 256 threads that one launch may have: a grid's threads are
+// counted in 32 bits.
+constexpr int64_t kMaxGroups = (1 << 24) - 1;
+
 // ---- gated linear recurrence (gated_scan.hip) --------------------------------
 // Saved states: h before every kGatedBlock-th step, [batch][ceil(L/kGatedBlock)][Dn].
 constexpr int kGatedBlock = 16;
@@ -52,6 +56,7 @@ size_t gated_fwd_ws(int batch, int64_t L, int Dn, bool bf16);  // bytes
 size_t gated_bwd_ws(int batch, int64_t L, int Dn, bool bf16);
 hipError_t launch_gated_fwd(GatedArgs a, bool bf16, void* workspace, hipStream_t s);
 hipError_t launch_gated_bwd(GatedArgs a, bool bf16, void* workspace, hipStream_t s);
+int64_t gated_step_workgroups(const GatedArgs& a);
 // One step: a.h_last is the state [batch][Dn], updated in place; L is 1.
 hipError_t launch_gated_step(const GatedArgs& a, bool bf16, hipStream_t s);
 

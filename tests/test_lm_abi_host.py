@@ -101,6 +101,23 @@ def test_logprob_refusals():
     assert bwd(ldd=39) == 2 and bwd(ldd=48) == 2  # over the logits with another stride
 
 
+def test_launches_too_large():
+    """A launch holds fewer than 2^24 workgroups of 256 threads."""
+    lib = ms.load()
+    # 65535 x 65539 channels, one by one
+    assert lib.ms_gated_step(P, P, P, P, P, 8.0, None, P, 65535, 65539, 1, None) == 7
+    assert lib.ms_gated_scan_workspace_bytes(65535, 1, 64 * 300, 1) == NONE
+    assert b"2^24-1" in lib.ms_last_error()
+    assert lib.ms_gated_scan_workspace_bytes(65535, 1, 64 * 200, 1) != NONE
+    assert lib.ms_embed_fwd(P, 64, P, 1.0, P, (1 << 31) - 1, 10, 1 << 12, 0, None) == 7
+    assert lib.ms_embed_bwd(P, 64, P, 1.0, -1, P, 0, 5, (1 << 31) - 1, 1 << 12, 0, P, 1 << 50,
+                            None) == 7
+    assert lib.ms_token_logprobs_fwd(P, 5, P, 64, 1.0, P, P, P, P, 0, None, None, 1 << 24, 5, 0,
+                                     None, 0, None) == 7
+    assert lib.ms_token_logprobs_bwd(P, 1 << 20, P, 64, 1.0, P, P, P, P, P, 1 << 20,
+                                     (1 << 24) - 1, 1 << 20, 0, None) == 7
+
+
 def test_binding_refuses_host_tensors():
     x = torch.zeros(2, 4, 8)
     with pytest.raises(ValueError, match="device"):
