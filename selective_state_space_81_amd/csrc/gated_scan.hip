@@ -53,8 +53,9 @@ struct RowIo<4, true> {
         v[3] = __uint_as_float(w[1] & 0xffff0000u);
     }
     static __device__ __forceinline__ T pack(const float (&v)[4]) {
-        auto bits = [](float f) { return (uint32_t)f32_to_bf16_rne(f); };
-        return T{bits(v[0]) | (bits(v[1]) << 16), bits(v[2]) | (bits(v[3]) << 16)};
+        typedef float F __attribute__((ext_vector_type(4)));
+        typedef __bf16 B __attribute__((ext_vector_type(4)));
+        return __builtin_bit_cast(T, __builtin_convertvector((F{v[0], v[1], v[2], v[3]}), B));
     }
 };
 template <>
@@ -231,69 +232,65 @@ __device__ __forceinline__ int slot_channel(const GatedArgs& a, uint32_t chain, 
 // after it once it knows the one before; a block looks back over up to
 // kWindow others for the nearest published state and applies the (P, H)
 // between in order, so the result is that of a serial chain whatever the
-// timing.  Work is handed out by a counter, earlier blocks first: a block
-// that is waited for has been started, and waits for earlier ones only, so
-// every wait ends.  A word of all ones is not yet published (the preparing
-// kernel writes it; published NaNs have another pattern).  The words are
+// timing.  As many workgroups as a chain has blocks come for its blocks, and a
+// counter hands them out, earlier blocks first: a block that is waited for has
+// been started, and waits for earlier ones only, so every wait ends.  (A
+// counter for each chain: one for all hands out a block each 12 ns, and the
+// kernel waited for it.  Chains move over the XCDs from block to block: where
+// each stayed on one, their times drifted apart and rows were read in pieces.
+// Layer 66 -> 60 us, long 363 -> 345, training's backward 118 -> 111.)  A word of all ones is not yet published (the preparing
+// kernel writes it; published NaNs have other patterns, also than kState).  The words are
 // single relaxed atomics at device scope: each carries its whole message, so
 // no fence orders anything else.
-constexpr uint32_t kNotYet = 0xffffffffu;
-constexpr int kWindow = 4;
+constexpr uint32_t kNotYet = 0xffffffffu, kState = 0xfffffffeu;
+// One sequence of 131072 steps at 64 channels is bound by this chain of
+// messages: 173 us with a window of 4, 117 with 8; 16 spill in the backward.
+constexpr int kWindow = 8;
+constexpr int kTicketStride = 16;  // words: a counter has 64 bytes to itself
 
 __device__ __forceinline__ float plain_nan(float v) { return v == v ? v : __builtin_nanf(""); }
 
-template <class T>
-__device__ __forceinline__ T peek(const T* p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
-// State words of one chain: [block][CH], in the order blocks are taken.
-template <int stride>
+// Messages of one chain, one a channel: [block][CH], in the order blocks are taken.
+template <int CH>
 struct Chain {
-    uint64_t* map;    // (P, H) of a block
-    uint32_t* state;  // the state after a block
-    int ch;           // this lane's channel
+    uint64_t* word;  // this lane's channel of the chain's first block
 
+    __device__ __forceinline__ void publish(int64_t blk, uint32_t low, float high) const {
+        const uint64_t w = ((uint64_t)__float_as_uint(plain_nan(high)) << 32) | low;
+        __hip_atomic_store(word + blk * CH, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
     __device__ __forceinline__ void publish_map(int64_t blk, float P, float H) const {
-        const uint64_t w = ((uint64_t)__float_as_uint(plain_nan(H)) << 32) |
-                           __float_as_uint(plain_nan(P));
-        __hip_atomic_store(map + blk * stride + ch, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        publish(blk, __float_as_uint(plain_nan(P)), H);
     }
     __device__ __forceinline__ void publish_state(int64_t blk, float h) const {
-        __hip_atomic_store(state + blk * stride + ch, __float_as_uint(plain_nan(h)),
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        publish(blk, kState, h);
     }
     // The state before block blk >= 1.  The first block publishes a state and
     // never a map, so what the window holds before it (another chain's words,
     // or the room left in front of the first) is never taken.
     template <bool RESET>
     __device__ __forceinline__ float before(int64_t blk) const {
-        const uint32_t* ps = state + (blk - 1) * stride + ch;
-        const uint64_t* pm = map + (blk - 1) * stride + ch;
+        const uint64_t* p = word + (blk - 1) * CH;
         for (;;) {
-            uint32_t st[kWindow];
-            uint64_t mp[kWindow];
+            uint64_t w[kWindow];
 #pragma unroll
-            for (int k = 0; k < kWindow; ++k) {
-                st[k] = peek(ps - k * stride);
-                mp[k] = peek(pm - k * stride);
-            }
-            // nearest state; every map nearer than it has to be there
+            for (int k = 0; k < kWindow; ++k)
+                w[k] = __hip_atomic_load(p - k * CH, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            // nearest state; every message nearer than it has to be there
             int at = -1;
             bool whole = true;
 #pragma unroll
             for (int k = 0; k < kWindow; ++k) {
-                if (at < 0 && whole && st[k] != kNotYet) at = k;
-                whole = whole && (uint32_t)mp[k] != kNotYet;
+                if (at < 0 && whole && (uint32_t)w[k] == kState) at = k;
+                whole = whole && (uint32_t)w[k] != kNotYet;
             }
             if (at >= 0) {
                 float h = 0.f;
 #pragma unroll
                 for (int k = kWindow - 1; k >= 0; --k) {
-                    if (k == at) h = __uint_as_float(st[k]);
-                    if (k < at)
-                        h = apply<RESET>(__uint_as_float((uint32_t)mp[k]), h,
-                                         __uint_as_float((uint32_t)(mp[k] >> 32)));
+                    const float high = __uint_as_float((uint32_t)(w[k] >> 32));
+                    if (k == at) h = high;
+                    if (k < at) h = apply<RESET>(__uint_as_float((uint32_t)w[k]), h, high);
                 }
                 return h;
             }
@@ -304,18 +301,14 @@ struct Chain {
 
 template <class G>
 __device__ __forceinline__ Chain<G::CH> chain_of(const GatedArgs& a, uint32_t chain) {
-    const int64_t at = (int64_t)chain * a.blocks * G::CH;
-    return Chain<G::CH>{a.map + at, a.state + at, (int)threadIdx.x};
+    return Chain<G::CH>{a.word + (int64_t)chain * a.blocks * G::CH + threadIdx.x};
 }
 
 // Nothing published, no work handed out.
 __global__ void __launch_bounds__(256) gated_prepare(GatedArgs a, int64_t words) {
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x, n = (int64_t)gridDim.x * 256;
-    for (int64_t k = t; k < words; k += n) {
-        a.state[k] = kNotYet;
-        a.map[k] = ~(uint64_t)0;
-    }
-    if (t == 0) *a.ticket = 0;
+    for (int64_t k = t; k < words; k += n) a.word[k] = ~(uint64_t)0;
+    for (int64_t k = t; k < a.chains; k += n) a.ticket[k * kTicketStride] = 0;
 }
 
 __global__ void __launch_bounds__(256) gated_copy(const float* from, float* to, int64_t n) {
@@ -323,7 +316,7 @@ __global__ void __launch_bounds__(256) gated_copy(const float* from, float* to, 
         to[k] = from[k];
 }
 
-// This workgroup's chain and its turn in it: earlier turns of all chains first.
+// This workgroup's chain, and its turn in it.
 struct Work {
     uint32_t chain;
     int64_t turn;
@@ -331,10 +324,10 @@ struct Work {
 __device__ __forceinline__ Work take_work(const GatedArgs& a) {
     if (a.blocks == 1) return Work{blockIdx.x, 0};
     __shared__ uint32_t s_ticket;
-    if (threadIdx.x == 0) s_ticket = atomicAdd(a.ticket, 1u);
+    const uint32_t round = blockIdx.x / a.chains, chain = (blockIdx.x + round) % a.chains;
+    if (threadIdx.x == 0) s_ticket = atomicAdd(a.ticket + (size_t)chain * kTicketStride, 1u);
     __syncthreads();
-    const uint32_t t = __builtin_amdgcn_readfirstlane(s_ticket), turn = t / a.chains;
-    return Work{t - turn * a.chains, turn};
+    return Work{chain, __builtin_amdgcn_readfirstlane(s_ticket)};
 }
 
 // -c log2 e softplus(lam) of the workgroup's channels, one a thread, for all
@@ -776,7 +769,7 @@ __global__ void __launch_bounds__(64 * kLamWaves) gated_dlam(GatedArgs a, int64_
 // A thread takes VEC channels of BR batch rows, so that the rate's logarithm
 // is taken once for all of them and their loads travel together.  Bound by its
 // bytes, h read and written and one row of each input, and below some ten
-// megabytes by the launch: 512 x 2560 bf16 moves 23.6 MB in 8.3 us (2.8 TB/s),
+// megabytes by the launch: 256 x 5120 bf16 moves 23.6 MB in 8.3 us (2.8 TB/s),
 // of which about 3 us are a launch that does nothing.
 template <int VEC, int BR, bool BF16>
 __global__ void __launch_bounds__(256) gated_step(GatedArgs a) {
@@ -862,18 +855,17 @@ Cut bwd_cut(int batch, int64_t L, int Dn, bool bf16) {
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Words between blocks: [ticket][state][map]; nothing for one block.
+// Words between blocks: [tickets][room in front][words]; nothing for one block.
 struct Ws {
-    size_t state, map, words, total;
+    size_t word, words, total;
 };
 Ws ws_of(const Cut& c) {
     Ws w{};
     if (c.blocks < 2) return w;
     w.words = (size_t)c.chains * (size_t)c.blocks * c.ch;
     const size_t front = (size_t)kWindow * c.ch;  // read, never taken (Chain::before)
-    w.state = 256 + up256(front * 4);
-    w.map = w.state + up256(w.words * 4) + up256(front * 8);
-    w.total = w.map + up256(w.words * 8);
+    w.word = up256((size_t)c.chains * kTicketStride * 4) + up256(front * 8);
+    w.total = w.word + up256(w.words * 8);
     return w;
 }
 
@@ -884,8 +876,7 @@ hipError_t prepare(GatedArgs& a, const Cut& c, void* workspace, hipStream_t s) {
     const Ws w = ws_of(c);
     char* ws = static_cast<char*>(workspace);
     a.ticket = reinterpret_cast<uint32_t*>(ws);
-    a.state = reinterpret_cast<uint32_t*>(ws + w.state);
-    a.map = reinterpret_cast<uint64_t*>(ws + w.map);
+    a.word = reinterpret_cast<uint64_t*>(ws + w.word);
     ProfScope ps(s, kPhasePrep);
     const size_t n = (w.words + 255) / 256;
     hipLaunchKernelGGL(gated_prepare, dim3((unsigned)(n < 2048 ? n : 2048)), dim3(256), 0, s, a,
@@ -974,7 +965,7 @@ hipError_t launch_gated_bwd(GatedArgs a, bool bf16, void* workspace, hipStream_t
 }
 
 // Two batch rows a thread where that leaves the chip half full of threads or
-// more (512 x 2560 bf16: 8.3 us, one row 9.1, four 8.6, eight 9.0).
+// more (256 x 5120 bf16: 8.3 us, one row 9.1, four 8.6, eight 9.0).
 static int step_rows(const GatedArgs& a) {
     return a.Dn % 4 == 0 && (int64_t)a.batch * (a.Dn / 4) >= 256 * 1024 ? 2 : 1;
 }

@@ -39,9 +39,8 @@ struct GatedArgs {
     float* dh0;   // or null
     float* part;  // workspace: partial sums of dlam, [batch][blocks][Dn]
     // workspace of blocks on workgroups of their own
-    uint32_t* ticket;  // work handed out
-    uint32_t* state;   // [chains][blocks][channels of a chain]: state after a block
-    uint64_t* map;     // the same: what a block does to a state
+    uint32_t* ticket;  // [chains], spaced: blocks of each handed out
+    uint64_t* word;    // [chains][blocks][channels of a chain]: messages of the blocks
     int64_t blocks;    // blocks of a chain
     uint32_t chains;   // channel tiles of all batch rows
     float sharp;
