@@ -20,6 +20,9 @@ LIB = os.path.join(HERE, "libmsscan.so")
 # hardware rate probes used by bench.py (not part of libmsscan's C ABI)
 PROBE_SRC = os.path.join(CSRC, "probe.hip")
 PROBE_LIB = os.path.join(HERE, "libmsprobe.so")
+# the binding's extension module (host code only)
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_LIB = os.path.join(HERE, "_marshal.so")
 SOURCES = [os.path.join(CSRC, "scan_kernels.hip"), os.path.join(CSRC, "scan_tile.hip"),
            os.path.join(CSRC, "scan_lane.hip"), os.path.join(CSRC, "scan_row.hip"),
            os.path.join(CSRC, "scan_row_wide.hip"), os.path.join(CSRC, "scan_row_dtproj.hip"),
@@ -85,7 +88,30 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     build_probe(verbose)
+    build_binding(verbose)
     return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Compile _marshal.so, the binding's extension module, against the
+    installed torch."""
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    tmp = BINDING_LIB + ".tmp"
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in cpp_extension.include_paths() + [sysconfig.get_path("include")]:
+        cmd += ["-isystem", d]
+    cmd += [BINDING_SRC, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_LIB)
+    return BINDING_LIB
 
 
 def build_probe(verbose: bool = False) -> str:

@@ -1,7 +1,7 @@
 """The operators of a recurrent language model beside the scan: the gated
 linear recurrence, the embedding with its gradient and the token log
-probabilities.  Argument marshalling only, as in the package's ``__init__``:
-the work is done by the HIP kernels behind ``include/msscan.h``.
+probabilities.  Argument marshalling only, as in the package's ``__init__``
+(its quick half in C++, csrc/binding.cpp): the work is done by the HIP kernels behind ``include/msscan.h``.
 
 Raw calls (``*_fwd``, ``*_bwd``, ``gated_step``) take and return device
 tensors; ``gated_scan``, ``embed`` and ``token_logprobs`` are the same as
@@ -52,50 +52,65 @@ def declare(lib) -> None:
         fn.restype, fn.argtypes = res, args
 
 
+@functools.lru_cache(maxsize=None)
+def _marshal():
+    """The extension module that checks, allocates and calls (csrc/binding.cpp),
+    bound to the loaded library."""
+    lib = ms.load()
+    try:
+        from selective_state_space_81_amd import _marshal as m
+    except ImportError as e:
+        raise ImportError("_marshal.so cannot be loaded; build it with "
+                          "`python -m selective_state_space_81_amd.build`") from e
+    for name in ("gated_scan_fwd", "gated_scan_bwd", "gated_step", "embed_fwd", "embed_bwd",
+                 "token_logprobs_fwd", "token_logprobs_bwd"):
+        m.bind(name, ctypes.cast(getattr(lib, "ms_" + name), ctypes.c_void_p).value)
+    return m
+
+
 class _Call:
     """One call's device and stream.  Allocations made for it are recorded on
     its stream when that is not the current one (their memory could otherwise
     be handed out again while the call still uses it)."""
 
-    __slots__ = ("torch", "device", "stream", "other")
+    __slots__ = ("torch", "m", "like", "index", "stream", "other")
 
-    def __init__(self, like, stream):
+    def __init__(self, m, like, stream):
         import torch
-        self.torch, self.device, self.other = torch, like.device, None
+        self.torch, self.m, self.like, self.other = torch, m, like, None
+        self.index = like.get_device()
         # the current stream's handle, without building a Stream around it
-        self.stream = torch._C._cuda_getCurrentRawStream(self.device.index)
+        self.stream = torch._C._cuda_getCurrentRawStream(self.index)
         if stream is not None:
             given = stream if isinstance(stream, int) else stream.cuda_stream
             if given != self.stream:
                 self.stream = given
-                self.other = torch.cuda.ExternalStream(given, device=self.device) \
+                self.other = torch.cuda.ExternalStream(given, device=like.device) \
                     if isinstance(stream, int) else stream
 
-    def empty(self, shape, dtype):
-        # (empty_strided costs a third less than empty: 1.2 of 1.7 us)
-        strides, n = [], 1
-        for k in reversed(shape):
-            strides.append(n)
-            n *= k or 1
-        strides.reverse()
-        t = self.torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
+    def empty(self, dtype, *shape):
+        t = self.m.empty(self.like, dtype, *shape)
         if self.other is not None:
             t.record_stream(self.other)
         return t
 
+    def together(self, *dtypes_and_sizes):
+        ts = self.m.together(self.like, *dtypes_and_sizes)
+        if self.other is not None:
+            ts[0].record_stream(self.other)  # the one allocation of all
+        return ts
+
     def workspace(self, given, need):
-        """(pointer, bytes, tensor) of the given workspace, or of a new one."""
-        if given is None and need:
-            given = self.empty((need,), self.torch.uint8)
+        """(tensor, bytes) of the given workspace, or of a new one."""
         if given is None:
-            return None, 0, None
-        if given.device != self.device or not given.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
-        return given.data_ptr(), given.numel() * given.element_size(), given
+            return (self.empty(self.torch.uint8, need), need) if need else (None, 0)
+        if given.device != self.like.device or not given.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {self.like.device}")
+        return given, given.numel() * given.element_size()
 
     def run(self, fn, *args):
-        if self.torch._C._cuda_getDevice() != self.device.index:
-            with self.torch.cuda.device(self.device):
+        if self.torch._C._cuda_getDevice() != self.index:
+            with self.torch.cuda.device(self.index):
                 rc = fn(*args, self.stream)
         else:
             rc = fn(*args, self.stream)
@@ -103,14 +118,25 @@ class _Call:
             ms._check(rc)
 
 
-def _chk(t, name, dtype, shape, device) -> None:
-    """The package's check of a tensor argument, and its device.  Written to
-    cost little when all is well: a step of a few microseconds makes a dozen."""
-    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and
-                     t.is_contiguous()):
-        return
-    ms._chk(t, name, dtype, shape)
-    raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _refuse(device, dtype, shape, **given):
+    """What is wrong with an argument that the extension's check refused: the
+    package's check of each, and its device."""
+    for name, t in given.items():
+        if t is not None:
+            ms._chk(t, name, dtype, tuple(shape))
+            if t.device != device:
+                raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _io_of(m, x, name, dims, text):
+    """The io code of a contiguous device tensor of so many dimensions."""
+    io = m.io(x, dims)
+    if io < 0:
+        if not getattr(x, "is_cuda", False) or x.dim() != dims:
+            raise ValueError(f"{name} must be a {text} device tensor")
+        io = ms._io(x)
+        ms._chk(x, name, x.dtype, tuple(x.shape))
+    return io
 
 
 def _size(n: int, what: str) -> int:
@@ -121,22 +147,24 @@ def _size(n: int, what: str) -> int:
 
 # ---- gated linear recurrence -------------------------------------------------------------
 
-def _chk_gated(x, r, i, lam, z, reset):
-    """Checks of the arguments both passes share; (shape, device, io, reset)."""
+def _chk_gated(m, x, r, i, lam, z, reset):
+    """Checks of the arguments both passes share; (shape, io, reset)."""
     import torch
-    if not getattr(x, "is_cuda", False) or x.dim() != 3:
-        raise ValueError("x must be a [batch, L, d_inner] device tensor")
-    io, shape, dev, dt = ms._io(x), x.shape, x.device, x.dtype
-    _chk(x, "x", dt, shape, dev)
-    _chk(r, "r", dt, shape, dev)
-    _chk(i, "i", dt, shape, dev)
-    _chk(lam, "lam", torch.float32, shape[2:], dev)
-    _chk(z, "z", dt, shape, dev)
+    io = _io_of(m, x, "x", 3, "[batch, L, d_inner]")
+    shape = x.shape
+    for t, name in ((r, "r"), (i, "i"), (lam, "lam")):
+        if t is None:
+            raise ValueError(f"{name} is required")
+    if not m.like(x, r, i, z):
+        _refuse(x.device, x.dtype, shape, r=r, i=i, z=z)
+    if not m.fits(x, torch.float32, (shape[2],), lam):
+        _refuse(x.device, torch.float32, shape[2:], lam=lam)
     if reset is not None:
         if reset.dtype == torch.bool:
             reset = reset.view(torch.uint8)
-        _chk(reset, "reset", torch.uint8, shape[:2], dev)
-    return shape, dev, io, reset
+        if not m.fits(x, torch.uint8, (shape[0], shape[1]), reset):
+            _refuse(x.device, torch.uint8, shape[:2], reset=reset)
+    return shape, io, reset
 
 
 @functools.lru_cache(maxsize=1024)
@@ -157,8 +185,10 @@ def gated_scan_states(x, stream=None):
     """An empty buffer for the states that gated_scan_fwd saves for
     gated_scan_bwd: [batch, ceil(L / 16), d_inner] fp32."""
     import torch
+    m = _marshal()
+    _io_of(m, x, "x", 3, "[batch, L, d_inner]")
     b, L, d = x.shape
-    return _Call(x, stream).empty((b, -(-L // GATED_BLOCK), d), torch.float32)
+    return _Call(m, x, stream).empty(torch.float32, b, -(-L // GATED_BLOCK), d)
 
 
 def gated_scan_fwd(x, r, i, lam, z=None, *, c=8.0, reset=None, y=None, h0=None, h_last=None,
@@ -170,20 +200,21 @@ def gated_scan_fwd(x, r, i, lam, z=None, *, c=8.0, reset=None, y=None, h0=None, 
     what the backward needs.  Allocates y (and the workspace) when not given.
     Returns y."""
     import torch
-    shape, dev, io, reset = _chk_gated(x, r, i, lam, z, reset)
+    m = _marshal()
+    shape, io, reset = _chk_gated(m, x, r, i, lam, z, reset)
     b, L, d = shape
     f32 = torch.float32
-    _chk(h0, "h0", f32, (b, d), dev)
-    _chk(h_last, "h_last", f32, (b, d), dev)
-    _chk(y, "y", x.dtype, shape, dev)
-    _chk(states, "states", f32, (b, -(-L // GATED_BLOCK), d), dev)
-    call = _Call(x, stream)
+    if not m.fits(x, f32, (b, d), h0, h_last):
+        _refuse(x.device, f32, (b, d), h0=h0, h_last=h_last)
+    if not m.fits(x, f32, (b, -(-L // GATED_BLOCK), d), states):
+        _refuse(x.device, f32, (b, -(-L // GATED_BLOCK), d), states=states)
+    if not m.like(x, y):
+        _refuse(x.device, x.dtype, shape, y=y)
+    call = _Call(m, x, stream)
     if y is None:
-        y = call.empty(shape, x.dtype)
-    wp, wn, keep = call.workspace(workspace, gated_scan_workspace_bytes(b, L, d, io))
-    p = ms._ptr
-    call.run(ms.load().ms_gated_scan_fwd, p(x), p(r), p(i), p(lam), c, p(z), p(reset), p(y), p(h0),
-             p(h_last), p(states), b, L, d, io, wp, wn)
+        y = call.empty(x.dtype, b, L, d)
+    ws, wn = call.workspace(workspace, gated_scan_workspace_bytes(b, L, d, io))
+    call.run(m.gated_scan_fwd, x, r, i, lam, c, z, reset, y, h0, h_last, states, b, L, d, io, ws, wn)
     return y
 
 
@@ -193,26 +224,28 @@ def gated_scan_bwd(x, r, i, lam, dy, states, z=None, *, c=8.0, reset=None, dh_la
     for dy (and optionally dh_last), with the states it saved.  Returns a dict:
     dx, dr, di, dz (io dtype; dz None without z), dlam and dh0 (fp32)."""
     import torch
-    shape, dev, io, reset = _chk_gated(x, r, i, lam, z, reset)
+    m = _marshal()
+    shape, io, reset = _chk_gated(m, x, r, i, lam, z, reset)
     b, L, d = shape
-    f32 = torch.float32
+    f32, dt = torch.float32, x.dtype
     if states is None:
         raise ValueError("states is required (gated_scan_fwd fills it)")
     if dy is None:
         raise ValueError("dy is required")
-    _chk(states, "states", f32, (b, -(-L // GATED_BLOCK), d), dev)
-    _chk(dy, "dy", x.dtype, shape, dev)
-    _chk(dh_last, "dh_last", f32, (b, d), dev)
-    call = _Call(x, stream)
-    out = {k: call.empty(shape, x.dtype) for k in ("dx", "dr", "di")}
-    out["dz"] = call.empty(shape, x.dtype) if z is not None else None
-    out["dlam"] = call.empty((d,), f32)
-    out["dh0"] = call.empty((b, d), f32) if want_dh0 else None
-    wp, wn, keep = call.workspace(workspace, gated_scan_bwd_workspace_bytes(b, L, d, io))
-    p = ms._ptr
-    call.run(ms.load().ms_gated_scan_bwd, p(x), p(r), p(i), p(lam), c, p(z), p(reset), p(states), p(dy),
-             p(dh_last), p(out["dx"]), p(out["dr"]), p(out["di"]), p(out["dz"]), p(out["dlam"]),
-             p(out["dh0"]), b, L, d, io, wp, wn)
+    if not m.fits(x, f32, (b, -(-L // GATED_BLOCK), d), states):
+        _refuse(x.device, f32, (b, -(-L // GATED_BLOCK), d), states=states)
+    if not m.like(x, dy):
+        _refuse(x.device, dt, shape, dy=dy)
+    if not m.fits(x, f32, (b, d), dh_last):
+        _refuse(x.device, f32, (b, d), dh_last=dh_last)
+    call = _Call(m, x, stream)
+    out = {k: call.empty(dt, b, L, d) for k in ("dx", "dr", "di")}
+    out["dz"] = call.empty(dt, b, L, d) if z is not None else None
+    out["dlam"] = call.empty(f32, d)
+    out["dh0"] = call.empty(f32, b, d) if want_dh0 else None
+    ws, wn = call.workspace(workspace, gated_scan_bwd_workspace_bytes(b, L, d, io))
+    call.run(m.gated_scan_bwd, x, r, i, lam, c, z, reset, states, dy, dh_last, out["dx"], out["dr"],
+             out["di"], out["dz"], out["dlam"], out["dh0"], b, L, d, io, ws, wn)
     return out
 
 
@@ -220,25 +253,23 @@ def gated_step(h, x_t, r_t, i_t, lam, z_t=None, *, c=8.0, y_t=None, stream=None)
     """ms_gated_step on torch device tensors: one step of the recurrence for
     x_t [batch, d]; h [batch, d] fp32 is updated in place.  Returns y_t."""
     import torch
-    if not getattr(x_t, "is_cuda", False) or x_t.dim() != 2:
-        raise ValueError("x_t must be a [batch, d_inner] device tensor")
-    io, shape, dev, dt = ms._io(x_t), x_t.shape, x_t.device, x_t.dtype
+    m = _marshal()
+    io = _io_of(m, x_t, "x_t", 2, "[batch, d_inner]")
+    b, d = x_t.shape
     f32 = torch.float32
-    if h is None:
-        raise ValueError("h is required")
-    _chk(h, "h", f32, shape, dev)
-    _chk(x_t, "x_t", dt, shape, dev)
-    _chk(r_t, "r_t", dt, shape, dev)
-    _chk(i_t, "i_t", dt, shape, dev)
-    _chk(lam, "lam", f32, shape[1:], dev)
-    _chk(z_t, "z_t", dt, shape, dev)
-    _chk(y_t, "y_t", dt, shape, dev)
-    call = _Call(x_t, stream)
+    for t, name in ((h, "h"), (r_t, "r_t"), (i_t, "i_t"), (lam, "lam")):
+        if t is None:
+            raise ValueError(f"{name} is required")
+    if not m.like(x_t, r_t, i_t, z_t, y_t):
+        _refuse(x_t.device, x_t.dtype, (b, d), r_t=r_t, i_t=i_t, z_t=z_t, y_t=y_t)
+    if not m.fits(x_t, f32, (b, d), h):
+        _refuse(x_t.device, f32, (b, d), h=h)
+    if not m.fits(x_t, f32, (d,), lam):
+        _refuse(x_t.device, f32, (d,), lam=lam)
+    call = _Call(m, x_t, stream)
     if y_t is None:
-        y_t = call.empty(shape, dt)
-    p = ms._ptr
-    call.run(ms.load().ms_gated_step, p(h), p(x_t), p(r_t), p(i_t), p(lam), c, p(z_t), p(y_t),
-             shape[0], shape[1], io)
+        y_t = call.empty(x_t.dtype, b, d)
+    call.run(m.gated_step, h, x_t, r_t, i_t, lam, c, z_t, y_t, b, d, io)
     return y_t
 
 
@@ -257,20 +288,18 @@ def embed_fwd(ids, weight, *, scale=1.0, out=None, stream=None):
     """ms_embed_fwd on torch device tensors: scale * weight[ids] for ids of
     any shape; ids outside the table give rows of zeros.  Returns
     [*ids.shape, dim]."""
-    if not getattr(weight, "is_cuda", False) or weight.dim() != 2:
-        raise ValueError("weight must be a [rows, dim] device tensor")
-    io = ms._io(weight)
+    m = _marshal()
+    io = _io_of(m, weight, "weight", 2, "[rows, dim]")
     rows, dim = weight.shape
-    bits, dev = _id_bits(ids, "ids"), weight.device
-    _chk(ids, "ids", ids.dtype, ids.shape, dev)
-    _chk(weight, "weight", weight.dtype, weight.shape, dev)
-    shape = (*ids.shape, dim)
-    _chk(out, "out", weight.dtype, shape, dev)
-    call = _Call(weight, stream)
+    bits, size = _id_bits(ids, "ids"), ids.shape
+    if not m.fits(weight, ids.dtype, size, ids):
+        _refuse(weight.device, ids.dtype, size, ids=ids)
+    if out is not None and not m.fits(weight, weight.dtype, (*size, dim), out):
+        _refuse(weight.device, weight.dtype, (*size, dim), out=out)
+    call = _Call(m, weight, stream)
     if out is None:
-        out = call.empty(shape, weight.dtype)
-    call.run(ms.load().ms_embed_fwd, ms._ptr(ids), bits, ms._ptr(weight), scale, ms._ptr(out),
-             ids.numel(), rows, dim, io)
+        out = call.empty(weight.dtype, *size, dim)
+    call.run(m.embed_fwd, ids, bits, weight, scale, out, ids.numel(), rows, dim, io)
     return out
 
 
@@ -287,26 +316,28 @@ def embed_bwd(ids, dy, rows, *, scale=1.0, padding=-1, grad_dtype=None, dweight=
     table of embed_fwd for dy [*ids.shape, dim], in grad_dtype (dy's when not
     given); the row `padding` gets none.  Returns dweight."""
     import torch
-    if not getattr(dy, "is_cuda", False) or dy.dim() != ids.dim() + 1:
-        raise ValueError("dy must be a [*ids.shape, dim] device tensor")
-    io = ms._io(dy)
-    bits = _id_bits(ids, "ids")
-    dim, dev = dy.shape[-1], dy.device
-    _chk(ids, "ids", ids.dtype, ids.shape, dev)
-    _chk(dy, "dy", dy.dtype, (*ids.shape, dim), dev)
+    m = _marshal()
+    size = ids.shape
+    io = _io_of(m, dy, "dy", len(size) + 1, "[*ids.shape, dim]")
+    bits, dim = _id_bits(ids, "ids"), dy.shape[-1]
+    if not m.fits(dy, ids.dtype, size, ids):
+        _refuse(dy.device, ids.dtype, size, ids=ids)
+    if not m.fits(dy, dy.dtype, (*size, dim), dy):
+        _refuse(dy.device, dy.dtype, (*size, dim), dy=dy)
     if grad_dtype is None:
         grad_dtype = dy.dtype if dweight is None else dweight.dtype
     if grad_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"grad_dtype must be float32 or bfloat16, got {grad_dtype}")
-    _chk(dweight, "dweight", grad_dtype, (rows, dim), dev)
+    if dweight is not None and not m.fits(dy, grad_dtype, (rows, dim), dweight):
+        _refuse(dy.device, grad_dtype, (rows, dim), dweight=dweight)
     n = ids.numel()
     need = embed_bwd_workspace_bytes(n, rows, dim, io)
-    call = _Call(dy, stream)
+    call = _Call(m, dy, stream)
     if dweight is None:
-        dweight = call.empty((rows, dim), grad_dtype)
-    wp, wn, keep = call.workspace(workspace, need)
-    call.run(ms.load().ms_embed_bwd, ms._ptr(ids), bits, ms._ptr(dy), scale, padding, ms._ptr(dweight),
-             ms.MS_BF16 if grad_dtype == torch.bfloat16 else ms.MS_F32, n, rows, dim, io, wp, wn)
+        dweight = call.empty(grad_dtype, rows, dim)
+    ws, wn = call.workspace(workspace, need)
+    call.run(m.embed_bwd, ids, bits, dy, scale, padding, dweight,
+             ms.MS_BF16 if grad_dtype == torch.bfloat16 else ms.MS_F32, n, rows, dim, io, ws, wn)
     return dweight
 
 
@@ -325,10 +356,11 @@ def _chk_logits(logits, name="logits"):
     return rows, vocab, ld
 
 
-def _chk_targets(targets, rows, device):
+def _chk_targets(m, targets, rows, logits):
     if targets is None:
         return 64
-    _chk(targets, "targets", targets.dtype, (rows,), device)
+    if not m.fits(logits, targets.dtype, (rows,), targets):
+        _refuse(logits.device, targets.dtype, (rows,), targets=targets)
     return _id_bits(targets, "targets")
 
 
@@ -346,23 +378,23 @@ def token_logprobs_fwd(logits, targets=None, *, top=0, scale=1.0, workspace=None
     gradient), top_logprob [rows, top] fp32 and
     top_id [rows, top] int32."""
     import torch
+    m = _marshal()
     rows, vocab, ld = _chk_logits(logits)
     io = ms._io(logits)
-    bits = _chk_targets(targets, rows, logits.device)
+    bits = _chk_targets(m, targets, rows, logits)
     f32 = torch.float32
     need = token_logprobs_workspace_bytes(rows, vocab, top, io)
-    call = _Call(logits, stream)
-    out = {"logprob": call.empty((rows,), f32) if targets is not None else None,
-           "entropy": call.empty((rows,), f32), "lse": call.empty((rows,), f32),
-           "stats": call.empty((rows, 2), f32),
-           "top_logprob": call.empty((rows, top), f32),
-           "top_id": call.empty((rows, top), torch.int32)}
-    wp, wn, keep = call.workspace(workspace, need)
-    p = ms._ptr
-    call.run(ms.load().ms_token_logprobs_fwd, p(logits), ld, p(targets), bits, scale, p(out["logprob"]),
-             p(out["entropy"]), p(out["lse"]), p(out["stats"]), top, p(out["top_logprob"]),
-             p(out["top_id"]), rows, vocab, io, wp, wn)
-    return out
+    call = _Call(m, logits, stream)
+    each = (rows,)
+    logprob, entropy, lse, stats, top_logprob, top_id = call.together(
+        f32, each, f32, each, f32, each, f32, (rows, 2), f32, (rows, top), torch.int32, (rows, top))
+    if targets is None:
+        logprob = None
+    ws, wn = call.workspace(workspace, need)
+    call.run(m.token_logprobs_fwd, logits, ld, targets, bits, scale, logprob, entropy, lse, stats,
+             top, top_logprob, top_id, rows, vocab, io, ws, wn)
+    return {"logprob": logprob, "entropy": entropy, "lse": lse, "stats": stats,
+            "top_logprob": top_logprob, "top_id": top_id}
 
 
 def token_logprobs_bwd(logits, targets, stats, entropy=None, dlogprob=None, dentropy=None, *,
@@ -372,27 +404,28 @@ def token_logprobs_bwd(logits, targets, stats, entropy=None, dlogprob=None, dent
     the stats and entropy that token_logprobs_fwd returned.  dlogits may be
     logits.  Returns dlogits."""
     import torch
+    m = _marshal()
     rows, vocab, ld = _chk_logits(logits)
     io = ms._io(logits)
-    dev = logits.device
-    bits = _chk_targets(targets, rows, dev)
+    bits = _chk_targets(m, targets, rows, logits)
     f32 = torch.float32
-    _chk(stats, "stats", f32, (rows, 2), dev)
-    for t, name in ((entropy, "entropy"), (dlogprob, "dlogprob"), (dentropy, "dentropy")):
-        _chk(t, name, f32, (rows,), dev)
-    call = _Call(logits, stream)
+    if not m.fits(logits, f32, (rows, 2), stats):
+        _refuse(logits.device, f32, (rows, 2), stats=stats)
+    if not m.fits(logits, f32, (rows,), entropy, dlogprob, dentropy):
+        _refuse(logits.device, f32, (rows,), entropy=entropy, dlogprob=dlogprob,
+                dentropy=dentropy)
+    call = _Call(m, logits, stream)
     if dlogits is None:
-        dlogits = call.empty((rows, vocab), logits.dtype)
+        dlogits = call.empty(logits.dtype, rows, vocab)
     r2, v2, ldd = _chk_logits(dlogits, "dlogits")
     if dlogits.dtype != logits.dtype:
         raise TypeError(f"dlogits must be {logits.dtype}, got {dlogits.dtype}")
     if (r2, v2) != (rows, vocab):
         raise ValueError(f"dlogits must have shape {(rows, vocab)}, got {(r2, v2)}")
-    if dlogits.device != dev:
-        raise ValueError(f"dlogits is on {dlogits.device}, not on {dev}")
-    p = ms._ptr
-    call.run(ms.load().ms_token_logprobs_bwd, p(logits), ld, p(targets), bits, scale, p(stats), p(entropy),
-             p(dlogprob), p(dentropy), p(dlogits), ldd, rows, vocab, io)
+    if dlogits.device != logits.device:
+        raise ValueError(f"dlogits is on {dlogits.device}, not on {logits.device}")
+    call.run(m.token_logprobs_bwd, logits, ld, targets, bits, scale, stats, entropy, dlogprob,
+             dentropy, dlogits, ldd, rows, vocab, io)
     return dlogits
 
 

@@ -130,3 +130,38 @@ def test_binding_refuses_host_tensors():
         ms.embed_bwd(torch.zeros(3, dtype=torch.int64), torch.zeros(3, 8), 5)
     with pytest.raises(ValueError, match="device"):
         ms.token_logprobs_fwd(torch.zeros(3, 8))
+
+
+def test_marshalling():
+    """The binding's extension module on host tensors (it looks at no memory)."""
+    m = ms.lm._marshal()
+    x, f32 = torch.zeros(3, 4), torch.float32
+    assert m.io(x, 2) == -1  # not on a device
+    assert m.like(x, None, torch.ones(3, 4)) and not m.like(x, torch.ones(4, 3))
+    assert not m.like(x, torch.ones(4, 3).t()) and not m.like(x, x.double())
+    assert not m.like(x, 7) and not m.like(None, x)
+    assert m.fits(x, torch.int32, (2,), None, torch.zeros(2, dtype=torch.int32))
+    assert not m.fits(x, f32, (3,), x) and not m.fits(x, f32, (3, 5), x)
+    assert not m.fits(x, f32, (4, 3), torch.zeros(3, 4).t())
+    with pytest.raises(TypeError):
+        m.fits(x, f32, (3, "4"), x)
+    e = m.empty(x, torch.bfloat16, 2, 0, 5)
+    assert e.shape == (2, 0, 5) and e.dtype == torch.bfloat16
+    with pytest.raises(TypeError):
+        m.empty(x, 5)
+    a, b = m.together(x, f32, (5,), torch.int64, (2, 3))
+    assert a.shape == (5,) and b.shape == (2, 3) and b.dtype == torch.int64
+    a.fill_(1), b.fill_(2)
+    assert a.sum() == 5 and b.sum() == 12 and not a._is_view()
+    for bad in ((f32,), (f32, (-1,)), (f32, 5), (5, (1,))):
+        with pytest.raises(TypeError):
+            m.together(x, *bad)
+    # wrong counts and types never reach the library
+    with pytest.raises(TypeError):
+        m.gated_step(x)
+    with pytest.raises(TypeError):
+        m.gated_step(x, x, x, x, x, "8", None, x, 3, 4, 0, 0)
+    with pytest.raises(OverflowError):
+        m.gated_step(x, x, x, x, x, 8.0, None, x, 1 << 40, 4, 0, 0)
+    assert m.gated_step(x, x, x, x, x, 8.0, None, x, 0, 4, 0, 0) == 2  # MS_ERR_SHAPE
+    assert m.gated_step(None, x, x, x, x, 8.0, None, x, 3, 4, 0, None) == 1  # MS_ERR_NULL
