@@ -149,6 +149,7 @@ PyObject* together(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // A C argument from a Python one: pointers from tensors, addresses or None.
 template <class T>
 T convert(PyObject* o) {
+    if (PyErr_Occurred()) return T{};  // an earlier argument's
     if constexpr (std::is_pointer<T>::value) {
         if (o == Py_None) return nullptr;
         if (const at::Tensor* t = tensor_of(o))
