@@ -13,12 +13,13 @@
 // ln2 (log2 s - T / s) has no cancellation against a large maximum.
 //
 // Alternatives come from the same pass.  A wave holds a threshold that at least
-// `top` logits of the row reach, first from the maxima of its lanes' first
-// block (the top-th largest of them), and the best of what the workgroup's
-// other waves have found.  A lane whose block of 32 (16 in fp32) logits reaches
+// `top` logits of the row reach: the top-th largest of the maxima of the
+// workgroup's lanes (or of groups of lanes, Threshold below) over their first
+// block.  A lane whose block of 32 (16 in fp32) logits reaches
 // it, known from the maximum that the softmax needs anyway, notes the block:
 // one comparison a block, and some four notes in 2000 logits at top 5.  At the
-// end few of the noted blocks reach the last threshold; those are read again
+// end the threshold is taken once more, from the maxima over all blocks, and
+// few of the noted blocks reach it; those are read again
 // (they are in cache), and each logit that reaches it finds its rank by
 // counting the larger ones of the workgroup, in LDS.
 #include <hip/hip_runtime.h>
@@ -195,7 +196,7 @@ struct Notes {
 struct Noted {
     Notes* q;
     float thr;    // what a block's largest logit has to reach to be noted
-    float bound;  // what at least `top` logits of the wave reach
+    float bound;  // what at least `top` logits of the row reach
     int top, count, lane;
 
     __device__ __forceinline__ void init(Notes* notes, int top_, int lane_) {
@@ -204,31 +205,6 @@ struct Noted {
         top = top_;
         count = 0;
         lane = lane_;
-    }
-    // A value that at least `top` of the wave's logits reach: the top-th largest
-    // of its 64 lanes' maxima, or, for few alternatives, of the maxima of 16
-    // quads of lanes (a threshold almost as high for a quarter of the work), as
-    // the least of those with fewer than `top` above them.
-    __device__ __forceinline__ float reached(float lane_max) const {
-        float v = lane_max == lane_max ? lane_max : -__builtin_inff();
-        int above = 0;
-        auto count_above = [&](auto step) {
-#pragma unroll 16
-            for (int l = 0; l < 64; l += decltype(step)::value)
-                above += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l)) > v;
-        };
-        if (top <= 8) {
-            auto dpp = [&](auto ctrl) {
-                v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(
-                                 __float_as_int(v), decltype(ctrl)::value, 0xf, 0xf, true)));
-            };
-            dpp(std::integral_constant<int, 0xB1>{});  // quad_perm 1,0,3,2
-            dpp(std::integral_constant<int, 0x4E>{});  // quad_perm 2,3,0,1
-            count_above(std::integral_constant<int, 4>{});
-        } else {
-            count_above(std::integral_constant<int, 1>{});
-        }
-        return -wave_max(above < top ? -v : -__builtin_inff());
     }
     __device__ __forceinline__ void note(bool in, uint32_t first, float high) {
         const uint64_t m = __ballot(in);
@@ -283,6 +259,44 @@ struct Noted {
             thr = fmaxf(thr, next_above(bound));
         }
         wave_sync();
+    }
+};
+
+// A value that at least `top` logits of the workgroup reach: the top-th largest
+// of the maxima of its lanes, or of neighbouring lanes together, four maxima or
+// more for each alternative (that is almost as high, and fewer are compared).
+struct Threshold {
+    float high[64 * kLpWaves], least[kLpWaves];
+
+    // By the whole workgroup; two barriers.  lane_max: -inf where there is none.
+    __device__ __forceinline__ float take(float lane_max, int top) {
+        float v = lane_max == lane_max ? lane_max : -__builtin_inff();
+        auto join = [&](auto ctrl) {
+            v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(
+                             __float_as_int(v), decltype(ctrl)::value, 0xf, 0xf, true)));
+        };
+        int shift = 0;  // log2 of the lanes together
+        if (top <= 32) join(std::integral_constant<int, 0xB1>{}), shift = 1;  // quad_perm 1,0,3,2
+        if (top <= 16) join(std::integral_constant<int, 0x4E>{}), shift = 2;  // quad_perm 2,3,0,1
+        if (top <= 8) join(std::integral_constant<int, 0x141>{}), shift = 3;  // row_half_mirror
+        const int n = (64 * kLpWaves) >> shift, tid = threadIdx.x;
+        if ((tid & ((1 << shift) - 1)) == 0) high[tid >> shift] = v;
+        __syncthreads();
+        if ((tid & ~63) < n) {  // whole waves
+            const float own = high[min(tid, n - 1)];
+            int above = 0;
+#pragma unroll 8
+            for (int k = 0; k < n; k += 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) above += high[k + e] > own;
+            }
+            const float lo = -wave_max(above < top ? -own : -__builtin_inff());
+            if ((tid & 63) == 0) least[tid >> 6] = lo;
+        }
+        __syncthreads();
+        float t = least[0];
+        for (int w = 1; w * 64 < n; ++w) t = fminf(t, least[w]);
+        return t;
     }
 };
 
@@ -388,7 +402,8 @@ __global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(Logpro
     constexpr int D = 3;                            // blocks in hand or under way
     __shared__ uint64_t s_key[TOP ? kMaxKeys : 1], s_best[TOP ? kMaxTop : 1];
     __shared__ Notes s_notes[TOP ? kLpWaves : 1];
-    __shared__ float s_stat[kLpWaves][4], s_thr[kLpWaves];
+    __shared__ Threshold s_level[1];
+    __shared__ float s_stat[kLpWaves][4], s_bound[kLpWaves];
     __shared__ int s_count;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -412,18 +427,8 @@ __global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(Logpro
     Noted noted;
     if constexpr (TOP) {
         noted.init(&s_notes[wave], a.top, lane);
-        if (threadIdx.x < kLpWaves) s_thr[threadIdx.x] = -__builtin_inff();
         if (threadIdx.x == 0) s_count = 0;
-        __syncthreads();
     }
-    auto shared_threshold = [&]() {
-        float t = -__builtin_inff();
-#pragma unroll
-        for (int k = 0; k < kLpWaves; ++k)
-            t = fmaxf(t, __hip_atomic_load(&s_thr[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
-        return t;
-    };
-    bool first = true;
 
     // the lane's K logits (-inf where there is none; any: one is), from `token`
     auto take = [&](auto& v, auto K, bool any, uint32_t token) {
@@ -432,17 +437,6 @@ __global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(Logpro
 #pragma unroll
         for (int e = 1; e < kN; ++e) mb = fmaxf(mb, v[e]);
         if constexpr (TOP) {
-            if (first) {
-                first = false;
-                noted.bound = noted.reached(mb);
-                if (lane == 0)
-                    __hip_atomic_store(&s_thr[wave], noted.bound, __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_WORKGROUP);
-                noted.thr = noted.bound;
-            }
-            // (How much of the other waves' thresholds is here by now changes
-            // what is noted, not what comes out.)
-            noted.thr = fmaxf(noted.thr, shared_threshold());
             const bool in = any && mb >= noted.thr;
             if (__any(in)) noted.note(in, token, mb);
         }
@@ -461,8 +455,8 @@ __global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(Logpro
 #pragma unroll
         for (int u = 0; u < U; ++u) r[u] = L::load(x + (int64_t)min(b + u * 64 + lane, v1 - 1) * N);
     };
-    auto block = [&](uint32_t b, const typename L::T(&r)[U]) {
-        float v[U * N];
+    // a block's logits in order of their tokens; false where the lane has none
+    auto unpack = [&](uint32_t b, const typename L::T(&r)[U], float(&v)[U * N]) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float t[N];
@@ -470,16 +464,18 @@ __global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(Logpro
 #pragma unroll
             for (int e = 0; e < N; ++e) v[u * N + e] = t[e];
         }
-        bool any = true;
-        if (b + 64 * U > v1) {  // the end of the vectors
-            any = b + lane < v1;
+        if (b + 64 * U <= v1) return true;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const bool in = b + u * 64 + lane < v1;
+        for (int u = 0; u < U; ++u) {  // the end of the vectors
+            const bool in = b + u * 64 + lane < v1;
 #pragma unroll
-                for (int e = 0; e < N; ++e) v[u * N + e] = in ? v[u * N + e] : -__builtin_inff();
-            }
+            for (int e = 0; e < N; ++e) v[u * N + e] = in ? v[u * N + e] : -__builtin_inff();
         }
+        return b + lane < v1;
+    };
+    auto block = [&](uint32_t b, const typename L::T(&r)[U]) {
+        float v[U * N];
+        const bool any = unpack(b, r, v);
         take(v, std::integral_constant<int, U * N>{}, any, (b + lane) * N);
     };
     constexpr uint32_t kStep = 64 * U * kLpWaves;
@@ -491,6 +487,17 @@ __global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(Logpro
     const int64_t target = target_of(a, row);
     float tl = 0.f;
     if (wave == 0 && target >= 0) tl = L::one(x + target);
+    if constexpr (TOP) {
+        float m = -__builtin_inff();
+        if (b < v1) {
+            float v[U * N];
+            unpack(b, w[0], v);
+            m = v[0];
+#pragma unroll
+            for (int e = 1; e < U * N; ++e) m = fmaxf(m, v[e]);
+        }
+        noted.thr = noted.bound = s_level[0].take(m, a.top);
+    }
     while (b < v1) {  // D blocks a turn, D - 1 under way while one is taken
 #pragma unroll
         for (int d = 0; d < D; ++d) {
@@ -507,10 +514,10 @@ __global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(Logpro
         float v[1] = {in ? L::one(x + i) : -__builtin_inff()};
         take(v, std::integral_constant<int, 1>{}, in, (uint32_t)i);
     }
+    float level = 0.f;
     if constexpr (TOP) {
-        const float t = fmaxf(noted.reached(high), noted.bound);
-        if (lane == 0)
-            __hip_atomic_store(&s_thr[wave], t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        if (lane == 0) s_bound[wave] = noted.bound;
+        level = s_level[0].take(high, a.top);
     }
     st.join_wave();
     high = wave_max(high);
@@ -525,7 +532,9 @@ __global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(Logpro
     if constexpr (TOP) {
         // Noted blocks that reach the row's last threshold, G logits each, read
         // again 64 / G blocks at a time; f gets every logit that reaches it.
-        const float t = shared_threshold();
+        float t = level;
+#pragma unroll
+        for (int k = 0; k < kLpWaves; ++k) t = fmaxf(t, s_bound[k]);
         constexpr int G = U * N;
         auto read_again = [&](auto f) {
             const Notes& q = s_notes[wave];
@@ -601,19 +610,20 @@ __global__ void __launch_bounds__(64 * kLpWaves) logprob_join(LogprobArgs a) {
     float tl = 0.f;
     if (threadIdx.x == 0 && target >= 0) tl = L::one(x + target);
     if constexpr (TOP) {
-        // every split has `top` keys not below its last: the best such last
-        // bounds the row's, and few keys reach it
-        __shared__ uint64_t s_bound;
+        // A key that at least `top` keys reach: each split's j-th is reached by
+        // j of its own, so the k-th largest of those, k j >= top.  Few reach it.
+        __shared__ uint64_t s_bound, s_jth[64];
         __shared__ int s_count;
         const uint64_t* list = a.list + row * a.splits * a.top;
-        if (threadIdx.x < 64) {
-            uint64_t b = (int)threadIdx.x < a.splits ? list[threadIdx.x * a.top + a.top - 1] : 0;
-#pragma unroll
-            for (int off = 32; off > 0; off >>= 1) {
-                const uint64_t o = shfl64(b, threadIdx.x ^ off);
-                b = b > o ? b : o;
-            }
-            if (threadIdx.x == 0) s_bound = b, s_count = 0;
+        const int j = (a.top + a.splits - 1) / a.splits, kth = (a.top + j - 1) / j;
+        const uint64_t own = (int)threadIdx.x < a.splits ? list[threadIdx.x * a.top + j - 1] : 0;
+        if (threadIdx.x < 64) s_jth[threadIdx.x] = own;
+        if (threadIdx.x == 0) s_bound = 0, s_count = 0;
+        __syncthreads();
+        if ((int)threadIdx.x < a.splits && own) {  // keys differ: one rank is kth - 1
+            int above = 0;
+            for (int q = 0; q < a.splits; ++q) above += s_jth[q] > own;
+            if (above == kth - 1) s_bound = own;
         }
         __syncthreads();
         for (int k = threadIdx.x; k < a.splits * a.top; k += 64 * kLpWaves) {
