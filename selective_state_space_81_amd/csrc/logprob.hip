@@ -704,7 +704,7 @@ uint32_t grad_chunks(const LogprobArgs& a, bool bf16) {
 
 void logprob_plan(LogprobArgs& a, bool bf16) {
     // Few rows are split over about 512 workgroups, of 4096 logits at least (64
-    // rows of 131072 at top 20: 20 us, with 1024 27, with 256 21).
+    // rows of 131072 at top 20: 17.0 us, with 1024 18.5).
     const int64_t vec = bf16 ? 8 : 4, nvec = a.V / vec;
     int64_t n = a.rows > 0 ? (512 + a.rows - 1) / a.rows : 1;
     const int64_t most = (a.V + 4095) / 4096, keys = a.top ? kMaxKeys / a.top : 64;
