@@ -136,6 +136,7 @@ struct LogprobArgs {
     int64_t ldd;
     int top;
     int splits;    // workgroups of a row
+    int waves;     // of a workgroup, 4 or 16
     uint32_t per;  // vectors each of them takes
 };
 struct LogprobWs {

@@ -43,7 +43,6 @@ namespace {
 
 using namespace dev;
 
-constexpr int kLpWaves = 4;
 constexpr int kMaxKeys = 1024;  // keys that a workgroup ranks
 // References stay within +-kFar; a row whose largest logit is past it (all of
 // them the type's lowest value, say) has its sums taken again by far_row.
@@ -272,8 +271,9 @@ struct Noted {
 // A value that at least `top` logits of the workgroup reach: the top-th largest
 // of the maxima of its lanes, or of neighbouring lanes together, four maxima or
 // more for each alternative (that is almost as high, and fewer are compared).
+template <int W>
 struct Threshold {
-    float high[64 * kLpWaves], least[kLpWaves];
+    float high[64 * W], least[W];
 
     // By the whole workgroup; two barriers.  lane_max: -inf where there is none.
     __device__ __forceinline__ float take(float lane_max, int top) {
@@ -282,11 +282,14 @@ struct Threshold {
             v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(
                              __float_as_int(v), decltype(ctrl)::value, 0xf, 0xf, true)));
         };
-        int shift = 0;  // log2 of the lanes together
-        if (top <= 32) join(std::integral_constant<int, 0xB1>{}), shift = 1;  // quad_perm 1,0,3,2
-        if (top <= 16) join(std::integral_constant<int, 0x4E>{}), shift = 2;  // quad_perm 2,3,0,1
-        if (top <= 8) join(std::integral_constant<int, 0x141>{}), shift = 3;  // row_half_mirror
-        const int n = (64 * kLpWaves) >> shift, tid = threadIdx.x;
+        // log2 of the lanes together, 4 at most (a DPP row)
+        int shift = top <= 8 ? 3 : top <= 16 ? 2 : top <= 32 ? 1 : 0;
+        if (W == 16) shift = min(shift + 2, 4);
+        if (shift > 0) join(std::integral_constant<int, 0xB1>{});   // quad_perm 1,0,3,2
+        if (shift > 1) join(std::integral_constant<int, 0x4E>{});   // quad_perm 2,3,0,1
+        if (shift > 2) join(std::integral_constant<int, 0x141>{});  // row_half_mirror
+        if (shift > 3) join(std::integral_constant<int, 0x140>{});  // row_mirror
+        const int n = (64 * W) >> shift, tid = threadIdx.x;
         if ((tid & ((1 << shift) - 1)) == 0) high[tid >> shift] = v;
         __syncthreads();
         if ((tid & ~63) < n) {  // whole waves
@@ -401,21 +404,21 @@ __device__ __forceinline__ void end_row(const LogprobArgs& a, int64_t row, const
 }
 
 // ---- forward ------------------------------------------------------------------------------
-// One workgroup a row, or a split of one.  A wave takes blocks of 64 * U vectors
+// One workgroup of W waves a row, or a split of one.  A wave takes blocks of 64 * U vectors
 // in turn with the others, one in hand and D - 1 on the way.  Without
 // alternatives (8192 x 32001 bf16): U, D = 4, 3 at 4 waves a SIMD 129 us; 4, 2 at
 // 6 134; 2, 3 at 8 138; 1, 4 at 8 144.  With them registers hold U = 2 (U = 4, D =
 // 2: 8192 x 50280 at 5 213 against 185).
-template <bool BF16, bool TOP>
-__global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(LogprobArgs a) {
+template <bool BF16, bool TOP, int W>
+__global__ void __launch_bounds__(64 * W, TOP && W == 4 ? 5 : 4) logprob_fwd(LogprobArgs a) {
     using L = Lg<BF16>;
     using E = typename L::E;
     constexpr int N = L::N, U = TOP ? 2 : 4;  // vectors a lane takes of a block
     constexpr int D = 3;                      // blocks in hand or under way
     __shared__ uint64_t s_key[TOP ? kMaxKeys : 1], s_best[TOP ? kMaxTop : 1];
-    __shared__ Notes s_notes[TOP ? kLpWaves : 1];
-    __shared__ Threshold s_level[1];
-    __shared__ float s_stat[kLpWaves][4], s_bound[kLpWaves];
+    __shared__ Notes s_notes[TOP ? W : 1];
+    __shared__ Threshold<W> s_level[1];
+    __shared__ float s_stat[W][4], s_bound[W];
     __shared__ int s_count;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(Logpro
         const bool any = unpack(b, r, v);
         take(v, std::integral_constant<int, U * N>{}, any, (b + lane) * N);
     };
-    constexpr uint32_t kStep = 64 * U * kLpWaves;
+    constexpr uint32_t kStep = 64 * U * W;
     uint32_t b = v0 + wave * (64 * U);
 #pragma unroll
     for (int d = 0; d < D - 1; ++d)
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(Logpro
         // again 64 / G blocks at a time; f gets every logit that reaches it.
         float t = level;
 #pragma unroll
-        for (int k = 0; k < kLpWaves; ++k) t = fmaxf(t, s_bound[k]);
+        for (int k = 0; k < W; ++k) t = fmaxf(t, s_bound[k]);
         constexpr int G = U * N;
         auto read_again = [&](auto f) {
             const Notes& q = s_notes[wave];
@@ -588,7 +591,7 @@ __global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(Logpro
             });
             __syncthreads();
             s_key[wave * 64 + lane] = list;
-            n = 64 * kLpWaves;
+            n = 64 * W;
             __syncthreads();
         }
         rank_keys(s_key, n, a.top, s_best);
@@ -598,7 +601,7 @@ __global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(Logpro
             if ((int)threadIdx.x < a.top) a.list[at * a.top + threadIdx.x] = s_best[threadIdx.x];
         }
         if (wave != 0) return;
-        st = join_lanes(&s_stat[0][0], kLpWaves, 4, high);
+        st = join_lanes(&s_stat[0][0], W, 4, high);
         if (lane == 0) {
             a.part[at * 4] = st.r;
             a.part[at * 4 + 1] = st.s;
@@ -608,12 +611,13 @@ __global__ void __launch_bounds__(64 * kLpWaves, TOP ? 5 : 4) logprob_fwd(Logpro
         return;
     }
     if (wave != 0) return;
-    end_row<L>(a, row, &s_stat[0][0], kLpWaves, x, tl, target >= 0, s_best);
+    end_row<L>(a, row, &s_stat[0][0], W, x, tl, target >= 0, s_best);
 }
 
 // Joins the splits of a row (64 at most, and kMaxKeys keys).
+constexpr int kJoinWaves = 4;
 template <bool BF16, bool TOP>
-__global__ void __launch_bounds__(64 * kLpWaves) logprob_join(LogprobArgs a) {
+__global__ void __launch_bounds__(64 * kJoinWaves) logprob_join(LogprobArgs a) {
     using L = Lg<BF16>;
     __shared__ uint64_t s_key[TOP ? kMaxKeys : 1], s_best[TOP ? kMaxTop : 1];
     const int64_t row = blockIdx.x;
@@ -638,7 +642,7 @@ __global__ void __launch_bounds__(64 * kLpWaves) logprob_join(LogprobArgs a) {
             if (above == kth - 1) s_bound = own;
         }
         __syncthreads();
-        for (int k = threadIdx.x; k < a.splits * a.top; k += 64 * kLpWaves) {
+        for (int k = threadIdx.x; k < a.splits * a.top; k += 64 * kJoinWaves) {
             const uint64_t v = list[k];
             if (v && v >= s_bound) s_key[atomicAdd(&s_count, 1)] = v;
         }
@@ -726,6 +730,15 @@ void logprob_plan(LogprobArgs& a, bool bf16) {
     if (n > keys) n = keys;
     if (n > 64) n = 64;
     if (n < 1) n = 1;
+    // Instead of splits, one workgroup of 16 waves a row, with no second launch:
+    // for rows that are short, or fill the chip (256 of them: a compute unit
+    // each), as GPU time alone at top 5 has it, in us split and whole: one row of
+    // 20000 bf16 8.8 and 7.4, of 50280 fp32 9.6 and 10.5 (and 2 between the
+    // launches), of 131072 bf16 9.1 and 13.9; 64 of those 13.2 and 15.5, 96 16.9
+    // and 15.9, 200 21.7 and 18.0, 260 25.8 and 30.8.
+    const int64_t bytes = a.V * (bf16 ? 2 : 4);
+    a.waves = 4;
+    if (n > 1 && a.rows <= 256 && (a.rows >= 96 || bytes <= 224 * 1024)) a.waves = 16, n = 1;
     const int64_t per = (nvec + n - 1) / n;
     a.per = (uint32_t)((per + 63) / 64 * 64);  // whole waves of vectors
     a.splits = n == 1 ? 1 : (int)((nvec + a.per - 1) / a.per);
@@ -742,26 +755,33 @@ LogprobWs logprob_ws(const LogprobArgs& a) {
     return w;
 }
 
+template <int W>
+static void fwd_variant(const LogprobArgs& a, bool bf16, hipStream_t s) {
+    const dim3 grid((unsigned)(a.rows * a.splits)), blk(64 * W);
+    if (bf16) {
+        if (a.top) hipLaunchKernelGGL((logprob_fwd<true, true, W>), grid, blk, 0, s, a);
+        else hipLaunchKernelGGL((logprob_fwd<true, false, W>), grid, blk, 0, s, a);
+    } else {
+        if (a.top) hipLaunchKernelGGL((logprob_fwd<false, true, W>), grid, blk, 0, s, a);
+        else hipLaunchKernelGGL((logprob_fwd<false, false, W>), grid, blk, 0, s, a);
+    }
+}
+
 hipError_t launch_logprob_fwd(LogprobArgs a, bool bf16, void* workspace, hipStream_t s) {
     const LogprobWs w = logprob_ws(a);
     if (a.splits > 1) {
         a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part);
         a.list = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + w.list);
     }
-    const dim3 grid((unsigned)(a.rows * a.splits)), rows((unsigned)a.rows), blk(64 * kLpWaves);
     {
         ProfScope ps(s, kPhaseMain);
-        if (bf16) {
-            if (a.top) hipLaunchKernelGGL((logprob_fwd<true, true>), grid, blk, 0, s, a);
-            else hipLaunchKernelGGL((logprob_fwd<true, false>), grid, blk, 0, s, a);
-        } else {
-            if (a.top) hipLaunchKernelGGL((logprob_fwd<false, true>), grid, blk, 0, s, a);
-            else hipLaunchKernelGGL((logprob_fwd<false, false>), grid, blk, 0, s, a);
-        }
+        if (a.waves == 16) fwd_variant<16>(a, bf16, s);
+        else fwd_variant<4>(a, bf16, s);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     ProfScope ps(s, kPhaseReduce);
+    const dim3 rows((unsigned)a.rows), blk(64 * kJoinWaves);
     if (bf16) {
         if (a.top) hipLaunchKernelGGL((logprob_join<true, true>), rows, blk, 0, s, a);
         else hipLaunchKernelGGL((logprob_join<true, false>), rows, blk, 0, s, a);

@@ -174,7 +174,7 @@ def test_launches_are_timed(gpu):
     w = torch.randn(40, 128, device=DEV)
     ids = torch.arange(5000, device=DEV) % 40
     t = torch.zeros(3, dtype=torch.int64, device=DEV)
-    logits = torch.randn(3, 30000, device=DEV)
+    logits, long = torch.randn(3, 30000, device=DEV), torch.randn(3, 90000, device=DEV)
     # (call, launches of each phase)
     calls = [(lambda: gpu.gated_scan_fwd(x, x, x, lam, states=states), {"prep": 1, "main": 1}),
              (lambda: gpu.gated_scan_bwd(x, x, x, lam, x, states),
@@ -183,7 +183,8 @@ def test_launches_are_timed(gpu):
              (lambda: gpu.embed_fwd(ids, w), {"main": 1}),
              (lambda: gpu.embed_bwd(ids, torch.ones(5000, 128, device=DEV), 40),
               {"main": 1, "reduce": 1}),
-             (lambda: gpu.token_logprobs_fwd(logits, t, top=5), {"main": 1, "reduce": 1})]
+             (lambda: gpu.token_logprobs_fwd(logits, t, top=5), {"main": 1}),
+             (lambda: gpu.token_logprobs_fwd(long, t, top=5), {"main": 1, "reduce": 1})]
     for k, (call, want) in enumerate(calls):
         gpu.profile_begin(1)
         call()

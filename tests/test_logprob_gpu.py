@@ -250,3 +250,14 @@ def test_refusals(gpu):
         gpu.token_logprobs_bwd(x, t, r["stats"], None, None, torch.ones(3, device=DEV))
     none = gpu.token_logprobs_fwd(x[:0], t[:0], top=2)
     assert none["logprob"].shape == (0,) and none["top_id"].shape == (0, 2)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_plans(gpu, io):
+    """One workgroup a row, one of many waves, and rows split over workgroups,
+    on both sides of the sizes where one gives way to the other."""
+    for rows, vocab in ((1, 4100), (2, 57344), (2, 57345), (1, 114689), (95, 120000), (96, 120000),
+                        (256, 9001), (257, 9001), (512, 4500)):
+        x, t = make(rows, vocab, io, seed=rows + vocab)
+        for top in (0, 7, 33, 64) if rows < 90 else (33,):
+            check(gpu, x, t, top=top)
