@@ -513,15 +513,18 @@ __global__ void __launch_bounds__(64 * W, TOP && W == 4 ? 5 : 4) logprob_fwd(Log
         }
         noted.thr = noted.bound = s_level[0].take(m, a.top);
     }
-    while (b < v1) {  // D blocks a turn, D - 1 under way while one is taken
+    // D - 1 blocks are under way while one is taken.  One body for all: three in
+    // turn, without the moves, measured 10.3 against 9.7 us for a row of 50280
+    // fp32 and 171 against 165 for 8192 of bf16, at top 5.
+#pragma unroll 1
+    for (; b < v1; b += kStep) {
+        const uint32_t ahead = b + (D - 1) * kStep;
+        if (ahead < v1) load(ahead, w[D - 1]);
+        block(b, w[0]);
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const uint32_t ahead = b + (D - 1) * kStep;
-            if (ahead < v1) load(ahead, w[(d + D - 1) % D]);
-            block(b, w[d]);
-            b += kStep;
-            if (b >= v1) break;
-        }
+        for (int d = 0; d + 1 < D; ++d)
+#pragma unroll
+            for (int u = 0; u < U; ++u) w[d][u] = w[d + 1][u];
     }
     if (wave == 0 && last && (int64_t)nvec * N < a.V) {  // the row's last V % N logits
         const int64_t i = (int64_t)nvec * N + lane;
