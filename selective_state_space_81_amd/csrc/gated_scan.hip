@@ -837,7 +837,9 @@ __global__ void __launch_bounds__(256) gated_step(GatedArgs a) {
 // a SIMD), since each lane's map costs a scan over the lanes.  The forward at 8
 // x 2048 x 1536 bf16 and at 131072 x 1536, in us: 60 and 346; 2 waves along time
 // 59 and 497, 8 waves 70 and 380, 4 steps a lane 67 and 473, 32 lanes across
-// channels 61 and 486 (shorter blocks make the chain of messages longer).
+// channels 61 and 486 (shorter blocks make the chain of messages longer).  The
+// backward at the first: 112; 8 steps a lane (which spills) 151, 2 waves a SIMD
+// 127, 3 or 6 waves along time 115 and 170.
 template <bool BF16>
 using Fwd = Geo<4, 16, 8, 4, BF16>;
 template <bool BF16>
