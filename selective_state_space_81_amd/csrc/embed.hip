@@ -332,7 +332,9 @@ __global__ void __launch_bounds__(256) sort_place(EmbedArgs a, SortPass p) {
 }
 
 // Up to kSmall entries: one workgroup sorts them whole, in LDS, all passes in
-// one launch, in the same manner.
+// one launch, in the same manner (the gradient of 5000 rows of 256 bf16 27.4 us
+// for 31.3 with four launches, of 8192 equal, of 16384 more: this sort alone
+// takes 34 us then).
 constexpr int kSmallWaves = 16, kSmallRounds = kSmall / (64 * kSmallWaves);
 
 __global__ void __launch_bounds__(64 * kSmallWaves) sort_small(EmbedArgs a, SortPass p) {

@@ -90,7 +90,9 @@ def test_logprob_refusals():
     assert fwd(scale=0.0) == 2 and fwd(scale=float("inf")) == 2
     assert fwd(x=4) == 5
     assert fwd(rows=0, x=None) == 0
-    assert fwd(rows=1, V=50000, ld=50000, ws=None) == 6
+    # a shape that is split over workgroups, and so needs a workspace
+    assert lib.ms_token_logprobs_workspace_bytes(1, 100000, 0, 0) > 0
+    assert fwd(rows=1, V=100000, ld=100000, ws=None) == 6
 
     def bwd(x=P, t=P, stats=P, ent=P, gl=P, gh=P, d=P, ld=40, ldd=40):
         return lib.ms_token_logprobs_bwd(x, ld, t, 64, 1.0, stats, ent, gl, gh, d, ldd, 3, 40, 0,
