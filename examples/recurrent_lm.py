@@ -41,7 +41,7 @@ class Block(torch.nn.Module):
 
     def parts(self, x):
         dt = torch.bfloat16
-        return [t.contiguous() for t in self.proj(self.norm(x)).to(dt).chunk(4, dim=-1)]
+        return self.proj(self.norm(x)).to(dt).chunk(4, dim=-1)  # read where they are
 
     def forward(self, x, reset):
         u, r, i, z = self.parts(x)

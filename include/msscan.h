@@ -352,7 +352,11 @@ ms_status ms_conv1d_silu(const void* x, const float* weight, const float* bias,
  *   y[b,t,d] = h                           (z == NULL)
  *            = h * z * sigmoid(z)          (z given)
  *
- *   x, r, i, z, y : [batch][seqlen][d_inner] io dtype (z optional)
+ *   x, r, i, z    : [batch][seqlen] rows of d_inner io values, ld >= d_inner
+ *                   apart (z optional): with ld > d_inner column slices of one
+ *                   wider tensor (a projection that gives all four), which need
+ *                   no alignment beyond their element's
+ *   y             : [batch][seqlen][d_inner] io dtype
  *   lam           : [d_inner] fp32
  *   sharpness     : > 0 and finite (MS_ERR_SHAPE otherwise)
  *   reset         : [batch][seqlen] bytes, optional.  A nonzero byte starts a
@@ -366,37 +370,39 @@ ms_status ms_conv1d_silu(const void* x, const float* weight, const float* bias,
  *   workspace     : ms_gated_scan_workspace_bytes bytes (may be 0), 16-byte
  *                   aligned, no initialisation needed.
  * batch, seqlen, d_inner and io as in ms_dims (MS_ERR_UNSUPPORTED where a
- * launch would need more than 2^24 - 1 workgroups).  The state, the decay and the
- * gates are fp32; y is rounded once.  Deterministic.
+ * launch would need more than 2^24 - 1 workgroups, or rows of ld values are 2^24
+ * bytes or more).  The state, the decay and the gates are fp32; y is rounded
+ * once.  Deterministic.
  *
  * ms_gated_scan_bwd: gradients for dy and, optionally, dh_last ([batch]
  *   [d_inner] fp32), from the same inputs and the states the forward saved
- *   (h0 is in them).  dx, dr, di, dz in the io dtype (dz required with z),
+ *   (h0 is in them).  dy, dx, dr, di, dz [batch][seqlen][d_inner] in the io dtype
+ *   (dz required with z),
  *   dlam [d_inner] fp32 (sum over batch and time), dh0 [batch][d_inner] fp32
  *   (optional).  No gradient crosses a reset.  The derivative of
  *   sqrt(1 - a^2) is taken together with that of a, and stays finite where a
  *   tends to 1.  Outputs must not overlap inputs.
  * ms_gated_step: one timestep; h [batch][d_inner] fp32 is updated in place;
- *   x_t, r_t, i_t, z_t, y_t [batch][d_inner].
+ *   x_t, r_t, i_t, z_t [batch] rows ld apart, y_t [batch][d_inner].
  */
 size_t ms_gated_scan_workspace_bytes(int32_t batch, int64_t seqlen, int32_t d_inner, int32_t io);
 size_t ms_gated_scan_states_bytes(int32_t batch, int64_t seqlen, int32_t d_inner);
 ms_status ms_gated_scan_fwd(const void* x, const void* r, const void* i, const float* lam,
                             float sharpness, const void* z, const uint8_t* reset, void* y,
                             const float* h0, float* h_last, float* states, int32_t batch,
-                            int64_t seqlen, int32_t d_inner, int32_t io, void* workspace,
-                            size_t workspace_bytes, void* stream);
+                            int64_t seqlen, int32_t d_inner, int64_t ld, int32_t io,
+                            void* workspace, size_t workspace_bytes, void* stream);
 size_t ms_gated_scan_bwd_workspace_bytes(int32_t batch, int64_t seqlen, int32_t d_inner,
                                          int32_t io);
 ms_status ms_gated_scan_bwd(const void* x, const void* r, const void* i, const float* lam,
                             float sharpness, const void* z, const uint8_t* reset,
                             const float* states, const void* dy, const float* dh_last, void* dx,
                             void* dr, void* di, void* dz, float* dlam, float* dh0, int32_t batch,
-                            int64_t seqlen, int32_t d_inner, int32_t io, void* workspace,
-                            size_t workspace_bytes, void* stream);
+                            int64_t seqlen, int32_t d_inner, int64_t ld, int32_t io,
+                            void* workspace, size_t workspace_bytes, void* stream);
 ms_status ms_gated_step(float* h, const void* x_t, const void* r_t, const void* i_t,
                         const float* lam, float sharpness, const void* z_t, void* y_t,
-                        int32_t batch, int32_t d_inner, int32_t io, void* stream);
+                        int32_t batch, int32_t d_inner, int64_t ld, int32_t io, void* stream);
 
 /*
  * Embedding lookup with scaling, and the gradient of its table:

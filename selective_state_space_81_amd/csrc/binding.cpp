@@ -45,6 +45,43 @@ PyObject* io(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// rows(x, dims, *ts): 2 ld + io code, where x is a device tensor of dims
+// dimensions and MS_F32 or MS_BF16, whose rows (the last dimension) are
+// contiguous and ld apart, in order, and each of ts is None or has the same
+// dtype, sizes, device and ld; -1 of anything else.
+int64_t row_pitch(const at::Tensor& t) {
+    const int64_t dims = t.dim(), d = t.size(dims - 1);
+    if (d > 1 && t.stride(dims - 1) != 1) return -1;
+    if (t.numel() == 0) return d;
+    int64_t ld = 0, want = 0;
+    for (int64_t k = dims - 2; k >= 0; --k) {
+        if (t.size(k) == 1) continue;
+        if (!ld) ld = want = t.stride(k);
+        if (t.stride(k) != want) return -1;
+        want *= t.size(k);
+    }
+    if (!ld) return d;
+    return ld >= d ? ld : -1;
+}
+PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const at::Tensor* x = n >= 2 ? tensor_of(a[0]) : nullptr;
+    if (!x || !x->is_cuda() || x->layout() != at::kStrided || x->dim() != PyLong_AsLong(a[1]) ||
+        (x->scalar_type() != at::kFloat && x->scalar_type() != at::kBFloat16))
+        return PyLong_FromLong(-1);
+    const int64_t ld = row_pitch(*x);
+    bool ok = ld >= 0;
+    for (Py_ssize_t k = 2; ok && k < n; ++k) {
+        if (a[k] == Py_None) continue;
+        const at::Tensor* t = tensor_of(a[k]);
+        ok = t && t->layout() == at::kStrided && t->scalar_type() == x->scalar_type() &&
+             t->sizes() == x->sizes() && t->device() == x->device() && row_pitch(*t) == ld;
+    }
+    const int64_t io = x->scalar_type() == at::kFloat ? MS_F32 : MS_BF16;
+    return PyLong_FromLongLong(ok ? 2 * ld + io : -1);
+    END_HANDLE_TH_ERRORS
+}
+
 // like(x, *ts): each of ts is None or a contiguous tensor of x's dtype, shape
 // and device.
 PyObject* like(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -217,7 +254,7 @@ PyObject* bind(PyObject*, PyObject* args) {
 
 #define METHOD_(name) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr},
-PyMethodDef methods[] = {METHOD_(io) METHOD_(like) METHOD_(fits) METHOD_(empty) METHOD_(together)
+PyMethodDef methods[] = {METHOD_(io) METHOD_(rows) METHOD_(like) METHOD_(fits) METHOD_(empty) METHOD_(together)
                          ENTRIES_(METHOD_)
                          {"bind", bind, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

@@ -177,7 +177,8 @@ template <class G>
 struct Lane {
     int lane, wave, rg, lc, b, ch;
     bool live;    // the lane's channels exist
-    uint32_t chb, rowb;  // byte offset of the lane's channels, bytes of a row
+    uint32_t chb;        // byte offset of the lane's channels
+    uint32_t rowb, inb;  // bytes from one row to the next: of x, r, i and z inb
     __device__ __forceinline__ Lane(const GatedArgs& a, uint32_t chain) {
         lane = threadIdx.x & 63;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -193,19 +194,19 @@ struct Lane {
         ch = min(ch, a.Dn - G::VEC);
         constexpr int E = G::BF16 ? 2 : 4;
         chb = (uint32_t)ch * E;
-        rowb = (uint32_t)a.Dn * E;  // below 2^24 (the entry points check d_inner)
+        rowb = (uint32_t)a.Dn * E;  // both below 2^24 (the entry points check)
+        inb = (uint32_t)a.ld * E;
     }
     // Byte offset of the lane's step j within its wave's TW steps, of which
-    // `left` exist (reads past them repeat the last one).
-    __device__ __forceinline__ uint32_t at(int j, int left) const {
-        return __umul24((uint32_t)min(rg * G::TAU + j, left - 1), rowb) + chb;
+    // `left` exist (reads past them repeat the last one), in rows `pitch` apart.
+    __device__ __forceinline__ uint32_t at(int j, int left, uint32_t pitch) const {
+        return __umul24((uint32_t)min(rg * G::TAU + j, left - 1), pitch) + chb;
     }
     // Address of step t of the wave's batch row (wave-uniform).
-    __device__ __forceinline__ const char* row(const GatedArgs& a, const void* p, int64_t t) const {
-        return static_cast<const char*>(p) + ((int64_t)b * a.L + t) * rowb;
-    }
-    __device__ __forceinline__ char* row(const GatedArgs& a, void* p, int64_t t) const {
-        return static_cast<char*>(p) + ((int64_t)b * a.L + t) * rowb;
+    template <class P>
+    __device__ __forceinline__ auto row(const GatedArgs& a, P* p, int64_t t, uint32_t pitch) const {
+        typedef typename std::conditional<std::is_const<P>::value, const char, char>::type C;
+        return static_cast<C*>(p) + ((int64_t)b * a.L + t) * pitch;
     }
 };
 
@@ -377,9 +378,9 @@ __global__ void __launch_bounds__(64 * G::W, G::BF16 ? 3 : 2) gated_fwd(GatedArg
 
     T rx[TAU], rr[TAU], ri[TAU], rz[TAU];
     auto load = [&](const void* p, T(&w)[TAU]) {
-        const char* q = g.row(a, p, pl.tr);
+        const char* q = g.row(a, p, pl.tr, g.inb);
 #pragma unroll
-        for (int j = 0; j < TAU; ++j) w[j] = ld_row<R>(q, g.at(j, pl.left));
+        for (int j = 0; j < TAU; ++j) w[j] = ld_row<R>(q, g.at(j, pl.left, g.inb));
     };
     load(a.r, rr);
     load(a.i, ri);
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(64 * G::W, G::BF16 ? 3 : 2) gated_fwd(GatedArg
 #pragma unroll
             for (int c = 0; c < VEC; ++c) st[c] = h[c];
         }
-        char* py = g.row(a, a.y, pl.tw);
+        char* py = g.row(a, a.y, pl.tw, g.rowb);
 #pragma unroll
         for (int j = 0; j < TAU; ++j) {
             float o[VEC];
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(64 * G::W, G::BF16 ? 3 : 2) gated_fwd(GatedArg
 #pragma unroll
                 for (int c = 0; c < VEC; ++c) o[c] *= silu_f(z[c]);
             }
-            if (j < mine) st_row<R>(py, g.at(j, pl.left), R::pack(o));
+            if (j < mine) st_row<R>(py, g.at(j, pl.left, g.rowb), R::pack(o));
         }
     }
 }
@@ -525,20 +526,20 @@ __global__ void __launch_bounds__(64 * G::W, 3) gated_bwd(GatedArgs a) {
     const int left = pl.left, mine = pl.mine(g);
 
     T rx[TAU], rr[TAU], ri[TAU], rz[TAU], ry[TAU];
-    auto load = [&](const void* p, T(&w)[TAU]) {
-        const char* q = g.row(a, p, tr);
+    auto load = [&](const void* p, T(&w)[TAU], uint32_t pitch) {
+        const char* q = g.row(a, p, tr, pitch);
 #pragma unroll
-        for (int j = 0; j < TAU; ++j) w[j] = ld_row<R>(q, g.at(j, left));
+        for (int j = 0; j < TAU; ++j) w[j] = ld_row<R>(q, g.at(j, left, pitch));
     };
-    load(a.r, rr);
-    load(a.i, ri);
-    load(a.x, rx);
+    load(a.r, rr, g.inb);
+    load(a.i, ri, g.inb);
+    load(a.x, rx, g.inb);
     float h[VEC];
     const float* st = a.states + ((int64_t)g.b * a.nstates + tr / kGatedBlock) * a.Dn + g.ch;
 #pragma unroll
     for (int c = 0; c < VEC; ++c) h[c] = st[c];
-    load(a.dy, ry);
-    if constexpr (GATE) load(a.z, rz);
+    load(a.dy, ry, g.rowb);
+    if constexpr (GATE) load(a.z, rz, g.inb);
     share_rates<G>(a, chain, s_k);
     if (pl.ragged) {  // no gradient arrives at steps past the end either
         pad_steps<R, TAU>(mine, rr, rx);
@@ -597,7 +598,7 @@ __global__ void __launch_bounds__(64 * G::W, 3) gated_bwd(GatedArgs a) {
     }
     // h_{t-1} of every step, dz, and the gradient arriving at h_t from y_t
     float gh[TAU][VEC];
-    char* oz = g.row(a, a.dz, tw);
+    char* oz = g.row(a, a.dz, tw, g.rowb);
 #pragma unroll
     for (int j = 0; j < TAU; ++j) {
         const bool in = j < mine;
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(64 * G::W, 3) gated_bwd(GatedArgs a) {
                 dz[c] = dy[c] * h[c] * sz * fmaf(z[c], 1.f - sz, 1.f);
                 gh[j][c] *= z[c] * sz;
             }
-            if (g.live && in) st_row<R>(oz, g.at(j, left), R::pack(dz));
+            if (g.live && in) st_row<R>(oz, g.at(j, left, g.rowb), R::pack(dz));
         }
         __builtin_amdgcn_sched_barrier(0);
     }
@@ -698,7 +699,8 @@ __global__ void __launch_bounds__(64 * G::W, 3) gated_bwd(GatedArgs a) {
     }
 #pragma unroll
     for (int c = 0; c < VEC; ++c) m[c] = apply<RESET>(P[c], m[c], C[c]);
-    char *ox = g.row(a, a.dx, tw), *orr = g.row(a, a.dr, tw), *oi = g.row(a, a.di, tw);
+    char *ox = g.row(a, a.dx, tw, g.rowb), *orr = g.row(a, a.dr, tw, g.rowb),
+         *oi = g.row(a, a.di, tw, g.rowb);
 #pragma unroll
     for (int j = TAU - 1; j >= 0; --j) {
         const bool in = j < mine;
@@ -718,7 +720,7 @@ __global__ void __launch_bounds__(64 * G::W, 3) gated_bwd(GatedArgs a) {
             dlam[c] += q;
         }
         if (g.live && in) {
-            const uint32_t o = g.at(j, left);
+            const uint32_t o = g.at(j, left, g.rowb);
             st_row<R>(ox, o, R::pack(dx));
             st_row<R>(orr, o, R::pack(dr));
             st_row<R>(oi, o, R::pack(di));
@@ -792,12 +794,16 @@ __global__ void __launch_bounds__(256) gated_step(GatedArgs a) {
     T x[BR], r[BR], i[BR], z[BR];
 #pragma unroll
     for (int k = 0; k < BR; ++k) {
-        const int64_t at = (int64_t)min(row0 + k, a.batch - 1) * vecs + v;
-        h[k] = reinterpret_cast<const F*>(a.h_last)[at];
-        r[k] = static_cast<const T*>(a.r)[at];
-        i[k] = static_cast<const T*>(a.i)[at];
-        x[k] = static_cast<const T*>(a.x)[at];
-        if (a.z) z[k] = static_cast<const T*>(a.z)[at];
+        const int64_t row = min(row0 + k, a.batch - 1);
+        h[k] = reinterpret_cast<const F*>(a.h_last)[row * vecs + v];
+        auto in = [&](const void* p) {
+            return *reinterpret_cast<const typename R::M*>(static_cast<const typename R::E*>(p) +
+                                                           row * a.ld + v * VEC);
+        };
+        r[k] = in(a.r);
+        i[k] = in(a.i);
+        x[k] = in(a.x);
+        if (a.z) z[k] = in(a.z);
     }
     float rate[VEC];
 #pragma unroll

@@ -26,6 +26,7 @@ ms_status fail(ms_status s, const char* fmt, ...) {
 }
 
 constexpr int64_t kMax31 = 0x7fffffffLL;
+constexpr int64_t kMaxRowBytes = (1 << 24) - 1;  // of the gated scan: offsets are 24-bit products
 
 ms_status check_aligned(std::initializer_list<const void*> ptrs) {
     for (const void* p : ptrs)
@@ -84,6 +85,20 @@ ms_status check_sharpness(float c) {
     return MS_OK;
 }
 
+// Rows of x, r, i and z, `most` bytes long at the most, and their alignment.
+ms_status check_rows(int32_t d_inner, int64_t ld, int32_t io, int64_t most,
+                     std::initializer_list<const void*> ptrs) {
+    const int64_t e = io == MS_BF16 ? 2 : 4;
+    if (ld < d_inner) return fail(MS_ERR_SHAPE, "ld=%lld is below d_inner", (long long)ld);
+    if (ld > most / e)
+        return fail(MS_ERR_UNSUPPORTED, "rows of ld=%lld values are too long", (long long)ld);
+    if (ld == d_inner) return check_aligned(ptrs);
+    for (const void* p : ptrs)
+        if (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(e - 1))
+            return fail(MS_ERR_ALIGN, "pointer %p is not aligned to its element", p);
+    return MS_OK;
+}
+
 int64_t state_rows(int64_t seqlen) { return (seqlen + kGatedBlock - 1) / kGatedBlock; }
 
 // ---- embedding -------------------------------------------------------------------
@@ -135,22 +150,22 @@ size_t ms_gated_scan_states_bytes(int32_t batch, int64_t seqlen, int32_t d_inner
 ms_status ms_gated_scan_fwd(const void* x, const void* r, const void* i, const float* lam,
                             float sharpness, const void* z, const uint8_t* reset, void* y,
                             const float* h0, float* h_last, float* states, int32_t batch,
-                            int64_t seqlen, int32_t d_inner, int32_t io, void* workspace,
-                            size_t workspace_bytes, void* stream) {
+                            int64_t seqlen, int32_t d_inner, int64_t ld, int32_t io,
+                            void* workspace, size_t workspace_bytes, void* stream) {
     clear_error();
     ms_status st = check_gated(batch, seqlen, d_inner, io);
     if (st != MS_OK) return st;
     if ((st = check_sharpness(sharpness)) != MS_OK) return st;
     if (!x || !r || !i || !lam || !y) return fail(MS_ERR_NULL, "x, r, i, lam and y are required");
-    if ((st = check_aligned({x, r, i, lam, z, reset, y, h0, h_last, states, workspace})) != MS_OK)
-        return st;
+    if ((st = check_rows(d_inner, ld, io, kMaxRowBytes, {x, r, i, z})) != MS_OK) return st;
+    if ((st = check_aligned({lam, reset, y, h0, h_last, states, workspace})) != MS_OK) return st;
     if ((st = check_workspace(ms_gated_scan_workspace_bytes(batch, seqlen, d_inner, io), workspace,
                               workspace_bytes)) != MS_OK)
         return st;
     GatedArgs a{};
     a.x = x; a.r = r; a.i = i; a.z = z; a.lam = lam; a.reset = reset; a.h0 = h0; a.y = y;
     a.h_last = h_last; a.states = states; a.sharp = sharpness; a.L = seqlen;
-    a.nstates = state_rows(seqlen); a.batch = batch; a.Dn = d_inner;
+    a.nstates = state_rows(seqlen); a.batch = batch; a.Dn = d_inner; a.ld = ld;
     prof_call();
     return launched(launch_gated_fwd(a, io == MS_BF16, workspace, static_cast<hipStream_t>(stream)));
 }
@@ -165,8 +180,8 @@ ms_status ms_gated_scan_bwd(const void* x, const void* r, const void* i, const f
                             float sharpness, const void* z, const uint8_t* reset,
                             const float* states, const void* dy, const float* dh_last, void* dx,
                             void* dr, void* di, void* dz, float* dlam, float* dh0, int32_t batch,
-                            int64_t seqlen, int32_t d_inner, int32_t io, void* workspace,
-                            size_t workspace_bytes, void* stream) {
+                            int64_t seqlen, int32_t d_inner, int64_t ld, int32_t io,
+                            void* workspace, size_t workspace_bytes, void* stream) {
     clear_error();
     ms_status st = check_gated(batch, seqlen, d_inner, io);
     if (st != MS_OK) return st;
@@ -174,8 +189,9 @@ ms_status ms_gated_scan_bwd(const void* x, const void* r, const void* i, const f
     if (!x || !r || !i || !lam || !states || !dy || !dx || !dr || !di || !dlam)
         return fail(MS_ERR_NULL, "x, r, i, lam, states, dy, dx, dr, di and dlam are required");
     if (z && !dz) return fail(MS_ERR_NULL, "dz is required when z is given");
-    if ((st = check_aligned({x, r, i, lam, z, reset, states, dy, dh_last, dx, dr, di, dz, dlam,
-                             dh0, workspace})) != MS_OK)
+    if ((st = check_rows(d_inner, ld, io, kMaxRowBytes, {x, r, i, z})) != MS_OK) return st;
+    if ((st = check_aligned({lam, reset, states, dy, dh_last, dx, dr, di, dz, dlam, dh0,
+                             workspace})) != MS_OK)
         return st;
     if ((st = check_workspace(ms_gated_scan_bwd_workspace_bytes(batch, seqlen, d_inner, io),
                               workspace, workspace_bytes)) != MS_OK)
@@ -185,24 +201,26 @@ ms_status ms_gated_scan_bwd(const void* x, const void* r, const void* i, const f
     a.states = const_cast<float*>(states);  // only read
     a.dh_last = dh_last; a.dx = dx; a.dr = dr; a.di = di; a.dz = dz; a.dlam = dlam; a.dh0 = dh0;
     a.sharp = sharpness; a.L = seqlen;
-    a.nstates = state_rows(seqlen); a.batch = batch; a.Dn = d_inner;
+    a.nstates = state_rows(seqlen); a.batch = batch; a.Dn = d_inner; a.ld = ld;
     prof_call();
     return launched(launch_gated_bwd(a, io == MS_BF16, workspace, static_cast<hipStream_t>(stream)));
 }
 
 ms_status ms_gated_step(float* h, const void* x_t, const void* r_t, const void* i_t,
                         const float* lam, float sharpness, const void* z_t, void* y_t,
-                        int32_t batch, int32_t d_inner, int32_t io, void* stream) {
+                        int32_t batch, int32_t d_inner, int64_t ld, int32_t io, void* stream) {
     clear_error();
     ms_status st = check_gated_sizes(batch, 1, d_inner, io);
     if (st != MS_OK) return st;
     if ((st = check_sharpness(sharpness)) != MS_OK) return st;
     if (!h || !x_t || !r_t || !i_t || !lam || !y_t)
         return fail(MS_ERR_NULL, "h, x_t, r_t, i_t, lam and y_t are required");
-    if ((st = check_aligned({h, x_t, r_t, i_t, lam, z_t, y_t})) != MS_OK) return st;
+    if ((st = check_rows(d_inner, ld, io, (int64_t)1 << 40, {x_t, r_t, i_t, z_t})) != MS_OK)
+        return st;
+    if ((st = check_aligned({h, lam, y_t})) != MS_OK) return st;
     GatedArgs a{};
     a.x = x_t; a.r = r_t; a.i = i_t; a.z = z_t; a.lam = lam; a.h_last = h; a.y = y_t;
-    a.sharp = sharpness; a.L = 1; a.batch = batch; a.Dn = d_inner;
+    a.sharp = sharpness; a.L = 1; a.batch = batch; a.Dn = d_inner; a.ld = ld;
     if (gated_step_workgroups(a) > kMaxGroups)
         return fail(MS_ERR_UNSUPPORTED, "batch x d_inner needs more than 2^24-1 workgroups");
     prof_call();

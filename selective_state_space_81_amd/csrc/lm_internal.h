@@ -18,7 +18,7 @@ constexpr int64_t kMaxGroups = (1 << 24) - 1;
 constexpr int kGatedBlock = 16;
 
 struct GatedArgs {
-    const void* x;
+    const void* x;  // x, r, i, z: rows `ld` values apart
     const void* r;
     const void* i;
     const void* z;         // or null
@@ -46,6 +46,7 @@ struct GatedArgs {
     float sharp;
     int64_t L;
     int64_t nstates;  // ceil(L / kGatedBlock)
+    int64_t ld;
     int batch;
     int Dn;
 };

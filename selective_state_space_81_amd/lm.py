@@ -34,11 +34,11 @@ def declare(lib) -> None:
             ("ms_gated_scan_workspace_bytes", sz, [i32, i64, i32, i32]),
             ("ms_gated_scan_states_bytes", sz, [i32, i64, i32]),
             ("ms_gated_scan_fwd", ctypes.c_int,
-             [vp] * 4 + [f32] + [vp] * 6 + [i32, i64, i32, i32, vp, sz, vp]),
+             [vp] * 4 + [f32] + [vp] * 6 + [i32, i64, i32, i64, i32, vp, sz, vp]),
             ("ms_gated_scan_bwd_workspace_bytes", sz, [i32, i64, i32, i32]),
             ("ms_gated_scan_bwd", ctypes.c_int,
-             [vp] * 4 + [f32] + [vp] * 11 + [i32, i64, i32, i32, vp, sz, vp]),
-            ("ms_gated_step", ctypes.c_int, [vp] * 5 + [f32, vp, vp, i32, i32, i32, vp]),
+             [vp] * 4 + [f32] + [vp] * 11 + [i32, i64, i32, i64, i32, vp, sz, vp]),
+            ("ms_gated_step", ctypes.c_int, [vp] * 5 + [f32, vp, vp, i32, i32, i64, i32, vp]),
             ("ms_embed_fwd", ctypes.c_int, [vp, i32, vp, f32, vp, i64, i64, i32, i32, vp]),
             ("ms_embed_bwd_workspace_bytes", sz, [i64, i64, i32, i32]),
             ("ms_embed_bwd", ctypes.c_int,
@@ -147,16 +147,30 @@ def _size(n: int, what: str) -> int:
 
 # ---- gated linear recurrence -------------------------------------------------------------
 
+def _refuse_rows(dims, text, **given):
+    """What is wrong with the tensors whose rows have one distance (x first)."""
+    name, x = next(iter(given.items()))
+    if not getattr(x, "is_cuda", False) or x.dim() != dims:
+        raise ValueError(f"{name} must be a {text} device tensor")
+    ms._io(x)
+    for k, t in given.items():
+        if t is None and k[0] != "z":
+            raise ValueError(f"{k} is required")
+    _refuse(x.device, x.dtype, x.shape, **given)
+    raise ValueError(f"{', '.join(given)} must be contiguous, or slices of rows that are as far "
+                     "apart in one as in the other")
+
+
 def _chk_gated(m, x, r, i, lam, z, reset):
-    """Checks of the arguments both passes share; (shape, io, reset)."""
+    """Checks of the arguments both passes share; (shape, ld, io, reset)."""
     import torch
-    io = _io_of(m, x, "x", 3, "[batch, L, d_inner]")
+    code = m.rows(x, 3, r, i, z)
+    if code < 0 or r is None or i is None:
+        _refuse_rows(3, "[batch, L, d_inner]", x=x, r=r, i=i, z=z)
+    ld, io = code >> 1, code & 1
     shape = x.shape
-    for t, name in ((r, "r"), (i, "i"), (lam, "lam")):
-        if t is None:
-            raise ValueError(f"{name} is required")
-    if not m.like(x, r, i, z):
-        _refuse(x.device, x.dtype, shape, r=r, i=i, z=z)
+    if lam is None:
+        raise ValueError("lam is required")
     if not m.fits(x, torch.float32, (shape[2],), lam):
         _refuse(x.device, torch.float32, shape[2:], lam=lam)
     if reset is not None:
@@ -164,7 +178,7 @@ def _chk_gated(m, x, r, i, lam, z, reset):
             reset = reset.view(torch.uint8)
         if not m.fits(x, torch.uint8, (shape[0], shape[1]), reset):
             _refuse(x.device, torch.uint8, shape[:2], reset=reset)
-    return shape, io, reset
+    return shape, ld, io, reset
 
 
 @functools.lru_cache(maxsize=1024)
@@ -186,7 +200,8 @@ def gated_scan_states(x, stream=None):
     gated_scan_bwd: [batch, ceil(L / 16), d_inner] fp32."""
     import torch
     m = _marshal()
-    _io_of(m, x, "x", 3, "[batch, L, d_inner]")
+    if m.rows(x, 3) < 0:
+        _refuse_rows(3, "[batch, L, d_inner]", x=x)
     b, L, d = x.shape
     return _Call(m, x, stream).empty(torch.float32, b, -(-L // GATED_BLOCK), d)
 
@@ -197,24 +212,26 @@ def gated_scan_fwd(x, r, i, lam, z=None, *, c=8.0, reset=None, y=None, h0=None, 
     of x [batch, L, d] with decay gate r, input gate i (pre-activations), rate
     lam [d] and sharpness c, optionally gated by silu(z).  reset [batch, L]
     (uint8 or bool) starts new sequences; states (gated_scan_states) receives
-    what the backward needs.  Allocates y (and the workspace) when not given.
+    what the backward needs.  x, r, i and z are contiguous, or column slices of
+    one wider tensor (their rows as far apart in one as in the other).  Allocates y (and the workspace) when not given.
     Returns y."""
     import torch
     m = _marshal()
-    shape, io, reset = _chk_gated(m, x, r, i, lam, z, reset)
+    shape, ld, io, reset = _chk_gated(m, x, r, i, lam, z, reset)
     b, L, d = shape
     f32 = torch.float32
     if not m.fits(x, f32, (b, d), h0, h_last):
         _refuse(x.device, f32, (b, d), h0=h0, h_last=h_last)
     if not m.fits(x, f32, (b, -(-L // GATED_BLOCK), d), states):
         _refuse(x.device, f32, (b, -(-L // GATED_BLOCK), d), states=states)
-    if not m.like(x, y):
+    if y is not None and not m.fits(x, x.dtype, (b, L, d), y):
         _refuse(x.device, x.dtype, shape, y=y)
     call = _Call(m, x, stream)
     if y is None:
         y = call.empty(x.dtype, b, L, d)
     ws, wn = call.workspace(workspace, gated_scan_workspace_bytes(b, L, d, io))
-    call.run(m.gated_scan_fwd, x, r, i, lam, c, z, reset, y, h0, h_last, states, b, L, d, io, ws, wn)
+    call.run(m.gated_scan_fwd, x, r, i, lam, c, z, reset, y, h0, h_last, states, b, L, d, ld, io,
+             ws, wn)
     return y
 
 
@@ -225,7 +242,7 @@ def gated_scan_bwd(x, r, i, lam, dy, states, z=None, *, c=8.0, reset=None, dh_la
     dx, dr, di, dz (io dtype; dz None without z), dlam and dh0 (fp32)."""
     import torch
     m = _marshal()
-    shape, io, reset = _chk_gated(m, x, r, i, lam, z, reset)
+    shape, ld, io, reset = _chk_gated(m, x, r, i, lam, z, reset)
     b, L, d = shape
     f32, dt = torch.float32, x.dtype
     if states is None:
@@ -234,7 +251,7 @@ def gated_scan_bwd(x, r, i, lam, dy, states, z=None, *, c=8.0, reset=None, dh_la
         raise ValueError("dy is required")
     if not m.fits(x, f32, (b, -(-L // GATED_BLOCK), d), states):
         _refuse(x.device, f32, (b, -(-L // GATED_BLOCK), d), states=states)
-    if not m.like(x, dy):
+    if not m.fits(x, dt, (b, L, d), dy):
         _refuse(x.device, dt, shape, dy=dy)
     if not m.fits(x, f32, (b, d), dh_last):
         _refuse(x.device, f32, (b, d), dh_last=dh_last)
@@ -245,23 +262,26 @@ def gated_scan_bwd(x, r, i, lam, dy, states, z=None, *, c=8.0, reset=None, dh_la
     out["dh0"] = call.empty(f32, b, d) if want_dh0 else None
     ws, wn = call.workspace(workspace, gated_scan_bwd_workspace_bytes(b, L, d, io))
     call.run(m.gated_scan_bwd, x, r, i, lam, c, z, reset, states, dy, dh_last, out["dx"], out["dr"],
-             out["di"], out["dz"], out["dlam"], out["dh0"], b, L, d, io, ws, wn)
+             out["di"], out["dz"], out["dlam"], out["dh0"], b, L, d, ld, io, ws, wn)
     return out
 
 
 def gated_step(h, x_t, r_t, i_t, lam, z_t=None, *, c=8.0, y_t=None, stream=None):
     """ms_gated_step on torch device tensors: one step of the recurrence for
-    x_t [batch, d]; h [batch, d] fp32 is updated in place.  Returns y_t."""
+    x_t [batch, d]; h [batch, d] fp32 is updated in place.  x_t, r_t, i_t and z_t
+    may be column slices of one wider tensor.  Returns y_t."""
     import torch
     m = _marshal()
-    io = _io_of(m, x_t, "x_t", 2, "[batch, d_inner]")
+    code = m.rows(x_t, 2, r_t, i_t, z_t)
+    if code < 0 or r_t is None or i_t is None:
+        _refuse_rows(2, "[batch, d_inner]", x_t=x_t, r_t=r_t, i_t=i_t, z_t=z_t)
     b, d = x_t.shape
     f32 = torch.float32
-    for t, name in ((h, "h"), (r_t, "r_t"), (i_t, "i_t"), (lam, "lam")):
+    for t, name in ((h, "h"), (lam, "lam")):
         if t is None:
             raise ValueError(f"{name} is required")
-    if not m.like(x_t, r_t, i_t, z_t, y_t):
-        _refuse(x_t.device, x_t.dtype, (b, d), r_t=r_t, i_t=i_t, z_t=z_t, y_t=y_t)
+    if y_t is not None and not m.fits(x_t, x_t.dtype, (b, d), y_t):
+        _refuse(x_t.device, x_t.dtype, (b, d), y_t=y_t)
     if not m.fits(x_t, f32, (b, d), h):
         _refuse(x_t.device, f32, (b, d), h=h)
     if not m.fits(x_t, f32, (d,), lam):
@@ -269,7 +289,7 @@ def gated_step(h, x_t, r_t, i_t, lam, z_t=None, *, c=8.0, y_t=None, stream=None)
     call = _Call(m, x_t, stream)
     if y_t is None:
         y_t = call.empty(x_t.dtype, b, d)
-    call.run(m.gated_step, h, x_t, r_t, i_t, lam, c, z_t, y_t, b, d, io)
+    call.run(m.gated_step, h, x_t, r_t, i_t, lam, c, z_t, y_t, b, d, code >> 1, code & 1)
     return y_t
 
 
@@ -457,7 +477,7 @@ def _functions():
         @staticmethod
         def backward(ctx, dy, dh_last):
             x, r, i, lam, z, states, reset = ctx.saved_tensors
-            dy = torch.zeros_like(x) if dy is None else dy.contiguous()
+            dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
             if dh_last is not None:
                 dh_last = dh_last.contiguous()
             g = gated_scan_bwd(x, r, i, lam, dy, states, z, c=ctx.c, reset=reset,

@@ -251,6 +251,43 @@ def test_autograd(gpu):
         ref.assert_close(t[k].grad, w, ref.grad_bound(w, "f32"), k)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d,off,ld", [(64, 0, 320), (36, 3, 155), (33, 1, 140), (2, 1, 11), (8, 8, 41)])
+def test_slices_of_a_wider_tensor(gpu, io, d, off, ld):
+    """x, r, i and z as columns of one projection, at offsets of any alignment:
+    the same bits as from contiguous copies."""
+    s = inputs(3, 150, d, io, True, True, True, seed=d)
+    wide = torch.full((3, 150, ld), float("nan"), device=DEV).to(IO[io])
+    for k, name in enumerate(("x", "r", "i", "z")):
+        wide[:, :, off + k * d:off + (k + 1) * d] = s[name]
+    v = [wide[:, :, off + k * d:off + (k + 1) * d] for k in range(4)]
+    c = [s[k] for k in ("x", "r", "i", "z")]
+    out = []
+    for x, r, i, z in (c, v):
+        states, hl = gpu.gated_scan_states(x), torch.empty(3, d, device=DEV)
+        y = gpu.gated_scan_fwd(x, r, i, s["lam"], z, reset=s["reset"], h0=s["h0"], h_last=hl,
+                               states=states)
+        g = gpu.gated_scan_bwd(x, r, i, s["lam"], s["dy"], states, z, reset=s["reset"],
+                               dh_last=s["dh_last"])
+        h = s["h0"].clone()
+        yt = gpu.gated_step(h, x[:, 7], r[:, 7], i[:, 7], s["lam"], z[:, 7]) \
+            if x is v[0] else gpu.gated_step(h, *(t[:, 7].contiguous() for t in (x, r, i)),
+                                             s["lam"], z[:, 7].contiguous())
+        out.append([y, hl, states, h, yt] + [g[k] for k in sorted(g)])
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+    # one pitch for all
+    with pytest.raises(ValueError, match="contiguous"):
+        gpu.gated_scan_fwd(v[0], c[1], v[2], s["lam"])
+    # gradients reach the wider tensor
+    leaf = wide.nan_to_num().requires_grad_()
+    x, r, i, z = (leaf[:, :, off + k * d:off + (k + 1) * d] for k in range(4))
+    gpu.gated_scan(x, r, i, s["lam"], z, s["h0"], reset=s["reset"]).backward(s["dy"])
+    g = gpu.gated_scan_bwd(*c[:3], s["lam"], s["dy"], out[0][2], c[3], reset=s["reset"])
+    for k, name in enumerate(("dx", "dr", "di", "dz")):
+        assert torch.equal(leaf.grad[:, :, off + k * d:off + (k + 1) * d], g[name])
+
+
 def test_refusals(gpu):
     s = inputs(2, 10, 8, "f32", False, False, False)
     x, r, i, lam = s["x"], s["r"], s["i"], s["lam"]

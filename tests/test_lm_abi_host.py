@@ -33,27 +33,29 @@ def test_sizes():
 def test_gated_refusals():
     lib = ms.load()
 
-    def fwd(x=P, y=P, lam=P, c=8.0, h0=None, b=1, L=40, d=8, io=1):
-        return lib.ms_gated_scan_fwd(x, P, P, lam, c, None, None, y, h0, None, None, b, L, d, io,
-                                     P, 1 << 40, None)
+    def fwd(x=P, y=P, lam=P, c=8.0, h0=None, b=1, L=40, d=8, io=1, ld=None):
+        return lib.ms_gated_scan_fwd(x, P, P, lam, c, None, None, y, h0, None, None, b, L, d,
+                                     d if ld is None else ld, io, P, 1 << 40, None)
 
     assert fwd(x=None) == 1 and fwd(y=None) == 1 and fwd(lam=None) == 1
     assert fwd(b=0) == 2 and fwd(L=0) == 2 and fwd(d=0) == 2 and fwd(L=1 << 31) == 2
     assert fwd(io=2) == 3
     assert fwd(x=24) == 5 and fwd(h0=8) == 5
+    assert fwd(ld=7) == 2 and fwd(ld=1 << 23) == 7
+    assert fwd(ld=20, x=17) == 5 and fwd(ld=20, y=24) == 5  # only rows may lie off 16 bytes
     for c in (0.0, -2.0, float("inf"), float("nan")):
         assert fwd(c=c) == 2
     assert b"sharpness" in lib.ms_last_error()
 
     def bwd(z=None, dz=None, states=P, ws=P, n=1 << 40):
         return lib.ms_gated_scan_bwd(P, P, P, P, 8.0, z, None, states, P, None, P, P, P, dz, P,
-                                     None, 1, 40, 8, 1, ws, n, None)
+                                     None, 1, 40, 8, 8, 1, ws, n, None)
 
     assert bwd(states=None) == 1 and bwd(z=P) == 1
     assert bwd(ws=None) == 6 and bwd(n=8) == 6
-    assert lib.ms_gated_step(None, P, P, P, P, 8.0, None, P, 1, 8, 1, None) == 1
-    assert lib.ms_gated_step(P, P, P, P, P, 8.0, None, P, 0, 8, 1, None) == 2
-    assert lib.ms_gated_step(P, P, 20, P, P, 8.0, None, P, 1, 8, 1, None) == 5
+    assert lib.ms_gated_step(None, P, P, P, P, 8.0, None, P, 1, 8, 8, 1, None) == 1
+    assert lib.ms_gated_step(P, P, P, P, P, 8.0, None, P, 0, 8, 8, 1, None) == 2
+    assert lib.ms_gated_step(P, P, 20, P, P, 8.0, None, P, 1, 8, 8, 1, None) == 5
 
 
 def test_embed_refusals():
@@ -107,7 +109,7 @@ def test_launches_too_large():
     """A launch holds fewer than 2^24 workgroups of 256 threads."""
     lib = ms.load()
     # 65535 x 65539 channels, one by one
-    assert lib.ms_gated_step(P, P, P, P, P, 8.0, None, P, 65535, 65539, 1, None) == 7
+    assert lib.ms_gated_step(P, P, P, P, P, 8.0, None, P, 65535, 65539, 65539, 1, None) == 7
     assert lib.ms_gated_scan_workspace_bytes(65535, 1, 64 * 300, 1) == NONE
     assert b"2^24-1" in lib.ms_last_error()
     assert lib.ms_gated_scan_workspace_bytes(65535, 1, 64 * 200, 1) != NONE
@@ -138,7 +140,7 @@ def test_marshalling():
     """The binding's extension module on host tensors (it looks at no memory)."""
     m = ms.lm._marshal()
     x, f32 = torch.zeros(3, 4), torch.float32
-    assert m.io(x, 2) == -1  # not on a device
+    assert m.io(x, 2) == -1 and m.rows(x, 2) == -1  # not on a device
     assert m.like(x, None, torch.ones(3, 4)) and not m.like(x, torch.ones(4, 3))
     assert not m.like(x, torch.ones(4, 3).t()) and not m.like(x, x.double())
     assert not m.like(x, 7) and not m.like(None, x)
@@ -162,8 +164,8 @@ def test_marshalling():
     with pytest.raises(TypeError):
         m.gated_step(x)
     with pytest.raises(TypeError):
-        m.gated_step(x, x, x, x, x, "8", None, x, 3, 4, 0, 0)
+        m.gated_step(x, x, x, x, x, "8", None, x, 3, 4, 4, 0, 0)
     with pytest.raises(OverflowError):
-        m.gated_step(x, x, x, x, x, 8.0, None, x, 1 << 40, 4, 0, 0)
-    assert m.gated_step(x, x, x, x, x, 8.0, None, x, 0, 4, 0, 0) == 2  # MS_ERR_SHAPE
-    assert m.gated_step(None, x, x, x, x, 8.0, None, x, 3, 4, 0, None) == 1  # MS_ERR_NULL
+        m.gated_step(x, x, x, x, x, 8.0, None, x, 1 << 40, 4, 4, 0, 0)
+    assert m.gated_step(x, x, x, x, x, 8.0, None, x, 0, 4, 4, 0, 0) == 2  # MS_ERR_SHAPE
+    assert m.gated_step(None, x, x, x, x, 8.0, None, x, 3, 4, 4, 0, None) == 1  # MS_ERR_NULL
