@@ -78,7 +78,7 @@ def test_gradient(gpu, n, rows, dim, io):
     check_grad(gpu, ids, dy, rows, grad_dtype=torch.bfloat16)
 
 
-@pytest.mark.parametrize("n", [32, 33, 64, 100, 5000, 30000])
+@pytest.mark.parametrize("n", [32, 33, 64, 100, 127, 128, 129, 5000, 6144, 6145, 30000])
 def test_runs_across_workgroups(gpu, n):
     g = gen(n)
     dy = torch.randn(n, 20, generator=g, device=DEV)
@@ -188,6 +188,7 @@ def test_refusals(gpu):
         gpu.embed_bwd(ids, torch.zeros(4, 8, device=DEV), 10, grad_dtype=torch.float16)
     with pytest.raises(gpu.MsError):
         gpu.embed_bwd(ids, torch.zeros(4, 8, device=DEV), 0)
+    ids = torch.zeros(4000, dtype=torch.int64, device=DEV)  # a few need no workspace
     with pytest.raises(gpu.MsError, match="workspace"):
-        gpu.embed_bwd(ids, torch.zeros(4, 8, device=DEV), 10,
+        gpu.embed_bwd(ids, torch.zeros(4000, 8, device=DEV), 10,
                       workspace=torch.empty(16, dtype=torch.uint8, device=DEV))

@@ -71,8 +71,10 @@ def test_embed_refusals():
     assert fwd(w=8) == 5
     assert fwd(ids=None, n=0) == 0  # nothing to do, nothing launched
 
+    assert lib.ms_embed_bwd_workspace_bytes(5000, 10, 8, 0) > 0
+
     def bwd(ids=P, dw=P, gd=0, ws=P, n=1 << 40):
-        return lib.ms_embed_bwd(ids, 64, P, 1.0, -1, dw, gd, 5, 10, 8, 0, ws, n, None)
+        return lib.ms_embed_bwd(ids, 64, P, 1.0, -1, dw, gd, 5000, 10, 8, 0, ws, n, None)
 
     assert bwd(ids=None) == 1 and bwd(dw=None) == 1 and bwd(gd=5) == 3
     assert bwd(ws=None) == 6 and bwd(n=1) == 6 and bwd(ws=8) == 5
