@@ -82,22 +82,6 @@ PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// like(x, *ts): each of ts is None or a contiguous tensor of x's dtype, shape
-// and device.
-PyObject* like(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    HANDLE_TH_ERRORS
-    const at::Tensor* x = n ? tensor_of(a[0]) : nullptr;
-    bool ok = x != nullptr;
-    for (Py_ssize_t k = 1; ok && k < n; ++k) {
-        if (a[k] == Py_None) continue;
-        const at::Tensor* t = tensor_of(a[k]);
-        ok = t && t->scalar_type() == x->scalar_type() && t->sizes() == x->sizes() &&
-             t->device() == x->device() && t->is_contiguous();
-    }
-    return PyBool_FromLong(ok);
-    END_HANDLE_TH_ERRORS
-}
-
 // fits(x, dtype, sizes, *ts): each of ts is None or a contiguous tensor of
 // that dtype and those sizes on x's device.
 PyObject* fits(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -254,7 +238,7 @@ PyObject* bind(PyObject*, PyObject* args) {
 
 #define METHOD_(name) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr},
-PyMethodDef methods[] = {METHOD_(io) METHOD_(rows) METHOD_(like) METHOD_(fits) METHOD_(empty) METHOD_(together)
+PyMethodDef methods[] = {METHOD_(io) METHOD_(rows) METHOD_(fits) METHOD_(empty) METHOD_(together)
                          ENTRIES_(METHOD_)
                          {"bind", bind, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

@@ -118,12 +118,14 @@ class _Call:
             ms._check(rc)
 
 
-def _refuse(device, dtype, shape, **given):
+def _refuse(device, dtype, shape, rows=False, **given):
     """What is wrong with an argument that the extension's check refused: the
-    package's check of each, and its device."""
+    package's check of each (rows: it may be a slice), and its device."""
     for name, t in given.items():
         if t is not None:
-            ms._chk(t, name, dtype, tuple(shape))
+            if not (rows and getattr(t, "is_cuda", False) and t.dtype == dtype and
+                    t.shape == shape):
+                ms._chk(t, name, dtype, tuple(shape))
             if t.device != device:
                 raise ValueError(f"{name} is on {t.device}, not on {device}")
 
@@ -156,7 +158,7 @@ def _refuse_rows(dims, text, **given):
     for k, t in given.items():
         if t is None and k[0] != "z":
             raise ValueError(f"{k} is required")
-    _refuse(x.device, x.dtype, x.shape, **given)
+    _refuse(x.device, x.dtype, x.shape, rows=True, **given)
     raise ValueError(f"{', '.join(given)} must be contiguous, or slices of rows that are as far "
                      "apart in one as in the other")
 

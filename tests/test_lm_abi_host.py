@@ -143,9 +143,6 @@ def test_marshalling():
     m = ms.lm._marshal()
     x, f32 = torch.zeros(3, 4), torch.float32
     assert m.io(x, 2) == -1 and m.rows(x, 2) == -1  # not on a device
-    assert m.like(x, None, torch.ones(3, 4)) and not m.like(x, torch.ones(4, 3))
-    assert not m.like(x, torch.ones(4, 3).t()) and not m.like(x, x.double())
-    assert not m.like(x, 7) and not m.like(None, x)
     assert m.fits(x, torch.int32, (2,), None, torch.zeros(2, dtype=torch.int32))
     assert not m.fits(x, f32, (3,), x) and not m.fits(x, f32, (3, 5), x)
     assert not m.fits(x, f32, (4, 3), torch.zeros(3, 4).t())
