@@ -24,11 +24,10 @@
 //
 // What bounds it: bytes, with the arithmetic close behind (42 instructions an
 // element forward, 8 of them transcendental; 90 backward).  At 8 x 2048 x 1536
-// bf16 with the gate the forward moves 252 MB in 60 us (4.2 TB/s of the 5.6
-// that a copy reaches) and keeps the vector units busy for half of that; the
-// same without its arithmetic and without waiting for other blocks takes 57.
-// The backward moves 466 MB in 111 us.  One sequence of 131072 x 1536, no gate:
-// 1.61 GB in 346 us, of which 25 are waiting for the block before.
+// bf16 with the gate the forward moves 252 MB in 58 us (4.3 TB/s of the 5.6
+// that a copy reaches) and keeps the vector units busy for half of that.  The
+// backward moves 466 MB in 111 us.  One sequence of 131072 x 1536, no gate: 1.61
+// GB in 333 us, of which 25 are waiting for the block before.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -65,6 +64,34 @@ struct RowIo<4, true> {
         typedef __bf16 B __attribute__((ext_vector_type(4)));
         return __builtin_bit_cast(T, __builtin_convertvector((F{v[0], v[1], v[2], v[3]}), B));
     }
+};
+template <>
+struct RowIo<2, true> {
+    typedef uint16_t E;
+    typedef uint32_t T;
+    typedef T M __attribute__((aligned(2)));
+    static __device__ __forceinline__ T out() { return 0xff80ff80u; }
+    static __device__ __forceinline__ void unpack(T w, float (&v)[2]) {
+        v[0] = __uint_as_float(w << 16);
+        v[1] = __uint_as_float(w & 0xffff0000u);
+    }
+    static __device__ __forceinline__ T pack(const float (&v)[2]) {
+        typedef float F __attribute__((ext_vector_type(2)));
+        typedef __bf16 B __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(T, __builtin_convertvector((F{v[0], v[1]}), B));
+    }
+};
+template <>
+struct RowIo<2, false> {
+    typedef float E;
+    typedef float T __attribute__((ext_vector_type(2)));
+    typedef T M __attribute__((aligned(4)));
+    static __device__ __forceinline__ T out() {
+        const float f = -__builtin_inff();
+        return T{f, f};
+    }
+    static __device__ __forceinline__ void unpack(T w, float (&v)[2]) { v[0] = w[0], v[1] = w[1]; }
+    static __device__ __forceinline__ T pack(const float (&v)[2]) { return T{v[0], v[1]}; }
 };
 template <>
 struct RowIo<1, true> {
@@ -838,16 +865,18 @@ __global__ void __launch_bounds__(256) gated_step(GatedArgs a) {
 }
 
 // ---- variants -------------------------------------------------------------------------
-// 16 lanes of 4 channels take a line of 128 bytes of bf16 in each row.  As many
-// steps a lane as registers hold without spills (8 forward, 4 backward: 3 waves
-// a SIMD), since each lane's map costs a scan over the lanes.  The forward at 8
-// x 2048 x 1536 bf16 and at 131072 x 1536, in us: 60 and 346; 2 waves along time
-// 59 and 497, 8 waves 70 and 380, 4 steps a lane 67 and 473, 32 lanes across
-// channels 61 and 486 (shorter blocks make the chain of messages longer).  The
-// backward at the first: 112; 8 steps a lane (which spills) 151, 2 waves a SIMD
-// 127, 3 or 6 waves along time 115 and 170.
+// The lanes across channels take a line of 128 bytes of bf16 in each row.  As
+// many steps a lane as registers hold without spills (3 waves a SIMD), since
+// each lane's map costs a scan over the lanes: with 2 channels a lane instead of
+// 4 the forward has half as many lanes to scan over.  Forward at 8 x 2048 x 1536
+// bf16 with the gate and at 131072 x 1536 without, in us: 58 and 333; 4 channels x
+// 8 steps a lane 60 and 349 (with 2 waves along time 59 and 497, with 8 70 and
+// 380), 1 x 32 73 and 331, 2 x 8 56 and 391 (shorter blocks make the chain of
+// messages longer).  Backward at the first: 111; 2 channels x 8 steps 114, 1 x 16
+// 140, 4 x 8 (which spills) 151, 2 waves a SIMD 127, 3 or 6 waves along time 115
+// and 170.
 template <bool BF16>
-using Fwd = Geo<4, 16, 8, 4, BF16>;
+using Fwd = Geo<2, 32, 16, 4, BF16>;
 template <bool BF16>
 using Bwd = Geo<4, 16, 4, 4, BF16>;
 // fewer than four channels
@@ -922,11 +951,11 @@ int64_t gated_workgroups(int batch, int64_t L, int Dn, bool bf16) {
     return (int64_t)(n > m ? n : m);
 }
 
-// A channel count that four does not divide: some channels belong to two
-// lanes, maybe of two workgroups, and where h_last lies over h0 one may store
-// it before the other has read it.  Then h0 is copied first.
+// An odd channel count: one channel belongs to two lanes, maybe of two
+// workgroups, and where h_last lies over h0 one may store it before the other
+// has read it.  Then h0 is copied first.
 static size_t start_bytes(int batch, int Dn) {
-    return Dn > 4 && Dn % 4 ? up256((size_t)batch * (size_t)Dn * 4) : 0;
+    return Dn > 4 && Dn % 2 ? up256((size_t)batch * (size_t)Dn * 4) : 0;
 }
 
 size_t gated_fwd_ws(int batch, int64_t L, int Dn, bool bf16) {
