@@ -26,7 +26,7 @@
 // element forward, 8 of them transcendental; 90 backward).  At 8 x 2048 x 1536
 // bf16 with the gate the forward moves 252 MB in 58 us (4.3 TB/s of the 5.6
 // that a copy reaches) and keeps the vector units busy for half of that.  The
-// backward moves 466 MB in 111 us.  One sequence of 131072 x 1536, no gate: 1.61
+// backward moves 466 MB in 102 us.  One sequence of 131072 x 1536, no gate: 1.61
 // GB in 333 us, of which 25 are waiting for the block before.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -565,13 +565,8 @@ __global__ void __launch_bounds__(64 * G::W, 3) gated_bwd(GatedArgs a) {
     const float* st = a.states + ((int64_t)g.b * a.nstates + tr / kGatedBlock) * a.Dn + g.ch;
 #pragma unroll
     for (int c = 0; c < VEC; ++c) h[c] = st[c];
-    load(a.dy, ry, g.rowb);
-    if constexpr (GATE) load(a.z, rz, g.inb);
     share_rates<G>(a, chain, s_k);
-    if (pl.ragged) {  // no gradient arrives at steps past the end either
-        pad_steps<R, TAU>(mine, rr, rx);
-        pad_steps<R, TAU>(mine, ry, ry);
-    }
+    if (pl.ragged) pad_steps<R, TAU>(mine, rr, rx);
     __syncthreads();
     float k[VEC], dlam[VEC];
 #pragma unroll
@@ -606,6 +601,11 @@ __global__ void __launch_bounds__(64 * G::W, 3) gated_bwd(GatedArgs a) {
         }
         __builtin_amdgcn_sched_barrier(0);  // one step's temporaries at a time
     }
+    // Asked for here, not with the others: 8 x 2048 x 1536 bf16 102 us for 112.
+    load(a.dy, ry, g.rowb);
+    if constexpr (GATE) load(a.z, rz, g.inb);
+    // no gradient arrives at steps past the end either
+    if (pl.ragged) pad_steps<R, TAU>(mine, ry, ry);
 #pragma unroll
     for (int off = LC; off < 64; off <<= 1) {
 #pragma unroll
@@ -872,9 +872,9 @@ __global__ void __launch_bounds__(256) gated_step(GatedArgs a) {
 // bf16 with the gate and at 131072 x 1536 without, in us: 58 and 333; 4 channels x
 // 8 steps a lane 60 and 349 (with 2 waves along time 59 and 497, with 8 70 and
 // 380), 1 x 32 73 and 331, 2 x 8 56 and 391 (shorter blocks make the chain of
-// messages longer).  Backward at the first: 111; 2 channels x 8 steps 114, 1 x 16
-// 140, 4 x 8 (which spills) 151, 2 waves a SIMD 127, 3 or 6 waves along time 115
-// and 170.
+// messages longer).  Backward at the first, in units of its 102 us: 2 channels x
+// 8 steps 1.04, 1 x 16 1.26, 4 x 8 (which spills) 1.36, 2 waves a SIMD 1.1, 3 or 6
+// waves along time 1.03 and 1.5.
 template <bool BF16>
 using Fwd = Geo<2, 32, 16, 4, BF16>;
 template <bool BF16>
