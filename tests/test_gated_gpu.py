@@ -204,6 +204,39 @@ def test_repeats_bit_for_bit_also_on_another_stream(gpu):
             assert torch.equal(p, q)
 
 
+def test_side_by_side_on_streams(gpu):
+    """Scans of many blocks on several streams at once, each with a workspace of
+    its own, beside matrix products that take the rest of the chip: every block's
+    wait for earlier ones ends, and the bits are those of a scan alone."""
+    sets = [inputs(*shape, "bf16", True, False, True, seed=40 + k)
+            for k, shape in enumerate(((1, 20000, 64), (4, 5000, 320), (2, 9000, 100)))]
+    a = torch.randn(4096, 4096, device=DEV, dtype=torch.bfloat16)
+
+    def run(s):
+        states = gpu.gated_scan_states(s["x"])
+        y = gpu.gated_scan_fwd(s["x"], s["r"], s["i"], s["lam"], s["z"], reset=s["reset"],
+                               states=states)
+        g = gpu.gated_scan_bwd(s["x"], s["r"], s["i"], s["lam"], s["dy"], states, s["z"],
+                               reset=s["reset"])
+        return [y] + [g[k] for k in sorted(g)]
+
+    alone = [run(s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(len(sets) + 1)]
+    for _ in range(5):
+        got = []
+        with torch.cuda.stream(streams[-1]):
+            for _ in range(4):
+                a @ a
+        for s, stream in zip(sets, streams):
+            with torch.cuda.stream(stream):
+                got.append(run(s))
+        torch.cuda.synchronize()
+        for one, other in zip(alone, got):
+            for u, v in zip(one, other):
+                assert torch.equal(u, v)
+
+
 def test_in_a_graph(gpu):
     s = inputs(1, 5000, 40, "bf16", True, True, True, seed=16)
     io = gpu.MS_BF16
