@@ -26,7 +26,7 @@
 // element forward, 8 of them transcendental; 90 backward).  At 8 x 2048 x 1536
 // bf16 with the gate the forward moves 252 MB in 58 us (4.3 TB/s of the 5.6
 // that a copy reaches) and keeps the vector units busy for half of that.  The
-// backward moves 466 MB in 102 us.  One sequence of 131072 x 1536, no gate: 1.61
+// backward moves 466 MB in 100 us.  One sequence of 131072 x 1536, no gate: 1.61
 // GB in 333 us, of which 25 are waiting for the block before.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -545,8 +545,8 @@ __global__ void __launch_bounds__(64 * G::W, 3) gated_bwd(GatedArgs a) {
     __shared__ float s_h[G::CH], s_k[G::CH];
     __shared__ float s_lam[W][G::CH];
     // h_{t-1} and the gradient arriving at h_t, a lane's own: in registers they
-    // spill (8 x 2048 x 1536 bf16 with gate and resets 152 us for 111, with the gate
-    // 117 for 104).
+    // spill (4 channels x 4 steps a lane, 8 x 2048 x 1536 bf16 with gate and resets:
+    // 152 us for 111, with the gate 117 for 104).
     typedef float F __attribute__((ext_vector_type(VEC)));
     __shared__ F s_hp[TAU][64 * W], s_gh[TAU][64 * W];
     const Work wk = take_work(a);
@@ -876,13 +876,12 @@ __global__ void __launch_bounds__(256) gated_step(GatedArgs a) {
 // bf16 with the gate and at 131072 x 1536 without, in us: 58 and 333; 4 channels x
 // 8 steps a lane 60 and 349 (with 2 waves along time 59 and 497, with 8 70 and
 // 380), 1 x 32 73 and 331, 2 x 8 56 and 391 (shorter blocks make the chain of
-// messages longer).  Backward at the first, in units of its 102 us: 2 channels x
-// 8 steps 1.04, 1 x 16 1.26, 4 x 8 (which spills) 1.36, 2 waves a SIMD 1.1, 3 or 6
-// waves along time 1.03 and 1.5.
+// messages longer).  Backward at the first: 100; 4 channels x 4 steps a lane 107
+// (with 2 waves along time 110, with 8 130), 1 x 16 110.
 template <bool BF16>
 using Fwd = Geo<2, 32, 16, 4, BF16>;
 template <bool BF16>
-using Bwd = Geo<4, 16, 4, 4, BF16>;
+using Bwd = Geo<2, 32, 8, 4, BF16>;
 // fewer than four channels
 template <bool BF16>
 using FwdOne = Geo<1, 4, 2, 4, BF16>;
