@@ -20,6 +20,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "lm_internal.h"
 #include "msscan_internal.h"
@@ -449,6 +451,30 @@ __device__ __forceinline__ bool place(const EmbedArgs& a, int64_t& work, int& co
     return ok;
 }
 
+// Zeros in the rows from v of which none occurs: over their bytes in whole
+// vectors, whatever the row's own alignment, with no lanes past the end of a row.
+// Row by row instead, stores cross lines: 126108 rows of 1530 fp32 with 19 entries
+// 196 us for 150 (of 1536 145 for 139), 40296 of 2115 bf16 with 5206 63 for 50, and
+// the same where most rows occur.
+template <int VEC, bool GBF16>
+__device__ __forceinline__ void clear_rows(const EmbedArgs& a, int64_t v, int rows) {
+    using G = typename std::conditional<GBF16, uint16_t, float>::type;
+    constexpr int N = 16 / sizeof(G);
+    const int lanes = a.lanes, per = 256 / lanes;
+    const int cgroups = (a.D + lanes * VEC - 1) / (lanes * VEC);
+    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / lanes);
+    const int piece = (int)(((int64_t)blockIdx.x * per + group) % cgroups);
+    const int64_t at = piece * (int64_t)lanes + threadIdx.x % lanes;
+    const int64_t step = (int64_t)cgroups * lanes;
+    const int64_t e0 = v * a.D, e1 = e0 + (int64_t)rows * a.D;
+    const int64_t v0 = (e0 + N - 1) / N, v1 = e1 / N;  // its whole vectors
+    G* g = static_cast<G*>(a.dweight);
+    for (int64_t i = v0 + at; i < v1; i += step) reinterpret_cast<uint4*>(g)[i] = uint4{0, 0, 0, 0};
+    const int64_t head = min(v0 * N, e1), tail = max(v1 * N, head);
+    if (e0 + at < head) g[e0 + at] = 0;
+    if (tail + at < e1) g[tail + at] = 0;
+}
+
 template <bool BF16, int VEC, bool GBF16>
 __global__ void __launch_bounds__(256) embed_sum(EmbedArgs a, const uint32_t* key,
                                                  const uint32_t* pos) {
@@ -468,10 +494,12 @@ __global__ void __launch_bounds__(256) embed_sum(EmbedArgs a, const uint32_t* ke
             has = at < a.n && key[at] == (uint32_t)v;
         }
         const uint64_t m = __ballot(has);
-        if (!live) return;
-        const float zero[VEC] = {};
-        for (int k = 0; k < kZeroRows; ++k)
-            if (!((m >> k) & 1)) store_grad<VEC, GBF16>(a.dweight, (v0 + k) * a.D + col, zero);
+        uint32_t none = ~(uint32_t)m & ((1u << kZeroRows) - 1);
+        while (none) {
+            const int k = __ffs(none) - 1, n = __ffs(~(none >> k)) - 1;
+            clear_rows<VEC, GBF16>(a, v0 + k, n);
+            none &= ~(((1u << n) - 1) << k);
+        }
         return;
     }
     const int64_t e0 = work * a.chunk, e1 = min(a.n, e0 + a.chunk);
@@ -619,6 +647,7 @@ __global__ void __launch_bounds__(256) embed_few(EmbedArgs a) {
                 (uint32_t)(k * 64 + lane) | (uint32_t)(t[k] - v0) << 16;
         hits += __popcll(m);
     }
+    if (!hits) return clear_rows<VEC, GBF16>(a, v0, rows);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     const E* dy = static_cast<const E*>(a.dy) + col;
