@@ -453,8 +453,8 @@ __device__ __forceinline__ bool place(const EmbedArgs& a, int64_t& work, int& co
 
 // Zeros in the rows from v of which none occurs: over their bytes in whole
 // vectors, whatever the row's own alignment, with no lanes past the end of a row.
-// Row by row instead, stores cross lines: 126108 rows of 1530 fp32 with 19 entries
-// 196 us for 150 (of 1536 145 for 139), 40296 of 2115 bf16 with 5206 63 for 50, and
+// Row by row instead, stores cross lines: 126108 rows of 1530 fp32 with 300 entries
+// 208 us for 163 (of 1536 157 for 151), 40296 of 2115 bf16 with 5206 63 for 50, and
 // the same where most rows occur.
 template <int VEC, bool GBF16>
 __device__ __forceinline__ void clear_rows(const EmbedArgs& a, int64_t v, int rows) {
@@ -613,85 +613,109 @@ __global__ void __launch_bounds__(256) embed_join(EmbedArgs a, const uint32_t* k
     store_grad<VEC, GBF16>(a.dweight, (int64_t)run * D + col, acc);
 }
 
-// Up to kFew entries: no sort.  A group takes kZeroRows rows of the table; each
-// of its waves goes through all ids for the entries of those rows, and sums
-// them row by row in order.  One launch for three: 64 rows of 768 bf16 in a
-// table of 50280 14.8 us for 22.8, 200 17.5 for 24.9; but the rows of a token that
-// fills a third of the batch come one after another: 200 of 312 fp32 in 300 15.0
-// for 13.5, 512 33 for 14.
+// Up to kFew entries: no sort, one launch for three.  Groups first cover the
+// entries: the group of a token's first entry sums them all in order.  The other
+// workgroups take the gradient's bytes in order, a vector a lane, and write zeros
+// where no entry's row lies: memory takes stores best in the order of workgroups
+// (775 MB 115 us with 4 KB a workgroup, 128 with 8 or 16, 143 with 96).  19 entries in
+// 126108 rows of 1530 fp32 110 us for 150 with 16 rows a group, 64 of 768 bf16 in
+// 50280 14.8 for 16.3.
 template <bool BF16, int VEC, bool GBF16>
 __global__ void __launch_bounds__(256) embed_few(EmbedArgs a) {
     using V = Vec<BF16, VEC>;
     using E = typename V::E;
-    __shared__ uint32_t s_hit[4][kFew];  // position, and row of the group << 16
-    static_assert(kFew <= 1 << 16, "positions and rows in one word");
+    const int lane = threadIdx.x & 63, n = (int)a.n;
+    constexpr int K = kFew / 64;
+    int64_t t[K];  // a lane's entries: their rows, or -1
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        t[k] = k * 64 + lane < n ? token_at(a.ids, a.wide, k * 64 + lane) : -1;
+        if (t[k] < 0 || t[k] >= a.rows || t[k] == a.padding) t[k] = -1;
+    }
+    if (blockIdx.x >= a.sums) {
+        using G = typename std::conditional<GBF16, uint16_t, float>::type;
+        constexpr int N = 16 / sizeof(G);
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int64_t all = a.rows * a.D;
+        const int64_t e0 = (((int64_t)blockIdx.x - a.sums) * 4 + wave) * 64 * N;
+        const int64_t e = e0 + lane * N;
+        uint32_t take = 0;  // elements of this lane's vector that lie in an entry's row
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t s0 = t[k] * a.D;
+            const bool in = t[k] >= 0 && s0 < e0 + 64 * N && s0 + a.D > e0;
+            for (uint64_t m = __ballot(in); m; m &= m - 1) {
+                const int64_t r0 = __shfl(s0, __ffsll((unsigned long long)m) - 1);
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (e + j >= r0 && e + j < r0 + a.D) take |= 1u << j;
+            }
+        }
+        G* g = static_cast<G*>(a.dweight) + e;
+        if (!take && e + N <= all) {
+            *reinterpret_cast<uint4*>(g) = uint4{0, 0, 0, 0};
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (!((take >> j) & 1) && e + j < all) g[j] = 0;
+        }
+        return;
+    }
     int64_t work;
     int col;
     const bool live = place<VEC>(a, work, col);
-    if (work >= a.zeros) return;
-    const int lane = threadIdx.x & 63, n = (int)a.n;
-    uint32_t* hit = s_hit[threadIdx.x >> 6];
-    const int64_t v0 = work * kZeroRows;
-    const int rows = (int)min(a.rows - v0, (int64_t)kZeroRows);
-    int64_t t[kFew / 64];
+    if (work >= a.chunks) return;  // chunks are entries here
+    int64_t row = -1;
 #pragma unroll
-    for (int k = 0; k < kFew / 64; ++k)
-        t[k] = k * 64 + lane < n ? token_at(a.ids, a.wide, k * 64 + lane) : -1;
-    int hits = 0;
+    for (int k = 0; k < K; ++k)
+        if (work >> 6 == k) row = __shfl(t[k], (int)(work & 63));
+    if (row < 0) return;
+    uint64_t m[K];
+    bool first = true;
 #pragma unroll
-    for (int k = 0; k < kFew / 64; ++k) {
-        const bool in = t[k] >= v0 && t[k] < v0 + rows && t[k] != a.padding;
-        const uint64_t m = __ballot(in);
-        if (in)
-            hit[hits + __popcll(m & ((1ull << lane) - 1))] =
-                (uint32_t)(k * 64 + lane) | (uint32_t)(t[k] - v0) << 16;
-        hits += __popcll(m);
+    for (int k = 0; k < K; ++k) {
+        m[k] = __ballot(t[k] == row);
+        const int64_t before = work - k * 64;
+        if (before >= 64 ? m[k] != 0 : before > 0 && (m[k] & ((1ull << before) - 1))) first = false;
     }
-    if (!hits) return clear_rows<VEC, GBF16>(a, v0, rows);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    if (!first) return;
     const E* dy = static_cast<const E*>(a.dy) + col;
     constexpr int U = 8;  // rows on the way at a time
-    for (int r = 0; r < rows; ++r) {
-        float acc[VEC] = {};
-        bool some = false;
-        for (int b = 0; b < hits; b += 64) {
-            const uint32_t h = b + lane < hits ? hit[b + lane] : 0xffffffffu;
-            uint64_t m = __ballot((int)(h >> 16) == r);
-            some = some || m;
-            while (m) {
-                typename V::T w[U];
-                int got = 0;
+    float acc[VEC] = {};
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (!m) break;
-                    const uint32_t e = __builtin_amdgcn_readlane(h, __ffsll((unsigned long long)m) - 1);
-                    m &= m - 1;
-                    w[u] = ldv<V>(dy + (int64_t)(e & 0xffffu) * a.D);
-                    ++got;
-                }
+    for (int k = 0; k < K; ++k) {
+        while (m[k]) {
+            typename V::T w[U];
+            int got = 0;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (u >= got) break;
-                    float v[VEC];
-                    V::unpack(w[u], v);
+            for (int u = 0; u < U; ++u) {
+                if (!m[k]) break;
+                const int at = k * 64 + __ffsll((unsigned long long)m[k]) - 1;
+                m[k] &= m[k] - 1;
+                w[u] = ldv<V>(dy + (int64_t)at * a.D);
+                ++got;
+            }
 #pragma unroll
-                    for (int c = 0; c < VEC; ++c) acc[c] += v[c];
-                }
+            for (int u = 0; u < U; ++u) {
+                if (u >= got) break;
+                float v[VEC];
+                V::unpack(w[u], v);
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) acc[c] += v[c];
             }
         }
-        if (!live) continue;
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) acc[c] = some ? acc[c] * a.scale : 0.f;
-        store_grad<VEC, GBF16>(a.dweight, (v0 + r) * a.D + col, acc);
     }
+    if (!live) return;
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) acc[c] *= a.scale;
+    store_grad<VEC, GBF16>(a.dweight, row * a.D + col, acc);
 }
 
 template <bool BF16, int VEC>
 hipError_t sum_variant(const EmbedArgs& a, bool gbf16, const uint32_t* key, const uint32_t* pos,
                        hipStream_t s) {
     const int64_t cgroups = (a.D + a.lanes * VEC - 1) / (a.lanes * VEC), per = 256 / a.lanes;
-    const dim3 grid((unsigned)embed_sum_workgroups(a, BF16)), blk(256);
+    const dim3 grid((unsigned)embed_sum_workgroups(a, BF16, gbf16)), blk(256);
     if (a.few) {
         ProfScope ps(s, kPhaseMain);
         if (gbf16) hipLaunchKernelGGL((embed_few<BF16, VEC, true>), grid, blk, 0, s, a);
@@ -719,9 +743,13 @@ int embed_vec(int D, bool bf16) {
     return D >= v ? v : 1;
 }
 
-int64_t embed_sum_workgroups(const EmbedArgs& a, bool bf16) {
-    const int64_t cols = (int64_t)a.lanes * embed_vec(a.D, bf16), per = 256 / a.lanes;
-    return ((a.chunks + a.zeros) * ((a.D + cols - 1) / cols) + per - 1) / per;
+int64_t embed_sum_workgroups(const EmbedArgs& a, bool bf16, bool gbf16) {
+    if (!a.few) {
+        const int64_t vec = embed_vec(a.D, bf16), cols = a.lanes * vec, per = 256 / a.lanes;
+        return ((a.chunks + a.zeros) * ((a.D + cols - 1) / cols) + per - 1) / per;
+    }
+    const int64_t span = 256 * (gbf16 ? 8 : 4);  // elements
+    return a.sums + (a.rows * a.D + span - 1) / span;
 }
 
 int64_t embed_fwd_workgroups(const EmbedArgs& a, bool bf16) {
@@ -764,9 +792,12 @@ void embed_plan(EmbedArgs& a, bool bf16) {
     const int64_t chunk = a.n * cgroups * a.lanes / (2048 * 256);
     a.chunk = chunk < 32 ? 32 : chunk > 256 ? 256 : chunk;
     a.chunks = (a.n + a.chunk - 1) / a.chunk;
-    a.few = a.n <= kFew;
-    if (a.few) a.chunks = 0;
+    // a table whose vectors are too many for one launch is sorted for
+    a.few = a.n <= kFew && (double)a.rows * a.D <= 0x1p33;
+    if (a.few) a.chunks = a.n;
     a.small = a.n <= kSmall;
+    const int64_t per = 256 / a.lanes;
+    a.sums = (a.chunks * cgroups + per - 1) / per;
     a.zeros = (a.rows + kZeroRows - 1) / kZeroRows;
 }
 

@@ -273,7 +273,7 @@ ms_status ms_embed_bwd(const void* ids, int32_t id_bits, const void* dy, float s
     a.dweight = dweight; a.n = n; a.rows = rows; a.D = dim;
     embed_plan(a, io == MS_BF16);
     if ((st = check_workspace(embed_ws(a).total, workspace, workspace_bytes)) != MS_OK) return st;
-    if (embed_sum_workgroups(a, io == MS_BF16) > kMaxGroups)
+    if (embed_sum_workgroups(a, io == MS_BF16, grad_dtype == MS_BF16) > kMaxGroups)
         return fail(MS_ERR_UNSUPPORTED, "n, rows and dim need more than 2^24-1 workgroups");
     prof_call();
     return launched(launch_embed_bwd(a, io == MS_BF16, grad_dtype == MS_BF16, workspace,

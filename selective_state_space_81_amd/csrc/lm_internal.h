@@ -88,8 +88,9 @@ struct EmbedArgs {
     int small;      // one workgroup sorts
     int lanes;      // threads that share a piece of the sums
     int64_t chunk;  // sorted entries in a piece
-    int64_t chunks;
+    int64_t chunks;  // without a sort, the entries
     int64_t zeros;  // pieces that write rows of tokens that do not occur
+    int64_t sums;   // without a sort: workgroups of the sums, before those of zeros
 };
 struct SortPass {
     const uint32_t* key_in;
@@ -108,7 +109,7 @@ int embed_vec(int D, bool bf16);
 void embed_plan(EmbedArgs& a, bool bf16);  // from n, rows, D
 EmbedWs embed_ws(const EmbedArgs& a);
 int64_t embed_fwd_workgroups(const EmbedArgs& a, bool bf16);
-int64_t embed_sum_workgroups(const EmbedArgs& a, bool bf16);
+int64_t embed_sum_workgroups(const EmbedArgs& a, bool bf16, bool gbf16);
 hipError_t launch_embed_fwd(const EmbedArgs& a, bool bf16, hipStream_t s);
 hipError_t launch_embed_bwd(EmbedArgs a, bool bf16, bool gbf16, void* workspace, hipStream_t s);
 
