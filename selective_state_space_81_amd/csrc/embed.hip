@@ -619,13 +619,14 @@ __global__ void __launch_bounds__(256) embed_join(EmbedArgs a, const uint32_t* k
 // where no entry's row lies: memory takes stores best in the order of workgroups
 // (775 MB 115 us with 4 KB a workgroup, 128 with 8 or 16, 143 with 96).  19 entries in
 // 126108 rows of 1530 fp32 110 us for 150 with 16 rows a group, 64 of 768 bf16 in
-// 50280 14.8 for 16.3.
-template <bool BF16, int VEC, bool GBF16>
+// 50280 14.8 for 16.3.  K entries a lane, that each wave looks through: with 4 up to 128
+// entries take 125 and 18 there; 200 entries 130 and 19, sorted 163 and 25, with 8
+// 215 and 27.
+template <bool BF16, int VEC, bool GBF16, int K>
 __global__ void __launch_bounds__(256) embed_few(EmbedArgs a) {
     using V = Vec<BF16, VEC>;
     using E = typename V::E;
     const int lane = threadIdx.x & 63, n = (int)a.n;
-    constexpr int K = kFew / 64;
     int64_t t[K];  // a lane's entries: their rows, or -1
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -718,8 +719,14 @@ hipError_t sum_variant(const EmbedArgs& a, bool gbf16, const uint32_t* key, cons
     const dim3 grid((unsigned)embed_sum_workgroups(a, BF16, gbf16)), blk(256);
     if (a.few) {
         ProfScope ps(s, kPhaseMain);
-        if (gbf16) hipLaunchKernelGGL((embed_few<BF16, VEC, true>), grid, blk, 0, s, a);
-        else hipLaunchKernelGGL((embed_few<BF16, VEC, false>), grid, blk, 0, s, a);
+        auto go = [&](auto k) {
+            constexpr int K = decltype(k)::value;
+            if (gbf16) hipLaunchKernelGGL((embed_few<BF16, VEC, true, K>), grid, blk, 0, s, a);
+            else hipLaunchKernelGGL((embed_few<BF16, VEC, false, K>), grid, blk, 0, s, a);
+        };
+        constexpr int most = kFew / 64;
+        if (a.n <= kFew / 2) go(std::integral_constant<int, most / 2>{});
+        else go(std::integral_constant<int, most>{});
         return hipGetLastError();
     }
     {

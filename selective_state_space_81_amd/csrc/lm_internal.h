@@ -63,7 +63,7 @@ hipError_t launch_gated_step(const GatedArgs& a, bool bf16, hipStream_t s);
 // ---- embedding (embed.hip) ----------------------------------------------------
 constexpr int kDigitBits = 9;   // sort digit: two passes up to 2^18 tokens
 constexpr int kMaxTiles = 256;  // sort workgroups
-constexpr int kFew = 128;       // entries that are not sorted
+constexpr int kFew = 256;       // entries that are not sorted
 constexpr int kSmall = 6144;    // entries one workgroup sorts
 
 struct EmbedArgs {
