@@ -89,6 +89,24 @@ def test_runs_across_workgroups(gpu, n):
     check_grad(gpu, torch.arange(n, device=DEV) % 2 * (n - 1), dy, n)
 
 
+@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 128, 130, 200, 256, 257])
+@pytest.mark.parametrize("dim", [1, 3, 5, 8, 100, 1030])
+def test_few_entries(gpu, n, dim):
+    """Rows that start and end inside a 16-byte vector, beside zeros; tokens that
+    occur again; first, last and neighbouring rows; ids without a row."""
+    g = gen(n * dim)
+    dy = torch.randn(n, dim, generator=g, device=DEV)
+    rows = 301
+    ids = torch.randint(-2, rows + 2, (n,), generator=g, device=DEV)
+    ids[0] = rows - 1
+    ids[n // 2:n // 2 + 3] = torch.arange(3, device=DEV)[:max(min(3, n - n // 2), 0)]
+    ids[n - 1] = ids[0]
+    check_grad(gpu, ids, dy, rows, scale=0.3)
+    check_grad(gpu, ids, dy.bfloat16(), rows, padding=1)
+    check_grad(gpu, ids.int(), dy.bfloat16(), rows, grad_dtype=torch.float32)
+    check_grad(gpu, torch.full_like(ids, 1), dy, 3, grad_dtype=torch.bfloat16)
+
+
 def test_ignored_ids_and_shapes(gpu):
     g = gen(5)
     ids = torch.randint(-3, 14, (4, 50), generator=g, device=DEV)
