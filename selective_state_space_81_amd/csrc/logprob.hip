@@ -36,6 +36,7 @@
 
 #include "device_common.h"
 #include "lm_internal.h"
+#include "logprob_notes.h"
 #include "msscan_internal.h"
 
 namespace msscan {
@@ -151,12 +152,6 @@ __device__ __forceinline__ float key_value(uint64_t k) {
     return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// The smallest float above v (x > v is then x >= next for every fp32 x).
-__device__ __forceinline__ float next_above(float v) {
-    const uint32_t b = __float_as_uint(v + 0.f);
-    return __uint_as_float((b >> 31) ? b - 1 : b + 1);
-}
-
 // LDS between lanes of one wave: its accesses stay in order.
 __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -189,83 +184,10 @@ __device__ __forceinline__ uint64_t merge_in(uint64_t list, uint64_t v, int lane
     return v;
 }
 
-// Blocks that a wave has noted, in LDS: the first token and the largest logit
-// of each.  kNoteRoom: what is kept of a flush (below) is at most what came
-// together since the one before (kNoteFlush and a block of 64 lanes) and fewer
-// than `top` (64) more, and another block may follow.
-constexpr int kNoteFlush = 128, kNoteRoom = kNoteFlush + 64 + 64 + 64;
-struct Notes {
-    uint32_t first[kNoteRoom];
-    float high[kNoteRoom];
-};
-
-struct Noted {
-    Notes* q;
-    float thr;    // what a block's largest logit has to reach to be noted
-    float bound;  // what at least `top` logits of the row reach
-    int top, count, lane;
-
-    __device__ __forceinline__ void init(Notes* notes, int top_, int lane_) {
-        q = notes;
-        thr = bound = -__builtin_inff();
-        top = top_;
-        count = 0;
-        lane = lane_;
-    }
-    __device__ __forceinline__ void note(bool in, uint32_t first, float high) {
-        const uint64_t m = __ballot(in);
-        if (in) {
-            const int k = count + __popcll(m & ((1ull << lane) - 1));
-            q->first[k] = first;
-            q->high[k] = high;
-        }
-        count += __popcll(m);
-        if (count >= kNoteFlush) flush();
-    }
-    // Many notes (rows that rise): the top-th largest of their maxima is reached
-    // by `top` logits, so notes below it go.  Blocks to come have higher tokens
-    // and have to exceed it.
-    __device__ __forceinline__ void flush() {
-        constexpr int K = kNoteRoom / 64;
-        wave_sync();
-        uint32_t first[K], o[K];
-        float high[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const bool in = k * 64 + lane < count;
-            first[k] = in ? q->first[k * 64 + lane] : 0;
-            high[k] = in ? q->high[k * 64 + lane] : 0.f;
-            const uint32_t b = __float_as_uint(high[k] + 0.f);
-            o[k] = in ? b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u) : 0;  // ordered; 0 is below all
-        }
-        uint32_t x = 0;  // the largest number that `top` of them reach, bit by bit
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t y = x | (1u << bit);
-            int n = 0;
-#pragma unroll
-            for (int k = 0; k < K; ++k) n += __popcll(__ballot(o[k] >= y));
-            if (n >= top) x = y;
-        }
-        wave_sync();
-        int kept = 0;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const bool in = o[k] != 0 && o[k] >= x;
-            const uint64_t m = __ballot(in);
-            if (in) {
-                const int at = kept + __popcll(m & ((1ull << lane) - 1));
-                q->first[at] = first[k];
-                q->high[at] = high[k];
-            }
-            kept += __popcll(m);
-        }
-        count = kept;
-        if (x) {
-            bound = __uint_as_float(x ^ ((x >> 31) ? 0x80000000u : 0xffffffffu));
-            thr = fmaxf(thr, next_above(bound));
-        }
-        wave_sync();
-    }
+// The wave that Noted runs on.
+struct Wave {
+    static __device__ __forceinline__ uint64_t ballot(bool v) { return __ballot(v); }
+    static __device__ __forceinline__ void sync() { wave_sync(); }
 };
 
 // A value that at least `top` logits of the workgroup reach: the top-th largest
@@ -439,7 +361,7 @@ __global__ void __launch_bounds__(64 * W, TOP && W == 4 ? 5 : 4) logprob_fwd(Log
 
     Stat st{-kFar, 0.f, 0.f};
     float high = -__builtin_inff();  // the lane's largest logit
-    Noted noted;
+    Noted<Wave> noted;
     if constexpr (TOP) {
         noted.init(&s_notes[wave], a.top, lane);
         if (threadIdx.x == 0) s_count = 0;
@@ -573,7 +495,8 @@ __global__ void __launch_bounds__(64 * W, TOP && W == 4 ? 5 : 4) logprob_fwd(Log
                     const int e = lane % G;
                     const uint32_t tok = from + e / N * (64 * N) + e % N;
                     // a block ends with the vectors; the logits after them are alone
-                    const bool have = from != 0xffffffffu && (from < v1 * N ? tok < v1 * N : e == 0);
+                    const bool have = from != 0xffffffffu &&
+                                      (from < v1 * N ? tok < v1 * N : e == 0 && tok < (uint32_t)a.V);
                     float v = -__builtin_inff();
                     if (have) v = L::one(x + tok);
                     f(have && v >= t, v, tok);

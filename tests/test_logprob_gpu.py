@@ -261,3 +261,31 @@ def test_plans(gpu, io):
         x, t = make(rows, vocab, io, seed=rows + vocab)
         for top in (0, 7, 33, 64) if rows < 90 else (33,):
             check(gpu, x, t, top=top)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(6, 50280), (300, 50280), (6, 131072), (100, 131072),
+                                        (300, 131072)])
+def test_many_infinities(gpu, rows, vocab, io):
+    """Rows of +inf, in one workgroup of few or many waves and in splits: NaN
+    results, the lowest tokens that hold one as alternatives; other rows as ever."""
+    x, t = make(rows, vocab, io, seed=rows + vocab)
+    k = torch.arange(vocab, device=DEV)
+    x[0] = math.inf
+    x[1, ::2] = math.inf
+    x[2] = torch.where(k > vocab // 2, math.inf, k / vocab).to(IO[io])
+    x[3, vocab - 3:] = math.inf
+    x[4, 7::16] = math.inf
+    x[4, ::3] = float("nan")
+    raw = x[:6].cpu().float().numpy()
+    ids = np.argsort(np.where(np.isnan(raw), np.inf, -raw), axis=1, kind="stable")
+    for top in (1, 5, 64):
+        got = gpu.token_logprobs_fwd(x, t, top=top)
+        for name in ("logprob", "entropy", "lse", "top_logprob"):
+            assert torch.isnan(got[name][:5]).all(), name
+            assert torch.isfinite(got[name][5:]).all(), name
+        assert (got["top_id"][:6].cpu().numpy() == ids[:, :top]).all()
+    gl, gh = upstream(rows, 5)
+    r = gpu.token_logprobs_fwd(x, t)
+    d = gpu.token_logprobs_bwd(x, t, r["stats"], r["entropy"], gl, gh)
+    assert torch.isfinite(d[5:]).all()
