@@ -53,15 +53,14 @@ int64_t row_pitch(const at::Tensor& t) {
     const int64_t dims = t.dim(), d = t.size(dims - 1);
     if (d > 1 && t.stride(dims - 1) != 1) return -1;
     if (t.numel() == 0) return d;
-    int64_t ld = 0, want = 0;
+    int64_t ld = -1, want = 0;  // -1: no dimension before the rows' has told it yet
     for (int64_t k = dims - 2; k >= 0; --k) {
         if (t.size(k) == 1) continue;
-        if (!ld) ld = want = t.stride(k);
-        if (t.stride(k) != want) return -1;
+        if (ld < 0) ld = want = t.stride(k);
+        if (ld < d || t.stride(k) != want) return -1;  // overlapping (an expanded dimension's is 0)
         want *= t.size(k);
     }
-    if (!ld) return d;
-    return ld >= d ? ld : -1;
+    return ld < 0 ? d : ld;
 }
 PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS

@@ -168,3 +168,27 @@ def test_marshalling():
         m.gated_step(x, x, x, x, x, 8.0, None, x, 1 << 40, 4, 4, 0, 0)
     assert m.gated_step(x, x, x, x, x, 8.0, None, x, 0, 4, 4, 0, 0) == 2  # MS_ERR_SHAPE
     assert m.gated_step(None, x, x, x, x, 8.0, None, x, 3, 4, 4, 0, None) == 1  # MS_ERR_NULL
+
+
+@pytest.mark.parametrize("shape,to", [((64,), (2, 100, 64)), ((2, 1, 64), (2, 100, 64)),
+                                      ((1, 100, 64), (2, 100, 64)), ((1, 1, 64), (1, 100, 64)),
+                                      ((1, 1, 64), (7, 1, 64)), ((1, 64), (8, 64)), ((1, 1), (8, 1))])
+def test_expanded_rows_are_refused(shape, to):
+    """A broadcast input has fewer rows in memory than its sizes say."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    m = ms.lm._marshal()
+    with FakeTensorMode():  # device tensors without a device
+        whole = torch.empty(to, device="cuda:0")
+        wide = torch.empty(*to[:-1], 3 * to[-1] + 1, device="cuda:0")[..., to[-1]:2 * to[-1]]
+        few = torch.empty(shape, device="cuda:0").expand(to)
+        dims = len(to)
+        assert m.rows(whole, dims) == 2 * to[-1] and m.rows(wide, dims) == 2 * (3 * to[-1] + 1)
+        assert m.rows(few, dims) == -1 and m.rows(whole, dims, few) == -1
+        lam = torch.empty(to[-1], device="cuda:0")
+        for k in range(4):
+            args = [few if j == k else whole for j in range(4)]
+            with pytest.raises(ValueError, match="contiguous"):
+                if dims == 2:
+                    ms.gated_step(torch.empty(to, device="cuda:0"), *args[:3], lam, args[3])
+                else:
+                    ms.gated_scan_fwd(*args[:3], lam, args[3])
