@@ -6,8 +6,10 @@ probabilities.  Argument marshalling only, as in the package's ``__init__``
 Raw calls (``*_fwd``, ``*_bwd``, ``gated_step``) take and return device
 tensors; ``gated_scan``, ``embed`` and ``token_logprobs`` are the same as
 differentiable torch operations.  Work goes to the current stream of the
-tensors' device, or to ``stream``; buffers allocated here are kept from reuse
-until that stream has passed them.
+tensors' device, or to ``stream``.  Buffers allocated here belong to the stream
+that the work goes to, and results are kept from reuse until the current one
+has passed them too; the inputs of a call on another stream have to be ready
+there, and kept until it has passed them.
 """
 from __future__ import annotations
 
@@ -69,11 +71,12 @@ def _marshal():
 
 
 class _Call:
-    """One call's device and stream.  Allocations made for it are recorded on
-    its stream when that is not the current one (their memory could otherwise
-    be handed out again while the call still uses it)."""
+    """One call's device and stream.  What it allocates comes from that
+    stream's memory: memory that the current stream has freed may still be in
+    use by work queued there, which another stream does not wait for.  Results
+    are recorded on the current stream, whose work may use them."""
 
-    __slots__ = ("torch", "m", "like", "index", "stream", "other")
+    __slots__ = ("torch", "m", "like", "index", "stream", "other", "current")
 
     def __init__(self, m, like, stream):
         import torch
@@ -84,26 +87,33 @@ class _Call:
         if stream is not None:
             given = stream if isinstance(stream, int) else stream.cuda_stream
             if given != self.stream:
+                self.current = torch.cuda.current_stream(self.index)
                 self.stream = given
                 self.other = torch.cuda.ExternalStream(given, device=like.device) \
                     if isinstance(stream, int) else stream
 
+    def _make(self, make, *args):
+        if self.other is None:
+            return make(self.like, *args)
+        with self.torch.cuda.stream(self.other):
+            return make(self.like, *args)
+
     def empty(self, dtype, *shape):
-        t = self.m.empty(self.like, dtype, *shape)
+        t = self._make(self.m.empty, dtype, *shape)
         if self.other is not None:
-            t.record_stream(self.other)
+            t.record_stream(self.current)
         return t
 
     def together(self, *dtypes_and_sizes):
-        ts = self.m.together(self.like, *dtypes_and_sizes)
+        ts = self._make(self.m.together, *dtypes_and_sizes)
         if self.other is not None:
-            ts[0].record_stream(self.other)  # the one allocation of all
+            ts[0].record_stream(self.current)  # the one allocation of all
         return ts
 
     def workspace(self, given, need):
         """(tensor, bytes) of the given workspace, or of a new one."""
         if given is None:
-            return (self.empty(self.torch.uint8, need), need) if need else (None, 0)
+            return (self._make(self.m.empty, self.torch.uint8, need), need) if need else (None, 0)
         if given.device != self.like.device or not given.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {self.like.device}")
         return given, given.numel() * given.element_size()

@@ -348,3 +348,39 @@ def test_refusals(gpu):
         gpu.gated_scan_bwd(x, r, i, lam, s["dy"], gpu.gated_scan_states(x),
                            workspace=torch.empty(1, dtype=torch.uint8, device=DEV))
     np.testing.assert_equal(gpu.gated_scan_states(x).shape, (2, 1, 8))
+
+
+def test_calls_on_two_streams_in_turn(gpu):
+    """A call on another stream takes no memory that the current stream has
+    freed (its queue may still use it): calls in turn, with nothing between them,
+    give the bits of calls alone."""
+    side = torch.cuda.Stream()
+    s = inputs(2, 6000, 136, "bf16", True, False, True, seed=18)
+    t = inputs(2, 6000, 136, "bf16", True, False, True, seed=19)
+
+    def run(v, stream=None):
+        states = gpu.gated_scan_states(v["x"], stream=stream)
+        y = gpu.gated_scan_fwd(v["x"], v["r"], v["i"], v["lam"], v["z"], reset=v["reset"],
+                               states=states, stream=stream)
+        g = gpu.gated_scan_bwd(v["x"], v["r"], v["i"], v["lam"], v["dy"], states, v["z"],
+                               reset=v["reset"], stream=stream)
+        return [y] + [g[k] for k in sorted(g) if g[k] is not None]
+
+    want = run(s), run(t)
+    torch.cuda.synchronize()
+    n = gpu.gated_scan_bwd_workspace_bytes(2, 6000, 136, gpu.MS_BF16)
+    m = gpu.lm._marshal()
+    for stream in (side, side.cuda_stream):
+        freed = torch.empty(n, dtype=torch.uint8, device=DEV)
+        at = freed.data_ptr()
+        del freed
+        call = gpu.lm._Call(m, s["x"], stream)
+        assert call.workspace(None, n)[0].data_ptr() != at
+        assert call.empty(torch.uint8, n).data_ptr() != at
+        assert call.together(torch.uint8, (n,))[0].data_ptr() != at
+    for _ in range(8):
+        got = [(run(s), run(t, side)) for _ in range(3)]
+        torch.cuda.synchronize()
+        for one in got:
+            for a, b in zip(want, one):
+                assert all(torch.equal(p, q) for p, q in zip(a, b))

@@ -1,6 +1,8 @@
 """Host-only checks of the language-model operators' C ABI: sizes, and every
 refusal that needs no GPU (nothing is launched on any of these calls)."""
+import contextlib
 import ctypes
+import types
 
 import pytest
 import torch
@@ -192,3 +194,44 @@ def test_expanded_rows_are_refused(shape, to):
                     ms.gated_step(torch.empty(to, device="cuda:0"), *args[:3], lam, args[3])
                 else:
                     ms.gated_scan_fwd(*args[:3], lam, args[3])
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_buffers_come_from_the_stream_of_the_call(monkeypatch, as_int):
+    """What is allocated for a call on another stream is allocated there (the
+    current stream's freed memory may still be in use by its queue), and results,
+    not workspaces, are recorded on the current stream."""
+    current, side = (types.SimpleNamespace(cuda_stream=k) for k in (1, 2))
+    stack = [current]
+
+    @contextlib.contextmanager
+    def on(stream):
+        stack.append(stream)
+        yield
+        stack.pop()
+
+    class Made:
+        def __init__(self):
+            self.of, self.recorded = stack[-1], []
+
+        def record_stream(self, stream):
+            self.recorded.append(stream)
+
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda k: 1, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda k=None: stack[-1])
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: {2: side}[h])
+    m = types.SimpleNamespace(empty=lambda like, dtype, *shape: Made(),
+                              together=lambda like, *sizes: [Made(), Made()])
+    like = types.SimpleNamespace(get_device=lambda: 0, device="cuda:0")
+    for stream, of in ((None, current), (current, current), (side, side)):
+        given = stream.cuda_stream if as_int and stream else stream
+        call = ms.lm._Call(m, like, given)
+        assert call.stream == of.cuda_stream
+        out, several = call.empty(torch.float32, 3), call.together(torch.float32, (3,))
+        ws, n = call.workspace(None, 256)
+        assert n == 256 and out.of is of and ws.of is of and all(t.of is of for t in several)
+        assert stack == [current]
+        there = [current] if of is side else []
+        assert out.recorded == there and several[0].recorded == there and ws.recorded == []
+        assert call.workspace(None, 0) == (None, 0)
