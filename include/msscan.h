@@ -362,7 +362,9 @@ ms_status ms_conv1d_silu(const void* x, const float* weight, const float* bias,
  *   reset         : [batch][seqlen] bytes, optional.  A nonzero byte starts a
  *                   new sequence there: nothing of the state before it comes
  *                   through, NaN and infinities included (nor does anything
- *                   through a step whose decay is exactly 0).
+ *                   through a step whose decay is exactly 0).  Up to there a
+ *                   state that is not finite stays so (an infinity may become
+ *                   NaN), however far the decays' product has fallen.
  *   h0, h_last    : [batch][d_inner] fp32, optional.  h_last may equal h0.
  *   states        : optional; receives the state before steps 0, 16, 32, ...
  *                   ([batch][ceil(seqlen / 16)][d_inner] fp32, that is

@@ -169,13 +169,34 @@ __device__ __forceinline__ float one_minus_square(float t, float a) {
 
 __device__ __forceinline__ float sqrt_f(float v) { return __builtin_amdgcn_sqrtf(v); }
 
-// (P, H) applied to h.  With resets a decay of 0 cuts the past off whole: a
-// NaN or infinity before the reset must not come through as 0 * NaN.
+// With resets a step that resets, or whose own decay is exactly 0, has the decay
+// kCut: a product of decays that falls to 0 must not pass for one, and a 0 would
+// let a NaN or infinity before the reset through as 0 * NaN.
+constexpr float kCut = -1.f;
+
+// (P, H) applied to h.
 template <bool RESET>
 __device__ __forceinline__ float apply(float P, float h, float H) {
     const float v = fmaf(P, h, H);
-    if constexpr (RESET) return P == 0.f ? H : v;
+    if constexpr (RESET) return P < 0.f ? H : v;
     return v;
+}
+
+// The decay of two maps in a row: the product, which is at most each of them,
+// or kCut where one cuts (then that is the least of the three).  A NaN may be
+// lost to the other's number here: the H of its map is NaN as well.
+template <bool RESET>
+__device__ __forceinline__ float both(float P, float Q) {
+    const float v = P * Q;
+    if constexpr (RESET) return fminf(fminf(P, Q), v);
+    return v;
+}
+
+// The decay of a step.
+template <bool RESET>
+__device__ __forceinline__ float decay(float e, bool cut) {
+    if constexpr (RESET) return cut || e == 0.f ? kCut : e;
+    return e;
 }
 
 // ---- geometry -----------------------------------------------------------------------
@@ -437,10 +458,10 @@ __global__ void __launch_bounds__(64 * G::W, G::BF16 ? 3 : 2) gated_fwd(GatedArg
             const float la2 = k[c] * sigmoid_f(r[c]);
             const float e = hw_exp2(la2);
             const float n = sqrt_f(one_minus_square(la2, e));
-            A[j][c] = cut ? 0.f : e;
+            A[j][c] = decay<RESET>(e, cut);
             B[j][c] = n * sigmoid_f(i[c]) * x[c];
             H[c] = apply<RESET>(A[j][c], H[c], B[j][c]);
-            P[c] *= A[j][c];
+            P[c] = both<RESET>(P[c], A[j][c]);
         }
         __builtin_amdgcn_sched_barrier(0);  // one step's temporaries at a time
     }
@@ -453,7 +474,7 @@ __global__ void __launch_bounds__(64 * G::W, G::BF16 ? 3 : 2) gated_fwd(GatedArg
             const float Pu = __shfl_up(P[c], off), Hu = __shfl_up(H[c], off);
             if (g.lane >= off) {
                 H[c] = apply<RESET>(P[c], Hu, H[c]);
-                P[c] *= Pu;
+                P[c] = both<RESET>(P[c], Pu);
             }
         }
     }
@@ -476,7 +497,7 @@ __global__ void __launch_bounds__(64 * G::W, G::BF16 ? 3 : 2) gated_fwd(GatedArg
         for (int w = 0; w < W; ++w) {
             const float2 v = s_sum[w][threadIdx.x];
             bh = apply<RESET>(v.x, bh, v.y);
-            bp *= v.x;
+            bp = both<RESET>(bp, v.x);
         }
         const int64_t at = (int64_t)g.b * a.Dn + slot_channel<G>(a, chain, (int)threadIdx.x);
         if (blk > 0) {
@@ -600,9 +621,9 @@ __global__ void __launch_bounds__(64 * G::W, 3) gated_bwd(GatedArgs a) {
             const float la2 = k[c] * sr[j][c];
             e[j][c] = hw_exp2(la2);
             n[j][c] = sqrt_f(one_minus_square(la2, e[j][c]));
-            A[j][c] = cut ? 0.f : e[j][c];
+            A[j][c] = decay<RESET>(e[j][c], cut);
             H[c] = apply<RESET>(A[j][c], H[c], n[j][c] * si[j][c] * x[c]);
-            P[c] *= A[j][c];
+            P[c] = both<RESET>(P[c], A[j][c]);
         }
         __builtin_amdgcn_sched_barrier(0);  // one step's temporaries at a time
     }
@@ -618,7 +639,7 @@ __global__ void __launch_bounds__(64 * G::W, 3) gated_bwd(GatedArgs a) {
             const float Pu = __shfl_up(P[c], off), Hu = __shfl_up(H[c], off);
             if (g.lane >= off) {
                 H[c] = apply<RESET>(P[c], Hu, H[c]);
-                P[c] *= Pu;
+                P[c] = both<RESET>(P[c], Pu);
             }
         }
     }
@@ -670,7 +691,7 @@ __global__ void __launch_bounds__(64 * G::W, 3) gated_bwd(GatedArgs a) {
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
             C[c] = apply<RESET>(A[j][c], gh[c] + C[c], 0.f);
-            P[c] *= A[j][c];
+            P[c] = both<RESET>(P[c], A[j][c]);
         }
     }
 #pragma unroll
@@ -680,7 +701,7 @@ __global__ void __launch_bounds__(64 * G::W, 3) gated_bwd(GatedArgs a) {
             const float Pd = __shfl_down(P[c], off), Cd = __shfl_down(C[c], off);
             if (g.lane + off < 64) {
                 C[c] = apply<RESET>(P[c], Cd, C[c]);
-                P[c] *= Pd;
+                P[c] = both<RESET>(P[c], Pd);
             }
         }
     }
@@ -703,7 +724,7 @@ __global__ void __launch_bounds__(64 * G::W, 3) gated_bwd(GatedArgs a) {
         for (int w = W - 1; w >= 0; --w) {
             const float2 q = s_sum[w][threadIdx.x];
             bc = apply<RESET>(q.x, bc, q.y);
-            bp *= q.x;
+            bp = both<RESET>(bp, q.x);
         }
         if (turn > 0) {
             if (!last) cn.publish_map(turn, bp, bc);

@@ -384,3 +384,57 @@ def test_calls_on_two_streams_in_turn(gpu):
         for one in got:
             for a, b in zip(want, one):
                 assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def same_with_nan(p, q):
+    n, m = torch.isnan(p), torch.isnan(q)
+    return torch.equal(n, m) and torch.equal(p.masked_fill(n, 0), q.masked_fill(m, 0))
+
+
+@pytest.mark.parametrize("d", [44, 45, 3])
+def test_fast_decays_are_no_resets(gpu, d):
+    """Decays of 0.06: their product over a block is 0, which cuts nothing off.
+    Resets that are all zero give what no resets give, and what is not finite
+    stays so up to a reset, also beside a decay that is NaN itself."""
+    L = 700
+    s = inputs(2, L, d, "f32", False, True, False, seed=20)
+    s["lam"][::2], s["lam"][1], s["lam"][d - 1] = 0.0, 0.0, 0.0
+    s["r"] *= 0.1
+    nan, inf = float("nan"), float("inf")
+    s["x"][0, 100, 0], s["x"][1, 130, 0] = nan, inf
+    s["h0"][1, 1] = nan
+    s["r"][0, 298, 1] = nan
+    s["dy"][0, 650, d - 1], s["dh_last"][1, d - 1] = nan, inf
+    zeros = torch.zeros(2, L, dtype=torch.uint8, device=DEV)
+
+    def run(reset):
+        hl, states = torch.empty(2, d, device=DEV), gpu.gated_scan_states(s["x"])
+        y = gpu.gated_scan_fwd(s["x"], s["r"], s["i"], s["lam"], reset=reset, h0=s["h0"],
+                               h_last=hl, states=states)
+        g = gpu.gated_scan_bwd(s["x"], s["r"], s["i"], s["lam"], s["dy"], states, reset=reset,
+                               dh_last=s["dh_last"])
+        return {"y": y, "h_last": hl, "states": states, **{k: g[k] for k in g if g[k] is not None}}
+
+    none, zero = run(None), run(zeros)
+    for k in none:
+        assert same_with_nan(none[k], zero[k]), k
+    y, hl, dx = zero["y"], zero["h_last"], zero["dx"]
+    assert torch.isnan(y[0, 100:, 0]).all() and torch.isnan(hl[0, 0])
+    assert not torch.isfinite(y[1, 130:, 0]).any() and not torch.isfinite(hl[1, 0])
+    assert torch.isnan(y[1, :, 1]).all() and torch.isnan(y[0, 298:, 1]).all()
+    assert torch.isnan(dx[0, :651, d - 1]).all() and torch.isfinite(dx[0, 651:, d - 1]).all()
+    assert not torch.isfinite(dx[1, :, d - 1]).any()
+    # the same with resets at 300 and, in the second row, at 60
+    cut = zeros.clone()
+    cut[:, 300], cut[1, 60] = 1, 7
+    got = run(cut)
+    yr, _, hr = ref.gated_forward(s["x"], s["r"], s["i"], s["lam"], None, s["h0"], cut)
+    rest = torch.isfinite(yr)
+    assert rest[:, 300:].all() and (torch.isfinite(got["y"]).cpu() == rest).all()
+    assert_within(torch.where(rest.to(DEV), got["y"], torch.zeros_like(y)),
+                  torch.where(rest, yr, torch.zeros_like(yr)).numpy(), "f32")
+    assert_within(got["h_last"], hr.numpy(), "f32")
+    dx = got["dx"]
+    assert torch.isnan(dx[0, 300:651, d - 1]).all() and not torch.isfinite(dx[1, 300:, d - 1]).any()
+    assert torch.isfinite(dx[:, :300, d - 1]).all() and torch.isfinite(dx[0, 651:, d - 1]).all()
+    assert torch.isfinite(got["dh0"][:, d - 1]).all()
