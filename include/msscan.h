@@ -42,7 +42,8 @@
  *       A              : [d_inner][d_state]       (fp32)
  *       D, delta_bias  : [d_inner]                (fp32)
  *       h0, h_last, h  : [batch][d_inner][d_state] (fp32)
- *   - Every base pointer must be 16-byte aligned (MS_ERR_ALIGN otherwise).
+ *   - Every base pointer must be 16-byte aligned (MS_ERR_ALIGN otherwise),
+ *     except where a section below asks for less.
  *   - Validation is synchronous and host-only: on any error status nothing has
  *     been launched.  Work is enqueued on `stream` (a hipStream_t; NULL means
  *     the default stream) and outputs are valid once the stream reaches it.
@@ -72,7 +73,7 @@ typedef enum {
     MS_ERR_SHAPE = 2,       /* a size is out of range                           */
     MS_ERR_DTYPE = 3,       /* io is not MS_F32 or MS_BF16                      */
     MS_ERR_FLAGS = 4,       /* unknown flag bits, or MS_ZOH with MS_BILINEAR    */
-    MS_ERR_ALIGN = 5,       /* a base pointer is not 16-byte aligned            */
+    MS_ERR_ALIGN = 5,       /* a base pointer is not aligned as it has to be    */
     MS_ERR_WORKSPACE = 6,   /* workspace missing or smaller than required       */
     MS_ERR_UNSUPPORTED = 7, /* valid request this library does not serve        */
     MS_ERR_HIP = 8          /* a HIP runtime call failed (text: ms_last_error)  */
@@ -359,6 +360,7 @@ ms_status ms_conv1d_silu(const void* x, const float* weight, const float* bias,
  *   y             : [batch][seqlen][d_inner] io dtype
  *   lam           : [d_inner] fp32
  *   sharpness     : > 0 and finite (MS_ERR_SHAPE otherwise)
+ *   alignment     : lam, reset, dy and dh_last need their element's only
  *   reset         : [batch][seqlen] bytes, optional.  A nonzero byte starts a
  *                   new sequence there: nothing of the state before it comes
  *                   through, NaN and infinities included (nor does anything
@@ -419,6 +421,7 @@ ms_status ms_gated_step(float* h, const void* x_t, const void* r_t, const void* 
  *   dweight  : [rows][dim] grad_dtype (MS_F32 or MS_BF16); every row is
  *              written, zero where no id names it.
  *   padding  : an id whose row gets no gradient, or -1.
+ *   alignment: ids and dy need their element's only
  *   n in 0 .. 2^31-1 (0: the lookup does nothing, the gradient is all zero);
  *   rows in 1 .. 2^31-1; dim in 1 .. 2^24; scale finite.
  *   workspace: ms_embed_bwd_workspace_bytes, 16-byte aligned, no
@@ -454,6 +457,8 @@ ms_status ms_embed_bwd(const void* ids, int32_t id_bits, const void* dy, float s
  *             the sum beside a large maximum)
  *   top     : 0 .. 64 and <= vocab; top_logprob [rows][top] fp32 and top_id
  *             [rows][top] int32 are required when it is not 0
+ *   alignment: targets, and what the gradient reads per row, need their
+ *             element's only
  *   rows in 0 .. 2^24-1 (0: nothing is done; MS_ERR_UNSUPPORTED past it), vocab
  *   in 1 .. 2^31-1, scale > 0 and finite.
  * Masked logits of -inf have probability 0 and add nothing to the entropy.  A

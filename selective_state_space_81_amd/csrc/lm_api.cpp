@@ -35,6 +35,16 @@ ms_status check_aligned(std::initializer_list<const void*> ptrs) {
     return MS_OK;
 }
 
+// What is read element by element, or in vectors that assume no more.
+ms_status check_element_aligned(size_t size, std::initializer_list<const void*> ptrs) {
+    for (const void* p : ptrs)
+        if (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(size - 1))
+            return fail(MS_ERR_ALIGN, "pointer %p is not aligned to its element", p);
+    return MS_OK;
+}
+
+size_t io_size(int32_t io) { return io == MS_BF16 ? 2 : 4; }
+
 ms_status check_io(int32_t io, const char* name = "io") {
     if (io != MS_F32 && io != MS_BF16)
         return fail(MS_ERR_DTYPE, "%s=%d is not MS_F32 (0) or MS_BF16 (1)", name, io);
@@ -88,15 +98,10 @@ ms_status check_sharpness(float c) {
 // Rows of x, r, i and z, `most` bytes long at the most, and their alignment.
 ms_status check_rows(int32_t d_inner, int64_t ld, int32_t io, int64_t most,
                      std::initializer_list<const void*> ptrs) {
-    const int64_t e = io == MS_BF16 ? 2 : 4;
     if (ld < d_inner) return fail(MS_ERR_SHAPE, "ld=%lld is below d_inner", (long long)ld);
-    if (ld > most / e)
+    if (ld > most / (int64_t)io_size(io))
         return fail(MS_ERR_UNSUPPORTED, "rows of ld=%lld values are too long", (long long)ld);
-    if (ld == d_inner) return check_aligned(ptrs);
-    for (const void* p : ptrs)
-        if (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(e - 1))
-            return fail(MS_ERR_ALIGN, "pointer %p is not aligned to its element", p);
-    return MS_OK;
+    return ld == d_inner ? check_aligned(ptrs) : check_element_aligned(io_size(io), ptrs);
 }
 
 int64_t state_rows(int64_t seqlen) { return (seqlen + kGatedBlock - 1) / kGatedBlock; }
@@ -158,7 +163,8 @@ ms_status ms_gated_scan_fwd(const void* x, const void* r, const void* i, const f
     if ((st = check_sharpness(sharpness)) != MS_OK) return st;
     if (!x || !r || !i || !lam || !y) return fail(MS_ERR_NULL, "x, r, i, lam and y are required");
     if ((st = check_rows(d_inner, ld, io, kMaxRowBytes, {x, r, i, z})) != MS_OK) return st;
-    if ((st = check_aligned({lam, reset, y, h0, h_last, states, workspace})) != MS_OK) return st;
+    if ((st = check_aligned({y, h0, h_last, states, workspace})) != MS_OK) return st;
+    if ((st = check_element_aligned(4, {lam})) != MS_OK) return st;
     if ((st = check_workspace(ms_gated_scan_workspace_bytes(batch, seqlen, d_inner, io), workspace,
                               workspace_bytes)) != MS_OK)
         return st;
@@ -190,9 +196,9 @@ ms_status ms_gated_scan_bwd(const void* x, const void* r, const void* i, const f
         return fail(MS_ERR_NULL, "x, r, i, lam, states, dy, dx, dr, di and dlam are required");
     if (z && !dz) return fail(MS_ERR_NULL, "dz is required when z is given");
     if ((st = check_rows(d_inner, ld, io, kMaxRowBytes, {x, r, i, z})) != MS_OK) return st;
-    if ((st = check_aligned({lam, reset, states, dy, dh_last, dx, dr, di, dz, dlam, dh0,
-                             workspace})) != MS_OK)
-        return st;
+    if ((st = check_aligned({states, dx, dr, di, dz, dlam, dh0, workspace})) != MS_OK) return st;
+    if ((st = check_element_aligned(io_size(io), {dy})) != MS_OK) return st;
+    if ((st = check_element_aligned(4, {lam, dh_last})) != MS_OK) return st;
     if ((st = check_workspace(ms_gated_scan_bwd_workspace_bytes(batch, seqlen, d_inner, io),
                               workspace, workspace_bytes)) != MS_OK)
         return st;
@@ -217,7 +223,8 @@ ms_status ms_gated_step(float* h, const void* x_t, const void* r_t, const void* 
         return fail(MS_ERR_NULL, "h, x_t, r_t, i_t, lam and y_t are required");
     if ((st = check_rows(d_inner, ld, io, (int64_t)1 << 40, {x_t, r_t, i_t, z_t})) != MS_OK)
         return st;
-    if ((st = check_aligned({h, lam, y_t})) != MS_OK) return st;
+    if ((st = check_aligned({h, y_t})) != MS_OK) return st;
+    if ((st = check_element_aligned(4, {lam})) != MS_OK) return st;
     GatedArgs a{};
     a.x = x_t; a.r = r_t; a.i = i_t; a.z = z_t; a.lam = lam; a.h_last = h; a.y = y_t;
     a.sharp = sharpness; a.L = 1; a.batch = batch; a.Dn = d_inner; a.ld = ld;
@@ -237,7 +244,8 @@ ms_status ms_embed_fwd(const void* ids, int32_t id_bits, const void* weight, flo
     if ((st = check_scale(scale, false)) != MS_OK) return st;
     if (n == 0) return MS_OK;
     if (!ids || !weight || !out) return fail(MS_ERR_NULL, "ids, weight and out are required");
-    if ((st = check_aligned({ids, weight, out})) != MS_OK) return st;
+    if ((st = check_aligned({weight, out})) != MS_OK) return st;
+    if ((st = check_element_aligned(id_bits / 8, {ids})) != MS_OK) return st;
     EmbedArgs a{};
     a.ids = ids; a.wide = id_bits == 64; a.weight = weight; a.scale = scale; a.out = out; a.n = n;
     a.rows = rows; a.D = dim;
@@ -267,7 +275,9 @@ ms_status ms_embed_bwd(const void* ids, int32_t id_bits, const void* dy, float s
     if ((st = check_scale(scale, false)) != MS_OK) return st;
     if (!dweight || (n && (!ids || !dy)))
         return fail(MS_ERR_NULL, "ids, dy and dweight are required");
-    if ((st = check_aligned({ids, dy, dweight, workspace})) != MS_OK) return st;
+    if ((st = check_aligned({dweight, workspace})) != MS_OK) return st;
+    if ((st = check_element_aligned(id_bits / 8, {ids})) != MS_OK) return st;
+    if ((st = check_element_aligned(io_size(io), {dy})) != MS_OK) return st;
     EmbedArgs a{};
     a.ids = ids; a.wide = id_bits == 64; a.dy = dy; a.scale = scale; a.padding = padding;
     a.dweight = dweight; a.n = n; a.rows = rows; a.D = dim;
@@ -303,9 +313,10 @@ ms_status ms_token_logprobs_fwd(const void* logits, int64_t ld, const void* targ
     if (!logits || (logprob && !targets) || (top && (!top_logprob || !top_id)))
         return fail(MS_ERR_NULL, "logits are required, targets with logprob, and top_logprob and "
                                  "top_id with top");
-    if ((st = check_aligned({logits, targets, logprob, entropy, lse, stats, top_logprob,
-                             top_id, workspace})) != MS_OK)
+    if ((st = check_aligned({logits, logprob, entropy, lse, stats, top_logprob, top_id, workspace})) !=
+        MS_OK)
         return st;
+    if ((st = check_element_aligned(id_bits / 8, {targets})) != MS_OK) return st;
     LogprobArgs a{};
     a.logits = logits; a.targets = targets; a.wide = id_bits == 64; a.logprob = logprob;
     a.entropy = entropy; a.lse = lse; a.stats = stats; a.top = top; a.top_logprob = top_logprob; a.top_id = top_id;
@@ -336,8 +347,9 @@ ms_status ms_token_logprobs_bwd(const void* logits, int64_t ld, const void* targ
                                  "entropy with dentropy");
     if (dlogits == logits && ld != ldd)
         return fail(MS_ERR_SHAPE, "dlogits over logits needs ldd == ld");
-    if ((st = check_aligned({logits, targets, stats, entropy, dlogprob, dentropy, dlogits})) != MS_OK)
-        return st;
+    if ((st = check_aligned({logits, dlogits})) != MS_OK) return st;
+    if ((st = check_element_aligned(id_bits / 8, {targets})) != MS_OK) return st;
+    if ((st = check_element_aligned(4, {stats, entropy, dlogprob, dentropy})) != MS_OK) return st;
     LogprobArgs a{};
     a.logits = logits; a.targets = targets; a.wide = id_bits == 64;
     a.stats = const_cast<float*>(stats);      // only read

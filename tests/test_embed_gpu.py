@@ -210,3 +210,24 @@ def test_refusals(gpu):
     with pytest.raises(gpu.MsError, match="workspace"):
         gpu.embed_bwd(ids, torch.zeros(4000, 8, device=DEV), 10,
                       workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [50, 7000])
+def test_ids_and_gradients_off_16_bytes(gpu, n, io):
+    """ids after the first of a text, and gradients as torch.cat hands them on:
+    contiguous, aligned to their element."""
+    g = gen(n)
+    text = torch.randint(0, 90, (n + 1,), generator=g, device=DEV)
+    dy = torch.randn(n * 37 + 1, generator=g, device=DEV).to(IO[io])[1:].view(n, 37)
+    w = torch.randn(90, 37, generator=g, device=DEV).to(IO[io])
+    for ids in (text[1:], text.int()[1:]):
+        assert ids.data_ptr() % 16 and dy.data_ptr() % 16
+        assert torch.equal(gpu.embed_fwd(ids, w), w[ids.long()])
+        assert torch.equal(gpu.embed_bwd(ids, dy, 90), gpu.embed_bwd(ids.clone(), dy.clone(), 90))
+    one = w.clone().requires_grad_()
+    up = torch.randn(n + 3, 37, generator=g, device=DEV).to(IO[io])
+    (torch.cat([gpu.embed(text[:3], one), gpu.embed(text[1:], one)]) * up).sum().backward()
+    want = gpu.embed_bwd(text[:3].clone(), up[:3].clone(), 90, scale=37 ** 0.5) + \
+        gpu.embed_bwd(text[1:].clone(), up[3:].clone(), 90, scale=37 ** 0.5)
+    assert torch.equal(one.grad, want)

@@ -60,3 +60,14 @@ def test_packed_documents_are_apart(lm):
     t = both.reshape(-1)
     x, y = (ms.token_logprobs_fwd(v, t)["logprob"] for v in (packed, alone))
     assert (x - y).abs().max() < 0.05
+
+
+def test_loss_of_one_row(lm):
+    """The targets of one row are a view into its tokens; the loss is the one
+    that two equal rows have (projections of other sizes, 0.05 as above)."""
+    model = lm.Model().cuda()
+    tokens, reset = (t.cuda() for t in lm.documents(torch.Generator().manual_seed(1), 1, 50))
+    one = lm.loss_of(model, tokens, reset, bonus=0.01)
+    one.backward()
+    two = lm.loss_of(model, tokens.repeat(2, 1), reset.repeat(2, 1), bonus=0.01)
+    assert torch.isfinite(one) and abs(float(one - two)) < 0.05

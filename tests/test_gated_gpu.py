@@ -438,3 +438,39 @@ def test_fast_decays_are_no_resets(gpu, d):
     assert torch.isnan(dx[0, 300:651, d - 1]).all() and not torch.isfinite(dx[1, 300:, d - 1]).any()
     assert torch.isfinite(dx[:, :300, d - 1]).all() and torch.isfinite(dx[0, 651:, d - 1]).all()
     assert torch.isfinite(got["dh0"][:, d - 1]).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_gradients_off_16_bytes(gpu, io):
+    """Gradients as torch.cat hands them on, resets and rates inside a larger
+    buffer: contiguous, aligned to their element."""
+    s = inputs(3, 41, 37, io, True, True, True, seed=21)
+    off = {}
+    for k in ("dy", "dh_last", "reset", "lam"):
+        off[k] = torch.cat([s[k].flatten()[:1], s[k].flatten()])[1:].view(s[k].shape)
+        assert off[k].data_ptr() % 16
+    leaves = [{k: s[k].clone().requires_grad_() for k in ("x", "r", "i", "lam", "z", "h0")}
+              for _ in range(2)]
+    for t, v in zip(leaves, (s, off)):
+        # t["lam"] itself is aligned; the raw calls below take the one that is not
+        y, hl = gpu.gated_scan(t["x"], t["r"], t["i"], t["lam"], t["z"], t["h0"],
+                               reset=v["reset"], return_last=True)
+        if v is off:
+            pad = lambda u: torch.cat([u.new_zeros(1), u.flatten()])  # noqa: E731
+            ((pad(y) * pad(s["dy"])).sum() + (pad(hl) * pad(s["dh_last"])).sum()).backward()
+        else:
+            torch.autograd.backward([y, hl], [s["dy"], s["dh_last"]])
+    for k in leaves[0]:
+        assert torch.equal(leaves[0][k].grad, leaves[1][k].grad), k
+    out = []
+    for v in (s, off):
+        states = gpu.gated_scan_states(s["x"])
+        y = gpu.gated_scan_fwd(s["x"], s["r"], s["i"], v["lam"], s["z"], reset=v["reset"],
+                               h0=s["h0"], states=states)
+        g = gpu.gated_scan_bwd(s["x"], s["r"], s["i"], v["lam"], v["dy"], states, s["z"],
+                               reset=v["reset"], dh_last=v["dh_last"])
+        h = s["h0"].clone()
+        yt = gpu.gated_step(h, *(s[k][:, 3].contiguous() for k in ("x", "r", "i")), v["lam"])
+        out.append([y, h, yt] + [g[k] for k in sorted(g)])
+    for a, b in zip(*out):
+        assert torch.equal(a, b)

@@ -235,3 +235,58 @@ def test_buffers_come_from_the_stream_of_the_call(monkeypatch, as_int):
         there = [current] if of is side else []
         assert out.recorded == there and several[0].recorded == there and ws.recorded == []
         assert call.workspace(None, 0) == (None, 0)
+
+
+def test_alignment_of_what_is_read_by_element():
+    """ids, targets, resets, rates and gradients need their element's alignment
+    only.  Each call is refused for something that is checked after it."""
+    lib = ms.load()
+    none, large = 6, 7  # no workspace, too large a launch
+    many = (1 << 31) - 1
+
+    def fwd(lam=P, reset=None):
+        return lib.ms_gated_scan_fwd(P, P, P, lam, 8.0, None, reset, P, None, None, None, 1, 4000, 8,
+                                     8, 1, None, 0, None)
+
+    assert fwd() == none and fwd(lam=P + 4) == none and fwd(reset=P + 1) == none
+    assert fwd(lam=P + 2) == 5
+
+    def bwd(lam=P, reset=None, dy=P, dh_last=None, states=P, io=1):
+        return lib.ms_gated_scan_bwd(P, P, P, lam, 8.0, None, reset, states, dy, dh_last, P, P, P,
+                                     None, P, None, 1, 4000, 8, 8, io, None, 0, None)
+
+    assert bwd() == none and bwd(lam=P + 4, reset=P + 3, dy=P + 2, dh_last=P + 4) == none
+    assert bwd(dy=P + 4, io=0) == none and bwd(states=P + 4) == 5
+    assert bwd(dy=P + 1) == 5 and bwd(dy=P + 2, io=0) == 5 and bwd(dh_last=P + 2) == 5
+
+    def step(lam):
+        return lib.ms_gated_step(P, P, P, P, lam, 8.0, None, P, 65535, 65539, 65539, 1, None)
+
+    assert step(P + 4) == large and step(P + 2) == 5
+
+    def lookup(ids, bits):
+        return lib.ms_embed_fwd(ids, bits, P, 1.0, P, many, 10, 1 << 12, 0, None)
+
+    assert lookup(P + 8, 64) == large and lookup(P + 4, 32) == large
+    assert lookup(P + 4, 64) == 5 and lookup(P + 2, 32) == 5
+
+    def table(ids=P, bits=64, dy=P, io=1):
+        return lib.ms_embed_bwd(ids, bits, dy, 1.0, -1, P, 0, 5000, 10, 8, io, None, 0, None)
+
+    assert table(ids=P + 8, dy=P + 2) == none and table(ids=P + 4, bits=32, dy=P + 4, io=0) == none
+    assert table(ids=P + 4) == 5 and table(dy=P + 1) == 5 and table(dy=P + 2, io=0) == 5
+
+    def logp(t, bits):
+        return lib.ms_token_logprobs_fwd(P, 100000, t, bits, 1.0, P, P, P, P, 0, None, None, 1, 100000,
+                                         0, None, 0, None)
+
+    assert logp(P + 8, 64) == none and logp(P + 4, 32) == none
+    assert logp(P + 4, 64) == 5 and logp(P + 1, 32) == 5
+
+    def grad(t=P, stats=P, ent=P, gl=P, gh=P):
+        return lib.ms_token_logprobs_bwd(P, 1 << 20, t, 64, 1.0, stats, ent, gl, gh, P, 1 << 20,
+                                         (1 << 24) - 1, 1 << 20, 0, None)
+
+    assert grad(t=P + 8, stats=P + 4, ent=P + 12, gl=P + 4, gh=P + 8) == large
+    for bad in ("stats", "ent", "gl", "gh", "t"):
+        assert grad(**{bad: P + 2}) == 5, bad

@@ -289,3 +289,23 @@ def test_many_infinities(gpu, rows, vocab, io):
     r = gpu.token_logprobs_fwd(x, t)
     d = gpu.token_logprobs_bwd(x, t, r["stats"], r["entropy"], gl, gh)
     assert torch.isfinite(d[5:]).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_targets_and_gradients_off_16_bytes(gpu, io):
+    """Targets after the first of a text, and gradients as torch.cat hands them
+    on: contiguous, aligned to their element."""
+    x, t = make(12, 3001, io, seed=12)
+    for u in (t[1:], t.int()[1:]):
+        assert u.data_ptr() % 16
+        check(gpu, x[:11], u, top=5)
+    a, b = (v.clone().requires_grad_() for v in (x[:5], x[5:11]))
+    lp, ent = (torch.cat(v) for v in zip(gpu.token_logprobs(a, t[:5])[:2],
+                                         gpu.token_logprobs(b, t[6:12])[:2]))
+    gl, gh = upstream(11, 6)
+    (lp * gl + ent * gh).sum().backward()
+    for v, u, k in ((a, t[:5], slice(0, 5)), (b, t[6:12], slice(5, 11))):
+        r = gpu.token_logprobs_fwd(v.detach(), u)
+        want = gpu.token_logprobs_bwd(v.detach(), u, r["stats"], r["entropy"], gl[k].clone(),
+                                      gh[k].clone())
+        assert torch.equal(v.grad, want)
