@@ -48,7 +48,9 @@ PyObject* io(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // rows(x, dims, *ts): 2 ld + io code, where x is a device tensor of dims
 // dimensions and MS_F32 or MS_BF16, whose rows (the last dimension) are
 // contiguous and ld apart, in order, and each of ts is None or has the same
-// dtype, sizes, device and ld; -1 of anything else.
+// dtype, sizes, device and ld; -1 of anything else.  A row that is alone has no
+// ld: where one of them does not begin on 16 bytes it is a slice of a wider
+// row, and has the ld of one.
 int64_t row_pitch(const at::Tensor& t) {
     const int64_t dims = t.dim(), d = t.size(dims - 1);
     if (d > 1 && t.stride(dims - 1) != 1) return -1;
@@ -68,14 +70,21 @@ PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!x || !x->is_cuda() || x->layout() != at::kStrided || x->dim() != PyLong_AsLong(a[1]) ||
         (x->scalar_type() != at::kFloat && x->scalar_type() != at::kBFloat16))
         return PyLong_FromLong(-1);
-    const int64_t ld = row_pitch(*x);
+    int64_t ld = row_pitch(*x);
     bool ok = ld >= 0;
+    const bool alone = x->numel() && x->numel() == x->size(-1);
+    auto off = [&](const at::Tensor& t) {
+        return alone && (reinterpret_cast<uintptr_t>(t.const_data_ptr()) & 15u);
+    };
+    bool slice = off(*x);
     for (Py_ssize_t k = 2; ok && k < n; ++k) {
         if (a[k] == Py_None) continue;
         const at::Tensor* t = tensor_of(a[k]);
         ok = t && t->layout() == at::kStrided && t->scalar_type() == x->scalar_type() &&
              t->sizes() == x->sizes() && t->device() == x->device() && row_pitch(*t) == ld;
+        slice = slice || (ok && off(*t));
     }
+    ld += slice;
     const int64_t io = x->scalar_type() == at::kFloat ? MS_F32 : MS_BF16;
     return PyLong_FromLongLong(ok ? 2 * ld + io : -1);
     END_HANDLE_TH_ERRORS

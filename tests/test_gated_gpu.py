@@ -474,3 +474,25 @@ def test_gradients_off_16_bytes(gpu, io):
         out.append([y, h, yt] + [g[k] for k in sorted(g)])
     for a, b in zip(*out):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d,off", [(36, 3), (33, 1), (64, 0), (2, 1), (10, 0)])
+def test_slices_of_one_row(gpu, io, d, off):
+    """One row has no distance to the next, and is still a slice of a wider one."""
+    s = inputs(1, 1, d, io, True, True, False, seed=d)
+    wide = torch.zeros(1, 1, 4 * d + off + 5, device=DEV).to(IO[io])
+    v = [wide[..., off + k * d:off + (k + 1) * d] for k in range(4)]
+    for a, name in zip(v, ("x", "r", "i", "z")):
+        a.copy_(s[name])
+    out = []
+    for x, r, i, z in ([s[k] for k in ("x", "r", "i", "z")], v):
+        h, states, hl = s["h0"].clone(), gpu.gated_scan_states(x), torch.empty(1, d, device=DEV)
+        y = gpu.gated_scan_fwd(x, r, i, s["lam"], z, h0=s["h0"], h_last=hl, states=states)
+        g = gpu.gated_scan_bwd(x, r, i, s["lam"], s["dy"], states, z, dh_last=s["dh_last"])
+        yt = gpu.gated_step(h, x[0], r[0], i[0], s["lam"], z[0])
+        assert_within(yt, y[0].double().cpu().numpy(), io)
+        assert_within(h, hl.double().cpu().numpy(), "f32")
+        out.append([y, hl, states, h, yt] + [g[k] for k in sorted(g)])
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
