@@ -477,6 +477,7 @@ def _functions():
     class GatedScan(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, r, i, lam, z, h0, c, reset):
+            reset = None if reset is None else reset.contiguous()
             states = gated_scan_states(x)
             h_last = torch.empty(x.shape[0], x.shape[2], dtype=torch.float32, device=x.device)
             y = gated_scan_fwd(x, r, i, lam, z, c=c, reset=reset, h0=h0, h_last=h_last,
@@ -499,6 +500,7 @@ def _functions():
     class Embed(torch.autograd.Function):
         @staticmethod
         def forward(ctx, ids, weight, scale, padding):
+            ids = ids.contiguous()
             ctx.save_for_backward(ids)
             ctx.rows, ctx.scale, ctx.padding = weight.shape[0], scale, padding
             return embed_fwd(ids, weight, scale=scale)
@@ -512,6 +514,7 @@ def _functions():
     class TokenLogprobs(torch.autograd.Function):
         @staticmethod
         def forward(ctx, logits, targets, top, scale):
+            targets = None if targets is None else targets.contiguous()
             r = token_logprobs_fwd(logits, targets, top=top, scale=scale)
             ctx.save_for_backward(logits, targets, r["stats"], r["entropy"])
             ctx.scale = scale
@@ -534,15 +537,15 @@ def gated_scan(x, r, i, lam, z=None, h0=None, *, c=8.0, reset=None, return_last=
     """The gated linear recurrence as a differentiable torch operation
     (ms_gated_scan_fwd with its saved states, ms_gated_scan_bwd).  Returns y,
     or (y, h_last) with return_last; gradients reach every tensor argument
-    but reset."""
+    but reset, which may be a slice of a wider one."""
     y, h_last = _functions()[0].apply(x, r, i, lam, z, h0, c, reset)
     return (y, h_last) if return_last else y
 
 
 def embed(ids, weight, *, scale=None, padding=-1):
-    """Embedding lookup as a differentiable torch operation; scale None means
-    sqrt(dim).  The gradient of the table is dense, in its dtype; the row
-    `padding` gets none."""
+    """Embedding lookup as a differentiable torch operation for ids of any
+    shape and strides; scale None means sqrt(dim).  The gradient of the table is
+    dense, in its dtype; the row `padding` gets none."""
     if scale is None:
         scale = math.sqrt(weight.shape[1])
     return _functions()[1].apply(ids, weight, scale, padding)
@@ -550,6 +553,6 @@ def embed(ids, weight, *, scale=None, padding=-1):
 
 def token_logprobs(logits, targets, *, top=0, scale=1.0):
     """Token log probabilities as a differentiable torch operation: (logprob,
-    entropy, top_logprob, top_id); gradients reach the logits from logprob and
-    entropy."""
+    entropy, top_logprob, top_id) for targets of any stride; gradients reach the
+    logits from logprob and entropy."""
     return _functions()[2].apply(logits, targets, top, scale)

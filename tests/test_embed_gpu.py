@@ -231,3 +231,15 @@ def test_ids_and_gradients_off_16_bytes(gpu, n, io):
     want = gpu.embed_bwd(text[:3].clone(), up[:3].clone(), 90, scale=37 ** 0.5) + \
         gpu.embed_bwd(text[1:].clone(), up[3:].clone(), 90, scale=37 ** 0.5)
     assert torch.equal(one.grad, want)
+
+
+def test_autograd_takes_slices_of_a_token_tensor(gpu):
+    g = gen(14)
+    tokens = torch.randint(0, 30, (4, 41), generator=g, device=DEV)
+    dy = torch.randn(4, 40, 16, generator=g, device=DEV)
+    grads = []
+    for ids in (tokens[:, :-1], tokens[:, :-1].contiguous()):
+        w = torch.randn(30, 16, generator=gen(15), device=DEV, requires_grad=True)
+        gpu.embed(ids, w).backward(dy)
+        grads.append(w.grad)
+    assert torch.equal(*grads)

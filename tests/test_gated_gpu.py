@@ -496,3 +496,11 @@ def test_slices_of_one_row(gpu, io, d, off):
         out.append([y, hl, states, h, yt] + [g[k] for k in sorted(g)])
     for a, b in zip(*out):
         assert torch.equal(a, b)
+
+
+def test_autograd_takes_slices_of_the_resets(gpu):
+    s = inputs(3, 50, 24, "f32", False, False, True, seed=22)
+    wide = torch.cat([s["reset"], torch.ones_like(s["reset"][:, :3])], 1)
+    a, b = (gpu.gated_scan(s["x"], s["r"], s["i"], s["lam"], reset=v)
+            for v in (wide[:, :50], wide.bool()[:, :50].contiguous()))
+    assert torch.equal(a, b)

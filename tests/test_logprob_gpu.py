@@ -309,3 +309,10 @@ def test_targets_and_gradients_off_16_bytes(gpu, io):
         want = gpu.token_logprobs_bwd(v.detach(), u, r["stats"], r["entropy"], gl[k].clone(),
                                       gh[k].clone())
         assert torch.equal(v.grad, want)
+
+
+def test_autograd_takes_slices_of_a_token_tensor(gpu):
+    x, _ = make(7, 200, "f32", seed=13)
+    tokens = torch.randint(0, 200, (7, 5), generator=torch.Generator().manual_seed(3)).to(DEV)
+    a, b = (gpu.token_logprobs(x, t)[0] for t in (tokens[:, 2], tokens[:, 2].contiguous()))
+    assert torch.equal(a, b)
