@@ -473,6 +473,8 @@ def _functions():
     if _fns is not None:
         return _fns
     import torch
+    # a gradient of a gradient would be missing what came through these: refused
+    from torch.autograd.function import once_differentiable
 
     class GatedScan(torch.autograd.Function):
         @staticmethod
@@ -488,6 +490,7 @@ def _functions():
             return y, h_last
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, dy, dh_last):
             x, r, i, lam, z, states, reset = ctx.saved_tensors
             dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
@@ -506,6 +509,7 @@ def _functions():
             return embed_fwd(ids, weight, scale=scale)
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, dy):
             ids, = ctx.saved_tensors
             return None, embed_bwd(ids, dy.contiguous(), ctx.rows, scale=ctx.scale,
@@ -523,6 +527,7 @@ def _functions():
             return r["logprob"], r["entropy"], r["top_logprob"], r["top_id"]
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, dlogprob, dentropy, _dtop, _did):
             logits, targets, stats, entropy = ctx.saved_tensors
             dlogprob, dentropy = (t if t is None else t.contiguous() for t in (dlogprob, dentropy))
@@ -536,16 +541,16 @@ def _functions():
 def gated_scan(x, r, i, lam, z=None, h0=None, *, c=8.0, reset=None, return_last=False):
     """The gated linear recurrence as a differentiable torch operation
     (ms_gated_scan_fwd with its saved states, ms_gated_scan_bwd).  Returns y,
-    or (y, h_last) with return_last; gradients reach every tensor argument
-    but reset, which may be a slice of a wider one."""
+    or (y, h_last) with return_last; gradients (of the first order) reach every
+    tensor argument but reset, which may be a slice of a wider one."""
     y, h_last = _functions()[0].apply(x, r, i, lam, z, h0, c, reset)
     return (y, h_last) if return_last else y
 
 
 def embed(ids, weight, *, scale=None, padding=-1):
     """Embedding lookup as a differentiable torch operation for ids of any
-    shape and strides; scale None means sqrt(dim).  The gradient of the table is
-    dense, in its dtype; the row `padding` gets none."""
+    shape and strides; scale None means sqrt(dim).  The gradient of the table (of the
+    first order) is dense, in its dtype; the row `padding` gets none."""
     if scale is None:
         scale = math.sqrt(weight.shape[1])
     return _functions()[1].apply(ids, weight, scale, padding)
@@ -553,6 +558,6 @@ def embed(ids, weight, *, scale=None, padding=-1):
 
 def token_logprobs(logits, targets, *, top=0, scale=1.0):
     """Token log probabilities as a differentiable torch operation: (logprob,
-    entropy, top_logprob, top_id) for targets of any stride; gradients reach the
-    logits from logprob and entropy."""
+    entropy, top_logprob, top_id) for targets of any stride; gradients (of
+    the first order) reach the logits from logprob and entropy."""
     return _functions()[2].apply(logits, targets, top, scale)

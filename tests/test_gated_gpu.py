@@ -504,3 +504,25 @@ def test_autograd_takes_slices_of_the_resets(gpu):
     a, b = (gpu.gated_scan(s["x"], s["r"], s["i"], s["lam"], reset=v)
             for v in (wide[:, :50], wide.bool()[:, :50].contiguous()))
     assert torch.equal(a, b)
+
+
+def second_order(outputs, inputs):
+    """First-order gradients that have a graph; differentiating them raises."""
+    loss = sum((o * o).sum() for o in outputs)
+    grads = torch.autograd.grad(loss, inputs, create_graph=True)
+    plain = torch.autograd.grad(sum((o * o).sum() for o in outputs), inputs, retain_graph=True)
+    for a, b in zip(grads, plain):
+        assert torch.equal(a.detach(), b)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        sum((g * g).sum() for g in grads).backward()
+
+
+def test_second_derivatives_are_refused(gpu):
+    """A gradient penalty would silently lose what goes through these."""
+    s = inputs(2, 30, 16, "f32", True, True, False, seed=23)
+    t = [s[k].clone().requires_grad_() for k in ("x", "r", "i", "lam", "z", "h0")]
+    second_order(gpu.gated_scan(*t, return_last=True), t)
+    w = torch.randn(20, 16, device=DEV, requires_grad=True)
+    second_order([gpu.embed(torch.arange(5, device=DEV), w)], [w])
+    x = torch.randn(4, 30, device=DEV, requires_grad=True)
+    second_order(gpu.token_logprobs(x, torch.arange(4, device=DEV))[:2], [x])
