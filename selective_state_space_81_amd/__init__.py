@@ -343,6 +343,7 @@ def _scan_function():
     global _scan_fn
     if _scan_fn is None:
         import torch
+        from torch.autograd.function import once_differentiable
 
         class ScanFn(torch.autograd.Function):
             @staticmethod
@@ -361,6 +362,7 @@ def _scan_function():
                 return y
 
             @staticmethod
+            @once_differentiable  # a gradient of a gradient would be missing this part
             def backward(ctx, dy):
                 u, delta, A, B, C, D, z, delta_bias, h0, ck = ctx.saved_tensors
                 softplus, zoh, bilinear = ctx.disc
@@ -383,8 +385,8 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, h0=None, 
                    softplus=True, zoh=False, bilinear=False, save_states=True):
     """The scan as a differentiable torch operation: the forward is
     ms_scan_fwd and the backward ms_scan_bwd (gradients of every tensor
-    argument; dB and dC are returned in B's and C's dtype).  With save_states,
-    where the checkpointed pair serves the dims (ms_scan_checkpoint_bytes > 0)
+    argument, of the first order; dB and dC are returned in B's and C's
+    dtype).  With save_states, where the checkpointed pair serves the dims (ms_scan_checkpoint_bytes > 0)
     the forward is ms_scan_fwd_checkpoint and its block states are kept for
     ms_scan_bwd_checkpoint (4 * d_state / 16 bytes per element) instead of
     being recomputed.  Returns y."""

@@ -72,3 +72,16 @@ def test_autograd_bf16_and_optional_terms(gpu):
     gu = u.grad.double().cpu().numpy()
     assert np.all(np.abs(gu - ref["du"]) <= 2.0 ** -8 * np.abs(ref["du"]) + 2e-4 *
                   (np.abs(ref["du"]) + np.sqrt(np.mean(ref["du"] ** 2))))
+
+
+def test_second_derivatives_are_refused(gpu):
+    """A gradient penalty would silently lose what goes through the scan."""
+    w = synth.workload("tiny", batch=1, L=40, Dn=16, N=8, io="f32")
+    x = synth.scan_inputs(w, device=DEV, seed=84)
+    u = x["u"].clone().requires_grad_(True)
+    y = gpu.selective_scan(u, x["delta"], x["A"], x["B"], x["C"])
+    g, = torch.autograd.grad((y * y).sum(), u, create_graph=True)
+    plain, = torch.autograd.grad((y * y).sum(), u, retain_graph=True)
+    assert torch.equal(g.detach(), plain)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (g * g).sum().backward()
