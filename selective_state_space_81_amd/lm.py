@@ -89,8 +89,12 @@ class _Call:
             if given != self.stream:
                 self.current = torch.cuda.current_stream(self.index)
                 self.stream = given
-                self.other = torch.cuda.ExternalStream(given, device=like.device) \
-                    if isinstance(stream, int) else stream
+                if not isinstance(stream, int):
+                    self.other = stream
+                elif given:
+                    self.other = torch.cuda.ExternalStream(given, device=like.device)
+                else:  # as an external handle 0 becomes a new stream
+                    self.other = torch.cuda.default_stream(self.index)
 
     def _make(self, make, *args):
         if self.other is None:

@@ -526,3 +526,14 @@ def test_second_derivatives_are_refused(gpu):
     second_order([gpu.embed(torch.arange(5, device=DEV), w)], [w])
     x = torch.randn(4, 30, device=DEV, requires_grad=True)
     second_order(gpu.token_logprobs(x, torch.arange(4, device=DEV))[:2], [x])
+
+
+def test_default_stream_by_its_handle(gpu):
+    s = inputs(2, 3000, 72, "bf16", True, False, False, seed=24)
+    want = gpu.gated_scan_fwd(s["x"], s["r"], s["i"], s["lam"], s["z"])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        assert gpu.lm._Call(gpu.lm._marshal(), s["x"], 0).other == torch.cuda.default_stream()
+        got = gpu.gated_scan_fwd(s["x"], s["r"], s["i"], s["lam"], s["z"], stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(want, got)

@@ -290,3 +290,17 @@ def test_alignment_of_what_is_read_by_element():
     assert grad(t=P + 8, stats=P + 4, ent=P + 12, gl=P + 4, gh=P + 8) == large
     for bad in ("stats", "ent", "gl", "gh", "t"):
         assert grad(**{bad: P + 2}) == 5, bad
+
+
+def test_handle_0_is_the_default_stream(monkeypatch):
+    """torch makes a stream of its own of an external handle of 0."""
+    current, default = (types.SimpleNamespace(cuda_stream=k) for k in (1, 0))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda k: 1, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda k=None: current)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda k=None: default)
+    monkeypatch.setattr(torch.cuda, "ExternalStream",
+                        lambda h, device=None: types.SimpleNamespace(cuda_stream=h or 77))
+    like = types.SimpleNamespace(get_device=lambda: 0, device="cuda:0")
+    call = ms.lm._Call(None, like, 0)
+    assert call.stream == 0 and call.other is default
+    assert ms.lm._Call(None, like, 5).other.cuda_stream == 5
