@@ -366,8 +366,12 @@ ms_status ms_conv1d_silu(const void* x, const float* weight, const float* bias,
  *                   through, NaN and infinities included (nor does anything
  *                   through a step whose decay is exactly 0).  Up to there a
  *                   state that is not finite stays so (an infinity may become
- *                   NaN), however far the decays' product has fallen.
- *   h0, h_last    : [batch][d_inner] fp32, optional.  h_last may equal h0.
+ *                   NaN), however far the decays' product has fallen.  The
+ *                   input keeps its factor sqrt(1 - a^2) at a reset, as at the
+ *                   first step without h0 (a model whose factor is 1 there has
+ *                   to scale x at those steps by 1 / sqrt(1 - a^2)).
+ *   h0, h_last    : [batch][d_inner] fp32, optional.  h_last may equal h0;
+ *                   other outputs must not overlap inputs.
  *   states        : optional; receives the state before steps 0, 16, 32, ...
  *                   ([batch][ceil(seqlen / 16)][d_inner] fp32, that is
  *                   ms_gated_scan_states_bytes), for ms_gated_scan_bwd.

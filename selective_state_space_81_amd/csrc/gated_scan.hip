@@ -891,14 +891,16 @@ __global__ void __launch_bounds__(256) gated_step(GatedArgs a) {
 
 // ---- variants -------------------------------------------------------------------------
 // The lanes across channels take a line of 128 bytes of bf16 in each row.  As
-// many steps a lane as registers hold without spills (3 waves a SIMD), since
-// each lane's map costs a scan over the lanes: with 2 channels a lane instead of
-// 4 the forward has half as many lanes to scan over.  Forward at 8 x 2048 x 1536
-// bf16 with the gate and at 131072 x 1536 without, in us: 58 and 333; 4 channels x
-// 8 steps a lane 60 and 349 (with 2 waves along time 59 and 497, with 8 70 and
-// 380), 1 x 32 73 and 331, 2 x 8 56 and 391 (shorter blocks make the chain of
-// messages longer).  Backward at the first: 100; 4 channels x 4 steps a lane 107
-// (with 2 waves along time 110, with 8 130), 1 x 16 110.
+// many steps a lane as registers hold (3 waves a SIMD; without resets nothing
+// spills, with them 36 to 57 scalar registers of the forward, and 5 vector
+// registers of the fp32 backward with the gate), since each lane's map costs a
+// scan over the lanes: with 2 channels a lane instead of 4 the forward has half as
+// many lanes to scan over.  Forward at 8 x 2048 x 1536 bf16 with the gate and at
+// 131072 x 1536 without, in us: 58 and 333; 4 channels x 8 steps a lane 60 and 349
+// (with 2 waves along time 59 and 497, with 8 70 and 380), 1 x 32 73 and 331, 2 x 8
+// 56 and 391 (shorter blocks make the chain of messages longer).  Backward at the
+// first: 100; 4 channels x 4 steps a lane 107 (with 2 waves along time 110, with 8
+// 130), 1 x 16 110.
 template <bool BF16>
 using Fwd = Geo<2, 32, 16, 4, BF16>;
 template <bool BF16>

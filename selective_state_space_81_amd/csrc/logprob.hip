@@ -15,20 +15,20 @@
 // Alternatives come from the same pass.  A wave holds a threshold that at least
 // `top` logits of the row reach: the top-th largest of the maxima of the
 // workgroup's lanes (or of groups of lanes, Threshold below) over their first
-// block.  A lane whose block of 32 (16 in fp32) logits reaches
-// it, known from the maximum that the softmax needs anyway, notes the block:
-// one comparison a block, and some four notes in 2000 logits at top 5.  At the
-// end the threshold is taken once more, from the maxima over all blocks, and
-// few of the noted blocks reach it; those are read again
-// (they are in cache), and each logit that reaches it finds its rank by
-// counting the larger ones of the workgroup, in LDS.
+// block.  A lane whose block of 16 (8 in fp32) logits reaches it, known from the
+// maximum that the softmax needs anyway, notes the block (logprob_notes.h): one
+// comparison a block, and some five notes in 4000 normal logits at top 5.  At the
+// end the threshold is taken once more, from the maxima over all blocks, and few
+// of the noted blocks reach it; those are read again (they are in cache), and
+// each logit that reaches it finds its rank by counting the larger ones of the
+// workgroup, in LDS.
 //
 // Measured (5.6 TB/s is what a copy reaches): 8192 x 50280 bf16 with 5
 // alternatives 148 to 182 us (824 MB, 5.6 to 4.5 TB/s, as much of it as is still
 // in the last-level cache); 8192 x 32001 bf16, none, 129 us, and its gradient 173
-// (1.05 GB, 6.1 TB/s); 64 x 131072 bf16 with 20 alternatives 12.5 + 4.2 us and
-// one row of 50280 fp32 6.2 + 3.6, both bound by latency: three trips to memory,
-// five barriers and a second launch.
+// (1.05 GB, 6.1 TB/s); 64 x 131072 bf16 with 20 alternatives 12.2 + 4.1 us and
+// one row of 50280 fp32 9.6, both bound by latency: three trips to memory, five
+// barriers and, in the first, a second launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
