@@ -470,6 +470,11 @@ def token_logprobs_bwd(logits, targets, stats, entropy=None, dlogprob=None, dent
 _fns = None
 
 
+def _aligned(t):
+    """t, or a copy of a tensor that begins off 16 bytes (the calls above refuse it)."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _functions():
     """The autograd Functions, built on first use (importing the package does
     not import torch)."""
@@ -484,6 +489,9 @@ def _functions():
         @staticmethod
         def forward(ctx, x, r, i, lam, z, h0, c, reset):
             reset = None if reset is None else reset.contiguous()
+            if x.is_contiguous():  # and no slice of a wider tensor, which may begin anywhere
+                x, r, i, z = map(_aligned, (x, r, i, z))
+            h0 = _aligned(h0)
             states = gated_scan_states(x)
             h_last = torch.empty(x.shape[0], x.shape[2], dtype=torch.float32, device=x.device)
             y = gated_scan_fwd(x, r, i, lam, z, c=c, reset=reset, h0=h0, h_last=h_last,
@@ -510,7 +518,7 @@ def _functions():
             ids = ids.contiguous()
             ctx.save_for_backward(ids)
             ctx.rows, ctx.scale, ctx.padding = weight.shape[0], scale, padding
-            return embed_fwd(ids, weight, scale=scale)
+            return embed_fwd(ids, _aligned(weight), scale=scale)
 
         @staticmethod
         @once_differentiable
@@ -523,6 +531,7 @@ def _functions():
         @staticmethod
         def forward(ctx, logits, targets, top, scale):
             targets = None if targets is None else targets.contiguous()
+            logits = _aligned(logits)
             r = token_logprobs_fwd(logits, targets, top=top, scale=scale)
             ctx.save_for_backward(logits, targets, r["stats"], r["entropy"])
             ctx.scale = scale

@@ -537,3 +537,26 @@ def test_default_stream_by_its_handle(gpu):
         got = gpu.gated_scan_fwd(s["x"], s["r"], s["i"], s["lam"], s["z"], stream=0)
     torch.cuda.synchronize()
     assert torch.equal(want, got)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_autograd_off_16_bytes(gpu, io):
+    """The differentiable operations take what begins at its element's alignment."""
+    def off(t):
+        return torch.cat([t.flatten()[:1], t.flatten()])[1:].view(t.shape)
+
+    s = inputs(2, 40, 33, io, True, True, False, seed=25)
+    names = ("x", "r", "i", "lam", "z", "h0")
+    grads = []
+    for f in (lambda t: t.clone(), off):
+        t = [f(s[k]).requires_grad_() for k in names]
+        assert f is not off or all(v.data_ptr() % 16 for v in t)
+        torch.autograd.backward(gpu.gated_scan(*t, return_last=True), [s["dy"], s["dh_last"]])
+        w = f(s["x"][0]).requires_grad_()
+        gpu.embed(torch.arange(9, device=DEV), w).backward(s["dy"][0, :9])
+        v = f(s["x"][1]).requires_grad_()
+        lp, ent = gpu.token_logprobs(v, torch.arange(40, device=DEV) % 33)[:2]
+        torch.autograd.backward([lp, ent], [s["h0"].flatten()[:40], s["h0"].flatten()[20:60]])
+        grads.append([k.grad for k in (*t, w, v)])
+    for a, b in zip(*grads):
+        assert torch.equal(a, b)
