@@ -489,6 +489,163 @@ ms_status ms_token_logprobs_bwd(const void* logits, int64_t ld, const void* targ
                                 const float* dentropy, void* dlogits, int64_t ldd, int64_t rows,
                                 int64_t vocab, int32_t io, void* stream);
 
+/*
+ * Linear attention with a decay for each head: a recurrence whose state is a
+ * matrix a head, computed in blocks of tokens on the matrix cores.  For every
+ * batch row and head, along t,
+ *
+ *   S   = exp(g[b,t,h]) * S + k_t v_t^T         (S starts at h0, else 0)
+ *   o_t = scale * S^T q_t
+ *
+ *   q, k          : [batch][seqlen] rows, ldq and ldk values apart, of kheads
+ *                   heads of dk io values.  kheads divides heads: head h reads
+ *                   q and k of head h / (heads / kheads).
+ *   v             : [batch][seqlen] rows, ldv apart, of heads heads of dv values
+ *                   (q, k and v may be column slices of one wider tensor and
+ *                   need no alignment beyond their element's)
+ *   g             : log decays, fp32: [batch][seqlen][heads], or [heads] when
+ *                   `fixed` is not 0.  Any value is computed as written; a
+ *                   decay that is 0 in fp32 (g below -104, -inf) drops the
+ *                   state as a reset does.
+ *   reset         : [batch][seqlen] bytes, optional.  A nonzero byte starts a
+ *                   new sequence there: the decay of that step is 0, and
+ *                   nothing of the state before it comes through, NaN and
+ *                   infinities included.
+ *   o             : [batch][seqlen][heads][dv] io dtype
+ *   h0, h_last    : [batch][heads][dk][dv] fp32, optional; h_last may equal h0.
+ *   states        : optional; receives what ms_linear_attn_bwd needs
+ *                   (ms_linear_attn_states_bytes bytes, in the kernels' order).
+ *   scale         : finite
+ *   workspace     : ms_linear_attn_workspace_bytes bytes (may be 0).
+ * batch, heads, kheads >= 1, seqlen in 1 .. 2^31-1, dk and dv in 1 .. 128
+ * (MS_ERR_UNSUPPORTED above, and where a launch would need more than 2^24 - 1
+ * workgroups).  q, k, v, d_o, g and dh_last need their element's alignment
+ * only.  Outputs must not overlap inputs, but for h_last.
+ * States, decays and sums are fp32 or more (products of bf16 with an fp32
+ * state take it in 24 bits where the result is fp32); with bf16 io the scores,
+ * and the state that a query meets, are rounded to bf16 ahead of the product
+ * that ends in o.  A token that is not finite reaches o from its own step on
+ * only.  Deterministic.
+ *
+ * ms_linear_attn_bwd: gradients for d_o ([batch][seqlen][heads][dv], io dtype)
+ *   and, optionally, dh_last, from the same inputs and the states the forward
+ *   saved (h0 is in them).  dq, d_k [batch][seqlen][kheads][dk] (sums over the
+ *   heads that share them) and d_v [batch][seqlen][heads][dv] in the io dtype; dg
+ *   of g's shape, fp32 (of fixed decays the sum over batch and time); dh0
+ *   [batch][heads][dk][dv] fp32, optional.  No gradient crosses a reset, and
+ *   the decay of one has gradient 0.
+ * ms_linear_attn_step: the next `tokens` (1 .. 64) tokens of every sequence
+ *   from the state h [batch][heads][dk][dv]; q, k, v, g as above with seqlen =
+ *   tokens, o [batch][tokens][heads][dv].
+ *   counts        : [batch] int32, optional: tokens of each row that are there
+ *                   (taken as 0 .. tokens).  The others do nothing, and their
+ *                   rows of o are left as they were.
+ *   update        : 0 leaves h as it was (drafted tokens scored ahead of their
+ *                   acceptance); else h is updated in place.
+ *   q             : may be NULL with update: the state moves on, o is not read.
+ */
+size_t ms_linear_attn_workspace_bytes(int32_t batch, int64_t seqlen, int32_t heads, int32_t kheads,
+                                      int32_t dk, int32_t dv, int32_t io);
+size_t ms_linear_attn_states_bytes(int32_t batch, int64_t seqlen, int32_t heads, int32_t dk,
+                                   int32_t dv, int32_t io);
+ms_status ms_linear_attn_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                             int64_t ldv, const float* g, int32_t fixed, float scale,
+                             const uint8_t* reset, void* o, const float* h0, float* h_last,
+                             float* states, int32_t batch, int64_t seqlen, int32_t heads,
+                             int32_t kheads, int32_t dk, int32_t dv, int32_t io, void* workspace,
+                             size_t workspace_bytes, void* stream);
+size_t ms_linear_attn_bwd_workspace_bytes(int32_t batch, int64_t seqlen, int32_t heads,
+                                          int32_t kheads, int32_t dk, int32_t dv, int32_t fixed,
+                                          int32_t io);
+ms_status ms_linear_attn_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                             int64_t ldv, const float* g, int32_t fixed, float scale,
+                             const uint8_t* reset, const float* states, const void* d_o,
+                             const float* dh_last, void* dq, void* d_k, void* d_v, float* dg,
+                             float* dh0, int32_t batch, int64_t seqlen, int32_t heads,
+                             int32_t kheads, int32_t dk, int32_t dv, int32_t io, void* workspace,
+                             size_t workspace_bytes, void* stream);
+ms_status ms_linear_attn_step(float* h, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                              const void* v, int64_t ldv, const float* g, int32_t fixed,
+                              float scale, const int32_t* counts, int32_t update, void* o,
+                              int32_t batch, int32_t tokens, int32_t heads, int32_t kheads,
+                              int32_t dk, int32_t dv, int32_t io, void* stream);
+
+/*
+ * Norm of each row's channels in groups (the heads of a linear attention),
+ * with scale, shift and a silu gate:
+ *
+ *   u   = x            or x * silu(z)            (gate_first != 0)
+ *   c   = u - mean(u)  (center != 0)   or u      over each group of a row
+ *   hat = c / sqrt(mean(c^2) + eps)
+ *   y   = hat * weight + bias                    (z NULL, or gate_first)
+ *       = (hat * weight + bias) * silu(z)        (z given)
+ *
+ *   x, z          : [rows], ldx and ldz values apart, of groups * size io
+ *                   values (z optional); slices of wider rows are read in place
+ *   weight, bias  : [groups * size] fp32, each optional (1 and 0)
+ *   y             : [rows][groups * size] io dtype
+ *   eps           : > 0 and finite
+ *   rows in 0 .. 2^31-1, groups >= 1, size in 1 .. 8192 (MS_ERR_UNSUPPORTED
+ *   above), groups * size up to 2^24.
+ * x, z, dy, weight and bias need their element's alignment only.  Sums are
+ * fp32, in an order that depends on the shape alone: deterministic.
+ *
+ * ms_group_norm_bwd: dx, dz (with z) [rows][groups * size] io dtype, dweight
+ *   and dbias [groups * size] fp32 (each optional) for dy [rows][groups * size].
+ *   workspace: ms_group_norm_bwd_workspace_bytes (not needed where neither
+ *   dweight nor dbias is asked for).  Outputs must not overlap inputs.
+ */
+ms_status ms_group_norm_fwd(const void* x, int64_t ldx, const float* weight, const float* bias,
+                            const void* z, int64_t ldz, int32_t center, int32_t gate_first,
+                            float eps, void* y, int64_t rows, int32_t groups, int32_t size,
+                            int32_t io, void* stream);
+size_t ms_group_norm_bwd_workspace_bytes(int64_t rows, int32_t groups, int32_t size, int32_t io);
+ms_status ms_group_norm_bwd(const void* x, int64_t ldx, const float* weight, const float* bias,
+                            const void* z, int64_t ldz, int32_t center, int32_t gate_first,
+                            float eps, const void* dy, void* dx, void* dz, float* dweight,
+                            float* dbias, int64_t rows, int32_t groups, int32_t size, int32_t io,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from
+ * given random numbers.  With p_t and q_t the probabilities exp(scale * logit) /
+ * sum of the target's and the drafting model's row t, drafts x_t are accepted
+ * one after another while
+ *
+ *   uniforms[b][t] * q_t(x_t) < p_t(x_t)
+ *
+ * and the next token is drawn: from max(p_t - q_t, 0) at the first draft t that
+ * is refused, from p_t behind the last (t = drafts) if none is.  Drawn is the
+ * first v whose cumulative mass exceeds uniforms[b][drafts] of the whole.
+ * Without draft_logits q_t is 1 at x_t and 0 elsewhere.
+ *
+ *   logits        : [batch][drafts + 1] rows of vocab io values, ld apart
+ *   draft_logits  : [batch][drafts] rows, ldd apart, optional
+ *   drafts_in     : [batch][drafts] int32 or int64 (id_bits).  One outside
+ *                   [0, vocab) is refused.
+ *   uniforms      : [batch][drafts + 1] fp32, in [0, 1)
+ *   tokens        : [batch][drafts + 1] int32: the accepted drafts, the token
+ *                   drawn, and -1 behind it
+ *   count         : [batch] int32: how many drafts were accepted
+ *   logprob       : [batch][drafts + 1] fp32: log p of each token, 0 where none
+ *   workspace     : ms_verify_drafts_workspace_bytes (drafted: draft_logits are
+ *                   given), 16-byte aligned
+ * drafts in 0 .. 64 (0: one token is drawn), vocab in 1 .. 2^31-1, scale > 0 and
+ * finite, batch >= 0.  All but the workspace need their element's alignment
+ * only.  Logits of -inf have probability 0.  Where nothing is left of p - q the
+ * token is drawn from p.  A row of the target that is no distribution (NaN,
+ * +inf, or all -inf) has its draft refused and gives token -1; such a row of
+ * the drafting model has its draft refused and counts as q = 0.  Everything
+ * is computed in fp64: deterministic, and borders fall where the formulas say.
+ */
+size_t ms_verify_drafts_workspace_bytes(int32_t batch, int32_t drafts, int64_t vocab,
+                                        int32_t drafted, int32_t io);
+ms_status ms_verify_drafts(const void* logits, int64_t ld, const void* draft_logits, int64_t ldd,
+                           const void* drafts_in, int32_t id_bits, const float* uniforms,
+                           float scale, int32_t* tokens, int32_t* count, float* logprob,
+                           int32_t batch, int32_t drafts, int64_t vocab, int32_t io,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* ms_status_string(ms_status s);
 

@@ -12,7 +12,12 @@ import ctypes
 import os
 from typing import Optional
 
-from . import lm
+from . import attn, lm
+from .attn import (group_norm, group_norm_bwd, group_norm_bwd_workspace_bytes,  # noqa: F401
+                   group_norm_fwd, linear_attn, linear_attn_bwd, linear_attn_bwd_workspace_bytes,
+                   linear_attn_fwd, linear_attn_states, linear_attn_states_bytes,
+                   linear_attn_step, linear_attn_workspace_bytes, verify_drafts,
+                   verify_drafts_workspace_bytes)
 from .lm import (embed, embed_bwd, embed_bwd_workspace_bytes, embed_fwd, gated_scan,  # noqa: F401
                  gated_scan_bwd, gated_scan_bwd_workspace_bytes, gated_scan_fwd,
                  gated_scan_states, gated_scan_workspace_bytes, gated_step, token_logprobs,
@@ -37,7 +42,7 @@ EXPORTS = ("ms_scan_workspace_bytes", "ms_scan_fwd", "ms_state_update", "ms_stat
            "ms_conv1d_silu", "ms_scan_bwd_workspace_bytes", "ms_scan_bwd",
            "ms_scan_fwd_dtproj", "ms_scan_dtproj_workspace_bytes", "ms_scan_fwd_noalloc",
            "ms_scan_checkpoint_bytes", "ms_scan_fwd_checkpoint",
-           "ms_scan_bwd_checkpoint_workspace_bytes", "ms_scan_bwd_checkpoint") + lm.EXPORTS
+           "ms_scan_bwd_checkpoint_workspace_bytes", "ms_scan_bwd_checkpoint") + lm.EXPORTS + attn.EXPORTS
 
 PHASES = ("prep", "summary", "carry", "main", "step", "conv", "reduce")  # ms_phase order
 
@@ -126,6 +131,7 @@ def load(path: Optional[str] = None):
     lib.ms_profile_end.restype = ctypes.c_int
     lib.ms_profile_end.argtypes = [ctypes.POINTER(MsProfile)]
     lm.declare(lib)
+    attn.declare(lib)
     if path is None:
         _lib = lib
     return lib

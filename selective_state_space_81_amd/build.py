@@ -32,6 +32,9 @@ SOURCES = [os.path.join(CSRC, "scan_kernels.hip"), os.path.join(CSRC, "scan_tile
            os.path.join(CSRC, "bwd_wide.hip"), os.path.join(CSRC, "bwd_row.hip"),
            os.path.join(CSRC, "gated_scan.hip"), os.path.join(CSRC, "embed.hip"),
            os.path.join(CSRC, "logprob.hip"), os.path.join(CSRC, "lm_api.cpp"),
+           os.path.join(CSRC, "linear_attn.hip"), os.path.join(CSRC, "linear_attn_bwd.hip"),
+           os.path.join(CSRC, "group_norm.hip"), os.path.join(CSRC, "verify.hip"),
+           os.path.join(CSRC, "attn_api.cpp"),
            os.path.join(CSRC, "api.cpp"), os.path.join(CSRC, "profile.cpp"),
            os.path.join(CSRC, "noalloc.hip")]
 ARCH = os.environ.get("MSSCAN_ARCH", "gfx950")

@@ -3,7 +3,7 @@
 // calls of the C ABI with tensors for pointers.  A decode step of 8 us of GPU
 // time has a dozen arguments; checked and converted one by one in Python they
 // took as long again.  What a refused argument is told, and everything else,
-// is in lm.py.
+// is in lm.py and attn.py.
 //
 // The library itself stays the one that the package loaded: bind() is given
 // the addresses of its entry points.
@@ -87,6 +87,34 @@ PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     ld += slice;
     const int64_t io = x->scalar_type() == at::kFloat ? MS_F32 : MS_BF16;
     return PyLong_FromLongLong(ok ? 2 * ld + io : -1);
+    END_HANDLE_TH_ERRORS
+}
+
+// pitch(x, dims, inner): 2 ld + io code, where x is a device tensor of dims
+// dimensions and MS_F32 or MS_BF16, whose last `inner` dimensions are one
+// contiguous row, the rows ld apart and in order; -1 of anything else.
+PyObject* pitch(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const at::Tensor* x = n == 3 ? tensor_of(a[0]) : nullptr;
+    if (!x || !x->is_cuda() || x->layout() != at::kStrided || x->dim() != PyLong_AsLong(a[1]) ||
+        (x->scalar_type() != at::kFloat && x->scalar_type() != at::kBFloat16))
+        return PyLong_FromLong(-1);
+    const int64_t dims = x->dim(), inner = PyLong_AsLong(a[2]);
+    const int64_t io = x->scalar_type() == at::kFloat ? MS_F32 : MS_BF16;
+    int64_t d = 1;
+    for (int64_t k = dims - 1; k >= dims - inner; --k) {
+        if (x->numel() && x->size(k) > 1 && x->stride(k) != d) return PyLong_FromLong(-1);
+        d *= x->size(k);
+    }
+    if (x->numel() == 0) return PyLong_FromLongLong(2 * d + io);
+    int64_t ld = -1, want = 0;  // -1: every dimension so far has one entry
+    for (int64_t k = dims - inner - 1; k >= 0; --k) {
+        if (x->size(k) == 1) continue;
+        if (ld < 0) ld = want = x->stride(k);
+        if (ld < d || x->stride(k) != want) return PyLong_FromLong(-1);
+        want *= x->size(k);
+    }
+    return PyLong_FromLongLong(2 * (ld < 0 ? d : ld) + io);
     END_HANDLE_TH_ERRORS
 }
 
@@ -225,7 +253,9 @@ PyObject* call(ms_status (*f)(A...), PyObject* const* a, Py_ssize_t n) {
     }
 #define ENTRIES_(do_)                                                       \
     do_(gated_scan_fwd) do_(gated_scan_bwd) do_(gated_step) do_(embed_fwd)  \
-    do_(embed_bwd) do_(token_logprobs_fwd) do_(token_logprobs_bwd)
+    do_(embed_bwd) do_(token_logprobs_fwd) do_(token_logprobs_bwd)          \
+    do_(linear_attn_fwd) do_(linear_attn_bwd) do_(linear_attn_step)         \
+    do_(group_norm_fwd) do_(group_norm_bwd) do_(verify_drafts)
 ENTRIES_(ENTRY_)
 
 // bind(name, address) of an entry point
@@ -246,7 +276,8 @@ PyObject* bind(PyObject*, PyObject* args) {
 
 #define METHOD_(name) \
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr},
-PyMethodDef methods[] = {METHOD_(io) METHOD_(rows) METHOD_(fits) METHOD_(empty) METHOD_(together)
+PyMethodDef methods[] = {METHOD_(io) METHOD_(rows) METHOD_(pitch) METHOD_(fits)
+                         METHOD_(empty) METHOD_(together)
                          ENTRIES_(METHOD_)
                          {"bind", bind, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

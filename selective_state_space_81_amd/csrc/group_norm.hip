@@ -1,0 +1,400 @@
+// group_norm.hip -- norm of each row's channels in groups (the heads of a linear
+// attention), with scale, shift and a silu gate, and its gradient:
+//
+//   u = x, or x silu(z) (gate first)      c = u - mean(u), or u
+//   hat = c / sqrt(mean(c^2) + eps)       y = (hat w + b) [silu(z)]
+//
+// Bytes are all that counts: every input is read once, in vectors of 16 bytes,
+// and kept in registers from the sums to the output.  A group is shared by the
+// fewest lanes (a power of two) that hold it in one vector each, up to a wave
+// with 4 vectors, and by a workgroup beyond that; the groups of a wave lie side
+// by side in a row.  A wave keeps its channels and goes down the rows: the
+// weights are read once, and the gradients of weights add up in registers.
+// They are joined over waves in LDS and over workgroups by a second launch, in
+// fixed orders.
+#include <type_traits>
+
+#include "device_common.h"
+#include "lm_internal.h"
+#include "msscan_internal.h"
+
+namespace msscan {
+namespace norm {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreads = 256;
+constexpr int kWaves = 4;
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef u4 u4_align2 __attribute__((aligned(2)));
+typedef u4 u4_align4 __attribute__((aligned(4)));
+
+template <bool BF16>
+constexpr int vec() { return BF16 ? 8 : 4; }
+
+// A vector of a group's values from place i on; zeros behind the group's end n.
+template <bool BF16>
+struct Vec {
+    static constexpr int W = vec<BF16>();
+    typedef typename std::conditional<BF16, uint16_t, float>::type E;
+    typedef typename std::conditional<BF16, u4_align2, u4_align4>::type U;
+    float v[W];
+
+    __device__ __forceinline__ void load(const void* row, int64_t at, int i, int n) {
+        const E* p = static_cast<const E*>(row) + at + i;
+        if (i + W <= n) {
+            const u4 x = *reinterpret_cast<const U*>(p);
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if constexpr (BF16)
+                    v[e] = __uint_as_float(e & 1 ? x[e / 2] & 0xffff0000u : x[e / 2] << 16);
+                else
+                    v[e] = __uint_as_float(x[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = i + e < n ? ld<BF16>(p, e) : 0.f;
+        }
+    }
+    __device__ __forceinline__ void store(void* row, int64_t at, int i, int n) const {
+        E* p = static_cast<E*>(row) + at + i;
+        if (i + W <= n) {
+            u4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if constexpr (BF16)
+                    x[e] = (uint32_t)f32_to_bf16_rne(v[2 * e]) |
+                           (uint32_t)f32_to_bf16_rne(v[2 * e + 1]) << 16;
+                else
+                    x[e] = __float_as_uint(v[e]);
+            *reinterpret_cast<U*>(p) = x;
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if (i + e < n) st<BF16>(p, e, v[e]);
+        }
+    }
+    // a row of fp32 values that are the same for every row (or `other`)
+    __device__ __forceinline__ void weights(const float* row, int64_t at, int i, int n,
+                                            float other) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] = i + e >= n ? 0.f : row ? row[at + i + e] : other;
+    }
+};
+
+// Where a lane works: its first vector's place in its group, and its group.
+template <bool WIDE>
+struct Lane {
+    int first, step, group, lanes;
+    float* scratch;
+    __device__ __forceinline__ Lane(const NormArgs& a, float* sums) : scratch(sums) {
+        lanes = a.lanes;
+        if (WIDE) {
+            first = threadIdx.x;
+            group = blockIdx.x % a.columns;
+        } else {
+            const int l = threadIdx.x & 63;
+            first = l & (lanes - 1);
+            group = (blockIdx.x % a.columns) * (64 / lanes) + l / lanes;
+        }
+    }
+    // over the lanes of a group
+    __device__ __forceinline__ float sum(float x) const {
+        for (int d = 1; d < (WIDE ? 64 : lanes); d *= 2) x += __shfl_xor(x, d);
+        if (WIDE) {
+            __syncthreads();
+            if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = x;
+            __syncthreads();
+            x = (scratch[0] + scratch[1]) + (scratch[2] + scratch[3]);
+        }
+        return x;
+    }
+};
+
+__device__ __forceinline__ float sigmoid(float z) {
+    return hw_rcp(1.f + hw_exp2(-z * kLog2e));
+}
+
+// The normalised values of a group in place of u, and the factor they took.
+template <bool BF16, int NV, bool WIDE>
+__device__ __forceinline__ float normalise(const NormArgs& a, const Lane<WIDE>& at,
+                                           Vec<BF16> (&u)[NV]) {
+    constexpr int W = vec<BF16>();
+    const float inv = 1.f / (float)a.size;
+    if (a.center) {
+        float s = 0.f;
+#pragma unroll
+        for (int m = 0; m < NV; ++m)
+#pragma unroll
+            for (int e = 0; e < W; ++e) s += u[m].v[e];
+        const float mean = at.sum(s) * inv;
+#pragma unroll
+        for (int m = 0; m < NV; ++m)
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                u[m].v[e] = (at.first + m * at.lanes) * W + e < a.size ? u[m].v[e] - mean : 0.f;
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int m = 0; m < NV; ++m)
+#pragma unroll
+        for (int e = 0; e < W; ++e) s = fmaf(u[m].v[e], u[m].v[e], s);
+    const float factor = 1.f / sqrtf(fmaf(at.sum(s), inv, a.eps));
+#pragma unroll
+    for (int m = 0; m < NV; ++m)
+#pragma unroll
+        for (int e = 0; e < W; ++e) u[m].v[e] *= factor;
+    return factor;
+}
+
+template <bool BF16, int NV, bool WIDE>
+__global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
+    constexpr int W = vec<BF16>();
+    __shared__ float sums[kWaves];
+    const Lane<WIDE> at(a, sums);
+    if (!WIDE && at.group >= a.groups) return;
+    const int64_t base = (int64_t)at.group * a.size;
+    const int64_t stride = WIDE ? a.strips : a.strips * kWaves;
+    int64_t row = blockIdx.x / a.columns;
+    if (!WIDE) row = row * kWaves + (threadIdx.x >> 6);
+    Vec<BF16> w[NV], b[NV];
+#pragma unroll
+    for (int m = 0; m < NV; ++m) {
+        const int i = (at.first + m * at.lanes) * W;
+        w[m].weights(a.weight, base, i, a.size, 1.f);
+        b[m].weights(a.bias, base, i, a.size, 0.f);
+    }
+    const int64_t width = (int64_t)a.groups * a.size;
+    for (; row < a.rows; row += stride) {
+        Vec<BF16> u[NV], z[NV];
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int i = (at.first + m * at.lanes) * W;
+            u[m].load(a.x, row * a.ldx + base, i, a.size);
+            if (a.z) {
+                z[m].load(a.z, row * a.ldz + base, i, a.size);
+#pragma unroll
+                for (int e = 0; e < W; ++e) z[m].v[e] *= sigmoid(z[m].v[e]);
+                if (a.gate_first)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) u[m].v[e] *= z[m].v[e];
+            }
+        }
+        normalise<BF16, NV, WIDE>(a, at, u);
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int i = (at.first + m * at.lanes) * W;
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                u[m].v[e] = fmaf(u[m].v[e], w[m].v[e], b[m].v[e]);
+                if (a.z && !a.gate_first) u[m].v[e] *= z[m].v[e];
+            }
+            u[m].store(a.y, row * width + base, i, a.size);
+        }
+    }
+}
+
+template <bool BF16, int NV, bool WIDE>
+__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
+    constexpr int W = vec<BF16>();
+    __shared__ float sums[kWaves];
+    __shared__ float joined[WIDE ? 1 : kWaves][WIDE ? 1 : 64 * NV * W];
+    const Lane<WIDE> at(a, sums);
+    const bool mine = WIDE || at.group < a.groups;
+    const int64_t base = (int64_t)at.group * a.size, width = (int64_t)a.groups * a.size;
+    const int64_t strip = blockIdx.x / a.columns;
+    const int64_t stride = WIDE ? a.strips : a.strips * kWaves;
+    int64_t row = WIDE ? strip : strip * kWaves + (threadIdx.x >> 6);
+    const float inv = 1.f / (float)a.size;
+    Vec<BF16> w[NV], b[NV], dw[NV], db[NV];
+#pragma unroll
+    for (int m = 0; m < NV; ++m) {
+        const int i = (at.first + m * at.lanes) * W;
+        w[m].weights(a.weight, base, i, mine ? a.size : 0, 1.f);
+        b[m].weights(a.bias, base, i, mine ? a.size : 0, 0.f);
+#pragma unroll
+        for (int e = 0; e < W; ++e) dw[m].v[e] = db[m].v[e] = 0.f;
+    }
+    for (; mine && row < a.rows; row += stride) {
+        Vec<BF16> hat[NV], dy[NV], z[NV], x[NV];
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int i = (at.first + m * at.lanes) * W;
+            x[m].load(a.x, row * a.ldx + base, i, a.size);
+            dy[m].load(a.dy, row * width + base, i, a.size);
+            hat[m] = x[m];
+            if (a.z) {
+                z[m].load(a.z, row * a.ldz + base, i, a.size);
+                if (a.gate_first)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) hat[m].v[e] *= z[m].v[e] * sigmoid(z[m].v[e]);
+            }
+        }
+        const float factor = normalise<BF16, NV, WIDE>(a, at, hat);
+        float s = 0.f, sh = 0.f;
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                float d = dy[m].v[e];
+                if (a.z && !a.gate_first) {
+                    const float zz = z[m].v[e], sg = sigmoid(zz), gate = zz * sg;
+                    // d silu = sigmoid (1 + z (1 - sigmoid))
+                    z[m].v[e] = d * fmaf(hat[m].v[e], w[m].v[e], b[m].v[e]) *
+                                fmaf(gate, 1.f - sg, sg);
+                    d *= gate;
+                }
+                dw[m].v[e] = fmaf(d, hat[m].v[e], dw[m].v[e]);
+                db[m].v[e] += d;
+                d *= w[m].v[e];
+                dy[m].v[e] = d;
+                s += d;
+                sh = fmaf(d, hat[m].v[e], sh);
+            }
+        }
+        sh = at.sum(sh) * inv;
+        s = a.center ? at.sum(s) * inv : 0.f;
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int i = (at.first + m * at.lanes) * W;
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                float d = (fmaf(-hat[m].v[e], sh, dy[m].v[e]) - s) * factor;
+                if (a.z && a.gate_first) {
+                    const float zz = z[m].v[e], sg = sigmoid(zz), gate = zz * sg;
+                    z[m].v[e] = d * x[m].v[e] * fmaf(gate, 1.f - sg, sg);
+                    d *= gate;
+                }
+                dy[m].v[e] = d;
+            }
+            dy[m].store(a.dx, row * width + base, i, a.size);
+            if (a.z) z[m].store(a.dz, row * width + base, i, a.size);
+        }
+    }
+    if (!a.part) return;
+    float* out = a.part + strip * 2 * width;
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int m = 0; m < NV; ++m)
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const int i = (at.first + m * at.lanes) * W + e;
+                if (i < a.size) {
+                    out[base + i] = dw[m].v[e];
+                    out[width + base + i] = db[m].v[e];
+                }
+            }
+    } else {
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+#pragma unroll
+            for (int m = 0; m < NV; ++m)
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+                    joined[wave][(m * W + e) * 64 + lane] = which ? db[m].v[e] : dw[m].v[e];
+            __syncthreads();
+            // the lane's own channels again, a quarter of them for each wave
+            if (mine)
+                for (int x = wave; x < NV * W; x += kWaves) {
+                    const int i = (at.first + x / W * at.lanes) * W + x % W, p = x * 64 + lane;
+                    if (i < a.size)
+                        out[which * width + base + i] = (joined[0][p] + joined[1][p]) +
+                                                        (joined[2][p] + joined[3][p]);
+                }
+        }
+    }
+}
+
+// dweight and dbias from the strips' sums: 64 channels a workgroup of 16 waves,
+// which share the strips.
+constexpr int kJoinWaves = 16;
+__global__ __launch_bounds__(64 * kJoinWaves) void norm_join_kernel(NormArgs a) {
+    __shared__ float sums[kJoinWaves][64];
+    const int64_t width = (int64_t)a.groups * a.size;
+    const int which = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t i = (int64_t)blockIdx.x * 64 + lane;
+    float* out = which ? a.dbias : a.dweight;
+    if (!out) return;
+    float s = 0.f;
+    if (i < width)
+        for (int64_t n = wave; n < a.strips; n += kJoinWaves)
+            s += a.part[(n * 2 + which) * width + i];
+    sums[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && i < width) {
+        s = 0.f;
+#pragma unroll
+        for (int n = 0; n < kJoinWaves; ++n) s += sums[n][lane];
+        out[i] = s;
+    }
+}
+
+}  // namespace
+}  // namespace norm
+
+using namespace norm;
+
+void norm_plan(NormArgs& a, bool bf16, bool backward) {
+    const int units = (a.size + (bf16 ? 7 : 3)) / (bf16 ? 8 : 4);
+    a.lanes = 1;
+    while (a.lanes < 64 && a.lanes < units) a.lanes *= 2;
+    if (units > 256) a.lanes = kThreads;  // more than 4 vectors of a wave's lanes
+    const bool wide = a.lanes == kThreads;
+    a.vecs = (units + a.lanes - 1) / a.lanes;
+    a.columns = wide ? a.groups : (a.groups + 64 / a.lanes - 1) / (64 / a.lanes);
+    // Forward: as many workgroups as rows give, up to 16 a CU (weights are read
+    // once for several rows then).  Backward: 4 a CU, for every strip costs a
+    // row of partial sums.
+    const int64_t most = ((backward ? 1024 : 4096) + a.columns - 1) / a.columns;
+    const int64_t need = wide ? a.rows : (a.rows + kWaves - 1) / kWaves;
+    a.strips = need < most ? need : most;
+    if (a.strips < 1) a.strips = 1;
+}
+
+size_t norm_bwd_ws(const NormArgs& a) {
+    return (size_t)a.strips * 2 * a.groups * a.size * sizeof(float);
+}
+
+int64_t norm_workgroups(const NormArgs& a) { return a.strips * a.columns; }
+
+#define NORM_(kernel, B)                                                                \
+    do {                                                                                \
+        if (a.lanes == kThreads) {                                                      \
+            if (a.vecs <= 2) kernel<B, 2, true><<<n, kThreads, 0, s>>>(a);              \
+            else if (B || a.vecs <= 4) kernel<B, 4, true><<<n, kThreads, 0, s>>>(a);    \
+            else kernel<false, 8, true><<<n, kThreads, 0, s>>>(a);                      \
+        } else if (a.vecs == 1) kernel<B, 1, false><<<n, kThreads, 0, s>>>(a);          \
+        else if (a.vecs == 2) kernel<B, 2, false><<<n, kThreads, 0, s>>>(a);            \
+        else if (a.vecs == 3) kernel<B, 3, false><<<n, kThreads, 0, s>>>(a);            \
+        else kernel<B, 4, false><<<n, kThreads, 0, s>>>(a);                             \
+    } while (0)
+
+hipError_t launch_norm_fwd(const NormArgs& a, bool bf16, hipStream_t s) {
+    ProfScope ps(s, kPhaseMain);
+    const unsigned n = (unsigned)norm_workgroups(a);
+    if (bf16) NORM_(norm_fwd_kernel, true);
+    else NORM_(norm_fwd_kernel, false);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_bwd(NormArgs a, bool bf16, void* workspace, hipStream_t s) {
+    const unsigned n = (unsigned)norm_workgroups(a);
+    a.part = a.dweight || a.dbias ? (float*)workspace : nullptr;
+    {
+        ProfScope ps(s, kPhaseMain);
+        if (bf16) NORM_(norm_bwd_kernel, true);
+        else NORM_(norm_bwd_kernel, false);
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.part) return e;
+    ProfScope ps(s, kPhaseReduce);
+    const int64_t width = (int64_t)a.groups * a.size;
+    norm_join_kernel<<<dim3((unsigned)((width + 63) / 64), a.dbias ? 2 : 1), 64 * kJoinWaves, 0,
+                       s>>>(a);
+    return hipGetLastError();
+}
+#undef NORM_
+
+}  // namespace msscan

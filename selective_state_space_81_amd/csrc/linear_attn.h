@@ -1,0 +1,332 @@
+// linear_attn.h -- what the kernels of the linear attention share: operand
+// fragments of the matrix instructions, tiles of tokens in LDS, and the decays
+// inside a block of tokens.  Included only by linear_attn*.hip.
+//
+// Notation: a block is kBlock tokens of one head.  With G_i the sum of the log
+// decays up to token i of the block (in base 2), and a document starting at
+// start_i <= i,
+//   o_i    = scale sum_{start_i <= j <= i} 2^(G_i - G_j) (q_i . k_j) v_j
+//            + scale 2^G_i S^T q_i        (S before the block; no start up to i)
+//   S_next = 2^G_last S + sum_j 2^(G_last - G_j) k_j v_j^T     (of the last document)
+#pragma once
+
+#include "device_common.h"
+#include "lm_internal.h"
+
+namespace msscan {
+namespace attn {
+
+using namespace dev;
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef float f8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef u4 u4_align2 __attribute__((aligned(2)));
+typedef u4 u4_align4 __attribute__((aligned(4)));
+typedef f8 f8_align16 __attribute__((aligned(16)));
+
+constexpr int kThreads = 256;
+constexpr int kWaves = 4;
+
+// ---- operands of the matrix instructions ---------------------------------------
+//
+// D = A B over 32 of the summed index.  Lane l = 16 g + s holds row s of A (or
+// column s of B), entries 8 g .. 8 g + 7 of the summed index, and of D column
+// s, rows 4 g .. 4 g + 3.  In bf16 that is one 16x16x32 instruction; in fp32
+// eight 16x16x4 ones, the e-th of which takes entry e of every lane: the order
+// of a sum does not matter to which operands meet.
+template <bool BF16>
+struct Io;
+template <>
+struct Io<true> {
+    typedef uint16_t E;
+    typedef b8 Frag;
+    typedef b4 Half;
+    static constexpr int kBlock = kAttnBlockBf16;
+    static constexpr int kPad = 8;  // of a row of LDS: rows of 16 lanes fall on all banks
+    static constexpr int kParts = 3;
+};
+template <>
+struct Io<false> {
+    typedef float E;
+    typedef f8 Frag;
+    typedef f4 Half;
+    static constexpr int kBlock = kAttnBlockF32;
+    static constexpr int kPad = 4;
+    static constexpr int kParts = 1;
+};
+
+__device__ __forceinline__ f4 mma(b8 a, b8 b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f4 mma(f8 a, f8 b, f4 c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+}
+
+// fp32 values as an operand.  round() keeps 8 bits of them in bf16: what it is
+// used for (scores, and the state that a query meets) ends in a bf16 output and
+// adds as much error as that output's own rounding.  Parts keeps all 24 bits, as
+// a sum of three bf16 numbers, for what ends in fp32 (states, gradients of
+// decays): two would leave 3e-6 of a state, three leave fp32's own error.
+__device__ __forceinline__ b8 round(f8 x, b8) {
+    b8 y;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = (__bf16)x[e];
+    return y;
+}
+__device__ __forceinline__ f8 round(f8 x, f8) { return x; }
+__device__ __forceinline__ f8 widen(b8 x) {
+    f8 y;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = (float)x[e];
+    return y;
+}
+__device__ __forceinline__ f8 widen(f8 x) { return x; }
+
+template <bool BF16>
+struct Parts {
+    typename Io<BF16>::Frag p[Io<BF16>::kParts];
+    __device__ __forceinline__ explicit Parts(f8 x) {
+        if constexpr (BF16) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const __bf16 h = (__bf16)x[e];
+                const float r = x[e] - (float)h;
+                const __bf16 m = (__bf16)r;
+                p[0][e] = h;
+                p[1][e] = m;
+                p[2][e] = (__bf16)(r - (float)m);
+            }
+        } else {
+            p[0] = x;
+        }
+    }
+    __device__ __forceinline__ f4 times(typename Io<BF16>::Frag b, f4 c) const {
+#pragma unroll
+        for (int n = Io<BF16>::kParts - 1; n >= 0; --n) c = mma(p[n], b, c);
+        return c;
+    }
+};
+
+// A lane's 8 entries of an operand from a tile in LDS, rows of LD values:
+// along(): operand index = tile row, summed index along the row;
+// across(): operand index = tile column, summed index down the rows (in bf16 by
+// the transposing read: 16 lanes read 4 rows of 16 columns, a lane gets a column).
+template <int LD>
+__device__ __forceinline__ b8 along(const uint16_t* tile, int row0, int k0) {
+    const int l = threadIdx.x & 63;
+    return *reinterpret_cast<const b8*>(tile + (row0 + (l & 15)) * LD + k0 + (l >> 4) * 8);
+}
+template <int LD>
+__device__ __forceinline__ f8 along(const float* tile, int row0, int k0) {
+    const int l = threadIdx.x & 63;
+    const float* p = tile + (row0 + (l & 15)) * LD + k0 + (l >> 4) * 8;
+    const f4 a = *reinterpret_cast<const f4*>(p), b = *reinterpret_cast<const f4*>(p + 4);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+template <int LD>
+__device__ __forceinline__ b8 across(const uint16_t* tile, int k0, int col0) {
+    typedef __attribute__((address_space(3))) s4* Lds;
+    const int l = threadIdx.x & 63, g = l >> 4, s = l & 15;
+    const uint16_t* p = tile + (k0 + g * 8 + (s >> 2)) * LD + col0 + (s & 3) * 4;
+    const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)p);
+    const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + 4 * LD));
+    return __builtin_bit_cast(b8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <int LD>
+__device__ __forceinline__ f8 across(const float* tile, int k0, int col0) {
+    const int l = threadIdx.x & 63;
+    const float* p = tile + (k0 + (l >> 4) * 8) * LD + col0 + (l & 15);
+    f8 y;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = p[e * LD];
+    return y;
+}
+// Entries of an operand for a summed index that is taken 4 + 4 from two blocks
+// of 16, as two tiles of D hold them: along() with k0 + 4 g .. and k0 + 16 + 4 g ..
+template <int LD>
+__device__ __forceinline__ b8 along_pair(const uint16_t* tile, int row0, int k0) {
+    const int l = threadIdx.x & 63;
+    const uint16_t* p = tile + (row0 + (l & 15)) * LD + k0 + (l >> 4) * 4;
+    const s4 a = *reinterpret_cast<const s4*>(p), b = *reinterpret_cast<const s4*>(p + 16);
+    return __builtin_bit_cast(b8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <int LD>
+__device__ __forceinline__ f8 along_pair(const float* tile, int row0, int k0) {
+    const int l = threadIdx.x & 63;
+    const float* p = tile + (row0 + (l & 15)) * LD + k0 + (l >> 4) * 4;
+    const f4 a = *reinterpret_cast<const f4*>(p), b = *reinterpret_cast<const f4*>(p + 16);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+__device__ __forceinline__ void put4(uint16_t* p, f4 x) {
+    b4 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = (__bf16)x[e];
+    *reinterpret_cast<b4*>(p) = y;
+}
+__device__ __forceinline__ void put4(float* p, f4 x) { *reinterpret_cast<f4*>(p) = x; }
+__device__ __forceinline__ void put8(uint16_t* p, b8 x) { *reinterpret_cast<b8*>(p) = x; }
+__device__ __forceinline__ void put8(float* p, f8 x) { *reinterpret_cast<f8_align16*>(p) = x; }
+__device__ __forceinline__ float get(const uint16_t* p) {
+    return __uint_as_float((uint32_t)*p << 16);
+}
+__device__ __forceinline__ float get(const float* p) { return *p; }
+__device__ __forceinline__ f4 get4(const uint16_t* p) {
+    const b4 x = *reinterpret_cast<const b4*>(p);
+    f4 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = (float)x[e];
+    return y;
+}
+__device__ __forceinline__ f4 get4(const float* p) { return *reinterpret_cast<const f4*>(p); }
+
+// Four values of a row of n from place i on, where they are in it.
+template <class E>
+__device__ __forceinline__ void store4(E* row, int i, int n, f4 x) {
+    typedef typename std::conditional<sizeof(E) == 2, b4, f4>::type V;
+    typedef V VA __attribute__((aligned(sizeof(E))));
+    if (i + 4 <= n) {
+        V y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = x[e];
+        *reinterpret_cast<VA*>(row + i) = y;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (i + e < n) st<sizeof(E) == 2>(row, i + e, x[e]);
+    }
+}
+
+// ---- tiles of tokens --------------------------------------------------------------
+
+// kBlock rows of W values (n of them there), from global memory through
+// registers to LDS, zeros beyond the rows and columns that there are.
+template <bool BF16, int W>
+struct Tile {
+    typedef typename Io<BF16>::E E;
+    static constexpr int kRows = Io<BF16>::kBlock;
+    static constexpr int kLd = W + Io<BF16>::kPad;
+    static constexpr int kVecs = W / 8;  // of 8 values, in a row
+    static constexpr int kMine = kRows * kVecs / kThreads;
+    static constexpr int kWords = BF16 ? 4 : 8;  // 32-bit words of 8 values
+    static constexpr int kSize = kRows * kLd;    // in LDS, values
+    static_assert(kRows * kVecs % kThreads == 0, "whole rounds of the threads");
+    uint32_t r[kMine][kWords];
+
+    __device__ __forceinline__ void load(const E* base, int64_t ld, int64_t rows, int n) {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+            const int id = m * kThreads + threadIdx.x, row = id / kVecs, c = id % kVecs * 8;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) r[m][w] = 0;
+            if (row < rows && c < n) {
+                const E* p = base + row * ld + c;
+                if (c + 8 <= n) {
+                    typedef typename std::conditional<BF16, u4_align2, u4_align4>::type V;
+#pragma unroll
+                    for (int h = 0; h < kWords / 4; ++h) {
+                        const u4 x = *reinterpret_cast<const V*>(p + h * 4);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) r[m][h * 4 + w] = x[w];
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 7; ++e)
+                        if (c + e < n) {
+                            if constexpr (BF16)
+                                r[m][e / 2] |= (uint32_t)p[e] << (e % 2 * 16);
+                            else
+                                r[m][e] = __float_as_uint(p[e]);
+                        }
+                }
+            }
+        }
+    }
+    // To LDS; whether something was infinite or NaN.
+    __device__ __forceinline__ bool store(E* tile) const {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+            const int id = m * kThreads + threadIdx.x, row = id / kVecs, c = id % kVecs * 8;
+#pragma unroll
+            for (int h = 0; h < kWords / 4; ++h)
+                *reinterpret_cast<u4*>(tile + row * kLd + c + h * 4) =
+                    u4{r[m][h * 4], r[m][h * 4 + 1], r[m][h * 4 + 2], r[m][h * 4 + 3]};
+            // an exponent of all ones, plus one, carries into the sign's place
+#pragma unroll
+            for (int w = 0; w < kWords; ++w)
+                bad |= BF16 ? (r[m][w] & 0x7f807f80u) + 0x00800080u
+                            : (r[m][w] & 0x7f800000u) + 0x00800000u;
+        }
+        return (bad & (BF16 ? 0x80008000u : 0x80000000u)) != 0;
+    }
+};
+
+// ---- decays of a block ---------------------------------------------------------------
+
+// Sums of log decays in two floats each: they reach hundreds inside a block,
+// and the decay between neighbours needs the difference to 2^-24.
+template <int N>
+struct Decays {
+    float hi[N], lo[N];
+    float first[N];  // 2^G_i, from the block's start to token i; 0 behind a document's start
+    float last[N];   // 2^(G_last - G_i), from token i to the block's end; 0 before a start
+    int start[N];    // where i's document starts in the block, or -1 before it
+    float whole;     // 2^G_last
+    int bad;         // number of the last block in which something was not finite
+
+    // By one wave, lane i for token i (x: its log decay in base 2; cut: it
+    // starts a document).
+    __device__ __forceinline__ void make(float g, bool cut) {
+        const int i = threadIdx.x & 63;
+        double G = cut || i >= N ? 0.0 : (double)g * 1.4426950408889634;
+        int s = cut && i < N ? i : -1;
+#pragma unroll
+        for (int d = 1; d < N; d *= 2) {
+            const double G2 = __shfl_up(G, d);
+            const int s2 = __shfl_up(s, d);
+            if (i >= d) {
+                G += G2;
+                s = s > s2 ? s : s2;
+            }
+        }
+        const float h = (float)G, l = (float)(G - (double)h);
+        const double end = __shfl(G, N - 1);
+        const int send = __shfl(s, N - 1);
+        if (i < N) {
+            hi[i] = h;
+            lo[i] = l;
+            first[i] = s < 0 ? hw_exp2(h) * fmaf(l, kLn2, 1.f) : 0.f;
+            const double d = end - G;
+            const float dh = (float)d;
+            last[i] = i >= send ? hw_exp2(dh) * fmaf((float)(d - (double)dh), kLn2, 1.f) : 0.f;
+            start[i] = s;
+            if (i == N - 1) whole = first[i];
+        }
+    }
+    __device__ __forceinline__ bool cut() const { return start[N - 1] >= 0; }
+    // Decay from token j to token i, 0 outside of j's document or time.
+    __device__ __forceinline__ float between(float hi_i, float lo_i, int start_i, int i, float hi_j,
+                                             float lo_j, int j) const {
+        const float d = hw_exp2((hi_i - hi_j) + (lo_i - lo_j));
+        return j <= i && j >= start_i ? d : 0.f;
+    }
+};
+
+// A decay that is 0 in fp32 starts a document.
+constexpr float kNoDecay = -104.f;
+
+// Place of the log decay of (batch row, token, head).
+__device__ __forceinline__ float log_decay(const AttnArgs& a, int64_t row, int h) {
+    return a.fixed ? a.g[h] : a.g[row * a.H + h];
+}
+
+}  // namespace attn
+}  // namespace msscan

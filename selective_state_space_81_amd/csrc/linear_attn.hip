@@ -1,0 +1,627 @@
+// linear_attn.hip -- linear attention with a decay for each head, forward:
+//
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T      (S_{t-1} dropped where reset_t)
+//   o_t = scale S_t^T q_t
+//
+// In blocks of tokens (linear_attn.h) all of it but the decays is products of
+// small matrices, on the matrix cores.  A workgroup walks along the blocks of
+// one (batch row, head, 64 columns of dv), each wave with 16 of the columns: its
+// state, [dk][16] in fp32, stays in registers in the layout in which the matrix
+// instructions leave it, which is also the one in which they take it as the
+// operand of q S (with the summed index permuted, which a sum allows).  So every
+// input is read once and the state never moves.  q, k and v of the next block
+// are on their way into registers while the present one is computed.
+//
+// A sequence is cut into segments where heads and columns are too few for the
+// chip: a first pass sums up the segments but the last (k and v only), a second
+// joins these, and the walk above starts from what they give.
+#include <type_traits>
+
+#include "linear_attn.h"
+#include "msscan_internal.h"
+
+namespace msscan {
+namespace attn {
+namespace {
+
+// Workgroup -> columns (quickest), head, segment, batch row: heads that share
+// q and k lie side by side, on one XCD.
+struct Place {
+    int tile, h, seg, b;
+    __device__ __forceinline__ explicit Place(const AttnArgs& a, int nseg) {
+        uint32_t id = xcd_logical(blockIdx.x, gridDim.x);
+        tile = id % a.tiles, id /= a.tiles;
+        h = id % a.H, id /= a.H;
+        seg = id % nseg;
+        b = id / nseg;
+    }
+};
+
+// A wave's 16 columns of a state: tile t, entry r is S[16 t + 4 g + r][col].
+template <int DK>
+struct State {
+    static constexpr int kTiles = DK / 16;
+    f4 s[kTiles];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) s[t] = f4{0, 0, 0, 0};
+    }
+    // p: [dk][dv] of one head
+    __device__ __forceinline__ void load(const float* p, int dk, int dv, int col) {
+        const int row = (threadIdx.x & 63) >> 4 << 2;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int d = t * 16 + row + r;
+                s[t][r] = d < dk && col < dv ? p[(int64_t)d * dv + col] : 0.f;
+            }
+    }
+    __device__ __forceinline__ void store(float* p, int dk, int dv, int col) const {
+        const int row = (threadIdx.x & 63) >> 4 << 2;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int d = t * 16 + row + r;
+                if (d < dk && col < dv) p[(int64_t)d * dv + col] = s[t][r];
+            }
+    }
+    // The block's end: s = whole s + sum_j w_j x_j y_j^T, x in rows of xt, y in
+    // rows of yt.  Nothing of a state before a document's start comes through.
+    template <bool BF16, int XLD, int YLD, int N, class E>
+    __device__ __forceinline__ void advance(const E* xt, const E* yt, int ycol, const Decays<N>& d,
+                                            const float* w, float scale) {
+        const bool cut = d.cut();
+        const float whole = d.whole;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[t][r] = cut ? 0.f : s[t][r] * whole;
+        const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+        for (int k0 = 0; k0 < N; k0 += 32) {
+            f8 y = widen(across<YLD>(yt, k0, ycol));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] *= w[k0 + g * 8 + e] * scale;
+            const Parts<BF16> yp(y);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+                s[t] = mma_rows<BF16>(across<XLD>(xt, k0, t * 16), yp, s[t]);
+        }
+    }
+    template <bool BF16>
+    static __device__ __forceinline__ f4 mma_rows(typename Io<BF16>::Frag a, const Parts<BF16>& b,
+                                                  f4 c) {
+#pragma unroll
+        for (int n = Io<BF16>::kParts - 1; n >= 0; --n) c = mma(a, b.p[n], c);
+        return c;
+    }
+    // One token, where matrix products would carry what is not finite into
+    // places that it does not reach: s = decay s + x y (keep false: s = x y).
+    template <class E>
+    __device__ __forceinline__ void token(const E* x, float y, float decay, bool keep, int dk) {
+        const int row = (threadIdx.x & 63) >> 4 << 2;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int d = t * 16 + row + r;
+                if (d < dk) s[t][r] = fmaf(get(x + d), y, keep ? s[t][r] * decay : 0.f);
+            }
+    }
+};
+
+// ---- forward ------------------------------------------------------------------------
+
+template <bool BF16, int DK>
+__global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnArgs a) {
+    typedef typename Io<BF16>::E E;
+    typedef typename Io<BF16>::Frag Frag;
+    constexpr int N = Io<BF16>::kBlock, kIts = N / 16;
+    typedef Tile<BF16, DK> QK;
+    typedef Tile<BF16, 64> V;
+    constexpr int PLD = N + Io<BF16>::kPad;
+    __shared__ __align__(16) E qt[QK::kSize];
+    __shared__ __align__(16) E kt[QK::kSize];
+    __shared__ __align__(16) E vt[V::kSize];
+    __shared__ __align__(16) E pt[N * PLD];  // scores, [i][j]
+    __shared__ Decays<N> dec;
+    __shared__ float glog[N];
+
+    const Place at(a, a.nseg);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, s16 = lane & 15;
+    const int col0 = at.tile * 64, vcol = wave * 16, mycol = col0 + vcol + s16;
+    const int nv = a.dv - col0 < 64 ? a.dv - col0 : 64;
+    const int kh = at.h / (a.H / a.Hk);
+    const int64_t row0 = (int64_t)at.b * a.L;
+    const E* q = (const E*)a.q + row0 * a.ldq + (int64_t)kh * a.dk;
+    const E* k = (const E*)a.k + row0 * a.ldk + (int64_t)kh * a.dk;
+    const E* v = (const E*)a.v + row0 * a.ldv + (int64_t)at.h * a.dv + col0;
+    const int64_t c0 = at.seg * a.per, c1 = c0 + a.per < a.blocks ? c0 + a.per : a.blocks;
+    const int64_t head = ((int64_t)at.b * a.H + at.h) * a.dk * a.dv;
+
+    State<DK> S;
+    if (at.seg)
+        S.load(a.seg + (((int64_t)at.b * a.nseg + at.seg) * a.H + at.h) * a.dk * a.dv, a.dk, a.dv,
+               mycol);
+    else if (a.h0)
+        S.load(a.h0 + head, a.dk, a.dv, mycol);
+    else
+        S.clear();
+    for (int i = threadIdx.x; i < N * PLD; i += kThreads) pt[i] = E(0);  // keys after queries
+    if (threadIdx.x == 0) dec.bad = -1;
+    __syncthreads();
+
+    QK qr, kr;
+    V vr;
+    float gr = 0.f;
+    bool cut = false;
+    auto fetch = [&](int64_t c) {
+        const int64_t t0 = c * N, rows = a.L - t0;
+        qr.load(q + t0 * a.ldq, a.ldq, rows, a.dk);
+        kr.load(k + t0 * a.ldk, a.ldk, rows, a.dk);
+        vr.load(v + t0 * a.ldv, a.ldv, rows, nv);
+        if (wave == 0) {
+            gr = 0.f, cut = false;
+            if (lane < N && t0 + lane < a.L) {
+                gr = log_decay(a, row0 + t0 + lane, at.h);
+                cut = gr < kNoDecay || (a.reset && a.reset[row0 + t0 + lane]);
+            }
+        }
+    };
+    fetch(c0);
+    for (int64_t c = c0; c < c1; ++c) {
+        const int64_t t0 = c * N;
+        qr.store(qt);  // a query that is not finite stays in its own row
+        bool bad = kr.store(kt);
+        bad |= vr.store(vt);
+        if (bad) dec.bad = (int)(c - c0);
+        if (wave == 0) {
+            dec.make(gr, cut);
+            if (lane < N) glog[lane] = gr;
+        }
+        __syncthreads();
+        if (c + 1 < c1) fetch(c + 1);
+        if (a.states) {
+            float* st = a.states +
+                        (((int64_t)at.b * a.blocks + c) * a.H + at.h) * a.DKs * (int64_t)a.DVs;
+            S.store(st, a.DKs, a.DVs, mycol);
+        }
+        E* o = (E*)a.o + (row0 + t0) * a.H * a.dv + (int64_t)at.h * a.dv + col0;
+        const int64_t rows = a.L - t0;
+        if (dec.bad == (int)(c - c0)) {
+            // token by token
+            const int n = rows < N ? (int)rows : N;
+            for (int t = 0; t < n; ++t) {
+                const bool starts = dec.start[t] == t;
+                S.token(kt + t * QK::kLd, get(vt + t * V::kLd + vcol + s16),
+                        hw_exp2(glog[t] * kLog2e), !starts, a.dk);
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < State<DK>::kTiles; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int d = i * 16 + g * 4 + r;
+                        if (d < a.dk) sum = fmaf(get(qt + t * QK::kLd + d), S.s[i][r], sum);
+                    }
+                sum += __shfl_xor(sum, 16);
+                sum += __shfl_xor(sum, 32);
+                if (g == 0 && vcol + s16 < nv)
+                    st<BF16>(o, (int64_t)t * a.H * a.dv + vcol + s16, sum * a.scale);
+            }
+            __syncthreads();
+            continue;
+        }
+        // scores of queries i and keys j <= i, tiles dealt to the waves
+#pragma unroll
+        for (int n = 0; n < (kIts * (kIts + 1) / 2 + kWaves - 1) / kWaves; ++n) {
+            int it = 0, jt = n * kWaves + wave;
+            while (jt > it) jt -= ++it;
+            if (it >= kIts) break;
+            f4 p = {0, 0, 0, 0};
+#pragma unroll
+            for (int d = 0; d < DK; d += 32)
+                p = mma(along<QK::kLd>(kt, jt * 16, d), along<QK::kLd>(qt, it * 16, d), p);
+            const int i = it * 16 + s16, j = jt * 16 + g * 4;
+            const float hi = dec.hi[i], lo = dec.lo[i];
+            const int start = dec.start[i];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float w = dec.between(hi, lo, start, i, dec.hi[j + r], dec.lo[j + r], j + r);
+                p[r] = j + r <= i && j + r >= start ? p[r] * (w * a.scale) : 0.f;
+            }
+            put4(pt + i * PLD + j, p);
+        }
+        // what the state before the block gives
+        f4 oacc[kIts];
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) oacc[it] = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < State<DK>::kTiles; t += 2) {
+            const Frag sf = round(
+                __builtin_shufflevector(S.s[t], S.s[t + 1], 0, 1, 2, 3, 4, 5, 6, 7), Frag{});
+#pragma unroll
+            for (int it = 0; it < kIts; ++it)
+                oacc[it] = mma(sf, along_pair<QK::kLd>(qt, it * 16, t * 16), oacc[it]);
+        }
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) {
+            const bool in = dec.start[it * 16 + s16] < 0;
+            const float w = dec.first[it * 16 + s16] * a.scale;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) oacc[it][r] = in ? oacc[it][r] * w : 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k0 = 0; k0 < N; k0 += 32) {
+            const Frag vf = across<V::kLd>(vt, k0, vcol);
+#pragma unroll
+            for (int it = k0 / 16; it < kIts; ++it)
+                oacc[it] = mma(vf, along<PLD>(pt, it * 16, k0), oacc[it]);
+        }
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) {
+            const int i = it * 16 + s16;
+            if (i < rows) store4(o + (int64_t)i * a.H * a.dv, vcol + g * 4, nv, oacc[it]);
+        }
+        S.template advance<BF16, QK::kLd, V::kLd>(kt, vt, vcol, dec, dec.last, 1.f);
+        __syncthreads();
+    }
+    if (a.h_last && c1 == a.blocks) S.store(a.h_last + head, a.dk, a.dv, mycol);
+}
+
+// ---- walk of the states alone ----------------------------------------------------------
+//
+// Forward in time over (k, v), or backward over (scale q, dO), where the state
+// is the gradient of the states: R before a block (in the walk's order) is dL/dS
+// at the block's end, and a token's decay comes behind its own term.
+template <bool BF16, int DK, bool REV, bool FULL>
+__global__ __launch_bounds__(kThreads) void attn_walk_kernel(AttnArgs a) {
+    typedef typename Io<BF16>::E E;
+    constexpr int N = Io<BF16>::kBlock;
+    typedef Tile<BF16, DK> X;
+    typedef Tile<BF16, 64> Y;
+    __shared__ __align__(16) E xt[X::kSize];
+    __shared__ __align__(16) E yt[Y::kSize];
+    __shared__ Decays<N> dec;
+    __shared__ float glog[N];
+
+    const Place at(a, FULL ? a.nseg : a.nseg - 1);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, s16 = lane & 15;
+    const int col0 = at.tile * 64, vcol = wave * 16, mycol = col0 + vcol + s16;
+    const int nv = a.dv - col0 < 64 ? a.dv - col0 : 64;
+    const int kh = at.h / (a.H / a.Hk);
+    const int64_t row0 = (int64_t)at.b * a.L;
+    const int64_t ldx = REV ? a.ldq : a.ldk, ldy = REV ? (int64_t)a.H * a.dv : a.ldv;
+    const E* x = (const E*)(REV ? a.q : a.k) + row0 * ldx + (int64_t)kh * a.dk;
+    const E* y = (const E*)(REV ? a.dO : a.v) + row0 * ldy + (int64_t)at.h * a.dv + col0;
+    const float scale = REV ? a.scale : 1.f;
+    const int64_t n0 = at.seg * a.per, n1 = n0 + a.per < a.blocks ? n0 + a.per : a.blocks;
+    const int64_t head = ((int64_t)at.b * a.H + at.h) * a.dk * a.dv;
+    const int64_t seg = (((int64_t)at.b * a.nseg + at.seg) * a.H + at.h);
+    const float* first = REV ? a.dh_last : a.h0;
+
+    State<DK> S;
+    S.clear();
+    if (FULL) {
+        if (at.seg)
+            S.load(a.seg + seg * a.dk * a.dv, a.dk, a.dv, mycol);
+        else if (first)
+            S.load(first + head, a.dk, a.dv, mycol);
+    }
+    if (threadIdx.x == 0) dec.bad = -1;
+    __syncthreads();
+
+    double total = 0.0;  // of the segment's log decays, in base 2
+    bool any = false;    // a document starts in it
+    X xr;
+    Y yr;
+    float gr = 0.f;
+    bool cut = false;
+    auto fetch = [&](int64_t n) {
+        const int64_t t0 = (REV ? a.blocks - 1 - n : n) * N, rows = a.L - t0;
+        xr.load(x + t0 * ldx, ldx, rows, a.dk);
+        yr.load(y + t0 * ldy, ldy, rows, nv);
+        if (wave == 0) {
+            gr = 0.f, cut = false;
+            if (lane < N && t0 + lane < a.L) {
+                gr = log_decay(a, row0 + t0 + lane, at.h);
+                cut = gr < kNoDecay || (a.reset && a.reset[row0 + t0 + lane]);
+            }
+        }
+    };
+    fetch(n0);
+    for (int64_t n = n0; n < n1; ++n) {
+        const int64_t c = REV ? a.blocks - 1 - n : n;
+        bool bad = xr.store(xt);
+        bad |= yr.store(yt);
+        if (bad) dec.bad = (int)(n - n0);
+        if (wave == 0) {
+            dec.make(gr, cut);
+            if (lane < N) glog[lane] = gr;
+        }
+        __syncthreads();
+        if (n + 1 < n1) fetch(n + 1);
+        if (FULL && REV)
+            S.store(a.grads + (((int64_t)at.b * a.blocks + c) * a.H + at.h) * a.DKs * (int64_t)a.DVs,
+                    a.DKs, a.DVs, mycol);
+        any |= dec.cut();
+        total += (double)dec.hi[N - 1] + (double)dec.lo[N - 1];
+        if (dec.bad == (int)(n - n0)) {
+            const int m = a.L - c * N < N ? (int)(a.L - c * N) : N;
+            for (int e = 0; e < m; ++e) {
+                const int t = REV ? m - 1 - e : e;
+                const bool starts = dec.start[t] == t;
+                const float decay = hw_exp2(glog[t] * kLog2e);
+                const float val = get(yt + t * Y::kLd + vcol + s16) * scale;
+                if (REV) {
+                    S.token(xt + t * X::kLd, val, 1.f, true, a.dk);
+#pragma unroll
+                    for (int i = 0; i < State<DK>::kTiles; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) S.s[i][r] = starts ? 0.f : S.s[i][r] * decay;
+                } else {
+                    S.token(xt + t * X::kLd, val, decay, !starts, a.dk);
+                }
+            }
+        } else {
+            S.template advance<BF16, X::kLd, Y::kLd>(xt, yt, vcol, dec,
+                                                     REV ? dec.first : dec.last, scale);
+        }
+        __syncthreads();
+    }
+    if (FULL) {
+        if (REV && a.dh0 && n1 == a.blocks) S.store(a.dh0 + head, a.dk, a.dv, mycol);
+    } else {
+        S.store(a.seg + seg * a.dk * a.dv, a.dk, a.dv, mycol);
+        if (at.tile == 0 && threadIdx.x == 0) a.seg_f[seg] = any ? -1.f : (float)exp2(total);
+    }
+}
+
+// ---- joining the segments -------------------------------------------------------------
+// In place: the sums of segments become the states before them.
+__global__ __launch_bounds__(kThreads) void attn_carry_kernel(AttnArgs a, const float* first) {
+    const int64_t per = (int64_t)a.H * a.dk * a.dv, each = (int64_t)a.dk * a.dv;
+    const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (e >= per * a.batch) return;
+    const int64_t b = e / per, i = e - b * per;
+    float* p = a.seg + b * a.nseg * per + i;
+    const float* f = a.seg_f + b * a.nseg * a.H + i / each;
+    float s = first ? first[e] : 0.f;
+    float own = p[0], decay = f[0];
+    for (int n = 0; n < a.nseg - 1; ++n) {
+        const float next = n + 2 < a.nseg ? p[(n + 1) * per] : 0.f;
+        const float fnext = n + 2 < a.nseg ? f[(int64_t)(n + 1) * a.H] : 0.f;
+        s = decay < 0.f ? own : fmaf(decay, s, own);
+        p[(n + 1) * per] = s;
+        own = next, decay = fnext;
+    }
+}
+
+// ---- steps -------------------------------------------------------------------------------
+//
+// A few tokens from a state that is read once (and written once): its bytes are
+// all that counts.  A workgroup takes 64 columns of a head's state, a thread
+// four columns of every 16th row, in registers; tokens' q, k, v and decays wait
+// in LDS.  The sum over rows is joined by two shuffles and, over the waves,
+// through LDS.
+constexpr int kStepBlock = 16;  // tokens in LDS
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void attn_step_kernel(AttnArgs a) {
+    typedef typename Io<BF16>::E E;
+    constexpr int kRows = kMaxHeadDim / 16;
+    __shared__ float qs[kStepBlock][kMaxHeadDim], ks[kStepBlock][kMaxHeadDim];
+    __shared__ __align__(16) float vs[kStepBlock][64];
+    __shared__ __align__(16) float sums[2][kWaves][64];
+    __shared__ float decay[kStepBlock];
+
+    const Place at(a, 1);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int c = (threadIdx.x & 15) * 4, r0 = threadIdx.x >> 4;
+    const int col0 = at.tile * 64, nv = a.dv - col0 < 64 ? a.dv - col0 : 64;
+    const int kh = at.h / (a.H / a.Hk);
+    const int T = (int)a.L;
+    int count = T;
+    if (a.counts) {
+        count = a.counts[at.b];
+        count = count < 0 ? 0 : count > T ? T : count;
+    }
+    if (count == 0) return;
+    float* h = a.h + ((int64_t)at.b * a.H + at.h) * a.dk * a.dv + col0;
+    const bool whole = a.dv % 4 == 0;
+    f4 S[kRows];
+#pragma unroll
+    for (int m = 0; m < kRows; ++m) {
+        const int d = m * 16 + r0;
+        S[m] = f4{0, 0, 0, 0};
+        if (d < a.dk) {
+            const float* p = h + (int64_t)d * a.dv + c;
+            if (whole && c < nv) {
+                S[m] = *reinterpret_cast<const f4*>(p);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < nv) S[m][e] = p[e];
+            }
+        }
+    }
+    const int64_t row0 = (int64_t)at.b * T;
+    for (int t0 = 0; t0 < count; t0 += kStepBlock) {
+        const int n = count - t0 < kStepBlock ? count - t0 : kStepBlock;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n * kMaxHeadDim; i += kThreads) {
+            const int t = i / kMaxHeadDim, d = i % kMaxHeadDim;
+            const int64_t row = row0 + t0 + t;
+            if (d < a.dk) {
+                ks[t][d] = ld<BF16>(a.k, row * a.ldk + (int64_t)kh * a.dk + d);
+                if (a.q) qs[t][d] = ld<BF16>(a.q, row * a.ldq + (int64_t)kh * a.dk + d);
+            }
+        }
+        for (int i = threadIdx.x; i < n * 64; i += kThreads) {
+            const int t = i / 64, d = i % 64;
+            vs[t][d] = d < nv ? ld<BF16>(a.v, (row0 + t0 + t) * a.ldv + (int64_t)at.h * a.dv + col0 + d)
+                              : 0.f;
+        }
+        if ((int)threadIdx.x < n) {
+            const float g = log_decay(a, row0 + t0 + threadIdx.x, at.h);
+            const float x = g * kLog2e;  // and what its rounding left
+            const float rest = fmaf(g, kLog2e, -x) + g * 1.925963033500011079e-8f;
+            decay[threadIdx.x] = g < kNoDecay ? -1.f : hw_exp2(x) * fmaf(rest, kLn2, 1.f);
+        }
+        __syncthreads();
+        for (int t = 0; t < n; ++t) {
+            const f4 v = *reinterpret_cast<const f4*>(&vs[t][c]);
+            const float w = decay[t];
+            f4 o = {0, 0, 0, 0};
+#pragma unroll
+            for (int m = 0; m < kRows; ++m) {
+                const int d = m * 16 + r0;
+                if (d >= a.dk) break;
+                const float kd = ks[t][d];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[m][e] = fmaf(kd, v[e], w < 0.f ? 0.f : S[m][e] * w);
+                if (a.q) {
+                    const float qd = qs[t][d];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = fmaf(qd, S[m][e], o[e]);
+                }
+            }
+            if (!a.q) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                o[e] += __shfl_xor(o[e], 16);
+                o[e] += __shfl_xor(o[e], 32);
+            }
+            // two buffers: the next token's sums do not wait for this one's readers
+            if (lane < 16) *reinterpret_cast<f4*>(&sums[t & 1][wave][c]) = o;
+            __syncthreads();
+            if ((int)threadIdx.x < nv) {
+                const int d = threadIdx.x;
+                const float sum = (sums[t & 1][0][d] + sums[t & 1][1][d]) +
+                                  (sums[t & 1][2][d] + sums[t & 1][3][d]);
+                st<BF16>(a.o, ((row0 + t0 + t) * a.H + at.h) * a.dv + col0 + d, sum * a.scale);
+            }
+        }
+    }
+    if (!a.update) return;
+#pragma unroll
+    for (int m = 0; m < kRows; ++m) {
+        const int d = m * 16 + r0;
+        if (d < a.dk) {
+            float* p = h + (int64_t)d * a.dv + c;
+            if (whole && c < nv) {
+                *reinterpret_cast<f4*>(p) = S[m];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < nv) p[e] = S[m][e];
+            }
+        }
+    }
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+void attn_plan(AttnArgs& a, bool bf16) {
+    const int64_t block = bf16 ? kAttnBlockBf16 : kAttnBlockF32;
+    a.blocks = (a.L + block - 1) / block;
+    a.tiles = (a.dv + 63) / 64;
+    a.DKs = (a.dk + 15) / 16 * 16;
+    a.DVs = (a.dv + 15) / 16 * 16;
+    // Two workgroups a CU; segments of at least four blocks, or the joining
+    // costs more than it brings.
+    const int64_t wgs = (int64_t)a.batch * a.H * a.tiles;
+    int64_t nseg = wgs >= 256 ? 1 : (512 + wgs - 1) / wgs;
+    if (nseg > a.blocks / 4) nseg = a.blocks / 4;
+    if (nseg < 1) nseg = 1;
+    a.per = (a.blocks + nseg - 1) / nseg;
+    a.nseg = (int)((a.blocks + a.per - 1) / a.per);
+}
+
+AttnWs attn_ws(const AttnArgs& a, bool backward) {
+    AttnWs w{};
+    const size_t heads = (size_t)a.batch * a.H;
+    size_t at = 0;
+    w.seg = at;
+    if (a.nseg > 1) at += up256(heads * a.nseg * a.dk * a.dv * sizeof(float));
+    w.seg_f = at;
+    if (a.nseg > 1) at += up256(heads * a.nseg * sizeof(float));
+    w.grads = at;
+    if (backward) at += up256(heads * a.blocks * a.DKs * a.DVs * sizeof(float));
+    w.part = at;
+    if (backward && a.fixed) at += up256(heads * a.blocks * sizeof(float));
+    w.total = at;
+    return w;
+}
+
+int64_t attn_workgroups(const AttnArgs& a) {
+    const int64_t walk = (int64_t)a.batch * a.H * a.tiles * a.nseg;
+    const int64_t grad = (int64_t)a.batch * a.Hk * a.blocks;
+    const int64_t carry = ((int64_t)a.batch * a.H * a.dk * a.dv + kThreads - 1) / kThreads;
+    const int64_t most = walk > grad ? walk : grad;
+    return most > carry ? most : carry;
+}
+
+hipError_t launch_attn_carry(const AttnArgs& a, const float* first, hipStream_t s) {
+    ProfScope ps(s, kPhaseCarry);
+    const int64_t n = (int64_t)a.batch * a.H * a.dk * a.dv;
+    attn_carry_kernel<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a, first);
+    return hipGetLastError();
+}
+
+hipError_t launch_attn_walk(const AttnArgs& a, bool bf16, bool reverse, bool full, hipStream_t s) {
+    ProfScope ps(s, full ? kPhaseMain : kPhaseSummary);
+    const unsigned n = (unsigned)((int64_t)a.batch * a.H * a.tiles * (full ? a.nseg : a.nseg - 1));
+#define WALK_(B, DK)                                                                      \
+    do {                                                                                  \
+        if (!reverse)                                                                     \
+            attn_walk_kernel<B, DK, false, false><<<n, kThreads, 0, s>>>(a);              \
+        else if (full)                                                                    \
+            attn_walk_kernel<B, DK, true, true><<<n, kThreads, 0, s>>>(a);                \
+        else                                                                              \
+            attn_walk_kernel<B, DK, true, false><<<n, kThreads, 0, s>>>(a);               \
+    } while (0)
+    if (bf16 && a.dk <= 64) WALK_(true, 64);
+    else if (bf16) WALK_(true, 128);
+    else if (a.dk <= 64) WALK_(false, 64);
+    else WALK_(false, 128);
+#undef WALK_
+    return hipGetLastError();
+}
+
+hipError_t launch_attn_fwd(AttnArgs a, bool bf16, void* workspace, hipStream_t s) {
+    const AttnWs w = attn_ws(a, false);
+    a.seg = (float*)((char*)workspace + w.seg);
+    a.seg_f = (float*)((char*)workspace + w.seg_f);
+    if (a.nseg > 1) {
+        hipError_t e = launch_attn_walk(a, bf16, false, false, s);
+        if (e != hipSuccess) return e;
+        if ((e = launch_attn_carry(a, a.h0, s)) != hipSuccess) return e;
+    }
+    ProfScope ps(s, kPhaseMain);
+    const unsigned n = (unsigned)((int64_t)a.batch * a.H * a.tiles * a.nseg);
+    if (bf16 && a.dk <= 64) attn_fwd_kernel<true, 64><<<n, kThreads, 0, s>>>(a);
+    else if (bf16) attn_fwd_kernel<true, 128><<<n, kThreads, 0, s>>>(a);
+    else if (a.dk <= 64) attn_fwd_kernel<false, 64><<<n, kThreads, 0, s>>>(a);
+    else attn_fwd_kernel<false, 128><<<n, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+int64_t attn_step_workgroups(const AttnArgs& a) { return (int64_t)a.batch * a.H * a.tiles; }
+
+hipError_t launch_attn_step(const AttnArgs& a, bool bf16, hipStream_t s) {
+    ProfScope ps(s, kPhaseStep);
+    const unsigned n = (unsigned)attn_step_workgroups(a);
+    if (bf16) attn_step_kernel<true><<<n, kThreads, 0, s>>>(a);
+    else attn_step_kernel<false><<<n, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace msscan

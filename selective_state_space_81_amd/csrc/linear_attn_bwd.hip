@@ -1,0 +1,448 @@
+// linear_attn_bwd.hip -- gradients of the linear attention.
+//
+// With R the gradient of the state at a block's end and S the state before the
+// block, the block's gradients need nothing of other blocks.  With
+//   A_ij = scale D_ij q_i . k_j       B_ij = scale D_ij dO_i . v_j
+// (D the decays between tokens of one document, f and l those from the block's
+// start and to its end, w the whole block's):
+//   dv_j = sum_i A_ij dO_i + l_j R^T k_j
+//   dq_i = sum_j B_ij k_j  + scale f_i S dO_i
+//   dk_j = sum_i B_ij q_i  + l_j R v_j
+//   dg_t = sum_{i >= t > j} A_ij dO_i . v_j + sum_{i >= t} scale f_i q_i . S dO_i
+//          + sum_{j < t} l_j k_j . R v_j + w <R, S>
+// The first sum of dg is a suffix sum, within the block, of row sums less
+// column sums: no cancellation over more than a block's tokens.
+//
+// The forward leaves S before each block (states); a walk backward in time
+// (linear_attn.hip) leaves R (grads); then one workgroup a block and group of
+// heads that share keys makes all gradients, adding those of q and k over the
+// group's heads in registers, in their order: deterministic.
+#include <type_traits>
+
+#include "linear_attn.h"
+#include "msscan_internal.h"
+
+namespace msscan {
+namespace attn {
+namespace {
+
+__device__ __forceinline__ float sum_groups(float x) {  // over lanes of the same l & 15
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+__device__ __forceinline__ float sum_row(float x) {  // over 16 lanes
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) x += __shfl_xor(x, d);
+    return x;
+}
+
+template <bool BF16, int DK, int DV>
+struct GradShared {
+    typedef typename Io<BF16>::E E;
+    static constexpr int N = Io<BF16>::kBlock, kIts = N / 16;
+    static constexpr int kScoreLd = N + Io<BF16>::kPad, kStateLd = DV + Io<BF16>::kPad;
+    __align__(16) E q[Tile<BF16, DK>::kSize];
+    __align__(16) E k[Tile<BF16, DK>::kSize];
+    __align__(16) E v[Tile<BF16, DV>::kSize];
+    __align__(16) E dO[Tile<BF16, DV>::kSize];
+    __align__(16) E A[N * kScoreLd];  // [i][j]
+    __align__(16) E B[N * kScoreLd];
+    __align__(16) E R[DK * kStateLd];  // rounded, for dv
+    Decays<N> dec;
+    float glog[N];
+    float rows[kIts][N];  // [key tile][i]: sums of A_ij dO_i . v_j
+    float cols[kIts][N];  // [query tile][j]
+    float later[kWaves][N], earlier[kWaves][N], both[kWaves];
+};
+
+template <bool BF16, int DK, int DV>
+__global__ __launch_bounds__(kThreads) void attn_grad_kernel(AttnArgs a) {
+    typedef typename Io<BF16>::E E;
+    typedef typename Io<BF16>::Frag Frag;
+    typedef GradShared<BF16, DK, DV> Shared;
+    typedef Tile<BF16, DK> QK;
+    typedef Tile<BF16, DV> V;
+    constexpr int N = Shared::N, kIts = Shared::kIts, SLD = Shared::kScoreLd,
+                  RLD = Shared::kStateLd, QLD = QK::kLd, VLD = V::kLd;
+    constexpr int kKt = DK / 64, kVt = DV / 64;  // tiles of 16 channels a wave takes
+    extern __shared__ __align__(16) char memory[];
+    Shared& sh = *reinterpret_cast<Shared*>(memory);
+
+    uint32_t id = xcd_logical(blockIdx.x, gridDim.x);
+    const int kh = id % a.Hk;
+    id /= a.Hk;
+    const int64_t c = id % (uint32_t)a.blocks;
+    const int b = id / (uint32_t)a.blocks;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, s16 = lane & 15;
+    const int group = a.H / a.Hk;
+    const int64_t row0 = (int64_t)b * a.L + c * N, rows = a.L - c * N;
+    const int n = rows < N ? (int)rows : N;
+
+    for (int i = threadIdx.x; i < N * SLD; i += kThreads) sh.A[i] = sh.B[i] = E(0);
+    if (threadIdx.x == 0) sh.dec.bad = 0;
+    __syncthreads();
+
+    f4 dq[kKt][kIts], dk[kKt][kIts];
+#pragma unroll
+    for (int m = 0; m < kKt; ++m)
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) dq[m][it] = dk[m][it] = f4{0, 0, 0, 0};
+
+    bool qkbad = false;
+    {
+        QK t;
+        t.load((const E*)a.q + row0 * a.ldq + (int64_t)kh * a.dk, a.ldq, rows, a.dk);
+        qkbad = t.store(sh.q);
+        t.load((const E*)a.k + row0 * a.ldk + (int64_t)kh * a.dk, a.ldk, rows, a.dk);
+        qkbad |= t.store(sh.k);
+    }
+    for (int n_head = 0; n_head < group; ++n_head) {
+        const int h = kh * group + n_head;
+        bool bad = qkbad;
+        {
+            V t;
+            const int64_t ldo = (int64_t)a.H * a.dv;
+            t.load((const E*)a.v + row0 * a.ldv + (int64_t)h * a.dv, a.ldv, rows, a.dv);
+            bad |= t.store(sh.v);
+            t.load((const E*)a.dO + row0 * ldo + (int64_t)h * a.dv, ldo, rows, a.dv);
+            bad |= t.store(sh.dO);
+        }
+        if (bad) sh.dec.bad = n_head + 1;
+        float gr = 0.f;
+        bool cut = false;
+        if (wave == 0) {
+            if (lane < n) {
+                gr = log_decay(a, row0 + lane, h);
+                cut = gr < kNoDecay || (a.reset && a.reset[row0 + lane]);
+            }
+            sh.dec.make(gr, cut);
+        }
+        __syncthreads();
+        const bool slow = sh.dec.bad == n_head + 1;
+        const Decays<N>& dec = sh.dec;
+
+        // scores, and the sums over them that the decays' gradient needs
+#pragma unroll
+        for (int m = 0; m < (kIts * (kIts + 1) / 2 + kWaves - 1) / kWaves; ++m) {
+            int it = 0, jt = m * kWaves + wave;
+            while (jt > it) jt -= ++it;
+            if (it >= kIts) break;
+            f4 qk = {0, 0, 0, 0}, ov = {0, 0, 0, 0};
+#pragma unroll
+            for (int d = 0; d < DK; d += 32)
+                qk = mma(along<QLD>(sh.k, jt * 16, d), along<QLD>(sh.q, it * 16, d), qk);
+#pragma unroll
+            for (int d = 0; d < DV; d += 32)
+                ov = mma(along<VLD>(sh.v, jt * 16, d), along<VLD>(sh.dO, it * 16, d), ov);
+            const int i = it * 16 + s16, j = jt * 16 + g * 4;
+            const float hi = dec.hi[i], lo = dec.lo[i];
+            const int start = dec.start[i];
+            f4 A, B, M;
+            float row = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool in = j + r <= i && j + r >= start;
+                const float w =
+                    a.scale * dec.between(hi, lo, start, i, dec.hi[j + r], dec.lo[j + r], j + r);
+                A[r] = in ? qk[r] * w : 0.f;
+                B[r] = in ? ov[r] * w : 0.f;
+                M[r] = in ? A[r] * ov[r] : 0.f;
+                row += M[r];
+                const float col = sum_row(M[r]);
+                if (s16 == 0) sh.cols[it][j + r] = col;
+            }
+            row = sum_groups(row);
+            if (g == 0) sh.rows[jt][i] = row;
+            put4(sh.A + i * SLD + j, A);
+            put4(sh.B + i * SLD + j, B);
+        }
+        // dq and dk: what other blocks give
+        const int64_t at = (((int64_t)b * a.blocks + c) * a.H + h) * a.DKs * (int64_t)a.DVs;
+        const float *S = a.states + at, *R = a.grads + at;
+        f4 dqs[kIts], dks[kIts];
+        float later[kIts], earlier[kIts], both = 0.f;
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) later[it] = earlier[it] = 0.f;
+#pragma unroll
+        for (int m = 0; m < kKt; ++m) {
+            const int d0 = (m * kWaves + wave) * 16;
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) dqs[it] = dks[it] = f4{0, 0, 0, 0};
+#pragma unroll
+            for (int e0 = 0; e0 < DV; e0 += 32) {
+                f8 sf = {}, rf = {};
+                const int e = e0 + g * 8;
+                if (d0 < a.DKs && e < a.DVs) {
+                    const int64_t p = (int64_t)(d0 + s16) * a.DVs + e;
+                    sf = *reinterpret_cast<const f8_align16*>(S + p);
+                    rf = *reinterpret_cast<const f8_align16*>(R + p);
+                }
+#pragma unroll
+                for (int x = 0; x < 8; ++x) both = fmaf(sf[x], rf[x], both);
+                const Parts<BF16> sp(sf), rp(rf);
+                put8(sh.R + (d0 + s16) * RLD + e, rp.p[0]);
+#pragma unroll
+                for (int it = 0; it < kIts; ++it) {
+                    dqs[it] = sp.times(along<VLD>(sh.dO, it * 16, e0), dqs[it]);
+                    dks[it] = rp.times(along<VLD>(sh.v, it * 16, e0), dks[it]);
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+                const int i = it * 16 + s16;
+                const bool before = dec.start[i] < 0, after = i >= dec.start[N - 1];
+                const float f = dec.first[i] * a.scale, l = dec.last[i];
+                const f4 qi = get4(sh.q + i * QLD + d0 + g * 4);
+                const f4 ki = get4(sh.k + i * QLD + d0 + g * 4);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float x = before ? dqs[it][r] * f : 0.f;
+                    const float y = after ? dks[it][r] * l : 0.f;
+                    dq[m][it][r] += x;
+                    dk[m][it][r] += y;
+                    later[it] += before ? qi[r] * x : 0.f;
+                    earlier[it] += after ? ki[r] * y : 0.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) {
+            later[it] = sum_groups(later[it]);
+            earlier[it] = sum_groups(earlier[it]);
+            if (g == 0) {
+                sh.later[wave][it * 16 + s16] = later[it];
+                sh.earlier[wave][it * 16 + s16] = earlier[it];
+            }
+        }
+        both = sum_groups(sum_row(both));
+        if (lane == 0) sh.both[wave] = both;
+        __syncthreads();
+
+        // within the block
+        f4 dv[kVt][kIts];
+#pragma unroll
+        for (int m = 0; m < kVt; ++m)
+#pragma unroll
+            for (int jt = 0; jt < kIts; ++jt) dv[m][jt] = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int m = 0; m < kVt; ++m) {
+            const int e0 = (m * kWaves + wave) * 16;
+#pragma unroll
+            for (int d = 0; d < DK; d += 32) {
+                const Frag rf = across<RLD>(sh.R, d, e0);
+#pragma unroll
+                for (int jt = 0; jt < kIts; ++jt)
+                    dv[m][jt] = mma(rf, along<QLD>(sh.k, jt * 16, d), dv[m][jt]);
+            }
+#pragma unroll
+            for (int jt = 0; jt < kIts; ++jt) {
+                const int j = jt * 16 + s16;
+                const bool after = j >= dec.start[N - 1];
+                const float l = dec.last[j];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dv[m][jt][r] = after ? dv[m][jt][r] * l : 0.f;
+            }
+        }
+        if (!slow) {
+#pragma unroll
+            for (int k0 = 0; k0 < N; k0 += 32) {
+#pragma unroll
+                for (int m = 0; m < kKt; ++m) {
+                    const int d0 = (m * kWaves + wave) * 16;
+                    const Frag kf = across<QLD>(sh.k, k0, d0), qf = across<QLD>(sh.q, k0, d0);
+#pragma unroll
+                    for (int it = k0 / 16; it < kIts; ++it)
+                        dq[m][it] = mma(kf, along<SLD>(sh.B, it * 16, k0), dq[m][it]);
+#pragma unroll
+                    for (int jt = 0; jt < k0 / 16 + 2; ++jt)
+                        dk[m][jt] = mma(qf, across<SLD>(sh.B, k0, jt * 16), dk[m][jt]);
+                }
+#pragma unroll
+                for (int m = 0; m < kVt; ++m) {
+                    const Frag of = across<VLD>(sh.dO, k0, (m * kWaves + wave) * 16);
+#pragma unroll
+                    for (int jt = 0; jt < k0 / 16 + 2; ++jt)
+                        dv[m][jt] = mma(of, across<SLD>(sh.A, k0, jt * 16), dv[m][jt]);
+                }
+            }
+        } else {
+            // something is not finite: only the pairs of tokens that there are
+            for (int x = 0; x < n; ++x) {
+#pragma unroll
+                for (int it = 0; it < kIts; ++it) {
+                    const int i = it * 16 + s16;
+                    const bool to = x <= i && x >= dec.start[i] && i < n;
+                    const bool from = i <= x && i >= dec.start[x];
+#pragma unroll
+                    for (int m = 0; m < kKt; ++m) {
+                        const int d0 = (m * kWaves + wave) * 16 + g * 4;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            if (to)
+                                dq[m][it][r] = fmaf(get(sh.B + i * SLD + x),
+                                                    get(sh.k + x * QLD + d0 + r), dq[m][it][r]);
+                            if (from)
+                                dk[m][it][r] = fmaf(get(sh.B + x * SLD + i),
+                                                    get(sh.q + x * QLD + d0 + r), dk[m][it][r]);
+                        }
+                    }
+#pragma unroll
+                    for (int m = 0; m < kVt; ++m) {
+                        const int e0 = (m * kWaves + wave) * 16 + g * 4;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (from)
+                                dv[m][it][r] = fmaf(get(sh.A + x * SLD + i),
+                                                    get(sh.dO + x * VLD + e0 + r), dv[m][it][r]);
+                    }
+                }
+            }
+        }
+        E* out = (E*)a.dv_out + row0 * a.H * a.dv + (int64_t)h * a.dv;
+#pragma unroll
+        for (int m = 0; m < kVt; ++m)
+#pragma unroll
+            for (int jt = 0; jt < kIts; ++jt) {
+                const int j = jt * 16 + s16;
+                if (j < n)
+                    store4(out + (int64_t)j * a.H * a.dv, (m * kWaves + wave) * 16 + g * 4, a.dv,
+                           dv[m][jt]);
+            }
+        // the decays
+        if (slow) {
+            // the pairs that straddle each token, by themselves: sums over rows and
+            // columns would carry a NaN to tokens that it does not reach
+            for (int t = wave; t < n; t += kWaves) {
+                float sum = 0.f;
+                if (lane >= t && lane < n) {
+                    const int i = lane, start = dec.start[i];
+                    for (int j = start < 0 ? 0 : start; j < t; ++j) {
+                        float qk = 0.f, ov = 0.f;
+                        for (int d = 0; d < a.dk; ++d)
+                            qk = fmaf(get(sh.q + i * QLD + d), get(sh.k + j * QLD + d), qk);
+                        for (int d = 0; d < a.dv; ++d)
+                            ov = fmaf(get(sh.dO + i * VLD + d), get(sh.v + j * VLD + d), ov);
+                        sum += qk * ov * a.scale *
+                               dec.between(dec.hi[i], dec.lo[i], start, i, dec.hi[j], dec.lo[j], j);
+                    }
+                }
+                sum = sum_groups(sum_row(sum));
+                if (lane == 0) sh.glog[t] = sum;
+            }
+            __syncthreads();
+        }
+        if (wave == 0) {
+            const int t = lane < N ? lane : N - 1;
+            float net = 0.f, late = 0.f, early = 0.f;
+            if (lane < n) {
+                if (!slow) {
+                    for (int x = 0; x <= t / 16; ++x) net += sh.rows[x][t];
+                    for (int x = t / 16; x < kIts; ++x) net -= sh.cols[x][t];
+                }
+                late = sh.later[0][t] + sh.later[1][t] + sh.later[2][t] + sh.later[3][t];
+                early = sh.earlier[0][t] + sh.earlier[1][t] + sh.earlier[2][t] + sh.earlier[3][t];
+            }
+            net += late;
+#pragma unroll
+            for (int d = 1; d < N; d *= 2) {
+                const float x = __shfl_down(net, d), y = __shfl_up(early, d);
+                if (lane + d < N) net += x;
+                if (lane >= d) early += y;
+            }
+            early = __shfl_up(early, 1);
+            if (lane == 0) early = 0.f;
+            const float rs = dec.cut() ? 0.f
+                                       : dec.whole * ((sh.both[0] + sh.both[1]) +
+                                                      (sh.both[2] + sh.both[3]));
+            float dg = net + early + rs;
+            if (slow && lane < n) dg += sh.glog[lane];
+            if (dec.start[t] == t || lane >= n) dg = 0.f;
+            if (a.fixed) {
+                dg = sum_groups(sum_row(dg));
+                if (lane == 0) a.part[((int64_t)b * a.blocks + c) * a.H + h] = dg;
+            } else if (lane < n) {
+                a.dg[(row0 + lane) * a.H + h] = dg;
+            }
+        }
+        __syncthreads();
+    }
+    const int64_t ldo = (int64_t)a.Hk * a.dk;
+    E* oq = (E*)a.dq + row0 * ldo + (int64_t)kh * a.dk;
+    E* ok = (E*)a.dk_out + row0 * ldo + (int64_t)kh * a.dk;
+#pragma unroll
+    for (int m = 0; m < kKt; ++m)
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) {
+            const int i = it * 16 + s16, d0 = (m * kWaves + wave) * 16 + g * 4;
+            if (i < n) {
+                store4(oq + i * ldo, d0, a.dk, dq[m][it]);
+                store4(ok + i * ldo, d0, a.dk, dk[m][it]);
+            }
+        }
+}
+
+// Gradient of decays that are fixed for a head: the blocks' sums, in order
+// within a thread and then as a tree.
+__global__ __launch_bounds__(kThreads) void attn_fixed_kernel(AttnArgs a) {
+    __shared__ double sums[kThreads];
+    const int h = blockIdx.x;
+    const int64_t n = a.batch * a.blocks;
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) s += (double)a.part[i * a.H + h];
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    for (int d = kThreads / 2; d; d /= 2) {
+        if ((int)threadIdx.x < d) sums[threadIdx.x] += sums[threadIdx.x + d];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) a.dg[h] = (float)sums[0];
+}
+
+template <bool BF16, int DK, int DV>
+hipError_t launch_grad(const AttnArgs& a, hipStream_t s) {
+    constexpr int bytes = (int)sizeof(GradShared<BF16, DK, DV>);
+    static_assert(bytes <= 160 * 1024, "LDS of a CU");
+    const hipError_t e =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(attn_grad_kernel<BF16, DK, DV>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    const unsigned n = (unsigned)((int64_t)a.batch * a.Hk * a.blocks);
+    attn_grad_kernel<BF16, DK, DV><<<n, kThreads, bytes, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+hipError_t launch_attn_bwd(AttnArgs a, bool bf16, void* workspace, hipStream_t s) {
+    const AttnWs w = attn_ws(a, true);
+    a.seg = (float*)((char*)workspace + w.seg);
+    a.seg_f = (float*)((char*)workspace + w.seg_f);
+    a.grads = (float*)((char*)workspace + w.grads);
+    a.part = (float*)((char*)workspace + w.part);
+    hipError_t e;
+    if (a.nseg > 1) {
+        if ((e = launch_attn_walk(a, bf16, true, false, s)) != hipSuccess) return e;
+        if ((e = launch_attn_carry(a, a.dh_last, s)) != hipSuccess) return e;
+    }
+    if ((e = launch_attn_walk(a, bf16, true, true, s)) != hipSuccess) return e;
+    {
+        ProfScope ps(s, kPhaseMain);
+#define GRAD_(B)                                                                       \
+    (a.dk <= 64 ? a.dv <= 64 ? launch_grad<B, 64, 64>(a, s) : launch_grad<B, 64, 128>(a, s) \
+                : a.dv <= 64 ? launch_grad<B, 128, 64>(a, s) : launch_grad<B, 128, 128>(a, s))
+        e = bf16 ? GRAD_(true) : GRAD_(false);
+#undef GRAD_
+        if (e != hipSuccess) return e;
+    }
+    if (a.fixed) {
+        ProfScope ps(s, kPhaseReduce);
+        attn_fixed_kernel<<<a.H, kThreads, 0, s>>>(a);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+}  // namespace msscan

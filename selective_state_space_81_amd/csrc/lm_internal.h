@@ -1,6 +1,7 @@
 // lm_internal.h -- launch interface between the C ABI of the language-model
-// operators beside the scan (lm_api.cpp) and their kernels (gated_scan.hip,
-// embed.hip, logprob.hip).  Not part of the public ABI.
+// operators beside the scan (lm_api.cpp, attn_api.cpp) and their kernels
+// (gated_scan.hip, embed.hip, logprob.hip; linear_attn*.hip, group_norm.hip,
+// verify.hip).  Not part of the public ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -151,5 +152,130 @@ LogprobWs logprob_ws(const LogprobArgs& a);
 hipError_t launch_logprob_fwd(LogprobArgs a, bool bf16, void* workspace, hipStream_t s);
 int64_t logprob_bwd_workgroups(const LogprobArgs& a, bool bf16);
 hipError_t launch_logprob_bwd(const LogprobArgs& a, bool bf16, hipStream_t s);
+
+// ---- linear attention (linear_attn.hip, linear_attn_bwd.hip) ----------------------
+constexpr int kAttnBlockBf16 = 64;  // tokens of a block
+constexpr int kAttnBlockF32 = 32;
+constexpr int kMaxHeadDim = 128;  // of dk and dv
+constexpr int kStepTokens = 64;   // most tokens of a step
+
+struct AttnArgs {
+    const void* q;  // [batch][L] rows ldq apart, of Hk heads of dk
+    const void* k;
+    const void* v;         // of H heads of dv
+    const float* g;        // [batch][L][H], or [H] (fixed)
+    const uint8_t* reset;  // [batch][L] or null
+    const float* h0;       // [batch][H][dk][dv] or null
+    void* o;               // [batch][L][H][dv]
+    float* h_last;         // [batch][H][dk][dv] or null
+    float* states;         // [batch][blocks][H][DKs][DVs]; forward: written, or null
+    // backward
+    const void* dO;
+    const float* dh_last;
+    void* dq;
+    void* dk_out;
+    void* dv_out;
+    float* dg;   // [batch][L][H], or [H] (fixed)
+    float* dh0;  // or null
+    // step
+    float* h;
+    const int32_t* counts;  // [batch] or null
+    int update;
+    // workspace
+    float* seg;     // [batch][nseg][H][dk][dv]: states at the ends, then the starts, of segments
+    float* seg_f;   // [batch][nseg][H]: decay of a segment, -1 where a document starts in it
+    float* grads;   // [batch][blocks][H][DKs][DVs]: gradients of the states at the blocks' ends
+    float* part;    // [batch][blocks][H]: sums of a fixed decay's gradient
+    int64_t ldq, ldk, ldv;
+    int64_t L;
+    int64_t blocks;
+    int64_t per;  // blocks of a segment
+    float scale;
+    int nseg;
+    int fixed;
+    int batch, H, Hk, dk, dv;
+    int DKs, DVs;  // dk and dv in whole tiles of 16
+    int tiles;     // tiles of 64 columns of dv
+};
+struct AttnWs {
+    size_t seg, seg_f, grads, part, total;
+};
+void attn_plan(AttnArgs& a, bool bf16);
+AttnWs attn_ws(const AttnArgs& a, bool backward);
+int64_t attn_workgroups(const AttnArgs& a);  // the most of a launch
+hipError_t launch_attn_fwd(AttnArgs a, bool bf16, void* workspace, hipStream_t s);
+hipError_t launch_attn_bwd(AttnArgs a, bool bf16, void* workspace, hipStream_t s);
+// The states of segments of the walk over blocks, forward in time (k, v) or
+// backward (q, dO): with `every`, the state before each block goes to `every`
+// and the last one to `last`; otherwise only the sums of segments to a.seg.
+hipError_t launch_attn_walk(const AttnArgs& a, bool bf16, bool reverse, bool full, hipStream_t s);
+hipError_t launch_attn_carry(const AttnArgs& a, const float* first, hipStream_t s);
+int64_t attn_step_workgroups(const AttnArgs& a);
+hipError_t launch_attn_step(const AttnArgs& a, bool bf16, hipStream_t s);
+
+// ---- group norm of each row's channels (group_norm.hip) ------------------------------
+constexpr int kMaxNormGroup = 8192;  // channels of a group
+
+struct NormArgs {
+    const void* x;  // [rows], ldx apart, of groups * size
+    const void* z;  // [rows], ldz apart, or null
+    const float* weight;  // [groups * size] or null
+    const float* bias;    // or null
+    void* y;              // [rows][groups * size]
+    // backward
+    const void* dy;
+    void* dx;
+    void* dz;
+    float* dweight;  // or null
+    float* dbias;    // or null
+    float* part;     // [strips][2][groups * size]: sums of dweight and dbias
+    int64_t ldx, ldz;
+    int64_t rows;
+    float eps;
+    int groups, size;
+    int center, gate_first;
+    // plan
+    int lanes;      // that share a group: a power of two, or 256 (a workgroup)
+    int vecs;       // vectors of a lane
+    int columns;    // workgroups side by side for a row's groups
+    int64_t strips;  // workgroups one above the other
+};
+void norm_plan(NormArgs& a, bool bf16, bool backward);
+size_t norm_bwd_ws(const NormArgs& a);
+int64_t norm_workgroups(const NormArgs& a);
+hipError_t launch_norm_fwd(const NormArgs& a, bool bf16, hipStream_t s);
+hipError_t launch_norm_bwd(NormArgs a, bool bf16, void* workspace, hipStream_t s);
+
+// ---- verification of drafted tokens (verify.hip) --------------------------------------
+constexpr int kMaxDrafts = 64;
+
+struct VerifyArgs {
+    const void* logits;  // [batch][drafts + 1] rows ld apart
+    const void* draft_logits;  // [batch][drafts] rows ldd apart, or null
+    const void* tokens_in;     // [batch][drafts], int32 or int64
+    const float* uniforms;     // [batch][drafts + 1]
+    int32_t* tokens;           // [batch][drafts + 1]
+    int32_t* count;            // [batch]
+    float* logprob;            // [batch][drafts + 1]
+    double* part;  // [rows][splits][2]: largest exponent, sum beside it
+    double* mass;  // [batch][pieces][2]: of what is left, and of the target's
+    int64_t ld, ldd;
+    int64_t V;
+    float scale;
+    int wide;
+    int batch, drafts;
+    // plan
+    int64_t rows;    // of both, the target's first
+    int splits;      // workgroups of a row
+    int64_t per;     // values each of them takes
+    int pieces;      // of a row that is drawn from
+};
+struct VerifyWs {
+    size_t part, mass, total;
+};
+void verify_plan(VerifyArgs& a, bool bf16, bool drafted);
+VerifyWs verify_ws(const VerifyArgs& a);
+int64_t verify_workgroups(const VerifyArgs& a);
+hipError_t launch_verify(VerifyArgs a, bool bf16, void* workspace, hipStream_t s);
 
 }  // namespace msscan

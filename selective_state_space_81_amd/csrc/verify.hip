@@ -1,0 +1,465 @@
+// verify.hip -- verification of drafted tokens against the target's
+// probabilities, from given random numbers.
+//
+// With p_t and q_t the target's and the drafting model's probabilities, drafts
+// x_t are accepted one after another while u_t q_t(x_t) < p_t(x_t).  At the
+// first that is not, a token is drawn from max(p_t - q_t, 0), and behind the
+// last one, if all are, from p_t: the first v whose cumulative mass exceeds
+// u_last times the whole.
+//
+// Whole numbers come out of comparisons of sums over the vocabulary, so all of
+// it is in fp64, the exponentials too (a polynomial of 2^f, relative error
+// 3e-13): in fp32 one draw in some hundred would fall on the other side of a
+// border.  Three launches: the largest logit and the sum of every row, in one
+// pass over all logits; the mass of pieces of the one row of each sequence that
+// is drawn from (every workgroup finds out which by itself: a few comparisons);
+// and the search, over pieces and then inside one.
+#include <type_traits>
+
+#include "device_common.h"
+#include "lm_internal.h"
+#include "msscan_internal.h"
+
+namespace msscan {
+namespace verify {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreads = 256;
+constexpr int kPiece = 4096;  // values of a piece: 16 a thread in the search
+constexpr int kMine = kPiece / kThreads;
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef u4 u4_align2 __attribute__((aligned(2)));
+typedef u4 u4_align4 __attribute__((aligned(4)));
+
+// 2^x for x <= 0 (or NaN); 0 from -1000 down, which no sum notices.
+__device__ __forceinline__ double exp2_64(double x) {
+    const double n = __builtin_rint(x), f = (x - n) * 0.693147180559945309417;
+    // the series of e^f, |f| <= 0.3466: the first term left out is 2e-13
+    double p = 1.0 / 3628800.0;
+    p = fma(p, f, 1.0 / 362880.0);
+    p = fma(p, f, 1.0 / 40320.0);
+    p = fma(p, f, 1.0 / 5040.0);
+    p = fma(p, f, 1.0 / 720.0);
+    p = fma(p, f, 1.0 / 120.0);
+    p = fma(p, f, 1.0 / 24.0);
+    p = fma(p, f, 1.0 / 6.0);
+    p = fma(p, f, 0.5);
+    p = fma(p, f, 1.0);
+    p = fma(p, f, 1.0);
+    const double y = __builtin_amdgcn_ldexp(p, (int)n);
+    return x < -1000.0 ? 0.0 : y;
+}
+
+// Largest exponent (in base 2) and sum beside it.  Nothing yet, or only masked
+// logits: m = -inf, s = 0.  NaN and +inf: s becomes NaN.
+struct Sum {
+    double m, s;
+    __device__ __forceinline__ void add(const Sum& o) {
+        if (o.m > m) {
+            s = (m == -INFINITY ? s : s * exp2_64(m - o.m)) + o.s;
+            m = o.m;
+        } else {
+            s += o.m == -INFINITY ? o.s : o.s * exp2_64(o.m - m);
+        }
+    }
+};
+__device__ __forceinline__ double shfl_xor64(double x, int d) { return __shfl_xor(x, d); }
+
+template <bool BF16>
+struct Row {
+    static constexpr int W = BF16 ? 8 : 4;
+    typedef typename std::conditional<BF16, uint16_t, float>::type E;
+    typedef typename std::conditional<BF16, u4_align2, u4_align4>::type U;
+    // W values from place i on of n; -inf behind the end
+    static __device__ __forceinline__ void load(const void* row, int64_t i, int64_t n,
+                                                float (&v)[W]) {
+        const E* p = static_cast<const E*>(row) + i;
+        if (i + W <= n) {
+            const u4 x = *reinterpret_cast<const U*>(p);
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if constexpr (BF16)
+                    v[e] = __uint_as_float(e & 1 ? x[e / 2] & 0xffff0000u : x[e / 2] << 16);
+                else
+                    v[e] = __uint_as_float(x[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = i + e < n ? ld<BF16>(p, e) : -INFINITY;
+        }
+    }
+};
+
+template <bool BF16>
+__device__ __forceinline__ const void* row_of(const VerifyArgs& a, int64_t r) {
+    constexpr int size = BF16 ? 2 : 4;
+    const int64_t own = (int64_t)a.batch * (a.drafts + 1);
+    return r < own ? static_cast<const char*>(a.logits) + r * a.ld * size
+                   : static_cast<const char*>(a.draft_logits) + (r - own) * a.ldd * size;
+}
+
+// ---- sums of rows ------------------------------------------------------------------
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a) {
+    constexpr int W = Row<BF16>::W;
+    __shared__ Sum sums[kThreads / 64];
+    const int64_t r = blockIdx.x / a.splits;
+    const int split = blockIdx.x % a.splits;
+    const int64_t i0 = split * a.per, i1 = i0 + a.per < a.V ? i0 + a.per : a.V;
+    const void* row = row_of<BF16>(a, r);
+    const double c = (double)a.scale * 1.4426950408889634074;
+    float top = -INFINITY;  // the largest logit so far, of this thread
+    double m = -INFINITY, s = 0.0;
+    for (int64_t i = i0 + threadIdx.x * W; i < i1; i += kThreads * W) {
+        float v[W];
+        Row<BF16>::load(row, i, i1, v);
+        float t = v[0];
+#pragma unroll
+        for (int e = 1; e < W; ++e) t = fmaxf(t, v[e]);
+        if (t > top) {
+            const double now = (double)t * c;
+            s = top == -INFINITY ? s : s * exp2_64(m - now);
+            top = t, m = now;
+        }
+        if (top == -INFINITY) {  // nothing but masked logits, or NaN
+#pragma unroll
+            for (int e = 0; e < W; ++e) s += v[e] == v[e] ? 0.0 : (double)v[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e) s += exp2_64((double)v[e] * c - m);
+        }
+    }
+    Sum x{m, s};
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) x.add(Sum{shfl_xor64(x.m, d), shfl_xor64(x.s, d)});
+    if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = x;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kThreads / 64; ++w) x.add(sums[w]);
+        a.part[blockIdx.x * 2] = x.m;
+        a.part[blockIdx.x * 2 + 1] = x.s;
+    }
+}
+
+// ---- which drafts are accepted --------------------------------------------------------
+struct Shared {
+    Sum p[kMaxDrafts + 1], q[kMaxDrafts];
+    int yes[kMaxDrafts];
+    int count;
+};
+
+__device__ __forceinline__ Sum row_sum(const VerifyArgs& a, int64_t r) {
+    Sum x{-INFINITY, 0.0};
+    for (int n = 0; n < a.splits; ++n)
+        x.add(Sum{a.part[(r * a.splits + n) * 2], a.part[(r * a.splits + n) * 2 + 1]});
+    return x;
+}
+// whether the row is a distribution
+__device__ __forceinline__ bool proper(const Sum& x) { return x.s > 0.0 && x.s < INFINITY; }
+
+__device__ __forceinline__ int64_t draft(const VerifyArgs& a, int b, int t) {
+    const int64_t i = (int64_t)b * a.drafts + t;
+    return a.wide ? static_cast<const int64_t*>(a.tokens_in)[i]
+                  : static_cast<const int32_t*>(a.tokens_in)[i];
+}
+
+template <bool BF16>
+__device__ __forceinline__ double prob(const VerifyArgs& a, const void* row, int64_t v,
+                                       const Sum& x) {
+    const double c = (double)a.scale * 1.4426950408889634074;
+    return exp2_64((double)ld<BF16>(row, v) * c - x.m) / x.s;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void decide(const VerifyArgs& a, int b, Shared& sh) {
+    const int T = a.drafts, t = threadIdx.x;
+    const int64_t first = (int64_t)b * (T + 1);
+    if (t <= T) {
+        sh.p[t] = row_sum(a, first + t);
+    } else if (t >= 128 && t - 128 < T && a.draft_logits) {
+        sh.q[t - 128] = row_sum(a, (int64_t)a.batch * (T + 1) + (int64_t)b * T + t - 128);
+    }
+    __syncthreads();
+    if (t < T) {
+        const int64_t v = draft(a, b, t);
+        bool yes = false;
+        if (v >= 0 && v < a.V && proper(sh.p[t])) {
+            const double p = prob<BF16>(a, row_of<BF16>(a, first + t), v, sh.p[t]);
+            double q = 1.0;
+            if (a.draft_logits)
+                q = proper(sh.q[t]) ? prob<BF16>(a, row_of<BF16>(a, (int64_t)a.batch * (T + 1) +
+                                                                       (int64_t)b * T + t),
+                                                 v, sh.q[t])
+                                    : INFINITY;
+            yes = (double)a.uniforms[first + t] * q < p;
+        }
+        sh.yes[t] = yes;
+    }
+    __syncthreads();
+    if (t == 0) {
+        int n = 0;
+        while (n < T && sh.yes[n]) ++n;
+        sh.count = n;
+    }
+    __syncthreads();
+}
+
+// What is drawn from: the mass that is left of the target's at place v, and the
+// target's own (in units of its largest).
+struct Left {
+    double p, left;
+};
+template <bool BF16>
+struct Drawn {
+    const void *prow, *qrow;
+    Sum p, q;
+    double c, ratio;  // of what a unit of q's row is worth in p's
+    int64_t one;      // a draft without probabilities of its own
+    __device__ __forceinline__ Drawn(const VerifyArgs& a, int b, const Shared& sh) {
+        const int n = sh.count, T = a.drafts;
+        c = (double)a.scale * 1.4426950408889634074;
+        prow = row_of<BF16>(a, (int64_t)b * (T + 1) + n);
+        p = sh.p[n];
+        qrow = nullptr;
+        one = -1;
+        if (n < T) {
+            if (!a.draft_logits) {
+                one = draft(a, b, n);
+            } else if (proper(sh.q[n])) {
+                qrow = row_of<BF16>(a, (int64_t)a.batch * (T + 1) + (int64_t)b * T + n);
+                q = sh.q[n];
+                ratio = p.s / q.s;
+            }
+        }
+    }
+    __device__ __forceinline__ Left at(float x, float y, int64_t v) const {
+        const double mine = exp2_64((double)x * c - p.m);
+        double left = mine;
+        if (qrow) left = mine - exp2_64((double)y * c - q.m) * ratio;
+        if (v == one) left = 0.0;
+        return {mine, left > 0.0 ? left : 0.0};
+    }
+};
+
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) x += shfl_xor64(x, d);
+    return x;
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void verify_mass_kernel(VerifyArgs a) {
+    constexpr int W = Row<BF16>::W;
+    __shared__ Shared sh;
+    __shared__ double sums[2][kThreads / 64];
+    const int b = blockIdx.x / a.pieces, piece = blockIdx.x % a.pieces;
+    decide<BF16>(a, b, sh);
+    const Drawn<BF16> from(a, b, sh);
+    const int64_t i0 = (int64_t)piece * kPiece,
+                  i1 = i0 + kPiece < a.V ? i0 + kPiece : a.V;
+    double left = 0.0, own = 0.0;
+    if (proper(from.p))
+        for (int64_t i = i0 + threadIdx.x * W; i < i1; i += kThreads * W) {
+            float x[W], y[W];
+            Row<BF16>::load(from.prow, i, i1, x);
+            if (from.qrow) Row<BF16>::load(from.qrow, i, i1, y);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const Left l = from.at(x[e], from.qrow ? y[e] : 0.f, i + e);
+                left += l.left;
+                own += l.p;
+            }
+        }
+    left = wave_sum(left);
+    own = wave_sum(own);
+    if ((threadIdx.x & 63) == 0) {
+        sums[0][threadIdx.x >> 6] = left;
+        sums[1][threadIdx.x >> 6] = own;
+    }
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        const double* s = sums[threadIdx.x];
+        a.mass[blockIdx.x * 2 + threadIdx.x] = (s[0] + s[1]) + (s[2] + s[3]);
+    }
+}
+
+// Sums up to and with each thread's x, over the workgroup.
+__device__ __forceinline__ double scan(double x, double (&sums)[kThreads / 64]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const double y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 63) sums[wave] = x;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) x += sums[w];
+    return x;
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a) {
+    __shared__ Shared sh;
+    __shared__ double sums[kThreads / 64];
+    __shared__ double before;   // mass ahead of the piece
+    __shared__ int piece;       // that holds the border
+    __shared__ int last;        // place of the last value with mass in it
+    __shared__ int found;       // first place past the border
+    const int b = blockIdx.x, T = a.drafts, tid = threadIdx.x;
+    decide<BF16>(a, b, sh);
+    const Drawn<BF16> from(a, b, sh);
+    const double* mass = a.mass + (int64_t)b * a.pieces * 2;
+    if (tid == 0) {
+        piece = -1;
+        last = -1;
+        found = kPiece;
+    }
+    // the whole: of what is left, or of the target's where nothing is
+    double whole = 0.0;
+    int which = 0;
+    for (; which < 2; ++which) {
+        double x = 0.0;
+        for (int n = tid; n < a.pieces; n += kThreads) x += mass[n * 2 + which];
+        x = wave_sum(x);
+        __syncthreads();
+        if ((tid & 63) == 0) sums[tid >> 6] = x;
+        __syncthreads();
+        whole = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        if (whole > 0.0) break;
+    }
+    const double u = (double)a.uniforms[(int64_t)b * (T + 1) + T];
+    int drawn = -1;
+    if (proper(from.p) && whole > 0.0) {
+        const double border = u * whole;
+        // the first piece past the border, or the last one with mass at all
+        double ahead = 0.0;
+        for (int n0 = 0; n0 < a.pieces && piece < 0; n0 += kThreads) {
+            const int n = n0 + tid;
+            const double x = n < a.pieces ? mass[n * 2 + which] : 0.0;
+            const double upto = ahead + scan(x, sums);
+            const double whole_so_far = ahead + ((sums[0] + sums[1]) + (sums[2] + sums[3]));
+            const bool past = x > 0.0 && upto > border;
+            if (x > 0.0) atomicMax(&last, n);
+            if (past) atomicMin(&found, n - n0);
+            __syncthreads();
+            if (found < kPiece && tid == found) {
+                piece = n;
+                before = upto - x;
+            }
+            ahead = whole_so_far;
+            __syncthreads();
+        }
+        if (piece < 0 && tid == 0) {  // rounding, or a number that is not below 1
+            piece = last;
+            before = 0.0;
+        }
+        __syncthreads();
+        const bool over = found == kPiece;
+        __syncthreads();
+        if (tid == 0) {
+            found = kPiece;
+            last = -1;
+        }
+        __syncthreads();
+        const int64_t i0 = (int64_t)piece * kPiece,
+                      i1 = i0 + kPiece < a.V ? i0 + kPiece : a.V;
+        // kMine neighbouring values a thread
+        double x[kMine], sum = 0.0;
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) {
+            const int64_t v = i0 + tid * kMine + e;
+            x[e] = 0.0;
+            if (v < i1) {
+                const Left l = from.at(ld<BF16>(from.prow, v),
+                                       from.qrow ? ld<BF16>(from.qrow, v) : 0.f, v);
+                x[e] = which ? l.p : l.left;
+            }
+            sum += x[e];
+        }
+        double upto = before + (scan(sum, sums) - sum);
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) {
+            upto += x[e];
+            if (x[e] > 0.0) {
+                atomicMax(&last, tid * kMine + e);
+                if (!over && upto > border) atomicMin(&found, tid * kMine + e);
+            }
+        }
+        __syncthreads();
+        drawn = (int)i0 + (found < kPiece ? found : last);
+    }
+    // the tokens, and their log probabilities under the target
+    if (tid <= T) {
+        const int64_t at = (int64_t)b * (T + 1) + tid;
+        int64_t v = -1;
+        if (tid < sh.count) v = draft(a, b, tid);
+        else if (tid == sh.count) v = drawn;
+        double lp = 0.0;
+        if (v >= 0) {
+            const double c = (double)a.scale;
+            lp = (double)ld<BF16>(row_of<BF16>(a, at), v) * c -
+                 sh.p[tid].m * 0.693147180559945309417 - log(sh.p[tid].s);
+        }
+        a.tokens[at] = (int32_t)v;
+        a.logprob[at] = (float)lp;
+    }
+    if (tid == 0) a.count[b] = sh.count;
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace verify
+
+using namespace verify;
+
+void verify_plan(VerifyArgs& a, bool bf16, bool drafted) {
+    a.rows = (int64_t)a.batch * (a.drafts + 1 + (drafted ? a.drafts : 0));
+    // Workgroups for 8 a CU, of at least 2048 values each.
+    const int64_t round = kThreads * (bf16 ? 8 : 4);
+    int64_t splits = (2048 + a.rows - 1) / a.rows;
+    const int64_t most = (a.V + 2047) / 2048;
+    if (splits > most) splits = most;
+    if (splits > 64) splits = 64;
+    a.per = ((a.V + splits - 1) / splits + round - 1) / round * round;
+    a.splits = (int)((a.V + a.per - 1) / a.per);
+    a.pieces = (int)((a.V + kPiece - 1) / kPiece);
+}
+
+VerifyWs verify_ws(const VerifyArgs& a) {
+    VerifyWs w{};
+    w.part = 0;
+    w.mass = up256((size_t)a.rows * a.splits * 2 * sizeof(double));
+    w.total = w.mass + up256((size_t)a.batch * a.pieces * 2 * sizeof(double));
+    return w;
+}
+
+int64_t verify_workgroups(const VerifyArgs& a) {
+    const int64_t x = a.rows * a.splits, y = (int64_t)a.batch * a.pieces;
+    return x > y ? x : y;
+}
+
+hipError_t launch_verify(VerifyArgs a, bool bf16, void* workspace, hipStream_t s) {
+    const VerifyWs w = verify_ws(a);
+    a.part = (double*)((char*)workspace + w.part);
+    a.mass = (double*)((char*)workspace + w.mass);
+    const unsigned n = (unsigned)(a.rows * a.splits), m = (unsigned)((int64_t)a.batch * a.pieces);
+    {
+        ProfScope ps(s, kPhaseMain);
+        if (bf16) verify_sum_kernel<true><<<n, kThreads, 0, s>>>(a);
+        else verify_sum_kernel<false><<<n, kThreads, 0, s>>>(a);
+    }
+    {
+        ProfScope ps(s, kPhaseSummary);
+        if (bf16) verify_mass_kernel<true><<<m, kThreads, 0, s>>>(a);
+        else verify_mass_kernel<false><<<m, kThreads, 0, s>>>(a);
+    }
+    ProfScope ps(s, kPhaseReduce);
+    if (bf16) verify_draw_kernel<true><<<a.batch, kThreads, 0, s>>>(a);
+    else verify_draw_kernel<false><<<a.batch, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace msscan

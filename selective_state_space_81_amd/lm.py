@@ -65,7 +65,8 @@ def _marshal():
         raise ImportError("_marshal.so cannot be loaded; build it with "
                           "`python -m selective_state_space_81_amd.build`") from e
     for name in ("gated_scan_fwd", "gated_scan_bwd", "gated_step", "embed_fwd", "embed_bwd",
-                 "token_logprobs_fwd", "token_logprobs_bwd"):
+                 "token_logprobs_fwd", "token_logprobs_bwd", "linear_attn_fwd", "linear_attn_bwd",
+                 "linear_attn_step", "group_norm_fwd", "group_norm_bwd", "verify_drafts"):
         m.bind(name, ctypes.cast(getattr(lib, "ms_" + name), ctypes.c_void_p).value)
     return m
 
