@@ -56,6 +56,18 @@ ms_status check_pitch(const char* name, int64_t ld, int64_t width) {
     return MS_OK;
 }
 
+// Rows of q, k and v: 32 bits hold a place in a block of them.
+ms_status check_rows_of_heads(int64_t ldq, int64_t ldk, int64_t ldv, int64_t qk, int64_t v) {
+    ms_status st;
+    if ((st = check_pitch("ldq", ldq, qk)) != MS_OK) return st;
+    if ((st = check_pitch("ldk", ldk, qk)) != MS_OK) return st;
+    if ((st = check_pitch("ldv", ldv, v)) != MS_OK) return st;
+    const int64_t most = (1 << 22) - 1;
+    if (ldq > most || ldk > most || ldv > most)
+        return fail(MS_ERR_UNSUPPORTED, "rows of 2^22 values or more are too long");
+    return MS_OK;
+}
+
 ms_status check_norm(NormArgs& a, int64_t rows, int32_t groups, int32_t size, float eps, int32_t io,
                      bool backward) {
     if (rows < 0 || rows > kMax31)
@@ -124,9 +136,8 @@ ms_status ms_linear_attn_fwd(const void* q, int64_t ldq, const void* k, int64_t 
     if (st != MS_OK) return st;
     if ((st = check_scale(scale, false)) != MS_OK) return st;
     if (!q || !k || !v || !g || !o) return fail(MS_ERR_NULL, "q, k, v, g and o are required");
-    if ((st = check_pitch("ldq", ldq, (int64_t)kheads * dk)) != MS_OK) return st;
-    if ((st = check_pitch("ldk", ldk, (int64_t)kheads * dk)) != MS_OK) return st;
-    if ((st = check_pitch("ldv", ldv, (int64_t)heads * dv)) != MS_OK) return st;
+    if ((st = check_rows_of_heads(ldq, ldk, ldv, (int64_t)kheads * dk, (int64_t)heads * dv)) != MS_OK)
+        return st;
     if ((st = check_aligned({o, h0, h_last, states, workspace})) != MS_OK) return st;
     if ((st = check_element_aligned(io_size(io), {q, k, v})) != MS_OK) return st;
     if ((st = check_element_aligned(4, {g})) != MS_OK) return st;
@@ -161,9 +172,8 @@ ms_status ms_linear_attn_bwd(const void* q, int64_t ldq, const void* k, int64_t 
     if ((st = check_scale(scale, false)) != MS_OK) return st;
     if (!q || !k || !v || !g || !states || !d_o || !dq || !d_k || !d_v || !dg)
         return fail(MS_ERR_NULL, "q, k, v, g, states, d_o, dq, d_k, d_v and dg are required");
-    if ((st = check_pitch("ldq", ldq, (int64_t)kheads * dk)) != MS_OK) return st;
-    if ((st = check_pitch("ldk", ldk, (int64_t)kheads * dk)) != MS_OK) return st;
-    if ((st = check_pitch("ldv", ldv, (int64_t)heads * dv)) != MS_OK) return st;
+    if ((st = check_rows_of_heads(ldq, ldk, ldv, (int64_t)kheads * dk, (int64_t)heads * dv)) != MS_OK)
+        return st;
     if ((st = check_aligned({states, dq, d_k, d_v, dg, dh0, workspace})) != MS_OK) return st;
     if ((st = check_element_aligned(io_size(io), {q, k, v, d_o})) != MS_OK) return st;
     if ((st = check_element_aligned(4, {g, dh_last})) != MS_OK) return st;

@@ -10,6 +10,8 @@
 //   S_next = 2^G_last S + sum_j 2^(G_last - G_j) k_j v_j^T     (of the last document)
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "lm_internal.h"
 
@@ -28,9 +30,19 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 typedef u4 u4_align2 __attribute__((aligned(2)));
 typedef u4 u4_align4 __attribute__((aligned(4)));
 typedef f8 f8_align16 __attribute__((aligned(16)));
+typedef b4 b4_align2 __attribute__((aligned(2)));
+typedef f4 f4_align4 __attribute__((aligned(4)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
+
+// A barrier for what waves share in LDS.  __syncthreads also waits for every
+// load and store of global memory under way, the next block's inputs among them.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
 
 // ---- operands of the matrix instructions ---------------------------------------
 //
@@ -187,17 +199,18 @@ __device__ __forceinline__ f4 get4(const uint16_t* p) {
 }
 __device__ __forceinline__ f4 get4(const float* p) { return *reinterpret_cast<const f4*>(p); }
 
-// Four values of a row of n from place i on, where they are in it.
-template <class E>
+// Four values of a row of n from place i on, where they are in it (WHOLE: all of
+// them or none).
+template <bool WHOLE, class E>
 __device__ __forceinline__ void store4(E* row, int i, int n, f4 x) {
     typedef typename std::conditional<sizeof(E) == 2, b4, f4>::type V;
-    typedef V VA __attribute__((aligned(sizeof(E))));
-    if (i + 4 <= n) {
+    typedef typename std::conditional<sizeof(E) == 2, b4_align2, f4_align4>::type VA;
+    if (WHOLE ? i < n : i + 4 <= n) {
         V y;
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = x[e];
         *reinterpret_cast<VA*>(row + i) = y;
-    } else {
+    } else if (!WHOLE) {
 #pragma unroll
         for (int e = 0; e < 3; ++e)
             if (i + e < n) st<sizeof(E) == 2>(row, i + e, x[e]);
@@ -207,8 +220,12 @@ __device__ __forceinline__ void store4(E* row, int i, int n, f4 x) {
 // ---- tiles of tokens --------------------------------------------------------------
 
 // kBlock rows of W values (n of them there), from global memory through
-// registers to LDS, zeros beyond the rows and columns that there are.
-template <bool BF16, int W>
+// registers to LDS, zeros beyond the rows and columns that there are.  Rows lie
+// less than 2^22 values apart, so 32 bits hold a place in a block.
+// WHOLE: n is a multiple of 8, and loads need no branch: they ask for places
+// that are there (store() clears what lies beyond), and nothing waits for them
+// until then.  Other rows end in single values.
+template <bool BF16, int W, bool WHOLE>
 struct Tile {
     typedef typename Io<BF16>::E E;
     static constexpr int kRows = Io<BF16>::kBlock;
@@ -220,22 +237,30 @@ struct Tile {
     static_assert(kRows * kVecs % kThreads == 0, "whole rounds of the threads");
     uint32_t r[kMine][kWords];
 
-    __device__ __forceinline__ void load(const E* base, int64_t ld, int64_t rows, int n) {
+    __device__ __forceinline__ void vector(int m, const E* p) {
+        typedef typename std::conditional<BF16, u4_align2, u4_align4>::type V;
+#pragma unroll
+        for (int h = 0; h < kWords / 4; ++h) {
+            const u4 x = *reinterpret_cast<const V*>(p + h * (BF16 ? 8 : 4));
+#pragma unroll
+            for (int w = 0; w < 4; ++w) r[m][h * 4 + w] = x[w];
+        }
+    }
+    __device__ __forceinline__ void load(const E* base, int ld, int rows, int n) {
+        const int last = (rows < kRows ? rows : kRows) - 1;
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
             const int id = m * kThreads + threadIdx.x, row = id / kVecs, c = id % kVecs * 8;
+            if constexpr (WHOLE) {
+                vector(m, base + (uint32_t)(min(row, last) * ld + min(c, n - 8)));
+                continue;
+            }
 #pragma unroll
             for (int w = 0; w < kWords; ++w) r[m][w] = 0;
-            if (row < rows && c < n) {
-                const E* p = base + row * ld + c;
+            if (row <= last && c < n) {
+                const E* p = base + (uint32_t)(row * ld + c);
                 if (c + 8 <= n) {
-                    typedef typename std::conditional<BF16, u4_align2, u4_align4>::type V;
-#pragma unroll
-                    for (int h = 0; h < kWords / 4; ++h) {
-                        const u4 x = *reinterpret_cast<const V*>(p + h * 4);
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) r[m][h * 4 + w] = x[w];
-                    }
+                    vector(m, p);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 7; ++e)
@@ -250,11 +275,15 @@ struct Tile {
         }
     }
     // To LDS; whether something was infinite or NaN.
-    __device__ __forceinline__ bool store(E* tile) const {
+    __device__ __forceinline__ bool store(E* tile, int rows, int n) {
         uint32_t bad = 0;
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
             const int id = m * kThreads + threadIdx.x, row = id / kVecs, c = id % kVecs * 8;
+            if (WHOLE && !(row < rows && c < n)) {
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) r[m][w] = 0;
+            }
 #pragma unroll
             for (int h = 0; h < kWords / 4; ++h)
                 *reinterpret_cast<u4*>(tile + row * kLd + c + h * 4) =
@@ -271,6 +300,30 @@ struct Tile {
 
 // ---- decays of a block ---------------------------------------------------------------
 
+// Sums over the lanes up to each, in fp64, with DPP moves: no trip through LDS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp64(double x) {  // 0 where no lane gives anything
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0u, (uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0u, (uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double scan64(double x) {
+    x += dpp64<0x111, 0xf>(x);  // row_shr 1, 2, 4, 8: within 16 lanes
+    x += dpp64<0x112, 0xf>(x);
+    x += dpp64<0x114, 0xf>(x);
+    x += dpp64<0x118, 0xf>(x);
+    x += dpp64<0x142, 0xa>(x);  // lane 15 of a row to the next one, lane 31 to the upper half
+    x += dpp64<0x143, 0xc>(x);
+    return x;
+}
+__device__ __forceinline__ double lane64(double x, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, lane);
+    const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // Sums of log decays in two floats each: they reach hundreds inside a block,
 // and the decay between neighbours needs the difference to 2^-24.
 template <int N>
@@ -282,24 +335,18 @@ struct Decays {
     float whole;     // 2^G_last
     int bad;         // number of the last block in which something was not finite
 
-    // By one wave, lane i for token i (x: its log decay in base 2; cut: it
-    // starts a document).
+    // By one wave, lane i for token i (g: its log decay; cut: it starts a
+    // document).
     __device__ __forceinline__ void make(float g, bool cut) {
         const int i = threadIdx.x & 63;
         double G = cut || i >= N ? 0.0 : (double)g * 1.4426950408889634;
-        int s = cut && i < N ? i : -1;
-#pragma unroll
-        for (int d = 1; d < N; d *= 2) {
-            const double G2 = __shfl_up(G, d);
-            const int s2 = __shfl_up(s, d);
-            if (i >= d) {
-                G += G2;
-                s = s > s2 ? s : s2;
-            }
-        }
+        G = scan64(G);
+        const uint64_t cuts = __ballot(cut && i < N);
+        const uint64_t upto = cuts & (~0ull >> (63 - i));
+        const int s = upto ? 63 - __builtin_clzll(upto) : -1;
         const float h = (float)G, l = (float)(G - (double)h);
-        const double end = __shfl(G, N - 1);
-        const int send = __shfl(s, N - 1);
+        const double end = lane64(G, N - 1);
+        const int send = cuts ? 63 - __builtin_clzll(cuts) : -1;
         if (i < N) {
             hi[i] = h;
             lo[i] = l;
@@ -308,7 +355,7 @@ struct Decays {
             const float dh = (float)d;
             last[i] = i >= send ? hw_exp2(dh) * fmaf((float)(d - (double)dh), kLn2, 1.f) : 0.f;
             start[i] = s;
-            if (i == N - 1) whole = first[i];
+            if (i == N - 1) whole = s < 0 ? first[i] : 0.f;
         }
     }
     __device__ __forceinline__ bool cut() const { return start[N - 1] >= 0; }

@@ -37,6 +37,9 @@ struct Place {
     }
 };
 
+// Tokens left, as far as a block goes.
+__device__ __forceinline__ int there(int64_t n) { return n < 128 ? (int)n : 128; }
+
 // A wave's 16 columns of a state: tile t, entry r is S[16 t + 4 g + r][col].
 template <int DK>
 struct State {
@@ -67,6 +70,17 @@ struct State {
                 const int d = t * 16 + row + r;
                 if (d < dk && col < dv) p[(int64_t)d * dv + col] = s[t][r];
             }
+    }
+    // In whole tiles of 16 (a.DKs, a.DVs), the wave's first column vcol.
+    __device__ __forceinline__ void keep(float* p, int dks, int dvs, int vcol) const {
+        const int l = threadIdx.x & 63, row = l >> 4 << 2;
+        if (vcol >= dvs) return;
+        p += row * dvs + vcol + (l & 15);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+            if (t * 16 < dks)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) p[(t * 16 + r) * dvs] = s[t][r];
     }
     // The block's end: s = whole s + sum_j w_j x_j y_j^T, x in rows of xt, y in
     // rows of yt.  Nothing of a state before a document's start comes through.
@@ -115,13 +129,13 @@ struct State {
 
 // ---- forward ------------------------------------------------------------------------
 
-template <bool BF16, int DK>
-__global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnArgs a) {
+template <bool BF16, int DK, bool WHOLE>
+__global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_fwd_kernel(AttnArgs a) {
     typedef typename Io<BF16>::E E;
     typedef typename Io<BF16>::Frag Frag;
     constexpr int N = Io<BF16>::kBlock, kIts = N / 16;
-    typedef Tile<BF16, DK> QK;
-    typedef Tile<BF16, 64> V;
+    typedef Tile<BF16, DK, WHOLE> QK;
+    typedef Tile<BF16, 64, WHOLE> V;
     constexpr int PLD = N + Io<BF16>::kPad;
     __shared__ __align__(16) E qt[QK::kSize];
     __shared__ __align__(16) E kt[QK::kSize];
@@ -139,6 +153,7 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnArgs a) {
     const E* q = (const E*)a.q + row0 * a.ldq + (int64_t)kh * a.dk;
     const E* k = (const E*)a.k + row0 * a.ldk + (int64_t)kh * a.dk;
     const E* v = (const E*)a.v + row0 * a.ldv + (int64_t)at.h * a.dv + col0;
+    const int ldo = a.H * a.dv;
     const int64_t c0 = at.seg * a.per, c1 = c0 + a.per < a.blocks ? c0 + a.per : a.blocks;
     const int64_t head = ((int64_t)at.b * a.H + at.h) * a.dk * a.dv;
 
@@ -152,17 +167,18 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnArgs a) {
         S.clear();
     for (int i = threadIdx.x; i < N * PLD; i += kThreads) pt[i] = E(0);  // keys after queries
     if (threadIdx.x == 0) dec.bad = -1;
-    __syncthreads();
+    lds_barrier();
 
     QK qr, kr;
     V vr;
     float gr = 0.f;
     bool cut = false;
     auto fetch = [&](int64_t c) {
-        const int64_t t0 = c * N, rows = a.L - t0;
-        qr.load(q + t0 * a.ldq, a.ldq, rows, a.dk);
-        kr.load(k + t0 * a.ldk, a.ldk, rows, a.dk);
-        vr.load(v + t0 * a.ldv, a.ldv, rows, nv);
+        const int64_t t0 = c * N;
+        const int rows = there(a.L - t0);
+        qr.load(q + t0 * a.ldq, (int)a.ldq, rows, a.dk);
+        kr.load(k + t0 * a.ldk, (int)a.ldk, rows, a.dk);
+        vr.load(v + t0 * a.ldv, (int)a.ldv, rows, nv);
         if (wave == 0) {
             gr = 0.f, cut = false;
             if (lane < N && t0 + lane < a.L) {
@@ -174,27 +190,26 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnArgs a) {
     fetch(c0);
     for (int64_t c = c0; c < c1; ++c) {
         const int64_t t0 = c * N;
-        qr.store(qt);  // a query that is not finite stays in its own row
-        bool bad = kr.store(kt);
-        bad |= vr.store(vt);
+        const int rows = there(a.L - t0);
+        qr.store(qt, rows, a.dk);  // a query that is not finite stays in its own row
+        bool bad = kr.store(kt, rows, a.dk);
+        bad |= vr.store(vt, rows, nv);
         if (bad) dec.bad = (int)(c - c0);
         if (wave == 0) {
             dec.make(gr, cut);
             if (lane < N) glog[lane] = gr;
         }
-        __syncthreads();
+        lds_barrier();
         if (c + 1 < c1) fetch(c + 1);
         if (a.states) {
             float* st = a.states +
                         (((int64_t)at.b * a.blocks + c) * a.H + at.h) * a.DKs * (int64_t)a.DVs;
-            S.store(st, a.DKs, a.DVs, mycol);
+            S.keep(st, a.DKs, a.DVs, col0 + vcol);
         }
         E* o = (E*)a.o + (row0 + t0) * a.H * a.dv + (int64_t)at.h * a.dv + col0;
-        const int64_t rows = a.L - t0;
         if (dec.bad == (int)(c - c0)) {
             // token by token
-            const int n = rows < N ? (int)rows : N;
-            for (int t = 0; t < n; ++t) {
+            for (int t = 0; t < min(rows, N); ++t) {
                 const bool starts = dec.start[t] == t;
                 S.token(kt + t * QK::kLd, get(vt + t * V::kLd + vcol + s16),
                         hw_exp2(glog[t] * kLog2e), !starts, a.dk);
@@ -209,9 +224,9 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnArgs a) {
                 sum += __shfl_xor(sum, 16);
                 sum += __shfl_xor(sum, 32);
                 if (g == 0 && vcol + s16 < nv)
-                    st<BF16>(o, (int64_t)t * a.H * a.dv + vcol + s16, sum * a.scale);
+                    st<BF16>(o, t * ldo + vcol + s16, sum * a.scale);
             }
-            __syncthreads();
+            lds_barrier();
             continue;
         }
         // scores of queries i and keys j <= i, tiles dealt to the waves
@@ -253,7 +268,7 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) oacc[it][r] = in ? oacc[it][r] * w : 0.f;
         }
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
         for (int k0 = 0; k0 < N; k0 += 32) {
             const Frag vf = across<V::kLd>(vt, k0, vcol);
@@ -264,10 +279,10 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnArgs a) {
 #pragma unroll
         for (int it = 0; it < kIts; ++it) {
             const int i = it * 16 + s16;
-            if (i < rows) store4(o + (int64_t)i * a.H * a.dv, vcol + g * 4, nv, oacc[it]);
+            if (i < rows) store4<WHOLE>(o + i * ldo, vcol + g * 4, nv, oacc[it]);
         }
         S.template advance<BF16, QK::kLd, V::kLd>(kt, vt, vcol, dec, dec.last, 1.f);
-        __syncthreads();
+        lds_barrier();
     }
     if (a.h_last && c1 == a.blocks) S.store(a.h_last + head, a.dk, a.dv, mycol);
 }
@@ -277,12 +292,12 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_kernel(AttnArgs a) {
 // Forward in time over (k, v), or backward over (scale q, dO), where the state
 // is the gradient of the states: R before a block (in the walk's order) is dL/dS
 // at the block's end, and a token's decay comes behind its own term.
-template <bool BF16, int DK, bool REV, bool FULL>
-__global__ __launch_bounds__(kThreads) void attn_walk_kernel(AttnArgs a) {
+template <bool BF16, int DK, bool WHOLE, bool REV, bool FULL>
+__global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_walk_kernel(AttnArgs a) {
     typedef typename Io<BF16>::E E;
     constexpr int N = Io<BF16>::kBlock;
-    typedef Tile<BF16, DK> X;
-    typedef Tile<BF16, 64> Y;
+    typedef Tile<BF16, DK, WHOLE> X;
+    typedef Tile<BF16, 64, WHOLE> Y;
     __shared__ __align__(16) E xt[X::kSize];
     __shared__ __align__(16) E yt[Y::kSize];
     __shared__ Decays<N> dec;
@@ -312,7 +327,7 @@ __global__ __launch_bounds__(kThreads) void attn_walk_kernel(AttnArgs a) {
             S.load(first + head, a.dk, a.dv, mycol);
     }
     if (threadIdx.x == 0) dec.bad = -1;
-    __syncthreads();
+    lds_barrier();
 
     double total = 0.0;  // of the segment's log decays, in base 2
     bool any = false;    // a document starts in it
@@ -321,9 +336,10 @@ __global__ __launch_bounds__(kThreads) void attn_walk_kernel(AttnArgs a) {
     float gr = 0.f;
     bool cut = false;
     auto fetch = [&](int64_t n) {
-        const int64_t t0 = (REV ? a.blocks - 1 - n : n) * N, rows = a.L - t0;
-        xr.load(x + t0 * ldx, ldx, rows, a.dk);
-        yr.load(y + t0 * ldy, ldy, rows, nv);
+        const int64_t t0 = (REV ? a.blocks - 1 - n : n) * N;
+        const int rows = there(a.L - t0);
+        xr.load(x + t0 * ldx, (int)ldx, rows, a.dk);
+        yr.load(y + t0 * ldy, (int)ldy, rows, nv);
         if (wave == 0) {
             gr = 0.f, cut = false;
             if (lane < N && t0 + lane < a.L) {
@@ -335,22 +351,23 @@ __global__ __launch_bounds__(kThreads) void attn_walk_kernel(AttnArgs a) {
     fetch(n0);
     for (int64_t n = n0; n < n1; ++n) {
         const int64_t c = REV ? a.blocks - 1 - n : n;
-        bool bad = xr.store(xt);
-        bad |= yr.store(yt);
+        const int rows = there(a.L - c * N);
+        bool bad = xr.store(xt, rows, a.dk);
+        bad |= yr.store(yt, rows, nv);
         if (bad) dec.bad = (int)(n - n0);
         if (wave == 0) {
             dec.make(gr, cut);
             if (lane < N) glog[lane] = gr;
         }
-        __syncthreads();
+        lds_barrier();
         if (n + 1 < n1) fetch(n + 1);
         if (FULL && REV)
-            S.store(a.grads + (((int64_t)at.b * a.blocks + c) * a.H + at.h) * a.DKs * (int64_t)a.DVs,
-                    a.DKs, a.DVs, mycol);
+            S.keep(a.grads + (((int64_t)at.b * a.blocks + c) * a.H + at.h) * a.DKs * (int64_t)a.DVs,
+                   a.DKs, a.DVs, col0 + vcol);
         any |= dec.cut();
         total += (double)dec.hi[N - 1] + (double)dec.lo[N - 1];
         if (dec.bad == (int)(n - n0)) {
-            const int m = a.L - c * N < N ? (int)(a.L - c * N) : N;
+            const int m = min(rows, N);
             for (int e = 0; e < m; ++e) {
                 const int t = REV ? m - 1 - e : e;
                 const bool starts = dec.start[t] == t;
@@ -370,7 +387,7 @@ __global__ __launch_bounds__(kThreads) void attn_walk_kernel(AttnArgs a) {
             S.template advance<BF16, X::kLd, Y::kLd>(xt, yt, vcol, dec,
                                                      REV ? dec.first : dec.last, scale);
         }
-        __syncthreads();
+        lds_barrier();
     }
     if (FULL) {
         if (REV && a.dh0 && n1 == a.blocks) S.store(a.dh0 + head, a.dk, a.dv, mycol);
@@ -450,7 +467,7 @@ __global__ __launch_bounds__(kThreads) void attn_step_kernel(AttnArgs a) {
     const int64_t row0 = (int64_t)at.b * T;
     for (int t0 = 0; t0 < count; t0 += kStepBlock) {
         const int n = count - t0 < kStepBlock ? count - t0 : kStepBlock;
-        __syncthreads();
+        lds_barrier();
         for (int i = threadIdx.x; i < n * kMaxHeadDim; i += kThreads) {
             const int t = i / kMaxHeadDim, d = i % kMaxHeadDim;
             const int64_t row = row0 + t0 + t;
@@ -470,7 +487,7 @@ __global__ __launch_bounds__(kThreads) void attn_step_kernel(AttnArgs a) {
             const float rest = fmaf(g, kLog2e, -x) + g * 1.925963033500011079e-8f;
             decay[threadIdx.x] = g < kNoDecay ? -1.f : hw_exp2(x) * fmaf(rest, kLn2, 1.f);
         }
-        __syncthreads();
+        lds_barrier();
         for (int t = 0; t < n; ++t) {
             const f4 v = *reinterpret_cast<const f4*>(&vs[t][c]);
             const float w = decay[t];
@@ -496,7 +513,7 @@ __global__ __launch_bounds__(kThreads) void attn_step_kernel(AttnArgs a) {
             }
             // two buffers: the next token's sums do not wait for this one's readers
             if (lane < 16) *reinterpret_cast<f4*>(&sums[t & 1][wave][c]) = o;
-            __syncthreads();
+            lds_barrier();
             if ((int)threadIdx.x < nv) {
                 const int d = threadIdx.x;
                 const float sum = (sums[t & 1][0][d] + sums[t & 1][1][d]) +
@@ -521,6 +538,25 @@ __global__ __launch_bounds__(kThreads) void attn_step_kernel(AttnArgs a) {
         }
     }
 }
+
+// A kernel for the io type, dk's size, and rows of whole vectors or not.
+#define ATTN_EACH_(do_, bf16, a)                            \
+    do {                                                    \
+        const bool whole_ = a.dk % 8 == 0 && a.dv % 8 == 0; \
+        if (bf16 && a.dk <= 64) {                           \
+            if (whole_) do_(true, 64, true);                \
+            else do_(true, 64, false);                      \
+        } else if (bf16) {                                  \
+            if (whole_) do_(true, 128, true);               \
+            else do_(true, 128, false);                     \
+        } else if (a.dk <= 64) {                            \
+            if (whole_) do_(false, 64, true);               \
+            else do_(false, 64, false);                     \
+        } else {                                            \
+            if (whole_) do_(false, 128, true);              \
+            else do_(false, 128, false);                    \
+        }                                                   \
+    } while (0)
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -579,19 +615,16 @@ hipError_t launch_attn_carry(const AttnArgs& a, const float* first, hipStream_t 
 hipError_t launch_attn_walk(const AttnArgs& a, bool bf16, bool reverse, bool full, hipStream_t s) {
     ProfScope ps(s, full ? kPhaseMain : kPhaseSummary);
     const unsigned n = (unsigned)((int64_t)a.batch * a.H * a.tiles * (full ? a.nseg : a.nseg - 1));
-#define WALK_(B, DK)                                                                      \
+#define WALK_(B, DK, W)                                                                   \
     do {                                                                                  \
         if (!reverse)                                                                     \
-            attn_walk_kernel<B, DK, false, false><<<n, kThreads, 0, s>>>(a);              \
+            attn_walk_kernel<B, DK, W, false, false><<<n, kThreads, 0, s>>>(a);           \
         else if (full)                                                                    \
-            attn_walk_kernel<B, DK, true, true><<<n, kThreads, 0, s>>>(a);                \
+            attn_walk_kernel<B, DK, W, true, true><<<n, kThreads, 0, s>>>(a);             \
         else                                                                              \
-            attn_walk_kernel<B, DK, true, false><<<n, kThreads, 0, s>>>(a);               \
+            attn_walk_kernel<B, DK, W, true, false><<<n, kThreads, 0, s>>>(a);            \
     } while (0)
-    if (bf16 && a.dk <= 64) WALK_(true, 64);
-    else if (bf16) WALK_(true, 128);
-    else if (a.dk <= 64) WALK_(false, 64);
-    else WALK_(false, 128);
+    ATTN_EACH_(WALK_, bf16, a);
 #undef WALK_
     return hipGetLastError();
 }
@@ -607,10 +640,9 @@ hipError_t launch_attn_fwd(AttnArgs a, bool bf16, void* workspace, hipStream_t s
     }
     ProfScope ps(s, kPhaseMain);
     const unsigned n = (unsigned)((int64_t)a.batch * a.H * a.tiles * a.nseg);
-    if (bf16 && a.dk <= 64) attn_fwd_kernel<true, 64><<<n, kThreads, 0, s>>>(a);
-    else if (bf16) attn_fwd_kernel<true, 128><<<n, kThreads, 0, s>>>(a);
-    else if (a.dk <= 64) attn_fwd_kernel<false, 64><<<n, kThreads, 0, s>>>(a);
-    else attn_fwd_kernel<false, 128><<<n, kThreads, 0, s>>>(a);
+#define FWD_(B, DK, W) attn_fwd_kernel<B, DK, W><<<n, kThreads, 0, s>>>(a)
+    ATTN_EACH_(FWD_, bf16, a);
+#undef FWD_
     return hipGetLastError();
 }
 

@@ -36,15 +36,15 @@ __device__ __forceinline__ float sum_row(float x) {  // over 16 lanes
     return x;
 }
 
-template <bool BF16, int DK, int DV>
+template <bool BF16, int DK, int DV, bool WHOLE>
 struct GradShared {
     typedef typename Io<BF16>::E E;
     static constexpr int N = Io<BF16>::kBlock, kIts = N / 16;
     static constexpr int kScoreLd = N + Io<BF16>::kPad, kStateLd = DV + Io<BF16>::kPad;
-    __align__(16) E q[Tile<BF16, DK>::kSize];
-    __align__(16) E k[Tile<BF16, DK>::kSize];
-    __align__(16) E v[Tile<BF16, DV>::kSize];
-    __align__(16) E dO[Tile<BF16, DV>::kSize];
+    __align__(16) E q[Tile<BF16, DK, WHOLE>::kSize];
+    __align__(16) E k[Tile<BF16, DK, WHOLE>::kSize];
+    __align__(16) E v[Tile<BF16, DV, WHOLE>::kSize];
+    __align__(16) E dO[Tile<BF16, DV, WHOLE>::kSize];
     __align__(16) E A[N * kScoreLd];  // [i][j]
     __align__(16) E B[N * kScoreLd];
     __align__(16) E R[DK * kStateLd];  // rounded, for dv
@@ -55,13 +55,13 @@ struct GradShared {
     float later[kWaves][N], earlier[kWaves][N], both[kWaves];
 };
 
-template <bool BF16, int DK, int DV>
-__global__ __launch_bounds__(kThreads) void attn_grad_kernel(AttnArgs a) {
+template <bool BF16, int DK, int DV, bool WHOLE>
+__global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_kernel(AttnArgs a) {
     typedef typename Io<BF16>::E E;
     typedef typename Io<BF16>::Frag Frag;
-    typedef GradShared<BF16, DK, DV> Shared;
-    typedef Tile<BF16, DK> QK;
-    typedef Tile<BF16, DV> V;
+    typedef GradShared<BF16, DK, DV, WHOLE> Shared;
+    typedef Tile<BF16, DK, WHOLE> QK;
+    typedef Tile<BF16, DV, WHOLE> V;
     constexpr int N = Shared::N, kIts = Shared::kIts, SLD = Shared::kScoreLd,
                   RLD = Shared::kStateLd, QLD = QK::kLd, VLD = V::kLd;
     constexpr int kKt = DK / 64, kVt = DV / 64;  // tiles of 16 channels a wave takes
@@ -75,12 +75,12 @@ __global__ __launch_bounds__(kThreads) void attn_grad_kernel(AttnArgs a) {
     const int b = id / (uint32_t)a.blocks;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, s16 = lane & 15;
     const int group = a.H / a.Hk;
-    const int64_t row0 = (int64_t)b * a.L + c * N, rows = a.L - c * N;
-    const int n = rows < N ? (int)rows : N;
+    const int64_t row0 = (int64_t)b * a.L + c * N;
+    const int n = a.L - c * N < N ? (int)(a.L - c * N) : N, rows = n;
 
     for (int i = threadIdx.x; i < N * SLD; i += kThreads) sh.A[i] = sh.B[i] = E(0);
     if (threadIdx.x == 0) sh.dec.bad = 0;
-    __syncthreads();
+    lds_barrier();
 
     f4 dq[kKt][kIts], dk[kKt][kIts];
 #pragma unroll
@@ -91,21 +91,21 @@ __global__ __launch_bounds__(kThreads) void attn_grad_kernel(AttnArgs a) {
     bool qkbad = false;
     {
         QK t;
-        t.load((const E*)a.q + row0 * a.ldq + (int64_t)kh * a.dk, a.ldq, rows, a.dk);
-        qkbad = t.store(sh.q);
-        t.load((const E*)a.k + row0 * a.ldk + (int64_t)kh * a.dk, a.ldk, rows, a.dk);
-        qkbad |= t.store(sh.k);
+        t.load((const E*)a.q + row0 * a.ldq + (int64_t)kh * a.dk, (int)a.ldq, rows, a.dk);
+        qkbad = t.store(sh.q, rows, a.dk);
+        t.load((const E*)a.k + row0 * a.ldk + (int64_t)kh * a.dk, (int)a.ldk, rows, a.dk);
+        qkbad |= t.store(sh.k, rows, a.dk);
     }
     for (int n_head = 0; n_head < group; ++n_head) {
         const int h = kh * group + n_head;
         bool bad = qkbad;
         {
             V t;
-            const int64_t ldo = (int64_t)a.H * a.dv;
-            t.load((const E*)a.v + row0 * a.ldv + (int64_t)h * a.dv, a.ldv, rows, a.dv);
-            bad |= t.store(sh.v);
+            const int ldo = a.H * a.dv;
+            t.load((const E*)a.v + row0 * a.ldv + (int64_t)h * a.dv, (int)a.ldv, rows, a.dv);
+            bad |= t.store(sh.v, rows, a.dv);
             t.load((const E*)a.dO + row0 * ldo + (int64_t)h * a.dv, ldo, rows, a.dv);
-            bad |= t.store(sh.dO);
+            bad |= t.store(sh.dO, rows, a.dv);
         }
         if (bad) sh.dec.bad = n_head + 1;
         float gr = 0.f;
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(kThreads) void attn_grad_kernel(AttnArgs a) {
             }
             sh.dec.make(gr, cut);
         }
-        __syncthreads();
+        lds_barrier();
         const bool slow = sh.dec.bad == n_head + 1;
         const Decays<N>& dec = sh.dec;
 
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void attn_grad_kernel(AttnArgs a) {
         }
         both = sum_groups(sum_row(both));
         if (lane == 0) sh.both[wave] = both;
-        __syncthreads();
+        lds_barrier();
 
         // within the block
         f4 dv[kVt][kIts];
@@ -305,7 +305,7 @@ __global__ __launch_bounds__(kThreads) void attn_grad_kernel(AttnArgs a) {
             for (int jt = 0; jt < kIts; ++jt) {
                 const int j = jt * 16 + s16;
                 if (j < n)
-                    store4(out + (int64_t)j * a.H * a.dv, (m * kWaves + wave) * 16 + g * 4, a.dv,
+                    store4<WHOLE>(out + (int64_t)j * a.H * a.dv, (m * kWaves + wave) * 16 + g * 4, a.dv,
                            dv[m][jt]);
             }
         // the decays
@@ -329,7 +329,7 @@ __global__ __launch_bounds__(kThreads) void attn_grad_kernel(AttnArgs a) {
                 sum = sum_groups(sum_row(sum));
                 if (lane == 0) sh.glog[t] = sum;
             }
-            __syncthreads();
+            lds_barrier();
         }
         if (wave == 0) {
             const int t = lane < N ? lane : N - 1;
@@ -364,7 +364,7 @@ __global__ __launch_bounds__(kThreads) void attn_grad_kernel(AttnArgs a) {
                 a.dg[(row0 + lane) * a.H + h] = dg;
             }
         }
-        __syncthreads();
+        lds_barrier();
     }
     const int64_t ldo = (int64_t)a.Hk * a.dk;
     E* oq = (E*)a.dq + row0 * ldo + (int64_t)kh * a.dk;
@@ -375,8 +375,8 @@ __global__ __launch_bounds__(kThreads) void attn_grad_kernel(AttnArgs a) {
         for (int it = 0; it < kIts; ++it) {
             const int i = it * 16 + s16, d0 = (m * kWaves + wave) * 16 + g * 4;
             if (i < n) {
-                store4(oq + i * ldo, d0, a.dk, dq[m][it]);
-                store4(ok + i * ldo, d0, a.dk, dk[m][it]);
+                store4<WHOLE>(oq + i * ldo, d0, a.dk, dq[m][it]);
+                store4<WHOLE>(ok + i * ldo, d0, a.dk, dk[m][it]);
             }
         }
 }
@@ -390,24 +390,24 @@ __global__ __launch_bounds__(kThreads) void attn_fixed_kernel(AttnArgs a) {
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < n; i += kThreads) s += (double)a.part[i * a.H + h];
     sums[threadIdx.x] = s;
-    __syncthreads();
+    lds_barrier();
     for (int d = kThreads / 2; d; d /= 2) {
         if ((int)threadIdx.x < d) sums[threadIdx.x] += sums[threadIdx.x + d];
-        __syncthreads();
+        lds_barrier();
     }
     if (threadIdx.x == 0) a.dg[h] = (float)sums[0];
 }
 
-template <bool BF16, int DK, int DV>
+template <bool BF16, int DK, int DV, bool WHOLE>
 hipError_t launch_grad(const AttnArgs& a, hipStream_t s) {
-    constexpr int bytes = (int)sizeof(GradShared<BF16, DK, DV>);
+    constexpr int bytes = (int)sizeof(GradShared<BF16, DK, DV, WHOLE>);
     static_assert(bytes <= 160 * 1024, "LDS of a CU");
     const hipError_t e =
-        hipFuncSetAttribute(reinterpret_cast<const void*>(attn_grad_kernel<BF16, DK, DV>),
+        hipFuncSetAttribute(reinterpret_cast<const void*>(attn_grad_kernel<BF16, DK, DV, WHOLE>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
     const unsigned n = (unsigned)((int64_t)a.batch * a.Hk * a.blocks);
-    attn_grad_kernel<BF16, DK, DV><<<n, kThreads, bytes, s>>>(a);
+    attn_grad_kernel<BF16, DK, DV, WHOLE><<<n, kThreads, bytes, s>>>(a);
     return hipGetLastError();
 }
 
@@ -430,10 +430,13 @@ hipError_t launch_attn_bwd(AttnArgs a, bool bf16, void* workspace, hipStream_t s
     if ((e = launch_attn_walk(a, bf16, true, true, s)) != hipSuccess) return e;
     {
         ProfScope ps(s, kPhaseMain);
-#define GRAD_(B)                                                                       \
-    (a.dk <= 64 ? a.dv <= 64 ? launch_grad<B, 64, 64>(a, s) : launch_grad<B, 64, 128>(a, s) \
-                : a.dv <= 64 ? launch_grad<B, 128, 64>(a, s) : launch_grad<B, 128, 128>(a, s))
-        e = bf16 ? GRAD_(true) : GRAD_(false);
+#define GRAD_(B, W)                                                     \
+    (a.dk <= 64 ? a.dv <= 64 ? launch_grad<B, 64, 64, W>(a, s)          \
+                             : launch_grad<B, 64, 128, W>(a, s)         \
+                : a.dv <= 64 ? launch_grad<B, 128, 64, W>(a, s)         \
+                             : launch_grad<B, 128, 128, W>(a, s))
+        if (a.dk % 8 == 0 && a.dv % 8 == 0) e = bf16 ? GRAD_(true, true) : GRAD_(false, true);
+        else e = bf16 ? GRAD_(true, false) : GRAD_(false, false);
 #undef GRAD_
         if (e != hipSuccess) return e;
     }
