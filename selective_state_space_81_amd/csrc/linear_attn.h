@@ -30,7 +30,7 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 typedef u4 u4_align2 __attribute__((aligned(2)));
 typedef u4 u4_align4 __attribute__((aligned(4)));
 typedef f8 f8_align16 __attribute__((aligned(16)));
-typedef b4 b4_align2 __attribute__((aligned(2)));
+typedef u2 u2_align2 __attribute__((aligned(2)));
 typedef f4 f4_align4 __attribute__((aligned(4)));
 
 constexpr int kThreads = 256;
@@ -86,11 +86,14 @@ __device__ __forceinline__ f4 mma(f8 a, f8 b, f4 c) {
 // adds as much error as that output's own rounding.  Parts keeps all 24 bits, as
 // a sum of three bf16 numbers, for what ends in fp32 (states, gradients of
 // decays): two would leave 3e-6 of a state, three leave fp32's own error.
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {  // one conversion for both
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{lo, hi}), b2));
+}
 __device__ __forceinline__ b8 round(f8 x, b8) {
-    b8 y;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = (__bf16)x[e];
-    return y;
+    return __builtin_bit_cast(b8, u4{pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]),
+                                     pack(x[6], x[7])});
 }
 __device__ __forceinline__ f8 round(f8 x, f8) { return x; }
 __device__ __forceinline__ f8 widen(b8 x) {
@@ -106,15 +109,19 @@ struct Parts {
     typename Io<BF16>::Frag p[Io<BF16>::kParts];
     __device__ __forceinline__ explicit Parts(f8 x) {
         if constexpr (BF16) {
+            u4 part[3];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const __bf16 h = (__bf16)x[e];
-                const float r = x[e] - (float)h;
-                const __bf16 m = (__bf16)r;
-                p[0][e] = h;
-                p[1][e] = m;
-                p[2][e] = (__bf16)(r - (float)m);
+            for (int e = 0; e < 4; ++e) {
+                float lo = x[2 * e], hi = x[2 * e + 1];
+#pragma unroll
+                for (int n = 0; n < 3; ++n) {
+                    part[n][e] = pack(lo, hi);
+                    lo -= __uint_as_float(part[n][e] << 16);
+                    hi -= __uint_as_float(part[n][e] & 0xffff0000u);
+                }
             }
+#pragma unroll
+            for (int n = 0; n < 3; ++n) p[n] = __builtin_bit_cast(b8, part[n]);
         } else {
             p[0] = x;
         }
@@ -160,28 +167,32 @@ __device__ __forceinline__ f8 across(const float* tile, int k0, int col0) {
     for (int e = 0; e < 8; ++e) y[e] = p[e * LD];
     return y;
 }
-// Entries of an operand for a summed index that is taken 4 + 4 from two blocks
-// of 16, as two tiles of D hold them: along() with k0 + 4 g .. and k0 + 16 + 4 g ..
+// The same for a summed index that is taken 4 + 4 from two blocks of 16, as two
+// tiles of D hold them: rows k0 + 4 g .. and k0 + 16 + 4 g ..
 template <int LD>
-__device__ __forceinline__ b8 along_pair(const uint16_t* tile, int row0, int k0) {
-    const int l = threadIdx.x & 63;
-    const uint16_t* p = tile + (row0 + (l & 15)) * LD + k0 + (l >> 4) * 4;
-    const s4 a = *reinterpret_cast<const s4*>(p), b = *reinterpret_cast<const s4*>(p + 16);
+__device__ __forceinline__ b8 across_pair(const uint16_t* tile, int k0, int col0) {
+    typedef __attribute__((address_space(3))) s4* Lds;
+    const int l = threadIdx.x & 63, g = l >> 4, s = l & 15;
+    const uint16_t* p = tile + (k0 + g * 4 + (s >> 2)) * LD + col0 + (s & 3) * 4;
+    const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)p);
+    const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + 16 * LD));
     return __builtin_bit_cast(b8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 template <int LD>
-__device__ __forceinline__ f8 along_pair(const float* tile, int row0, int k0) {
+__device__ __forceinline__ f8 across_pair(const float* tile, int k0, int col0) {
     const int l = threadIdx.x & 63;
-    const float* p = tile + (row0 + (l & 15)) * LD + k0 + (l >> 4) * 4;
-    const f4 a = *reinterpret_cast<const f4*>(p), b = *reinterpret_cast<const f4*>(p + 16);
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    const float* p = tile + (k0 + (l >> 4) * 4) * LD + col0 + (l & 15);
+    f8 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        y[e] = p[e * LD];
+        y[4 + e] = p[(16 + e) * LD];
+    }
+    return y;
 }
 
 __device__ __forceinline__ void put4(uint16_t* p, f4 x) {
-    b4 y;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = (__bf16)x[e];
-    *reinterpret_cast<b4*>(p) = y;
+    *reinterpret_cast<u2*>(p) = u2{pack(x[0], x[1]), pack(x[2], x[3])};
 }
 __device__ __forceinline__ void put4(float* p, f4 x) { *reinterpret_cast<f4*>(p) = x; }
 __device__ __forceinline__ void put8(uint16_t* p, b8 x) { *reinterpret_cast<b8*>(p) = x; }
@@ -203,13 +214,11 @@ __device__ __forceinline__ f4 get4(const float* p) { return *reinterpret_cast<co
 // them or none).
 template <bool WHOLE, class E>
 __device__ __forceinline__ void store4(E* row, int i, int n, f4 x) {
-    typedef typename std::conditional<sizeof(E) == 2, b4, f4>::type V;
-    typedef typename std::conditional<sizeof(E) == 2, b4_align2, f4_align4>::type VA;
     if (WHOLE ? i < n : i + 4 <= n) {
-        V y;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = x[e];
-        *reinterpret_cast<VA*>(row + i) = y;
+        if constexpr (sizeof(E) == 2)
+            *reinterpret_cast<u2_align2*>(row + i) = u2{pack(x[0], x[1]), pack(x[2], x[3])};
+        else
+            *reinterpret_cast<f4_align4*>(row + i) = x;
     } else if (!WHOLE) {
 #pragma unroll
         for (int e = 0; e < 3; ++e)
@@ -248,6 +257,13 @@ struct Tile {
     }
     __device__ __forceinline__ void load(const E* base, int ld, int rows, int n) {
         const int last = (rows < kRows ? rows : kRows) - 1;
+        if (WHOLE && rows >= kRows) {
+            const int row = threadIdx.x / kVecs, c = threadIdx.x % kVecs * 8;
+            const uint32_t at = row * ld + min(c, n - 8);
+#pragma unroll
+            for (int m = 0; m < kMine; ++m) vector(m, base + m * (kThreads / kVecs) * ld + at);
+            return;
+        }
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
             const int id = m * kThreads + threadIdx.x, row = id / kVecs, c = id % kVecs * 8;
@@ -277,13 +293,18 @@ struct Tile {
     // To LDS; whether something was infinite or NaN.
     __device__ __forceinline__ bool store(E* tile, int rows, int n) {
         uint32_t bad = 0;
+        if (WHOLE && (rows < kRows || n < W)) {
+#pragma unroll
+            for (int m = 0; m < kMine; ++m) {
+                const int id = m * kThreads + threadIdx.x, row = id / kVecs, c = id % kVecs * 8;
+                if (!(row < rows && c < n))
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) r[m][w] = 0;
+            }
+        }
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
             const int id = m * kThreads + threadIdx.x, row = id / kVecs, c = id % kVecs * 8;
-            if (WHOLE && !(row < rows && c < n)) {
-#pragma unroll
-                for (int w = 0; w < kWords; ++w) r[m][w] = 0;
-            }
 #pragma unroll
             for (int h = 0; h < kWords / 4; ++h)
                 *reinterpret_cast<u4*>(tile + row * kLd + c + h * 4) =
@@ -295,6 +316,56 @@ struct Tile {
                             : (r[m][w] & 0x7f800000u) + 0x00800000u;
         }
         return (bad & (BF16 ? 0x80008000u : 0x80000000u)) != 0;
+    }
+};
+
+// 16 rows of W values as operands (along(), by lane), from global memory
+// straight into registers: what only one wave reads needs no LDS.
+template <bool BF16, int W, bool WHOLE>
+struct Rows {
+    typedef typename Io<BF16>::E E;
+    typedef typename Io<BF16>::Frag Frag;
+    static constexpr int kSteps = W / 32;
+    static constexpr int kWords = BF16 ? 4 : 8;
+    uint32_t r[kSteps][kWords];
+
+    __device__ __forceinline__ void load(const E* base, int ld, int row0, int rows, int n) {
+        const int l = threadIdx.x & 63;
+        const int row = min(row0 + (l & 15), rows - 1) * ld;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int c = s * 32 + (l >> 4) * 8;
+            typedef typename std::conditional<BF16, u4_align2, u4_align4>::type V;
+            if (WHOLE || c + 8 <= n) {
+                const E* p = base + (uint32_t)(row + (WHOLE ? min(c, n - 8) : c));
+#pragma unroll
+                for (int h = 0; h < kWords / 4; ++h) {
+                    const u4 x = *reinterpret_cast<const V*>(p + h * (BF16 ? 8 : 4));
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) r[s][h * 4 + w] = x[w];
+                }
+            } else {
+                const E* p = base + (uint32_t)(row + c);
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) r[s][w] = 0;
+#pragma unroll
+                for (int e = 0; e < 7; ++e)
+                    if (c + e < n) {
+                        if constexpr (BF16)
+                            r[s][e / 2] |= (uint32_t)p[e] << (e % 2 * 16);
+                        else
+                            r[s][e] = __float_as_uint(p[e]);
+                    }
+            }
+        }
+    }
+    __device__ __forceinline__ Frag operand(int s, int n) const {
+        typedef uint32_t U __attribute__((ext_vector_type(kWords)));
+        const bool in = !WHOLE || s * 32 + (int)((threadIdx.x & 63) >> 4) * 8 < n;
+        U x;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) x[w] = in ? r[s][w] : 0;
+        return __builtin_bit_cast(Frag, x);
     }
 };
 
@@ -324,16 +395,28 @@ __device__ __forceinline__ double lane64(double x, int lane) {
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+// x where `in`, else 0.  What computes x is kept out of the compiler's sight: a
+// branch around each exponential costs more than the exponentials.
+__device__ __forceinline__ float only(bool in, float x) {
+    asm volatile("" : "+v"(x));
+    return in ? x : 0.f;
+}
+
+// Decay from token j to token i (of whatever document), from the sums of log decays.
+__device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float lo_j) {
+    return hw_exp2((hi_i - hi_j) + (lo_i - lo_j));
+}
+
 // Sums of log decays in two floats each: they reach hundreds inside a block,
 // and the decay between neighbours needs the difference to 2^-24.
 template <int N>
 struct Decays {
-    float hi[N], lo[N];
+    __align__(16) float hi[N];
+    __align__(16) float lo[N];
     float first[N];  // 2^G_i, from the block's start to token i; 0 behind a document's start
     float last[N];   // 2^(G_last - G_i), from token i to the block's end; 0 before a start
     int start[N];    // where i's document starts in the block, or -1 before it
-    float whole;     // 2^G_last
-    int bad;         // number of the last block in which something was not finite
+    float whole;     // 2^G_last; 0 where a document starts in the block
 
     // By one wave, lane i for token i (g: its log decay; cut: it starts a
     // document).
@@ -359,12 +442,6 @@ struct Decays {
         }
     }
     __device__ __forceinline__ bool cut() const { return start[N - 1] >= 0; }
-    // Decay from token j to token i, 0 outside of j's document or time.
-    __device__ __forceinline__ float between(float hi_i, float lo_i, int start_i, int i, float hi_j,
-                                             float lo_j, int j) const {
-        const float d = hw_exp2((hi_i - hi_j) + (lo_i - lo_j));
-        return j <= i && j >= start_i ? d : 0.f;
-    }
 };
 
 // A decay that is 0 in fp32 starts a document.
@@ -374,6 +451,25 @@ constexpr float kNoDecay = -104.f;
 __device__ __forceinline__ float log_decay(const AttnArgs& a, int64_t row, int h) {
     return a.fixed ? a.g[h] : a.g[row * a.H + h];
 }
+
+// A lane's token of a block: its log decay and whether a document starts, asked
+// for ahead and looked at only when the block's turn comes.
+struct Token {
+    float g;
+    uint32_t reset;
+    __device__ __forceinline__ void load(const AttnArgs& a, int64_t row0, int rows, int h, int n) {
+        const int i = min((int)(threadIdx.x & 63), min(rows, n) - 1);
+        g = log_decay(a, row0 + i, h);
+        reset = 0;
+        if (a.reset) reset = a.reset[row0 + i];
+    }
+    // behind the last token the state stays as it is
+    __device__ __forceinline__ void settle(int rows) {
+        const bool in = (int)(threadIdx.x & 63) < rows;
+        g = in ? g : 0.f;
+        reset = in && (reset || g < kNoDecay);
+    }
+};
 
 }  // namespace attn
 }  // namespace msscan

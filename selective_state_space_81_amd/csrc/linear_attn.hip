@@ -5,12 +5,16 @@
 //
 // In blocks of tokens (linear_attn.h) all of it but the decays is products of
 // small matrices, on the matrix cores.  A workgroup walks along the blocks of
-// one (batch row, head, 64 columns of dv), each wave with 16 of the columns: its
-// state, [dk][16] in fp32, stays in registers in the layout in which the matrix
-// instructions leave it, which is also the one in which they take it as the
-// operand of q S (with the summed index permuted, which a sum allows).  So every
-// input is read once and the state never moves.  q, k and v of the next block
-// are on their way into registers while the present one is computed.
+// one (batch row, head, 64 columns of dv).  A wave takes 16 queries of a block
+// for the outputs: their scores stay in registers, in the layout in which one
+// matrix instruction leaves them and the next takes them (with the summed index
+// permuted, which a sum allows), and their rows of q come straight from memory.
+// And it takes 16 of the columns for the state: [dk][16] in fp32, in registers,
+// from which the block's end leaves a copy rounded to bf16 in LDS for the next
+// block's queries.  So inputs are read once, the state never moves, and two
+// barriers a block suffice.  Loads of the next block are under way while the
+// present one is computed; its decays are summed up by the first wave, which has
+// the fewest keys to look at.
 //
 // A sequence is cut into segments where heads and columns are too few for the
 // chip: a first pass sums up the segments but the last (k and v only), a second
@@ -39,6 +43,13 @@ struct Place {
 
 // Tokens left, as far as a block goes.
 __device__ __forceinline__ int there(int64_t n) { return n < 128 ? (int)n : 128; }
+
+// A number that is the same again and again, but not to the compiler, which
+// would keep a mask for every comparison with it.
+__device__ __forceinline__ int opaque(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
 
 // A wave's 16 columns of a state: tile t, entry r is S[16 t + 4 g + r][col].
 template <int DK>
@@ -96,34 +107,53 @@ struct State {
         const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
         for (int k0 = 0; k0 < N; k0 += 32) {
+            typename Io<BF16>::Frag xf[kTiles];
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) xf[t] = across<XLD>(xt, k0, t * 16);
             f8 y = widen(across<YLD>(yt, k0, ycol));
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] *= w[k0 + g * 8 + e] * scale;
             const Parts<BF16> yp(y);
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-                s[t] = mma_rows<BF16>(across<XLD>(xt, k0, t * 16), yp, s[t]);
+            for (int n = Io<BF16>::kParts - 1; n >= 0; --n)
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) s[t] = mma(xf[t], yp.p[n], s[t]);
         }
     }
-    template <bool BF16>
-    static __device__ __forceinline__ f4 mma_rows(typename Io<BF16>::Frag a, const Parts<BF16>& b,
-                                                  f4 c) {
+    // Rounded to the io type for the queries: [column][dk], this wave's columns.
+    template <int LD, class E>
+    __device__ __forceinline__ void publish(E* st, int vcol) const {
+        const int l = threadIdx.x & 63;
+        E* p = st + (vcol + (l & 15)) * LD + (l >> 4 << 2);
 #pragma unroll
-        for (int n = Io<BF16>::kParts - 1; n >= 0; --n) c = mma(a, b.p[n], c);
-        return c;
+        for (int t = 0; t < kTiles; ++t) put4(p + t * 16, s[t]);
     }
     // One token, where matrix products would carry what is not finite into
     // places that it does not reach: s = decay s + x y (keep false: s = x y).
     template <class E>
     __device__ __forceinline__ void token(const E* x, float y, float decay, bool keep, int dk) {
         const int row = (threadIdx.x & 63) >> 4 << 2;
+        const int left = opaque(dk - row);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int d = t * 16 + row + r;
-                if (d < dk) s[t][r] = fmaf(get(x + d), y, keep ? s[t][r] * decay : 0.f);
-            }
+            for (int r = 0; r < 4; ++r)
+                if (t * 16 + r < left)
+                    s[t][r] = fmaf(get(x + t * 16 + row + r), y, keep ? s[t][r] * decay : 0.f);
+    }
+    // q's product with the wave's columns, of one token
+    template <class E>
+    __device__ __forceinline__ float meet(const E* q, int dk) const {
+        const int row = (threadIdx.x & 63) >> 4 << 2;
+        const int left = opaque(dk - row);
+        float sum = 0.f;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (t * 16 + r < left) sum = fmaf(get(q + t * 16 + row + r), s[t][r], sum);
+        sum += __shfl_xor(sum, 16);
+        return sum + __shfl_xor(sum, 32);
     }
 };
 
@@ -133,20 +163,23 @@ template <bool BF16, int DK, bool WHOLE>
 __global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_fwd_kernel(AttnArgs a) {
     typedef typename Io<BF16>::E E;
     typedef typename Io<BF16>::Frag Frag;
-    constexpr int N = Io<BF16>::kBlock, kIts = N / 16;
-    typedef Tile<BF16, DK, WHOLE> QK;
+    constexpr int N = Io<BF16>::kBlock, kIts = N / 16;  // tiles of queries, and of keys
+    constexpr int kCols = 64 * kIts / kWaves;           // columns of a wave's outputs
+    typedef Tile<BF16, DK, WHOLE> K;
     typedef Tile<BF16, 64, WHOLE> V;
-    constexpr int PLD = N + Io<BF16>::kPad;
-    __shared__ __align__(16) E qt[QK::kSize];
-    __shared__ __align__(16) E kt[QK::kSize];
+    constexpr int SLD = DK + Io<BF16>::kPad;
+    __shared__ __align__(16) E kt[K::kSize];
     __shared__ __align__(16) E vt[V::kSize];
-    __shared__ __align__(16) E pt[N * PLD];  // scores, [i][j]
-    __shared__ Decays<N> dec;
-    __shared__ float glog[N];
+    __shared__ __align__(16) E st[64 * SLD];  // the state before the block, [column][dk]
+    __shared__ Decays<N> decays[2];
+    __shared__ float glog[2][N];
+    __shared__ int bad_block;  // the last one in which something was not finite
 
     const Place at(a, a.nseg);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, s16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, g = lane >> 4, s16 = lane & 15;
     const int col0 = at.tile * 64, vcol = wave * 16, mycol = col0 + vcol + s16;
+    const int it = wave % kIts, ocol = wave / kIts * kCols, i = it * 16 + s16;
     const int nv = a.dv - col0 < 64 ? a.dv - col0 : 64;
     const int kh = at.h / (a.H / a.Hk);
     const int64_t row0 = (int64_t)at.b * a.L;
@@ -154,7 +187,9 @@ __global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_fwd_kernel(At
     const E* k = (const E*)a.k + row0 * a.ldk + (int64_t)kh * a.dk;
     const E* v = (const E*)a.v + row0 * a.ldv + (int64_t)at.h * a.dv + col0;
     const int ldo = a.H * a.dv;
-    const int64_t c0 = at.seg * a.per, c1 = c0 + a.per < a.blocks ? c0 + a.per : a.blocks;
+    const int blocks = (int)a.blocks;
+    const int c0 = at.seg * (int)a.per, c1 = min(c0 + (int)a.per, blocks);
+    const float scale = a.scale;
     const int64_t head = ((int64_t)at.b * a.H + at.h) * a.dk * a.dv;
 
     State<DK> S;
@@ -165,126 +200,130 @@ __global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_fwd_kernel(At
         S.load(a.h0 + head, a.dk, a.dv, mycol);
     else
         S.clear();
-    for (int i = threadIdx.x; i < N * PLD; i += kThreads) pt[i] = E(0);  // keys after queries
-    if (threadIdx.x == 0) dec.bad = -1;
+    S.template publish<SLD>(st, vcol);
+    if (threadIdx.x == 0) bad_block = -1;
     lds_barrier();
 
-    QK qr, kr;
+    Rows<BF16, DK, WHOLE> qr, qn;  // of this block and the next
+    K kr;
     V vr;
-    float gr = 0.f;
-    bool cut = false;
-    auto fetch = [&](int64_t c) {
-        const int64_t t0 = c * N;
-        const int rows = there(a.L - t0);
-        qr.load(q + t0 * a.ldq, (int)a.ldq, rows, a.dk);
-        kr.load(k + t0 * a.ldk, (int)a.ldk, rows, a.dk);
-        vr.load(v + t0 * a.ldv, (int)a.ldv, rows, nv);
+    Token tok;
+    auto tokens = [&](int c) {  // of block c, at least one of which is there
+        if (wave == 0) tok.load(a, row0 + (int64_t)c * N, there(a.L - (int64_t)c * N), at.h, N);
+    };
+    auto settle = [&](int c) {
         if (wave == 0) {
-            gr = 0.f, cut = false;
-            if (lane < N && t0 + lane < a.L) {
-                gr = log_decay(a, row0 + t0 + lane, at.h);
-                cut = gr < kNoDecay || (a.reset && a.reset[row0 + t0 + lane]);
-            }
+            tok.settle(there(a.L - (int64_t)c * N));
+            decays[c & 1].make(tok.g, tok.reset);
+            if (lane < N) glog[c & 1][lane] = tok.g;
         }
     };
-    fetch(c0);
-    for (int64_t c = c0; c < c1; ++c) {
-        const int64_t t0 = c * N;
+    auto fetch = [&](int c) {
+        const int64_t t0 = (int64_t)c * N;
         const int rows = there(a.L - t0);
-        qr.store(qt, rows, a.dk);  // a query that is not finite stays in its own row
+        kr.load(k + t0 * a.ldk, (int)a.ldk, rows, a.dk);
+        vr.load(v + t0 * a.ldv, (int)a.ldv, rows, nv);
+        qn.load(q + t0 * a.ldq, (int)a.ldq, it * 16, rows, a.dk);
+    };
+    tokens(c0);
+    fetch(c0);
+    settle(c0);
+    if (c0 + 1 < c1) tokens(c0 + 1);
+    for (int c = c0; c < c1; ++c) {
+        const int64_t t0 = (int64_t)c * N;
+        const int rows = there(a.L - t0);
+        qr = qn;  // a query that is not finite stays in its own row
         bool bad = kr.store(kt, rows, a.dk);
         bad |= vr.store(vt, rows, nv);
-        if (bad) dec.bad = (int)(c - c0);
-        if (wave == 0) {
-            dec.make(gr, cut);
-            if (lane < N) glog[lane] = gr;
-        }
+        if (bad) bad_block = c - c0;
         lds_barrier();
-        if (c + 1 < c1) fetch(c + 1);
+        const Decays<N>& dec = decays[c & 1];
+        E* o = (E*)a.o + (row0 + t0) * ldo + (int64_t)at.h * a.dv + col0;
+        if (c + 1 < c1) {
+            settle(c + 1);
+            if (c + 2 < c1) tokens(c + 2);
+            fetch(c + 1);
+        }
         if (a.states) {
             float* st = a.states +
                         (((int64_t)at.b * a.blocks + c) * a.H + at.h) * a.DKs * (int64_t)a.DVs;
             S.keep(st, a.DKs, a.DVs, col0 + vcol);
         }
-        E* o = (E*)a.o + (row0 + t0) * a.H * a.dv + (int64_t)at.h * a.dv + col0;
-        if (dec.bad == (int)(c - c0)) {
-            // token by token
+        if (bad_block == c - c0) {
+            // token by token; the queries take the place of the state's copy
+            lds_barrier();
+            if (wave < kIts)
+#pragma unroll
+                for (int s = 0; s < DK / 32; ++s)
+                    put8(st + i * SLD + s * 32 + g * 8, qr.operand(s, a.dk));
+            lds_barrier();
             for (int t = 0; t < min(rows, N); ++t) {
                 const bool starts = dec.start[t] == t;
-                S.token(kt + t * QK::kLd, get(vt + t * V::kLd + vcol + s16),
-                        hw_exp2(glog[t] * kLog2e), !starts, a.dk);
-                float sum = 0.f;
+                S.token(kt + t * K::kLd, get(vt + t * V::kLd + vcol + s16),
+                        hw_exp2(glog[c & 1][t] * kLog2e), !starts, a.dk);
+                const float sum = S.meet(st + t * SLD, a.dk);
+                if (g == 0 && vcol + s16 < nv)
+                    dev::st<BF16>(o, t * ldo + vcol + s16, sum * scale);
+            }
+        } else {
+            Frag qf[DK / 32];
 #pragma unroll
-                for (int i = 0; i < State<DK>::kTiles; ++i)
+            for (int s = 0; s < DK / 32; ++s) qf[s] = qr.operand(s, a.dk);
+            // what the state before the block gives
+            f4 oacc[kCols / 16];
+#pragma unroll
+            for (int n = 0; n < kCols / 16; ++n) oacc[n] = f4{0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < DK / 32; ++s)
+#pragma unroll
+                for (int n = 0; n < kCols / 16; ++n)
+                    oacc[n] = mma(along<SLD>(st, ocol + n * 16, s * 32), qf[s], oacc[n]);
+            const int start = dec.start[i];
+            const float first = dec.first[i] * scale;
+#pragma unroll
+            for (int n = 0; n < kCols / 16; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) oacc[n][r] = start < 0 ? oacc[n][r] * first : 0.f;
+            // scores of 32 keys at a time, and what the keys' values give
+            const float hi = dec.hi[i], lo = dec.lo[i];
+            const int from = start < 0 ? 0 : start;
+#pragma unroll
+            for (int k0 = 0; k0 < N; k0 += 32) {
+                if (k0 > it * 16) break;
+                f4 p[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+                for (int s = 0; s < DK / 32; ++s)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        p[x] = mma(along<K::kLd>(kt, k0 + x * 16, s * 32), qf[s], p[x]);
+                f8 w;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int j = k0 + x * 16 + g * 4;
+                    const f4 hj = *reinterpret_cast<const f4*>(&dec.hi[j]);
+                    const f4 lj = *reinterpret_cast<const f4*>(&dec.lo[j]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int d = i * 16 + g * 4 + r;
-                        if (d < a.dk) sum = fmaf(get(qt + t * QK::kLd + d), S.s[i][r], sum);
+                        const bool in = (uint32_t)(j + r - from) <= (uint32_t)(i - from);
+                        w[x * 4 + r] =
+                            only(in, p[x][r] * (decay(hi, lo, hj[r], lj[r]) * scale));
                     }
-                sum += __shfl_xor(sum, 16);
-                sum += __shfl_xor(sum, 32);
-                if (g == 0 && vcol + s16 < nv)
-                    st<BF16>(o, t * ldo + vcol + s16, sum * a.scale);
+                }
+                const Frag pf = round(w, Frag{});
+#pragma unroll
+                for (int n = 0; n < kCols / 16; ++n)
+                    oacc[n] = mma(across_pair<V::kLd>(vt, k0, ocol + n * 16), pf, oacc[n]);
             }
-            lds_barrier();
-            continue;
-        }
-        // scores of queries i and keys j <= i, tiles dealt to the waves
+            if (i < rows)
 #pragma unroll
-        for (int n = 0; n < (kIts * (kIts + 1) / 2 + kWaves - 1) / kWaves; ++n) {
-            int it = 0, jt = n * kWaves + wave;
-            while (jt > it) jt -= ++it;
-            if (it >= kIts) break;
-            f4 p = {0, 0, 0, 0};
-#pragma unroll
-            for (int d = 0; d < DK; d += 32)
-                p = mma(along<QK::kLd>(kt, jt * 16, d), along<QK::kLd>(qt, it * 16, d), p);
-            const int i = it * 16 + s16, j = jt * 16 + g * 4;
-            const float hi = dec.hi[i], lo = dec.lo[i];
-            const int start = dec.start[i];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float w = dec.between(hi, lo, start, i, dec.hi[j + r], dec.lo[j + r], j + r);
-                p[r] = j + r <= i && j + r >= start ? p[r] * (w * a.scale) : 0.f;
-            }
-            put4(pt + i * PLD + j, p);
-        }
-        // what the state before the block gives
-        f4 oacc[kIts];
-#pragma unroll
-        for (int it = 0; it < kIts; ++it) oacc[it] = f4{0, 0, 0, 0};
-#pragma unroll
-        for (int t = 0; t < State<DK>::kTiles; t += 2) {
-            const Frag sf = round(
-                __builtin_shufflevector(S.s[t], S.s[t + 1], 0, 1, 2, 3, 4, 5, 6, 7), Frag{});
-#pragma unroll
-            for (int it = 0; it < kIts; ++it)
-                oacc[it] = mma(sf, along_pair<QK::kLd>(qt, it * 16, t * 16), oacc[it]);
-        }
-#pragma unroll
-        for (int it = 0; it < kIts; ++it) {
-            const bool in = dec.start[it * 16 + s16] < 0;
-            const float w = dec.first[it * 16 + s16] * a.scale;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) oacc[it][r] = in ? oacc[it][r] * w : 0.f;
+                for (int n = 0; n < kCols / 16; ++n)
+                    store4<WHOLE>(o + i * ldo, ocol + n * 16 + g * 4, nv, oacc[n]);
+            S.template advance<BF16, K::kLd, V::kLd>(kt, vt, vcol, dec, dec.last, 1.f);
         }
         lds_barrier();
-#pragma unroll
-        for (int k0 = 0; k0 < N; k0 += 32) {
-            const Frag vf = across<V::kLd>(vt, k0, vcol);
-#pragma unroll
-            for (int it = k0 / 16; it < kIts; ++it)
-                oacc[it] = mma(vf, along<PLD>(pt, it * 16, k0), oacc[it]);
-        }
-#pragma unroll
-        for (int it = 0; it < kIts; ++it) {
-            const int i = it * 16 + s16;
-            if (i < rows) store4<WHOLE>(o + i * ldo, vcol + g * 4, nv, oacc[it]);
-        }
-        S.template advance<BF16, QK::kLd, V::kLd>(kt, vt, vcol, dec, dec.last, 1.f);
-        lds_barrier();
+        if (c + 1 < c1) S.template publish<SLD>(st, vcol);
     }
-    if (a.h_last && c1 == a.blocks) S.store(a.h_last + head, a.dk, a.dv, mycol);
+    if (a.h_last && c1 == blocks) S.store(a.h_last + head, a.dk, a.dv, mycol);
 }
 
 // ---- walk of the states alone ----------------------------------------------------------
@@ -300,11 +339,13 @@ __global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_walk_kernel(A
     typedef Tile<BF16, 64, WHOLE> Y;
     __shared__ __align__(16) E xt[X::kSize];
     __shared__ __align__(16) E yt[Y::kSize];
-    __shared__ Decays<N> dec;
-    __shared__ float glog[N];
+    __shared__ Decays<N> decays[2];
+    __shared__ float glog[2][N];
+    __shared__ int bad_block;  // the last one in which something was not finite
 
     const Place at(a, FULL ? a.nseg : a.nseg - 1);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, s16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, s16 = lane & 15;
     const int col0 = at.tile * 64, vcol = wave * 16, mycol = col0 + vcol + s16;
     const int nv = a.dv - col0 < 64 ? a.dv - col0 : 64;
     const int kh = at.h / (a.H / a.Hk);
@@ -313,7 +354,8 @@ __global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_walk_kernel(A
     const E* x = (const E*)(REV ? a.q : a.k) + row0 * ldx + (int64_t)kh * a.dk;
     const E* y = (const E*)(REV ? a.dO : a.v) + row0 * ldy + (int64_t)at.h * a.dv + col0;
     const float scale = REV ? a.scale : 1.f;
-    const int64_t n0 = at.seg * a.per, n1 = n0 + a.per < a.blocks ? n0 + a.per : a.blocks;
+    const int blocks = (int)a.blocks;
+    const int n0 = at.seg * (int)a.per, n1 = min(n0 + (int)a.per, blocks);
     const int64_t head = ((int64_t)at.b * a.H + at.h) * a.dk * a.dv;
     const int64_t seg = (((int64_t)at.b * a.nseg + at.seg) * a.H + at.h);
     const float* first = REV ? a.dh_last : a.h0;
@@ -326,52 +368,60 @@ __global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_walk_kernel(A
         else if (first)
             S.load(first + head, a.dk, a.dv, mycol);
     }
-    if (threadIdx.x == 0) dec.bad = -1;
-    lds_barrier();
+    if (threadIdx.x == 0) bad_block = -1;
 
     double total = 0.0;  // of the segment's log decays, in base 2
     bool any = false;    // a document starts in it
     X xr;
     Y yr;
-    float gr = 0.f;
-    bool cut = false;
-    auto fetch = [&](int64_t n) {
-        const int64_t t0 = (REV ? a.blocks - 1 - n : n) * N;
+    Token tok;
+    auto block = [&](int n) { return REV ? blocks - 1 - n : n; };
+    auto tokens = [&](int n) {
+        const int64_t t0 = (int64_t)block(n) * N;
+        if (wave == 0) tok.load(a, row0 + t0, there(a.L - t0), at.h, N);
+    };
+    auto settle = [&](int n) {
+        if (wave == 0) {
+            tok.settle(there(a.L - (int64_t)block(n) * N));
+            decays[n & 1].make(tok.g, tok.reset);
+            if (lane < N) glog[n & 1][lane] = tok.g;
+        }
+    };
+    auto fetch = [&](int n) {
+        const int64_t t0 = (int64_t)block(n) * N;
         const int rows = there(a.L - t0);
         xr.load(x + t0 * ldx, (int)ldx, rows, a.dk);
         yr.load(y + t0 * ldy, (int)ldy, rows, nv);
-        if (wave == 0) {
-            gr = 0.f, cut = false;
-            if (lane < N && t0 + lane < a.L) {
-                gr = log_decay(a, row0 + t0 + lane, at.h);
-                cut = gr < kNoDecay || (a.reset && a.reset[row0 + t0 + lane]);
-            }
-        }
     };
+    tokens(n0);
     fetch(n0);
-    for (int64_t n = n0; n < n1; ++n) {
-        const int64_t c = REV ? a.blocks - 1 - n : n;
-        const int rows = there(a.L - c * N);
+    settle(n0);
+    if (n0 + 1 < n1) tokens(n0 + 1);
+    lds_barrier();
+    for (int n = n0; n < n1; ++n) {
+        const int c = block(n);
+        const int rows = there(a.L - (int64_t)c * N);
         bool bad = xr.store(xt, rows, a.dk);
         bad |= yr.store(yt, rows, nv);
-        if (bad) dec.bad = (int)(n - n0);
-        if (wave == 0) {
-            dec.make(gr, cut);
-            if (lane < N) glog[lane] = gr;
-        }
+        if (bad) bad_block = n - n0;
         lds_barrier();
-        if (n + 1 < n1) fetch(n + 1);
+        const Decays<N>& dec = decays[n & 1];
+        if (n + 1 < n1) {
+            settle(n + 1);
+            if (n + 2 < n1) tokens(n + 2);
+            fetch(n + 1);
+        }
         if (FULL && REV)
             S.keep(a.grads + (((int64_t)at.b * a.blocks + c) * a.H + at.h) * a.DKs * (int64_t)a.DVs,
                    a.DKs, a.DVs, col0 + vcol);
         any |= dec.cut();
         total += (double)dec.hi[N - 1] + (double)dec.lo[N - 1];
-        if (dec.bad == (int)(n - n0)) {
+        if (bad_block == n - n0) {
             const int m = min(rows, N);
             for (int e = 0; e < m; ++e) {
                 const int t = REV ? m - 1 - e : e;
                 const bool starts = dec.start[t] == t;
-                const float decay = hw_exp2(glog[t] * kLog2e);
+                const float decay = hw_exp2(glog[n & 1][t] * kLog2e);
                 const float val = get(yt + t * Y::kLd + vcol + s16) * scale;
                 if (REV) {
                     S.token(xt + t * X::kLd, val, 1.f, true, a.dk);
@@ -390,7 +440,7 @@ __global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_walk_kernel(A
         lds_barrier();
     }
     if (FULL) {
-        if (REV && a.dh0 && n1 == a.blocks) S.store(a.dh0 + head, a.dk, a.dv, mycol);
+        if (REV && a.dh0 && n1 == blocks) S.store(a.dh0 + head, a.dk, a.dv, mycol);
     } else {
         S.store(a.seg + seg * a.dk * a.dv, a.dk, a.dv, mycol);
         if (at.tile == 0 && threadIdx.x == 0) a.seg_f[seg] = any ? -1.f : (float)exp2(total);
@@ -571,10 +621,11 @@ void attn_plan(AttnArgs& a, bool bf16) {
     a.tiles = (a.dv + 63) / 64;
     a.DKs = (a.dk + 15) / 16 * 16;
     a.DVs = (a.dv + 15) / 16 * 16;
-    // Two workgroups a CU; segments of at least four blocks, or the joining
-    // costs more than it brings.
+    // Two workgroups a CU and none beyond them, which would run by themselves at
+    // the end; segments of at least four blocks, or the joining costs more than
+    // it brings (131072 tokens of 12 heads of 128: 504 workgroups 751 us, 528 1150).
     const int64_t wgs = (int64_t)a.batch * a.H * a.tiles;
-    int64_t nseg = wgs >= 256 ? 1 : (512 + wgs - 1) / wgs;
+    int64_t nseg = 512 / wgs;
     if (nseg > a.blocks / 4) nseg = a.blocks / 4;
     if (nseg < 1) nseg = 1;
     a.per = (a.blocks + nseg - 1) / nseg;

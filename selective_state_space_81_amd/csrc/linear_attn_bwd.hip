@@ -50,6 +50,7 @@ struct GradShared {
     __align__(16) E R[DK * kStateLd];  // rounded, for dv
     Decays<N> dec;
     float glog[N];
+    int bad;  // number of the last head in which something was not finite
     float rows[kIts][N];  // [key tile][i]: sums of A_ij dO_i . v_j
     float cols[kIts][N];  // [query tile][j]
     float later[kWaves][N], earlier[kWaves][N], both[kWaves];
@@ -79,7 +80,7 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
     const int n = a.L - c * N < N ? (int)(a.L - c * N) : N, rows = n;
 
     for (int i = threadIdx.x; i < N * SLD; i += kThreads) sh.A[i] = sh.B[i] = E(0);
-    if (threadIdx.x == 0) sh.dec.bad = 0;
+    if (threadIdx.x == 0) sh.bad = 0;
     lds_barrier();
 
     f4 dq[kKt][kIts], dk[kKt][kIts];
@@ -107,18 +108,15 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
             t.load((const E*)a.dO + row0 * ldo + (int64_t)h * a.dv, ldo, rows, a.dv);
             bad |= t.store(sh.dO, rows, a.dv);
         }
-        if (bad) sh.dec.bad = n_head + 1;
-        float gr = 0.f;
-        bool cut = false;
+        if (bad) sh.bad = n_head + 1;
         if (wave == 0) {
-            if (lane < n) {
-                gr = log_decay(a, row0 + lane, h);
-                cut = gr < kNoDecay || (a.reset && a.reset[row0 + lane]);
-            }
-            sh.dec.make(gr, cut);
+            Token tok;
+            tok.load(a, row0, rows, h, N);
+            tok.settle(rows);
+            sh.dec.make(tok.g, tok.reset);
         }
         lds_barrier();
-        const bool slow = sh.dec.bad == n_head + 1;
+        const bool slow = sh.bad == n_head + 1;
         const Decays<N>& dec = sh.dec;
 
         // scores, and the sums over them that the decays' gradient needs
@@ -136,17 +134,18 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
                 ov = mma(along<VLD>(sh.v, jt * 16, d), along<VLD>(sh.dO, it * 16, d), ov);
             const int i = it * 16 + s16, j = jt * 16 + g * 4;
             const float hi = dec.hi[i], lo = dec.lo[i];
-            const int start = dec.start[i];
+            const int start = dec.start[i], from = start < 0 ? 0 : start;
+            const f4 hj = *reinterpret_cast<const f4*>(&dec.hi[j]);
+            const f4 lj = *reinterpret_cast<const f4*>(&dec.lo[j]);
             f4 A, B, M;
             float row = 0.f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const bool in = j + r <= i && j + r >= start;
-                const float w =
-                    a.scale * dec.between(hi, lo, start, i, dec.hi[j + r], dec.lo[j + r], j + r);
-                A[r] = in ? qk[r] * w : 0.f;
-                B[r] = in ? ov[r] * w : 0.f;
-                M[r] = in ? A[r] * ov[r] : 0.f;
+                const bool in = (uint32_t)(j + r - from) <= (uint32_t)(i - from);
+                const float w = a.scale * decay(hi, lo, hj[r], lj[r]);
+                A[r] = only(in, qk[r] * w);
+                B[r] = only(in, ov[r] * w);
+                M[r] = only(in, A[r] * ov[r]);
                 row += M[r];
                 const float col = sum_row(M[r]);
                 if (s16 == 0) sh.cols[it][j + r] = col;
@@ -323,7 +322,7 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
                         for (int d = 0; d < a.dv; ++d)
                             ov = fmaf(get(sh.dO + i * VLD + d), get(sh.v + j * VLD + d), ov);
                         sum += qk * ov * a.scale *
-                               dec.between(dec.hi[i], dec.lo[i], start, i, dec.hi[j], dec.lo[j], j);
+                               decay(dec.hi[i], dec.lo[i], dec.hi[j], dec.lo[j]);
                     }
                 }
                 sum = sum_groups(sum_row(sum));
