@@ -259,6 +259,7 @@ struct VerifyArgs {
     float* logprob;            // [batch][drafts + 1]
     double* part;  // [rows][splits][2]: largest exponent, sum beside it
     double* mass;  // [batch][pieces][2]: of what is left, and of the target's
+    uint32_t* done;  // [batch]: pieces whose mass is there
     int64_t ld, ldd;
     int64_t V;
     float scale;
@@ -271,7 +272,7 @@ struct VerifyArgs {
     int pieces;      // of a row that is drawn from
 };
 struct VerifyWs {
-    size_t part, mass, total;
+    size_t part, mass, done, total;
 };
 void verify_plan(VerifyArgs& a, bool bf16, bool drafted);
 VerifyWs verify_ws(const VerifyArgs& a);

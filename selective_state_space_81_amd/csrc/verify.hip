@@ -9,11 +9,12 @@
 //
 // Whole numbers come out of comparisons of sums over the vocabulary, so all of
 // it is in fp64, the exponentials too (a polynomial of 2^f, relative error
-// 3e-13): in fp32 one draw in some hundred would fall on the other side of a
-// border.  Three launches: the largest logit and the sum of every row, in one
-// pass over all logits; the mass of pieces of the one row of each sequence that
-// is drawn from (every workgroup finds out which by itself: a few comparisons);
-// and the search, over pieces and then inside one.
+// 1e-13): in fp32 one draw in some hundred would fall on the other side of a
+// border.  Two launches: the largest logit and the sum of every row, in one pass
+// over all logits; then the mass of pieces of the one row of each sequence that
+// is drawn from (every workgroup finds out which by itself: a few comparisons),
+// and, in the workgroup that is the last of its sequence, the search over pieces
+// and inside one.
 #include <type_traits>
 
 #include "device_common.h"
@@ -52,8 +53,31 @@ __device__ __forceinline__ double exp2_64(double x) {
     return x < -1000.0 ? 0.0 : y;
 }
 
-// Largest exponent (in base 2) and sum beside it.  Nothing yet, or only masked
-// logits: m = -inf, s = 0.  NaN and +inf: s becomes NaN.
+// The same for a whole vocabulary, with the 64th roots of 2 in LDS: half the
+// fp64 operations, which bound the sums of rows (64 x 9 rows of 131072 bf16: 80
+// -> 50 us).  x = n / 64 + r, |r| <= 1/128; the series of 2^r up to r^4, whose
+// next term is 4e-14.  The addition of 3 2^45 leaves n in the low bits.
+struct Roots {
+    double v[64];
+    __device__ __forceinline__ void make() {
+        if (threadIdx.x < 64) v[threadIdx.x] = exp2_64((double)threadIdx.x / 64.0 - 1.0) * 2.0;
+    }
+    // x >= -1000 (or NaN)
+    __device__ __forceinline__ double exp2(double x) const {
+        const double magic = 105553116266496.0;
+        const double shifted = x + magic, r = x - (shifted - magic);
+        const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, shifted);
+        double p = 0.0096181291076284772;
+        p = fma(p, r, 0.0555041086648215800);
+        p = fma(p, r, 0.2402265069591007123);
+        p = fma(p, r, 0.6931471805599453094);
+        p = fma(p, r, 1.0);
+        return __builtin_amdgcn_ldexp(p * v[n & 63], n >> 6);
+    }
+};
+
+// An exponent (in base 2) near the largest, and the sum beside it.  Nothing yet,
+// or only masked logits: m = -inf, s = 0.  NaN and +inf: s becomes NaN.
 struct Sum {
     double m, s;
     __device__ __forceinline__ void add(const Sum& o) {
@@ -104,31 +128,46 @@ template <bool BF16>
 __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a) {
     constexpr int W = Row<BF16>::W;
     __shared__ Sum sums[kThreads / 64];
+    __shared__ Roots roots;
+    roots.make();
+    __syncthreads();
     const int64_t r = blockIdx.x / a.splits;
     const int split = blockIdx.x % a.splits;
     const int64_t i0 = split * a.per, i1 = i0 + a.per < a.V ? i0 + a.per : a.V;
     const void* row = row_of<BF16>(a, r);
     const double c = (double)a.scale * 1.4426950408889634074;
-    float top = -INFINITY;  // the largest logit so far, of this thread
+    // Sums stand beside 2^m of a logit met early on.  fp64 reaches far enough that
+    // only one 2^500 times as likely calls for another; and 2^-999 of it is nothing.
+    float high = -INFINITY, low = INFINITY;
     double m = -INFINITY, s = 0.0;
     for (int64_t i = i0 + threadIdx.x * W; i < i1; i += kThreads * W) {
         float v[W];
         Row<BF16>::load(row, i, i1, v);
-        float t = v[0];
+        float t = v[0], l = v[0];
 #pragma unroll
-        for (int e = 1; e < W; ++e) t = fmaxf(t, v[e]);
-        if (t > top) {
+        for (int e = 1; e < W; ++e) t = fmaxf(t, v[e]), l = fminf(l, v[e]);
+        if (t > high) {
             const double now = (double)t * c;
-            s = top == -INFINITY ? s : s * exp2_64(m - now);
-            top = t, m = now;
+            s = m == -INFINITY ? s : s * exp2_64(m - now);
+            m = now;
+            high = (float)((m + 500.0) / c);
+            low = (float)((m - 999.0) / c);
         }
-        if (top == -INFINITY) {  // nothing but masked logits, or NaN
+        if (m == -INFINITY) {  // nothing but masked logits, or NaN
 #pragma unroll
             for (int e = 0; e < W; ++e) s += v[e] == v[e] ? 0.0 : (double)v[e];
         } else {
+            if (l < low)
 #pragma unroll
-            for (int e = 0; e < W; ++e) s += exp2_64((double)v[e] * c - m);
+                for (int e = 0; e < W; ++e) v[e] = v[e] < low ? low : v[e];  // not a NaN
+#pragma unroll
+            for (int e = 0; e < W; ++e) s += roots.exp2(fma((double)v[e], c, -m));
         }
+    }
+    if (split == 0 && r < a.batch) {  // for the next launch
+        if (threadIdx.x == 0) a.done[r] = 0;
+        for (int n = threadIdx.x; n < 2 * a.pieces; n += kThreads)
+            a.mass[r * a.pieces * 2 + n] = -1.0;
     }
     Sum x{m, s};
 #pragma unroll
@@ -149,11 +188,29 @@ struct Shared {
     int count;
 };
 
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) x += shfl_xor64(x, d);
+    return x;
+}
+// A row's parts, one after another by a thread, or by the lanes of a wave.
 __device__ __forceinline__ Sum row_sum(const VerifyArgs& a, int64_t r) {
     Sum x{-INFINITY, 0.0};
     for (int n = 0; n < a.splits; ++n)
         x.add(Sum{a.part[(r * a.splits + n) * 2], a.part[(r * a.splits + n) * 2 + 1]});
     return x;
+}
+__device__ __forceinline__ Sum row_sum_by_wave(const VerifyArgs& a, int64_t r) {
+    const int n = threadIdx.x & 63;
+    Sum x{-INFINITY, 0.0};
+    if (n < a.splits) x = Sum{a.part[(r * a.splits + n) * 2], a.part[(r * a.splits + n) * 2 + 1]};
+    double m = x.m;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const double y = shfl_xor64(m, d);
+        m = y > m ? y : m;
+    }
+    return {m, wave_sum(m == -INFINITY ? x.s : x.s * exp2_64(x.m - m))};
 }
 // whether the row is a distribution
 __device__ __forceinline__ bool proper(const Sum& x) { return x.s > 0.0 && x.s < INFINITY; }
@@ -175,10 +232,16 @@ template <bool BF16>
 __device__ __forceinline__ void decide(const VerifyArgs& a, int b, Shared& sh) {
     const int T = a.drafts, t = threadIdx.x;
     const int64_t first = (int64_t)b * (T + 1);
-    if (t <= T) {
+    const int64_t first_q = (int64_t)a.batch * (T + 1) + (int64_t)b * T;
+    if (a.splits > 4) {
+        for (int n = t >> 6; n <= T + (a.draft_logits ? T : 0); n += kThreads / 64) {
+            const Sum x = row_sum_by_wave(a, n <= T ? first + n : first_q + n - T - 1);
+            if ((t & 63) == 0) (n <= T ? sh.p[n] : sh.q[n - T - 1]) = x;
+        }
+    } else if (t <= T) {
         sh.p[t] = row_sum(a, first + t);
     } else if (t >= 128 && t - 128 < T && a.draft_logits) {
-        sh.q[t - 128] = row_sum(a, (int64_t)a.batch * (T + 1) + (int64_t)b * T + t - 128);
+        sh.q[t - 128] = row_sum(a, first_q + t - 128);
     }
     __syncthreads();
     if (t < T) {
@@ -188,9 +251,7 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, int b, Shared& sh) {
             const double p = prob<BF16>(a, row_of<BF16>(a, first + t), v, sh.p[t]);
             double q = 1.0;
             if (a.draft_logits)
-                q = proper(sh.q[t]) ? prob<BF16>(a, row_of<BF16>(a, (int64_t)a.batch * (T + 1) +
-                                                                       (int64_t)b * T + t),
-                                                 v, sh.q[t])
+                q = proper(sh.q[t]) ? prob<BF16>(a, row_of<BF16>(a, first_q + t), v, sh.q[t])
                                     : INFINITY;
             yes = (double)a.uniforms[first + t] * q < p;
         }
@@ -233,56 +294,18 @@ struct Drawn {
             }
         }
     }
-    __device__ __forceinline__ Left at(float x, float y, int64_t v) const {
-        const double mine = exp2_64((double)x * c - p.m);
+    __device__ __forceinline__ Left at(const Roots& roots, float x, float y, int64_t v) const {
+        const double mine = unit(roots, fma((double)x, c, -p.m));
         double left = mine;
-        if (qrow) left = mine - exp2_64((double)y * c - q.m) * ratio;
+        if (qrow) left = fma(-unit(roots, fma((double)y, c, -q.m)), ratio, mine);
         if (v == one) left = 0.0;
         return {mine, left > 0.0 ? left : 0.0};
     }
+    static __device__ __forceinline__ double unit(const Roots& roots, double x) {
+        const double y = roots.exp2(x < -999.0 ? -999.0 : x);
+        return x < -999.0 ? 0.0 : y;
+    }
 };
-
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) x += shfl_xor64(x, d);
-    return x;
-}
-
-template <bool BF16>
-__global__ __launch_bounds__(kThreads) void verify_mass_kernel(VerifyArgs a) {
-    constexpr int W = Row<BF16>::W;
-    __shared__ Shared sh;
-    __shared__ double sums[2][kThreads / 64];
-    const int b = blockIdx.x / a.pieces, piece = blockIdx.x % a.pieces;
-    decide<BF16>(a, b, sh);
-    const Drawn<BF16> from(a, b, sh);
-    const int64_t i0 = (int64_t)piece * kPiece,
-                  i1 = i0 + kPiece < a.V ? i0 + kPiece : a.V;
-    double left = 0.0, own = 0.0;
-    if (proper(from.p))
-        for (int64_t i = i0 + threadIdx.x * W; i < i1; i += kThreads * W) {
-            float x[W], y[W];
-            Row<BF16>::load(from.prow, i, i1, x);
-            if (from.qrow) Row<BF16>::load(from.qrow, i, i1, y);
-#pragma unroll
-            for (int e = 0; e < W; ++e) {
-                const Left l = from.at(x[e], from.qrow ? y[e] : 0.f, i + e);
-                left += l.left;
-                own += l.p;
-            }
-        }
-    left = wave_sum(left);
-    own = wave_sum(own);
-    if ((threadIdx.x & 63) == 0) {
-        sums[0][threadIdx.x >> 6] = left;
-        sums[1][threadIdx.x >> 6] = own;
-    }
-    __syncthreads();
-    if (threadIdx.x < 2) {
-        const double* s = sums[threadIdx.x];
-        a.mass[blockIdx.x * 2 + threadIdx.x] = (s[0] + s[1]) + (s[2] + s[3]);
-    }
-}
 
 // Sums up to and with each thread's x, over the workgroup.
 __device__ __forceinline__ double scan(double x, double (&sums)[kThreads / 64]) {
@@ -299,29 +322,54 @@ __device__ __forceinline__ double scan(double x, double (&sums)[kThreads / 64]) 
     return x;
 }
 
+// The least x of the workgroup's threads that is not negative, or -1; and the
+// greatest.
+__device__ __forceinline__ int least(int x, int (&of)[kThreads / 64]) {
+    uint32_t u = (uint32_t)x;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) u = min(u, (uint32_t)__shfl_xor((int)u, d));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) of[threadIdx.x >> 6] = (int)u;
+    __syncthreads();
+    return (int)min(min((uint32_t)of[0], (uint32_t)of[1]), min((uint32_t)of[2], (uint32_t)of[3]));
+}
+__device__ __forceinline__ int greatest(int x, int (&of)[kThreads / 64]) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) x = max(x, __shfl_xor(x, d));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) of[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return max(max(of[0], of[1]), max(of[2], of[3]));
+}
+
+// A mass that another workgroup wrote in this launch.  It is one word, which no
+// fence has to order (a fence would write back and drop whole caches: 50 of 76 us
+// for 64 sequences); at most it is still on its way, for who reads it has seen
+// that its writer was past writing it.
+__device__ __forceinline__ double shared_load(const double* p) {
+    double x;
+    do {
+        x = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    } while (x < 0.0);
+    return x;
+}
+
+// The token drawn, or -1: over the pieces' masses, then inside one.
 template <bool BF16>
-__global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a) {
-    __shared__ Shared sh;
+__device__ __forceinline__ int64_t draw(const VerifyArgs& a, int b, const Drawn<BF16>& from,
+                                        const Roots& roots) {
     __shared__ double sums[kThreads / 64];
-    __shared__ double before;   // mass ahead of the piece
-    __shared__ int piece;       // that holds the border
-    __shared__ int last;        // place of the last value with mass in it
-    __shared__ int found;       // first place past the border
-    const int b = blockIdx.x, T = a.drafts, tid = threadIdx.x;
-    decide<BF16>(a, b, sh);
-    const Drawn<BF16> from(a, b, sh);
+    __shared__ int of[kThreads / 64];
+    __shared__ double before;  // mass ahead of the piece
+    constexpr int W = Row<BF16>::W;
+    const int tid = threadIdx.x;
     const double* mass = a.mass + (int64_t)b * a.pieces * 2;
-    if (tid == 0) {
-        piece = -1;
-        last = -1;
-        found = kPiece;
-    }
     // the whole: of what is left, or of the target's where nothing is
     double whole = 0.0;
     int which = 0;
     for (; which < 2; ++which) {
         double x = 0.0;
-        for (int n = tid; n < a.pieces; n += kThreads) x += mass[n * 2 + which];
+        for (int n = tid; n < a.pieces; n += kThreads) x += shared_load(mass + n * 2 + which);
         x = wave_sum(x);
         __syncthreads();
         if ((tid & 63) == 0) sums[tid >> 6] = x;
@@ -329,67 +377,101 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a) {
         whole = (sums[0] + sums[1]) + (sums[2] + sums[3]);
         if (whole > 0.0) break;
     }
-    const double u = (double)a.uniforms[(int64_t)b * (T + 1) + T];
-    int drawn = -1;
-    if (proper(from.p) && whole > 0.0) {
-        const double border = u * whole;
-        // the first piece past the border, or the last one with mass at all
-        double ahead = 0.0;
-        for (int n0 = 0; n0 < a.pieces && piece < 0; n0 += kThreads) {
-            const int n = n0 + tid;
-            const double x = n < a.pieces ? mass[n * 2 + which] : 0.0;
-            const double upto = ahead + scan(x, sums);
-            const double whole_so_far = ahead + ((sums[0] + sums[1]) + (sums[2] + sums[3]));
-            const bool past = x > 0.0 && upto > border;
-            if (x > 0.0) atomicMax(&last, n);
-            if (past) atomicMin(&found, n - n0);
-            __syncthreads();
-            if (found < kPiece && tid == found) {
-                piece = n;
-                before = upto - x;
-            }
-            ahead = whole_so_far;
-            __syncthreads();
-        }
-        if (piece < 0 && tid == 0) {  // rounding, or a number that is not below 1
-            piece = last;
-            before = 0.0;
-        }
-        __syncthreads();
-        const bool over = found == kPiece;
-        __syncthreads();
-        if (tid == 0) {
-            found = kPiece;
-            last = -1;
-        }
-        __syncthreads();
-        const int64_t i0 = (int64_t)piece * kPiece,
-                      i1 = i0 + kPiece < a.V ? i0 + kPiece : a.V;
-        // kMine neighbouring values a thread
-        double x[kMine], sum = 0.0;
-#pragma unroll
-        for (int e = 0; e < kMine; ++e) {
-            const int64_t v = i0 + tid * kMine + e;
-            x[e] = 0.0;
-            if (v < i1) {
-                const Left l = from.at(ld<BF16>(from.prow, v),
-                                       from.qrow ? ld<BF16>(from.qrow, v) : 0.f, v);
-                x[e] = which ? l.p : l.left;
-            }
-            sum += x[e];
-        }
-        double upto = before + (scan(sum, sums) - sum);
-#pragma unroll
-        for (int e = 0; e < kMine; ++e) {
-            upto += x[e];
-            if (x[e] > 0.0) {
-                atomicMax(&last, tid * kMine + e);
-                if (!over && upto > border) atomicMin(&found, tid * kMine + e);
-            }
-        }
-        __syncthreads();
-        drawn = (int)i0 + (found < kPiece ? found : last);
+    if (!proper(from.p) || !(whole > 0.0)) return -1;
+    const double border = (double)a.uniforms[(int64_t)b * (a.drafts + 1) + a.drafts] * whole;
+    // the first piece past the border, or else (rounding, or a number that is not
+    // below 1) the last one with mass at all
+    int piece = -1, last = -1;
+    double ahead = 0.0;
+    for (int n0 = 0; n0 < a.pieces && piece < 0; n0 += kThreads) {
+        const int n = n0 + tid;
+        const double x = n < a.pieces ? shared_load(mass + n * 2 + which) : 0.0;
+        const double upto = ahead + scan(x, sums);
+        ahead += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        piece = least(x > 0.0 && upto > border ? n : -1, of);
+        last = max(last, greatest(x > 0.0 ? n : -1, of));
+        if (n == piece) before = upto - x;
     }
+    const bool over = piece < 0;
+    if (over) piece = last;
+    __syncthreads();
+    const int64_t i0 = (int64_t)piece * kPiece, i1 = i0 + kPiece < a.V ? i0 + kPiece : a.V;
+    // kMine neighbouring values a thread
+    double x[kMine], sum = 0.0;
+    const int mine = tid * kMine;
+#pragma unroll
+    for (int k = 0; k < kMine; k += W) {
+        float u[W], v[W];
+        Row<BF16>::load(from.prow, i0 + mine + k, i1, u);
+        if (from.qrow) Row<BF16>::load(from.qrow, i0 + mine + k, i1, v);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            const Left l = from.at(roots, u[e], from.qrow ? v[e] : 0.f, i0 + mine + k + e);
+            x[k + e] = which ? l.p : l.left;
+            sum += x[k + e];
+        }
+    }
+    double upto = (over ? 0.0 : before) + (scan(sum, sums) - sum);
+    int found = -1;
+    last = -1;
+#pragma unroll
+    for (int e = 0; e < kMine; ++e) {
+        upto += x[e];
+        if (x[e] > 0.0) {
+            last = mine + e;
+            if (found < 0 && !over && upto > border) found = mine + e;
+        }
+    }
+    found = least(found, of);
+    last = greatest(last, of);
+    return i0 + (found >= 0 ? found : last);
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a) {
+    constexpr int W = Row<BF16>::W;
+    __shared__ Shared sh;
+    __shared__ Roots roots;
+    __shared__ double sums[2][kThreads / 64];
+    __shared__ bool finish;
+    const int b = blockIdx.x / a.pieces, piece = blockIdx.x % a.pieces;
+    const int tid = threadIdx.x, T = a.drafts;
+    roots.make();
+    decide<BF16>(a, b, sh);
+    const Drawn<BF16> from(a, b, sh);
+    const int64_t i0 = (int64_t)piece * kPiece, i1 = i0 + kPiece < a.V ? i0 + kPiece : a.V;
+    double left = 0.0, own = 0.0;
+    if (proper(from.p))
+        for (int64_t i = i0 + tid * W; i < i1; i += kThreads * W) {
+            float x[W], y[W];
+            Row<BF16>::load(from.prow, i, i1, x);
+            if (from.qrow) Row<BF16>::load(from.qrow, i, i1, y);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const Left l = from.at(roots, x[e], from.qrow ? y[e] : 0.f, i + e);
+                left += l.left;
+                own += l.p;
+            }
+        }
+    left = wave_sum(left);
+    own = wave_sum(own);
+    if ((tid & 63) == 0) {
+        sums[0][tid >> 6] = left;
+        sums[1][tid >> 6] = own;
+    }
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+            __hip_atomic_store(a.mass + (int64_t)blockIdx.x * 2 + n,
+                               (sums[n][0] + sums[n][1]) + (sums[n][2] + sums[n][3]),
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        finish = __hip_atomic_fetch_add(a.done + b, 1u, __ATOMIC_RELAXED,
+                                        __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)a.pieces - 1;
+    }
+    __syncthreads();
+    if (!finish) return;
+    const int64_t drawn = draw<BF16>(a, b, from, roots);
     // the tokens, and their log probabilities under the target
     if (tid <= T) {
         const int64_t at = (int64_t)b * (T + 1) + tid;
@@ -397,11 +479,9 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a) {
         if (tid < sh.count) v = draft(a, b, tid);
         else if (tid == sh.count) v = drawn;
         double lp = 0.0;
-        if (v >= 0) {
-            const double c = (double)a.scale;
-            lp = (double)ld<BF16>(row_of<BF16>(a, at), v) * c -
+        if (v >= 0)
+            lp = (double)ld<BF16>(row_of<BF16>(a, at), v) * (double)a.scale -
                  sh.p[tid].m * 0.693147180559945309417 - log(sh.p[tid].s);
-        }
         a.tokens[at] = (int32_t)v;
         a.logprob[at] = (float)lp;
     }
@@ -432,7 +512,8 @@ VerifyWs verify_ws(const VerifyArgs& a) {
     VerifyWs w{};
     w.part = 0;
     w.mass = up256((size_t)a.rows * a.splits * 2 * sizeof(double));
-    w.total = w.mass + up256((size_t)a.batch * a.pieces * 2 * sizeof(double));
+    w.done = w.mass + up256((size_t)a.batch * a.pieces * 2 * sizeof(double));
+    w.total = w.done + up256((size_t)a.batch * sizeof(uint32_t));
     return w;
 }
 
@@ -445,20 +526,18 @@ hipError_t launch_verify(VerifyArgs a, bool bf16, void* workspace, hipStream_t s
     const VerifyWs w = verify_ws(a);
     a.part = (double*)((char*)workspace + w.part);
     a.mass = (double*)((char*)workspace + w.mass);
+    a.done = (uint32_t*)((char*)workspace + w.done);
     const unsigned n = (unsigned)(a.rows * a.splits), m = (unsigned)((int64_t)a.batch * a.pieces);
     {
         ProfScope ps(s, kPhaseMain);
         if (bf16) verify_sum_kernel<true><<<n, kThreads, 0, s>>>(a);
         else verify_sum_kernel<false><<<n, kThreads, 0, s>>>(a);
     }
-    {
-        ProfScope ps(s, kPhaseSummary);
-        if (bf16) verify_mass_kernel<true><<<m, kThreads, 0, s>>>(a);
-        else verify_mass_kernel<false><<<m, kThreads, 0, s>>>(a);
-    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     ProfScope ps(s, kPhaseReduce);
-    if (bf16) verify_draw_kernel<true><<<a.batch, kThreads, 0, s>>>(a);
-    else verify_draw_kernel<false><<<a.batch, kThreads, 0, s>>>(a);
+    if (bf16) verify_draw_kernel<true><<<m, kThreads, 0, s>>>(a);
+    else verify_draw_kernel<false><<<m, kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
