@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "dpp64.h"
 #include "lm_internal.h"
 
 namespace msscan {
@@ -370,30 +371,6 @@ struct Rows {
 };
 
 // ---- decays of a block ---------------------------------------------------------------
-
-// Sums over the lanes up to each, in fp64, with DPP moves: no trip through LDS.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double dpp64(double x) {  // 0 where no lane gives anything
-    const uint64_t u = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0u, (uint32_t)u, CTRL, ROWS, 0xf, false);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0u, (uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ double scan64(double x) {
-    x += dpp64<0x111, 0xf>(x);  // row_shr 1, 2, 4, 8: within 16 lanes
-    x += dpp64<0x112, 0xf>(x);
-    x += dpp64<0x114, 0xf>(x);
-    x += dpp64<0x118, 0xf>(x);
-    x += dpp64<0x142, 0xa>(x);  // lane 15 of a row to the next one, lane 31 to the upper half
-    x += dpp64<0x143, 0xc>(x);
-    return x;
-}
-__device__ __forceinline__ double lane64(double x, int lane) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, lane);
-    const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), lane);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
 
 // x where `in`, else 0.  What computes x is kept out of the compiler's sight: a
 // branch around each exponential costs more than the exponentials.

@@ -270,6 +270,7 @@ struct VerifyArgs {
     int splits;      // workgroups of a row
     int64_t per;     // values each of them takes
     int pieces;      // of a row that is drawn from
+    int piece;       // values of one
 };
 struct VerifyWs {
     size_t part, mass, done, total;

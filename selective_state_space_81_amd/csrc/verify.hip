@@ -9,7 +9,7 @@
 //
 // Whole numbers come out of comparisons of sums over the vocabulary, so all of
 // it is in fp64, the exponentials too (a polynomial of 2^f, relative error
-// 1e-13): in fp32 one draw in some hundred would fall on the other side of a
+// 2e-12): in fp32 one draw in some hundred would fall on the other side of a
 // border.  Two launches: the largest logit and the sum of every row, in one pass
 // over all logits; then the mass of pieces of the one row of each sequence that
 // is drawn from (every workgroup finds out which by itself: a few comparisons),
@@ -18,6 +18,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "dpp64.h"
 #include "lm_internal.h"
 #include "msscan_internal.h"
 
@@ -28,13 +29,13 @@ namespace {
 using namespace dev;
 
 constexpr int kThreads = 256;
-constexpr int kPiece = 4096;  // values of a piece: 16 a thread in the search
-constexpr int kMine = kPiece / kThreads;
+constexpr int kMine = 8;  // values a thread looks at together in the search
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef u4 u4_align2 __attribute__((aligned(2)));
 typedef u4 u4_align4 __attribute__((aligned(4)));
 
-// 2^x for x <= 0 (or NaN); 0 from -1000 down, which no sum notices.
+// 2^x for x <= 0 (or NaN); 0 from -1000 down, which no sum notices.  power(): of
+// either sign, up to 1000.
 __device__ __forceinline__ double exp2_64(double x) {
     const double n = __builtin_rint(x), f = (x - n) * 0.693147180559945309417;
     // the series of e^f, |f| <= 0.3466: the first term left out is 2e-13
@@ -53,26 +54,30 @@ __device__ __forceinline__ double exp2_64(double x) {
     return x < -1000.0 ? 0.0 : y;
 }
 
-// The same for a whole vocabulary, with the 64th roots of 2 in LDS: half the
-// fp64 operations, which bound the sums of rows (64 x 9 rows of 131072 bf16: 80
-// -> 50 us).  x = n / 64 + r, |r| <= 1/128; the series of 2^r up to r^4, whose
-// next term is 4e-14.  The addition of 3 2^45 leaves n in the low bits.
+__device__ __forceinline__ double power(double x) {
+    return x > 0.0 ? 1.0 / exp2_64(-x) : exp2_64(x);
+}
+
+// The same for a whole vocabulary, with the 128th roots of 2 in LDS: half the
+// fp64 operations, which run at half fp32's rate here and bound the sums of rows
+// (64 x 9 rows of 131072 bf16: 80 -> 56 us).  x = n / 128 + r, |r| <= 1/256; the
+// series of 2^r up to r^3, whose next term is 2e-12.  The addition of 3 2^44
+// leaves n in the low bits.
 struct Roots {
-    double v[64];
+    double v[128];
     __device__ __forceinline__ void make() {
-        if (threadIdx.x < 64) v[threadIdx.x] = exp2_64((double)threadIdx.x / 64.0 - 1.0) * 2.0;
+        if (threadIdx.x < 128) v[threadIdx.x] = exp2_64((double)threadIdx.x / 128.0 - 1.0) * 2.0;
     }
     // x >= -1000 (or NaN)
     __device__ __forceinline__ double exp2(double x) const {
-        const double magic = 105553116266496.0;
+        const double magic = 52776558133248.0;
         const double shifted = x + magic, r = x - (shifted - magic);
         const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, shifted);
-        double p = 0.0096181291076284772;
-        p = fma(p, r, 0.0555041086648215800);
+        double p = 0.0555041086648215800;
         p = fma(p, r, 0.2402265069591007123);
         p = fma(p, r, 0.6931471805599453094);
         p = fma(p, r, 1.0);
-        return __builtin_amdgcn_ldexp(p * v[n & 63], n >> 6);
+        return __builtin_amdgcn_ldexp(p * v[n & 127], n >> 7);
     }
 };
 
@@ -89,7 +94,6 @@ struct Sum {
         }
     }
 };
-__device__ __forceinline__ double shfl_xor64(double x, int d) { return __shfl_xor(x, d); }
 
 template <bool BF16>
 struct Row {
@@ -156,13 +160,13 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a) {
         if (m == -INFINITY) {  // nothing but masked logits, or NaN
 #pragma unroll
             for (int e = 0; e < W; ++e) s += v[e] == v[e] ? 0.0 : (double)v[e];
-        } else {
-            if (l < low)
-#pragma unroll
-                for (int e = 0; e < W; ++e) v[e] = v[e] < low ? low : v[e];  // not a NaN
-#pragma unroll
-            for (int e = 0; e < W; ++e) s += roots.exp2(fma((double)v[e], c, -m));
+            continue;
         }
+        if (l < low)
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = v[e] < low ? low : v[e];  // not a NaN
+#pragma unroll
+        for (int e = 0; e < W; ++e) s += roots.exp2(fma((double)v[e], c, -m));
     }
     if (split == 0 && r < a.batch) {  // for the next launch
         if (threadIdx.x == 0) a.done[r] = 0;
@@ -171,7 +175,7 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a) {
     }
     Sum x{m, s};
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) x.add(Sum{shfl_xor64(x.m, d), shfl_xor64(x.s, d)});
+    for (int d = 1; d < 64; d *= 2) x.add(Sum{__shfl_xor(x.m, d), __shfl_xor(x.s, d)});
     if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = x;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -185,14 +189,11 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a) {
 struct Shared {
     Sum p[kMaxDrafts + 1], q[kMaxDrafts];
     int yes[kMaxDrafts];
+    double x[kMaxDrafts];  // the drafts' logits, times the scale
     int count;
 };
 
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) x += shfl_xor64(x, d);
-    return x;
-}
+__device__ __forceinline__ double wave_sum(double x) { return lane64(scan64(x), 63); }
 // A row's parts, one after another by a thread, or by the lanes of a wave.
 __device__ __forceinline__ Sum row_sum(const VerifyArgs& a, int64_t r) {
     Sum x{-INFINITY, 0.0};
@@ -207,7 +208,7 @@ __device__ __forceinline__ Sum row_sum_by_wave(const VerifyArgs& a, int64_t r) {
     double m = x.m;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-        const double y = shfl_xor64(m, d);
+        const double y = __shfl_xor(m, d);
         m = y > m ? y : m;
     }
     return {m, wave_sum(m == -INFINITY ? x.s : x.s * exp2_64(x.m - m))};
@@ -222,17 +223,23 @@ __device__ __forceinline__ int64_t draft(const VerifyArgs& a, int b, int t) {
 }
 
 template <bool BF16>
-__device__ __forceinline__ double prob(const VerifyArgs& a, const void* row, int64_t v,
-                                       const Sum& x) {
-    const double c = (double)a.scale * 1.4426950408889634074;
-    return exp2_64((double)ld<BF16>(row, v) * c - x.m) / x.s;
-}
-
-template <bool BF16>
 __device__ __forceinline__ void decide(const VerifyArgs& a, int b, Shared& sh) {
     const int T = a.drafts, t = threadIdx.x;
     const int64_t first = (int64_t)b * (T + 1);
     const int64_t first_q = (int64_t)a.batch * (T + 1) + (int64_t)b * T;
+    // the drafts' own logits are on their way while the rows' sums are joined
+    int64_t v = -1;
+    float u = 0.f, xp = 0.f, xq = 0.f;
+    if (t < T) {
+        v = draft(a, b, t);
+        u = a.uniforms[first + t];
+        if (v >= 0 && v < a.V) {
+            xp = ld<BF16>(row_of<BF16>(a, first + t), v);
+            if (a.draft_logits) xq = ld<BF16>(row_of<BF16>(a, first_q + t), v);
+        } else {
+            v = -1;
+        }
+    }
     if (a.splits > 4) {
         for (int n = t >> 6; n <= T + (a.draft_logits ? T : 0); n += kThreads / 64) {
             const Sum x = row_sum_by_wave(a, n <= T ? first + n : first_q + n - T - 1);
@@ -245,17 +252,17 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, int b, Shared& sh) {
     }
     __syncthreads();
     if (t < T) {
-        const int64_t v = draft(a, b, t);
+        const double c = (double)a.scale * 1.4426950408889634074;
         bool yes = false;
-        if (v >= 0 && v < a.V && proper(sh.p[t])) {
-            const double p = prob<BF16>(a, row_of<BF16>(a, first + t), v, sh.p[t]);
+        if (v >= 0 && proper(sh.p[t])) {
+            const double p = power((double)xp * c - sh.p[t].m) / sh.p[t].s;
             double q = 1.0;
             if (a.draft_logits)
-                q = proper(sh.q[t]) ? prob<BF16>(a, row_of<BF16>(a, first_q + t), v, sh.q[t])
-                                    : INFINITY;
-            yes = (double)a.uniforms[first + t] * q < p;
+                q = proper(sh.q[t]) ? power((double)xq * c - sh.q[t].m) / sh.q[t].s : INFINITY;
+            yes = (double)u * q < p;
         }
         sh.yes[t] = yes;
+        sh.x[t] = (double)xp * (double)a.scale;
     }
     __syncthreads();
     if (t == 0) {
@@ -294,6 +301,10 @@ struct Drawn {
             }
         }
     }
+    static __device__ __forceinline__ double unit(const Roots& roots, double x) {
+        const double y = roots.exp2(x < -999.0 ? -999.0 : x);
+        return x < -999.0 ? 0.0 : y;
+    }
     __device__ __forceinline__ Left at(const Roots& roots, float x, float y, int64_t v) const {
         const double mine = unit(roots, fma((double)x, c, -p.m));
         double left = mine;
@@ -301,20 +312,12 @@ struct Drawn {
         if (v == one) left = 0.0;
         return {mine, left > 0.0 ? left : 0.0};
     }
-    static __device__ __forceinline__ double unit(const Roots& roots, double x) {
-        const double y = roots.exp2(x < -999.0 ? -999.0 : x);
-        return x < -999.0 ? 0.0 : y;
-    }
 };
 
 // Sums up to and with each thread's x, over the workgroup.
 __device__ __forceinline__ double scan(double x, double (&sums)[kThreads / 64]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const double y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-    }
+    x = scan64(x);
     __syncthreads();
     if (lane == 63) sums[wave] = x;
     __syncthreads();
@@ -322,24 +325,20 @@ __device__ __forceinline__ double scan(double x, double (&sums)[kThreads / 64]) 
     return x;
 }
 
-// The least x of the workgroup's threads that is not negative, or -1; and the
-// greatest.
-__device__ __forceinline__ int least(int x, int (&of)[kThreads / 64]) {
-    uint32_t u = (uint32_t)x;
+// Of the workgroup's threads whose x is not negative, in order, the first one's
+// x, or the last one's; or -1.
+__device__ __forceinline__ int of_waves(int x, bool last, int (&of)[kThreads / 64]) {
+    const uint64_t in = __ballot(x >= 0);
+    int mine = -1;
+    if (in) mine = __builtin_amdgcn_readlane(x, last ? 63 - __builtin_clzll(in) : __builtin_ctzll(in));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) of[threadIdx.x >> 6] = mine;
+    __syncthreads();
+    int r = -1;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) u = min(u, (uint32_t)__shfl_xor((int)u, d));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) of[threadIdx.x >> 6] = (int)u;
-    __syncthreads();
-    return (int)min(min((uint32_t)of[0], (uint32_t)of[1]), min((uint32_t)of[2], (uint32_t)of[3]));
-}
-__device__ __forceinline__ int greatest(int x, int (&of)[kThreads / 64]) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) x = max(x, __shfl_xor(x, d));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) of[threadIdx.x >> 6] = x;
-    __syncthreads();
-    return max(max(of[0], of[1]), max(of[2], of[3]));
+    for (int w = 0; w < kThreads / 64; ++w)
+        if (of[w] >= 0 && (last || r < 0)) r = of[w];
+    return r;
 }
 
 // A mass that another workgroup wrote in this launch.  It is one word, which no
@@ -388,43 +387,49 @@ __device__ __forceinline__ int64_t draw(const VerifyArgs& a, int b, const Drawn<
         const double x = n < a.pieces ? shared_load(mass + n * 2 + which) : 0.0;
         const double upto = ahead + scan(x, sums);
         ahead += (sums[0] + sums[1]) + (sums[2] + sums[3]);
-        piece = least(x > 0.0 && upto > border ? n : -1, of);
-        last = max(last, greatest(x > 0.0 ? n : -1, of));
+        piece = of_waves(x > 0.0 && upto > border ? n : -1, false, of);
+        last = max(last, of_waves(x > 0.0 ? n : -1, true, of));
         if (n == piece) before = upto - x;
     }
     const bool over = piece < 0;
     if (over) piece = last;
     __syncthreads();
-    const int64_t i0 = (int64_t)piece * kPiece, i1 = i0 + kPiece < a.V ? i0 + kPiece : a.V;
-    // kMine neighbouring values a thread
-    double x[kMine], sum = 0.0;
-    const int mine = tid * kMine;
-#pragma unroll
-    for (int k = 0; k < kMine; k += W) {
-        float u[W], v[W];
-        Row<BF16>::load(from.prow, i0 + mine + k, i1, u);
-        if (from.qrow) Row<BF16>::load(from.qrow, i0 + mine + k, i1, v);
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-            const Left l = from.at(roots, u[e], from.qrow ? v[e] : 0.f, i0 + mine + k + e);
-            x[k + e] = which ? l.p : l.left;
-            sum += x[k + e];
-        }
-    }
-    double upto = (over ? 0.0 : before) + (scan(sum, sums) - sum);
-    int found = -1;
+    const int64_t i0 = (int64_t)piece * a.piece, i1 = i0 + a.piece < a.V ? i0 + a.piece : a.V;
+    ahead = over ? 0.0 : before;
     last = -1;
+    for (int64_t j0 = i0; j0 < i1; j0 += kThreads * kMine) {
+        // kMine neighbouring values a thread
+        double x[kMine], sum = 0.0;
+        const int mine = tid * kMine;
 #pragma unroll
-    for (int e = 0; e < kMine; ++e) {
-        upto += x[e];
-        if (x[e] > 0.0) {
-            last = mine + e;
-            if (found < 0 && !over && upto > border) found = mine + e;
+        for (int k = 0; k < kMine; k += W) {
+            float u[W], v[W];
+            Row<BF16>::load(from.prow, j0 + mine + k, i1, u);
+            if (from.qrow) Row<BF16>::load(from.qrow, j0 + mine + k, i1, v);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const Left l = from.at(roots, u[e], from.qrow ? v[e] : 0.f, j0 + mine + k + e);
+                x[k + e] = which ? l.p : l.left;
+                sum += x[k + e];
+            }
         }
+        double upto = ahead + (scan(sum, sums) - sum);
+        ahead += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        int found = -1, mass_at = -1;
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) {
+            upto += x[e];
+            if (x[e] > 0.0) {
+                mass_at = mine + e;
+                if (found < 0 && !over && upto > border) found = mine + e;
+            }
+        }
+        found = of_waves(found, false, of);
+        if (found >= 0) return j0 + found;
+        mass_at = of_waves(mass_at, true, of);
+        if (mass_at >= 0) last = (int)(j0 - i0) + mass_at;
     }
-    found = least(found, of);
-    last = greatest(last, of);
-    return i0 + (found >= 0 ? found : last);
+    return i0 + last;
 }
 
 template <bool BF16>
@@ -439,9 +444,10 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a) {
     roots.make();
     decide<BF16>(a, b, sh);
     const Drawn<BF16> from(a, b, sh);
-    const int64_t i0 = (int64_t)piece * kPiece, i1 = i0 + kPiece < a.V ? i0 + kPiece : a.V;
+    const int64_t i0 = (int64_t)piece * a.piece, i1 = i0 + a.piece < a.V ? i0 + a.piece : a.V;
     double left = 0.0, own = 0.0;
     if (proper(from.p))
+#pragma unroll 2
         for (int64_t i = i0 + tid * W; i < i1; i += kThreads * W) {
             float x[W], y[W];
             Row<BF16>::load(from.prow, i, i1, x);
@@ -479,9 +485,12 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a) {
         if (tid < sh.count) v = draft(a, b, tid);
         else if (tid == sh.count) v = drawn;
         double lp = 0.0;
-        if (v >= 0)
-            lp = (double)ld<BF16>(row_of<BF16>(a, at), v) * (double)a.scale -
-                 sh.p[tid].m * 0.693147180559945309417 - log(sh.p[tid].s);
+        if (v >= 0) {
+            const double x = tid < sh.count ? sh.x[tid]
+                                            : (double)ld<BF16>(row_of<BF16>(a, at), v) *
+                                                  (double)a.scale;
+            lp = x - sh.p[tid].m * 0.693147180559945309417 - log(sh.p[tid].s);
+        }
         a.tokens[at] = (int32_t)v;
         a.logprob[at] = (float)lp;
     }
@@ -505,7 +514,11 @@ void verify_plan(VerifyArgs& a, bool bf16, bool drafted) {
     if (splits > 64) splits = 64;
     a.per = ((a.V + splits - 1) / splits + round - 1) / round * round;
     a.splits = (int)((a.V + a.per - 1) / a.per);
-    a.pieces = (int)((a.V + kPiece - 1) / kPiece);
+    // Pieces of 2048 values for few sequences, where a workgroup's chain of trips to
+    // memory counts, and up to 8192, where their number does.
+    a.piece = 2048;
+    while (a.piece < 8192 && a.batch * ((a.V + a.piece - 1) / a.piece) > 1024) a.piece *= 2;
+    a.pieces = (int)((a.V + a.piece - 1) / a.piece);
 }
 
 VerifyWs verify_ws(const VerifyArgs& a) {
