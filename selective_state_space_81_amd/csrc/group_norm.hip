@@ -7,7 +7,7 @@
 // Bytes are all that counts: every input is read once, in vectors of 16 bytes,
 // and kept in registers from the sums to the output.  A group is shared by the
 // fewest lanes (a power of two) that hold it in one vector each, up to a wave
-// with 4 vectors, and by a workgroup beyond that; the groups of a wave lie side
+// with 2 vectors, and by a workgroup beyond that; the groups of a wave lie side
 // by side in a row.  A wave keeps its channels and goes down the rows: the
 // weights are read once, and the gradients of weights add up in registers.
 // They are joined over waves in LDS and over workgroups by a second launch, in
@@ -29,6 +29,14 @@ constexpr int kWaves = 4;
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef u4 u4_align2 __attribute__((aligned(2)));
 typedef u4 u4_align4 __attribute__((aligned(4)));
+
+// A barrier for what waves share in LDS, which does not wait for loads and stores
+// of global memory under way.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
 
 template <bool BF16>
 constexpr int vec() { return BF16 ? 8 : 4; }
@@ -82,6 +90,8 @@ struct Vec {
     }
 };
 
+enum { kNone = 0, kAfter = 1, kFirst = 2 };  // the gate
+
 // Where a lane works: its first vector's place in its group, and its group.
 template <bool WIDE>
 struct Lane {
@@ -98,14 +108,14 @@ struct Lane {
             group = (blockIdx.x % a.columns) * (64 / lanes) + l / lanes;
         }
     }
-    // over the lanes of a group
-    __device__ __forceinline__ float sum(float x) const {
+    // over the lanes of a group; `turn` alternates between sums that follow each other
+    __device__ __forceinline__ float sum(float x, int turn) const {
         for (int d = 1; d < (WIDE ? 64 : lanes); d *= 2) x += __shfl_xor(x, d);
         if (WIDE) {
-            __syncthreads();
-            if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = x;
-            __syncthreads();
-            x = (scratch[0] + scratch[1]) + (scratch[2] + scratch[3]);
+            float* part = scratch + turn * kWaves;
+            if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+            lds_barrier();
+            x = (part[0] + part[1]) + (part[2] + part[3]);
         }
         return x;
     }
@@ -127,7 +137,7 @@ __device__ __forceinline__ float normalise(const NormArgs& a, const Lane<WIDE>& 
         for (int m = 0; m < NV; ++m)
 #pragma unroll
             for (int e = 0; e < W; ++e) s += u[m].v[e];
-        const float mean = at.sum(s) * inv;
+        const float mean = at.sum(s, 0) * inv;
 #pragma unroll
         for (int m = 0; m < NV; ++m)
 #pragma unroll
@@ -139,7 +149,7 @@ __device__ __forceinline__ float normalise(const NormArgs& a, const Lane<WIDE>& 
     for (int m = 0; m < NV; ++m)
 #pragma unroll
         for (int e = 0; e < W; ++e) s = fmaf(u[m].v[e], u[m].v[e], s);
-    const float factor = 1.f / sqrtf(fmaf(at.sum(s), inv, a.eps));
+    const float factor = 1.f / sqrtf(fmaf(at.sum(s, 1), inv, a.eps));
 #pragma unroll
     for (int m = 0; m < NV; ++m)
 #pragma unroll
@@ -147,10 +157,10 @@ __device__ __forceinline__ float normalise(const NormArgs& a, const Lane<WIDE>& 
     return factor;
 }
 
-template <bool BF16, int NV, bool WIDE>
+template <bool BF16, int NV, bool WIDE, int GATE, bool BIAS>
 __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
     constexpr int W = vec<BF16>();
-    __shared__ float sums[kWaves];
+    __shared__ float sums[2 * kWaves];
     const Lane<WIDE> at(a, sums);
     if (!WIDE && at.group >= a.groups) return;
     const int64_t base = (int64_t)at.group * a.size;
@@ -162,7 +172,7 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
     for (int m = 0; m < NV; ++m) {
         const int i = (at.first + m * at.lanes) * W;
         w[m].weights(a.weight, base, i, a.size, 1.f);
-        b[m].weights(a.bias, base, i, a.size, 0.f);
+        if (BIAS) b[m].weights(a.bias, base, i, a.size, 0.f);
     }
     const int64_t width = (int64_t)a.groups * a.size;
     for (; row < a.rows; row += stride) {
@@ -171,11 +181,14 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
         for (int m = 0; m < NV; ++m) {
             const int i = (at.first + m * at.lanes) * W;
             u[m].load(a.x, row * a.ldx + base, i, a.size);
-            if (a.z) {
-                z[m].load(a.z, row * a.ldz + base, i, a.size);
+            if (GATE) z[m].load(a.z, row * a.ldz + base, i, a.size);
+        }
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            if (GATE) {
 #pragma unroll
                 for (int e = 0; e < W; ++e) z[m].v[e] *= sigmoid(z[m].v[e]);
-                if (a.gate_first)
+                if (GATE == kFirst)
 #pragma unroll
                     for (int e = 0; e < W; ++e) u[m].v[e] *= z[m].v[e];
             }
@@ -186,18 +199,19 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
             const int i = (at.first + m * at.lanes) * W;
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                u[m].v[e] = fmaf(u[m].v[e], w[m].v[e], b[m].v[e]);
-                if (a.z && !a.gate_first) u[m].v[e] *= z[m].v[e];
+                u[m].v[e] *= w[m].v[e];
+                if (BIAS) u[m].v[e] += b[m].v[e];
+                if (GATE == kAfter) u[m].v[e] *= z[m].v[e];
             }
             u[m].store(a.y, row * width + base, i, a.size);
         }
     }
 }
 
-template <bool BF16, int NV, bool WIDE>
+template <bool BF16, int NV, bool WIDE, int GATE, bool BIAS>
 __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
     constexpr int W = vec<BF16>();
-    __shared__ float sums[kWaves];
+    __shared__ float sums[2 * kWaves];
     __shared__ float joined[WIDE ? 1 : kWaves][WIDE ? 1 : 64 * NV * W];
     const Lane<WIDE> at(a, sums);
     const bool mine = WIDE || at.group < a.groups;
@@ -211,7 +225,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
     for (int m = 0; m < NV; ++m) {
         const int i = (at.first + m * at.lanes) * W;
         w[m].weights(a.weight, base, i, mine ? a.size : 0, 1.f);
-        b[m].weights(a.bias, base, i, mine ? a.size : 0, 0.f);
+        if (BIAS) b[m].weights(a.bias, base, i, mine ? a.size : 0, 0.f);
 #pragma unroll
         for (int e = 0; e < W; ++e) dw[m].v[e] = db[m].v[e] = 0.f;
     }
@@ -222,13 +236,14 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
             const int i = (at.first + m * at.lanes) * W;
             x[m].load(a.x, row * a.ldx + base, i, a.size);
             dy[m].load(a.dy, row * width + base, i, a.size);
+            if (GATE) z[m].load(a.z, row * a.ldz + base, i, a.size);
             hat[m] = x[m];
-            if (a.z) {
-                z[m].load(a.z, row * a.ldz + base, i, a.size);
-                if (a.gate_first)
+        }
+        if (GATE == kFirst) {
 #pragma unroll
-                    for (int e = 0; e < W; ++e) hat[m].v[e] *= z[m].v[e] * sigmoid(z[m].v[e]);
-            }
+            for (int m = 0; m < NV; ++m)
+#pragma unroll
+                for (int e = 0; e < W; ++e) hat[m].v[e] *= z[m].v[e] * sigmoid(z[m].v[e]);
         }
         const float factor = normalise<BF16, NV, WIDE>(a, at, hat);
         float s = 0.f, sh = 0.f;
@@ -237,30 +252,33 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
             for (int e = 0; e < W; ++e) {
                 float d = dy[m].v[e];
-                if (a.z && !a.gate_first) {
+                if (GATE == kAfter) {
                     const float zz = z[m].v[e], sg = sigmoid(zz), gate = zz * sg;
                     // d silu = sigmoid (1 + z (1 - sigmoid))
-                    z[m].v[e] = d * fmaf(hat[m].v[e], w[m].v[e], b[m].v[e]) *
-                                fmaf(gate, 1.f - sg, sg);
+                    float pre = hat[m].v[e] * w[m].v[e];
+                    if (BIAS) pre += b[m].v[e];
+                    z[m].v[e] = d * pre * fmaf(gate, 1.f - sg, sg);
                     d *= gate;
                 }
                 dw[m].v[e] = fmaf(d, hat[m].v[e], dw[m].v[e]);
-                db[m].v[e] += d;
+                if (BIAS) db[m].v[e] += d;
                 d *= w[m].v[e];
                 dy[m].v[e] = d;
                 s += d;
                 sh = fmaf(d, hat[m].v[e], sh);
             }
         }
-        sh = at.sum(sh) * inv;
-        s = a.center ? at.sum(s) * inv : 0.f;
+        // Turns 0, 1 (in normalise), 0, 1: a buffer comes again behind a barrier
+        // that all waves pass when they have read it.
+        sh = at.sum(sh, 0) * inv;
+        s = a.center ? at.sum(s, 1) * inv : 0.f;
 #pragma unroll
         for (int m = 0; m < NV; ++m) {
             const int i = (at.first + m * at.lanes) * W;
 #pragma unroll
             for (int e = 0; e < W; ++e) {
                 float d = (fmaf(-hat[m].v[e], sh, dy[m].v[e]) - s) * factor;
-                if (a.z && a.gate_first) {
+                if (GATE == kFirst) {
                     const float zz = z[m].v[e], sg = sigmoid(zz), gate = zz * sg;
                     z[m].v[e] = d * x[m].v[e] * fmaf(gate, 1.f - sg, sg);
                     d *= gate;
@@ -268,7 +286,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
                 dy[m].v[e] = d;
             }
             dy[m].store(a.dx, row * width + base, i, a.size);
-            if (a.z) z[m].store(a.dz, row * width + base, i, a.size);
+            if (GATE) z[m].store(a.dz, row * width + base, i, a.size);
         }
     }
     if (!a.part) return;
@@ -281,13 +299,13 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
                 const int i = (at.first + m * at.lanes) * W + e;
                 if (i < a.size) {
                     out[base + i] = dw[m].v[e];
-                    out[width + base + i] = db[m].v[e];
+                    if (BIAS) out[width + base + i] = db[m].v[e];
                 }
             }
     } else {
         const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
+        for (int which = 0; which < (BIAS ? 2 : 1); ++which) {
             __syncthreads();
 #pragma unroll
             for (int m = 0; m < NV; ++m)
@@ -307,23 +325,27 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
     }
 }
 
-// dweight and dbias from the strips' sums: 64 channels a workgroup of 16 waves,
-// which share the strips.
+// dweight and dbias from the strips' sums: 16 channels a workgroup, whose 64 rows
+// of lanes share the strips (64 channels and 16 rows left most of the chip idle:
+// 1024 strips of 1536 channels 21 us).
 constexpr int kJoinWaves = 16;
 __global__ __launch_bounds__(64 * kJoinWaves) void norm_join_kernel(NormArgs a) {
-    __shared__ float sums[kJoinWaves][64];
+    __shared__ float sums[kJoinWaves][16];
     const int64_t width = (int64_t)a.groups * a.size;
     const int which = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t i = (int64_t)blockIdx.x * 64 + lane;
+    const int64_t i = (int64_t)blockIdx.x * 16 + (lane & 15);
     float* out = which ? a.dbias : a.dweight;
     if (!out) return;
     float s = 0.f;
     if (i < width)
-        for (int64_t n = wave; n < a.strips; n += kJoinWaves)
+#pragma unroll 4
+        for (int64_t n = threadIdx.x >> 4; n < a.strips; n += kJoinWaves * 4)
             s += a.part[(n * 2 + which) * width + i];
-    sums[wave][lane] = s;
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lane < 16) sums[wave][lane] = s;
     __syncthreads();
-    if (wave == 0 && i < width) {
+    if (threadIdx.x < 16 && i < width) {
         s = 0.f;
 #pragma unroll
         for (int n = 0; n < kJoinWaves; ++n) s += sums[n][lane];
@@ -340,14 +362,16 @@ void norm_plan(NormArgs& a, bool bf16, bool backward) {
     const int units = (a.size + (bf16 ? 7 : 3)) / (bf16 ? 8 : 4);
     a.lanes = 1;
     while (a.lanes < 64 && a.lanes < units) a.lanes *= 2;
-    if (units > 256) a.lanes = kThreads;  // more than 4 vectors of a wave's lanes
+    if (units > 128) a.lanes = kThreads;  // more than 2 vectors of a wave's lanes
     const bool wide = a.lanes == kThreads;
     a.vecs = (units + a.lanes - 1) / a.lanes;
     a.columns = wide ? a.groups : (a.groups + 64 / a.lanes - 1) / (64 / a.lanes);
-    // Forward: as many workgroups as rows give, up to 16 a CU (weights are read
-    // once for several rows then).  Backward: 4 a CU, for every strip costs a
-    // row of partial sums.
-    const int64_t most = ((backward ? 1024 : 4096) + a.columns - 1) / a.columns;
+    // Workgroups that a CU holds side by side: weights are read, and partial sums
+    // written, once for each.  (16384 x 1536 bf16 backward, one group: 768 of them
+    // 110 us of a training pass, 1280 97, 2048 108; 5997 x 511 fp32, 7 groups: 1024
+    // 32, 2048 28.)
+    const int64_t all = backward && wide ? 1280 : 2048;
+    const int64_t most = (all + a.columns - 1) / a.columns;
     const int64_t need = wide ? a.rows : (a.rows + kWaves - 1) / kWaves;
     a.strips = need < most ? need : most;
     if (a.strips < 1) a.strips = 1;
@@ -359,23 +383,34 @@ size_t norm_bwd_ws(const NormArgs& a) {
 
 int64_t norm_workgroups(const NormArgs& a) { return a.strips * a.columns; }
 
-#define NORM_(kernel, B)                                                                \
+#define NORM_(kernel, B, G, S)                                                          \
     do {                                                                                \
         if (a.lanes == kThreads) {                                                      \
-            if (a.vecs <= 2) kernel<B, 2, true><<<n, kThreads, 0, s>>>(a);              \
-            else if (B || a.vecs <= 4) kernel<B, 4, true><<<n, kThreads, 0, s>>>(a);    \
-            else kernel<false, 8, true><<<n, kThreads, 0, s>>>(a);                      \
-        } else if (a.vecs == 1) kernel<B, 1, false><<<n, kThreads, 0, s>>>(a);          \
-        else if (a.vecs == 2) kernel<B, 2, false><<<n, kThreads, 0, s>>>(a);            \
-        else if (a.vecs == 3) kernel<B, 3, false><<<n, kThreads, 0, s>>>(a);            \
-        else kernel<B, 4, false><<<n, kThreads, 0, s>>>(a);                             \
+            if (a.vecs == 1) kernel<B, 1, true, G, S><<<n, kThreads, 0, s>>>(a);        \
+            else if (a.vecs == 2) kernel<B, 2, true, G, S><<<n, kThreads, 0, s>>>(a);   \
+            else if (B || a.vecs <= 4)                                                  \
+                kernel<B, 4, true, G, S><<<n, kThreads, 0, s>>>(a);                     \
+            else kernel<false, 8, true, G, S><<<n, kThreads, 0, s>>>(a);                \
+        } else if (a.vecs == 1) kernel<B, 1, false, G, S><<<n, kThreads, 0, s>>>(a);    \
+        else kernel<B, 2, false, G, S><<<n, kThreads, 0, s>>>(a);                       \
+    } while (0)
+#define NORM_GATE_(kernel, B, S)                              \
+    do {                                                      \
+        if (!a.z) NORM_(kernel, B, kNone, S);                 \
+        else if (a.gate_first) NORM_(kernel, B, kFirst, S);   \
+        else NORM_(kernel, B, kAfter, S);                     \
+    } while (0)
+#define NORM_BIAS_(kernel, B)                          \
+    do {                                               \
+        if (a.bias || a.dbias) NORM_GATE_(kernel, B, true); \
+        else NORM_GATE_(kernel, B, false);             \
     } while (0)
 
 hipError_t launch_norm_fwd(const NormArgs& a, bool bf16, hipStream_t s) {
     ProfScope ps(s, kPhaseMain);
     const unsigned n = (unsigned)norm_workgroups(a);
-    if (bf16) NORM_(norm_fwd_kernel, true);
-    else NORM_(norm_fwd_kernel, false);
+    if (bf16) NORM_BIAS_(norm_fwd_kernel, true);
+    else NORM_BIAS_(norm_fwd_kernel, false);
     return hipGetLastError();
 }
 
@@ -384,17 +419,19 @@ hipError_t launch_norm_bwd(NormArgs a, bool bf16, void* workspace, hipStream_t s
     a.part = a.dweight || a.dbias ? (float*)workspace : nullptr;
     {
         ProfScope ps(s, kPhaseMain);
-        if (bf16) NORM_(norm_bwd_kernel, true);
-        else NORM_(norm_bwd_kernel, false);
+        if (bf16) NORM_BIAS_(norm_bwd_kernel, true);
+        else NORM_BIAS_(norm_bwd_kernel, false);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
     ProfScope ps(s, kPhaseReduce);
     const int64_t width = (int64_t)a.groups * a.size;
-    norm_join_kernel<<<dim3((unsigned)((width + 63) / 64), a.dbias ? 2 : 1), 64 * kJoinWaves, 0,
+    norm_join_kernel<<<dim3((unsigned)((width + 15) / 16), a.dbias ? 2 : 1), 64 * kJoinWaves, 0,
                        s>>>(a);
     return hipGetLastError();
 }
+#undef NORM_BIAS_
+#undef NORM_GATE_
 #undef NORM_
 
 }  // namespace msscan

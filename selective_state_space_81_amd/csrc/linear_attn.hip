@@ -472,17 +472,15 @@ __global__ __launch_bounds__(kThreads) void attn_carry_kernel(AttnArgs a, const 
 // A few tokens from a state that is read once (and written once): its bytes are
 // all that counts.  A workgroup takes 64 columns of a head's state, a thread
 // four columns of every 16th row, in registers; tokens' q, k, v and decays wait
-// in LDS.  The sum over rows is joined by two shuffles and, over the waves,
-// through LDS.
-constexpr int kStepBlock = 16;  // tokens in LDS
-template <bool BF16>
+// in LDS, BLOCK of them at a time.  The sums over rows are joined by two
+// shuffles and, over the waves, through LDS, all tokens of a block at once.
+template <bool BF16, int BLOCK>
 __global__ __launch_bounds__(kThreads) void attn_step_kernel(AttnArgs a) {
-    typedef typename Io<BF16>::E E;
     constexpr int kRows = kMaxHeadDim / 16;
-    __shared__ float qs[kStepBlock][kMaxHeadDim], ks[kStepBlock][kMaxHeadDim];
-    __shared__ __align__(16) float vs[kStepBlock][64];
-    __shared__ __align__(16) float sums[2][kWaves][64];
-    __shared__ float decay[kStepBlock];
+    __shared__ float qs[BLOCK][kMaxHeadDim], ks[BLOCK][kMaxHeadDim];
+    __shared__ __align__(16) float vs[BLOCK][64];
+    __shared__ __align__(16) float sums[BLOCK][kWaves][64];
+    __shared__ float decay[BLOCK];
 
     const Place at(a, 1);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -515,9 +513,9 @@ __global__ __launch_bounds__(kThreads) void attn_step_kernel(AttnArgs a) {
         }
     }
     const int64_t row0 = (int64_t)at.b * T;
-    for (int t0 = 0; t0 < count; t0 += kStepBlock) {
-        const int n = count - t0 < kStepBlock ? count - t0 : kStepBlock;
-        lds_barrier();
+    for (int t0 = 0; t0 < count; t0 += BLOCK) {
+        const int n = count - t0 < BLOCK ? count - t0 : BLOCK;
+        if (t0) lds_barrier();
         for (int i = threadIdx.x; i < n * kMaxHeadDim; i += kThreads) {
             const int t = i / kMaxHeadDim, d = i % kMaxHeadDim;
             const int64_t row = row0 + t0 + t;
@@ -561,15 +559,15 @@ __global__ __launch_bounds__(kThreads) void attn_step_kernel(AttnArgs a) {
                 o[e] += __shfl_xor(o[e], 16);
                 o[e] += __shfl_xor(o[e], 32);
             }
-            // two buffers: the next token's sums do not wait for this one's readers
-            if (lane < 16) *reinterpret_cast<f4*>(&sums[t & 1][wave][c]) = o;
-            lds_barrier();
-            if ((int)threadIdx.x < nv) {
-                const int d = threadIdx.x;
-                const float sum = (sums[t & 1][0][d] + sums[t & 1][1][d]) +
-                                  (sums[t & 1][2][d] + sums[t & 1][3][d]);
+            if (lane < 16) *reinterpret_cast<f4*>(&sums[t][wave][c]) = o;
+        }
+        if (!a.q) continue;
+        lds_barrier();
+        for (int i = threadIdx.x; i < n * 64; i += kThreads) {
+            const int t = i / 64, d = i % 64;
+            const float sum = (sums[t][0][d] + sums[t][1][d]) + (sums[t][2][d] + sums[t][3][d]);
+            if (d < nv)
                 st<BF16>(a.o, ((row0 + t0 + t) * a.H + at.h) * a.dv + col0 + d, sum * a.scale);
-            }
         }
     }
     if (!a.update) return;
@@ -702,8 +700,13 @@ int64_t attn_step_workgroups(const AttnArgs& a) { return (int64_t)a.batch * a.H 
 hipError_t launch_attn_step(const AttnArgs& a, bool bf16, hipStream_t s) {
     ProfScope ps(s, kPhaseStep);
     const unsigned n = (unsigned)attn_step_workgroups(a);
-    if (bf16) attn_step_kernel<true><<<n, kThreads, 0, s>>>(a);
-    else attn_step_kernel<false><<<n, kThreads, 0, s>>>(a);
+    if (a.L == 1) {
+        if (bf16) attn_step_kernel<true, 1><<<n, kThreads, 0, s>>>(a);
+        else attn_step_kernel<false, 1><<<n, kThreads, 0, s>>>(a);
+    } else {
+        if (bf16) attn_step_kernel<true, 8><<<n, kThreads, 0, s>>>(a);
+        else attn_step_kernel<false, 8><<<n, kThreads, 0, s>>>(a);
+    }
     return hipGetLastError();
 }
 
