@@ -474,7 +474,7 @@ __global__ __launch_bounds__(kThreads) void attn_carry_kernel(AttnArgs a, const 
 // four columns of every 16th row, in registers; tokens' q, k, v and decays wait
 // in LDS, BLOCK of them at a time.  The sums over rows are joined by two
 // shuffles and, over the waves, through LDS, all tokens of a block at once.
-template <bool BF16, int BLOCK>
+template <bool BF16, int BLOCK, bool WHOLE, bool PAST>
 __global__ __launch_bounds__(kThreads) void attn_step_kernel(AttnArgs a) {
     constexpr int kRows = kMaxHeadDim / 16;
     __shared__ float qs[BLOCK][kMaxHeadDim], ks[BLOCK][kMaxHeadDim];
@@ -495,42 +495,55 @@ __global__ __launch_bounds__(kThreads) void attn_step_kernel(AttnArgs a) {
     }
     if (count == 0) return;
     float* h = a.h + ((int64_t)at.b * a.H + at.h) * a.dk * a.dv + col0;
-    const bool whole = a.dv % 4 == 0;
+    // Loads ask for places that are there, without a branch, which would wait for
+    // each; rows from dk on are not looked at, nor columns behind the last.
     f4 S[kRows];
 #pragma unroll
     for (int m = 0; m < kRows; ++m) {
-        const int d = m * 16 + r0;
-        S[m] = f4{0, 0, 0, 0};
-        if (d < a.dk) {
-            const float* p = h + (int64_t)d * a.dv + c;
-            if (whole && c < nv) {
-                S[m] = *reinterpret_cast<const f4*>(p);
-            } else {
+        const float* p = h + (int64_t)min(m * 16 + r0, a.dk - 1) * a.dv;
+        if constexpr (WHOLE) {
+            const f4* from = reinterpret_cast<const f4*>(p + min(c, nv - 4));
+            S[m] = PAST ? __builtin_nontemporal_load(from) : *from;
+        } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < nv) S[m][e] = p[e];
-            }
+            for (int e = 0; e < 4; ++e) S[m][e] = p[min(c + e, nv - 1)];
         }
     }
+    const void* qp = a.q ? a.q : a.k;
+    const int64_t ldq = a.q ? a.ldq : a.ldk;
     const int64_t row0 = (int64_t)at.b * T;
     for (int t0 = 0; t0 < count; t0 += BLOCK) {
         const int n = count - t0 < BLOCK ? count - t0 : BLOCK;
         if (t0) lds_barrier();
-        for (int i = threadIdx.x; i < n * kMaxHeadDim; i += kThreads) {
-            const int t = i / kMaxHeadDim, d = i % kMaxHeadDim;
+        // all loads ahead of what waits for them
+        constexpr int kQk = (BLOCK * kMaxHeadDim + kThreads - 1) / kThreads;
+        constexpr int kV = (BLOCK * 64 + kThreads - 1) / kThreads;
+        float kv[kQk], qv[kQk], vv[kV];
+#pragma unroll
+        for (int m = 0; m < kQk; ++m) {
+            const int i = m * kThreads + threadIdx.x, t = min(i / kMaxHeadDim, n - 1);
+            const int d = min(i % kMaxHeadDim, a.dk - 1);
             const int64_t row = row0 + t0 + t;
-            if (d < a.dk) {
-                ks[t][d] = ld<BF16>(a.k, row * a.ldk + (int64_t)kh * a.dk + d);
-                if (a.q) qs[t][d] = ld<BF16>(a.q, row * a.ldq + (int64_t)kh * a.dk + d);
-            }
+            kv[m] = ld<BF16>(a.k, row * a.ldk + (int64_t)kh * a.dk + d);
+            qv[m] = ld<BF16>(qp, row * ldq + (int64_t)kh * a.dk + d);
         }
-        for (int i = threadIdx.x; i < n * 64; i += kThreads) {
-            const int t = i / 64, d = i % 64;
-            vs[t][d] = d < nv ? ld<BF16>(a.v, (row0 + t0 + t) * a.ldv + (int64_t)at.h * a.dv + col0 + d)
-                              : 0.f;
+#pragma unroll
+        for (int m = 0; m < kV; ++m) {
+            const int i = m * kThreads + threadIdx.x, t = min(i / 64, n - 1), d = min(i % 64, nv - 1);
+            vv[m] = ld<BF16>(a.v, (row0 + t0 + t) * a.ldv + (int64_t)at.h * a.dv + col0 + d);
+        }
+        const float g = log_decay(a, row0 + t0 + min((int)threadIdx.x, n - 1), at.h);
+#pragma unroll
+        for (int m = 0; m < kQk; ++m) {
+            const int i = m * kThreads + threadIdx.x;
+            if (i < BLOCK * kMaxHeadDim) (&ks[0][0])[i] = kv[m], (&qs[0][0])[i] = qv[m];
+        }
+#pragma unroll
+        for (int m = 0; m < kV; ++m) {
+            const int i = m * kThreads + threadIdx.x;
+            if (i < BLOCK * 64) (&vs[0][0])[i] = vv[m];
         }
         if ((int)threadIdx.x < n) {
-            const float g = log_decay(a, row0 + t0 + threadIdx.x, at.h);
             const float x = g * kLog2e;  // and what its rounding left
             const float rest = fmaf(g, kLog2e, -x) + g * 1.925963033500011079e-8f;
             decay[threadIdx.x] = g < kNoDecay ? -1.f : hw_exp2(x) * fmaf(rest, kLn2, 1.f);
@@ -576,8 +589,11 @@ __global__ __launch_bounds__(kThreads) void attn_step_kernel(AttnArgs a) {
         const int d = m * 16 + r0;
         if (d < a.dk) {
             float* p = h + (int64_t)d * a.dv + c;
-            if (whole && c < nv) {
-                *reinterpret_cast<f4*>(p) = S[m];
+            if constexpr (WHOLE) {
+                if (c < nv) {
+                    if (PAST) __builtin_nontemporal_store(S[m], reinterpret_cast<f4*>(p));
+                    else *reinterpret_cast<f4*>(p) = S[m];
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -699,14 +715,27 @@ int64_t attn_step_workgroups(const AttnArgs& a) { return (int64_t)a.batch * a.H 
 
 hipError_t launch_attn_step(const AttnArgs& a, bool bf16, hipStream_t s) {
     ProfScope ps(s, kPhaseStep);
+    // A large state goes past the caches: until the next step on it, the rest of a
+    // model will have passed through them (256 sequences of 24 heads of 128 x 64,
+    // 201 MB, several such in turn: 91 us against 101; one by itself 80 against 74).
+    const bool past = (double)a.batch * a.H * a.dk * a.dv * 4.0 > 64e6, whole = a.dv % 4 == 0;
     const unsigned n = (unsigned)attn_step_workgroups(a);
-    if (a.L == 1) {
-        if (bf16) attn_step_kernel<true, 1><<<n, kThreads, 0, s>>>(a);
-        else attn_step_kernel<false, 1><<<n, kThreads, 0, s>>>(a);
-    } else {
-        if (bf16) attn_step_kernel<true, 8><<<n, kThreads, 0, s>>>(a);
-        else attn_step_kernel<false, 8><<<n, kThreads, 0, s>>>(a);
-    }
+#define STEP_(B)                                                                       \
+    do {                                                                               \
+        if (a.L > 1) {                                                                 \
+            if (whole) attn_step_kernel<B, 8, true, false><<<n, kThreads, 0, s>>>(a);  \
+            else attn_step_kernel<B, 8, false, false><<<n, kThreads, 0, s>>>(a);       \
+        } else if (!whole) {                                                           \
+            attn_step_kernel<B, 1, false, false><<<n, kThreads, 0, s>>>(a);            \
+        } else if (past) {                                                             \
+            attn_step_kernel<B, 1, true, true><<<n, kThreads, 0, s>>>(a);              \
+        } else {                                                                       \
+            attn_step_kernel<B, 1, true, false><<<n, kThreads, 0, s>>>(a);             \
+        }                                                                              \
+    } while (0)
+    if (bf16) STEP_(true);
+    else STEP_(false);
+#undef STEP_
     return hipGetLastError();
 }
 
