@@ -41,32 +41,75 @@ __device__ __forceinline__ void lds_barrier() {
 template <bool BF16>
 constexpr int vec() { return BF16 ? 8 : 4; }
 
-// A vector of a group's values from place i on; zeros behind the group's end n.
-template <bool BF16>
+// A vector of a group's values from place i on of n.  ask() has no branch, which
+// would wait for its loads: it takes a whole vector that is there, and take()
+// moves a group's last values down to where they belong (WHOLE: n is a multiple of
+// the vector, and none has to) and clears what lies behind the end.
+template <bool BF16, bool WHOLE>
 struct Vec {
     static constexpr int W = vec<BF16>();
     typedef typename std::conditional<BF16, uint16_t, float>::type E;
     typedef typename std::conditional<BF16, u4_align2, u4_align4>::type U;
-    float v[W];
+    union {
+        float v[W];
+        uint32_t raw[4];
+    };
 
-    __device__ __forceinline__ void load(const void* row, int64_t at, int i, int n) {
-        const E* p = static_cast<const E*>(row) + at + i;
-        if (i + W <= n) {
-            const u4 x = *reinterpret_cast<const U*>(p);
+    __device__ __forceinline__ void ask(const void* row, int64_t at, int i, int n) {
+        const E* p = static_cast<const E*>(row) + at;
+        if (WHOLE || n >= W) {
+            const u4 x = *reinterpret_cast<const U*>(p + min(i, n - W));
 #pragma unroll
-            for (int e = 0; e < W; ++e)
-                if constexpr (BF16)
-                    v[e] = __uint_as_float(e & 1 ? x[e / 2] & 0xffff0000u : x[e / 2] << 16);
-                else
-                    v[e] = __uint_as_float(x[e]);
-        } else {
+            for (int e = 0; e < 4; ++e) raw[e] = x[e];
+        } else {  // groups smaller than a vector
 #pragma unroll
-            for (int e = 0; e < W; ++e) v[e] = i + e < n ? ld<BF16>(p, e) : 0.f;
+            for (int e = 0; e < 4; ++e) raw[e] = 0;
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const uint32_t x = e < n ? bits(p[min(e, n - 1)]) : 0;
+                if constexpr (BF16) raw[e / 2] |= x << (e % 2 * 16);
+                else raw[e] = x;
+            }
         }
+    }
+    static __device__ __forceinline__ uint32_t bits(uint16_t x) { return x; }
+    static __device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
+    __device__ __forceinline__ void take(int i, int n) {
+        uint32_t x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = raw[e];
+        if (!WHOLE && n >= W) {
+            const int s = min(max(i + W - n, 0), W);  // values to move down by
+            if constexpr (BF16) {
+                const bool one = s & 1, two = s & 2, four = s & 4;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = one ? x[e] >> 16 | (e < 3 ? x[e + 1] << 16 : 0) : x[e];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = two ? (e < 3 ? x[e + 1] : 0) : x[e];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = four ? (e < 2 ? x[e + 2] : 0) : x[e];
+            } else {
+                const bool one = s & 1, two = s & 2;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = one ? (e < 3 ? x[e + 1] : 0) : x[e];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = two ? (e < 2 ? x[e + 2] : 0) : x[e];
+            }
+        }
+        const bool in = i < n;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = in ? x[e] : 0;
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if constexpr (BF16)
+                v[e] = __uint_as_float(e & 1 ? x[e / 2] & 0xffff0000u : x[e / 2] << 16);
+            else
+                v[e] = __uint_as_float(x[e]);
     }
     __device__ __forceinline__ void store(void* row, int64_t at, int i, int n) const {
         E* p = static_cast<E*>(row) + at + i;
-        if (i + W <= n) {
+        if (WHOLE ? i < n : i + W <= n) {
             u4 x;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -76,7 +119,7 @@ struct Vec {
                 else
                     x[e] = __float_as_uint(v[e]);
             *reinterpret_cast<U*>(p) = x;
-        } else {
+        } else if (!WHOLE) {
 #pragma unroll
             for (int e = 0; e < W; ++e)
                 if (i + e < n) st<BF16>(p, e, v[e]);
@@ -86,7 +129,9 @@ struct Vec {
     __device__ __forceinline__ void weights(const float* row, int64_t at, int i, int n,
                                             float other) {
 #pragma unroll
-        for (int e = 0; e < W; ++e) v[e] = i + e >= n ? 0.f : row ? row[at + i + e] : other;
+        for (int e = 0; e < W; ++e) v[e] = row ? row[at + min(i + e, n - 1)] : other;
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] = i + e < n ? v[e] : 0.f;
     }
 };
 
@@ -126,9 +171,9 @@ __device__ __forceinline__ float sigmoid(float z) {
 }
 
 // The normalised values of a group in place of u, and the factor they took.
-template <bool BF16, int NV, bool WIDE>
+template <bool BF16, int NV, bool WIDE, bool WHOLE>
 __device__ __forceinline__ float normalise(const NormArgs& a, const Lane<WIDE>& at,
-                                           Vec<BF16> (&u)[NV]) {
+                                           Vec<BF16, WHOLE> (&u)[NV]) {
     constexpr int W = vec<BF16>();
     const float inv = 1.f / (float)a.size;
     if (a.center) {
@@ -157,7 +202,7 @@ __device__ __forceinline__ float normalise(const NormArgs& a, const Lane<WIDE>& 
     return factor;
 }
 
-template <bool BF16, int NV, bool WIDE, int GATE, bool BIAS>
+template <bool BF16, int NV, bool WIDE, bool WHOLE, int GATE, bool BIAS>
 __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
     constexpr int W = vec<BF16>();
     __shared__ float sums[2 * kWaves];
@@ -167,7 +212,7 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
     const int64_t stride = WIDE ? a.strips : a.strips * kWaves;
     int64_t row = blockIdx.x / a.columns;
     if (!WIDE) row = row * kWaves + (threadIdx.x >> 6);
-    Vec<BF16> w[NV], b[NV];
+    Vec<BF16, WHOLE> w[NV], b[NV];
 #pragma unroll
     for (int m = 0; m < NV; ++m) {
         const int i = (at.first + m * at.lanes) * W;
@@ -176,12 +221,18 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
     }
     const int64_t width = (int64_t)a.groups * a.size;
     for (; row < a.rows; row += stride) {
-        Vec<BF16> u[NV], z[NV];
+        Vec<BF16, WHOLE> u[NV], z[NV];
 #pragma unroll
         for (int m = 0; m < NV; ++m) {
             const int i = (at.first + m * at.lanes) * W;
-            u[m].load(a.x, row * a.ldx + base, i, a.size);
-            if (GATE) z[m].load(a.z, row * a.ldz + base, i, a.size);
+            u[m].ask(a.x, row * a.ldx + base, i, a.size);
+            if (GATE) z[m].ask(a.z, row * a.ldz + base, i, a.size);
+        }
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int i = (at.first + m * at.lanes) * W;
+            u[m].take(i, a.size);
+            if (GATE) z[m].take(i, a.size);
         }
 #pragma unroll
         for (int m = 0; m < NV; ++m) {
@@ -193,7 +244,7 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
                     for (int e = 0; e < W; ++e) u[m].v[e] *= z[m].v[e];
             }
         }
-        normalise<BF16, NV, WIDE>(a, at, u);
+        normalise<BF16, NV, WIDE, WHOLE>(a, at, u);
 #pragma unroll
         for (int m = 0; m < NV; ++m) {
             const int i = (at.first + m * at.lanes) * W;
@@ -208,7 +259,7 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
     }
 }
 
-template <bool BF16, int NV, bool WIDE, int GATE, bool BIAS>
+template <bool BF16, int NV, bool WIDE, bool WHOLE, int GATE, bool BIAS>
 __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
     constexpr int W = vec<BF16>();
     __shared__ float sums[2 * kWaves];
@@ -220,23 +271,30 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
     const int64_t stride = WIDE ? a.strips : a.strips * kWaves;
     int64_t row = WIDE ? strip : strip * kWaves + (threadIdx.x >> 6);
     const float inv = 1.f / (float)a.size;
-    Vec<BF16> w[NV], b[NV], dw[NV], db[NV];
+    Vec<BF16, WHOLE> w[NV], b[NV], dw[NV], db[NV];
 #pragma unroll
     for (int m = 0; m < NV; ++m) {
         const int i = (at.first + m * at.lanes) * W;
-        w[m].weights(a.weight, base, i, mine ? a.size : 0, 1.f);
-        if (BIAS) b[m].weights(a.bias, base, i, mine ? a.size : 0, 0.f);
+        if (mine) w[m].weights(a.weight, base, i, a.size, 1.f);
+        if (BIAS && mine) b[m].weights(a.bias, base, i, a.size, 0.f);
 #pragma unroll
         for (int e = 0; e < W; ++e) dw[m].v[e] = db[m].v[e] = 0.f;
     }
     for (; mine && row < a.rows; row += stride) {
-        Vec<BF16> hat[NV], dy[NV], z[NV], x[NV];
+        Vec<BF16, WHOLE> hat[NV], dy[NV], z[NV], x[NV];
 #pragma unroll
         for (int m = 0; m < NV; ++m) {
             const int i = (at.first + m * at.lanes) * W;
-            x[m].load(a.x, row * a.ldx + base, i, a.size);
-            dy[m].load(a.dy, row * width + base, i, a.size);
-            if (GATE) z[m].load(a.z, row * a.ldz + base, i, a.size);
+            x[m].ask(a.x, row * a.ldx + base, i, a.size);
+            if (GATE) z[m].ask(a.z, row * a.ldz + base, i, a.size);
+            dy[m].ask(a.dy, row * width + base, i, a.size);
+        }
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int i = (at.first + m * at.lanes) * W;
+            x[m].take(i, a.size);
+            if (GATE) z[m].take(i, a.size);
+            dy[m].take(i, a.size);
             hat[m] = x[m];
         }
         if (GATE == kFirst) {
@@ -245,7 +303,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
                 for (int e = 0; e < W; ++e) hat[m].v[e] *= z[m].v[e] * sigmoid(z[m].v[e]);
         }
-        const float factor = normalise<BF16, NV, WIDE>(a, at, hat);
+        const float factor = normalise<BF16, NV, WIDE, WHOLE>(a, at, hat);
         float s = 0.f, sh = 0.f;
 #pragma unroll
         for (int m = 0; m < NV; ++m) {
@@ -383,27 +441,33 @@ size_t norm_bwd_ws(const NormArgs& a) {
 
 int64_t norm_workgroups(const NormArgs& a) { return a.strips * a.columns; }
 
-#define NORM_(kernel, B, G, S)                                                          \
-    do {                                                                                \
-        if (a.lanes == kThreads) {                                                      \
-            if (a.vecs == 1) kernel<B, 1, true, G, S><<<n, kThreads, 0, s>>>(a);        \
-            else if (a.vecs == 2) kernel<B, 2, true, G, S><<<n, kThreads, 0, s>>>(a);   \
-            else if (B || a.vecs <= 4)                                                  \
-                kernel<B, 4, true, G, S><<<n, kThreads, 0, s>>>(a);                     \
-            else kernel<false, 8, true, G, S><<<n, kThreads, 0, s>>>(a);                \
-        } else if (a.vecs == 1) kernel<B, 1, false, G, S><<<n, kThreads, 0, s>>>(a);    \
-        else kernel<B, 2, false, G, S><<<n, kThreads, 0, s>>>(a);                       \
+#define NORM_(kernel, B, L, G, S)                                                         \
+    do {                                                                                  \
+        if (a.lanes == kThreads) {                                                        \
+            if (a.vecs == 1) kernel<B, 1, true, L, G, S><<<n, kThreads, 0, s>>>(a);       \
+            else if (a.vecs == 2) kernel<B, 2, true, L, G, S><<<n, kThreads, 0, s>>>(a);  \
+            else if (B || a.vecs <= 4)                                                    \
+                kernel<B, 4, true, L, G, S><<<n, kThreads, 0, s>>>(a);                    \
+            else kernel<false, 8, true, L, G, S><<<n, kThreads, 0, s>>>(a);               \
+        } else if (a.vecs == 1) kernel<B, 1, false, L, G, S><<<n, kThreads, 0, s>>>(a);   \
+        else kernel<B, 2, false, L, G, S><<<n, kThreads, 0, s>>>(a);                      \
     } while (0)
-#define NORM_GATE_(kernel, B, S)                              \
-    do {                                                      \
-        if (!a.z) NORM_(kernel, B, kNone, S);                 \
-        else if (a.gate_first) NORM_(kernel, B, kFirst, S);   \
-        else NORM_(kernel, B, kAfter, S);                     \
+#define NORM_GATE_(kernel, B, L, S)                              \
+    do {                                                         \
+        if (!a.z) NORM_(kernel, B, L, kNone, S);                 \
+        else if (a.gate_first) NORM_(kernel, B, L, kFirst, S);   \
+        else NORM_(kernel, B, L, kAfter, S);                     \
     } while (0)
-#define NORM_BIAS_(kernel, B)                          \
-    do {                                               \
-        if (a.bias || a.dbias) NORM_GATE_(kernel, B, true); \
-        else NORM_GATE_(kernel, B, false);             \
+#define NORM_BIAS_(kernel, B)                                          \
+    do {                                                               \
+        const bool whole_ = a.size % vec<B>() == 0;                    \
+        if (a.bias || a.dbias) {                                       \
+            if (whole_) NORM_GATE_(kernel, B, true, true);             \
+            else NORM_GATE_(kernel, B, false, true);                   \
+        } else {                                                       \
+            if (whole_) NORM_GATE_(kernel, B, true, false);            \
+            else NORM_GATE_(kernel, B, false, false);                  \
+        }                                                              \
     } while (0)
 
 hipError_t launch_norm_fwd(const NormArgs& a, bool bf16, hipStream_t s) {
