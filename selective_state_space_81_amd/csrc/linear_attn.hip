@@ -639,7 +639,7 @@ void attn_plan(AttnArgs& a, bool bf16) {
     // the end; segments of at least four blocks, or the joining costs more than
     // it brings (131072 tokens of 12 heads of 128: 504 workgroups 751 us, 528 1150).
     const int64_t wgs = (int64_t)a.batch * a.H * a.tiles;
-    int64_t nseg = 512 / wgs;
+    int64_t nseg = wgs >= 192 ? 1 : 512 / wgs;
     if (nseg > a.blocks / 4) nseg = a.blocks / 4;
     if (nseg < 1) nseg = 1;
     a.per = (a.blocks + nseg - 1) / nseg;

@@ -26,14 +26,25 @@ namespace msscan {
 namespace attn {
 namespace {
 
-__device__ __forceinline__ float sum_groups(float x) {  // over lanes of the same l & 15
-    x += __shfl_xor(x, 16);
-    return x + __shfl_xor(x, 32);
+// Sums over the four lanes of the same l & 15, and over 16 neighbouring lanes, in
+// every one of them, without trips through LDS.
+__device__ __forceinline__ float sum_groups(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t v = __float_as_uint(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
-__device__ __forceinline__ float sum_row(float x) {  // over 16 lanes
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2) x += __shfl_xor(x, d);
-    return x;
+template <int CTRL>
+__device__ __forceinline__ float turned(float x) {
+    return __uint_as_float(
+        __builtin_amdgcn_update_dpp(0u, __float_as_uint(x), CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float sum_row(float x) {
+    x += turned<0x128>(x);  // row_ror 8, 4, 2, 1
+    x += turned<0x124>(x);
+    x += turned<0x122>(x);
+    return x + turned<0x121>(x);
 }
 
 template <bool BF16, int DK, int DV, bool WHOLE>
@@ -74,7 +85,8 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
     id /= a.Hk;
     const int64_t c = id % (uint32_t)a.blocks;
     const int b = id / (uint32_t)a.blocks;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, s16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, g = lane >> 4, s16 = lane & 15;
     const int group = a.H / a.Hk;
     const int64_t row0 = (int64_t)b * a.L + c * N;
     const int n = a.L - c * N < N ? (int)(a.L - c * N) : N, rows = n;
@@ -89,35 +101,52 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
 #pragma unroll
         for (int it = 0; it < kIts; ++it) dq[m][it] = dk[m][it] = f4{0, 0, 0, 0};
 
-    bool qkbad = false;
+    // Everything is asked for before the first wait; of a group's next head, v and
+    // dO while the present one is worked on.
+    V vr, dr;
+    const int ldo = a.H * a.dv;
+    auto fetch = [&](int h) {
+        vr.load((const E*)a.v + row0 * a.ldv + (int64_t)h * a.dv, (int)a.ldv, rows, a.dv);
+        dr.load((const E*)a.dO + row0 * ldo + (int64_t)h * a.dv, ldo, rows, a.dv);
+    };
+    bool qkbad;
     {
-        QK t;
-        t.load((const E*)a.q + row0 * a.ldq + (int64_t)kh * a.dk, (int)a.ldq, rows, a.dk);
-        qkbad = t.store(sh.q, rows, a.dk);
-        t.load((const E*)a.k + row0 * a.ldk + (int64_t)kh * a.dk, (int)a.ldk, rows, a.dk);
-        qkbad |= t.store(sh.k, rows, a.dk);
+        QK qr, kr;
+        qr.load((const E*)a.q + row0 * a.ldq + (int64_t)kh * a.dk, (int)a.ldq, rows, a.dk);
+        kr.load((const E*)a.k + row0 * a.ldk + (int64_t)kh * a.dk, (int)a.ldk, rows, a.dk);
+        fetch(kh * group);
+        qkbad = qr.store(sh.q, rows, a.dk);
+        qkbad |= kr.store(sh.k, rows, a.dk);
     }
     for (int n_head = 0; n_head < group; ++n_head) {
         const int h = kh * group + n_head;
+        // tiles of the states as operands, on their way during the scores
+        const int64_t at = (((int64_t)b * a.blocks + c) * a.H + h) * a.DKs * (int64_t)a.DVs;
+        f8 sf[DV / 32], rf[DV / 32];
+        auto states = [&](int m) {
+            const int row = min((m * kWaves + wave) * 16 + s16, a.DKs - 1) * a.DVs;
+#pragma unroll
+            for (int e = 0; e < DV / 32; ++e) {
+                const int p = row + min(e * 32 + g * 8, a.DVs - 8);
+                sf[e] = *reinterpret_cast<const f8_align16*>(a.states + at + p);
+                rf[e] = *reinterpret_cast<const f8_align16*>(a.grads + at + p);
+            }
+        };
+        states(0);
+        Token tok;
+        if (wave == 0) tok.load(a, row0, rows, h, N);
         bool bad = qkbad;
-        {
-            V t;
-            const int ldo = a.H * a.dv;
-            t.load((const E*)a.v + row0 * a.ldv + (int64_t)h * a.dv, (int)a.ldv, rows, a.dv);
-            bad |= t.store(sh.v, rows, a.dv);
-            t.load((const E*)a.dO + row0 * ldo + (int64_t)h * a.dv, ldo, rows, a.dv);
-            bad |= t.store(sh.dO, rows, a.dv);
-        }
+        bad |= vr.store(sh.v, rows, a.dv);
+        bad |= dr.store(sh.dO, rows, a.dv);
         if (bad) sh.bad = n_head + 1;
         if (wave == 0) {
-            Token tok;
-            tok.load(a, row0, rows, h, N);
             tok.settle(rows);
             sh.dec.make(tok.g, tok.reset);
         }
         lds_barrier();
         const bool slow = sh.bad == n_head + 1;
         const Decays<N>& dec = sh.dec;
+        if (n_head + 1 < group) fetch(h + 1);
 
         // scores, and the sums over them that the decays' gradient needs
 #pragma unroll
@@ -156,8 +185,6 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
             put4(sh.B + i * SLD + j, B);
         }
         // dq and dk: what other blocks give
-        const int64_t at = (((int64_t)b * a.blocks + c) * a.H + h) * a.DKs * (int64_t)a.DVs;
-        const float *S = a.states + at, *R = a.grads + at;
         f4 dqs[kIts], dks[kIts];
         float later[kIts], earlier[kIts], both = 0.f;
 #pragma unroll
@@ -167,18 +194,19 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
             const int d0 = (m * kWaves + wave) * 16;
 #pragma unroll
             for (int it = 0; it < kIts; ++it) dqs[it] = dks[it] = f4{0, 0, 0, 0};
+            if (m) states(m);
 #pragma unroll
             for (int e0 = 0; e0 < DV; e0 += 32) {
-                f8 sf = {}, rf = {};
                 const int e = e0 + g * 8;
-                if (d0 < a.DKs && e < a.DVs) {
-                    const int64_t p = (int64_t)(d0 + s16) * a.DVs + e;
-                    sf = *reinterpret_cast<const f8_align16*>(S + p);
-                    rf = *reinterpret_cast<const f8_align16*>(R + p);
-                }
+                f8 s = sf[e0 / 32], r = rf[e0 / 32];
+                const bool in = d0 < a.DKs && e < a.DVs;
 #pragma unroll
-                for (int x = 0; x < 8; ++x) both = fmaf(sf[x], rf[x], both);
-                const Parts<BF16> sp(sf), rp(rf);
+                for (int x = 0; x < 8; ++x) {
+                    s[x] = in ? s[x] : 0.f;
+                    r[x] = in ? r[x] : 0.f;
+                    both = fmaf(s[x], r[x], both);
+                }
+                const Parts<BF16> sp(s), rp(r);
                 put8(sh.R + (d0 + s16) * RLD + e, rp.p[0]);
 #pragma unroll
                 for (int it = 0; it < kIts; ++it) {
@@ -304,7 +332,7 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
             for (int jt = 0; jt < kIts; ++jt) {
                 const int j = jt * 16 + s16;
                 if (j < n)
-                    store4<WHOLE>(out + (int64_t)j * a.H * a.dv, (m * kWaves + wave) * 16 + g * 4, a.dv,
+                    store4<WHOLE>(out + j * ldo, (m * kWaves + wave) * 16 + g * 4, a.dv,
                            dv[m][jt]);
             }
         // the decays
@@ -365,17 +393,17 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
         }
         lds_barrier();
     }
-    const int64_t ldo = (int64_t)a.Hk * a.dk;
-    E* oq = (E*)a.dq + row0 * ldo + (int64_t)kh * a.dk;
-    E* ok = (E*)a.dk_out + row0 * ldo + (int64_t)kh * a.dk;
+    const int ldqk = a.Hk * a.dk;
+    E* oq = (E*)a.dq + row0 * ldqk + (int64_t)kh * a.dk;
+    E* ok = (E*)a.dk_out + row0 * ldqk + (int64_t)kh * a.dk;
 #pragma unroll
     for (int m = 0; m < kKt; ++m)
 #pragma unroll
         for (int it = 0; it < kIts; ++it) {
             const int i = it * 16 + s16, d0 = (m * kWaves + wave) * 16 + g * 4;
             if (i < n) {
-                store4<WHOLE>(oq + i * ldo, d0, a.dk, dq[m][it]);
-                store4<WHOLE>(ok + i * ldo, d0, a.dk, dk[m][it]);
+                store4<WHOLE>(oq + i * ldqk, d0, a.dk, dq[m][it]);
+                store4<WHOLE>(ok + i * ldqk, d0, a.dk, dk[m][it]);
             }
         }
 }
