@@ -229,12 +229,32 @@ __device__ __forceinline__ void store4(E* row, int i, int n, f4 x) {
 
 // ---- tiles of tokens --------------------------------------------------------------
 
+// The eight values of a vector moved down by s places, whose last s are lost.
+template <bool BF16>
+__device__ __forceinline__ void move_down(uint32_t (&x)[BF16 ? 4 : 8], int s) {
+    constexpr int kWords = BF16 ? 4 : 8;
+    if constexpr (BF16) {
+        const bool half = s & 1;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w)
+            x[w] = half ? x[w] >> 16 | (w + 1 < kWords ? x[w + 1] << 16 : 0) : x[w];
+        s >>= 1;
+    }
+#pragma unroll
+    for (int d = 1; d < kWords; d *= 2) {
+        const bool on = s & d;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) x[w] = on ? (w + d < kWords ? x[w + d] : 0) : x[w];
+    }
+}
+
 // kBlock rows of W values (n of them there), from global memory through
 // registers to LDS, zeros beyond the rows and columns that there are.  Rows lie
 // less than 2^22 values apart, so 32 bits hold a place in a block.
-// WHOLE: n is a multiple of 8, and loads need no branch: they ask for places
-// that are there (store() clears what lies beyond), and nothing waits for them
-// until then.  Other rows end in single values.
+// Loads need no branch, which would wait for each: they ask for whole vectors
+// that are there, and nothing waits for them until store(), which moves a row's
+// last values to where they belong (WHOLE: n is a multiple of 8, and none has
+// to) and clears what lies beyond.  Rows of less than 8 values are the exception.
 template <bool BF16, int W, bool WHOLE>
 struct Tile {
     typedef typename Io<BF16>::E E;
@@ -244,7 +264,8 @@ struct Tile {
     static constexpr int kMine = kRows * kVecs / kThreads;
     static constexpr int kWords = BF16 ? 4 : 8;  // 32-bit words of 8 values
     static constexpr int kSize = kRows * kLd;    // in LDS, values
-    static_assert(kRows * kVecs % kThreads == 0, "whole rounds of the threads");
+    static_assert(kRows * kVecs % kThreads == 0 && kThreads % kVecs == 0,
+                  "whole rounds of the threads, which keep their columns");
     uint32_t r[kMine][kWords];
 
     __device__ __forceinline__ void vector(int m, const E* p) {
@@ -258,57 +279,56 @@ struct Tile {
     }
     __device__ __forceinline__ void load(const E* base, int ld, int rows, int n) {
         const int last = (rows < kRows ? rows : kRows) - 1;
-        if (WHOLE && rows >= kRows) {
-            const int row = threadIdx.x / kVecs, c = threadIdx.x % kVecs * 8;
-            const uint32_t at = row * ld + min(c, n - 8);
+        const int row = threadIdx.x / kVecs, c = threadIdx.x % kVecs * 8;
+        if (WHOLE || n >= 8) {
+            if (rows >= kRows) {
+                const uint32_t at = row * ld + min(c, n - 8);
 #pragma unroll
-            for (int m = 0; m < kMine; ++m) vector(m, base + m * (kThreads / kVecs) * ld + at);
+                for (int m = 0; m < kMine; ++m) vector(m, base + m * (kThreads / kVecs) * ld + at);
+            } else {
+#pragma unroll
+                for (int m = 0; m < kMine; ++m)
+                    vector(m, base + (uint32_t)(min(row + m * (kThreads / kVecs), last) * ld +
+                                                min(c, n - 8)));
+            }
             return;
         }
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
-            const int id = m * kThreads + threadIdx.x, row = id / kVecs, c = id % kVecs * 8;
-            if constexpr (WHOLE) {
-                vector(m, base + (uint32_t)(min(row, last) * ld + min(c, n - 8)));
-                continue;
-            }
+            const E* p = base + (uint32_t)(min(row + m * (kThreads / kVecs), last) * ld);
 #pragma unroll
             for (int w = 0; w < kWords; ++w) r[m][w] = 0;
-            if (row <= last && c < n) {
-                const E* p = base + (uint32_t)(row * ld + c);
-                if (c + 8 <= n) {
-                    vector(m, p);
-                } else {
 #pragma unroll
-                    for (int e = 0; e < 7; ++e)
-                        if (c + e < n) {
-                            if constexpr (BF16)
-                                r[m][e / 2] |= (uint32_t)p[e] << (e % 2 * 16);
-                            else
-                                r[m][e] = __float_as_uint(p[e]);
-                        }
+            for (int e = 0; e < 7; ++e)
+                if (e < n) {
+                    if constexpr (BF16)
+                        r[m][e / 2] |= (uint32_t)p[e] << (e % 2 * 16);
+                    else
+                        r[m][e] = __float_as_uint(p[e]);
                 }
-            }
         }
     }
     // To LDS; whether something was infinite or NaN.
     __device__ __forceinline__ bool store(E* tile, int rows, int n) {
         uint32_t bad = 0;
-        if (WHOLE && (rows < kRows || n < W)) {
+        const int row = threadIdx.x / kVecs, c = threadIdx.x % kVecs * 8;
+        if (!WHOLE && n >= 8) {
+            const int s = min(max(c + 8 - n, 0), 8);
 #pragma unroll
-            for (int m = 0; m < kMine; ++m) {
-                const int id = m * kThreads + threadIdx.x, row = id / kVecs, c = id % kVecs * 8;
-                if (!(row < rows && c < n))
+            for (int m = 0; m < kMine; ++m) move_down<BF16>(r[m], s);
+        }
+        if (rows < kRows || n < W) {
+#pragma unroll
+            for (int m = 0; m < kMine; ++m)
+                if (!(row + m * (kThreads / kVecs) < rows && c < n))
 #pragma unroll
                     for (int w = 0; w < kWords; ++w) r[m][w] = 0;
-            }
         }
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
-            const int id = m * kThreads + threadIdx.x, row = id / kVecs, c = id % kVecs * 8;
 #pragma unroll
             for (int h = 0; h < kWords / 4; ++h)
-                *reinterpret_cast<u4*>(tile + row * kLd + c + h * 4) =
+                *reinterpret_cast<u4*>(tile + (row + m * (kThreads / kVecs)) * kLd + c + h * 4) =
                     u4{r[m][h * 4], r[m][h * 4 + 1], r[m][h * 4 + 2], r[m][h * 4 + 3]};
             // an exponent of all ones, plus one, carries into the sign's place
 #pragma unroll
@@ -337,8 +357,8 @@ struct Rows {
         for (int s = 0; s < kSteps; ++s) {
             const int c = s * 32 + (l >> 4) * 8;
             typedef typename std::conditional<BF16, u4_align2, u4_align4>::type V;
-            if (WHOLE || c + 8 <= n) {
-                const E* p = base + (uint32_t)(row + (WHOLE ? min(c, n - 8) : c));
+            if (WHOLE || n >= 8) {
+                const E* p = base + (uint32_t)(row + min(c, n - 8));
 #pragma unroll
                 for (int h = 0; h < kWords / 4; ++h) {
                     const u4 x = *reinterpret_cast<const V*>(p + h * (BF16 ? 8 : 4));
@@ -346,12 +366,12 @@ struct Rows {
                     for (int w = 0; w < 4; ++w) r[s][h * 4 + w] = x[w];
                 }
             } else {
-                const E* p = base + (uint32_t)(row + c);
+                const E* p = base + (uint32_t)row;
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) r[s][w] = 0;
 #pragma unroll
                 for (int e = 0; e < 7; ++e)
-                    if (c + e < n) {
+                    if (e < n) {
                         if constexpr (BF16)
                             r[s][e / 2] |= (uint32_t)p[e] << (e % 2 * 16);
                         else
@@ -362,10 +382,14 @@ struct Rows {
     }
     __device__ __forceinline__ Frag operand(int s, int n) const {
         typedef uint32_t U __attribute__((ext_vector_type(kWords)));
-        const bool in = !WHOLE || s * 32 + (int)((threadIdx.x & 63) >> 4) * 8 < n;
+        const int c = s * 32 + (int)((threadIdx.x & 63) >> 4) * 8;
+        uint32_t y[kWords];
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) y[w] = r[s][w];
+        if (!WHOLE && n >= 8) move_down<BF16>(y, min(max(c + 8 - n, 0), 8));
         U x;
 #pragma unroll
-        for (int w = 0; w < kWords; ++w) x[w] = in ? r[s][w] : 0;
+        for (int w = 0; w < kWords; ++w) x[w] = c < n ? y[w] : 0;
         return __builtin_bit_cast(Frag, x);
     }
 };

@@ -17,6 +17,7 @@
 // (linear_attn.hip) leaves R (grads); then one workgroup a block and group of
 // heads that share keys makes all gradients, adding those of q and k over the
 // group's heads in registers, in their order: deterministic.
+#include <cstddef>
 #include <type_traits>
 
 #include "linear_attn.h"
@@ -91,7 +92,12 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
     const int64_t row0 = (int64_t)b * a.L + c * N;
     const int n = a.L - c * N < N ? (int)(a.L - c * N) : N, rows = n;
 
-    for (int i = threadIdx.x; i < N * SLD; i += kThreads) sh.A[i] = sh.B[i] = E(0);
+    // keys after queries; A and B lie side by side
+    static_assert(offsetof(Shared, B) == offsetof(Shared, A) + sizeof sh.A &&
+                      sizeof sh.A % sizeof(u4) == 0,
+                  "one run of vectors");
+    for (int i = threadIdx.x; i < (int)(2 * sizeof sh.A / sizeof(u4)); i += kThreads)
+        reinterpret_cast<u4*>(sh.A)[i] = u4{0, 0, 0, 0};
     if (threadIdx.x == 0) sh.bad = 0;
     lds_barrier();
 
@@ -109,6 +115,11 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
         vr.load((const E*)a.v + row0 * a.ldv + (int64_t)h * a.dv, (int)a.ldv, rows, a.dv);
         dr.load((const E*)a.dO + row0 * ldo + (int64_t)h * a.dv, ldo, rows, a.dv);
     };
+    Token tok;
+    auto token = [&](int h) {
+        if (wave == 0) tok.load(a, row0, rows, h, N);
+    };
+    token(kh * group);  // ahead of all else: its wave sums the decays up first
     bool qkbad;
     {
         QK qr, kr;
@@ -120,6 +131,10 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
     }
     for (int n_head = 0; n_head < group; ++n_head) {
         const int h = kh * group + n_head;
+        if (wave == 0) {
+            tok.settle(rows);
+            sh.dec.make(tok.g, tok.reset);
+        }
         // tiles of the states as operands, on their way during the scores
         const int64_t at = (((int64_t)b * a.blocks + c) * a.H + h) * a.DKs * (int64_t)a.DVs;
         f8 sf[DV / 32], rf[DV / 32];
@@ -133,20 +148,17 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
             }
         };
         states(0);
-        Token tok;
-        if (wave == 0) tok.load(a, row0, rows, h, N);
         bool bad = qkbad;
         bad |= vr.store(sh.v, rows, a.dv);
         bad |= dr.store(sh.dO, rows, a.dv);
         if (bad) sh.bad = n_head + 1;
-        if (wave == 0) {
-            tok.settle(rows);
-            sh.dec.make(tok.g, tok.reset);
-        }
         lds_barrier();
         const bool slow = sh.bad == n_head + 1;
         const Decays<N>& dec = sh.dec;
-        if (n_head + 1 < group) fetch(h + 1);
+        if (n_head + 1 < group) {
+            token(h + 1);
+            fetch(h + 1);
+        }
 
         // scores, and the sums over them that the decays' gradient needs
 #pragma unroll
@@ -391,7 +403,7 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
                 a.dg[(row0 + lane) * a.H + h] = dg;
             }
         }
-        lds_barrier();
+        if (n_head + 1 < group) lds_barrier();
     }
     const int ldqk = a.Hk * a.dk;
     E* oq = (E*)a.dq + row0 * ldqk + (int64_t)kh * a.dk;
