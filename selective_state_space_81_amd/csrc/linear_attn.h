@@ -255,16 +255,18 @@ __device__ __forceinline__ void move_down(uint32_t (&x)[BF16 ? 4 : 8], int s) {
 // that are there, and nothing waits for them until store(), which moves a row's
 // last values to where they belong (WHOLE: n is a multiple of 8, and none has
 // to) and clears what lies beyond.  Rows of less than 8 values are the exception.
-template <bool BF16, int W, bool WHOLE>
+template <bool BF16, int W, bool WHOLE, int THREADS = kThreads>
 struct Tile {
     typedef typename Io<BF16>::E E;
     static constexpr int kRows = Io<BF16>::kBlock;
     static constexpr int kLd = W + Io<BF16>::kPad;
     static constexpr int kVecs = W / 8;  // of 8 values, in a row
-    static constexpr int kMine = kRows * kVecs / kThreads;
-    static constexpr int kWords = BF16 ? 4 : 8;  // 32-bit words of 8 values
-    static constexpr int kSize = kRows * kLd;    // in LDS, values
-    static_assert(kRows * kVecs % kThreads == 0 && kThreads % kVecs == 0,
+    static constexpr bool kFew = kRows * kVecs < THREADS;  // not a vector for every thread
+    static constexpr int kMine = kFew ? 1 : kRows * kVecs / THREADS;
+    static constexpr int kStep = THREADS / kVecs;  // rows between a thread's vectors
+    static constexpr int kWords = BF16 ? 4 : 8;    // 32-bit words of 8 values
+    static constexpr int kSize = kRows * kLd;      // in LDS, values
+    static_assert((kFew || kRows * kVecs % THREADS == 0) && THREADS % kVecs == 0,
                   "whole rounds of the threads, which keep their columns");
     uint32_t r[kMine][kWords];
 
@@ -281,21 +283,21 @@ struct Tile {
         const int last = (rows < kRows ? rows : kRows) - 1;
         const int row = threadIdx.x / kVecs, c = threadIdx.x % kVecs * 8;
         if (WHOLE || n >= 8) {
-            if (rows >= kRows) {
+            if (!kFew && rows >= kRows) {
                 const uint32_t at = row * ld + min(c, n - 8);
 #pragma unroll
-                for (int m = 0; m < kMine; ++m) vector(m, base + m * (kThreads / kVecs) * ld + at);
+                for (int m = 0; m < kMine; ++m) vector(m, base + m * kStep * ld + at);
             } else {
 #pragma unroll
                 for (int m = 0; m < kMine; ++m)
-                    vector(m, base + (uint32_t)(min(row + m * (kThreads / kVecs), last) * ld +
+                    vector(m, base + (uint32_t)(min(row + m * kStep, last) * ld +
                                                 min(c, n - 8)));
             }
             return;
         }
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
-            const E* p = base + (uint32_t)(min(row + m * (kThreads / kVecs), last) * ld);
+            const E* p = base + (uint32_t)(min(row + m * kStep, last) * ld);
 #pragma unroll
             for (int w = 0; w < kWords; ++w) r[m][w] = 0;
 #pragma unroll
@@ -312,6 +314,7 @@ struct Tile {
     __device__ __forceinline__ bool store(E* tile, int rows, int n) {
         uint32_t bad = 0;
         const int row = threadIdx.x / kVecs, c = threadIdx.x % kVecs * 8;
+        if (kFew && row >= kRows) return false;
         if (!WHOLE && n >= 8) {
             const int s = min(max(c + 8 - n, 0), 8);
 #pragma unroll
@@ -320,7 +323,7 @@ struct Tile {
         if (rows < kRows || n < W) {
 #pragma unroll
             for (int m = 0; m < kMine; ++m)
-                if (!(row + m * (kThreads / kVecs) < rows && c < n))
+                if (!(row + m * kStep < rows && c < n))
 #pragma unroll
                     for (int w = 0; w < kWords; ++w) r[m][w] = 0;
         }
@@ -328,7 +331,7 @@ struct Tile {
         for (int m = 0; m < kMine; ++m) {
 #pragma unroll
             for (int h = 0; h < kWords / 4; ++h)
-                *reinterpret_cast<u4*>(tile + (row + m * (kThreads / kVecs)) * kLd + c + h * 4) =
+                *reinterpret_cast<u4*>(tile + (row + m * kStep) * kLd + c + h * 4) =
                     u4{r[m][h * 4], r[m][h * 4 + 1], r[m][h * 4 + 2], r[m][h * 4 + 3]};
             // an exponent of all ones, plus one, carries into the sign's place
 #pragma unroll

@@ -5,16 +5,15 @@
 //
 // In blocks of tokens (linear_attn.h) all of it but the decays is products of
 // small matrices, on the matrix cores.  A workgroup walks along the blocks of
-// one (batch row, head, 64 columns of dv).  A wave takes 16 queries of a block
-// for the outputs: their scores stay in registers, in the layout in which one
-// matrix instruction leaves them and the next takes them (with the summed index
-// permuted, which a sum allows), and their rows of q come straight from memory.
-// And it takes 16 of the columns for the state: [dk][16] in fp32, in registers,
-// from which the block's end leaves a copy rounded to bf16 in LDS for the next
-// block's queries.  So inputs are read once, the state never moves, and two
-// barriers a block suffice.  Loads of the next block are under way while the
-// present one is computed; its decays are summed up by the first wave, which has
-// the fewest keys to look at.
+// one (batch row, head, 64 columns of dv).  Four of its waves make a block's
+// outputs, 16 queries each: their scores stay in registers, in the layout in
+// which one matrix instruction leaves them and the next takes them (with the
+// summed index permuted, which a sum allows), and their rows of q come straight
+// from memory.  The other four move the state on, 16 columns each: [dk][16] in
+// fp32, in registers, with a copy rounded to bf16 in LDS for the block's queries.
+// Both need the state before the block only, so they run side by side.  Inputs
+// are read once, the state never moves, and two barriers a block suffice.  Loads
+// of the next block are under way while the present one is computed.
 //
 // A sequence is cut into segments where heads and columns are too few for the
 // chip: a first pass sums up the segments but the last (k and v only), a second
@@ -95,7 +94,7 @@ struct State {
     }
     // The block's end: s = whole s + sum_j w_j x_j y_j^T, x in rows of xt, y in
     // rows of yt.  Nothing of a state before a document's start comes through.
-    template <bool BF16, int XLD, int YLD, int N, class E>
+    template <bool BF16, int XLD, int YLD, int kAtOnce, int N, class E>
     __device__ __forceinline__ void advance(const E* xt, const E* yt, int ycol, const Decays<N>& d,
                                             const float* w, float scale) {
         const bool cut = d.cut();
@@ -107,17 +106,20 @@ struct State {
         const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
         for (int k0 = 0; k0 < N; k0 += 32) {
-            typename Io<BF16>::Frag xf[kTiles];
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) xf[t] = across<XLD>(xt, k0, t * 16);
             f8 y = widen(across<YLD>(yt, k0, ycol));
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] *= w[k0 + g * 8 + e] * scale;
             const Parts<BF16> yp(y);
 #pragma unroll
-            for (int n = Io<BF16>::kParts - 1; n >= 0; --n)
+            for (int t0 = 0; t0 < kTiles; t0 += kAtOnce) {
+                typename Io<BF16>::Frag xf[kAtOnce];
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t) s[t] = mma(xf[t], yp.p[n], s[t]);
+                for (int t = 0; t < kAtOnce; ++t) xf[t] = across<XLD>(xt, k0, (t0 + t) * 16);
+#pragma unroll
+                for (int n = Io<BF16>::kParts - 1; n >= 0; --n)
+#pragma unroll
+                    for (int t = 0; t < kAtOnce; ++t) s[t0 + t] = mma(xf[t], yp.p[n], s[t0 + t]);
+            }
         }
     }
     // Rounded to the io type for the queries: [column][dk], this wave's columns.
@@ -159,14 +161,22 @@ struct State {
 
 // ---- forward ------------------------------------------------------------------------
 
-template <bool BF16, int DK, bool WHOLE>
-__global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_fwd_kernel(AttnArgs a) {
+// Eight waves: four make the block's outputs, four move the state on.  Both need
+// the state before the block only, so they run side by side.
+constexpr int kFwdThreads = 2 * kThreads;
+
+// Two workgroups share a CU where dk is at most 64.  Above, a lone one has
+// registers for everything; two (PAIR) keep 128 a wave, at the price of some that
+// spill, of queries asked for late and of fewer tiles at once (one block a CU of
+// 2.7 us against two of 5.1).
+template <bool BF16, int DK, bool WHOLE, bool PAIR>
+__global__ __launch_bounds__(kFwdThreads, DK == 64 || PAIR ? 4 : 2) void attn_fwd_kernel(AttnArgs a) {
     typedef typename Io<BF16>::E E;
     typedef typename Io<BF16>::Frag Frag;
     constexpr int N = Io<BF16>::kBlock, kIts = N / 16;  // tiles of queries, and of keys
     constexpr int kCols = 64 * kIts / kWaves;           // columns of a wave's outputs
-    typedef Tile<BF16, DK, WHOLE> K;
-    typedef Tile<BF16, 64, WHOLE> V;
+    typedef Tile<BF16, DK, WHOLE, kFwdThreads> K;
+    typedef Tile<BF16, 64, WHOLE, kFwdThreads> V;
     constexpr int SLD = DK + Io<BF16>::kPad;
     __shared__ __align__(16) E kt[K::kSize];
     __shared__ __align__(16) E vt[V::kSize];
@@ -176,10 +186,10 @@ __global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_fwd_kernel(At
     __shared__ int bad_block;  // the last one in which something was not finite
 
     const Place at(a, a.nseg);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = id & 3;
+    const bool outputs = id < kWaves;
     const int lane = threadIdx.x & 63, g = lane >> 4, s16 = lane & 15;
     const int col0 = at.tile * 64, vcol = wave * 16, mycol = col0 + vcol + s16;
-    const int it = wave % kIts, ocol = wave / kIts * kCols, i = it * 16 + s16;
     const int nv = a.dv - col0 < 64 ? a.dv - col0 : 64;
     const int kh = at.h / (a.H / a.Hk);
     const int64_t row0 = (int64_t)at.b * a.L;
@@ -192,27 +202,19 @@ __global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_fwd_kernel(At
     const float scale = a.scale;
     const int64_t head = ((int64_t)at.b * a.H + at.h) * a.dk * a.dv;
 
-    State<DK> S;
-    if (at.seg)
-        S.load(a.seg + (((int64_t)at.b * a.nseg + at.seg) * a.H + at.h) * a.dk * a.dv, a.dk, a.dv,
-               mycol);
-    else if (a.h0)
-        S.load(a.h0 + head, a.dk, a.dv, mycol);
-    else
-        S.clear();
-    S.template publish<SLD>(st, vcol);
     if (threadIdx.x == 0) bad_block = -1;
     lds_barrier();
 
-    Rows<BF16, DK, WHOLE> qr, qn;  // of this block and the next
+    // Both roles load and store the tiles; wave 0, whose queries have the fewest
+    // keys, sums the next block's decays up.
     K kr;
     V vr;
     Token tok;
     auto tokens = [&](int c) {  // of block c, at least one of which is there
-        if (wave == 0) tok.load(a, row0 + (int64_t)c * N, there(a.L - (int64_t)c * N), at.h, N);
+        if (id == 0) tok.load(a, row0 + (int64_t)c * N, there(a.L - (int64_t)c * N), at.h, N);
     };
     auto settle = [&](int c) {
-        if (wave == 0) {
+        if (id == 0) {
             tok.settle(there(a.L - (int64_t)c * N));
             decays[c & 1].make(tok.g, tok.reset);
             if (lane < N) glog[c & 1][lane] = tok.g;
@@ -223,107 +225,145 @@ __global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_fwd_kernel(At
         const int rows = there(a.L - t0);
         kr.load(k + t0 * a.ldk, (int)a.ldk, rows, a.dk);
         vr.load(v + t0 * a.ldv, (int)a.ldv, rows, nv);
-        qn.load(q + t0 * a.ldq, (int)a.ldq, it * 16, rows, a.dk);
     };
-    tokens(c0);
-    fetch(c0);
-    settle(c0);
-    if (c0 + 1 < c1) tokens(c0 + 1);
-    for (int c = c0; c < c1; ++c) {
-        const int64_t t0 = (int64_t)c * N;
-        const int rows = there(a.L - t0);
-        qr = qn;  // a query that is not finite stays in its own row
+    // Tiles of block c in their places; whether it has to go token by token.
+    auto stage = [&](int c) {
+        const int rows = there(a.L - (int64_t)c * N);
         bool bad = kr.store(kt, rows, a.dk);
         bad |= vr.store(vt, rows, nv);
         if (bad) bad_block = c - c0;
         lds_barrier();
-        const Decays<N>& dec = decays[c & 1];
-        E* o = (E*)a.o + (row0 + t0) * ldo + (int64_t)at.h * a.dv + col0;
         if (c + 1 < c1) {
             settle(c + 1);
             if (c + 2 < c1) tokens(c + 2);
             fetch(c + 1);
         }
-        if (a.states) {
-            float* st = a.states +
-                        (((int64_t)at.b * a.blocks + c) * a.H + at.h) * a.DKs * (int64_t)a.DVs;
-            S.keep(st, a.DKs, a.DVs, col0 + vcol);
-        }
-        if (bad_block == c - c0) {
-            // token by token; the queries take the place of the state's copy
-            lds_barrier();
-            if (wave < kIts)
-#pragma unroll
-                for (int s = 0; s < DK / 32; ++s)
-                    put8(st + i * SLD + s * 32 + g * 8, qr.operand(s, a.dk));
-            lds_barrier();
-            for (int t = 0; t < min(rows, N); ++t) {
-                const bool starts = dec.start[t] == t;
-                S.token(kt + t * K::kLd, get(vt + t * V::kLd + vcol + s16),
-                        hw_exp2(glog[c & 1][t] * kLog2e), !starts, a.dk);
-                const float sum = S.meet(st + t * SLD, a.dk);
-                if (g == 0 && vcol + s16 < nv)
-                    dev::st<BF16>(o, t * ldo + vcol + s16, sum * scale);
+        return bad_block == c - c0;
+    };
+    tokens(c0);
+    fetch(c0);
+    settle(c0);
+    if (c0 + 1 < c1) tokens(c0 + 1);
+
+    if (!outputs) {
+        State<DK> S;
+        if (at.seg)
+            S.load(a.seg + (((int64_t)at.b * a.nseg + at.seg) * a.H + at.h) * a.dk * a.dv, a.dk,
+                   a.dv, mycol);
+        else if (a.h0)
+            S.load(a.h0 + head, a.dk, a.dv, mycol);
+        else
+            S.clear();
+        for (int c = c0; c < c1; ++c) {
+            S.template publish<SLD>(st, vcol);
+            const bool slow = stage(c);
+            const Decays<N>& dec = decays[c & 1];
+            if (a.states)
+                S.keep(a.states +
+                           (((int64_t)at.b * a.blocks + c) * a.H + at.h) * a.DKs * (int64_t)a.DVs,
+                       a.DKs, a.DVs, col0 + vcol);
+            if (slow) {
+                // token by token, outputs and all; the queries come where the
+                // state's copy was
+                const int64_t t0 = (int64_t)c * N;
+                E* o = (E*)a.o + (row0 + t0) * ldo + (int64_t)at.h * a.dv + col0;
+                lds_barrier();
+                lds_barrier();
+                for (int t = 0; t < min(there(a.L - t0), N); ++t) {
+                    const bool starts = dec.start[t] == t;
+                    S.token(kt + t * K::kLd, get(vt + t * V::kLd + vcol + s16),
+                            hw_exp2(glog[c & 1][t] * kLog2e), !starts, a.dk);
+                    const float sum = S.meet(st + t * SLD, a.dk);
+                    if (g == 0 && vcol + s16 < nv)
+                        dev::st<BF16>(o, t * ldo + vcol + s16, sum * scale);
+                }
+            } else {
+                S.template advance<BF16, K::kLd, V::kLd, PAIR ? 2 : 4>(kt, vt, vcol, dec, dec.last, 1.f);
             }
-        } else {
-            Frag qf[DK / 32];
+            lds_barrier();
+        }
+        if (a.h_last && c1 == blocks) S.store(a.h_last + head, a.dk, a.dv, mycol);
+        return;
+    }
+
+    const int it = wave % kIts, ocol = wave / kIts * kCols, i = it * 16 + s16;
+    Rows<BF16, DK, WHOLE> qr;
+    auto queries = [&](int c) {
+        const int64_t t0 = (int64_t)c * N;
+        qr.load(q + t0 * a.ldq, (int)a.ldq, it * 16, there(a.L - t0), a.dk);
+    };
+    queries(c0);
+    for (int c = c0; c < c1; ++c) {
+        const bool slow = stage(c);
+        const Decays<N>& dec = decays[c & 1];
+        const int64_t t0 = (int64_t)c * N;
+        const int rows = there(a.L - t0);
+        Frag qf[DK / 32];  // a query that is not finite stays in its own row
 #pragma unroll
-            for (int s = 0; s < DK / 32; ++s) qf[s] = qr.operand(s, a.dk);
-            // what the state before the block gives
-            f4 oacc[kCols / 16];
+        for (int s = 0; s < DK / 32; ++s) qf[s] = qr.operand(s, a.dk);
+        if (!PAIR && c + 1 < c1) queries(c + 1);
+        if (slow) {
+            lds_barrier();
+            if (id < kIts)
 #pragma unroll
-            for (int n = 0; n < kCols / 16; ++n) oacc[n] = f4{0, 0, 0, 0};
+                for (int s = 0; s < DK / 32; ++s) put8(st + i * SLD + s * 32 + g * 8, qf[s]);
+            lds_barrier();
+            if (PAIR && c + 1 < c1) queries(c + 1);
+            lds_barrier();
+            continue;
+        }
+        // what the state before the block gives
+        f4 oacc[kCols / 16];
+#pragma unroll
+        for (int n = 0; n < kCols / 16; ++n) oacc[n] = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < DK / 32; ++s)
+#pragma unroll
+            for (int n = 0; n < kCols / 16; ++n)
+                oacc[n] = mma(along<SLD>(st, ocol + n * 16, s * 32), qf[s], oacc[n]);
+        const int start = dec.start[i];
+        const float first = dec.first[i] * scale;
+#pragma unroll
+        for (int n = 0; n < kCols / 16; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) oacc[n][r] = start < 0 ? oacc[n][r] * first : 0.f;
+        // scores of 32 keys at a time, and what the keys' values give
+        const float hi = dec.hi[i], lo = dec.lo[i];
+        const int from = start < 0 ? 0 : start;
+#pragma unroll
+        for (int k0 = 0; k0 < N; k0 += 32) {
+            if (k0 > it * 16) break;
+            f4 p[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
             for (int s = 0; s < DK / 32; ++s)
 #pragma unroll
-                for (int n = 0; n < kCols / 16; ++n)
-                    oacc[n] = mma(along<SLD>(st, ocol + n * 16, s * 32), qf[s], oacc[n]);
-            const int start = dec.start[i];
-            const float first = dec.first[i] * scale;
+                for (int x = 0; x < 2; ++x)
+                    p[x] = mma(along<K::kLd>(kt, k0 + x * 16, s * 32), qf[s], p[x]);
+            f8 w;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int j = k0 + x * 16 + g * 4;
+                const f4 hj = *reinterpret_cast<const f4*>(&dec.hi[j]);
+                const f4 lj = *reinterpret_cast<const f4*>(&dec.lo[j]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bool in = (uint32_t)(j + r - from) <= (uint32_t)(i - from);
+                    w[x * 4 + r] = only(in, p[x][r] * (decay(hi, lo, hj[r], lj[r]) * scale));
+                }
+            }
+            const Frag pf = round(w, Frag{});
 #pragma unroll
             for (int n = 0; n < kCols / 16; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) oacc[n][r] = start < 0 ? oacc[n][r] * first : 0.f;
-            // scores of 32 keys at a time, and what the keys' values give
-            const float hi = dec.hi[i], lo = dec.lo[i];
-            const int from = start < 0 ? 0 : start;
-#pragma unroll
-            for (int k0 = 0; k0 < N; k0 += 32) {
-                if (k0 > it * 16) break;
-                f4 p[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-#pragma unroll
-                for (int s = 0; s < DK / 32; ++s)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        p[x] = mma(along<K::kLd>(kt, k0 + x * 16, s * 32), qf[s], p[x]);
-                f8 w;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int j = k0 + x * 16 + g * 4;
-                    const f4 hj = *reinterpret_cast<const f4*>(&dec.hi[j]);
-                    const f4 lj = *reinterpret_cast<const f4*>(&dec.lo[j]);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const bool in = (uint32_t)(j + r - from) <= (uint32_t)(i - from);
-                        w[x * 4 + r] =
-                            only(in, p[x][r] * (decay(hi, lo, hj[r], lj[r]) * scale));
-                    }
-                }
-                const Frag pf = round(w, Frag{});
-#pragma unroll
-                for (int n = 0; n < kCols / 16; ++n)
-                    oacc[n] = mma(across_pair<V::kLd>(vt, k0, ocol + n * 16), pf, oacc[n]);
-            }
-            if (i < rows)
-#pragma unroll
-                for (int n = 0; n < kCols / 16; ++n)
-                    store4<WHOLE>(o + i * ldo, ocol + n * 16 + g * 4, nv, oacc[n]);
-            S.template advance<BF16, K::kLd, V::kLd>(kt, vt, vcol, dec, dec.last, 1.f);
+                oacc[n] = mma(across_pair<V::kLd>(vt, k0, ocol + n * 16), pf, oacc[n]);
         }
+        if (PAIR && c + 1 < c1) queries(c + 1);
+        E* o = (E*)a.o + (row0 + t0) * ldo + (int64_t)at.h * a.dv + col0;
+        if (i < rows)
+#pragma unroll
+            for (int n = 0; n < kCols / 16; ++n)
+                store4<WHOLE>(o + i * ldo, ocol + n * 16 + g * 4, nv, oacc[n]);
         lds_barrier();
-        if (c + 1 < c1) S.template publish<SLD>(st, vcol);
     }
-    if (a.h_last && c1 == blocks) S.store(a.h_last + head, a.dk, a.dv, mycol);
 }
 
 // ---- walk of the states alone ----------------------------------------------------------
@@ -434,7 +474,7 @@ __global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_walk_kernel(A
                 }
             }
         } else {
-            S.template advance<BF16, X::kLd, Y::kLd>(xt, yt, vcol, dec,
+            S.template advance<BF16, X::kLd, Y::kLd, 4>(xt, yt, vcol, dec,
                                                      REV ? dec.first : dec.last, scale);
         }
         lds_barrier();
@@ -635,11 +675,13 @@ void attn_plan(AttnArgs& a, bool bf16) {
     a.tiles = (a.dv + 63) / 64;
     a.DKs = (a.dk + 15) / 16 * 16;
     a.DVs = (a.dv + 15) / 16 * 16;
-    // Two workgroups a CU and none beyond them, which would run by themselves at
-    // the end; segments of at least four blocks, or the joining costs more than
-    // it brings (131072 tokens of 12 heads of 128: 504 workgroups 751 us, 528 1150).
+    // Half a workgroup a CU and more walk the whole sequence: cut, they would pay
+    // for the sums of segments (130M width, 192 workgroups: 87 us, in 2 segments 127,
+    // in 4 115).  Fewer are cut until two a CU are there and none beyond them, which
+    // would run by themselves at the end (131072 tokens of 12 heads of 128: 504
+    // workgroups 805 us, 744 920); into segments of at least four blocks.
     const int64_t wgs = (int64_t)a.batch * a.H * a.tiles;
-    int64_t nseg = wgs >= 192 ? 1 : 512 / wgs;
+    int64_t nseg = wgs >= 128 ? 1 : 512 / wgs;
     if (nseg > a.blocks / 4) nseg = a.blocks / 4;
     if (nseg < 1) nseg = 1;
     a.per = (a.blocks + nseg - 1) / nseg;
@@ -663,7 +705,7 @@ AttnWs attn_ws(const AttnArgs& a, bool backward) {
 }
 
 int64_t attn_workgroups(const AttnArgs& a) {
-    const int64_t walk = (int64_t)a.batch * a.H * a.tiles * a.nseg;
+    const int64_t walk = 2 * (int64_t)a.batch * a.H * a.tiles * a.nseg;  // of twice the threads
     const int64_t grad = (int64_t)a.batch * a.Hk * a.blocks;
     const int64_t carry = ((int64_t)a.batch * a.H * a.dk * a.dv + kThreads - 1) / kThreads;
     const int64_t most = walk > grad ? walk : grad;
@@ -705,7 +747,11 @@ hipError_t launch_attn_fwd(AttnArgs a, bool bf16, void* workspace, hipStream_t s
     }
     ProfScope ps(s, kPhaseMain);
     const unsigned n = (unsigned)((int64_t)a.batch * a.H * a.tiles * a.nseg);
-#define FWD_(B, DK, W) attn_fwd_kernel<B, DK, W><<<n, kThreads, 0, s>>>(a)
+#define FWD_(B, DK, W)                                                                \
+    do {                                                                              \
+        if (DK > 64 && n > 256) attn_fwd_kernel<B, DK, W, DK != 64><<<n, kFwdThreads, 0, s>>>(a); \
+        else attn_fwd_kernel<B, DK, W, false><<<n, kFwdThreads, 0, s>>>(a);           \
+    } while (0)
     ATTN_EACH_(FWD_, bf16, a);
 #undef FWD_
     return hipGetLastError();
