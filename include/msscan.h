@@ -504,9 +504,11 @@ ms_status ms_token_logprobs_bwd(const void* logits, int64_t ld, const void* targ
  *                   (q, k and v may be column slices of one wider tensor and
  *                   need no alignment beyond their element's)
  *   g             : log decays, fp32: [batch][seqlen][heads], or [heads] when
- *                   `fixed` is not 0.  Any value is computed as written; a
- *                   decay that is 0 in fp32 (g below -104, -inf) drops the
- *                   state as a reset does.
+ *                   `fixed` is not 0.  Any finite value is computed as
+ *                   written; a decay that is 0 in fp32 (g below -104, -inf)
+ *                   drops the state as a reset does.  Behind one that is NaN or
+ *                   +inf results are NaN, those of up to 64 tokens past a reset
+ *                   too.
  *   reset         : [batch][seqlen] bytes, optional.  A nonzero byte starts a
  *                   new sequence there: the decay of that step is 0, and
  *                   nothing of the state before it comes through, NaN and

@@ -247,7 +247,7 @@ __global__ __launch_bounds__(kFwdThreads, DK == 64 || PAIR ? 4 : 2) void attn_fw
 
     if (!outputs) {
         State<DK> S;
-        if (at.seg)
+        if (a.nseg > 1)
             S.load(a.seg + (((int64_t)at.b * a.nseg + at.seg) * a.H + at.h) * a.dk * a.dv, a.dk,
                    a.dv, mycol);
         else if (a.h0)
@@ -403,7 +403,7 @@ __global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_walk_kernel(A
     State<DK> S;
     S.clear();
     if (FULL) {
-        if (at.seg)
+        if (a.nseg > 1)
             S.load(a.seg + seg * a.dk * a.dv, a.dk, a.dv, mycol);
         else if (first)
             S.load(first + head, a.dk, a.dv, mycol);
@@ -488,7 +488,8 @@ __global__ __launch_bounds__(kThreads, DK == 64 ? 3 : 2) void attn_walk_kernel(A
 }
 
 // ---- joining the segments -------------------------------------------------------------
-// In place: the sums of segments become the states before them.
+// In place: the sums of segments become the states before them, the first one's
+// (h0) too, for h_last may take its place while the first segment is yet to start.
 __global__ __launch_bounds__(kThreads) void attn_carry_kernel(AttnArgs a, const float* first) {
     const int64_t per = (int64_t)a.H * a.dk * a.dv, each = (int64_t)a.dk * a.dv;
     const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -498,6 +499,7 @@ __global__ __launch_bounds__(kThreads) void attn_carry_kernel(AttnArgs a, const 
     const float* f = a.seg_f + b * a.nseg * a.H + i / each;
     float s = first ? first[e] : 0.f;
     float own = p[0], decay = f[0];
+    p[0] = s;
     for (int n = 0; n < a.nseg - 1; ++n) {
         const float next = n + 2 < a.nseg ? p[(n + 1) * per] : 0.f;
         const float fnext = n + 2 < a.nseg ? f[(int64_t)(n + 1) * a.H] : 0.f;
