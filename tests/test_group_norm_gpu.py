@@ -195,6 +195,24 @@ def test_autograd(gpu):
     assert x.grad.shape == x.shape
 
 
+def test_gradients_of_absent_weights(gpu):
+    """The C ABI gives dweight and dbias also where weight and bias are 1 and 0
+    by their absence."""
+    s = inputs(50, 3, 40, "f32", True, False, False, seed=9)
+    out = [torch.full((50, 120), float("nan"), device=DEV) for _ in range(2)]
+    dw, db = (torch.full((120,), float("nan"), device=DEV) for _ in range(2))
+    n = gpu.group_norm_bwd_workspace_bytes(50, 3, 40, 0)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    rc = gpu.load().ms_group_norm_bwd(
+        s["x"].data_ptr(), 120, None, None, s["z"].data_ptr(), 120, 1, 0, 1e-3, s["dy"].data_ptr(),
+        out[0].data_ptr(), out[1].data_ptr(), dw.data_ptr(), db.data_ptr(), 50, 3, 40, 0,
+        ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    want = definition(s, 3, True, False, 1e-3)
+    for name, got in (("dx", out[0]), ("dz", out[1]), ("dweight", dw), ("dbias", db)):
+        compare(got, want[name], 40, 50, "f32", name)
+
+
 def test_refusals(gpu):
     s = inputs(6, 2, 40, "bf16", True, True, True)
     x, z, w = s["x"], s["z"], s["weight"]

@@ -221,6 +221,22 @@ def test_captured(gpu):
             assert torch.equal(d[n], wd[n]), n
 
 
+def test_two_calls_at_once(gpu):
+    """Calls on two streams side by side, each with a workspace of its own."""
+    a, da, ha = inputs(1, 3000, 2, 1, 64, 64, "bf16", True, True, seed=13)
+    b, db, hb = inputs(1, 2500, 2, 2, 100, 40, "f32", True, False, seed=14)
+    want = both(gpu, a, da, ha), both(gpu, b, db, hb)
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        got = [both(gpu, *args, stream=s) for args, s in zip(((a, da, ha), (b, db, hb)), streams)]
+        torch.cuda.synchronize()
+        for (o, h, d), (wo, wh, wd) in zip(got, want):
+            assert torch.equal(o, wo) and torch.equal(h, wh)
+            for n in d:
+                assert torch.equal(d[n], wd[n]), n
+
+
 # ---- steps ---------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
