@@ -202,12 +202,12 @@ struct AttnWs {
 };
 void attn_plan(AttnArgs& a, bool bf16);
 AttnWs attn_ws(const AttnArgs& a, bool backward);
-int64_t attn_workgroups(const AttnArgs& a);  // the most of a launch
+int64_t attn_workgroups(const AttnArgs& a);  // the most of a launch, as of 256 threads
 hipError_t launch_attn_fwd(AttnArgs a, bool bf16, void* workspace, hipStream_t s);
 hipError_t launch_attn_bwd(AttnArgs a, bool bf16, void* workspace, hipStream_t s);
-// The states of segments of the walk over blocks, forward in time (k, v) or
-// backward (q, dO): with `every`, the state before each block goes to `every`
-// and the last one to `last`; otherwise only the sums of segments to a.seg.
+// The walk of the states alone, forward in time (k, v) or backward (q, dO).  Not
+// full: sums of all segments but the last, to a.seg and a.seg_f.  Full (backward
+// only): from the segments' starts, each block's to a.grads and the last to a.dh0.
 hipError_t launch_attn_walk(const AttnArgs& a, bool bf16, bool reverse, bool full, hipStream_t s);
 hipError_t launch_attn_carry(const AttnArgs& a, const float* first, hipStream_t s);
 int64_t attn_step_workgroups(const AttnArgs& a);
