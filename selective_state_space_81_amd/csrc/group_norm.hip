@@ -143,9 +143,10 @@ enum { kNone = 0, kAfter = 1, kFirst = 2 };  // the gate
 // Where a lane works: its first vector's place in its group, and its group.
 template <bool WIDE>
 struct Lane {
-    int first, step, group, lanes;
-    float* scratch;
-    __device__ __forceinline__ Lane(const NormArgs& a, float* sums) : scratch(sums) {
+    int first, group, lanes;
+    float* scratch;  // two buffers of kWaves
+    int turn;        // of the next sum
+    __device__ __forceinline__ Lane(const NormArgs& a, float* sums) : scratch(sums), turn(0) {
         lanes = a.lanes;
         if (WIDE) {
             first = threadIdx.x;
@@ -156,11 +157,14 @@ struct Lane {
             group = (blockIdx.x % a.columns) * (64 / lanes) + l / lanes;
         }
     }
-    // over the lanes of a group; `turn` alternates between sums that follow each other
-    __device__ __forceinline__ float sum(float x, int turn) const {
+    // Over the lanes of a group.  Each sum takes the buffer that the last one did
+    // not, whoever calls it: a wave that writes into one has passed the barrier of
+    // the sum between, and so have all waves read the sum before that.
+    __device__ __forceinline__ float sum(float x) {
         for (int d = 1; d < (WIDE ? 64 : lanes); d *= 2) x += __shfl_xor(x, d);
         if (WIDE) {
-            float* part = scratch + turn * kWaves;
+            float* part = scratch + turn;
+            turn ^= kWaves;
             if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
             lds_barrier();
             x = (part[0] + part[1]) + (part[2] + part[3]);
@@ -175,7 +179,7 @@ __device__ __forceinline__ float sigmoid(float z) {
 
 // The normalised values of a group in place of u, and the factor they took.
 template <bool BF16, int NV, bool WIDE, bool WHOLE>
-__device__ __forceinline__ float normalise(const NormArgs& a, const Lane<WIDE>& at,
+__device__ __forceinline__ float normalise(const NormArgs& a, Lane<WIDE>& at,
                                            Vec<BF16, WHOLE> (&u)[NV]) {
     constexpr int W = vec<BF16>();
     const float inv = 1.f / (float)a.size;
@@ -185,7 +189,7 @@ __device__ __forceinline__ float normalise(const NormArgs& a, const Lane<WIDE>& 
         for (int m = 0; m < NV; ++m)
 #pragma unroll
             for (int e = 0; e < W; ++e) s += u[m].v[e];
-        const float mean = at.sum(s, 0) * inv;
+        const float mean = at.sum(s) * inv;
 #pragma unroll
         for (int m = 0; m < NV; ++m)
 #pragma unroll
@@ -197,7 +201,7 @@ __device__ __forceinline__ float normalise(const NormArgs& a, const Lane<WIDE>& 
     for (int m = 0; m < NV; ++m)
 #pragma unroll
         for (int e = 0; e < W; ++e) s = fmaf(u[m].v[e], u[m].v[e], s);
-    const float factor = 1.f / sqrtf(fmaf(at.sum(s, 1), inv, a.eps));
+    const float factor = 1.f / sqrtf(fmaf(at.sum(s), inv, a.eps));
 #pragma unroll
     for (int m = 0; m < NV; ++m)
 #pragma unroll
@@ -209,7 +213,7 @@ template <bool BF16, int NV, bool WIDE, bool WHOLE, int GATE, bool BIAS>
 __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
     constexpr int W = vec<BF16>();
     __shared__ float sums[2 * kWaves];
-    const Lane<WIDE> at(a, sums);
+    Lane<WIDE> at(a, sums);
     if (!WIDE && at.group >= a.groups) return;
     const int64_t base = (int64_t)at.group * a.size;
     const int64_t stride = WIDE ? a.strips : a.strips * kWaves;
@@ -267,7 +271,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
     constexpr int W = vec<BF16>();
     __shared__ float sums[2 * kWaves];
     __shared__ float joined[WIDE ? 1 : kWaves][WIDE ? 1 : 64 * NV * W];
-    const Lane<WIDE> at(a, sums);
+    Lane<WIDE> at(a, sums);
     const bool mine = WIDE || at.group < a.groups;
     const int64_t base = (int64_t)at.group * a.size, width = (int64_t)a.groups * a.size;
     const int64_t strip = blockIdx.x / a.columns;
@@ -329,10 +333,8 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
                 sh = fmaf(d, hat[m].v[e], sh);
             }
         }
-        // Turns 0, 1 (in normalise), 0, 1: a buffer comes again behind a barrier
-        // that all waves pass when they have read it.
-        sh = at.sum(sh, 0) * inv;
-        s = a.center ? at.sum(s, 1) * inv : 0.f;
+        sh = at.sum(sh) * inv;
+        s = a.center ? at.sum(s) * inv : 0.f;
 #pragma unroll
         for (int m = 0; m < NV; ++m) {
             const int i = (at.first + m * at.lanes) * W;
