@@ -19,6 +19,7 @@
 // 64 sequences of 4 drafts over 131072 tokens bf16: 57 us for the sums (2.6 TB/s;
 // fp64 operations bound them) and 40 for the rest, half of it trips to memory one
 // after another; one sequence over 50280 fp32: 5 and 13 us.
+#include <cfloat>
 #include <type_traits>
 
 #include "device_common.h"
@@ -72,7 +73,7 @@ struct Roots {
     __device__ __forceinline__ void make() {
         if (threadIdx.x < 128) v[threadIdx.x] = exp2_64((double)threadIdx.x / 128.0 - 1.0) * 2.0;
     }
-    // x >= -1000 (or NaN)
+    // |x| up to 2000 (or NaN)
     __device__ __forceinline__ double exp2(double x) const {
         const double magic = 52776558133248.0;
         const double shifted = x + magic, r = x - (shifted - magic);
@@ -83,6 +84,39 @@ struct Roots {
         p = fma(p, r, 1.0);
         return __builtin_amdgcn_ldexp(p * v[n & 127], n >> 7);
     }
+    // any x up to 2000: 0 from -999 down
+    __device__ __forceinline__ double exp2_or_0(double x) const {
+        const double y = exp2(x < -999.0 ? -999.0 : x);
+        return x < -999.0 ? 0.0 : y;
+    }
+};
+
+// Exponents of logits, in base 2, are v c with c the scale times log2 e.  A product
+// by itself: part of a fused one, it would be another number than the m that a sum
+// stands beside.
+__device__ __forceinline__ double exponent(float v, double c) {
+#pragma clang fp contract(off)
+    return (double)v * c;
+}
+
+// The exponent of a logit over m, the rounded exponent of one of the row's (or of
+// a part's).  The fused product takes v c as it is, so weights are right beside m to
+// 2^-53 of their own exponents, however large m.  m's rounding then shows as a
+// factor that all weights share, 2^(v c - m) of the logit that m is of.  From
+// |m| = 2^50 on it would reach 2^-3 and more of an exponent, and leave fp64's range
+// at rows of the type's lowest value; but there neighbouring logits are 2^25 apart,
+// and a smaller c that is a power of two, in which products are exact, gives what
+// the full one does: 1 for the same logit, and 0 below it.
+struct Over {
+    double c, m;
+    __device__ __forceinline__ Over() = default;
+    __device__ __forceinline__ Over(double m_, double c_) : c(c_), m(m_) {
+        if (fabs(m_) >= 0x1p50 && fabs(m_) < INFINITY) {
+            c = __builtin_amdgcn_ldexp(1.0, __builtin_amdgcn_frexp_exp(c_) - 1);
+            m = exponent((float)(m_ / c_), c);  // the logit itself: fp32 rounds 2^-52 away
+        }
+    }
+    __device__ __forceinline__ double operator()(float v) const { return fma((double)v, c, -m); }
 };
 
 // An exponent (in base 2) near the largest, and the sum beside it.  Nothing yet,
@@ -145,8 +179,11 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a) {
     const void* row = row_of<BF16>(a, r);
     const double c = (double)a.scale * 1.4426950408889634074;
     // Sums stand beside 2^m of a logit met early on.  fp64 reaches far enough that
-    // only one 2^500 times as likely calls for another; and 2^-999 of it is nothing.
+    // only one 2^400 times as likely (800, where fp32's next logit is that far) calls
+    // for another; and 2^-999 of it is nothing.  The borders are fp32 and may be the
+    // logit itself, so what lies below `low` is looked at by its exponent.
     float high = -INFINITY, low = INFINITY;
+    Over over{};
     double m = -INFINITY, s = 0.0;
     for (int64_t i = i0 + threadIdx.x * W; i < i1; i += kThreads * W) {
         float v[W];
@@ -155,22 +192,25 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a) {
 #pragma unroll
         for (int e = 1; e < W; ++e) t = fmaxf(t, v[e]), l = fminf(l, v[e]);
         if (t > high) {
-            const double now = (double)t * c;
+            const double now = exponent(t, c);
             s = m == -INFINITY ? s : s * exp2_64(m - now);
             m = now;
-            high = (float)((m + 500.0) / c);
-            low = (float)((m - 999.0) / c);
+            over = Over(m, c);
+            high = (float)((over.m + 400.0) / over.c);
+            low = fmaxf((float)((over.m - 999.0) / over.c), -FLT_MAX);  // above -inf
         }
         if (m == -INFINITY) {  // nothing but masked logits, or NaN
 #pragma unroll
             for (int e = 0; e < W; ++e) s += v[e] == v[e] ? 0.0 : (double)v[e];
             continue;
         }
-        if (l < low)
+        if (l < low) {
 #pragma unroll
-            for (int e = 0; e < W; ++e) v[e] = v[e] < low ? low : v[e];  // not a NaN
+            for (int e = 0; e < W; ++e) s += roots.exp2_or_0(over(v[e]));
+            continue;
+        }
 #pragma unroll
-        for (int e = 0; e < W; ++e) s += roots.exp2(fma((double)v[e], c, -m));
+        for (int e = 0; e < W; ++e) s += roots.exp2(over(v[e]));
     }
     if (split == 0 && r < a.batch) {  // for the next launch
         if (threadIdx.x == 0) a.done[r] = 0;
@@ -193,7 +233,7 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a) {
 struct Shared {
     Sum p[kMaxDrafts + 1], q[kMaxDrafts];
     int yes[kMaxDrafts];
-    double x[kMaxDrafts];  // the drafts' logits, times the scale
+    double x[kMaxDrafts];  // the drafts' exponents over their rows' m
     int count;
 };
 
@@ -259,14 +299,15 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, int b, Shared& sh) {
         const double c = (double)a.scale * 1.4426950408889634074;
         bool yes = false;
         if (v >= 0 && proper(sh.p[t])) {
-            const double p = power((double)xp * c - sh.p[t].m) / sh.p[t].s;
+            const double x = Over(sh.p[t].m, c)(xp);
+            const double p = power(x) / sh.p[t].s;
             double q = 1.0;
             if (a.draft_logits)
-                q = proper(sh.q[t]) ? power((double)xq * c - sh.q[t].m) / sh.q[t].s : INFINITY;
+                q = proper(sh.q[t]) ? power(Over(sh.q[t].m, c)(xq)) / sh.q[t].s : INFINITY;
             yes = (double)u * q < p;
+            sh.x[t] = x;
         }
         sh.yes[t] = yes;
-        sh.x[t] = (double)xp * (double)a.scale;
     }
     __syncthreads();
     if (t == 0) {
@@ -286,13 +327,15 @@ template <bool BF16>
 struct Drawn {
     const void *prow, *qrow;
     Sum p, q;
-    double c, ratio;  // of what a unit of q's row is worth in p's
-    int64_t one;      // a draft without probabilities of its own
+    Over over_p, over_q;
+    double ratio;  // of what a unit of q's row is worth in p's
+    int64_t one;   // a draft without probabilities of its own
     __device__ __forceinline__ Drawn(const VerifyArgs& a, int b, const Shared& sh) {
         const int n = sh.count, T = a.drafts;
-        c = (double)a.scale * 1.4426950408889634074;
+        const double c = (double)a.scale * 1.4426950408889634074;
         prow = row_of<BF16>(a, (int64_t)b * (T + 1) + n);
         p = sh.p[n];
+        over_p = Over(p.m, c);
         qrow = nullptr;
         one = -1;
         if (n < T) {
@@ -301,18 +344,15 @@ struct Drawn {
             } else if (proper(sh.q[n])) {
                 qrow = row_of<BF16>(a, (int64_t)a.batch * (T + 1) + (int64_t)b * T + n);
                 q = sh.q[n];
+                over_q = Over(q.m, c);
                 ratio = p.s / q.s;
             }
         }
     }
-    static __device__ __forceinline__ double unit(const Roots& roots, double x) {
-        const double y = roots.exp2(x < -999.0 ? -999.0 : x);
-        return x < -999.0 ? 0.0 : y;
-    }
     __device__ __forceinline__ Left at(const Roots& roots, float x, float y, int64_t v) const {
-        const double mine = unit(roots, fma((double)x, c, -p.m));
+        const double mine = roots.exp2_or_0(over_p(x));
         double left = mine;
-        if (qrow) left = fma(-unit(roots, fma((double)y, c, -q.m)), ratio, mine);
+        if (qrow) left = fma(-roots.exp2_or_0(over_q(y)), ratio, mine);
         if (v == one) left = 0.0;
         return {mine, left > 0.0 ? left : 0.0};
     }
@@ -491,9 +531,8 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a) {
         double lp = 0.0;
         if (v >= 0) {
             const double x = tid < sh.count ? sh.x[tid]
-                                            : (double)ld<BF16>(row_of<BF16>(a, at), v) *
-                                                  (double)a.scale;
-            lp = x - sh.p[tid].m * 0.693147180559945309417 - log(sh.p[tid].s);
+                                            : from.over_p(ld<BF16>(row_of<BF16>(a, at), v));
+            lp = fma(x, 0.693147180559945309417, -log(sh.p[tid].s));
         }
         a.tokens[at] = (int32_t)v;
         a.logprob[at] = (float)lp;
