@@ -506,9 +506,10 @@ ms_status ms_token_logprobs_bwd(const void* logits, int64_t ld, const void* targ
  *   g             : log decays, fp32: [batch][seqlen][heads], or [heads] when
  *                   `fixed` is not 0.  Any finite value is computed as
  *                   written; a decay that is 0 in fp32 (g below -104, -inf)
- *                   drops the state as a reset does.  Behind one that is NaN or
- *                   +inf results are NaN, those of up to 64 tokens past a reset
- *                   too.
+ *                   drops the state as a reset does.  One that is NaN, or so
+ *                   large that its exponential is infinite, spoils results of its
+ *                   head from its own token to the next reset (gradients of the
+ *                   tokens ahead of it in the sequence too), and none beyond.
  *   reset         : [batch][seqlen] bytes, optional.  A nonzero byte starts a
  *                   new sequence there: the decay of that step is 0, and
  *                   nothing of the state before it comes through, NaN and

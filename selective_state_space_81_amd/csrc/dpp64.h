@@ -25,6 +25,18 @@ __device__ __forceinline__ double scan64(double x) {
     x += dpp64<0x143, 0xc>(x);
     return x;
 }
+// The same from lane `first` (of each lane's own run of neighbours, or below 0) on.
+__device__ __forceinline__ double scan64_from(double x, int first) {
+    const int i = threadIdx.x & 63;
+    double y;
+    y = dpp64<0x111, 0xf>(x), x += i - 1 >= first ? y : 0.0;
+    y = dpp64<0x112, 0xf>(x), x += i - 2 >= first ? y : 0.0;
+    y = dpp64<0x114, 0xf>(x), x += i - 4 >= first ? y : 0.0;
+    y = dpp64<0x118, 0xf>(x), x += i - 8 >= first ? y : 0.0;
+    y = dpp64<0x142, 0xa>(x), x += (i & 48) - 1 >= first ? y : 0.0;
+    y = dpp64<0x143, 0xc>(x), x += 31 >= first ? y : 0.0;
+    return x;
+}
 __device__ __forceinline__ double lane64(double x, int lane) {
     const uint64_t u = __builtin_bit_cast(uint64_t, x);
     const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, lane);

@@ -412,7 +412,8 @@ __device__ __forceinline__ float decay(float hi_i, float lo_i, float hi_j, float
 }
 
 // Sums of log decays in two floats each: they reach hundreds inside a block,
-// and the decay between neighbours needs the difference to 2^-24.
+// and the decay between neighbours needs the difference to 2^-24.  They run from
+// the block's start, or from the document's where that lies in the block.
 template <int N>
 struct Decays {
     __align__(16) float hi[N];
@@ -427,10 +428,12 @@ struct Decays {
     __device__ __forceinline__ void make(float g, bool cut) {
         const int i = threadIdx.x & 63;
         double G = cut || i >= N ? 0.0 : (double)g * 1.4426950408889634;
-        G = scan64(G);
         const uint64_t cuts = __ballot(cut && i < N);
         const uint64_t upto = cuts & (~0ull >> (63 - i));
         const int s = upto ? 63 - __builtin_clzll(upto) : -1;
+        // Sums begin anew with a document: differences across a start are never
+        // used, and a decay that is no number stays in its document.
+        G = cuts ? scan64_from(G, s) : scan64(G);
         const float h = (float)G, l = (float)(G - (double)h);
         const double end = lane64(G, N - 1);
         const int send = cuts ? 63 - __builtin_clzll(cuts) : -1;

@@ -1,0 +1,54 @@
+"""Documents packed into one sequence (resets): nothing of one reaches another's
+results, not by a rounding, and not where a log decay is no number."""
+import math
+
+import pytest
+import torch
+
+from test_linear_attn_gpu import both, inputs
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def packed(io, starts, L=700, heads=4, kheads=2, dk=40, dv=72, seed=0):
+    """Inputs of one sequence whose documents start at `starts` (and at 0)."""
+    s, do, _ = inputs(1, L, heads, kheads, dk, dv, io, seed=seed)
+    s["reset"] = torch.zeros(1, L, dtype=torch.uint8, device=DEV)
+    s["reset"][0, starts] = 1
+    return s, do
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, 3e38], ids=["nan", "inf", "3e38"])
+def test_decays_that_are_no_numbers(gpu, io, bad):
+    """A log decay that is NaN, infinite or past all exponents makes nothing of
+    the documents ahead of it and behind it other than it is: the same bits as
+    with a decay in its place."""
+    starts = [10, 23, 24, 100, 130, 300]
+    s, do = packed(io, starts, seed=1)
+    want = both(gpu, s, do, None)
+    t = dict(s, g=s["g"].clone())
+    t["g"][0, 5, 1] = t["g"][0, 110, 0] = t["g"][0, 250] = bad
+    t["g"][0, 24, 2] = bad  # that of a document's first token is not looked at
+    o, h, d = both(gpu, t, do, None)
+    spoilt = [(0, 10), (100, 130), (130, 300)]
+    fine = torch.ones(700, dtype=torch.bool, device=DEV)
+    for i, j in spoilt:
+        fine[i:j] = False
+    assert torch.equal(h, want[1]) and torch.isfinite(h).all()
+    assert torch.equal(o[:, fine], want[0][:, fine])
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(d[n][:, fine], want[2][n][:, fine]), n
+    # in the document itself: outputs ahead of it, and all of the other heads
+    assert torch.equal(o[:, :5], want[0][:, :5]) and torch.equal(o[:, 130:250], want[0][:, 130:250])
+    assert torch.equal(o[:, :24, [0, 2, 3]], want[0][:, :24, [0, 2, 3]])
+    if not math.isfinite(bad):
+        assert torch.isnan(o[:, 250:300]).all()
+    # among tokens that are not finite either
+    t["k"] = s["k"].clone()
+    t["k"][0, 3, 0, 1] = t["k"][0, 105, 1, 0] = math.nan
+    o, h, d = both(gpu, t, do, None)
+    assert torch.isfinite(h).all()
+    for x in (o, d["dq"], d["dk"], d["dv"]):
+        assert torch.isfinite(x[:, fine]).all()
