@@ -10,8 +10,8 @@
 //   dk_j = sum_i B_ij q_i  + l_j R v_j
 //   dg_t = sum_{i >= t > j} A_ij dO_i . v_j + sum_{i >= t} scale f_i q_i . S dO_i
 //          + sum_{j < t} l_j k_j . R v_j + w <R, S>
-// The first sum of dg is a suffix sum, within the block, of row sums less
-// column sums: no cancellation over more than a block's tokens.
+// The first sum of dg is a suffix sum, within the block and the document, of row
+// sums less column sums: no cancellation over more than a block's tokens.
 //
 // The forward leaves S before each block (states); a walk backward in time
 // (linear_attn.hip) leaves R (grads); then one workgroup a block and group of
@@ -387,10 +387,13 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
                 early = sh.earlier[0][t] + sh.earlier[1][t] + sh.earlier[2][t] + sh.earlier[3][t];
             }
             net += late;
+            // a document's tokens lie side by side and share its start
+            const int start = dec.start[t];
 #pragma unroll
             for (int d = 1; d < N; d *= 2) {
                 const float x = __shfl_down(net, d), y = __shfl_up(early, d);
-                if (lane + d < N) net += x;
+                const int theirs = __shfl_down(start, d);
+                if (lane + d < N && theirs == start) net += x;
                 if (lane >= d) early += y;
             }
             early = __shfl_up(early, 1);
@@ -400,7 +403,7 @@ __global__ __launch_bounds__(kThreads, DK + DV <= 128 ? 2 : 1) void attn_grad_ke
                                                       (sh.both[2] + sh.both[3]));
             float dg = net + early + rs;
             if (slow && lane < n) dg += sh.glog[lane];
-            if (dec.start[t] == t || lane >= n) dg = 0.f;
+            if (start == t || lane >= n) dg = 0.f;
             if (a.fixed) {
                 dg = sum_groups(sum_row(dg));
                 if (lane == 0) a.part[((int64_t)b * a.blocks + c) * a.H + h] = dg;

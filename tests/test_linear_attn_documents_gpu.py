@@ -52,3 +52,42 @@ def test_decays_that_are_no_numbers(gpu, io, bad):
     assert torch.isfinite(h).all()
     for x in (o, d["dq"], d["dk"], d["dv"]):
         assert torch.isfinite(x[:, fine]).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, 3e38], ids=["nan", "inf", "3e38"])
+def test_gradients_beside_decays_that_are_no_numbers(gpu, io, bad):
+    """The gradients of the decays, too, are those of their own document: sums
+    over a block's tokens stop at its ends."""
+    s, do = packed(io, [10, 40, 70, 120], L=150, seed=5)
+    want = both(gpu, s, do, None)[2]["dg"]
+    for token, (i, j) in ((5, (0, 10)), (20, (10, 40)), (100, (70, 120)), (130, (120, 150))):
+        t = dict(s, g=s["g"].clone())
+        t["g"][0, token] = bad
+        dg = both(gpu, t, do, None)[2]["dg"]
+        assert torch.equal(dg[:, :i], want[:, :i]) and torch.equal(dg[:, j:], want[:, j:])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_documents_do_not_meet(gpu, io):
+    """A document's results are the same bits whatever lies in the others of its
+    block, also where sums over theirs are large or overflow."""
+    s, do = packed(io, [20, 50, 90], L=150, seed=2)
+    o, h, d = both(gpu, s, do, None)
+    other, odo = packed(io, [20, 50, 90], L=150, seed=3)
+    for size in (1.0, 1e12, 1e37):
+        for i, j in ((0, 20), (20, 50), (50, 90), (90, 150)):
+            keep = torch.zeros(150, dtype=torch.bool, device=DEV)
+            keep[i:j] = True
+            t = dict(s)
+            for n in ("q", "k", "v", "g"):
+                t[n] = torch.where(keep.view(1, -1, *(1,) * (s[n].dim() - 2)), s[n], other[n])
+            # 4.6 at the most times 1e37 is finite
+            tdo = torch.where(keep.view(1, -1, 1, 1), do, (odo.float() * size).to(do.dtype))
+            assert torch.isfinite(tdo).all()
+            to, th, td = both(gpu, t, tdo, None)
+            assert torch.equal(to[:, i:j], o[:, i:j]), (size, i)
+            if j == 150:
+                assert torch.equal(th, h)
+            for n in ("dq", "dk", "dv", "dg"):
+                assert torch.equal(td[n][:, i:j], d[n][:, i:j]), (size, i, n)
