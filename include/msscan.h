@@ -527,8 +527,10 @@ ms_status ms_token_logprobs_bwd(const void* logits, int64_t ld, const void* targ
  * States, decays and sums are fp32 or more (products of bf16 with an fp32
  * state take it in 24 bits where the result is fp32); with bf16 io the scores,
  * and the state that a query meets, are rounded to bf16 ahead of the product
- * that ends in o.  A token that is not finite reaches o from its own step on
- * only.  Deterministic.
+ * that ends in o; in the gradient the scores and their gradients, and in dv the
+ * gradient of the state.  A token that is not finite reaches o from its own step
+ * on only.  Gradients are finite where the formulas' are and only there; of the
+ * others some are NaN where a formula has an infinity.  Deterministic.
  *
  * ms_linear_attn_bwd: gradients for d_o ([batch][seqlen][heads][dv], io dtype)
  *   and, optionally, dh_last, from the same inputs and the states the forward

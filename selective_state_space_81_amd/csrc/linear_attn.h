@@ -83,10 +83,14 @@ __device__ __forceinline__ f4 mma(f8 a, f8 b, f4 c) {
 }
 
 // fp32 values as an operand.  round() keeps 8 bits of them in bf16: what it is
-// used for (scores, and the state that a query meets) ends in a bf16 output and
-// adds as much error as that output's own rounding.  Parts keeps all 24 bits, as
-// a sum of three bf16 numbers, for what ends in fp32 (states, gradients of
-// decays): two would leave 3e-6 of a state, three leave fp32's own error.
+// used for (scores, the state that a query meets; in the gradient the scores and
+// their gradients, and R for dv) ends in a bf16 output and adds as much error as
+// that output's own rounding.  Parts keeps all 24 bits, as a sum of three bf16
+// numbers, for what ends in fp32 (states, gradients of decays): two would leave
+// 3e-6 of a state, three leave fp32's own error.  The parts of an infinite value
+// sum to NaN.  That is let be: it is met in gradients alone, where an infinite
+// state leaves nothing finite, and a second way through them for it cost 6 of 322
+// us of a training pass where all is finite.
 typedef float f2 __attribute__((ext_vector_type(2)));
 typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {  // one conversion for both

@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+import attn_reference as ref
 from test_linear_attn_gpu import both, inputs
 
 pytestmark = pytest.mark.gpu
@@ -91,3 +92,27 @@ def test_documents_do_not_meet(gpu, io):
                 assert torch.equal(th, h)
             for n in ("dq", "dk", "dv", "dg"):
                 assert torch.equal(td[n][:, i:j], d[n][:, i:j]), (size, i, n)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_infinities(gpu, io):
+    """An infinite key among positive numbers makes infinite sums: o and the state
+    have them.  Gradients are finite where the definition's are and only there."""
+    s, do, _ = inputs(1, 200, 4, 2, 40, 36, io, seed=4)
+    for n in ("q", "k", "v"):
+        s[n] = s[n].abs() + 0.125
+    do = do.abs() + 0.125
+    s["g"] = s["g"].clamp_min(-0.5)
+    for where, value in ((("k", (0, 3, 0, 5)), math.inf), (("do", (0, 100, 1, 7)), math.inf)):
+        t, tdo = dict(s, k=s["k"].clone()), do.clone()
+        (t["k"] if where[0] == "k" else tdo)[where[1]] = value
+        o, h, d = both(gpu, t, tdo, None)
+        want, states, first = ref.forward(t, 0.3)
+        w = ref.backward(t, 0.3, states, first, tdo)
+        for x, y in ((o, want), (h, states[-1])):
+            assert not torch.isnan(y).any() and not torch.isnan(x).any()
+            assert torch.equal(torch.isposinf(x), torch.isposinf(y))
+        for n in ("dq", "dk"):
+            w[n] = ref.shared(w[n], 2)
+        for n in ("dq", "dk", "dv", "dg"):
+            assert torch.equal(torch.isfinite(d[n]), torch.isfinite(w[n])), (where, n)
