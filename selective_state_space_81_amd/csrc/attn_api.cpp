@@ -34,16 +34,16 @@ AttnArgs attn_args(int32_t batch, int64_t seqlen, int32_t heads, int32_t kheads,
     return a;
 }
 
-// Sizes, and that every launch has a grid: the plan of them in `a`.
+// Sizes, and that every launch of the pass has a grid: the plan of them in `a`.
 ms_status plan_attn(AttnArgs& a, int32_t batch, int64_t seqlen, int32_t heads, int32_t kheads,
-                    int32_t dk, int32_t dv, int32_t io) {
+                    int32_t dk, int32_t dv, int32_t io, bool backward) {
     ms_status st = check_attn(batch, seqlen, heads, kheads, dk, dv, io);
     if (st != MS_OK) return st;
     a = attn_args(batch, seqlen, heads, kheads, dk, dv);
     if ((double)batch * heads * 2.0 > 0x1p30)
         return fail(MS_ERR_UNSUPPORTED, "batch x heads needs more than 2^24-1 workgroups");
     attn_plan(a, io == MS_BF16);
-    if (attn_workgroups(a) > kMaxGroups)
+    if (attn_workgroups(a, backward) > kMaxGroups)
         return fail(MS_ERR_UNSUPPORTED, "batch x seqlen x heads needs more than 2^24-1 workgroups");
     return MS_OK;
 }
@@ -113,14 +113,14 @@ extern "C" {
 size_t ms_linear_attn_workspace_bytes(int32_t batch, int64_t seqlen, int32_t heads, int32_t kheads,
                                       int32_t dk, int32_t dv, int32_t io) {
     AttnArgs a;
-    if (plan_attn(a, batch, seqlen, heads, kheads, dk, dv, io) != MS_OK) return (size_t)-1;
+    if (plan_attn(a, batch, seqlen, heads, kheads, dk, dv, io, false) != MS_OK) return (size_t)-1;
     return attn_ws(a, false).total;
 }
 
 size_t ms_linear_attn_states_bytes(int32_t batch, int64_t seqlen, int32_t heads, int32_t dk,
                                    int32_t dv, int32_t io) {
-    AttnArgs a;
-    if (plan_attn(a, batch, seqlen, heads, heads, dk, dv, io) != MS_OK) return (size_t)-1;
+    AttnArgs a;  // of the backward with one head of keys, which needs the fewest workgroups
+    if (plan_attn(a, batch, seqlen, heads, 1, dk, dv, io, true) != MS_OK) return (size_t)-1;
     return (size_t)batch * a.blocks * heads * a.DKs * a.DVs * sizeof(float);
 }
 
@@ -132,7 +132,7 @@ ms_status ms_linear_attn_fwd(const void* q, int64_t ldq, const void* k, int64_t 
                              size_t workspace_bytes, void* stream) {
     clear_error();
     AttnArgs a;
-    ms_status st = plan_attn(a, batch, seqlen, heads, kheads, dk, dv, io);
+    ms_status st = plan_attn(a, batch, seqlen, heads, kheads, dk, dv, io, false);
     if (st != MS_OK) return st;
     if ((st = check_scale(scale, false)) != MS_OK) return st;
     if (!q || !k || !v || !g || !o) return fail(MS_ERR_NULL, "q, k, v, g and o are required");
@@ -153,7 +153,7 @@ size_t ms_linear_attn_bwd_workspace_bytes(int32_t batch, int64_t seqlen, int32_t
                                           int32_t kheads, int32_t dk, int32_t dv, int32_t fixed,
                                           int32_t io) {
     AttnArgs a;
-    if (plan_attn(a, batch, seqlen, heads, kheads, dk, dv, io) != MS_OK) return (size_t)-1;
+    if (plan_attn(a, batch, seqlen, heads, kheads, dk, dv, io, true) != MS_OK) return (size_t)-1;
     a.fixed = fixed;
     return attn_ws(a, true).total;
 }
@@ -167,7 +167,7 @@ ms_status ms_linear_attn_bwd(const void* q, int64_t ldq, const void* k, int64_t 
                              size_t workspace_bytes, void* stream) {
     clear_error();
     AttnArgs a;
-    ms_status st = plan_attn(a, batch, seqlen, heads, kheads, dk, dv, io);
+    ms_status st = plan_attn(a, batch, seqlen, heads, kheads, dk, dv, io, true);
     if (st != MS_OK) return st;
     if ((st = check_scale(scale, false)) != MS_OK) return st;
     if (!q || !k || !v || !g || !states || !d_o || !dq || !d_k || !d_v || !dg)

@@ -714,9 +714,9 @@ AttnWs attn_ws(const AttnArgs& a, bool backward) {
     return w;
 }
 
-int64_t attn_workgroups(const AttnArgs& a) {
+int64_t attn_workgroups(const AttnArgs& a, bool backward) {
     const int64_t walk = 2 * (int64_t)a.batch * a.H * a.tiles * a.nseg;  // of twice the threads
-    const int64_t grad = (int64_t)a.batch * a.Hk * a.blocks;
+    const int64_t grad = backward ? (int64_t)a.batch * a.Hk * a.blocks : 0;
     const int64_t carry = ((int64_t)a.batch * a.H * a.dk * a.dv + kThreads - 1) / kThreads;
     const int64_t most = walk > grad ? walk : grad;
     return most > carry ? most : carry;

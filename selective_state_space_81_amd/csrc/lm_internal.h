@@ -202,7 +202,7 @@ struct AttnWs {
 };
 void attn_plan(AttnArgs& a, bool bf16);
 AttnWs attn_ws(const AttnArgs& a, bool backward);
-int64_t attn_workgroups(const AttnArgs& a);  // the most of a launch, as of 256 threads
+int64_t attn_workgroups(const AttnArgs& a, bool backward);  // the most of a launch, as of 256 threads
 hipError_t launch_attn_fwd(AttnArgs a, bool bf16, void* workspace, hipStream_t s);
 hipError_t launch_attn_bwd(AttnArgs a, bool bf16, void* workspace, hipStream_t s);
 // The walk of the states alone, forward in time (k, v) or backward (q, dO).  Not
