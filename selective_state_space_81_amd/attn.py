@@ -364,6 +364,24 @@ def _rows(m, t, inner):
     return t if t is None or m.pitch(t, t.dim(), inner) >= 0 else t.contiguous()
 
 
+def _taken(q, k, v, g, h0, reset):
+    """The arguments of linear_attn as the raw calls take them."""
+    m = lm._marshal()
+    return tuple(_rows(m, t, 2) for t in (q, k, v)) + tuple(
+        t if t is None else t.contiguous() for t in (g, h0, reset))
+
+
+def _attend(q, k, v, g, h0, scale, reset, last, states):
+    """(o, h_last or None)"""
+    import torch
+    h_last = None
+    if last:
+        (b, _, h, _, dk, dv, _), *_ = _chk_heads(lm._marshal(), q, k, v, g, reset)
+        h_last = torch.empty(b, h, dk, dv, dtype=torch.float32, device=k.device)
+    return linear_attn_fwd(q, k, v, g, scale=scale, reset=reset, h0=lm._aligned(h0),
+                           h_last=h_last, states=states), h_last
+
+
 def _functions():
     """The autograd Functions, built on first use (importing the package does
     not import torch)."""
@@ -375,17 +393,12 @@ def _functions():
 
     class LinearAttn(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, q, k, v, g, h0, scale, reset):
-            m = lm._marshal()
-            q, k, v = (_rows(m, t, 2) for t in (q, k, v))
-            g, reset, h0 = (t if t is None else t.contiguous() for t in (g, reset, h0))
+        def forward(ctx, q, k, v, g, h0, scale, reset, last):
+            q, k, v, g, h0, reset = _taken(q, k, v, g, h0, reset)
             states = linear_attn_states(k, v)
-            h_last = torch.empty(k.shape[0], v.shape[2], k.shape[3], v.shape[3],
-                                 dtype=torch.float32, device=k.device)
-            o = linear_attn_fwd(q, k, v, g, scale=scale, reset=reset, h0=lm._aligned(h0),
-                                h_last=h_last, states=states)
+            o, h_last = _attend(q, k, v, g, h0, scale, reset, last, states)
             ctx.save_for_backward(q, k, v, g, states, reset)
-            ctx.scale, ctx.start = scale, h0 is not None
+            ctx.scale, ctx.start = scale, h0 is not None and ctx.needs_input_grad[4]
             ctx.set_materialize_grads(False)
             return o, h_last
 
@@ -399,7 +412,7 @@ def _functions():
                 dh_last = dh_last.contiguous()
             d = linear_attn_bwd(q, k, v, g, do, states, scale=ctx.scale, reset=reset,
                                 dh_last=dh_last, want_dh0=ctx.start)
-            return d["dq"], d["dk"], d["dv"], d["dg"], d["dh0"], None, None
+            return d["dq"], d["dk"], d["dv"], d["dg"], d["dh0"], None, None, None
 
     class GroupNorm(torch.autograd.Function):
         @staticmethod
@@ -426,8 +439,15 @@ def _functions():
 def linear_attn(q, k, v, g, h0=None, *, scale=1.0, reset=None, return_last=False):
     """Linear attention as a differentiable torch operation (linear_attn_fwd
     with its saved states, linear_attn_bwd).  Returns o, or (o, h_last) with
-    return_last; gradients (of the first order) reach q, k, v, g and h0."""
-    o, h_last = _functions()[0].apply(q, k, v, g, h0, scale, reset)
+    return_last; gradients (of the first order) reach q, k, v, g and h0.  Where
+    none is asked for, no states are saved."""
+    import torch
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
+                                       for t in (q, k, v, g, h0)):
+        o, h_last = _functions()[0].apply(q, k, v, g, h0, scale, reset, return_last)
+    else:
+        q, k, v, g, h0, reset = _taken(q, k, v, g, h0, reset)
+        o, h_last = _attend(q, k, v, g, h0, scale, reset, return_last, None)
     return (o, h_last) if return_last else o
 
 
