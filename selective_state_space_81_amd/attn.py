@@ -279,24 +279,27 @@ def group_norm_bwd_workspace_bytes(rows: int, groups: int, size: int, io: int) -
 
 
 def group_norm_bwd(x, dy, groups, weight=None, bias=None, z=None, *, center=True,
-                   gate_first=False, eps=1e-5, workspace=None, stream=None):
+                   gate_first=False, eps=1e-5, workspace=None, stream=None, want_dweight=True,
+                   want_dbias=True):
     """ms_group_norm_bwd on torch device tensors: gradients of group_norm_fwd
     for dy (of x's shape).  Returns a dict: dx, dz (io dtype; dz None without
-    z), dweight and dbias (fp32; None where the argument was)."""
+    z), dweight and dbias (fp32; None where the argument was, or it is not
+    wanted)."""
     import torch
     m = lm._marshal()
     _need(dy=dy)
     rows, size, ldx, ldz, io = _chk_norm(m, x, groups, weight, bias, z)
     if not m.fits(x, x.dtype, tuple(x.shape), dy):
         lm._refuse(x.device, x.dtype, tuple(x.shape), dy=dy)
+    want_dweight, want_dbias = want_dweight and weight is not None, want_dbias and bias is not None
     need = group_norm_bwd_workspace_bytes(rows, groups, size, io)
     call = lm._Call(m, x, stream)
     f32, c = torch.float32, x.shape[-1]
     out = {"dx": call.empty(x.dtype, *x.shape),
            "dz": call.empty(x.dtype, *x.shape) if z is not None else None,
-           "dweight": call.empty(f32, c) if weight is not None else None,
-           "dbias": call.empty(f32, c) if bias is not None else None}
-    if weight is None and bias is None:
+           "dweight": call.empty(f32, c) if want_dweight else None,
+           "dbias": call.empty(f32, c) if want_dbias else None}
+    if not (want_dweight or want_dbias):
         need = 0
     ws, wn = call.workspace(workspace, need)
     call.run(m.group_norm_bwd, x, ldx, weight, bias, z, ldz, int(center), int(gate_first), eps, dy,
@@ -429,7 +432,9 @@ def _functions():
         @once_differentiable
         def backward(ctx, dy):
             x, weight, bias, z = ctx.saved_tensors
-            d = group_norm_bwd(x, dy.contiguous(), ctx.groups, weight, bias, z, **ctx.how)
+            d = group_norm_bwd(x, dy.contiguous(), ctx.groups, weight, bias, z, **ctx.how,
+                               want_dweight=ctx.needs_input_grad[2],
+                               want_dbias=ctx.needs_input_grad[3])
             return d["dx"], None, d["dweight"], d["dbias"], d["dz"], None, None, None
 
     _fns = (LinearAttn, GroupNorm)

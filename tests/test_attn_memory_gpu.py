@@ -73,3 +73,29 @@ def test_refusals_without_a_gradient(gpu):
         for last in (False, True):
             with pytest.raises((ValueError, TypeError)):
                 gpu.linear_attn(*bad, return_last=last)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_group_norm_gradients_of_some(gpu, io):
+    """dweight and dbias are made (and their workspace is taken) only where they
+    are wanted; all else is the same."""
+    from test_group_norm_gpu import inputs as norm_inputs
+    rows, groups, size = 9000, 2, 256
+    s = norm_inputs(rows, groups, size, io, True, True, True, seed=60)
+    args = (groups, s["weight"], s["bias"], s["z"])
+    want, with_weights = peak(lambda: gpu.group_norm_bwd(s["x"], s["dy"], *args))
+    need = gpu.group_norm_bwd_workspace_bytes(rows, groups, size, int(io == "bf16"))
+    assert need > 1 << 20
+    for w in (False, True):
+        for b in (False, True):
+            d, used = peak(lambda: gpu.group_norm_bwd(s["x"], s["dy"], *args, want_dweight=w,
+                                                      want_dbias=b))
+            assert (d["dweight"] is not None) == w and (d["dbias"] is not None) == b
+            for n, x in d.items():
+                assert x is None or torch.equal(x, want[n]), n
+            assert w or b or used <= with_weights - need
+    for only in ("x", "weight", "bias", "z"):
+        t = {n: s[n].clone().requires_grad_(n == only) for n in ("x", "weight", "bias", "z")}
+        gpu.group_norm(t["x"], groups, t["weight"], t["bias"], t["z"]).backward(s["dy"])
+        assert torch.equal(t[only].grad, want["d" + only]), only
+        assert all(x.grad is None for n, x in t.items() if n != only)
