@@ -84,9 +84,12 @@ struct Roots {
         p = fma(p, r, 1.0);
         return __builtin_amdgcn_ldexp(p * v[n & 127], n >> 7);
     }
-    // any x up to 2000: 0 from -999 down
+    // any x up to 2000: 2^-999 (beside what reaches 1, nothing) or 0 from -999 down
+    __device__ __forceinline__ double exp2_above(double x) const {
+        return exp2(x < -999.0 ? -999.0 : x);
+    }
     __device__ __forceinline__ double exp2_or_0(double x) const {
-        const double y = exp2(x < -999.0 ? -999.0 : x);
+        const double y = exp2_above(x);
         return x < -999.0 ? 0.0 : y;
     }
 };
@@ -206,7 +209,7 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(VerifyArgs a) {
         }
         if (l < low) {
 #pragma unroll
-            for (int e = 0; e < W; ++e) s += roots.exp2_or_0(over(v[e]));
+            for (int e = 0; e < W; ++e) s += roots.exp2_above(over(v[e]));
             continue;
         }
 #pragma unroll
