@@ -641,7 +641,8 @@ ms_status ms_group_norm_bwd(const void* x, int64_t ldx, const float* weight, con
  * token is drawn from p.  A row of the target that is no distribution (NaN,
  * +inf, or all -inf) has its draft refused and gives token -1; such a row of
  * the drafting model has its draft refused and counts as q = 0.  Everything
- * is computed in fp64: deterministic, and borders fall where the formulas say.
+ * is computed in fp64, probabilities to 5e-12 of themselves whatever the scale:
+ * deterministic, and borders fall where the formulas say.
  */
 size_t ms_verify_drafts_workspace_bytes(int32_t batch, int32_t drafts, int64_t vocab,
                                         int32_t drafted, int32_t io);

@@ -21,9 +21,9 @@
 //
 // Bound by what a wave issues and waits for along its blocks, one after another
 // (2.7 us each), with 1300 cycles of matrix instructions a wave in them: 8 x 2048
-// tokens of 24 heads of 64 columns and shared keys of 128, 91 us; heads of 64 with
-// keys of their own, states saved, 107 us; 131072 tokens of 12 heads of 128 x 128,
-// 807 us, of them 290 for the sums of segments.
+// tokens of 24 heads of 64 columns and shared keys of 128, 93 us; heads of 64 with
+// keys of their own, states saved, 108 us; 131072 tokens of 12 heads of 128 x 128,
+// 804 us, a third of them for the sums of segments.
 #include <type_traits>
 
 #include "linear_attn.h"
@@ -686,9 +686,13 @@ void attn_plan(AttnArgs& a, bool bf16) {
     a.DKs = (a.dk + 15) / 16 * 16;
     a.DVs = (a.dv + 15) / 16 * 16;
     // Half a workgroup a CU and more walk the whole sequence: cut, they would pay
-    // for the sums of segments (130M width, 192 workgroups: 87 us, in 2 segments 127,
-    // in 4 115).  Fewer are cut until two a CU are there and none beyond them, which
-    // would run by themselves at the end (131072 tokens of 12 heads of 128: 504
+    // for the sums of segments.  Both sides, whole and cut (bf16, 64 x 64 of own keys
+    // and 128 x 64 of shared ones, 2048 tokens): 96 workgroups 66 and 83 us, cut 50
+    // and 68; 128 66 and 84, cut 52 and 73; 160 67 and 85, cut 65 and 89; 192 68,
+    // cut 80; 240 86, cut 115.  The border is on the safe side: up to 160 a cut would
+    // still win at 8192 tokens (327 and 403 us, cut 260 and 323), from 192 on never
+    // (331, cut 359).  Fewer are cut until two a CU are there and none beyond them,
+    // which would run by themselves at the end (131072 tokens of 12 heads of 128: 504
     // workgroups 805 us, 744 920); into segments of at least four blocks.
     const int64_t wgs = (int64_t)a.batch * a.H * a.tiles;
     int64_t nseg = wgs >= 128 ? 1 : 512 / wgs;

@@ -18,8 +18,8 @@
 // heads that share keys makes all gradients, adding those of q and k over the
 // group's heads in registers, in their order: deterministic.
 //
-// 8 x 2048 tokens of 24 heads of 64 x 64 bf16: 151 us, 550 MB (both states are 200
-// of them), and 73 for the walk.  Two workgroups a CU, each a chain of loads,
+// 8 x 2048 tokens of 24 heads of 64 x 64 bf16: 152 us, 550 MB (both states are 200
+// of them), and 72 for the walk.  Two workgroups a CU, each a chain of loads,
 // scores, and products with the states' three parts; matrix instructions take a
 // tenth of the time.  In fp32 with heads of 40 x 72, 3 x 1999 tokens of 6: 59 us.
 #include <cstddef>

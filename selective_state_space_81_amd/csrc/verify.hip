@@ -16,9 +16,9 @@
 // and, in the workgroup that is the last of its sequence, the search over pieces
 // and inside one.
 //
-// 64 sequences of 4 drafts over 131072 tokens bf16: 57 us for the sums (2.6 TB/s;
+// 64 sequences of 4 drafts over 131072 tokens bf16: 59 us for the sums (2.5 TB/s;
 // fp64 operations bound them) and 40 for the rest, half of it trips to memory one
-// after another; one sequence over 50280 fp32: 5 and 13 us.
+// after another; one sequence over 50280 fp32: 6 and 14 us.
 #include <cfloat>
 #include <type_traits>
 
