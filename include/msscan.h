@@ -508,8 +508,9 @@ ms_status ms_token_logprobs_bwd(const void* logits, int64_t ld, const void* targ
  *                   written; a decay that is 0 in fp32 (g below -104, -inf)
  *                   drops the state as a reset does.  One that is NaN, or so
  *                   large that its exponential is infinite, spoils results of its
- *                   head from its own token to the next reset (gradients of the
- *                   tokens ahead of it in the sequence too), and none beyond.
+ *                   head (and gradients of the q and k that it shares) from its
+ *                   own token to the next reset, gradients of the tokens ahead of
+ *                   it in the sequence too, and none beyond.
  *   reset         : [batch][seqlen] bytes, optional.  A nonzero byte starts a
  *                   new sequence there: the decay of that step is 0, and
  *                   nothing of the state before it comes through, NaN and
@@ -529,8 +530,9 @@ ms_status ms_token_logprobs_bwd(const void* logits, int64_t ld, const void* targ
  * and the state that a query meets, are rounded to bf16 ahead of the product
  * that ends in o; in the gradient the scores and their gradients, and in dv the
  * gradient of the state.  A token that is not finite reaches o from its own step
- * on only.  Gradients are finite where the formulas' are and only there; of the
- * others some are NaN where a formula has an infinity.  Deterministic.
+ * on only.  Gradients (beside log decays as above) are finite where the formulas'
+ * are and only there; of the others some are NaN where a formula has an infinity.
+ * Deterministic.
  *
  * ms_linear_attn_bwd: gradients for d_o ([batch][seqlen][heads][dv], io dtype)
  *   and, optionally, dh_last, from the same inputs and the states the forward
