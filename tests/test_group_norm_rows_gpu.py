@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 
 # rows, groups, size: groups of a workgroup with 1, 2, 4 and 8 vectors a lane, one to
 # three rows of a workgroup, with columns beside each other; a wave's with 1 and 2
-# vectors, some lanes or all of them; rows that leave the last round unfilled
+# vectors, some lanes or all of them; rows that do not fill the last pass
 WIDE = [(4100, 1, 1536), (300, 16, 1100), (2600, 1, 2049), (2500, 1, 4500), (1400, 2, 530)]
 NARROW = [(9000, 1, 64), (9001, 3, 73), (8500, 1, 1000), (20000, 1, 8), (17000, 1, 300)]
 
